@@ -235,6 +235,115 @@ int maxsim_topk_no_alloc(const float *scores, int64_t n, int rows, int k, float 
 /* Bytes of the static scratch array maxsim_topk_no_alloc uses on each GPU. */
 size_t maxsim_topk_scratch_bytes(void);
 
+/* ---- What an encoder in front of the scoring needs ---- */
+
+/*
+ * Rotary positions: the first `rot` entries of every head are turned in pairs (a, b) by the
+ * angle position * freq[f], f the pair's index:
+ *     (a, b) -> mscale * (a cos - b sin, b cos + a sin)
+ * and the entries past them are copied. The angle is taken in 64 bits, so that far positions
+ * keep their phase.
+ *   x       [n_tokens][n_heads][d] in `dtype`: entries of a head lie side by side, tokens and
+ *           heads at strides given in elements
+ *   freq    fp32 [rot / 2], angle per position (a caller that stretches positions for long
+ *           texts divides it)
+ *   rot     even, 2 <= rot <= d; d even, <= MAXSIM_MAX_D; n_heads * d <= 65536
+ *   layout  MAXSIM_ROTARY_HALF: pair f is entries f and f + rot / 2;
+ *           MAXSIM_ROTARY_INTERLEAVED: entries 2f and 2f + 1
+ *   mscale  factor of the turned entries (1 for none)
+ *   inverse 0, or 1 for the opposite angle: the gradient of x from the gradient of the result
+ *   positions    nullable int32 [n_tokens]
+ *   doc_offsets  nullable int64 [n_docs + 1]: without positions, a token's position is its index
+ *                in its document; without either, its index. Both together are refused.
+ *   out     as x, with its own strides; may be x itself with x's strides
+ */
+enum maxsim_rotary_layout { MAXSIM_ROTARY_HALF = 0, MAXSIM_ROTARY_INTERLEAVED = 1 };
+
+int maxsim_rotary(const void *x, int64_t n_tokens, int n_heads, int d, int64_t x_token_stride,
+                  int64_t x_head_stride, int dtype, const float *freq, int rot, int layout,
+                  float mscale, int inverse, const int64_t *doc_offsets, int64_t n_docs,
+                  const int32_t *positions, void *out, int64_t out_token_stride,
+                  int64_t out_head_stride, void *stream);
+
+/*
+ * Attention within documents. For row i of a document, head h, and the document's keys j
+ * (key/value head h / (n_heads / n_kv_heads)):
+ *     x = scale * <q_i, k_j>
+ *     y = softcap > 0 ? softcap * tanh(x / softcap) : x
+ *     y = y - slopes[h] * |i - j|                        (with slopes)
+ *     j is visible when not causal, or j <= i, or j < prefix_lens[document]
+ *     lse[h][i] = log sum_j exp(y),   o_i = sum_j exp(y - lse) v_j     over visible j
+ * A row that sees nothing (a token past doc_lens, or of no document) has o = 0, lse = -inf.
+ * Products run on the matrix cores with fp32 sums; softmax statistics are fp32. The weights
+ * are rounded to `dtype` for the product with v; o is rounded once.
+ *
+ * Layouts: packed, with doc_offsets (int64 [n_docs + 1], not decreasing; entries are clamped
+ * to [0, n_tokens]); or fixed, n_docs documents of nd tokens (n_tokens = n_docs * nd) with a
+ * nullable doc_lens (int32 [n_docs], clamped to [0, nd]). The contents of rows past doc_lens
+ * are never used.
+ *   q       [token][n_heads][d]; k, v [token][n_kv_heads][d], all in `dtype`, at any token,
+ *           head and (fixed layout) document strides, given in elements; every stride and
+ *           address a multiple of 16 bytes; a token's stride at most 16 MiB
+ *   d       a multiple of 8, 8 <= d <= MAXSIM_MAX_HEAD (fp32: <= MAXSIM_MAX_HEAD_FP32, else
+ *           MAXSIM_ERR_UNSUPPORTED)
+ *   scale   > 0
+ *   o       [n_tokens][n_heads][d] in `dtype`;  lse fp32 [n_heads][n_tokens]
+ * n_tokens == 0 enqueues nothing.
+ */
+#define MAXSIM_MAX_HEAD 256
+#define MAXSIM_MAX_HEAD_FP32 128
+
+typedef struct maxsim_attention_tensor {
+  const void *data;
+  int64_t token_stride, head_stride, doc_stride; /* doc_stride: fixed layout only */
+} maxsim_attention_tensor;
+
+typedef struct maxsim_attention_desc {
+  maxsim_attention_tensor q, k, v;
+  const int64_t *doc_offsets; /* packed layout, or NULL */
+  const int32_t *doc_lens;    /* fixed layout, or NULL */
+  int64_t n_tokens, n_docs;
+  const int32_t *prefix_lens; /* int32 [n_docs], or NULL; needs causal */
+  const float *slopes;        /* fp32 [n_heads], or NULL */
+  int nd, n_heads, n_kv_heads, d, dtype, causal;
+  float softcap, scale;
+} maxsim_attention_desc;
+
+int maxsim_attention(const maxsim_attention_desc *desc, void *o, float *lse, void *stream);
+
+/*
+ * Gradients of maxsim_attention from grad_o (laid out like o) and the forward's o and lse:
+ * dq [n_tokens][n_heads][d], dk and dv [n_tokens][n_kv_heads][d] (summed over the heads that
+ * share them), in `dtype`. dq may be NULL, and so may dk and dv together. Rows without a token
+ * get zeros. Sums are fp32; the weights and their gradients are rounded to `dtype` for the
+ * products (fp16: scaled by a power of two taken from grad_o and v first, so that small
+ * gradients are not lost).
+ *   workspace  16-byte aligned, maxsim_attention_backward_workspace_size bytes
+ */
+int maxsim_attention_backward(const maxsim_attention_desc *desc, const void *o, const float *lse,
+                              const void *grad_o, void *dq, void *dk, void *dv, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+size_t maxsim_attention_backward_workspace_size(int64_t n_tokens, int n_heads);
+
+/*
+ * Global norm of many tensors, and clipping:
+ *     norm = sqrt(sum of g * g over all tensors),  out = g * min(1, max_norm / (norm + 1e-6))
+ * Squares are summed in 64 bits. A NaN norm makes every output NaN.
+ *   grads, outs, numel, dtypes  HOST arrays of n_tensors entries, read during the call: device
+ *            addresses of densely packed tensors, element counts (0 allowed) and maxsim_dtype;
+ *            outs may be NULL (in place: nothing is written where the factor is 1), and
+ *            entries of outs may equal those of grads
+ *   max_norm >= 0
+ *   norm     fp32, one element
+ *   workspace  8-byte aligned, maxsim_clip_grad_norm_workspace_size bytes
+ */
+int maxsim_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *numel,
+                          const int32_t *dtypes, int n_tensors, double max_norm, float *norm,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+size_t maxsim_clip_grad_norm_workspace_size(int n_tensors);
+
 /* Static description of a status code. */
 const char *maxsim_status_string(int status);
 

@@ -7,11 +7,17 @@ kernels of libmaxsim. There is no CPU fallback: if the library is missing or no
 gfx950 device is present, the calls raise.
 
     score(q_i, d_j) summed:  out[b] = sum_i max_j <q_i, d_j>
+
+Beside the scoring it has what the encoder in front of it needs, on the same document
+layouts: attention within documents, rotary positions, and the clipping of gradients by their
+global norm.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from array import array
 
 import torch
 
@@ -31,6 +37,21 @@ class MaxSimError(RuntimeError):
     def __init__(self, status: int, func: str, msg: str):
         super().__init__(f"{func}: {STATUS.get(status, status)} ({msg})")
         self.status = status
+
+
+class _AttentionTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("doc_stride", ctypes.c_int64)]
+
+
+class _AttentionDesc(ctypes.Structure):
+    _fields_ = [("q", _AttentionTensor), ("k", _AttentionTensor), ("v", _AttentionTensor),
+                ("doc_offsets", ctypes.c_void_p), ("doc_lens", ctypes.c_void_p),
+                ("n_tokens", ctypes.c_int64), ("n_docs", ctypes.c_int64),
+                ("prefix_lens", ctypes.c_void_p), ("slopes", ctypes.c_void_p),
+                ("nd", ctypes.c_int), ("n_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("d", ctypes.c_int), ("dtype", ctypes.c_int), ("causal", ctypes.c_int),
+                ("softcap", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
 _lib_handle = None
@@ -62,12 +83,24 @@ def lib() -> ctypes.CDLL:
         L.maxsim_topk_no_alloc.argtypes = [vp, i64, i32, i32, vp, vp, vp]
         L.maxsim_topk_scratch_bytes.argtypes = []
         L.maxsim_topk_scratch_bytes.restype = ctypes.c_size_t
+        f32, f64, sz = ctypes.c_float, ctypes.c_double, ctypes.c_size_t
+        L.maxsim_rotary.argtypes = [vp, i64, i32, i32, i64, i64, i32, vp, i32, i32, f32, i32, vp,
+                                    i64, vp, vp, i64, i64, vp]
+        L.maxsim_attention.argtypes = [ctypes.POINTER(_AttentionDesc), vp, vp, vp]
+        L.maxsim_attention_backward.argtypes = [ctypes.POINTER(_AttentionDesc), vp, vp, vp, vp,
+                                                vp, vp, vp, sz, vp]
+        L.maxsim_attention_backward_workspace_size.argtypes = [i64, i32]
+        L.maxsim_attention_backward_workspace_size.restype = sz
+        L.maxsim_clip_grad_norm.argtypes = [vp, vp, vp, vp, i32, f64, vp, vp, sz, vp]
+        L.maxsim_clip_grad_norm_workspace_size.argtypes = [i32]
+        L.maxsim_clip_grad_norm_workspace_size.restype = sz
         L.maxsim_status_string.argtypes = [i32]
         L.maxsim_status_string.restype = ctypes.c_char_p
         L.maxsim_version.argtypes = []
         for f in ("maxsim_score", "maxsim_score_fixed", "maxsim_score_i8", "maxsim_pq_tables",
                   "maxsim_score_pq", "maxsim_version", "maxsim_score_argmax", "maxsim_backward",
-                  "maxsim_score_batch", "maxsim_topk", "maxsim_topk_no_alloc"):
+                  "maxsim_score_batch", "maxsim_topk", "maxsim_topk_no_alloc", "maxsim_rotary",
+                  "maxsim_attention", "maxsim_attention_backward", "maxsim_clip_grad_norm"):
             getattr(L, f).restype = ctypes.c_int
         _lib_handle = L
     return _lib_handle
@@ -418,6 +451,293 @@ def maxsim_score_pq(T: torch.Tensor, codes: torch.Tensor, doc_offsets: torch.Ten
                                  _dev(doc_offsets, "doc_offsets"), n_docs, nd, _dev(out, "out"),
                                  _stream(stream)), "maxsim_score_pq")
     return out
+
+
+# ---- what an encoder in front of the scoring needs ----
+
+def _on(t: torch.Tensor, name: str, device) -> int:
+    """Address of a device tensor of any strides on `device`."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _ours(t: torch.Tensor, stream) -> torch.Tensor:
+    """A buffer allocated here for work on `stream`: the allocator may not hand it out again
+    before that stream is past it."""
+    if stream is not None and t.is_cuda:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        t.record_stream(s)
+    return t
+
+
+_ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
+
+
+def maxsim_rotary(x: torch.Tensor, freq: torch.Tensor, doc_offsets: torch.Tensor | None = None,
+                  positions: torch.Tensor | None = None, layout: str = "half",
+                  mscale: float = 1.0, inverse: bool = False, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Rotary positions of x [n_tokens, n_heads, d], whose entries of a head lie side by side.
+    The first 2 * len(freq) entries of each head are turned in pairs by position * freq (fp32,
+    angle per position) and multiplied by mscale, the others copied. layout: "half" pairs entry
+    f with f + len(freq), "interleaved" 2f with 2f + 1. A token's position is positions[t]
+    (int32), or its index in its document (doc_offsets int64 [n_docs + 1]), or its index.
+    inverse turns by the opposite angle: the gradient of x from the gradient of the result. out
+    may be x itself. Returns a tensor shaped like x."""
+    _need(x, "x", _FLOAT_STORAGE, dim=3)
+    _need(freq, "freq", torch.float32, dim=1)
+    n, heads, d = x.shape
+    rot = 2 * freq.numel()
+    if layout not in _ROTARY_LAYOUT:
+        raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")
+    if rot < 2 or rot > d:
+        raise ValueError(f"freq has {freq.numel()} entries for heads of d = {d}")
+    if doc_offsets is not None and positions is not None:
+        raise ValueError("give doc_offsets or positions, not both")
+    _need(positions, "positions", torch.int32, shape=(n,))
+    _need(doc_offsets, "doc_offsets", torch.int64, dim=1)
+    if doc_offsets is not None and doc_offsets.numel() < 1:
+        raise ValueError("doc_offsets needs n_docs + 1 >= 1 entries")
+    if x.stride(2) != 1:
+        raise ValueError("x needs the entries of a head side by side")
+    if out is None:
+        out = _ours(torch.empty((n, heads, d), dtype=x.dtype, device=x.device), stream)
+    _need(out, "out", x.dtype, shape=(n, heads, d))
+    if out.stride(2) != 1:
+        raise ValueError("out needs the entries of a head side by side")
+    _check(lib().maxsim_rotary(
+        _on(x, "x", x.device), n, heads, d, x.stride(0), x.stride(1), _dtype_code(x),
+        _dev(freq, "freq"), rot, _ROTARY_LAYOUT[layout], float(mscale), int(bool(inverse)),
+        _dev(doc_offsets, "doc_offsets"), 0 if doc_offsets is None else doc_offsets.numel() - 1,
+        _dev(positions, "positions"), _on(out, "out", x.device), out.stride(0), out.stride(1),
+        _stream(stream)), "maxsim_rotary")
+    return out
+
+
+class RotaryFunction(torch.autograd.Function):
+    """Differentiable rotary positions; freq and the positions are constants."""
+
+    @staticmethod
+    def forward(ctx, x, freq, doc_offsets, positions, layout, mscale):
+        ctx.save_for_backward(freq, doc_offsets, positions)
+        ctx.layout, ctx.mscale = layout, mscale
+        return maxsim_rotary(x, freq, doc_offsets, positions, layout, mscale)
+
+    @staticmethod
+    def backward(ctx, grad):
+        freq, doc_offsets, positions = ctx.saved_tensors
+        if grad.stride(2) != 1:
+            grad = grad.contiguous()
+        dx = maxsim_rotary(grad, freq, doc_offsets, positions, ctx.layout, ctx.mscale, inverse=True)
+        return dx, None, None, None, None, None
+
+
+def rotary(x: torch.Tensor, freq: torch.Tensor, doc_offsets: torch.Tensor | None = None,
+           positions: torch.Tensor | None = None, layout: str = "half",
+           mscale: float = 1.0) -> torch.Tensor:
+    """maxsim_rotary that autograd can differentiate with respect to x."""
+    return RotaryFunction.apply(x, freq, doc_offsets, positions, layout, mscale)
+
+
+def _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap, slopes, scale):
+    """The library's description of an attention call, with the checks that it cannot make."""
+    packed = doc_offsets is not None
+    dim = 3 if packed else 4
+    _need(q, "q", _FLOAT_STORAGE, dim=dim)
+    heads, d = q.shape[-2:]
+    for t, name in ((k, "k"), (v, "v")):
+        _need(t, name, q.dtype, dim=dim)
+        if t.shape[:-2] != q.shape[:-2] or t.shape[-1] != d:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, q has {tuple(q.shape)}")
+    kv = k.shape[-2]
+    if v.shape[-2] != kv:
+        raise ValueError(f"k has {kv} heads, v has {v.shape[-2]}")
+    if kv < 1 or heads % kv:
+        raise ValueError(f"{heads} query heads cannot share {kv} key/value heads")
+    if packed:
+        _need(doc_offsets, "doc_offsets", torch.int64, dim=1)
+        if doc_offsets.numel() < 1:
+            raise ValueError("doc_offsets needs n_docs + 1 >= 1 entries")
+        if doc_lens is not None:
+            raise ValueError("give doc_offsets or doc_lens, not both")
+        n_docs, nd, rows = doc_offsets.numel() - 1, 0, q.shape[0]
+    else:
+        n_docs, nd = q.shape[:2]
+        rows = n_docs * nd
+        _need(doc_lens, "doc_lens", torch.int32, shape=(n_docs,))
+    if prefix_lens is not None and not causal:
+        raise ValueError("prefix_lens needs causal")
+    _need(prefix_lens, "prefix_lens", torch.int32, shape=(n_docs,))
+    _need(slopes, "slopes", torch.float32, shape=(heads,))
+    scale = d ** -0.5 if scale is None else float(scale)
+    softcap = float(softcap or 0.0)
+    if not (scale > 0 and math.isfinite(scale)):
+        raise ValueError(f"scale must be positive and finite, got {scale}")
+    if not (softcap >= 0 and math.isfinite(softcap)):
+        raise ValueError(f"softcap must be finite and not negative, got {softcap}")
+
+    def tensor(t, name):
+        if t.stride(-1) != 1 and t.shape[-1] != 1:
+            raise ValueError(f"{name} needs the entries of a head side by side")
+        return _AttentionTensor(_on(t, name, q.device), t.stride(-3), t.stride(-2),
+                                0 if packed else t.stride(0))
+    return _AttentionDesc(
+        tensor(q, "q"), tensor(k, "k"), tensor(v, "v"), _dev(doc_offsets, "doc_offsets"),
+        _dev(doc_lens, "doc_lens"), rows, n_docs, _dev(prefix_lens, "prefix_lens"),
+        _dev(slopes, "slopes"), nd, heads, kv, d, _dtype_code(q), int(bool(causal)), softcap, scale)
+
+
+def maxsim_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     doc_offsets: torch.Tensor | None = None,
+                     doc_lens: torch.Tensor | None = None, causal: bool = False,
+                     prefix_lens: torch.Tensor | None = None, softcap: float = 0.0,
+                     slopes: torch.Tensor | None = None, scale: float | None = None, out=None,
+                     lse=None, stream=None):
+    """Attention within documents. Packed: q [n_tokens, n_heads, d], k and v [n_tokens,
+    n_kv_heads, d] with doc_offsets int64 [n_docs + 1]; fixed: q [n_docs, nd, n_heads, d], k and
+    v alike, with optional doc_lens int32 [n_docs] (tokens past a length are padding). Any
+    strides with the entries of a head side by side and 16-byte steps. causal: a token sees the
+    ones up to itself and those below its document's prefix_lens (int32 [n_docs]); softcap:
+    scores become softcap * tanh(score / softcap); slopes (fp32 [n_heads]): slope * |i - j| is
+    taken off; scale: d ** -0.5 unless given. Returns (o shaped like q, lse fp32 [n_heads,
+    tokens])."""
+    desc = _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap, slopes,
+                           scale)
+    shape = (desc.n_heads, desc.n_tokens)
+    if out is None:
+        out = _ours(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream)
+    if lse is None:
+        lse = _ours(torch.empty(shape, dtype=torch.float32, device=q.device), stream)
+    _need(out, "out", q.dtype, shape=tuple(q.shape))
+    _need(lse, "lse", torch.float32, shape=shape)
+    _check(lib().maxsim_attention(desc, _dev(out, "out"), _dev(lse, "lse"), _stream(stream)),
+           "maxsim_attention")
+    return out, lse
+
+
+def attention_backward_workspace_size(n_tokens: int, n_heads: int) -> int:
+    """Bytes of workspace maxsim_attention_backward needs."""
+    return int(lib().maxsim_attention_backward_workspace_size(n_tokens, n_heads))
+
+
+def maxsim_attention_backward(grad_o: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                              v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
+                              doc_offsets: torch.Tensor | None = None,
+                              doc_lens: torch.Tensor | None = None, causal: bool = False,
+                              prefix_lens: torch.Tensor | None = None, softcap: float = 0.0,
+                              slopes: torch.Tensor | None = None, scale: float | None = None,
+                              want_dq: bool = True, want_dkv: bool = True, dq=None, dk=None,
+                              dv=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of maxsim_attention from its result's gradient grad_o and its
+    outputs o and lse; None for what is not wanted. The other arguments are the forward's."""
+    desc = _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap, slopes,
+                           scale)
+    _need(grad_o, "grad_o", q.dtype, shape=tuple(q.shape))
+    _need(o, "o", q.dtype, shape=tuple(q.shape))
+    _need(lse, "lse", torch.float32, shape=(desc.n_heads, desc.n_tokens))
+    _need(workspace, "workspace", torch.uint8)
+
+    def grad(g, like, name, want):
+        if not want:
+            return None
+        _need(g, name, like.dtype, shape=tuple(like.shape))
+        return g if g is not None else _ours(
+            torch.empty(like.shape, dtype=like.dtype, device=like.device), stream)
+    dq, dk, dv = grad(dq, q, "dq", want_dq), grad(dk, k, "dk", want_dkv), grad(dv, v, "dv", want_dkv)
+    if workspace is None:
+        workspace = _ours(torch.empty(attention_backward_workspace_size(desc.n_tokens, desc.n_heads),
+                                      dtype=torch.uint8, device=q.device), stream)
+    _check(lib().maxsim_attention_backward(
+        desc, _dev(o, "o"), _dev(lse, "lse"), _dev(grad_o, "grad_o"), _dev(dq, "dq"),
+        _dev(dk, "dk"), _dev(dv, "dv"), _dev(workspace, "workspace"), workspace.numel(),
+        _stream(stream)), "maxsim_attention_backward")
+    return dq, dk, dv
+
+
+class AttentionFunction(torch.autograd.Function):
+    """Differentiable attention: gradients of q, k and v; the slopes are constants."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap, slopes, scale):
+        o, lse = maxsim_attention(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap,
+                                  slopes, scale)
+        ctx.save_for_backward(q, k, v, o, lse, doc_offsets, doc_lens, prefix_lens, slopes)
+        ctx.causal, ctx.softcap, ctx.scale = causal, softcap, scale
+        return o
+
+    @staticmethod
+    def backward(ctx, grad):
+        q, k, v, o, lse, doc_offsets, doc_lens, prefix_lens, slopes = ctx.saved_tensors
+        dq, dk, dv = maxsim_attention_backward(
+            grad.contiguous(), q, k, v, o, lse, doc_offsets, doc_lens, ctx.causal, prefix_lens,
+            ctx.softcap, slopes, ctx.scale, want_dq=ctx.needs_input_grad[0],
+            want_dkv=ctx.needs_input_grad[1] or ctx.needs_input_grad[2])
+        return dq, dk, dv, None, None, None, None, None, None, None
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+              doc_offsets: torch.Tensor | None = None, doc_lens: torch.Tensor | None = None,
+              causal: bool = False, prefix_lens: torch.Tensor | None = None,
+              softcap: float = 0.0, slopes: torch.Tensor | None = None,
+              scale: float | None = None) -> torch.Tensor:
+    """maxsim_attention's o, which autograd can differentiate with respect to q, k and v."""
+    return AttentionFunction.apply(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap,
+                                   slopes, scale)
+
+
+def clip_grad_norm_workspace_size(n_tensors: int) -> int:
+    """Bytes of workspace maxsim_clip_grad_norm needs."""
+    return int(lib().maxsim_clip_grad_norm_workspace_size(n_tensors))
+
+
+def maxsim_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Scales a list of gradients (contiguous bf16, fp16 or fp32 tensors, mixed as they come) by
+    min(1, max_norm / (norm + 1e-6)), norm their global 2-norm. In place, or into the list `out`
+    of tensors like them. Returns the norm before clipping, an fp32 scalar on the device."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"out holds {len(outs)} tensors, grads {len(grads)}")
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    max_norm = float(max_norm)
+    if not max_norm >= 0:
+        raise ValueError(f"max_norm must not be negative, got {max_norm}")
+    device = grads[0].device
+    for name, ts in (("grads", grads), ("out", outs if out is not None else [])):
+        for i, t in enumerate(ts):
+            if t.dtype not in _TORCH_DTYPE:
+                raise ValueError(f"{name}[{i}] has unsupported dtype {t.dtype}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must be contiguous")
+            if t.device != device or not t.is_cuda:
+                raise ValueError(f"{name}[{i}] must be a device tensor on the first one's device")
+    if out is not None:
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if o.dtype != g.dtype or o.shape != g.shape:
+                raise ValueError(f"out[{i}] is {o.dtype} {tuple(o.shape)}, the gradient "
+                                 f"{g.dtype} {tuple(g.shape)}")
+    n = len(grads)
+    if norm is None:
+        norm = _ours(torch.empty((), dtype=torch.float32, device=device), stream)
+    _need(norm, "norm", torch.float32, numel=1)
+    _need(workspace, "workspace", torch.uint8)
+    if workspace is None:
+        workspace = _ours(torch.empty(clip_grad_norm_workspace_size(n), dtype=torch.uint8,
+                                      device=device), stream)
+    src = array("Q", [t.data_ptr() for t in grads])
+    dst = None if out is None else array("Q", [t.data_ptr() for t in outs])
+    numel = array("q", [t.numel() for t in grads])
+    code = array("i", [_TORCH_DTYPE[t.dtype] for t in grads])
+    _check(lib().maxsim_clip_grad_norm(
+        src.buffer_info()[0], None if dst is None else dst.buffer_info()[0], numel.buffer_info()[0],
+        code.buffer_info()[0], n, max_norm, _dev(norm, "norm"), _dev(workspace, "workspace"),
+        workspace.numel(), _stream(stream)), "maxsim_clip_grad_norm")
+    return norm
 
 
 def version() -> int:

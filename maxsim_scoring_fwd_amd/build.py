@@ -31,6 +31,19 @@ HIP_FLAGS = [
 ]
 
 
+# The encoder's operators (attention, rotary positions, clipping) meet NaN and infinities in
+# places that a mask or a norm has to handle, so their files keep NaN semantics.
+KEEP_NANS = ("attn_", "attention", "rotary", "clip_norm")
+
+
+def flags_of(source: str) -> list[str]:
+    """Compile flags of one source file."""
+    drop = {"-shared"}
+    if os.path.basename(source).startswith(KEEP_NANS):
+        drop.add("-fno-honor-nans")
+    return [f for f in HIP_FLAGS if f not in drop]
+
+
 OBJ_DIR = os.path.join(PKG, "_build")
 
 
@@ -52,10 +65,9 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = sources()
     objs = [os.path.join(OBJ_DIR, os.path.basename(s)[:-4] + ".o") for s in srcs]
-    compile_flags = [f for f in HIP_FLAGS if f != "-shared"]
     jobs = jobs or max(1, min(len(srcs), os.cpu_count() or 1, 16))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
-        list(ex.map(lambda so: _run([HIPCC, *compile_flags, "-c", "-o", so[1], so[0]], verbose),
+        list(ex.map(lambda so: _run([HIPCC, *flags_of(so[0]), "-c", "-o", so[1], so[0]], verbose),
                     zip(srcs, objs)))
     tmp = LIB + ".tmp%d" % os.getpid()
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], verbose)

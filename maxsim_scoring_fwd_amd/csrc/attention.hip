@@ -1,0 +1,186 @@
+// libmaxsim attention entry points (include/maxsim.h).
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "attn_delta.hpp"
+#include "attn_dispatch.hpp"
+#include "host_common.hpp"
+
+using namespace maxsim;
+
+namespace {
+
+constexpr int64_t MAX_TOKEN_BYTES = (int64_t)1 << 24;  // 64 rows of it stay within 31 bits
+
+// A tensor's strides (in elements, all multiples of 16 bytes) as byte strides.
+int strides(const maxsim_attention_tensor &x, int eb, int64_t &doc, int64_t &head, int &tok) {
+  if (!x.data) return MAXSIM_ERR_NULL;
+  if (!aligned(x.data, 16) || (x.doc_stride * eb) % 16 || (x.head_stride * eb) % 16 ||
+      (x.token_stride * eb) % 16)
+    return MAXSIM_ERR_ALIGN;
+  if (x.token_stride < 0 || x.token_stride * eb > MAX_TOKEN_BYTES || x.head_stride < 0 || x.doc_stride < 0)
+    return MAXSIM_ERR_SHAPE;
+  doc = x.doc_stride * eb;
+  head = x.head_stride * eb;
+  tok = (int)(x.token_stride * eb);
+  return MAXSIM_OK;
+}
+
+int fill(const maxsim_attention_desc *s, AttnArgs &a) {
+  if (!s) return MAXSIM_ERR_NULL;
+  const int eb = elem_bytes(s->dtype);
+  if (eb == 0) return MAXSIM_ERR_DTYPE;
+  const bool packed = s->doc_offsets != nullptr;
+  if (s->n_docs < 0 || s->n_tokens < 0 || s->n_heads < 1 || s->n_kv_heads < 1 ||
+      s->n_heads % s->n_kv_heads || s->d < 8 || s->d > MAXSIM_MAX_HEAD || s->d % 8)
+    return MAXSIM_ERR_SHAPE;
+  if (!packed && (s->nd < 0 || s->n_tokens != s->n_docs * s->nd)) return MAXSIM_ERR_SHAPE;
+  if (s->n_tokens >= ((int64_t)1 << 31) || s->n_heads > 65535 ||
+      (int64_t)s->n_heads * s->d * eb > MAX_TOKEN_BYTES)
+    return MAXSIM_ERR_SHAPE;
+  if (!(s->scale > 0) || !std::isfinite(s->scale) || !(s->softcap >= 0) || !std::isfinite(s->softcap))
+    return MAXSIM_ERR_SHAPE;
+  if (packed && s->doc_lens) return MAXSIM_ERR_UNSUPPORTED;
+  if (s->prefix_lens && !s->causal) return MAXSIM_ERR_UNSUPPORTED;
+  if (s->dtype == MAXSIM_FP32 && s->d > MAXSIM_MAX_HEAD_FP32) return MAXSIM_ERR_UNSUPPORTED;
+  if (!aligned(s->doc_offsets, 8) || !aligned(s->doc_lens, 4) || !aligned(s->prefix_lens, 4) ||
+      !aligned(s->slopes, 4))
+    return MAXSIM_ERR_ALIGN;
+  if (s->n_tokens == 0) return MAXSIM_OK;
+  int rc = strides(s->q, eb, a.q_doc, a.q_head, a.q_tok);
+  if (rc == MAXSIM_OK) rc = strides(s->k, eb, a.k_doc, a.k_head, a.k_tok);
+  if (rc == MAXSIM_OK) rc = strides(s->v, eb, a.v_doc, a.v_head, a.v_tok);
+  if (rc != MAXSIM_OK) return rc;
+  a.q = (const char *)s->q.data;
+  a.k = (const char *)s->k.data;
+  a.v = (const char *)s->v.data;
+  a.offsets = s->doc_offsets;
+  a.n_tokens = a.rows = s->n_tokens;
+  a.n_docs = s->n_docs;
+  a.nd = packed ? 0 : s->nd;
+  a.lens = s->doc_lens;
+  a.prefix = s->prefix_lens;
+  a.heads = s->n_heads;
+  a.kv_heads = s->n_kv_heads;
+  a.d = s->d;
+  a.causal = s->causal != 0;
+  a.softcap = s->softcap;
+  a.scale = s->scale;
+  a.slopes = s->slopes;
+  if (packed) {
+    a.slots = a.n_tokens / ATTN_ROWS + a.n_docs + 2;
+  } else {
+    a.tiles_per_doc = (a.nd + ATTN_ROWS - 1) / ATTN_ROWS;
+    a.slots = a.n_docs * a.tiles_per_doc;
+  }
+  return a.slots * a.heads > 0x7fffffff ? MAXSIM_ERR_SHAPE : MAXSIM_OK;
+}
+
+int mode_of(const AttnArgs &a) {
+  return a.softcap > 0 ? ATTN_CAP : a.slopes ? ATTN_BIAS : ATTN_PLAIN;
+}
+
+// One workgroup for every tile of tokens and each of n_heads heads.
+int run(const void *fn, AttnArgs &a, int n_heads, hipStream_t st) {
+  void *kargs[] = {&a};
+  if (hipLaunchKernel(fn, dim3((unsigned)(a.slots * n_heads)), dim3(ATTN_THREADS), kargs, 0, st) !=
+      hipSuccess) {
+    (void)hipGetLastError();
+    return MAXSIM_ERR_LAUNCH;
+  }
+  return MAXSIM_OK;
+}
+
+const void *pick(int dtype, int dp, int mode, const void *(*bf)(int, int),
+                 const void *(*fp)(int, int), const void *(*f32)(int, int)) {
+  return dtype == MAXSIM_BF16 ? bf(dp, mode) : dtype == MAXSIM_FP16 ? fp(dp, mode) : f32(dp, mode);
+}
+
+size_t delta_floats(int64_t n_tokens, int n_heads) {
+  return ((size_t)n_tokens * (size_t)n_heads + 3) / 4 * 4;
+}
+
+}  // namespace
+
+extern "C" {
+
+int maxsim_attention(const maxsim_attention_desc *desc, void *o, float *lse, void *stream) {
+  AttnArgs a{};
+  int rc = fill(desc, a);
+  if (rc != MAXSIM_OK) return rc;
+  if (desc->n_tokens == 0) return MAXSIM_OK;
+  if (!o || !lse) return MAXSIM_ERR_NULL;
+  if (!aligned(o, 16) || !aligned(lse, 4)) return MAXSIM_ERR_ALIGN;
+  DeviceInfo di;
+  rc = current_device(di);
+  if (rc != MAXSIM_OK) return rc;
+  a.o = (char *)o;
+  a.lse = lse;
+  return run(pick(desc->dtype, attn_width(a.d), mode_of(a), attn_fwd_bf16, attn_fwd_fp16, attn_fwd_fp32),
+             a, a.heads, (hipStream_t)stream);
+}
+
+size_t maxsim_attention_backward_workspace_size(int64_t n_tokens, int n_heads) {
+  if (n_tokens < 0 || n_heads < 1) return 0;
+  return (delta_floats(n_tokens, n_heads) + 2 * DELTA_GRID + 4) * sizeof(float);
+}
+
+int maxsim_attention_backward(const maxsim_attention_desc *desc, const void *o, const float *lse,
+                              const void *grad_o, void *dq, void *dk, void *dv, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+  AttnArgs a{};
+  int rc = fill(desc, a);
+  if (rc != MAXSIM_OK) return rc;
+  if (desc->n_tokens == 0) return MAXSIM_OK;
+  if (!o || !lse || !grad_o || !workspace) return MAXSIM_ERR_NULL;
+  if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(grad_o, 16) || !aligned(dq, 16) ||
+      !aligned(dk, 16) || !aligned(dv, 16) || !aligned(workspace, 16))
+    return MAXSIM_ERR_ALIGN;
+  if ((dk == nullptr) != (dv == nullptr)) return MAXSIM_ERR_NULL;
+  if (workspace_bytes < maxsim_attention_backward_workspace_size(desc->n_tokens, desc->n_heads))
+    return MAXSIM_ERR_SHAPE;
+  if (!dq && !dk) return MAXSIM_OK;
+  DeviceInfo di;
+  rc = current_device(di);
+  if (rc != MAXSIM_OK) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  a.o = (char *)const_cast<void *>(o);
+  a.lse = const_cast<float *>(lse);
+  a.dO = (const char *)grad_o;
+  a.dq = (char *)dq;
+  a.dk = (char *)dk;
+  a.dv = (char *)dv;
+  float *delta = (float *)workspace;
+  float2 *maxima = (float2 *)(delta + delta_floats(a.rows, a.heads));
+  float *gscale = (float *)(maxima + DELTA_GRID);
+  a.delta = delta;
+  a.grad_scale = gscale;
+  // 32 rows of a head a workgroup; fp16 needs one pair of maxima from each, so there are few
+  int64_t grid = (a.rows * a.heads + 31) / 32;
+  const int64_t most = desc->dtype == MAXSIM_FP16 ? DELTA_GRID : 16 * di.cus;
+  if (grid > most) grid = most;
+  const void *fn = desc->dtype == MAXSIM_BF16   ? (const void *)attn_delta_kernel<DT_BF16>
+                   : desc->dtype == MAXSIM_FP16 ? (const void *)attn_delta_kernel<DT_FP16>
+                                                : (const void *)attn_delta_kernel<DT_FP32>;
+  void *kargs[] = {&a, &delta, &maxima};
+  if (hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), kargs, 0, st) != hipSuccess) {
+    (void)hipGetLastError();
+    return MAXSIM_ERR_LAUNCH;
+  }
+  if (desc->dtype == MAXSIM_FP16) {
+    hipLaunchKernelGGL(attn_grad_scale_kernel, dim3(1), dim3(64), 0, st, maxima, (int)grid, gscale);
+    if (hipGetLastError() != hipSuccess) return MAXSIM_ERR_LAUNCH;
+  }
+  const int dp = attn_width(a.d), mode = mode_of(a);
+  if (dq) {
+    rc = run(pick(desc->dtype, dp, mode, attn_dq_bf16, attn_dq_fp16, attn_dq_fp32), a, a.heads, st);
+    if (rc != MAXSIM_OK) return rc;
+  }
+  if (dk)
+    return run(pick(desc->dtype, dp, mode, attn_dkv_bf16, attn_dkv_fp16, attn_dkv_fp32), a,
+               a.kv_heads, st);
+  return MAXSIM_OK;
+}
+
+}  // extern "C"

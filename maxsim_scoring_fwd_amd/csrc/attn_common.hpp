@@ -1,0 +1,370 @@
+// Pieces shared by the attention kernels (include/maxsim.h, maxsim_attention).
+//
+// All matrix work runs on 32x32 tiles. Accumulator layout: lane l holds column l % 32, and
+// element r of it is row (r & 3) + 8 * (r >> 2) + 4 * (l / 32). Operands: A's lane holds row
+// l % 32, B's lane column l % 32, and each lane half a share of the contraction index.
+//
+// The kernels compute scores so that the index they reduce over next runs along the
+// accumulator's rows, i.e. along a lane's own registers: S^T = K Q^T in the forward and dQ
+// kernels (a lane holds one query's scores), S = Q K^T in the dK / dV kernel (a lane holds one
+// key's). Then 8 consecutive registers are, as they stand, a B operand of the following
+// product: half 0 holds rows 0-3 and 8-11 of 16, half 1 rows 4-7 and 12-15. The A operand of
+// that product has to come in the same row order, which two transposing LDS reads deliver
+// (each gives a 16-lane group 4 rows x 16 columns, lane i the 4 values of column i).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.hpp"
+#include "doc_lookup.hpp"
+
+namespace maxsim {
+
+// Score forms: plain scale; scale and distance bias; tanh cap and bias (slope 0 without one).
+enum { ATTN_PLAIN = 0, ATTN_BIAS = 1, ATTN_CAP = 2 };
+
+struct AttnArgs {
+  const char *q, *k, *v;
+  int64_t q_doc, k_doc, v_doc;     // byte strides of documents (fixed layout)
+  int64_t q_head, k_head, v_head;  // of heads
+  int q_tok, k_tok, v_tok;         // of tokens
+  const int64_t *offsets;
+  int64_t n_tokens, n_docs;
+  int nd;
+  const int32_t *lens;
+  const int32_t *prefix;
+  int heads, kv_heads, d, causal;
+  float softcap, scale;
+  const float *slopes;
+  char *o;                 // [rows][heads][d]
+  float *lse;              // [heads][rows]
+  int64_t rows;            // rows of o: all tokens
+  int64_t slots;           // tiles along the tokens
+  int tiles_per_doc;       // fixed layout
+  // backward
+  const char *dO;          // [rows][heads][d]
+  const float *delta;      // [heads][rows]: <dO, o>
+  const float *grad_scale; // fp16: power of two that dS is scaled by before its rounding
+  char *dq, *dk, *dv;      // [rows][heads or kv_heads][d]
+};
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr int ATTN_THREADS = 256;
+constexpr int ATTN_ROWS = 128;  // tokens of a workgroup's tile: 32 to a wave
+
+template <int DT> struct AttnElem;
+template <> struct AttnElem<DT_BF16> { using type = __bf16; };
+template <> struct AttnElem<DT_FP16> { using type = _Float16; };
+template <> struct AttnElem<DT_FP32> { using type = float; };
+
+__device__ __forceinline__ f32x16_t zero16() {
+  f32x16_t z;
+#pragma unroll
+  for (int i = 0; i < 16; i++) z[i] = 0.0f;
+  return z;
+}
+
+// One 32-byte step of rows of A times rows of B: half h of the wave holds bytes 16 h .. 16 h + 15
+// of the step. The same bytes feed the same contraction index on both sides.
+template <int DT> __device__ __forceinline__ f32x16_t mma_rows(u32x4_t a, u32x4_t b, f32x16_t c) {
+  if constexpr (DT == DT_BF16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  } else if constexpr (DT == DT_FP16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a),
+                                                  __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+  } else {
+    const uint32_t a0 = a.x, a1 = a.y, a2 = a.z, a3 = a.w, b0 = b.x, b1 = b.y, b2 = b.z, b3 = b.w;
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a0), __uint_as_float(b0), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a1), __uint_as_float(b1), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a2), __uint_as_float(b2), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a3), __uint_as_float(b3), c, 0, 0, 0);
+    return c;
+  }
+}
+
+// A 32x32 accumulator as the B operand of the next product: rounded to the storage type (to
+// nearest even) for the 16-bit types, as it is for fp32.
+template <int DT> struct Packed {
+  u32x4_t f[2];
+  __device__ __forceinline__ void set(const f32x16_t &s) {
+    using T = typename AttnElem<DT>::type;
+    typedef T v8 __attribute__((ext_vector_type(8)));
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      v8 x;
+#pragma unroll
+      for (int e = 0; e < 8; e++) x[e] = (T)s[8 * t + e];
+      f[t] = __builtin_bit_cast(u32x4_t, x);
+    }
+  }
+};
+template <> struct Packed<DT_FP32> {
+  f32x16_t f;
+  __device__ __forceinline__ void set(const f32x16_t &s) { f = s; }
+};
+
+// acc += X^T[columns c0 .. c0 + 31, rows r0 .. r0 + 31] * P, X row-major in LDS with rows of
+// ROWB bytes. `x` is the tile's first byte plus this lane's tr_lane_offset.
+template <int DT, int ROWB>
+__device__ __forceinline__ int tr_lane_offset() {
+  const int l = threadIdx.x & 63, h = l >> 5;
+  if constexpr (DT == DT_FP32) return 4 * h * ROWB + (l & 31) * 4;
+  else return (4 * h + ((l & 15) >> 2)) * ROWB + ((l >> 4) & 1) * 32 + (l & 3) * 8;
+}
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
+
+template <int DT, int ROWB>
+__device__ __forceinline__ f32x16_t mma_cols(const char *x, int r0, int c0, const Packed<DT> &p,
+                                             f32x16_t acc) {
+  if constexpr (DT == DT_FP32) {
+#pragma unroll
+    for (int r = 0; r < 16; r++) {
+      const float a = *(const float *)(x + (r0 + (r & 3) + 8 * (r >> 2)) * ROWB + c0 * 4);
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p.f[r], acc, 0, 0, 0);
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      typedef __attribute__((address_space(3))) s16x4_t lds_v4;
+      const char *at = x + (r0 + 16 * t) * ROWB + c0 * 2;
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(lds_char *)at);
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(lds_char *)(at + 8 * ROWB));
+      typedef short s16x8_t __attribute__((ext_vector_type(8)));
+      const s16x8_t a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      acc = mma_rows<DT>(__builtin_bit_cast(u32x4_t, a), p.f[t], acc);
+    }
+  }
+  return acc;
+}
+
+// Rows of a head in LDS: DP columns (the head's size rounded up; the rest zeros) plus padding
+// that keeps 16-byte reads of 8 consecutive rows, and the transposing reads' 4 rows x 32 bytes,
+// on different banks.
+template <int DT, int DP> struct RowLayout {
+  static constexpr int eb = Elem<DT>::bytes;
+  static constexpr int chunks = DP * eb / 16;  // 16-byte chunks of a row
+  static constexpr int steps = DP * eb / 32;   // mma_rows steps of a row
+  static constexpr int bytes = DP * eb + 16;
+};
+
+// Copies ROWS rows of a head from global memory into LDS through registers: load() issues the
+// loads, store() writes them, so a tile travels while the one before is worked on.
+template <int DT, int DP, int ROWS> struct Stage {
+  using L = RowLayout<DT, DP>;
+  static constexpr int total = ROWS * L::chunks;
+  static constexpr int n = (total + ATTN_THREADS - 1) / ATTN_THREADS;
+  u32x4_t r[n];
+
+  // base: first row of the tile (uniform); rows past the last valid one repeat it, so that
+  // nothing outside the document is read and what follows stays finite.
+  __device__ __forceinline__ void load(const char *base, int stride, int valid, int row_bytes) {
+#pragma unroll
+    for (int i = 0; i < n; i++) {
+      const int at = threadIdx.x + i * ATTN_THREADS;
+      const int c = at % L::chunks;
+      int row = at / L::chunks;
+      row = row < valid ? row : valid - 1;
+      u32x4_t z = {0, 0, 0, 0};
+      if ((total % ATTN_THREADS == 0 || at < total) && c * 16 < row_bytes)
+        z = *(const u32x4_t *)(base + (uint32_t)(row * stride + c * 16));
+      r[i] = z;
+    }
+  }
+  __device__ __forceinline__ void store(char *lds) const {
+#pragma unroll
+    for (int i = 0; i < n; i++) {
+      const int at = threadIdx.x + i * ATTN_THREADS;
+      if (total % ATTN_THREADS == 0 || at < total)
+        *(u32x4_t *)(lds + at / L::chunks * L::bytes + at % L::chunks * 16) = r[i];
+    }
+  }
+};
+
+// This lane's share of 32 rows as an mma_rows operand held in registers: row l % 32 (clamped to
+// the last valid one), every step's 16 bytes; columns past the head's size are zero.
+template <int DT, int DP> struct Held {
+  using L = RowLayout<DT, DP>;
+  u32x4_t f[L::steps];
+  __device__ __forceinline__ void load(const char *base, int64_t stride, int row, int row_bytes) {
+    const int h = (threadIdx.x & 63) >> 5;
+    const char *p = base + row * stride;
+#pragma unroll
+    for (int s = 0; s < L::steps; s++) {
+      u32x4_t z = {0, 0, 0, 0};
+      if (s * 32 + h * 16 < row_bytes) z = load16(p + s * 32 + h * 16);
+      f[s] = z;
+    }
+  }
+};
+
+// 32 rows of an LDS tile times held columns.
+template <int DT, int DP>
+__device__ __forceinline__ f32x16_t mma_tile(const char *tile, const Held<DT, DP> &b) {
+  using L = RowLayout<DT, DP>;
+  const int l = threadIdx.x & 63;
+  const char *p = tile + (l & 31) * L::bytes + (l >> 5) * 16;
+  f32x16_t acc = zero16();
+#pragma unroll
+  for (int s = 0; s < L::steps; s++) acc = mma_rows<DT>(load16(p + 32 * s), b.f[s], acc);
+  return acc;
+}
+
+__device__ __forceinline__ int acc_row(int r) { return (r & 3) + 8 * (r >> 2); }
+
+// Constants of the scores, in units of log 2 (the exponentials are powers of two).
+struct ScoreForm {
+  float a, b, slope;
+};
+template <int DT, int MODE>
+__device__ __forceinline__ ScoreForm score_form(const AttnArgs &a, int head) {
+  ScoreForm f;
+  f.slope = MODE != ATTN_PLAIN && a.slopes ? a.slopes[head] * LOG2E : 0.0f;
+  if (MODE == ATTN_CAP) {
+    f.a = a.scale / a.softcap * (DT == DT_FP32 ? 1.0f : 2.0f * LOG2E);
+    f.b = a.softcap * LOG2E;
+  } else {
+    f.a = a.scale * LOG2E;
+    f.b = 0.0f;
+  }
+  return f;
+}
+
+// A product of q and k to its score: scale, cap and bias. dist: i - j. keep: the cap's slope
+// 1 - tanh^2, for the backward.
+// tanh(z) = 1 - 2 / (1 + exp(2 z)): off by about 1e-7 absolutely, which 16-bit inputs do not
+// see; fp32 takes tanhf.
+template <int DT, int MODE>
+__device__ __forceinline__ float score(const ScoreForm &f, float x, float dist, float *keep) {
+  if constexpr (MODE == ATTN_PLAIN) return x * f.a;
+  else if constexpr (MODE == ATTN_BIAS) return __builtin_fmaf(-f.slope, __builtin_fabsf(dist), x * f.a);
+  else {
+    float y;
+    if constexpr (DT == DT_FP32) {
+      const float t = tanhf(x * f.a);
+      y = f.b * t;
+      if (keep) *keep = __builtin_fmaf(-t, t, 1.0f);
+    } else {
+      const float r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * f.a));
+      y = __builtin_fmaf(-2.0f * f.b, r, f.b);
+      if (keep) *keep = 4.0f * r * (1.0f - r);
+    }
+    return __builtin_fmaf(-f.slope, __builtin_fabsf(dist), y);
+  }
+}
+
+// Where a workgroup works: a tile of a document's rows, and a head.
+struct AttnTile {
+  int64_t row0;    // first row of the document, among all rows
+  int64_t q, k, v; // byte offsets of the document's rows
+  int rows;        // rows of the span (its length, or nd)
+  int len;         // tokens that exist
+  int first;       // first row of the tile
+  int prefix;      // keys below it are visible to every row; len for no causal mask
+  int head;
+};
+
+// Workgroups of one key/value head follow each other on one XCD (workgroups are dealt to the 8
+// XCDs in turn), so that its L2 serves the keys and values that they share.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t n) {
+  const uint32_t x = id & 7, per = n >> 3, more = n & 7;
+  return x * per + (x < more ? x : more) + (id >> 3);
+}
+
+// False where the tile does not exist. group_heads: heads a workgroup's head index runs over
+// (all, or the key/value heads).
+__device__ __forceinline__ bool locate(const AttnArgs &a, int rows, int n_heads, AttnTile &t) {
+  const uint32_t id = xcd_order(blockIdx.x, gridDim.x);
+  const uint32_t group = (uint32_t)n_heads / a.kv_heads;
+  const uint32_t per_kv = (uint32_t)a.slots * group;
+  const uint32_t kv = id / per_kv, in = id - kv * per_kv;
+  int64_t slot = in / group;
+  t.head = kv * group + (in - (uint32_t)slot * group);
+  // with a causal mask the last tiles have the most keys: they start first
+  if (a.causal) slot = a.slots - 1 - slot;
+  int64_t doc;
+  if (a.offsets) {
+    const TileSpan s = find_tile(a.offsets, a.n_docs, a.n_tokens, slot, rows);
+    if (s.first >= s.len) return false;
+    t.row0 = s.begin;
+    t.rows = (int)s.len;
+    t.len = s.doc < 0 ? 0 : t.rows;
+    t.first = (int)s.first;
+    doc = s.doc;
+    t.q = t.row0 * a.q_tok;
+    t.k = t.row0 * a.k_tok;
+    t.v = t.row0 * a.v_tok;
+  } else {
+    doc = slot / a.tiles_per_doc;
+    t.first = (int)(slot - doc * a.tiles_per_doc) * rows;
+    t.row0 = doc * a.nd;
+    t.rows = a.nd;
+    const int n = a.lens ? uniform(a.lens[doc]) : a.nd;
+    t.len = n < 0 ? 0 : (n < a.nd ? n : a.nd);
+    t.q = doc * a.q_doc;
+    t.k = doc * a.k_doc;
+    t.v = doc * a.v_doc;
+  }
+  t.prefix = t.len;
+  if (a.causal) {
+    const int p = a.prefix && doc >= 0 ? a.prefix[doc] : 0;
+    t.prefix = p < 0 ? 0 : (p < t.len ? p : t.len);
+  }
+  t.row0 = uniform(t.row0);
+  t.q = uniform(t.q);
+  t.k = uniform(t.k);
+  t.v = uniform(t.v);
+  t.rows = uniform(t.rows);
+  t.len = uniform(t.len);
+  t.first = uniform(t.first);
+  t.prefix = uniform(t.prefix);
+  t.head = uniform(t.head);
+  return true;
+}
+
+// Keys that row i sees: those below the result.
+__device__ __forceinline__ int visible(const AttnArgs &a, const AttnTile &t, int i) {
+  if (!a.causal) return t.len;
+  const int n = i + 1 > t.prefix ? i + 1 : t.prefix;
+  return n < t.len ? n : t.len;
+}
+
+// Stores a transposed accumulator (this lane: row `row` of the output, columns c0 + ...) times f.
+template <int DT>
+__device__ __forceinline__ void store_cols(char *row, int c0, int d, const f32x16_t &acc, float f) {
+  using T = typename AttnElem<DT>::type;
+  const int h = (threadIdx.x & 63) >> 5;
+  typedef T v4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+  for (int g = 0; g < 4; g++) {
+    const int c = c0 + 8 * g + 4 * h;
+    v4 x;
+#pragma unroll
+    for (int e = 0; e < 4; e++) x[e] = (T)(acc[4 * g + e] * f);
+    if (c < d) *(v4 *)(row + c * sizeof(T)) = x;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void zero_row(char *row, int d) {
+  const int h = (threadIdx.x & 63) >> 5;
+  const u32x4_t z = {0, 0, 0, 0};
+  for (int c = h * 16; c < d * Elem<DT>::bytes; c += 32) *(u32x4_t *)(row + c) = z;
+}
+
+__device__ __forceinline__ float half_max(float v) {
+  uint32_t a, b;
+  row_pair<32>(__float_as_uint(v), a, b);
+  return __builtin_fmaxf(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  uint32_t a, b;
+  row_pair<32>(__float_as_uint(v), a, b);
+  return __uint_as_float(a) + __uint_as_float(b);
+}
+
+}  // namespace maxsim

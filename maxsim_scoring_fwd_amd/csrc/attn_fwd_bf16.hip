@@ -1,0 +1,5 @@
+// Attention fwd kernels, bf16.
+#include "attn_dispatch.hpp"
+#include "attn_fwd_kernel.hpp"
+
+MAXSIM_ATTN_PICK(attn_fwd_bf16, attn_fwd_kernel, DT_BF16)

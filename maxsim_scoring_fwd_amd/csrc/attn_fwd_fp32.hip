@@ -1,0 +1,5 @@
+// Attention fwd kernels, fp32.
+#include "attn_dispatch.hpp"
+#include "attn_fwd_kernel.hpp"
+
+MAXSIM_ATTN_PICK(attn_fwd_fp32, attn_fwd_kernel, DT_FP32)

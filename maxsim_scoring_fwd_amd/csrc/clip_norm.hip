@@ -1,0 +1,218 @@
+// Global gradient norm over many tensors, and clipping (include/maxsim.h,
+// maxsim_clip_grad_norm):
+//   norm = sqrt(sum over all tensors of g^2),  out = g * min(1, max_norm / (norm + 1e-6))
+// Two passes over the data, since no output is known before the whole norm: the first leaves
+// one partial sum per workgroup, the second sums the partials (every workgroup for itself, in
+// one order, so all hold the same norm) and scales. The second pass walks the chunks backwards:
+// what the first read last is what the caches still hold.
+#include <hip/hip_runtime.h>
+
+#include "host_common.hpp"
+
+using namespace maxsim;
+
+namespace {
+
+constexpr int CLIP_THREADS = 256;
+constexpr int CLIP_TENSORS = 96;      // per launch: the table travels in the kernel arguments
+constexpr int CLIP_CHUNK = 16384;     // elements of a workgroup's piece of a tensor
+constexpr int CLIP_GRID = 1024;       // most workgroups, and partial sums, of a launch
+
+struct ClipTable {
+  const void *src[CLIP_TENSORS];
+  void *dst[CLIP_TENSORS];
+  int64_t numel[CLIP_TENSORS];
+  uint32_t first[CLIP_TENSORS];  // first chunk of the tensor
+  uint8_t dtype[CLIP_TENSORS];
+  uint8_t wide[CLIP_TENSORS];  // 16-byte vectors on both sides
+  int n;
+  uint32_t chunks;
+};
+
+// The tensor that holds a chunk: the last one whose first chunk is not past it. Tensors without
+// elements have no chunk and are not in the table.
+__device__ __forceinline__ int tensor_of(const ClipTable &t, uint32_t chunk) {
+  int lo = 0, hi = t.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (t.first[mid] <= chunk) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Sum over the workgroup in a fixed order, in every thread.
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double part[CLIP_THREADS / 64];
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64] = v;
+  __syncthreads();
+  double s = 0;
+  for (int i = 0; i < CLIP_THREADS / 64; i++) s += part[i];
+  __syncthreads();
+  return s;
+}
+
+template <typename T> struct Vec16 {
+  static constexpr int n = 16 / sizeof(T);
+  T e[n];
+} __attribute__((aligned(16)));
+
+// Squares are summed in 64 bits: no overflow of large gradients, no loss of many small ones.
+template <typename T>
+__device__ __forceinline__ double squares(const T *p, int64_t n, bool wide) {
+  double s = 0;
+  if (wide) {
+    using V = Vec16<T>;
+    const int64_t nv = n / V::n;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < nv; i += CLIP_THREADS) {
+      const V v = ((const V *)p)[i];
+#pragma unroll
+      for (int e = 0; e < V::n; e++) s = __builtin_fma((double)(float)v.e[e], (double)(float)v.e[e], s);
+    }
+    for (int64_t i = nv * V::n + threadIdx.x; i < n; i += CLIP_THREADS)
+      s = __builtin_fma((double)(float)p[i], (double)(float)p[i], s);
+  } else {
+    for (int64_t i = threadIdx.x; i < n; i += CLIP_THREADS)
+      s = __builtin_fma((double)(float)p[i], (double)(float)p[i], s);
+  }
+  return s;
+}
+
+template <typename T>
+__device__ __forceinline__ void scaled(const T *p, T *o, int64_t n, bool wide, float c) {
+  if (wide) {
+    using V = Vec16<T>;
+    const int64_t nv = n / V::n;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < nv; i += CLIP_THREADS) {
+      V v = ((const V *)p)[i];
+#pragma unroll
+      for (int e = 0; e < V::n; e++) v.e[e] = (T)((float)v.e[e] * c);
+      ((V *)o)[i] = v;
+    }
+    for (int64_t i = nv * V::n + threadIdx.x; i < n; i += CLIP_THREADS) o[i] = (T)((float)p[i] * c);
+  } else {
+    for (int64_t i = threadIdx.x; i < n; i += CLIP_THREADS) o[i] = (T)((float)p[i] * c);
+  }
+}
+
+__global__ void __launch_bounds__(CLIP_THREADS) clip_squares_kernel(const ClipTable t, double *part) {
+  double s = 0;
+  for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const int k = tensor_of(t, c);
+    const int64_t at = (int64_t)(c - t.first[k]) * CLIP_CHUNK;
+    const int64_t n = t.numel[k] - at < CLIP_CHUNK ? t.numel[k] - at : CLIP_CHUNK;
+    const bool w = t.wide[k];
+    switch (t.dtype[k]) {
+    case MAXSIM_BF16: s += squares((const __bf16 *)t.src[k] + at, n, w); break;
+    case MAXSIM_FP16: s += squares((const _Float16 *)t.src[k] + at, n, w); break;
+    default: s += squares((const float *)t.src[k] + at, n, w); break;
+    }
+  }
+  s = block_sum(s);
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+__global__ void __launch_bounds__(CLIP_THREADS)
+clip_scale_kernel(const ClipTable t, const double *part, int n_part, double max_norm, float *norm,
+                  int write_norm) {
+  double s = 0;
+  for (int i = threadIdx.x; i < n_part; i += CLIP_THREADS) s += part[i];
+  s = __builtin_sqrt(block_sum(s));
+  if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)s;
+  // a NaN norm passes on into the factor and so into every gradient: it is not hidden
+  double f = max_norm / (s + 1e-6);
+  if (f > 1.0) f = 1.0;
+  const float c = (float)f;
+  for (int64_t i = (int64_t)((t.chunks - 1 - blockIdx.x) / gridDim.x) * gridDim.x + blockIdx.x;
+       i >= 0 && t.chunks; i -= gridDim.x) {
+    const int k = tensor_of(t, (uint32_t)i);
+    if (c == 1.0f && t.src[k] == t.dst[k]) continue;  // nothing to change
+    const int64_t at = (i - t.first[k]) * CLIP_CHUNK;
+    const int64_t n = t.numel[k] - at < CLIP_CHUNK ? t.numel[k] - at : CLIP_CHUNK;
+    const bool w = t.wide[k];
+    switch (t.dtype[k]) {
+    case MAXSIM_BF16: scaled((const __bf16 *)t.src[k] + at, (__bf16 *)t.dst[k] + at, n, w, c); break;
+    case MAXSIM_FP16:
+      scaled((const _Float16 *)t.src[k] + at, (_Float16 *)t.dst[k] + at, n, w, c);
+      break;
+    default: scaled((const float *)t.src[k] + at, (float *)t.dst[k] + at, n, w, c); break;
+    }
+  }
+}
+
+// Tensors [from, from + CLIP_TENSORS) of the caller's list that have elements.
+void fill_table(ClipTable &t, const void *const *grads, void *const *outs, const int64_t *numel,
+                const int32_t *dtypes, int from, int to) {
+  t.n = 0;
+  t.chunks = 0;
+  for (int i = from; i < to; i++) {
+    if (numel[i] == 0) continue;
+    const int k = t.n++;
+    t.src[k] = grads[i];
+    t.dst[k] = outs ? outs[i] : const_cast<void *>(grads[i]);
+    t.numel[k] = numel[i];
+    t.dtype[k] = (uint8_t)dtypes[i];
+    t.wide[k] = aligned(t.src[k], 16) && aligned(t.dst[k], 16);
+    t.first[k] = t.chunks;
+    t.chunks += (uint32_t)((numel[i] + CLIP_CHUNK - 1) / CLIP_CHUNK);
+  }
+}
+
+unsigned grid_of(const ClipTable &t) {
+  return t.chunks < CLIP_GRID ? (t.chunks ? t.chunks : 1) : CLIP_GRID;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t maxsim_clip_grad_norm_workspace_size(int n_tensors) {
+  if (n_tensors < 0) return 0;
+  const size_t launches = n_tensors ? ((size_t)n_tensors + CLIP_TENSORS - 1) / CLIP_TENSORS : 1;
+  return launches * CLIP_GRID * sizeof(double);
+}
+
+int maxsim_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *numel,
+                          const int32_t *dtypes, int n_tensors, double max_norm, float *norm,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+  if (n_tensors < 0 || !(max_norm >= 0)) return MAXSIM_ERR_SHAPE;
+  if (!norm || !workspace || (n_tensors && (!grads || !numel || !dtypes))) return MAXSIM_ERR_NULL;
+  if (!aligned(norm, 4) || !aligned(workspace, 8)) return MAXSIM_ERR_ALIGN;
+  if (workspace_bytes < maxsim_clip_grad_norm_workspace_size(n_tensors)) return MAXSIM_ERR_SHAPE;
+  for (int i = 0; i < n_tensors; i++) {
+    const int eb = elem_bytes(dtypes[i]);
+    if (eb == 0) return MAXSIM_ERR_DTYPE;
+    if (numel[i] < 0 || numel[i] > ((int64_t)1 << 36)) return MAXSIM_ERR_SHAPE;
+    if (numel[i] == 0) continue;
+    if (!grads[i] || (outs && !outs[i])) return MAXSIM_ERR_NULL;
+    if (!aligned(grads[i], eb) || (outs && !aligned(outs[i], eb))) return MAXSIM_ERR_ALIGN;
+  }
+  DeviceInfo di;
+  int rc = current_device(di);
+  if (rc != MAXSIM_OK) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  double *part = (double *)workspace;
+  ClipTable t;
+  int n_part = 0;
+  for (int from = 0; from == 0 || from < n_tensors; from += CLIP_TENSORS) {
+    const int to = n_tensors - from < CLIP_TENSORS ? n_tensors : from + CLIP_TENSORS;
+    fill_table(t, grads, outs, numel, dtypes, from, to);
+    const unsigned g = grid_of(t);
+    hipLaunchKernelGGL(clip_squares_kernel, dim3(g), dim3(CLIP_THREADS), 0, st, t, part + n_part);
+    if (hipGetLastError() != hipSuccess) return MAXSIM_ERR_LAUNCH;
+    n_part += (int)g;
+  }
+  for (int from = 0; from == 0 || from < n_tensors; from += CLIP_TENSORS) {
+    const int to = n_tensors - from < CLIP_TENSORS ? n_tensors : from + CLIP_TENSORS;
+    if (n_tensors > CLIP_TENSORS) fill_table(t, grads, outs, numel, dtypes, from, to);
+    hipLaunchKernelGGL(clip_scale_kernel, dim3(grid_of(t)), dim3(CLIP_THREADS), 0, st, t, part,
+                       n_part, max_norm, norm, from == 0);
+    if (hipGetLastError() != hipSuccess) return MAXSIM_ERR_LAUNCH;
+  }
+  return MAXSIM_OK;
+}
+
+}  // extern "C"
