@@ -16,7 +16,9 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
+import struct
 from array import array
 
 import torch
@@ -39,20 +41,9 @@ class MaxSimError(RuntimeError):
         self.status = status
 
 
-class _AttentionTensor(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64), ("doc_stride", ctypes.c_int64)]
-
-
-class _AttentionDesc(ctypes.Structure):
-    _fields_ = [("q", _AttentionTensor), ("k", _AttentionTensor), ("v", _AttentionTensor),
-                ("doc_offsets", ctypes.c_void_p), ("doc_lens", ctypes.c_void_p),
-                ("n_tokens", ctypes.c_int64), ("n_docs", ctypes.c_int64),
-                ("prefix_lens", ctypes.c_void_p), ("slopes", ctypes.c_void_p),
-                ("nd", ctypes.c_int), ("n_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
-                ("d", ctypes.c_int), ("dtype", ctypes.c_int), ("causal", ctypes.c_int),
-                ("softcap", ctypes.c_float), ("scale", ctypes.c_float)]
-
+# maxsim_attention_desc: q, k and v (address; token, head and document stride), offsets, lengths,
+# tokens, documents, prefixes, slopes; nd, heads, key/value heads, d, dtype, causal; cap, scale
+_ATTENTION_DESC = struct.Struct("@" + "Pqqq" * 3 + "PPqqPP" + "6i" + "2f")
 
 _lib_handle = None
 
@@ -86,9 +77,8 @@ def lib() -> ctypes.CDLL:
         f32, f64, sz = ctypes.c_float, ctypes.c_double, ctypes.c_size_t
         L.maxsim_rotary.argtypes = [vp, i64, i32, i32, i64, i64, i32, vp, i32, i32, f32, i32, vp,
                                     i64, vp, vp, i64, i64, vp]
-        L.maxsim_attention.argtypes = [ctypes.POINTER(_AttentionDesc), vp, vp, vp]
-        L.maxsim_attention_backward.argtypes = [ctypes.POINTER(_AttentionDesc), vp, vp, vp, vp,
-                                                vp, vp, vp, sz, vp]
+        L.maxsim_attention.argtypes = [vp, vp, vp, vp]
+        L.maxsim_attention_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.maxsim_attention_backward_workspace_size.argtypes = [i64, i32]
         L.maxsim_attention_backward_workspace_size.restype = sz
         L.maxsim_clip_grad_norm.argtypes = [vp, vp, vp, vp, i32, f64, vp, vp, sz, vp]
@@ -123,7 +113,8 @@ def _dev(t: torch.Tensor | None, name: str):
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without making the Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -157,7 +148,7 @@ def _need(t, name: str, dtypes, shape=None, numel=None, dim=None):
                          f"got {t.dtype}")
     if dim is not None and t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, got shape {tuple(t.shape)}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must hold {numel} elements, got {t.numel()}")
@@ -473,6 +464,11 @@ def _ours(t: torch.Tensor, stream) -> torch.Tensor:
     return t
 
 
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    """A new contiguous tensor like t, for work on `stream`."""
+    return _ours(torch.empty_like(t, memory_format=torch.contiguous_format), stream)
+
+
 _ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
 
 
@@ -490,30 +486,37 @@ def maxsim_rotary(x: torch.Tensor, freq: torch.Tensor, doc_offsets: torch.Tensor
     _need(x, "x", _FLOAT_STORAGE, dim=3)
     _need(freq, "freq", torch.float32, dim=1)
     n, heads, d = x.shape
-    rot = 2 * freq.numel()
+    x_token, x_head, x_entry = x.stride()
+    half, docs = freq.numel(), 0
     if layout not in _ROTARY_LAYOUT:
         raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")
-    if rot < 2 or rot > d:
-        raise ValueError(f"freq has {freq.numel()} entries for heads of d = {d}")
-    if doc_offsets is not None and positions is not None:
-        raise ValueError("give doc_offsets or positions, not both")
-    _need(positions, "positions", torch.int32, shape=(n,))
-    _need(doc_offsets, "doc_offsets", torch.int64, dim=1)
-    if doc_offsets is not None and doc_offsets.numel() < 1:
-        raise ValueError("doc_offsets needs n_docs + 1 >= 1 entries")
-    if x.stride(2) != 1:
+    if not 1 <= half <= d // 2:
+        raise ValueError(f"freq has {half} entries for heads of d = {d}")
+    if positions is not None:
+        if doc_offsets is not None:
+            raise ValueError("give doc_offsets or positions, not both")
+        _need(positions, "positions", torch.int32, shape=(n,))
+    elif doc_offsets is not None:
+        _need(doc_offsets, "doc_offsets", torch.int64, dim=1)
+        docs = doc_offsets.numel() - 1
+        if docs < 0:
+            raise ValueError("doc_offsets needs n_docs + 1 >= 1 entries")
+    if x_entry != 1:
         raise ValueError("x needs the entries of a head side by side")
     if out is None:
-        out = _ours(torch.empty((n, heads, d), dtype=x.dtype, device=x.device), stream)
-    _need(out, "out", x.dtype, shape=(n, heads, d))
-    if out.stride(2) != 1:
-        raise ValueError("out needs the entries of a head side by side")
+        out = _like(x, stream)
+        out_token, out_head = heads * d, d
+    else:
+        _need(out, "out", x.dtype, shape=x.shape)
+        out_token, out_head, out_entry = out.stride()
+        if out_entry != 1:
+            raise ValueError("out needs the entries of a head side by side")
+    dev = x.device
     _check(lib().maxsim_rotary(
-        _on(x, "x", x.device), n, heads, d, x.stride(0), x.stride(1), _dtype_code(x),
-        _dev(freq, "freq"), rot, _ROTARY_LAYOUT[layout], float(mscale), int(bool(inverse)),
-        _dev(doc_offsets, "doc_offsets"), 0 if doc_offsets is None else doc_offsets.numel() - 1,
-        _dev(positions, "positions"), _on(out, "out", x.device), out.stride(0), out.stride(1),
-        _stream(stream)), "maxsim_rotary")
+        _on(x, "x", dev), n, heads, d, x_token, x_head, _TORCH_DTYPE[x.dtype], _dev(freq, "freq"),
+        2 * half, _ROTARY_LAYOUT[layout], mscale, 1 if inverse else 0,
+        _dev(doc_offsets, "doc_offsets"), docs, _dev(positions, "positions"), _on(out, "out", dev),
+        out_token, out_head, _stream(stream)), "maxsim_rotary")
     return out
 
 
@@ -542,10 +545,9 @@ def rotary(x: torch.Tensor, freq: torch.Tensor, doc_offsets: torch.Tensor | None
     return RotaryFunction.apply(x, freq, doc_offsets, positions, layout, mscale)
 
 
-def _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap, slopes, scale):
-    """The library's description of an attention call, with the checks that it cannot make."""
-    packed = doc_offsets is not None
-    dim = 3 if packed else 4
+def _attention_refuse(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, slopes):
+    """Raises for the first argument of an attention call whose type or shape does not fit."""
+    dim = 4 if doc_offsets is None else 3
     _need(q, "q", _FLOAT_STORAGE, dim=dim)
     heads, d = q.shape[-2:]
     for t, name in ((k, "k"), (v, "v")):
@@ -557,37 +559,62 @@ def _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap
         raise ValueError(f"k has {kv} heads, v has {v.shape[-2]}")
     if kv < 1 or heads % kv:
         raise ValueError(f"{heads} query heads cannot share {kv} key/value heads")
-    if packed:
+    n_docs = q.shape[0]
+    if doc_offsets is not None:
         _need(doc_offsets, "doc_offsets", torch.int64, dim=1)
         if doc_offsets.numel() < 1:
             raise ValueError("doc_offsets needs n_docs + 1 >= 1 entries")
         if doc_lens is not None:
             raise ValueError("give doc_offsets or doc_lens, not both")
-        n_docs, nd, rows = doc_offsets.numel() - 1, 0, q.shape[0]
-    else:
-        n_docs, nd = q.shape[:2]
-        rows = n_docs * nd
-        _need(doc_lens, "doc_lens", torch.int32, shape=(n_docs,))
+        n_docs = doc_offsets.numel() - 1
+    _need(doc_lens, "doc_lens", torch.int32, shape=(n_docs,))
     if prefix_lens is not None and not causal:
         raise ValueError("prefix_lens needs causal")
     _need(prefix_lens, "prefix_lens", torch.int32, shape=(n_docs,))
     _need(slopes, "slopes", torch.float32, shape=(heads,))
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.stride(-1) != 1:
+            raise ValueError(f"{name} needs the entries of a head side by side")
+        _on(t, name, q.device)
+    raise ValueError("the arguments of the attention do not fit together")
+
+
+def _fits(t, dtype, shape) -> bool:
+    return t is None or (t.dtype == dtype and t.shape == shape)
+
+
+def _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap, slopes, scale):
+    """(the library's description of an attention call, heads, rows), with the checks that the
+    library cannot make: all in one condition, told apart only where it fails."""
+    sq, sk, dt, dev = q.shape, k.shape, q.dtype, q.device
+    tq, tk, tv = q.stride(), k.stride(), v.stride()
+    heads, d, kv = sq[-2], sq[-1], sk[-2]
     scale = d ** -0.5 if scale is None else float(scale)
     softcap = float(softcap or 0.0)
-    if not (scale > 0 and math.isfinite(scale)):
+    if not 0 < scale < math.inf:
         raise ValueError(f"scale must be positive and finite, got {scale}")
-    if not (softcap >= 0 and math.isfinite(softcap)):
+    if not 0 <= softcap < math.inf:
         raise ValueError(f"softcap must be finite and not negative, got {softcap}")
-
-    def tensor(t, name):
-        if t.stride(-1) != 1 and t.shape[-1] != 1:
-            raise ValueError(f"{name} needs the entries of a head side by side")
-        return _AttentionTensor(_on(t, name, q.device), t.stride(-3), t.stride(-2),
-                                0 if packed else t.stride(0))
-    return _AttentionDesc(
-        tensor(q, "q"), tensor(k, "k"), tensor(v, "v"), _dev(doc_offsets, "doc_offsets"),
-        _dev(doc_lens, "doc_lens"), rows, n_docs, _dev(prefix_lens, "prefix_lens"),
-        _dev(slopes, "slopes"), nd, heads, kv, d, _dtype_code(q), int(bool(causal)), softcap, scale)
+    if doc_offsets is not None:
+        docs, nd, rows, dim = doc_offsets.numel() - 1, 0, sq[0], 3
+        known = doc_lens is None and docs >= 0 and doc_offsets.dtype == torch.int64 and \
+            doc_offsets.dim() == 1
+    else:
+        docs, nd, dim = sq[0], sq[1], 4
+        rows = docs * nd
+        known = _fits(doc_lens, torch.int32, (docs,))
+    if not (known and dt in _TORCH_DTYPE and k.dtype == dt and v.dtype == dt and len(sq) == dim
+            and sk == v.shape and sk[:-2] == sq[:-2] and sk[-1] == d and kv and heads % kv == 0
+            and tq[-1] == 1 and tk[-1] == 1 and tv[-1] == 1 and q.is_cuda and k.device == dev
+            and v.device == dev and (prefix_lens is None or causal)
+            and _fits(prefix_lens, torch.int32, (docs,)) and _fits(slopes, torch.float32, (heads,))):
+        _attention_refuse(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, slopes)
+    return _ATTENTION_DESC.pack(
+        q.data_ptr(), tq[-3], tq[-2], tq[0], k.data_ptr(), tk[-3], tk[-2], tk[0],
+        v.data_ptr(), tv[-3], tv[-2], tv[0], _dev(doc_offsets, "doc_offsets") or 0,
+        _dev(doc_lens, "doc_lens") or 0, rows, docs, _dev(prefix_lens, "prefix_lens") or 0,
+        _dev(slopes, "slopes") or 0, nd, heads, kv, d, _TORCH_DTYPE[dt], 1 if causal else 0,
+        softcap, scale), heads, rows
 
 
 def maxsim_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -604,15 +631,16 @@ def maxsim_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     scores become softcap * tanh(score / softcap); slopes (fp32 [n_heads]): slope * |i - j| is
     taken off; scale: d ** -0.5 unless given. Returns (o shaped like q, lse fp32 [n_heads,
     tokens])."""
-    desc = _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap, slopes,
-                           scale)
-    shape = (desc.n_heads, desc.n_tokens)
+    desc, heads, rows = _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens,
+                                        softcap, slopes, scale)
     if out is None:
-        out = _ours(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream)
+        out = _like(q, stream)
+    else:
+        _need(out, "out", q.dtype, shape=q.shape)
     if lse is None:
-        lse = _ours(torch.empty(shape, dtype=torch.float32, device=q.device), stream)
-    _need(out, "out", q.dtype, shape=tuple(q.shape))
-    _need(lse, "lse", torch.float32, shape=shape)
+        lse = _ours(q.new_empty((heads, rows), dtype=torch.float32), stream)
+    else:
+        _need(lse, "lse", torch.float32, shape=(heads, rows))
     _check(lib().maxsim_attention(desc, _dev(out, "out"), _dev(lse, "lse"), _stream(stream)),
            "maxsim_attention")
     return out, lse
@@ -633,23 +661,22 @@ def maxsim_attention_backward(grad_o: torch.Tensor, q: torch.Tensor, k: torch.Te
                               dv=None, workspace=None, stream=None):
     """Gradients (dq, dk, dv) of maxsim_attention from its result's gradient grad_o and its
     outputs o and lse; None for what is not wanted. The other arguments are the forward's."""
-    desc = _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap, slopes,
-                           scale)
-    _need(grad_o, "grad_o", q.dtype, shape=tuple(q.shape))
-    _need(o, "o", q.dtype, shape=tuple(q.shape))
-    _need(lse, "lse", torch.float32, shape=(desc.n_heads, desc.n_tokens))
+    desc, heads, rows = _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens,
+                                        softcap, slopes, scale)
+    _need(grad_o, "grad_o", q.dtype, shape=q.shape)
+    _need(o, "o", q.dtype, shape=q.shape)
+    _need(lse, "lse", torch.float32, shape=(heads, rows))
     _need(workspace, "workspace", torch.uint8)
 
     def grad(g, like, name, want):
         if not want:
             return None
-        _need(g, name, like.dtype, shape=tuple(like.shape))
-        return g if g is not None else _ours(
-            torch.empty(like.shape, dtype=like.dtype, device=like.device), stream)
+        _need(g, name, like.dtype, shape=like.shape)
+        return _like(like, stream) if g is None else g
     dq, dk, dv = grad(dq, q, "dq", want_dq), grad(dk, k, "dk", want_dkv), grad(dv, v, "dv", want_dkv)
     if workspace is None:
-        workspace = _ours(torch.empty(attention_backward_workspace_size(desc.n_tokens, desc.n_heads),
-                                      dtype=torch.uint8, device=q.device), stream)
+        workspace = _ours(q.new_empty(attention_backward_workspace_size(rows, heads),
+                                      dtype=torch.uint8), stream)
     _check(lib().maxsim_attention_backward(
         desc, _dev(o, "o"), _dev(lse, "lse"), _dev(grad_o, "grad_o"), _dev(dq, "dq"),
         _dev(dk, "dk"), _dev(dv, "dv"), _dev(workspace, "workspace"), workspace.numel(),
@@ -693,6 +720,9 @@ def clip_grad_norm_workspace_size(n_tensors: int) -> int:
     return int(lib().maxsim_clip_grad_norm_workspace_size(n_tensors))
 
 
+_DTYPE_OF = operator.attrgetter("dtype")
+
+
 def maxsim_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
                           workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Scales a list of gradients (contiguous bf16, fp16 or fp32 tensors, mixed as they come) by
@@ -707,36 +737,36 @@ def maxsim_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor |
     max_norm = float(max_norm)
     if not max_norm >= 0:
         raise ValueError(f"max_norm must not be negative, got {max_norm}")
-    device = grads[0].device
-    for name, ts in (("grads", grads), ("out", outs if out is not None else [])):
-        for i, t in enumerate(ts):
-            if t.dtype not in _TORCH_DTYPE:
-                raise ValueError(f"{name}[{i}] has unsupported dtype {t.dtype}")
-            if not t.is_contiguous():
-                raise ValueError(f"{name}[{i}] must be contiguous")
-            if t.device != device or not t.is_cuda:
-                raise ValueError(f"{name}[{i}] must be a device tensor on the first one's device")
-    if out is not None:
-        for i, (g, o) in enumerate(zip(grads, outs)):
-            if o.dtype != g.dtype or o.shape != g.shape:
-                raise ValueError(f"out[{i}] is {o.dtype} {tuple(o.shape)}, the gradient "
-                                 f"{g.dtype} {tuple(g.shape)}")
+    each = grads if out is None else grads + outs
+    # whole lists at a time: an encoder has hundreds of gradients
+    if not set(map(_DTYPE_OF, each)) <= _TORCH_DTYPE.keys():
+        raise ValueError(f"unsupported dtype among {set(map(_DTYPE_OF, each))}")
+    if not all(map(torch.Tensor.is_contiguous, each)):
+        raise ValueError("every tensor must be contiguous")
+    devices = set(map(torch.Tensor.get_device, each))
+    if len(devices) != 1 or -1 in devices:
+        raise ValueError("every tensor must be a device tensor, all on one device")
     n = len(grads)
+    code = array("i", [_TORCH_DTYPE[t] for t in map(_DTYPE_OF, grads)])
+    numel = array("q", map(torch.Tensor.numel, grads))
+    if out is not None and (list(map(_DTYPE_OF, outs)) != list(map(_DTYPE_OF, grads)) or
+                            list(map(torch.Tensor.numel, outs)) != list(numel)):
+        raise ValueError("out must hold tensors of the gradients' dtypes and sizes")
+    ptrs = array("Q", map(torch.Tensor.data_ptr, each))
     if norm is None:
-        norm = _ours(torch.empty((), dtype=torch.float32, device=device), stream)
-    _need(norm, "norm", torch.float32, numel=1)
-    _need(workspace, "workspace", torch.uint8)
+        norm = _ours(torch.empty((), dtype=torch.float32, device=grads[0].device), stream)
+    else:
+        _need(norm, "norm", torch.float32, numel=1)
     if workspace is None:
         workspace = _ours(torch.empty(clip_grad_norm_workspace_size(n), dtype=torch.uint8,
-                                      device=device), stream)
-    src = array("Q", [t.data_ptr() for t in grads])
-    dst = None if out is None else array("Q", [t.data_ptr() for t in outs])
-    numel = array("q", [t.numel() for t in grads])
-    code = array("i", [_TORCH_DTYPE[t.dtype] for t in grads])
+                                      device=grads[0].device), stream)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    src = ptrs.buffer_info()[0]
     _check(lib().maxsim_clip_grad_norm(
-        src.buffer_info()[0], None if dst is None else dst.buffer_info()[0], numel.buffer_info()[0],
-        code.buffer_info()[0], n, max_norm, _dev(norm, "norm"), _dev(workspace, "workspace"),
-        workspace.numel(), _stream(stream)), "maxsim_clip_grad_norm")
+        src, None if out is None else src + 8 * n, numel.buffer_info()[0], code.buffer_info()[0], n,
+        max_norm, _dev(norm, "norm"), _dev(workspace, "workspace"), workspace.numel(),
+        _stream(stream)), "maxsim_clip_grad_norm")
     return norm
 
 

@@ -31,9 +31,9 @@ HIP_FLAGS = [
 ]
 
 
-# The encoder's operators (attention, rotary positions, clipping) meet NaN and infinities in
-# places that a mask or a norm has to handle, so their files keep NaN semantics.
-KEEP_NANS = ("attn_", "attention", "rotary", "clip_norm")
+# Clipping passes NaN and infinities on, and rotary positions the values that they are given:
+# these files keep NaN semantics.
+KEEP_NANS = ("rotary", "clip_norm")
 
 
 def flags_of(source: str) -> list[str]:

@@ -63,18 +63,17 @@ int fill(const maxsim_attention_desc *s, AttnArgs &a) {
   a.prefix = s->prefix_lens;
   a.heads = s->n_heads;
   a.kv_heads = s->n_kv_heads;
+  a.group = s->n_heads / s->n_kv_heads;
   a.d = s->d;
   a.causal = s->causal != 0;
   a.softcap = s->softcap;
   a.scale = s->scale;
   a.slopes = s->slopes;
-  if (packed) {
-    a.slots = a.n_tokens / ATTN_ROWS + a.n_docs + 2;
-  } else {
-    a.tiles_per_doc = (a.nd + ATTN_ROWS - 1) / ATTN_ROWS;
-    a.slots = a.n_docs * a.tiles_per_doc;
-  }
-  return a.slots * a.heads > 0x7fffffff ? MAXSIM_ERR_SHAPE : MAXSIM_OK;
+  a.tiles_per_doc = (uint32_t)(((int64_t)a.nd + ATTN_ROWS - 1) / ATTN_ROWS);
+  const int64_t slots = packed ? a.n_tokens / ATTN_ROWS + a.n_docs + 2 : a.n_docs * a.tiles_per_doc;
+  if (slots > 0x7fffffff || slots * a.heads > 0x7fffffff) return MAXSIM_ERR_SHAPE;
+  a.slots = (uint32_t)slots;
+  return MAXSIM_OK;
 }
 
 int mode_of(const AttnArgs &a) {
@@ -84,7 +83,7 @@ int mode_of(const AttnArgs &a) {
 // One workgroup for every tile of tokens and each of n_heads heads.
 int run(const void *fn, AttnArgs &a, int n_heads, hipStream_t st) {
   void *kargs[] = {&a};
-  if (hipLaunchKernel(fn, dim3((unsigned)(a.slots * n_heads)), dim3(ATTN_THREADS), kargs, 0, st) !=
+  if (hipLaunchKernel(fn, dim3(a.slots * (unsigned)n_heads), dim3(ATTN_THREADS), kargs, 0, st) !=
       hipSuccess) {
     (void)hipGetLastError();
     return MAXSIM_ERR_LAUNCH;

@@ -12,9 +12,9 @@ template <int DT, int DP, int MODE>
 __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a) {
   using L = RowLayout<DT, DP>;
   constexpr int BN = 32, OT = DP / 32, TILE = BN * L::bytes;
-  __shared__ __align__(16) char lds[2 * TILE];
+  __shared__ __align__(16) char lds[4 * TILE];  // two buffers: one barrier a tile
   AttnTile t;
-  if (!locate(a, ATTN_ROWS, a.heads, t)) return;
+  if (!locate(a, ATTN_ROWS, a.group, t)) return;
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave0 = t.first + (threadIdx.x >> 6) * 32;
   const int i = wave0 + (lane & 31);
@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
   Held<DT, DP> q, g;
   q.load(a.q + t.q + t.head * a.q_head, a.q_tok, iq, row_bytes);
   g.load(a.dO + (t.row0 * a.heads + t.head) * row_bytes, (int64_t)a.heads * row_bytes, iq, row_bytes);
-  const int kv = t.head / (a.heads / a.kv_heads);
+  const int kv = t.head / a.group;
   const char *kp = a.k + t.k + kv * a.k_head, *vp = a.v + t.v + kv * a.v_head;
   const ScoreForm form = score_form<DT, MODE>(a, t.head);
   const int vis = visible(a, t, iq), wave_least = visible(a, t, wave0);
@@ -45,17 +45,19 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
   f32x16_t acc[OT];
 #pragma unroll
   for (int c = 0; c < OT; c++) acc[c] = zero16();
-  char *const ldsk = lds, *const ldsv = lds + TILE;
-  const char *kt = ldsk + tr_lane_offset<DT, L::bytes>();
-  for (int j0 = 0; j0 < n_keys; j0 += BN) {
-    __syncthreads();
-    sk.store(ldsk);
-    sv.store(ldsv);
+  const int tr_lane = tr_lane_offset<DT, L::bytes>();
+  const int wave_most = visible(a, t, wave0 + 31 < t.len ? wave0 + 31 : t.len - 1);
+  int buf = 0;
+  for (int j0 = 0; j0 < n_keys; j0 += BN, buf ^= 2 * TILE) {
+    const char *const ldsk = lds + buf, *const ldsv = ldsk + TILE, *const kt = ldsk + tr_lane;
+    sk.store(lds + buf);
+    sv.store(lds + buf + TILE);
     __syncthreads();
     if (j0 + BN < n_keys) {
       sk.load(kp + (int64_t)(j0 + BN) * a.k_tok, a.k_tok, t.len - j0 - BN, row_bytes);
       sv.load(vp + (int64_t)(j0 + BN) * a.v_tok, a.v_tok, t.len - j0 - BN, row_bytes);
     }
+    if (wave0 >= t.len || j0 >= wave_most) continue;  // nothing for this wave's rows
     f32x16_t s = mma_tile<DT, DP>(ldsk, q);
     f32x16_t dp = mma_tile<DT, DP>(ldsv, g);
     const float dist0 = (float)(i - j0 - 4 * h);
@@ -87,10 +89,10 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
   constexpr int BM = 32, OT = DP / 32, TILE = BM * L::bytes;
   // fp16 P is rounded 2^8 times too large: rows over thousands of keys stay out of the subnormals
   constexpr float SHIFT = DT == DT_FP16 ? 8.0f : 0.0f;
-  __shared__ __align__(16) char lds[2 * TILE];
-  __shared__ __align__(16) float stat[2 * BM];
+  __shared__ __align__(16) char lds[4 * TILE];  // two buffers: one barrier a tile
+  __shared__ __align__(16) float stat[2][2 * BM];
   AttnTile t;
-  if (!locate(a, ATTN_ROWS, a.kv_heads, t)) return;
+  if (!locate(a, ATTN_ROWS, 1, t)) return;
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave0 = t.first + (threadIdx.x >> 6) * 32;
   const int j = wave0 + (lane & 31);
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
   Held<DT, DP> k, v;
   k.load(a.k + t.k + t.head * a.k_head, a.k_tok, jk, row_bytes);
   v.load(a.v + t.v + t.head * a.v_head, a.v_tok, jk, row_bytes);
-  const int group = a.heads / a.kv_heads;
+  const int group = a.group;
   // with a causal mask only rows from the key on see it, unless it lies in the prefix
   const int from = t.first >= t.prefix ? t.first : 0;
   const int jmask = j < t.prefix ? -1 : j;
@@ -140,16 +142,20 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
     dk[c] = zero16();
     dv[c] = zero16();
   }
-  char *const ldsq = lds, *const ldsg = lds + TILE;
-  const char *qt = ldsq + tr_lane_offset<DT, L::bytes>(), *gt = ldsg + tr_lane_offset<DT, L::bytes>();
-  for (int n = 0; n < total; n++) {
-    __syncthreads();
+  const int tr_lane = tr_lane_offset<DT, L::bytes>();
+  int buf = 0;
+  for (int n = 0; n < total; n++, buf ^= 1) {
+    char *const ldsq = lds + buf * 2 * TILE, *const ldsg = ldsq + TILE;
+    const char *const qt = ldsq + tr_lane, *const gt = ldsg + tr_lane;
+    const float *const stats = stat[buf];
     sq.store(ldsq);
     sg.store(ldsg);
-    if (threadIdx.x < 2 * BM) stat[threadIdx.x] = st;
+    if (threadIdx.x < 2 * BM) stat[buf][threadIdx.x] = st;
     __syncthreads();
     if (n + 1 < total) load(n + 1);
     const int i0 = from + n % n_tiles * BM;
+    // nothing where this wave has no keys, or where the tile's rows see none of them
+    if (wave0 >= t.len || (a.causal && wave0 >= t.prefix && wave0 > i0 + BM - 1)) continue;
     const ScoreForm form = score_form<DT, MODE>(a, t.head * group + n / n_tiles);
     f32x16_t s = mma_tile<DT, DP>(ldsq, k);
     f32x16_t dp = mma_tile<DT, DP>(ldsg, v);
@@ -157,8 +163,8 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
     const int hide = wave0 + 31 > i0 ? jmask - i0 - 4 * h : -1;  // rows below it do not see key j
 #pragma unroll
     for (int g4 = 0; g4 < 4; g4++) {
-      const f32x4_t ls = *(const f32x4_t *)(stat + 8 * g4 + 4 * h);
-      const f32x4_t de = *(const f32x4_t *)(stat + BM + 8 * g4 + 4 * h);
+      const f32x4_t ls = *(const f32x4_t *)(stats + 8 * g4 + 4 * h);
+      const f32x4_t de = *(const f32x4_t *)(stats + BM + 8 * g4 + 4 * h);
 #pragma unroll
       for (int e = 0; e < 4; e++) {
         const int r = 4 * g4 + e;

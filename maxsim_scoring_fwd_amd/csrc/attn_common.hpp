@@ -34,14 +34,14 @@ struct AttnArgs {
   int nd;
   const int32_t *lens;
   const int32_t *prefix;
-  int heads, kv_heads, d, causal;
+  int heads, kv_heads, group, d, causal;  // group: heads / kv_heads
   float softcap, scale;
   const float *slopes;
   char *o;                 // [rows][heads][d]
   float *lse;              // [heads][rows]
   int64_t rows;            // rows of o: all tokens
-  int64_t slots;           // tiles along the tokens
-  int tiles_per_doc;       // fixed layout
+  uint32_t slots;          // tiles along the tokens
+  uint32_t tiles_per_doc;  // fixed layout
   // backward
   const char *dO;          // [rows][heads][d]
   const float *delta;      // [heads][rows]: <dO, o>
@@ -235,7 +235,7 @@ __device__ __forceinline__ ScoreForm score_form(const AttnArgs &a, int head) {
 }
 
 // A product of q and k to its score: scale, cap and bias. dist: i - j. keep: the cap's slope
-// 1 - tanh^2, for the backward.
+// 1 - tanh^2, for the backward. The forward leaves the plain scale to the exponential's FMA.
 // tanh(z) = 1 - 2 / (1 + exp(2 z)): off by about 1e-7 absolutely, which 16-bit inputs do not
 // see; fp32 takes tanhf.
 template <int DT, int MODE>
@@ -275,15 +275,14 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t n) {
   return x * per + (x < more ? x : more) + (id >> 3);
 }
 
-// False where the tile does not exist. group_heads: heads a workgroup's head index runs over
-// (all, or the key/value heads).
-__device__ __forceinline__ bool locate(const AttnArgs &a, int rows, int n_heads, AttnTile &t) {
+// False where the tile does not exist. group: heads of the grid that share a key/value head
+// (1 where the grid runs over the key/value heads).
+__device__ __forceinline__ bool locate(const AttnArgs &a, int rows, uint32_t group, AttnTile &t) {
   const uint32_t id = xcd_order(blockIdx.x, gridDim.x);
-  const uint32_t group = (uint32_t)n_heads / a.kv_heads;
-  const uint32_t per_kv = (uint32_t)a.slots * group;
+  const uint32_t per_kv = a.slots * group;
   const uint32_t kv = id / per_kv, in = id - kv * per_kv;
-  int64_t slot = in / group;
-  t.head = kv * group + (in - (uint32_t)slot * group);
+  uint32_t slot = in / group;
+  t.head = kv * group + (in - slot * group);
   // with a causal mask the last tiles have the most keys: they start first
   if (a.causal) slot = a.slots - 1 - slot;
   int64_t doc;
@@ -300,7 +299,7 @@ __device__ __forceinline__ bool locate(const AttnArgs &a, int rows, int n_heads,
     t.v = t.row0 * a.v_tok;
   } else {
     doc = slot / a.tiles_per_doc;
-    t.first = (int)(slot - doc * a.tiles_per_doc) * rows;
+    t.first = (int)(slot - (uint32_t)doc * a.tiles_per_doc) * rows;
     t.row0 = doc * a.nd;
     t.rows = a.nd;
     const int n = a.lens ? uniform(a.lens[doc]) : a.nd;

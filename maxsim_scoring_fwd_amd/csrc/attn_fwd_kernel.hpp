@@ -10,14 +10,17 @@ template <int DT, int DP> struct FwdShape {
   static constexpr int lds = keys * RowLayout<DT, DP>::bytes;
 };
 
+template <int N> struct Blocks { static constexpr int value = N; };
+
 template <int DT, int DP, int MODE>
 __global__ void __launch_bounds__(ATTN_THREADS) attn_fwd_kernel(const AttnArgs a) {
   using L = RowLayout<DT, DP>;
   constexpr int BN = FwdShape<DT, DP>::keys, NT = BN / 32, OT = (DP + 31) / 32;
   constexpr int TILE = FwdShape<DT, DP>::lds;
-  __shared__ __align__(16) char lds[2 * TILE];
+  // two buffers of a K and a V tile: one barrier a tile
+  __shared__ __align__(16) char lds[4 * TILE];
   AttnTile t;
-  if (!locate(a, ATTN_ROWS, a.heads, t)) return;
+  if (!locate(a, ATTN_ROWS, a.group, t)) return;
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave0 = t.first + (threadIdx.x >> 6) * 32;
   const int i = wave0 + (lane & 31);
@@ -34,9 +37,10 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_fwd_kernel(const AttnArgs a
   const int iq = i < t.len ? i : t.len - 1;
   Held<DT, DP> q;
   q.load(a.q + t.q + t.head * a.q_head, a.q_tok, iq, row_bytes);
-  const int kv = t.head / (a.heads / a.kv_heads);
+  const int kv = t.head / a.group;
   const char *kp = a.k + t.k + kv * a.k_head, *vp = a.v + t.v + kv * a.v_head;
   const ScoreForm form = score_form<DT, MODE>(a, t.head);
+  const float post = MODE == ATTN_PLAIN ? form.a : 1.0f;  // factor left to the exponentials
   const int vis = visible(a, t, iq);
   const int wave_least = visible(a, t, wave0);
   const int last = t.first + ATTN_ROWS < t.len ? t.first + ATTN_ROWS - 1 : t.len - 1;
@@ -49,62 +53,79 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_fwd_kernel(const AttnArgs a
 #pragma unroll
   for (int c = 0; c < OT; c++) acc[c] = zero16();
   float m = -1e30f, sum = 0.0f;  // a finite start: exp2(-inf - m) is 0 for rows that see nothing yet
-  char *const ldsk = lds, *const ldsv = lds + TILE;
-  const char *vt = ldsv + tr_lane_offset<DT, L::bytes>();
+  const int tr_lane = TILE + tr_lane_offset<DT, L::bytes>();
+  const int wave_most = visible(a, t, wave0 + 31 < t.len ? wave0 + 31 : t.len - 1);
 
-  for (int j0 = 0; j0 < n_keys; j0 += BN) {
-    __syncthreads();
-    sk.store(ldsk);
-    sv.store(ldsv);
+  int buf = 0;
+  for (int j0 = 0; j0 < n_keys; j0 += BN, buf ^= 2 * TILE) {
+    const char *const ldsk = lds + buf, *const vt = ldsk + tr_lane;
+    sk.store(lds + buf);
+    sv.store(lds + buf + TILE);
     __syncthreads();
     if (j0 + BN < n_keys) {
       sk.load(kp + (int64_t)(j0 + BN) * a.k_tok, a.k_tok, t.len - j0 - BN, row_bytes);
       sv.load(vp + (int64_t)(j0 + BN) * a.v_tok, a.v_tok, t.len - j0 - BN, row_bytes);
     }
-    f32x16_t s[NT];
+    // what one wave does with the tile's first 32 * blocks keys
+    auto part = [&](auto blocks) {
+      constexpr int N = decltype(blocks)::value;
+      f32x16_t s[N];
 #pragma unroll
-    for (int n = 0; n < NT; n++) s[n] = mma_tile<DT, DP>(ldsk + n * 32 * L::bytes, q);
-    const float dist0 = (float)(i - j0 - 4 * h);
-    float top = -INFINITY;
+      for (int n = 0; n < N; n++) s[n] = mma_tile<DT, DP>(ldsk + n * 32 * L::bytes, q);
+      if constexpr (MODE != ATTN_PLAIN) {
+        const float dist0 = (float)(i - j0 - 4 * h);
 #pragma unroll
-    for (int n = 0; n < NT; n++)
+        for (int n = 0; n < N; n++)
 #pragma unroll
-      for (int r = 0; r < 16; r++)
-        s[n][r] = score<DT, MODE>(form, s[n][r], dist0 - (float)(n * 32 + acc_row(r)), nullptr);
-    if (j0 + BN > wave_least) {
-      const int left = vis - j0 - 4 * h;
-#pragma unroll
-      for (int n = 0; n < NT; n++)
-#pragma unroll
-        for (int r = 0; r < 16; r++)
-          s[n][r] = n * 32 + acc_row(r) < left ? s[n][r] : -INFINITY;
-    }
-#pragma unroll
-    for (int n = 0; n < NT; n++)
-#pragma unroll
-      for (int r = 0; r < 16; r++) top = __builtin_fmaxf(top, s[n][r]);
-    top = half_max(top);
-    const float mn = __builtin_fmaxf(m, top);
-    const float f = __builtin_amdgcn_exp2f(m - mn);
-    m = mn;
-    sum *= f;
-#pragma unroll
-    for (int c = 0; c < OT; c++)
-#pragma unroll
-      for (int r = 0; r < 16; r++) acc[c][r] *= f;
-#pragma unroll
-    for (int n = 0; n < NT; n++) {
-      Packed<DT> p;
-#pragma unroll
-      for (int r = 0; r < 16; r++) {
-        s[n][r] = __builtin_amdgcn_exp2f(s[n][r] - m);
-        sum += s[n][r];
+          for (int r = 0; r < 16; r++)
+            s[n][r] = score<DT, MODE>(form, s[n][r], dist0 - (float)(n * 32 + acc_row(r)), nullptr);
       }
-      p.set(s[n]);
+      if (j0 + BN > wave_least) {
+        const int left = vis - j0 - 4 * h;
 #pragma unroll
-      for (int c = 0; c < OT; c++)
-        acc[c] = mma_cols<DT, L::bytes>(vt, n * 32, c * 32, p, acc[c]);
-    }
+        for (int n = 0; n < N; n++)
+#pragma unroll
+          for (int r = 0; r < 16; r++)
+            s[n][r] = n * 32 + acc_row(r) < left ? s[n][r] : -INFINITY;
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < N; n++)
+#pragma unroll
+        for (int r = 0; r < 16; r++) top = __builtin_fmaxf(top, s[n][r]);
+      top = half_max(top) * post;
+      // The reference point of the exponentials follows the running maximum only once that is
+      // 2^8 away: sums and weights up to 256 lose nothing, and most tiles leave the accumulator
+      // as it is.
+      if (__any(top > m + 8.0f)) {
+        const float mn = __builtin_fmaxf(m, top);
+        const float f = __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        sum *= f;
+#pragma unroll
+        for (int c = 0; c < OT; c++)
+#pragma unroll
+          for (int r = 0; r < 16; r++) acc[c][r] *= f;
+      }
+#pragma unroll
+      for (int n = 0; n < N; n++) {
+        Packed<DT> p;
+#pragma unroll
+        for (int r = 0; r < 16; r++) {
+          s[n][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][r], post, -m));
+          sum += s[n][r];
+        }
+        p.set(s[n]);
+#pragma unroll
+        for (int c = 0; c < OT; c++)
+          acc[c] = mma_cols<DT, L::bytes>(vt, n * 32, c * 32, p, acc[c]);
+      }
+    };
+    // 32-key blocks that no row of this wave sees (past the document or above the diagonal, or
+    // all where the wave has no rows) are left out
+    if (wave0 >= t.len || j0 >= wave_most) continue;
+    if (NT == 1 || j0 + 32 < wave_most) part(Blocks<NT>{});
+    else part(Blocks<1>{});
   }
   sum = half_sum(sum);
   if (i < t.len) {

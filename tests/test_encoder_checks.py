@@ -92,15 +92,13 @@ def test_clip_binding_refuses():
 
 
 def desc(**k):
-    d = ms._AttentionDesc()
+    """maxsim_attention_desc as the header lays it out."""
     t = dict(data=P, token_stride=4 * 64, head_stride=64, doc_stride=5 * 4 * 64)
-    for n in "qkv":
-        setattr(d, n, ms._AttentionTensor(**{**t, **k.pop(n, {})}))
-    base = dict(doc_offsets=P, n_tokens=10, n_docs=2, n_heads=4, n_kv_heads=4, d=64, dtype=0,
-                scale=0.125)
-    for n, val in {**base, **k}.items():
-        setattr(d, n, val)
-    return d
+    f = [x for n in "qkv" for x in {**t, **k.pop(n, {})}.values()]
+    base = dict(doc_offsets=P, doc_lens=0, n_tokens=10, n_docs=2, prefix_lens=0, slopes=0, nd=0,
+                n_heads=4, n_kv_heads=4, d=64, dtype=0, causal=0, softcap=0.0, scale=0.125)
+    assert set(k) <= set(base)
+    return ms._ATTENTION_DESC.pack(*(x or 0 for x in f), *(x or 0 for x in {**base, **k}.values()))
 
 
 def test_attention_c_entry_refuses(L):
