@@ -45,11 +45,11 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
   f32x16_t acc[OT];
 #pragma unroll
   for (int c = 0; c < OT; c++) acc[c] = zero16();
-  const int tr_lane = tr_lane_offset<DT, L::bytes>();
+  const int tr_lane = tr_lane_offset<DT, DP>();
   const int wave_most = visible(a, t, wave0 + 31 < t.len ? wave0 + 31 : t.len - 1);
   int buf = 0;
   for (int j0 = 0; j0 < n_keys; j0 += BN, buf ^= 2 * TILE) {
-    const char *const ldsk = lds + buf, *const ldsv = ldsk + TILE, *const kt = ldsk + tr_lane;
+    const char *const ldsk = lds + buf, *const ldsv = ldsk + TILE;
     sk.store(lds + buf);
     sv.store(lds + buf + TILE);
     __syncthreads();
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
     Packed<DT> p;
     p.set(dp);
 #pragma unroll
-    for (int c = 0; c < OT; c++) acc[c] = mma_cols<DT, L::bytes>(kt, 0, c * 32, p, acc[c]);
+    for (int c = 0; c < OT; c++) acc[c] = mma_cols<DT, DP>(ldsk, tr_lane, 0, c * 32, p, acc[c]);
   }
   if (i < t.len) {
     const float f = a.scale / gs;
@@ -142,11 +142,10 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
     dk[c] = zero16();
     dv[c] = zero16();
   }
-  const int tr_lane = tr_lane_offset<DT, L::bytes>();
+  const int tr_lane = tr_lane_offset<DT, DP>();
   int buf = 0;
   for (int n = 0; n < total; n++, buf ^= 1) {
     char *const ldsq = lds + buf * 2 * TILE, *const ldsg = ldsq + TILE;
-    const char *const qt = ldsq + tr_lane, *const gt = ldsg + tr_lane;
     const float *const stats = stat[buf];
     sq.store(ldsq);
     sg.store(ldsg);
@@ -178,10 +177,10 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
     Packed<DT> p;
     p.set(s);
 #pragma unroll
-    for (int c = 0; c < OT; c++) dv[c] = mma_cols<DT, L::bytes>(gt, 0, c * 32, p, dv[c]);
+    for (int c = 0; c < OT; c++) dv[c] = mma_cols<DT, DP>(ldsg, tr_lane, 0, c * 32, p, dv[c]);
     p.set(dp);
 #pragma unroll
-    for (int c = 0; c < OT; c++) dk[c] = mma_cols<DT, L::bytes>(qt, 0, c * 32, p, dk[c]);
+    for (int c = 0; c < OT; c++) dk[c] = mma_cols<DT, DP>(ldsq, tr_lane, 0, c * 32, p, dk[c]);
   }
   if (j < t.len) {
     const float fk = a.scale / gs, fv = DT == DT_FP16 ? 1.0f / 256.0f : 1.0f;

@@ -106,51 +106,90 @@ template <> struct Packed<DT_FP32> {
   __device__ __forceinline__ void set(const f32x16_t &s) { f = s; }
 };
 
-// acc += X^T[columns c0 .. c0 + 31, rows r0 .. r0 + 31] * P, X row-major in LDS with rows of
-// ROWB bytes. `x` is the tile's first byte plus this lane's tr_lane_offset.
-template <int DT, int ROWB>
-__device__ __forceinline__ int tr_lane_offset() {
-  const int l = threadIdx.x & 63, h = l >> 5;
-  if constexpr (DT == DT_FP32) return 4 * h * ROWB + (l & 31) * 4;
-  else return (4 * h + ((l & 15) >> 2)) * ROWB + ((l >> 4) & 1) * 32 + (l & 3) * 8;
-}
-
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) char lds_char;
-
-template <int DT, int ROWB>
-__device__ __forceinline__ f32x16_t mma_cols(const char *x, int r0, int c0, const Packed<DT> &p,
-                                             f32x16_t acc) {
-  if constexpr (DT == DT_FP32) {
-#pragma unroll
-    for (int r = 0; r < 16; r++) {
-      const float a = *(const float *)(x + (r0 + (r & 3) + 8 * (r >> 2)) * ROWB + c0 * 4);
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p.f[r], acc, 0, 0, 0);
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < 2; t++) {
-      typedef __attribute__((address_space(3))) s16x4_t lds_v4;
-      const char *at = x + (r0 + 16 * t) * ROWB + c0 * 2;
-      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(lds_char *)at);
-      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(lds_char *)(at + 8 * ROWB));
-      typedef short s16x8_t __attribute__((ext_vector_type(8)));
-      const s16x8_t a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      acc = mma_rows<DT>(__builtin_bit_cast(u32x4_t, a), p.f[t], acc);
-    }
-  }
-  return acc;
-}
-
-// Rows of a head in LDS: DP columns (the head's size rounded up; the rest zeros) plus padding
-// that keeps 16-byte reads of 8 consecutive rows, and the transposing reads' 4 rows x 32 bytes,
-// on different banks.
+// Rows of a head in LDS: DP columns (the head's size rounded up; the rest zeros). LDS serves 16
+// lanes of a 16-byte read, or 32 lanes of an 8-byte one, a clock, if they fall on different 16
+// bytes of 256. 16-bit rows have no padding; their 16-byte chunks are stored at chunk ^ f(row):
+// 16 rows of one chunk (an operand in rows) then lie on 16 different places, and so do 4
+// consecutive rows x 4 chunks (the transposing reads). With fp32 the matrix core is the slower
+// by far; its rows are padded by a chunk instead.
 template <int DT, int DP> struct RowLayout {
   static constexpr int eb = Elem<DT>::bytes;
   static constexpr int chunks = DP * eb / 16;  // 16-byte chunks of a row
   static constexpr int steps = DP * eb / 32;   // mma_rows steps of a row
-  static constexpr int bytes = DP * eb + 16;
+  static constexpr int bytes = DP * eb + (DT == DT_FP32 ? 16 : 0);
+  // bits of a byte offset that f(row) reaches: as many as divide the row
+  static constexpr int mask = DT == DT_FP32     ? 0
+                              : chunks % 16 == 0 ? 255
+                              : chunks % 8 == 0  ? 127
+                                                 : 63;
+  // f(row) in bytes. Rows that differ by 16 share it, and row + 8 flips bit 5.
+  __device__ __forceinline__ static int f(int row) {
+    if (mask == 0) return 0;
+    const int high = (row >> 2) & 3;
+    return 16 * (mask == 255 ? (row & 3) << 2 | high : mask == 127 ? (row & 2) << 1 | high : high);
+  }
+  // A byte offset `at` plus `by` bytes along the row, where at contains f(row).
+  __device__ __forceinline__ static int along(int at, int by) {
+    return (at ^ (by & mask)) + (by & ~mask);
+  }
 };
+
+// acc += X^T[columns c0 .. c0 + 31, rows r0 .. r0 + 31] * P, X row-major in LDS; r0 a multiple of
+// 32. lane: this lane's tr_lane_offset in the tile.
+template <int DT, int DP> __device__ __forceinline__ int tr_lane_offset() {
+  using L = RowLayout<DT, DP>;
+  const int l = threadIdx.x & 63, h = l >> 5;
+  if constexpr (DT == DT_FP32) return 4 * h * L::bytes + (l & 31) * 4;
+  const int row = 4 * h + ((l & 15) >> 2);
+  return row * L::bytes + ((((l >> 4) & 1) * 32 + (l & 2) * 8) ^ L::f(row)) + (l & 1) * 8;
+}
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ s16x4_t read_tr(const char *p) {
+  typedef __attribute__((address_space(3))) char lds_char;
+  typedef __attribute__((address_space(3))) s16x4_t lds_v4;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(lds_char *)p);
+}
+
+// Operand `s` of 32 rows of an LDS tile (mma_rows' step s): lane is row_lane_offset.
+template <int DT, int DP> __device__ __forceinline__ int row_lane_offset() {
+  using L = RowLayout<DT, DP>;
+  const int l = threadIdx.x & 63;
+  return (l & 31) * L::bytes + ((l >> 5) * 16 ^ L::f(l));
+}
+template <int DT, int DP>
+__device__ __forceinline__ u32x4_t read_rows(const char *tile, int lane, int s) {
+  return load16(tile + RowLayout<DT, DP>::along(lane, 32 * s));
+}
+// Operand t of columns c0 .. c0 + 31, rows r0 + 16 t .., transposed (see mma_cols).
+template <int DT, int DP>
+__device__ __forceinline__ u32x4_t read_cols(const char *tile, int lane, int r0, int c0, int t) {
+  using L = RowLayout<DT, DP>;
+  const char *at = tile + (r0 + 16 * t) * L::bytes;
+  const s16x4_t lo = read_tr(at + L::along(lane, c0 * 2));
+  const s16x4_t hi = read_tr(at + 8 * L::bytes + L::along(lane ^ 32, c0 * 2));
+  return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <int DT, int DP>
+__device__ __forceinline__ f32x16_t mma_cols(const char *tile, int lane, int r0, int c0,
+                                             const Packed<DT> &p, f32x16_t acc) {
+  using L = RowLayout<DT, DP>;
+  if constexpr (DT == DT_FP32) {
+#pragma unroll
+    for (int r = 0; r < 16; r++) {
+      const float a = *(const float *)(tile + lane + (r0 + (r & 3) + 8 * (r >> 2)) * L::bytes + c0 * 4);
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p.f[r], acc, 0, 0, 0);
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < 2; t++)
+      acc = mma_rows<DT>(read_cols<DT, DP>(tile, lane, r0, c0, t), p.f[t], acc);
+  }
+  return acc;
+}
 
 // Copies ROWS rows of a head from global memory into LDS through registers: load() issues the
 // loads, store() writes them, so a tile travels while the one before is worked on.
@@ -180,7 +219,7 @@ template <int DT, int DP, int ROWS> struct Stage {
     for (int i = 0; i < n; i++) {
       const int at = threadIdx.x + i * ATTN_THREADS;
       if (total % ATTN_THREADS == 0 || at < total)
-        *(u32x4_t *)(lds + at / L::chunks * L::bytes + at % L::chunks * 16) = r[i];
+        *(u32x4_t *)(lds + at / L::chunks * L::bytes + (at % L::chunks * 16 ^ L::f(at / L::chunks))) = r[i];
     }
   }
 };
@@ -202,15 +241,38 @@ template <int DT, int DP> struct Held {
   }
 };
 
+// Nothing moves across: the compiler would put every LDS read right before its use, and a wave
+// would wait out the latency of each.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// N matrix instructions in order, their operands read from LDS AHEAD instructions before, with a
+// share of other work beside each: read(i) gives operand i, mma(i, operand) uses it, work(i) is
+// the i-th share.
+template <int N, int AHEAD, typename Read, typename Mma, typename Work>
+__device__ __forceinline__ void pipeline(Read read, Mma mma, Work work) {
+  constexpr int A = AHEAD < N ? AHEAD : N;
+  u32x4_t x[A];
+#pragma unroll
+  for (int i = 0; i < A; i++) x[i] = read(i);
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    keep_order();
+    mma(i, x[i % A]);
+    if (i + A < N) x[i % A] = read(i + A);
+    work(i);
+  }
+  keep_order();
+}
+
 // 32 rows of an LDS tile times held columns.
 template <int DT, int DP>
 __device__ __forceinline__ f32x16_t mma_tile(const char *tile, const Held<DT, DP> &b) {
   using L = RowLayout<DT, DP>;
-  const int l = threadIdx.x & 63;
-  const char *p = tile + (l & 31) * L::bytes + (l >> 5) * 16;
+  const int lane = row_lane_offset<DT, DP>();
   f32x16_t acc = zero16();
 #pragma unroll
-  for (int s = 0; s < L::steps; s++) acc = mma_rows<DT>(load16(p + 32 * s), b.f[s], acc);
+  for (int s = 0; s < L::steps; s++)
+    acc = mma_rows<DT>(read_rows<DT, DP>(tile, lane, s), b.f[s], acc);
   return acc;
 }
 
