@@ -69,8 +69,9 @@ int fill(const maxsim_attention_desc *s, AttnArgs &a) {
   a.softcap = s->softcap;
   a.scale = s->scale;
   a.slopes = s->slopes;
-  a.tiles_per_doc = (uint32_t)(((int64_t)a.nd + ATTN_ROWS - 1) / ATTN_ROWS);
-  const int64_t slots = packed ? a.n_tokens / ATTN_ROWS + a.n_docs + 2 : a.n_docs * a.tiles_per_doc;
+  const int64_t per_doc = ((int64_t)a.nd + ATTN_ROWS - 1) / ATTN_ROWS;
+  const int64_t slots = packed ? a.n_tokens / ATTN_ROWS + a.n_docs + 2 : a.n_docs * per_doc;
+  a.tiles_per_doc.set(per_doc ? (uint32_t)per_doc : 1);
   if (slots > 0x7fffffff || slots * a.heads > 0x7fffffff) return MAXSIM_ERR_SHAPE;
   a.slots = (uint32_t)slots;
   return MAXSIM_OK;
@@ -82,6 +83,8 @@ int mode_of(const AttnArgs &a) {
 
 // One workgroup for every tile of tokens and each of n_heads heads.
 int run(const void *fn, AttnArgs &a, int n_heads, hipStream_t st) {
+  a.per_group.set((uint32_t)(n_heads / a.kv_heads));
+  a.per_kv.set(a.slots * a.per_group.d);
   void *kargs[] = {&a};
   if (hipLaunchKernel(fn, dim3(a.slots * (unsigned)n_heads), dim3(ATTN_THREADS), kargs, 0, st) !=
       hipSuccess) {
@@ -176,9 +179,13 @@ int maxsim_attention_backward(const maxsim_attention_desc *desc, const void *o, 
     rc = run(pick(desc->dtype, dp, mode, attn_dq_bf16, attn_dq_fp16, attn_dq_fp32), a, a.heads, st);
     if (rc != MAXSIM_OK) return rc;
   }
-  if (dk)
-    return run(pick(desc->dtype, dp, mode, attn_dkv_bf16, attn_dkv_fp16, attn_dkv_fp32), a,
-               a.kv_heads, st);
+  for (int part = 0; dk && part < attn_dkv_launches(dp); part++) {
+    const void *kernel = desc->dtype == MAXSIM_BF16   ? attn_dkv_bf16(dp, mode, part)
+                         : desc->dtype == MAXSIM_FP16 ? attn_dkv_fp16(dp, mode, part)
+                                                      : attn_dkv_fp32(dp, mode, part);
+    rc = run(kernel, a, a.kv_heads, st);
+    if (rc != MAXSIM_OK) return rc;
+  }
   return MAXSIM_OK;
 }
 

@@ -12,11 +12,11 @@ template <int DT, int DP, int MODE>
 __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a) {
   using L = RowLayout<DT, DP>;
   constexpr int BN = 32, OT = DP / 32, TILE = BN * L::bytes;
-  __shared__ __align__(16) char lds[4 * TILE];  // two buffers: one barrier a tile
+  __shared__ __align__(256) char lds[4 * TILE];  // two buffers: one barrier a tile
   AttnTile t;
-  if (!locate(a, ATTN_ROWS, a.group, t)) return;
+  if (!locate(a, ATTN_ROWS, t)) return;
   const int lane = threadIdx.x & 63, h = lane >> 5;
-  const int wave0 = t.first + (threadIdx.x >> 6) * 32;
+  const int wave0 = t.first + (int)(threadIdx.x >> 6) * 32;
   const int i = wave0 + (lane & 31);
   const int row_bytes = a.d * L::eb;
   char *out = a.dq + ((t.row0 + i) * a.heads + t.head) * row_bytes;
@@ -40,8 +40,10 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
   const float delta = a.delta[at];
 
   Stage<DT, DP, BN> sk, sv;
-  sk.load(kp, a.k_tok, t.len, row_bytes);
-  sv.load(vp, a.v_tok, t.len, row_bytes);
+  sk.init(a.k_tok, row_bytes);
+  sv.init(a.v_tok, row_bytes);
+  sk.load(kp, a.k_tok, t.len);
+  sv.load(vp, a.v_tok, t.len);
   f32x16_t acc[OT];
 #pragma unroll
   for (int c = 0; c < OT; c++) acc[c] = zero16();
@@ -54,8 +56,8 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
     sv.store(lds + buf + TILE);
     __syncthreads();
     if (j0 + BN < n_keys) {
-      sk.load(kp + (int64_t)(j0 + BN) * a.k_tok, a.k_tok, t.len - j0 - BN, row_bytes);
-      sv.load(vp + (int64_t)(j0 + BN) * a.v_tok, a.v_tok, t.len - j0 - BN, row_bytes);
+      sk.load(kp + (int64_t)(j0 + BN) * a.k_tok, a.k_tok, t.len - j0 - BN);
+      sv.load(vp + (int64_t)(j0 + BN) * a.v_tok, a.v_tok, t.len - j0 - BN);
     }
     if (wave0 >= t.len || j0 >= wave_most) continue;  // nothing for this wave's rows
     f32x16_t s = mma_tile<DT, DP>(ldsk, q);
@@ -74,41 +76,41 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
 #pragma unroll
     for (int c = 0; c < OT; c++) acc[c] = mma_cols<DT, DP>(ldsk, tr_lane, 0, c * 32, p, acc[c]);
   }
-  if (i < t.len) {
-    const float f = a.scale / gs;
-#pragma unroll
-    for (int c = 0; c < OT; c++) store_cols<DT>(out, c * 32, a.d, acc[c], f);
-  } else if (i < t.rows) {
-    zero_row<DT>(out, a.d);
-  }
+  __syncthreads();  // the tiles' memory is free
+  store_rows<DT, DP>(lds + (threadIdx.x >> 6) * TILE, acc, i < t.len ? a.scale / gs : 0.0f,
+                     a.dq + ((t.row0 + wave0) * a.heads + t.head) * row_bytes,
+                     (int64_t)a.heads * row_bytes, t.rows - wave0, row_bytes);
 }
 
-template <int DT, int DP, int MODE>
+// WHAT: 1 for dK, 2 for dV, 3 for both. Heads wider than 128 take a launch for each: a wave has no
+// registers for both sums, and computing the scores again costs less than spilling.
+template <int DT, int DP, int MODE, int WHAT>
 __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a) {
   using L = RowLayout<DT, DP>;
   constexpr int BM = 32, OT = DP / 32, TILE = BM * L::bytes;
+  constexpr bool DK = WHAT & 1, DV = WHAT & 2;
   // fp16 P is rounded 2^8 times too large: rows over thousands of keys stay out of the subnormals
   constexpr float SHIFT = DT == DT_FP16 ? 8.0f : 0.0f;
-  __shared__ __align__(16) char lds[4 * TILE];  // two buffers: one barrier a tile
+  __shared__ __align__(256) char lds[4 * TILE];  // two buffers: one barrier a tile
   __shared__ __align__(16) float stat[2][2 * BM];
   AttnTile t;
-  if (!locate(a, ATTN_ROWS, 1, t)) return;
+  if (!locate(a, ATTN_ROWS, t)) return;
   const int lane = threadIdx.x & 63, h = lane >> 5;
-  const int wave0 = t.first + (threadIdx.x >> 6) * 32;
+  const int wave0 = t.first + (int)(threadIdx.x >> 6) * 32;
   const int j = wave0 + (lane & 31);
   const int row_bytes = a.d * L::eb;
   const int64_t out = ((t.row0 + j) * a.kv_heads + t.head) * row_bytes;
   if (t.first >= t.len) {
     if (j < t.rows) {
-      zero_row<DT>(a.dk + out, a.d);
-      zero_row<DT>(a.dv + out, a.d);
+      if (DK) zero_row<DT>(a.dk + out, a.d);
+      if (DV) zero_row<DT>(a.dv + out, a.d);
     }
     return;
   }
   const int jk = j < t.len ? j : t.len - 1;
   Held<DT, DP> k, v;
   k.load(a.k + t.k + t.head * a.k_head, a.k_tok, jk, row_bytes);
-  v.load(a.v + t.v + t.head * a.v_head, a.v_tok, jk, row_bytes);
+  if (DK) v.load(a.v + t.v + t.head * a.v_head, a.v_tok, jk, row_bytes);
   const int group = a.group;
   // with a causal mask only rows from the key on see it, unless it lies in the prefix
   const int from = t.first >= t.prefix ? t.first : 0;
@@ -120,10 +122,12 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
   Stage<DT, DP, BM> sq, sg;
   float st = 0.0f;
   const int tok = a.heads * row_bytes;
+  sq.init(a.q_tok, row_bytes);
+  sg.init(tok, row_bytes);
   auto load = [&](int n) {
     const int head = t.head * group + n / n_tiles, i0 = from + n % n_tiles * BM;
-    sq.load(a.q + t.q + head * a.q_head + (int64_t)i0 * a.q_tok, a.q_tok, t.len - i0, row_bytes);
-    sg.load(a.dO + ((t.row0 + i0) * a.heads + head) * row_bytes, tok, t.len - i0, row_bytes);
+    sq.load(a.q + t.q + head * a.q_head + (int64_t)i0 * a.q_tok, a.q_tok, t.len - i0);
+    sg.load(a.dO + ((t.row0 + i0) * a.heads + head) * row_bytes, tok, t.len - i0);
     if (threadIdx.x < 2 * BM) {
       const int r = threadIdx.x & (BM - 1);
       const bool is_lse = threadIdx.x < BM;
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
     if (wave0 >= t.len || (a.causal && wave0 >= t.prefix && wave0 > i0 + BM - 1)) continue;
     const ScoreForm form = score_form<DT, MODE>(a, t.head * group + n / n_tiles);
     f32x16_t s = mma_tile<DT, DP>(ldsq, k);
-    f32x16_t dp = mma_tile<DT, DP>(ldsg, v);
+    f32x16_t dp = DK ? mma_tile<DT, DP>(ldsg, v) : zero16();
     const float dist0 = (float)(i0 + 4 * h - j);
     const int hide = wave0 + 31 > i0 ? jmask - i0 - 4 * h : -1;  // rows below it do not see key j
 #pragma unroll
@@ -175,24 +179,27 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
       }
     }
     Packed<DT> p;
-    p.set(s);
+    if constexpr (DV) {
+      p.set(s);
 #pragma unroll
-    for (int c = 0; c < OT; c++) dv[c] = mma_cols<DT, DP>(ldsg, tr_lane, 0, c * 32, p, dv[c]);
-    p.set(dp);
-#pragma unroll
-    for (int c = 0; c < OT; c++) dk[c] = mma_cols<DT, DP>(ldsq, tr_lane, 0, c * 32, p, dk[c]);
-  }
-  if (j < t.len) {
-    const float fk = a.scale / gs, fv = DT == DT_FP16 ? 1.0f / 256.0f : 1.0f;
-#pragma unroll
-    for (int c = 0; c < OT; c++) {
-      store_cols<DT>(a.dk + out, c * 32, a.d, dk[c], fk);
-      store_cols<DT>(a.dv + out, c * 32, a.d, dv[c], fv);
+      for (int c = 0; c < OT; c++) dv[c] = mma_cols<DT, DP>(ldsg, tr_lane, 0, c * 32, p, dv[c]);
     }
-  } else if (j < t.rows) {
-    zero_row<DT>(a.dk + out, a.d);
-    zero_row<DT>(a.dv + out, a.d);
+    if constexpr (DK) {
+      p.set(dp);
+#pragma unroll
+      for (int c = 0; c < OT; c++) dk[c] = mma_cols<DT, DP>(ldsq, tr_lane, 0, c * 32, p, dk[c]);
+    }
   }
+  __syncthreads();  // the tiles' memory is free
+  const int64_t first = ((t.row0 + wave0) * a.kv_heads + t.head) * row_bytes;
+  const int64_t stride = (int64_t)a.kv_heads * row_bytes;
+  char *const mine = lds + (threadIdx.x >> 6) * TILE;
+  const bool real = j < t.len;
+  if constexpr (DK)
+    store_rows<DT, DP>(mine, dk, real ? a.scale / gs : 0.0f, a.dk + first, stride, t.rows - wave0, row_bytes);
+  if constexpr (DV)
+    store_rows<DT, DP>(mine, dv, real ? (DT == DT_FP16 ? 1.0f / 256.0f : 1.0f) : 0.0f, a.dv + first,
+                     stride, t.rows - wave0, row_bytes);
 }
 
 }  // namespace maxsim

@@ -41,7 +41,8 @@ struct AttnArgs {
   float *lse;              // [heads][rows]
   int64_t rows;            // rows of o: all tokens
   uint32_t slots;          // tiles along the tokens
-  uint32_t tiles_per_doc;  // fixed layout
+  FastDiv tiles_per_doc;   // fixed layout
+  FastDiv per_kv, per_group;  // workgroups of a key/value head, heads of the grid that share one
   // backward
   const char *dO;          // [rows][heads][d]
   const float *delta;      // [heads][rows]: <dO, o>
@@ -192,34 +193,41 @@ __device__ __forceinline__ f32x16_t mma_cols(const char *tile, int lane, int r0,
 }
 
 // Copies ROWS rows of a head from global memory into LDS through registers: load() issues the
-// loads, store() writes them, so a tile travels while the one before is worked on.
+// loads, store() writes them, so a tile travels while the one before is worked on. Rows past the
+// last valid one repeat it, and columns past the head's size its last 16 bytes: nothing outside
+// is read, what follows stays finite, and those columns meet zeros (Held) or are not stored.
 template <int DT, int DP, int ROWS> struct Stage {
   using L = RowLayout<DT, DP>;
   static constexpr int total = ROWS * L::chunks;
   static constexpr int n = (total + ATTN_THREADS - 1) / ATTN_THREADS;
   u32x4_t r[n];
+  uint32_t at[n];  // byte offset of this thread's pieces in a whole tile
+  uint32_t col[n];
 
-  // base: first row of the tile (uniform); rows past the last valid one repeat it, so that
-  // nothing outside the document is read and what follows stays finite.
-  __device__ __forceinline__ void load(const char *base, int stride, int valid, int row_bytes) {
+  __device__ __forceinline__ void init(int stride, int row_bytes) {
 #pragma unroll
     for (int i = 0; i < n; i++) {
-      const int at = threadIdx.x + i * ATTN_THREADS;
-      const int c = at % L::chunks;
-      int row = at / L::chunks;
-      row = row < valid ? row : valid - 1;
-      u32x4_t z = {0, 0, 0, 0};
-      if ((total % ATTN_THREADS == 0 || at < total) && c * 16 < row_bytes)
-        z = *(const u32x4_t *)(base + (uint32_t)(row * stride + c * 16));
-      r[i] = z;
+      const int p = threadIdx.x + i * ATTN_THREADS;
+      const int c = p % L::chunks * 16;
+      col[i] = c < row_bytes ? c : row_bytes - 16;
+      at[i] = (uint32_t)(p / L::chunks * stride) + col[i];
+    }
+  }
+  // base: first row of the tile (uniform); valid: rows that exist from it on, at least one.
+  __device__ __forceinline__ void load(const char *base, int stride, int valid) {
+    const uint32_t last = (uint32_t)((valid < ROWS ? valid : ROWS) - 1) * (uint32_t)stride;
+#pragma unroll
+    for (int i = 0; i < n; i++) {
+      const uint32_t limit = last + col[i];
+      r[i] = *(const u32x4_t *)(base + (at[i] < limit ? at[i] : limit));
     }
   }
   __device__ __forceinline__ void store(char *lds) const {
 #pragma unroll
     for (int i = 0; i < n; i++) {
-      const int at = threadIdx.x + i * ATTN_THREADS;
-      if (total % ATTN_THREADS == 0 || at < total)
-        *(u32x4_t *)(lds + at / L::chunks * L::bytes + (at % L::chunks * 16 ^ L::f(at / L::chunks))) = r[i];
+      const int p = threadIdx.x + i * ATTN_THREADS;
+      if (total % ATTN_THREADS == 0 || p < total)
+        *(u32x4_t *)(lds + p / L::chunks * L::bytes + (p % L::chunks * 16 ^ L::f(p / L::chunks))) = r[i];
     }
   }
 };
@@ -337,14 +345,12 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t n) {
   return x * per + (x < more ? x : more) + (id >> 3);
 }
 
-// False where the tile does not exist. group: heads of the grid that share a key/value head
-// (1 where the grid runs over the key/value heads).
-__device__ __forceinline__ bool locate(const AttnArgs &a, int rows, uint32_t group, AttnTile &t) {
+// False where the tile does not exist.
+__device__ __forceinline__ bool locate(const AttnArgs &a, int rows, AttnTile &t) {
   const uint32_t id = xcd_order(blockIdx.x, gridDim.x);
-  const uint32_t per_kv = a.slots * group;
-  const uint32_t kv = id / per_kv, in = id - kv * per_kv;
-  uint32_t slot = in / group;
-  t.head = kv * group + (in - slot * group);
+  const uint32_t kv = a.per_kv(id), in = id - kv * a.per_kv.d;
+  uint32_t slot = a.per_group(in);
+  t.head = kv * a.per_group.d + (in - slot * a.per_group.d);
   // with a causal mask the last tiles have the most keys: they start first
   if (a.causal) slot = a.slots - 1 - slot;
   int64_t doc;
@@ -360,8 +366,9 @@ __device__ __forceinline__ bool locate(const AttnArgs &a, int rows, uint32_t gro
     t.k = t.row0 * a.k_tok;
     t.v = t.row0 * a.v_tok;
   } else {
-    doc = slot / a.tiles_per_doc;
-    t.first = (int)(slot - (uint32_t)doc * a.tiles_per_doc) * rows;
+    const uint32_t b = a.tiles_per_doc(slot);
+    doc = b;
+    t.first = (int)(slot - b * a.tiles_per_doc.d) * rows;
     t.row0 = doc * a.nd;
     t.rows = a.nd;
     const int n = a.lens ? uniform(a.lens[doc]) : a.nd;
@@ -394,20 +401,37 @@ __device__ __forceinline__ int visible(const AttnArgs &a, const AttnTile &t, int
   return n < t.len ? n : t.len;
 }
 
-// Stores a transposed accumulator (this lane: row `row` of the output, columns c0 + ...) times f.
-template <int DT>
-__device__ __forceinline__ void store_cols(char *row, int c0, int d, const f32x16_t &acc, float f) {
+// Stores 32 rows of a wave's transposed accumulators, each lane's row times f (0 for rows that do
+// not exist), through the wave's own 32 rows of LDS: a lane holds 4 columns of a row here and
+// there, memory wants whole rows. out: the wave's first row, rows `stride` bytes apart, the first
+// `rows` of them written.
+template <int DT, int DP, int OT>
+__device__ __forceinline__ void store_rows(char *lds, const f32x16_t (&acc)[OT], float f, char *out,
+                                           int64_t stride, int rows, int row_bytes) {
+  using L = RowLayout<DT, DP>;
   using T = typename AttnElem<DT>::type;
-  const int h = (threadIdx.x & 63) >> 5;
   typedef T v4 __attribute__((ext_vector_type(4)));
+  int l = threadIdx.x & 63;
+  asm volatile("" : "+v"(l));  // nothing of this is kept in registers from before the main loop
+  const int row = l & 31, h = l >> 5;
 #pragma unroll
-  for (int g = 0; g < 4; g++) {
-    const int c = c0 + 8 * g + 4 * h;
-    v4 x;
+  for (int c = 0; c < OT; c++)
 #pragma unroll
-    for (int e = 0; e < 4; e++) x[e] = (T)(acc[4 * g + e] * f);
-    if (c < d) *(v4 *)(row + c * sizeof(T)) = x;
+    for (int g = 0; g < 4; g++) {
+      v4 x;
+#pragma unroll
+      for (int e = 0; e < 4; e++) x[e] = (T)(acc[c][4 * g + e] * f);
+      const int at = (c * 32 + 8 * g + 4 * h) * L::eb;
+      *(v4 *)(lds + row * L::bytes + ((at & ~15) ^ L::f(row)) + (at & 15)) = x;
+    }
+  wave_lds_sync();
+#pragma unroll
+  for (int i = 0; i < (32 * L::chunks) / 64; i++) {
+    const int p = i * 64 + l, r = p / L::chunks, c = p % L::chunks * 16;
+    const u32x4_t x = *(const u32x4_t *)(lds + r * L::bytes + (c ^ L::f(r)));
+    if (r < rows && c < row_bytes) *(u32x4_t *)(out + r * stride + c) = x;
   }
+  wave_lds_sync();
 }
 
 template <int DT>

@@ -12,33 +12,15 @@ const void *attn_fwd_fp32(int dp, int mode);
 const void *attn_dq_bf16(int dp, int mode);
 const void *attn_dq_fp16(int dp, int mode);
 const void *attn_dq_fp32(int dp, int mode);
-const void *attn_dkv_bf16(int dp, int mode);
-const void *attn_dkv_fp16(int dp, int mode);
-const void *attn_dkv_fp32(int dp, int mode);
+// part: 0, or 1 where there are two launches (attn_dkv_launches).
+const void *attn_dkv_bf16(int dp, int mode, int part);
+const void *attn_dkv_fp16(int dp, int mode, int part);
+const void *attn_dkv_fp32(int dp, int mode, int part);
 
-// Head sizes are rounded up to one of these widths; the columns past the size are zeros.
+// Head sizes are rounded up to one of these widths; the columns past the size are zeros. fp32
+// heads wider than 128 have no kernel (nullptr): they would need more registers than a wave has.
 inline int attn_width(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 96 ? 96 : d <= 128 ? 128 : 256; }
 
-#define MAXSIM_ATTN_MODES(KERNEL, DT, DP)                       \
-  case DP:                                                      \
-    return mode == ATTN_PLAIN  ? (const void *)KERNEL<DT, DP, ATTN_PLAIN> \
-           : mode == ATTN_BIAS ? (const void *)KERNEL<DT, DP, ATTN_BIAS>  \
-                               : (const void *)KERNEL<DT, DP, ATTN_CAP>;
-
-// fp32 heads wider than 128 would need more registers than a wave has.
-#define MAXSIM_ATTN_PICK(NAME, KERNEL, DT)          \
-  namespace maxsim {                                \
-  const void *NAME(int dp, int mode) {              \
-    switch (dp) {                                   \
-      MAXSIM_ATTN_MODES(KERNEL, DT, 32)             \
-      MAXSIM_ATTN_MODES(KERNEL, DT, 64)             \
-      MAXSIM_ATTN_MODES(KERNEL, DT, 96)             \
-      MAXSIM_ATTN_MODES(KERNEL, DT, 128)            \
-    }                                               \
-    if constexpr (DT != DT_FP32)                    \
-      switch (dp) { MAXSIM_ATTN_MODES(KERNEL, DT, 256) } \
-    return nullptr;                                 \
-  }                                                 \
-  }
+inline int attn_dkv_launches(int dp) { return dp > 128 ? 2 : 1; }
 
 }  // namespace maxsim

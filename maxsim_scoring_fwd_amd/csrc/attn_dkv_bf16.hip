@@ -2,4 +2,24 @@
 #include "attn_dispatch.hpp"
 #include "attn_bwd_kernel.hpp"
 
-MAXSIM_ATTN_PICK(attn_dkv_bf16, attn_dkv_kernel, DT_BF16)
+namespace maxsim {
+namespace {
+template <int DP, int WHAT> const void *pick(int mode) {
+  return mode == ATTN_PLAIN  ? (const void *)attn_dkv_kernel<DT_BF16, DP, ATTN_PLAIN, WHAT>
+         : mode == ATTN_BIAS ? (const void *)attn_dkv_kernel<DT_BF16, DP, ATTN_BIAS, WHAT>
+                             : (const void *)attn_dkv_kernel<DT_BF16, DP, ATTN_CAP, WHAT>;
+}
+}  // namespace
+
+const void *attn_dkv_bf16(int dp, int mode, int part) {
+  switch (dp) {
+  case 32: return pick<32, 3>(mode);
+  case 64: return pick<64, 3>(mode);
+  case 96: return pick<96, 3>(mode);
+  case 128: return pick<128, 3>(mode);
+  case 256: return part ? pick<256, 2>(mode) : pick<256, 1>(mode);
+  }
+  return nullptr;
+}
+
+}  // namespace maxsim

@@ -7,6 +7,9 @@
 
 #include "attn_common.hpp"
 
+#ifndef ATTN_FWD_KEYS256
+#define ATTN_FWD_KEYS256 32
+#endif
 #ifndef ATTN_FWD_KEYS
 #define ATTN_FWD_KEYS 32
 #endif
@@ -14,7 +17,7 @@
 namespace maxsim {
 
 template <int DT, int DP> struct FwdShape {
-  static constexpr int keys = DT == DT_FP32 || DP >= 128 ? 32 : ATTN_FWD_KEYS;  // keys of a tile
+  static constexpr int keys = DT == DT_FP32 || DP == 128 ? 32 : DP == 256 ? ATTN_FWD_KEYS256 : ATTN_FWD_KEYS;  // keys of a tile
   static constexpr int waves = DP >= 256 ? 1 : DP >= 96 ? 2 : 3;
 };
 
@@ -24,11 +27,12 @@ __attribute__((amdgpu_waves_per_eu(FwdShape<DT, DP>::waves, FwdShape<DT, DP>::wa
 attn_fwd_kernel(const AttnArgs a) {
   using L = RowLayout<DT, DP>;
   constexpr int BN = FwdShape<DT, DP>::keys, NT = BN / 32, OT = DP / 32, TILE = BN * L::bytes;
-  __shared__ __align__(256) char ldsk[2][TILE], ldsv[2][TILE];
+  __shared__ __align__(256) char lds[4][TILE];  // two buffers of K, two of V
+  static_assert(TILE >= 32 * L::bytes, "the result leaves through it, 32 rows a wave");
   AttnTile t;
-  if (!locate(a, ATTN_ROWS, a.group, t)) return;
+  if (!locate(a, ATTN_ROWS, t)) return;
   const int lane = threadIdx.x & 63, h = lane >> 5;
-  const int wave0 = t.first + (threadIdx.x >> 6) * 32;
+  const int wave0 = t.first + (int)(threadIdx.x >> 6) * 32;
   const int i = wave0 + (lane & 31);
   const int row_bytes = a.d * L::eb;
   char *out = a.o + ((t.row0 + i) * a.heads + t.head) * row_bytes;
@@ -59,12 +63,14 @@ attn_fwd_kernel(const AttnArgs a) {
   const int wave_tiles = wave0 < t.len ? (wave_most + BN - 1) / BN : 0;
 
   Stage<DT, DP, BN> sk, sv;
+  sk.init(a.k_tok, row_bytes);
+  sv.init(a.v_tok, row_bytes);
   auto load = [&](auto &stage, const char *p, int tok, int n) {
-    stage.load(p + (int64_t)n * BN * tok, tok, t.len - n * BN, row_bytes);
+    stage.load(p + (int64_t)n * BN * tok, tok, t.len - n * BN);
   };
   load(sk, kp, a.k_tok, 0);
   load(sv, vp, a.v_tok, 0);
-  sk.store(ldsk[0]);
+  sk.store(lds[0]);
   __syncthreads();
   if (tiles > 1) load(sk, kp, a.k_tok, 1);
 
@@ -72,14 +78,14 @@ attn_fwd_kernel(const AttnArgs a) {
 #pragma unroll
   for (int c = 0; c < OT; c++) acc[c] = zero16();
   float m = -1e30f, sum = 0.0f;  // a finite start: exp2(-inf - m) is 0 for rows that see nothing yet
-  float top = -INFINITY;
+  float top = -INFINITY, base = 0.0f;  // of the tile at hand
 
   const int row_lane = row_lane_offset<DT, DP>();
   constexpr int N1 = NT * L::steps, N2 = NT * OT * 2, E = NT * 16;  // products; elements of a lane
   // Matrix work of a step, with share i of other vector work beside instruction i. 16-bit types
   // run it as a pipeline; fp32 is bound by its matrix instructions alone.
   auto products = [&](f32x16_t (&x)[NT], int n, auto work) {
-    const char *tile = ldsk[n & 1];
+    const char *tile = lds[n & 1];
     if constexpr (DT == DT_FP32) {
 #pragma unroll
       for (int b = 0; b < NT; b++) x[b] = mma_tile<DT, DP>(tile + b * 32 * L::bytes, q);
@@ -96,7 +102,7 @@ attn_fwd_kernel(const AttnArgs a) {
     }
   };
   auto values = [&](const Packed<DT> (&p)[NT], int n, auto work) {
-    const char *tile = ldsv[n & 1];
+    const char *tile = lds[2 + (n & 1)];
     if constexpr (DT == DT_FP32) {
 #pragma unroll
       for (int b = 0; b < NT; b++)
@@ -113,25 +119,47 @@ attn_fwd_kernel(const AttnArgs a) {
           work);
     }
   };
-  // products of tile n to scores, and their maximum: elements from .. to - 1
-  auto scores = [&](f32x16_t (&x)[NT], int n, bool masked, int from, int to) {
+  // Products of tile n to scores, and their maximum, elements from .. to - 1. Where no key of the
+  // tile is hidden and all lie on one side of the wave's rows, the distance bias is linear in the
+  // key: a constant of the lane (`base`, left to the exponential) and one of the element, which
+  // joins an FMA that is there anyway.
+  f32x16_t slope_row;  // slope * key, and the cap's constant term
+#pragma unroll
+  for (int r = 0; r < 16; r++) slope_row[r] = __builtin_fmaf(form.slope, (float)acc_row(r), form.b);
+  constexpr bool LINEAR = MODE == ATTN_BIAS || (MODE == ATTN_CAP && DT != DT_FP32);
+  auto scores = [&](f32x16_t (&x)[NT], int n, bool linear, int from, int to) {
     const float dist0 = (float)(i - n * BN - 4 * h);
     const int left = vis - n * BN - 4 * h;
 #pragma unroll
     for (int e = from; e < to; e++) {
       float y = x[e / 16][e % 16];
-      const int key = e / 16 * 32 + acc_row(e % 16);
-      if constexpr (MODE != ATTN_PLAIN) y = score<DT, MODE>(form, y, dist0 - (float)key, nullptr);
-      if (masked) y = key < left ? y : -INFINITY;
+      const int b = e / 16 * 32, key = b + acc_row(e % 16);
+      const float far = b ? slope_row[e % 16] + form.slope * (float)b : slope_row[e % 16];
+      if (LINEAR && linear) {
+        if (MODE == ATTN_CAP)
+          y = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y * form.a)) * (-2.0f * form.b) + far;
+        else
+          y = __builtin_fmaf(y, form.a, far);
+      } else if (MODE != ATTN_PLAIN) {
+        y = score<DT, MODE>(form, y, dist0 - (float)key, nullptr);
+      }
+      if (!linear) y = key < left ? y : -INFINITY;
       top = __builtin_fmaxf(top, y);
       x[e / 16][e % 16] = y;
     }
   };
+  // Tile n is linear: nothing hidden, and all keys at or before the wave's rows (the far side,
+  // keys after the rows, would want the other sign: it takes the full form).
+  auto linear_at = [&](int n) {
+    const int end = (n + 1) * BN;
+    return end <= wave_least && (!LINEAR || end <= wave0 + 1 || form.slope == 0.0f);
+  };
   // scores to weights, not yet rounded
-  auto weights = [&](f32x16_t (&x)[NT], int from, int to) {
+  auto weights = [&](f32x16_t (&x)[NT], float off, int from, int to) {
 #pragma unroll
     for (int e = from; e < to; e++) {
-      const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e / 16][e % 16], post, -m));
+      const float w = __builtin_amdgcn_exp2f(MODE == ATTN_PLAIN ? __builtin_fmaf(x[e / 16][e % 16], post, off)
+                                                                : x[e / 16][e % 16] + off);
       sum += w;
       x[e / 16][e % 16] = w;
     }
@@ -140,12 +168,12 @@ attn_fwd_kernel(const AttnArgs a) {
 
   if (wave_tiles > 0) {
     products(s, 0, nothing);
-    scores(s, 0, true, 0, E);
+    scores(s, 0, false, 0, E);
     top = half_max(top) * post;
   }
   for (int n = 0; n < tiles; n++) {
-    if (n + 1 < tiles) sk.store(ldsk[(n + 1) & 1]);
-    sv.store(ldsv[n & 1]);
+    if (n + 1 < tiles) sk.store(lds[(n + 1) & 1]);
+    sv.store(lds[2 + (n & 1)]);
     __syncthreads();
     if (n + 2 < tiles) load(sk, kp, a.k_tok, n + 2);
     if (n + 1 < tiles) load(sv, vp, a.v_tok, n + 1);
@@ -153,7 +181,7 @@ attn_fwd_kernel(const AttnArgs a) {
     // The reference point of the exponentials follows the running maximum only once that is
     // 2^8 away: sums and weights up to 256 lose nothing, and most tiles leave the accumulator
     // as it is.
-    if (__any(top > m + 8.0f)) {
+    if (__builtin_amdgcn_ballot_w64(top > m + 8.0f)) {
       const float mn = __builtin_fmaxf(m, top);
       const float f = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
@@ -165,35 +193,36 @@ attn_fwd_kernel(const AttnArgs a) {
     }
     Packed<DT> p[NT];
     if (n + 1 == wave_tiles) {
-      weights(s, 0, E);
+      weights(s, base - m, 0, E);
 #pragma unroll
       for (int b = 0; b < NT; b++) p[b].set(s[b]);
       values(p, n, nothing);
       continue;
     }
     f32x16_t next[NT];
-    products(next, n + 1, [&](int i) { weights(s, i * E / N1, (i + 1) * E / N1); });
+    const float off = base - m;
+    products(next, n + 1, [&](int i) { weights(s, off, i * E / N1, (i + 1) * E / N1); });
 #pragma unroll
     for (int b = 0; b < NT; b++) p[b].set(s[b]);
     top = -INFINITY;
-    if ((n + 2) * BN > wave_least)
+    if (linear_at(n + 1)) {
       values(p, n, [&](int i) { scores(next, n + 1, true, i * E / N2, (i + 1) * E / N2); });
-    else
+      base = LINEAR ? -form.slope * (float)(i - (n + 1) * BN - 4 * h) : 0.0f;
+    } else {
       values(p, n, [&](int i) { scores(next, n + 1, false, i * E / N2, (i + 1) * E / N2); });
-    top = half_max(top) * post;
+      base = 0.0f;
+    }
+    top = half_max(__builtin_fmaf(top, post, base));  // the halves differ in base
 #pragma unroll
     for (int b = 0; b < NT; b++) s[b] = next[b];
   }
   sum = half_sum(sum);
-  if (i < t.len) {
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-    for (int c = 0; c < OT; c++) store_cols<DT>(out, c * 32, a.d, acc[c], inv);
-    if (h == 0) *lse = sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * LN2 : -INFINITY;
-  } else if (i < t.rows) {
-    zero_row<DT>(out, a.d);
-    if (h == 0) *lse = -INFINITY;
-  }
+  const bool real = i < t.len && sum > 0.0f;
+  __syncthreads();  // the tiles' memory is free
+  if (h == 0 && i < t.rows) *lse = real ? (m + __builtin_amdgcn_logf(sum)) * LN2 : -INFINITY;
+  store_rows<DT, DP>(lds[threadIdx.x >> 6], acc, real ? 1.0f / sum : 0.0f,
+                     a.o + ((t.row0 + wave0) * a.heads + t.head) * row_bytes,
+                     (int64_t)a.heads * row_bytes, t.rows - wave0, row_bytes);
 }
 
 }  // namespace maxsim

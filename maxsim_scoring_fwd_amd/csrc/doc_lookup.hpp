@@ -20,6 +20,30 @@ __device__ __forceinline__ int64_t place_in_document(const int64_t *offsets, int
   return lo == 0 ? t : t - offsets[lo - 1];
 }
 
+// v of one lane, in all.
+__device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)((uint64_t)v >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// n / d for n < 2^31 by a multiplication: with 2^s the first power of two that is at least d and
+// m = ceil(2^(31 + s) / d), m * d exceeds 2^(31 + s) by less than 2^s, which n < 2^31 does not
+// carry into the quotient.
+struct FastDiv {
+  uint32_t d, m, shift;
+  void set(uint32_t by) {
+    d = by;
+    uint32_t s = 0;
+    while (((uint64_t)1 << s) < by) s++;
+    m = by > 1 ? (uint32_t)((((uint64_t)1 << (31 + s)) + by - 1) / by) : 0;
+    shift = s ? s - 1 : 0;
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return d == 1 ? n : __umulhi(n, m) >> shift;
+  }
+};
+
 // Tiles over packed documents without a plan made beforehand and without reading the offsets
 // on the host. The token range is cut at every offset, which gives n_docs + 2 spans: the tokens
 // before the first offset (no document), the documents, and the tokens after the last offset
@@ -34,30 +58,29 @@ struct TileSpan {
   int64_t doc;    // document, or -1
 };
 
-// One wave's search, 64 probes a step: two steps for up to 4096 documents. Offsets are clamped
-// to the token range, so that no tile reaches past it whatever they hold.
+// One wave's search, 63 probes a step: one step for up to 61 documents, two for up to 3967. Lane
+// 63 looks one probe further, so that the last step also knows where the span ends. Offsets are
+// clamped to the token range, so that no tile reaches past it whatever they hold.
 __device__ __forceinline__ TileSpan find_tile(const int64_t *offsets, int64_t n_docs,
                                               int64_t n_tokens, int64_t slot, int rows) {
   const int lane = threadIdx.x & 63;
-  auto begin_of = [&](int64_t s) -> int64_t {
-    if (s == 0) return 0;
-    if (s > n_docs + 1) return n_tokens;
-    const int64_t o = offsets[s - 1];
-    return o < 0 ? 0 : (o > n_tokens ? n_tokens : o);
-  };
-  int64_t lo = 0, hi = n_docs + 2;
-  while (hi - lo > 1) {
-    const int64_t step = (hi - lo + 63) / 64;
-    const int64_t p = lo + lane * step;
-    const bool in = p < hi && (p == lo || begin_of(p) / rows + p <= slot);
-    const uint64_t mask = __ballot(in);
-    const int last = 63 - __builtin_clzll(mask | 1);
+  int64_t lo = 0, hi = n_docs + 2, begin = 0;
+  int last = 0;
+  do {
+    const int64_t step = (uint64_t)(hi - lo + 62) / 63;
+    int64_t p = lo + lane * step;
+    p = p < hi ? p : hi;
+    int64_t o = 0;
+    if (p > 0) o = p > n_docs + 1 ? n_tokens : offsets[p - 1];
+    begin = o < 0 ? 0 : (o > n_tokens ? n_tokens : o);
+    const bool in = lane < 63 && p < hi && (lane == 0 || begin / rows + p <= slot);
+    last = 63 - __builtin_clzll(__ballot(in) | 1);
     lo += last * step;
     hi = lo + step < hi ? lo + step : hi;
-  }
+  } while (hi - lo > 1);
   TileSpan t;
-  t.begin = begin_of(lo);
-  const int64_t end = begin_of(lo + 1);
+  t.begin = lane_value(begin, last);
+  const int64_t end = lane_value(begin, last + 1);
   t.len = end > t.begin ? end - t.begin : 0;
   t.first = (slot - (t.begin / rows + lo)) * rows;
   t.doc = lo == 0 || lo == n_docs + 1 ? -1 : lo - 1;
