@@ -39,42 +39,117 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
   const float gs = DT == DT_FP16 ? *a.grad_scale : 1.0f;
   const float delta = a.delta[at];
 
+  const int tiles = (n_keys + BN - 1) / BN;
+  const int wave_most = visible(a, t, wave0 + 31 < t.len ? wave0 + 31 : t.len - 1);
+  const int wave_tiles = wave0 < t.len ? (wave_most + BN - 1) / BN : 0;
+
+  // As in the forward, tile n + 1 is written to LDS piece by piece in iteration n, into the buffer
+  // that no wave reads any more, and tile n + 2's reads are issued in its place.
   Stage<DT, DP, BN> sk, sv;
   sk.init(a.k_tok, row_bytes);
   sv.init(a.v_tok, row_bytes);
-  sk.load(kp, a.k_tok, t.len);
-  sv.load(vp, a.v_tok, t.len);
+  auto aim = [&](int n) {
+    const int there = n < tiles ? n : tiles - 1, valid = n < tiles ? t.len - n * BN : 1;
+    sk.aim(kp + (int64_t)there * BN * a.k_tok, a.k_tok, valid);
+    sv.aim(vp + (int64_t)there * BN * a.v_tok, a.v_tok, valid);
+  };
+  aim(0);
+  sk.load_all();
+  sv.load_all();
+  sk.store_all(lds);
+  sv.store_all(lds + TILE);
+  aim(1);
+  sk.load_all();
+  sv.load_all();
   f32x16_t acc[OT];
 #pragma unroll
   for (int c = 0; c < OT; c++) acc[c] = zero16();
-  const int tr_lane = tr_lane_offset<DT, DP>();
-  const int wave_most = visible(a, t, wave0 + 31 < t.len ? wave0 + 31 : t.len - 1);
-  int buf = 0;
-  for (int j0 = 0; j0 < n_keys; j0 += BN, buf ^= 2 * TILE) {
-    const char *const ldsk = lds + buf, *const ldsv = ldsk + TILE;
-    sk.store(lds + buf);
-    sv.store(lds + buf + TILE);
-    __syncthreads();
-    if (j0 + BN < n_keys) {
-      sk.load(kp + (int64_t)(j0 + BN) * a.k_tok, a.k_tok, t.len - j0 - BN);
-      sv.load(vp + (int64_t)(j0 + BN) * a.v_tok, a.v_tok, t.len - j0 - BN);
-    }
-    if (wave0 >= t.len || j0 >= wave_most) continue;  // nothing for this wave's rows
-    f32x16_t s = mma_tile<DT, DP>(ldsk, q);
-    f32x16_t dp = mma_tile<DT, DP>(ldsv, g);
-    const float dist0 = (float)(i - j0 - 4 * h);
-    const int left = j0 + BN > wave_least ? vis - j0 - 4 * h : BN;
-#pragma unroll
-    for (int r = 0; r < 16; r++) {
-      float keep = 1.0f;
-      float y = score<DT, MODE>(form, s[r], dist0 - (float)acc_row(r), &keep);
-      y = acc_row(r) < left ? y : -INFINITY;
-      dp[r] = __builtin_amdgcn_exp2f(y - lse) * (dp[r] - delta) * (MODE == ATTN_CAP ? keep * gs : gs);
-    }
+  const int row_lane = row_lane_offset<DT, DP>(), tr_lane = tr_lane_offset<DT, DP>();
+  constexpr int A = L::steps, C = OT * 2, P = 2 * Stage<DT, DP, BN>::n;
+
+  auto tile = [&](int n, bool masked) {
+    const char *const ldsk = lds + (n & 1) * 2 * TILE, *const ldsv = ldsk + TILE;
+    char *const next = lds + ((n + 1) & 1) * 2 * TILE;
+    const float dist0 = (float)(i - n * BN - 4 * h);
+    const int left = vis - n * BN - 4 * h;
+    f32x16_t s, dp;
     Packed<DT> p;
-    p.set(dp);
+    auto travel = [&](int from, int to) {
 #pragma unroll
-    for (int c = 0; c < OT; c++) acc[c] = mma_cols<DT, DP>(ldsk, tr_lane, 0, c * 32, p, acc[c]);
+      for (int e = from; e < to; e++) {
+        if (e & 1) {
+          sv.store(next + TILE, e / 2);
+          sv.load(e / 2);
+        } else {
+          sk.store(next, e / 2);
+          sk.load(e / 2);
+        }
+      }
+    };
+    // products to weights, times the cap's slope where there is one
+    auto weights = [&](int from, int to) {
+#pragma unroll
+      for (int r = from; r < to; r++) {
+        float keep = 1.0f;
+        float y = score<DT, MODE>(form, s[r], dist0 - (float)acc_row(r), &keep);
+        if (masked) y = acc_row(r) < left ? y : -INFINITY;
+        s[r] = __builtin_amdgcn_exp2f(y - lse) * (MODE == ATTN_CAP ? keep * gs : gs);
+      }
+    };
+    auto grads = [&](int from, int to) {
+#pragma unroll
+      for (int r = from; r < to; r++) dp[r] = s[r] * (dp[r] - delta);
+    };
+    if constexpr (DT == DT_FP32) {
+      s = mma_tile<DT, DP>(ldsk, q, zero16());
+      dp = mma_tile<DT, DP>(ldsv, g, zero16());
+      weights(0, 16);
+      grads(0, 16);
+      p.set(dp);
+#pragma unroll
+      for (int c = 0; c < OT; c++) acc[c] = mma_cols<DT, DP>(ldsk, tr_lane, 0, c * 32, p, acc[c]);
+      travel(0, P);
+    } else {
+      pipeline<2 * A + C, 4>(
+          [&](int j) {
+            return j < A       ? read_rows<DT, DP>(ldsk, row_lane, j)
+                   : j < 2 * A ? read_rows<DT, DP>(ldsv, row_lane, j - A)
+                               : read_cols<DT, DP>(ldsk, tr_lane, 0, (j - 2 * A) % OT * 32, (j - 2 * A) / OT);
+          },
+          [&](int j, u32x4_t x) {
+            if (j < A) s = mma_rows<DT>(x, q.f[j % A], j ? s : zero16());
+            else if (j < 2 * A) dp = mma_rows<DT>(x, g.f[j % A], j > A ? dp : zero16());
+            else acc[(j - 2 * A) % OT] = mma_rows<DT>(x, p.f[(j - 2 * A) / OT], acc[(j - 2 * A) % OT]);
+          },
+          [&](int j) {
+            if (j < A) travel(j * P / A, (j + 1) * P / A);
+            else if (j < 2 * A) weights((j - A) * 16 / A, (j + 1 - A) * 16 / A);
+            // the first 16 keys' share of dQ runs while the other 16 keys' gradients are made
+            if (j == 2 * A - 1) {
+              grads(0, 8);
+              p.set_half(dp, 0);
+            }
+            if (j == 2 * A) {
+              grads(8, 16);
+              p.set_half(dp, 1);
+            }
+          });
+    }
+  };
+  for (int n = 0; n < tiles; n++) {
+    __syncthreads();
+    aim(n + 2);
+    if (n >= wave_tiles) {  // nothing for this wave's rows but to carry the tiles
+      char *const next = lds + ((n + 1) & 1) * 2 * TILE;
+      sk.store_all(next);
+      sv.store_all(next + TILE);
+      sk.load_all();
+      sv.load_all();
+    } else if ((n + 1) * BN > wave_least) {
+      tile(n, true);
+    } else {
+      tile(n, false);
+    }
   }
   __syncthreads();  // the tiles' memory is free
   store_rows<DT, DP>(lds + (threadIdx.x >> 6) * TILE, acc, i < t.len ? a.scale / gs : 0.0f,
@@ -115,79 +190,204 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
   // with a causal mask only rows from the key on see it, unless it lies in the prefix
   const int from = t.first >= t.prefix ? t.first : 0;
   const int jmask = j < t.prefix ? -1 : j;
-  const int n_tiles = (t.len - from + BM - 1) / BM, total = n_tiles * group;
+  const int total = (t.len - from + BM - 1) / BM * group;
   const float gs = DT == DT_FP16 ? *a.grad_scale : 1.0f;
   const float gs8 = gs * (DT == DT_FP16 ? 1.0f / 256.0f : 1.0f);
 
+  // Tiles travel as in the other kernels: n + 1 to LDS and n + 2's reads issued in iteration n.
+  // They come head by head.
   Stage<DT, DP, BM> sq, sg;
   float st = 0.0f;
   const int tok = a.heads * row_bytes;
   sq.init(a.q_tok, row_bytes);
   sg.init(tok, row_bytes);
-  auto load = [&](int n) {
-    const int head = t.head * group + n / n_tiles, i0 = from + n % n_tiles * BM;
-    sq.load(a.q + t.q + head * a.q_head + (int64_t)i0 * a.q_tok, a.q_tok, t.len - i0);
-    sg.load(a.dO + ((t.row0 + i0) * a.heads + head) * row_bytes, tok, t.len - i0);
-    if (threadIdx.x < 2 * BM) {
-      const int r = threadIdx.x & (BM - 1);
-      const bool is_lse = threadIdx.x < BM;
-      // rows past the document weigh nothing: exp2(y - inf) = 0
-      st = is_lse ? INFINITY : 0.0f;
-      if (i0 + r < t.len) {
-        const int64_t at = (int64_t)head * a.rows + t.row0 + i0 + r;
-        st = is_lse ? a.lse[at] * LOG2E - SHIFT : a.delta[at];
-      }
+  const float *stat_from = nullptr;  // row 0 of this thread's statistic of the tile to read
+  int stat_row = 0, stat_rows = 0;
+  int ahead_head = t.head * group, ahead = from;  // the tile to aim at next
+  const int end_head = ahead_head + group;
+  auto aim = [&]() {
+    const bool there = ahead_head < end_head;
+    const int head = there ? ahead_head : end_head - 1, i0 = there ? ahead : from;
+    const int valid = there ? t.len - i0 : 1;
+    sq.aim(a.q + t.q + head * a.q_head + (int64_t)i0 * a.q_tok, a.q_tok, valid);
+    sg.aim(a.dO + ((t.row0 + i0) * a.heads + head) * row_bytes, tok, valid);
+    stat_from = (threadIdx.x < BM ? a.lse : a.delta) + (int64_t)head * a.rows + t.row0;
+    stat_row = i0 + (threadIdx.x & (BM - 1));
+    ahead += BM;
+    if (ahead >= t.len) {
+      ahead = from;
+      ahead_head++;
     }
   };
-  load(0);
+  // Statistics of the rows, where S and dP start: -lse in units of the product (of the score
+  // behind a tanh), -inf for rows past the document, which weigh nothing; and -delta.
+  const float unit = MODE == ATTN_CAP ? 1.0f : score_form<DT, MODE>(a, t.head * group).a;
+  auto load_stat = [&]() {
+    if (threadIdx.x < 2 * BM) {
+      st = stat_from[stat_row < t.len ? stat_row : t.len - 1];
+      st = threadIdx.x >= BM ? -st : stat_row < t.len ? (SHIFT - st * LOG2E) / unit : -INFINITY;
+    }
+  };
+  auto store_stat = [&](int buf) {
+    if (threadIdx.x < 2 * BM) stat[buf][threadIdx.x] = st;
+  };
+  aim();
+  sq.load_all();
+  sg.load_all();
+  load_stat();
+  sq.store_all(lds);
+  sg.store_all(lds + TILE);
+  store_stat(0);
+  aim();
+  sq.load_all();
+  sg.load_all();
+  load_stat();
   f32x16_t dk[OT], dv[OT];
 #pragma unroll
   for (int c = 0; c < OT; c++) {
     dk[c] = zero16();
     dv[c] = zero16();
   }
-  const int tr_lane = tr_lane_offset<DT, DP>();
-  int buf = 0;
-  for (int n = 0; n < total; n++, buf ^= 1) {
-    char *const ldsq = lds + buf * 2 * TILE, *const ldsg = ldsq + TILE;
+  const int row_lane = row_lane_offset<DT, DP>(), tr_lane = tr_lane_offset<DT, DP>();
+  // matrix instructions of the four products, and pieces of a tile
+  constexpr int A = L::steps, B = DK ? A : 0, C = DV ? OT * 2 : 0, D = DK ? OT * 2 : 0;
+  constexpr int P = 2 * Stage<DT, DP, BM>::n;
+
+  auto tile = [&](const ScoreForm &form, int i0, int buf, bool masked) {
+    const char *const ldsq = lds + buf * 2 * TILE, *const ldsg = ldsq + TILE;
+    char *const next = lds + (buf ^ 1) * 2 * TILE;
     const float *const stats = stat[buf];
-    sq.store(ldsq);
-    sg.store(ldsg);
-    if (threadIdx.x < 2 * BM) stat[buf][threadIdx.x] = st;
-    __syncthreads();
-    if (n + 1 < total) load(n + 1);
-    const int i0 = from + n % n_tiles * BM;
-    // nothing where this wave has no keys, or where the tile's rows see none of them
-    if (wave0 >= t.len || (a.causal && wave0 >= t.prefix && wave0 > i0 + BM - 1)) continue;
-    const ScoreForm form = score_form<DT, MODE>(a, t.head * group + n / n_tiles);
-    f32x16_t s = mma_tile<DT, DP>(ldsq, k);
-    f32x16_t dp = DK ? mma_tile<DT, DP>(ldsg, v) : zero16();
     const float dist0 = (float)(i0 + 4 * h - j);
-    const int hide = wave0 + 31 > i0 ? jmask - i0 - 4 * h : -1;  // rows below it do not see key j
+    const int hide = jmask - i0 - 4 * h;  // rows below it do not see key j
+    f32x16_t s, dp;
+    Packed<DT> pv, pk;
+    auto travel = [&](int first, int to) {
 #pragma unroll
-    for (int g4 = 0; g4 < 4; g4++) {
-      const f32x4_t ls = *(const f32x4_t *)(stats + 8 * g4 + 4 * h);
-      const f32x4_t de = *(const f32x4_t *)(stats + BM + 8 * g4 + 4 * h);
+      for (int e = first; e < to; e++) {
+        if (e & 1) {
+          sg.store(next + TILE, e / 2);
+          sg.load(e / 2);
+        } else {
+          sq.store(next, e / 2);
+          sq.load(e / 2);
+        }
+      }
+    };
+    // The sums start from the rows' statistics: dP from -delta, S from -lse / scale, so that
+    // neither is subtracted (nor held) afterwards. The tanh wants S itself.
+    auto rows_of = [&](const float *from) {
+      f32x16_t x;
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const int r = 4 * g4 + e;
+      for (int g4 = 0; g4 < 4; g4++) {
+        const f32x4_t y = *(const f32x4_t *)(from + 8 * g4 + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[4 * g4 + e] = y[e];
+      }
+      return x;
+    };
+    const f32x16_t lse = rows_of(stats);
+    s = MODE == ATTN_CAP ? zero16() : lse;
+    if constexpr (DK) dp = rows_of(stats + BM);
+    f32x16_t slope;  // of the cap
+    auto weights = [&](int first, int to) {
+#pragma unroll
+      for (int r = first; r < to; r++) {
         float keep = 1.0f;
         float y = score<DT, MODE>(form, s[r], dist0 + (float)acc_row(r), &keep);
-        y = acc_row(r) < hide ? -INFINITY : y;
-        s[r] = __builtin_amdgcn_exp2f(y - ls[e]);
-        dp[r] = s[r] * (dp[r] - de[e]) * (MODE == ATTN_CAP ? keep * gs8 : gs8);
+        if (MODE == ATTN_CAP) y += lse[r];
+        if (masked) y = acc_row(r) < hide ? -INFINITY : y;
+        s[r] = __builtin_amdgcn_exp2f(y);
+        if (MODE == ATTN_CAP) slope[r] = keep;
       }
-    }
-    Packed<DT> p;
-    if constexpr (DV) {
-      p.set(s);
+    };
+    auto grads = [&](int first, int to) {
 #pragma unroll
-      for (int c = 0; c < OT; c++) dv[c] = mma_cols<DT, DP>(ldsg, tr_lane, 0, c * 32, p, dv[c]);
-    }
-    if constexpr (DK) {
-      p.set(dp);
+      for (int r = first; r < to; r++) {
+        dp[r] = s[r] * dp[r];
+        if (MODE == ATTN_CAP) dp[r] *= slope[r];
+        if (DT == DT_FP16) dp[r] *= gs8;
+      }
+    };
+    if constexpr (DT == DT_FP32) {
+      s = mma_tile<DT, DP>(ldsq, k, s);
+      dp = mma_tile<DT, DP>(ldsg, v, dp);
+      weights(0, 16);
+      pv.set(s);
 #pragma unroll
-      for (int c = 0; c < OT; c++) dk[c] = mma_cols<DT, DP>(ldsq, tr_lane, 0, c * 32, p, dk[c]);
+      for (int c = 0; c < OT; c++) dv[c] = mma_cols<DT, DP>(ldsg, tr_lane, 0, c * 32, pv, dv[c]);
+      grads(0, 16);
+      pk.set(dp);
+#pragma unroll
+      for (int c = 0; c < OT; c++) dk[c] = mma_cols<DT, DP>(ldsq, tr_lane, 0, c * 32, pk, dk[c]);
+      travel(0, P);
+    } else {
+      // S, then dP beside the weights, then dV beside dS, then dK beside the next tiles' travel
+      pipeline<A + B + C + D, 4>(
+          [&](int j) {
+            if (j < A) return read_rows<DT, DP>(ldsq, row_lane, j);
+            if (j < A + B) return read_rows<DT, DP>(ldsg, row_lane, j - A);
+            const int x = j < A + B + C ? j - A - B : j - A - B - C;
+            return read_cols<DT, DP>(j < A + B + C ? ldsg : ldsq, tr_lane, 0, x % OT * 32, x / OT);
+          },
+          [&](int j, u32x4_t x) {
+            if (j < A) {
+              s = mma_rows<DT>(x, k.f[j % A], s);
+            } else if (j < A + B) {
+              dp = mma_rows<DT>(x, v.f[(j - A) % A], dp);
+            } else if (j < A + B + C) {
+              const int y = j - A - B;
+              dv[y % OT] = mma_rows<DT>(x, pv.f[y / OT], dv[y % OT]);
+            } else {
+              const int y = j - A - B - C;
+              dk[y % OT] = mma_rows<DT>(x, pk.f[y / OT], dk[y % OT]);
+            }
+          },
+          [&](int j) {
+            if constexpr (DK) {
+              if (j >= A && j < A + B) weights((j - A) * 16 / A, (j + 1 - A) * 16 / A);
+            } else if (j == A - 1) {
+              weights(0, 16);
+            }
+            if (DV && j == A + B - 1) pv.set(s);
+            if constexpr (DK && DV) {
+              if (j >= A + B && j < A + B + C) grads((j - A - B) * 16 / C, (j + 1 - A - B) * 16 / C);
+              if (j == A + B + C - 1) pk.set(dp);
+              if (j >= A + B + C) travel((j - A - B - C) * P / D, (j + 1 - A - B - C) * P / D);
+            } else {
+              if (DK && j == A + B - 1) {
+                grads(0, 16);
+                pk.set(dp);
+              }
+              if (j < A) travel(j * P / A, (j + 1) * P / A);
+            }
+          });
+    }
+    store_stat(buf ^ 1);
+    load_stat();
+  };
+  int i0 = from, head = t.head * group;
+  for (int n = 0; n < total; n++) {
+    __syncthreads();
+    aim();
+    const int buf = n & 1;
+    // nothing where this wave has no keys, or where the tile's rows see none of them
+    if (wave0 >= t.len || (a.causal && wave0 >= t.prefix && wave0 > i0 + BM - 1)) {
+      char *const next = lds + (buf ^ 1) * 2 * TILE;
+      sq.store_all(next);
+      sg.store_all(next + TILE);
+      store_stat(buf ^ 1);
+      sq.load_all();
+      sg.load_all();
+      load_stat();
+    } else {
+      const ScoreForm form = score_form<DT, MODE>(a, head);
+      if (a.causal && wave0 + 31 > i0) tile(form, i0, buf, true);
+      else tile(form, i0, buf, false);
+    }
+    i0 += BM;
+    if (i0 >= t.len) {
+      i0 = from;
+      head++;
     }
   }
   __syncthreads();  // the tiles' memory is free

@@ -90,16 +90,17 @@ template <int DT> __device__ __forceinline__ f32x16_t mma_rows(u32x4_t a, u32x4_
 // nearest even) for the 16-bit types, as it is for fp32.
 template <int DT> struct Packed {
   u32x4_t f[2];
-  __device__ __forceinline__ void set(const f32x16_t &s) {
+  __device__ __forceinline__ void set_half(const f32x16_t &s, int t) {
     using T = typename AttnElem<DT>::type;
     typedef T v8 __attribute__((ext_vector_type(8)));
+    v8 x;
 #pragma unroll
-    for (int t = 0; t < 2; t++) {
-      v8 x;
-#pragma unroll
-      for (int e = 0; e < 8; e++) x[e] = (T)s[8 * t + e];
-      f[t] = __builtin_bit_cast(u32x4_t, x);
-    }
+    for (int e = 0; e < 8; e++) x[e] = (T)s[8 * t + e];
+    f[t] = __builtin_bit_cast(u32x4_t, x);
+  }
+  __device__ __forceinline__ void set(const f32x16_t &s) {
+    set_half(s, 0);
+    set_half(s, 1);
   }
 };
 template <> struct Packed<DT_FP32> {
@@ -192,10 +193,11 @@ __device__ __forceinline__ f32x16_t mma_cols(const char *tile, int lane, int r0,
   return acc;
 }
 
-// Copies ROWS rows of a head from global memory into LDS through registers: load() issues the
-// loads, store() writes them, so a tile travels while the one before is worked on. Rows past the
-// last valid one repeat it, and columns past the head's size its last 16 bytes: nothing outside
-// is read, what follows stays finite, and those columns meet zeros (Held) or are not stored.
+// Copies ROWS rows of a head from global memory into LDS through registers, in `n` pieces a
+// thread: load() issues a piece's read, store() writes it to LDS, so a tile travels while others
+// are worked on. Rows past the last valid one repeat it, and columns past the head's size its
+// last 16 bytes: nothing outside is read, what follows stays finite, and those columns meet zeros
+// (Held) or are not stored.
 template <int DT, int DP, int ROWS> struct Stage {
   using L = RowLayout<DT, DP>;
   static constexpr int total = ROWS * L::chunks;
@@ -203,6 +205,8 @@ template <int DT, int DP, int ROWS> struct Stage {
   u32x4_t r[n];
   uint32_t at[n];  // byte offset of this thread's pieces in a whole tile
   uint32_t col[n];
+  const char *base;  // first row of the tile that load() reads
+  uint32_t last;     // offset of its last row
 
   __device__ __forceinline__ void init(int stride, int row_bytes) {
 #pragma unroll
@@ -213,22 +217,28 @@ template <int DT, int DP, int ROWS> struct Stage {
       at[i] = (uint32_t)(p / L::chunks * stride) + col[i];
     }
   }
-  // base: first row of the tile (uniform); valid: rows that exist from it on, at least one.
-  __device__ __forceinline__ void load(const char *base, int stride, int valid) {
-    const uint32_t last = (uint32_t)((valid < ROWS ? valid : ROWS) - 1) * (uint32_t)stride;
-#pragma unroll
-    for (int i = 0; i < n; i++) {
-      const uint32_t limit = last + col[i];
-      r[i] = *(const u32x4_t *)(base + (at[i] < limit ? at[i] : limit));
-    }
+  // The tile at `first` (uniform) with `valid` rows from it on; at least one row is read.
+  __device__ __forceinline__ void aim(const char *first, int stride, int valid) {
+    base = first;
+    valid = valid < ROWS ? valid : ROWS;
+    last = (uint32_t)(valid > 1 ? valid - 1 : 0) * (uint32_t)stride;
   }
-  __device__ __forceinline__ void store(char *lds) const {
+  __device__ __forceinline__ void load(int i) {
+    const uint32_t limit = last + col[i];
+    r[i] = *(const u32x4_t *)(base + (at[i] < limit ? at[i] : limit));
+  }
+  __device__ __forceinline__ void store(char *lds, int i) const {
+    const int p = threadIdx.x + i * ATTN_THREADS;
+    if (total % ATTN_THREADS == 0 || p < total)
+      *(u32x4_t *)(lds + p / L::chunks * L::bytes + (p % L::chunks * 16 ^ L::f(p / L::chunks))) = r[i];
+  }
+  __device__ __forceinline__ void load_all() {
 #pragma unroll
-    for (int i = 0; i < n; i++) {
-      const int p = threadIdx.x + i * ATTN_THREADS;
-      if (total % ATTN_THREADS == 0 || p < total)
-        *(u32x4_t *)(lds + p / L::chunks * L::bytes + (p % L::chunks * 16 ^ L::f(p / L::chunks))) = r[i];
-    }
+    for (int i = 0; i < n; i++) load(i);
+  }
+  __device__ __forceinline__ void store_all(char *lds) const {
+#pragma unroll
+    for (int i = 0; i < n; i++) store(lds, i);
   }
 };
 
@@ -272,12 +282,11 @@ __device__ __forceinline__ void pipeline(Read read, Mma mma, Work work) {
   keep_order();
 }
 
-// 32 rows of an LDS tile times held columns.
+// 32 rows of an LDS tile times held columns, added to acc.
 template <int DT, int DP>
-__device__ __forceinline__ f32x16_t mma_tile(const char *tile, const Held<DT, DP> &b) {
+__device__ __forceinline__ f32x16_t mma_tile(const char *tile, const Held<DT, DP> &b, f32x16_t acc) {
   using L = RowLayout<DT, DP>;
   const int lane = row_lane_offset<DT, DP>();
-  f32x16_t acc = zero16();
 #pragma unroll
   for (int s = 0; s < L::steps; s++)
     acc = mma_rows<DT>(read_rows<DT, DP>(tile, lane, s), b.f[s], acc);

@@ -62,17 +62,33 @@ attn_fwd_kernel(const AttnArgs a) {
   const int wave_most = visible(a, t, wave0 + 31 < t.len ? wave0 + 31 : t.len - 1);
   const int wave_tiles = wave0 < t.len ? (wave_most + BN - 1) / BN : 0;
 
+  // Tiles travel through registers: a piece of K's tile n + 2 and of V's tile n + 1 is written to
+  // LDS in iteration n, into the buffer that no wave reads any more, and the next one's read is
+  // issued in its place. Past the last tile one row is read again, which keeps branches out.
   Stage<DT, DP, BN> sk, sv;
   sk.init(a.k_tok, row_bytes);
   sv.init(a.v_tok, row_bytes);
-  auto load = [&](auto &stage, const char *p, int tok, int n) {
-    stage.load(p + (int64_t)n * BN * tok, tok, t.len - n * BN);
+  auto aim = [&](auto &stage, const char *p, int tok, int n) {
+    const int there = n < tiles ? n : tiles - 1;
+    stage.aim(p + (int64_t)there * BN * tok, tok, n < tiles ? t.len - n * BN : 1);
   };
-  load(sk, kp, a.k_tok, 0);
-  load(sv, vp, a.v_tok, 0);
-  sk.store(lds[0]);
+  {
+    Stage<DT, DP, BN> sk1 = sk;
+    aim(sk, kp, a.k_tok, 0);
+    aim(sv, vp, a.v_tok, 0);
+    aim(sk1, kp, a.k_tok, 1);
+    sk.load_all();
+    sv.load_all();
+    sk1.load_all();
+    sk.store_all(lds[0]);
+    sv.store_all(lds[2]);
+    sk1.store_all(lds[1]);
+  }
+  aim(sk, kp, a.k_tok, 2);
+  aim(sv, vp, a.v_tok, 1);
+  sk.load_all();
+  sv.load_all();
   __syncthreads();
-  if (tiles > 1) load(sk, kp, a.k_tok, 1);
 
   f32x16_t acc[OT], s[NT];
 #pragma unroll
@@ -88,7 +104,7 @@ attn_fwd_kernel(const AttnArgs a) {
     const char *tile = lds[n & 1];
     if constexpr (DT == DT_FP32) {
 #pragma unroll
-      for (int b = 0; b < NT; b++) x[b] = mma_tile<DT, DP>(tile + b * 32 * L::bytes, q);
+      for (int b = 0; b < NT; b++) x[b] = mma_tile<DT, DP>(tile + b * 32 * L::bytes, q, zero16());
 #pragma unroll
       for (int i = 0; i < N1; i++) work(i);
     } else {
@@ -172,12 +188,27 @@ attn_fwd_kernel(const AttnArgs a) {
     top = half_max(top) * post;
   }
   for (int n = 0; n < tiles; n++) {
-    if (n + 1 < tiles) sk.store(lds[(n + 1) & 1]);
-    sv.store(lds[2 + (n & 1)]);
     __syncthreads();
-    if (n + 2 < tiles) load(sk, kp, a.k_tok, n + 2);
-    if (n + 1 < tiles) load(sv, vp, a.v_tok, n + 1);
-    if (n >= wave_tiles) continue;
+    char *const next_k = lds[n & 1], *const next_v = lds[2 + ((n + 1) & 1)];
+    aim(sk, kp, a.k_tok, n + 3);
+    aim(sv, vp, a.v_tok, n + 2);
+    constexpr int P = 2 * Stage<DT, DP, BN>::n;
+    auto travel = [&](int from, int to) {
+#pragma unroll
+      for (int i = from; i < to; i++) {
+        if (i & 1) {
+          sv.store(next_v, i / 2);
+          sv.load(i / 2);
+        } else {
+          sk.store(next_k, i / 2);
+          sk.load(i / 2);
+        }
+      }
+    };
+    if (n >= wave_tiles) {
+      travel(0, P);
+      continue;
+    }
     // The reference point of the exponentials follows the running maximum only once that is
     // 2^8 away: sums and weights up to 256 lose nothing, and most tiles leave the accumulator
     // as it is.
@@ -196,7 +227,7 @@ attn_fwd_kernel(const AttnArgs a) {
       weights(s, base - m, 0, E);
 #pragma unroll
       for (int b = 0; b < NT; b++) p[b].set(s[b]);
-      values(p, n, nothing);
+      values(p, n, [&](int i) { travel(i * P / N2, (i + 1) * P / N2); });
       continue;
     }
     f32x16_t next[NT];
@@ -206,10 +237,16 @@ attn_fwd_kernel(const AttnArgs a) {
     for (int b = 0; b < NT; b++) p[b].set(s[b]);
     top = -INFINITY;
     if (linear_at(n + 1)) {
-      values(p, n, [&](int i) { scores(next, n + 1, true, i * E / N2, (i + 1) * E / N2); });
+      values(p, n, [&](int i) {
+        scores(next, n + 1, true, i * E / N2, (i + 1) * E / N2);
+        travel(i * P / N2, (i + 1) * P / N2);
+      });
       base = LINEAR ? -form.slope * (float)(i - (n + 1) * BN - 4 * h) : 0.0f;
     } else {
-      values(p, n, [&](int i) { scores(next, n + 1, false, i * E / N2, (i + 1) * E / N2); });
+      values(p, n, [&](int i) {
+        scores(next, n + 1, false, i * E / N2, (i + 1) * E / N2);
+        travel(i * P / N2, (i + 1) * P / N2);
+      });
       base = 0.0f;
     }
     top = half_max(__builtin_fmaf(top, post, base));  // the halves differ in base
