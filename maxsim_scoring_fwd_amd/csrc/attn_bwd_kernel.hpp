@@ -43,49 +43,40 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
   const int wave_most = visible(a, t, wave0 + 31 < t.len ? wave0 + 31 : t.len - 1);
   const int wave_tiles = wave0 < t.len ? (wave_most + BN - 1) / BN : 0;
 
-  // As in the forward, tile n + 1 is written to LDS piece by piece in iteration n, into the buffer
-  // that no wave reads any more, and tile n + 2's reads are issued in its place.
-  Stage<DT, DP, BN> sk, sv;
-  sk.init(a.k_tok, row_bytes);
-  sv.init(a.v_tok, row_bytes);
+  // As in the forward, tile n + 1 is fetched in iteration n into the buffer that no wave reads any
+  // more.
+  const int wave = uniform((int)(threadIdx.x >> 6));
+  Carry<DT, DP, BN> ck, cv;
+  ck.init(a.k_tok, row_bytes);
+  cv.init(a.v_tok, row_bytes);
   auto aim = [&](int n) {
     const int there = n < tiles ? n : tiles - 1, valid = n < tiles ? t.len - n * BN : 1;
-    sk.aim(kp + (int64_t)there * BN * a.k_tok, a.k_tok, valid);
-    sv.aim(vp + (int64_t)there * BN * a.v_tok, a.v_tok, valid);
+    ck.aim(kp + (int64_t)there * BN * a.k_tok, a.k_tok, valid);
+    cv.aim(vp + (int64_t)there * BN * a.v_tok, a.v_tok, valid);
+  };
+  constexpr int P = 2 * Carry<DT, DP, BN>::n;
+  auto fetch = [&](int n, int from, int to) {  // pieces of tile n
+    char *const next = lds + (n & 1) * 2 * TILE;
+#pragma unroll
+    for (int e = from; e < to; e++) {
+      if (e & 1) cv.go(next + TILE, wave, e / 2);
+      else ck.go(next, wave, e / 2);
+    }
   };
   aim(0);
-  sk.load_all();
-  sv.load_all();
-  sk.store_all(lds);
-  sv.store_all(lds + TILE);
-  aim(1);
-  sk.load_all();
-  sv.load_all();
+  fetch(0, 0, P);
   f32x16_t acc[OT];
 #pragma unroll
   for (int c = 0; c < OT; c++) acc[c] = zero16();
   const int row_lane = row_lane_offset<DT, DP>(), tr_lane = tr_lane_offset<DT, DP>();
-  constexpr int A = L::steps, C = OT * 2, P = 2 * Stage<DT, DP, BN>::n;
+  constexpr int A = L::steps, C = OT * 2;
 
   auto tile = [&](int n, bool masked) {
     const char *const ldsk = lds + (n & 1) * 2 * TILE, *const ldsv = ldsk + TILE;
-    char *const next = lds + ((n + 1) & 1) * 2 * TILE;
     const float dist0 = (float)(i - n * BN - 4 * h);
     const int left = vis - n * BN - 4 * h;
     f32x16_t s, dp;
     Packed<DT> p;
-    auto travel = [&](int from, int to) {
-#pragma unroll
-      for (int e = from; e < to; e++) {
-        if (e & 1) {
-          sv.store(next + TILE, e / 2);
-          sv.load(e / 2);
-        } else {
-          sk.store(next, e / 2);
-          sk.load(e / 2);
-        }
-      }
-    };
     // products to weights, times the cap's slope where there is one
     auto weights = [&](int from, int to) {
 #pragma unroll
@@ -108,7 +99,7 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
       p.set(dp);
 #pragma unroll
       for (int c = 0; c < OT; c++) acc[c] = mma_cols<DT, DP>(ldsk, tr_lane, 0, c * 32, p, acc[c]);
-      travel(0, P);
+      fetch(n + 1, 0, P);
     } else {
       pipeline<2 * A + C, 4>(
           [&](int j) {
@@ -122,7 +113,7 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
             else acc[(j - 2 * A) % OT] = mma_rows<DT>(x, p.f[(j - 2 * A) / OT], acc[(j - 2 * A) % OT]);
           },
           [&](int j) {
-            if (j < A) travel(j * P / A, (j + 1) * P / A);
+            if (j < A) fetch(n + 1, j * P / A, (j + 1) * P / A);
             else if (j < 2 * A) weights((j - A) * 16 / A, (j + 1 - A) * 16 / A);
             // the first 16 keys' share of dQ runs while the other 16 keys' gradients are made
             if (j == 2 * A - 1) {
@@ -137,21 +128,19 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
     }
   };
   for (int n = 0; n < tiles; n++) {
-    __syncthreads();
-    aim(n + 2);
-    if (n >= wave_tiles) {  // nothing for this wave's rows but to carry the tiles
-      char *const next = lds + ((n + 1) & 1) * 2 * TILE;
-      sk.store_all(next);
-      sv.store_all(next + TILE);
-      sk.load_all();
-      sv.load_all();
+    tile_barrier();
+    aim(n + 1);
+    if (n >= wave_tiles) {  // nothing for this wave's rows but to fetch
+      fetch(n + 1, 0, P);
     } else if ((n + 1) * BN > wave_least) {
+      asm volatile("; masked");  // see the forward
       tile(n, true);
     } else {
+      asm volatile("; whole");
       tile(n, false);
     }
   }
-  __syncthreads();  // the tiles' memory is free
+  tile_barrier();  // the tiles' memory is free
   store_rows<DT, DP>(lds + (threadIdx.x >> 6) * TILE, acc, i < t.len ? a.scale / gs : 0.0f,
                      a.dq + ((t.row0 + wave0) * a.heads + t.head) * row_bytes,
                      (int64_t)a.heads * row_bytes, t.rows - wave0, row_bytes);
@@ -194,53 +183,62 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
   const float gs = DT == DT_FP16 ? *a.grad_scale : 1.0f;
   const float gs8 = gs * (DT == DT_FP16 ? 1.0f / 256.0f : 1.0f);
 
-  // Tiles travel as in the other kernels: n + 1 to LDS and n + 2's reads issued in iteration n.
-  // They come head by head.
-  Stage<DT, DP, BM> sq, sg;
+  // Tiles are fetched as in the other kernels, head by head; the rows' statistics pass through a
+  // register, one tile further ahead.
+  const int wave = uniform((int)(threadIdx.x >> 6));
+  Carry<DT, DP, BM> cq, cg;
   float st = 0.0f;
   const int tok = a.heads * row_bytes;
-  sq.init(a.q_tok, row_bytes);
-  sg.init(tok, row_bytes);
-  const float *stat_from = nullptr;  // row 0 of this thread's statistic of the tile to read
-  int stat_row = 0, stat_rows = 0;
-  int ahead_head = t.head * group, ahead = from;  // the tile to aim at next
-  const int end_head = ahead_head + group;
+  cq.init(a.q_tok, row_bytes);
+  cg.init(tok, row_bytes);
+  int next_head = t.head * group, next_row = from;  // of the tile to aim at
+  const int end_head = next_head + group;
   auto aim = [&]() {
-    const bool there = ahead_head < end_head;
-    const int head = there ? ahead_head : end_head - 1, i0 = there ? ahead : from;
+    const bool there = next_head < end_head;
+    const int head = there ? next_head : end_head - 1, i0 = there ? next_row : from;
     const int valid = there ? t.len - i0 : 1;
-    sq.aim(a.q + t.q + head * a.q_head + (int64_t)i0 * a.q_tok, a.q_tok, valid);
-    sg.aim(a.dO + ((t.row0 + i0) * a.heads + head) * row_bytes, tok, valid);
-    stat_from = (threadIdx.x < BM ? a.lse : a.delta) + (int64_t)head * a.rows + t.row0;
-    stat_row = i0 + (threadIdx.x & (BM - 1));
-    ahead += BM;
-    if (ahead >= t.len) {
-      ahead = from;
-      ahead_head++;
+    cq.aim(a.q + t.q + head * a.q_head + (int64_t)i0 * a.q_tok, a.q_tok, valid);
+    cg.aim(a.dO + ((t.row0 + i0) * a.heads + head) * row_bytes, tok, valid);
+    next_row += BM;
+    if (next_row >= t.len) {
+      next_row = from;
+      next_head++;
+    }
+  };
+  constexpr int P = 2 * Carry<DT, DP, BM>::n;
+  auto fetch = [&](int n, int first, int to) {  // pieces of tile n
+    char *const next = lds + (n & 1) * 2 * TILE;
+#pragma unroll
+    for (int e = first; e < to; e++) {
+      if (e & 1) cg.go(next + TILE, wave, e / 2);
+      else cq.go(next, wave, e / 2);
     }
   };
   // Statistics of the rows, where S and dP start: -lse in units of the product (of the score
   // behind a tanh), -inf for rows past the document, which weigh nothing; and -delta.
   const float unit = MODE == ATTN_CAP ? 1.0f : score_form<DT, MODE>(a, t.head * group).a;
+  int stat_head = t.head * group, stat_row = from;  // of the tile whose statistics come next
   auto load_stat = [&]() {
     if (threadIdx.x < 2 * BM) {
-      st = stat_from[stat_row < t.len ? stat_row : t.len - 1];
-      st = threadIdx.x >= BM ? -st : stat_row < t.len ? (SHIFT - st * LOG2E) / unit : -INFINITY;
+      const int row = stat_row + (threadIdx.x & (BM - 1));
+      const int head = stat_head < end_head ? stat_head : end_head - 1;
+      const float x = (threadIdx.x < BM ? a.lse : a.delta)[(int64_t)head * a.rows + t.row0 +
+                                                           (row < t.len ? row : t.len - 1)];
+      st = threadIdx.x >= BM ? -x : row < t.len ? (SHIFT - x * LOG2E) / unit : -INFINITY;
+    }
+    stat_row += BM;
+    if (stat_row >= t.len) {
+      stat_row = from;
+      stat_head++;
     }
   };
   auto store_stat = [&](int buf) {
     if (threadIdx.x < 2 * BM) stat[buf][threadIdx.x] = st;
   };
   aim();
-  sq.load_all();
-  sg.load_all();
+  fetch(0, 0, P);
   load_stat();
-  sq.store_all(lds);
-  sg.store_all(lds + TILE);
   store_stat(0);
-  aim();
-  sq.load_all();
-  sg.load_all();
   load_stat();
   f32x16_t dk[OT], dv[OT];
 #pragma unroll
@@ -251,28 +249,14 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
   const int row_lane = row_lane_offset<DT, DP>(), tr_lane = tr_lane_offset<DT, DP>();
   // matrix instructions of the four products, and pieces of a tile
   constexpr int A = L::steps, B = DK ? A : 0, C = DV ? OT * 2 : 0, D = DK ? OT * 2 : 0;
-  constexpr int P = 2 * Stage<DT, DP, BM>::n;
 
-  auto tile = [&](const ScoreForm &form, int i0, int buf, bool masked) {
-    const char *const ldsq = lds + buf * 2 * TILE, *const ldsg = ldsq + TILE;
-    char *const next = lds + (buf ^ 1) * 2 * TILE;
-    const float *const stats = stat[buf];
+  auto tile = [&](const ScoreForm &form, int i0, int n, bool masked) {
+    const char *const ldsq = lds + (n & 1) * 2 * TILE, *const ldsg = ldsq + TILE;
+    const float *const stats = stat[n & 1];
     const float dist0 = (float)(i0 + 4 * h - j);
     const int hide = jmask - i0 - 4 * h;  // rows below it do not see key j
     f32x16_t s, dp;
     Packed<DT> pv, pk;
-    auto travel = [&](int first, int to) {
-#pragma unroll
-      for (int e = first; e < to; e++) {
-        if (e & 1) {
-          sg.store(next + TILE, e / 2);
-          sg.load(e / 2);
-        } else {
-          sq.store(next, e / 2);
-          sq.load(e / 2);
-        }
-      }
-    };
     // The sums start from the rows' statistics: dP from -delta, S from -lse / scale, so that
     // neither is subtracted (nor held) afterwards. The tanh wants S itself.
     auto rows_of = [&](const float *from) {
@@ -319,9 +303,9 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
       pk.set(dp);
 #pragma unroll
       for (int c = 0; c < OT; c++) dk[c] = mma_cols<DT, DP>(ldsq, tr_lane, 0, c * 32, pk, dk[c]);
-      travel(0, P);
+      fetch(n + 1, 0, P);
     } else {
-      // S, then dP beside the weights, then dV beside dS, then dK beside the next tiles' travel
+      // S, then dP beside the weights, then dV beside dS, then dK; the next tile's fetch beside S
       pipeline<A + B + C + D, 4>(
           [&](int j) {
             if (j < A) return read_rows<DT, DP>(ldsq, row_lane, j);
@@ -352,37 +336,36 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
             if constexpr (DK && DV) {
               if (j >= A + B && j < A + B + C) grads((j - A - B) * 16 / C, (j + 1 - A - B) * 16 / C);
               if (j == A + B + C - 1) pk.set(dp);
-              if (j >= A + B + C) travel((j - A - B - C) * P / D, (j + 1 - A - B - C) * P / D);
             } else {
               if (DK && j == A + B - 1) {
                 grads(0, 16);
                 pk.set(dp);
               }
-              if (j < A) travel(j * P / A, (j + 1) * P / A);
             }
+            if (j < A) fetch(n + 1, j * P / A, (j + 1) * P / A);
           });
     }
-    store_stat(buf ^ 1);
+    store_stat((n + 1) & 1);
     load_stat();
   };
   int i0 = from, head = t.head * group;
   for (int n = 0; n < total; n++) {
-    __syncthreads();
+    tile_barrier();
     aim();
-    const int buf = n & 1;
     // nothing where this wave has no keys, or where the tile's rows see none of them
     if (wave0 >= t.len || (a.causal && wave0 >= t.prefix && wave0 > i0 + BM - 1)) {
-      char *const next = lds + (buf ^ 1) * 2 * TILE;
-      sq.store_all(next);
-      sg.store_all(next + TILE);
-      store_stat(buf ^ 1);
-      sq.load_all();
-      sg.load_all();
+      fetch(n + 1, 0, P);
+      store_stat((n + 1) & 1);
       load_stat();
     } else {
       const ScoreForm form = score_form<DT, MODE>(a, head);
-      if (a.causal && wave0 + 31 > i0) tile(form, i0, buf, true);
-      else tile(form, i0, buf, false);
+      if (a.causal && wave0 + 31 > i0) {
+        asm volatile("; masked");
+        tile(form, i0, n, true);
+      } else {
+        asm volatile("; whole");
+        tile(form, i0, n, false);
+      }
     }
     i0 += BM;
     if (i0 >= t.len) {
@@ -390,7 +373,7 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
       head++;
     }
   }
-  __syncthreads();  // the tiles' memory is free
+  tile_barrier();  // the tiles' memory is free
   const int64_t first = ((t.row0 + wave0) * a.kv_heads + t.head) * row_bytes;
   const int64_t stride = (int64_t)a.kv_heads * row_bytes;
   char *const mine = lds + (threadIdx.x >> 6) * TILE;

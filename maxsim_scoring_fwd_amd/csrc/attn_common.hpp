@@ -108,25 +108,20 @@ template <> struct Packed<DT_FP32> {
   __device__ __forceinline__ void set(const f32x16_t &s) { f = s; }
 };
 
-// Rows of a head in LDS: DP columns (the head's size rounded up; the rest zeros). LDS serves 16
-// lanes of a 16-byte read, or 32 lanes of an 8-byte one, a clock, if they fall on different 16
-// bytes of 256. 16-bit rows have no padding; their 16-byte chunks are stored at chunk ^ f(row):
-// 16 rows of one chunk (an operand in rows) then lie on 16 different places, and so do 4
-// consecutive rows x 4 chunks (the transposing reads). With fp32 the matrix core is the slower
-// by far; its rows are padded by a chunk instead.
+// Rows of a head in LDS: DP columns (the head's size rounded up), no padding. LDS serves 16 lanes
+// of a 16-byte read, or 32 lanes of an 8-byte one, a clock, if they fall on different 16 bytes of
+// 256. A row's 16-byte chunks are stored at chunk ^ f(row): 16 rows of one chunk (an operand in
+// rows) then lie on 16 different places, and so do 4 consecutive rows x 4 chunks (the transposing
+// reads). f is linear: f(a ^ b) = f(a) ^ f(b).
 template <int DT, int DP> struct RowLayout {
   static constexpr int eb = Elem<DT>::bytes;
   static constexpr int chunks = DP * eb / 16;  // 16-byte chunks of a row
   static constexpr int steps = DP * eb / 32;   // mma_rows steps of a row
-  static constexpr int bytes = DP * eb + (DT == DT_FP32 ? 16 : 0);
+  static constexpr int bytes = DP * eb;
   // bits of a byte offset that f(row) reaches: as many as divide the row
-  static constexpr int mask = DT == DT_FP32     ? 0
-                              : chunks % 16 == 0 ? 255
-                              : chunks % 8 == 0  ? 127
-                                                 : 63;
+  static constexpr int mask = chunks % 16 == 0 ? 255 : chunks % 8 == 0 ? 127 : 63;
   // f(row) in bytes. Rows that differ by 16 share it, and row + 8 flips bit 5.
-  __device__ __forceinline__ static int f(int row) {
-    if (mask == 0) return 0;
+  __device__ __forceinline__ static constexpr int f(int row) {
     const int high = (row >> 2) & 3;
     return 16 * (mask == 255 ? (row & 3) << 2 | high : mask == 127 ? (row & 2) << 1 | high : high);
   }
@@ -141,7 +136,7 @@ template <int DT, int DP> struct RowLayout {
 template <int DT, int DP> __device__ __forceinline__ int tr_lane_offset() {
   using L = RowLayout<DT, DP>;
   const int l = threadIdx.x & 63, h = l >> 5;
-  if constexpr (DT == DT_FP32) return 4 * h * L::bytes + (l & 31) * 4;
+  if constexpr (DT == DT_FP32) return 4 * h * L::bytes + (((l & 31) * 4) ^ L::f(4 * h));
   const int row = 4 * h + ((l & 15) >> 2);
   return row * L::bytes + ((((l >> 4) & 1) * 32 + (l & 2) * 8) ^ L::f(row)) + (l & 1) * 8;
 }
@@ -149,7 +144,9 @@ template <int DT, int DP> __device__ __forceinline__ int tr_lane_offset() {
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ s16x4_t read_tr(const char *p) {
+// restrict: without it the compiler takes the read for one of what a Carry may be fetching, and
+// waits for all of that first (tile_barrier has waited for the tile that is read).
+__device__ __forceinline__ s16x4_t read_tr(const char *__restrict__ p) {
   typedef __attribute__((address_space(3))) char lds_char;
   typedef __attribute__((address_space(3))) s16x4_t lds_v4;
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(lds_char *)p);
@@ -182,7 +179,9 @@ __device__ __forceinline__ f32x16_t mma_cols(const char *tile, int lane, int r0,
   if constexpr (DT == DT_FP32) {
 #pragma unroll
     for (int r = 0; r < 16; r++) {
-      const float a = *(const float *)(tile + lane + (r0 + (r & 3) + 8 * (r >> 2)) * L::bytes + c0 * 4);
+      // rows 8 (r / 4) + r % 4 of this half's, whose f is that row's on top of the lane's
+      const int row = (r & 3) + 8 * (r >> 2);
+      const float a = *(const float *)(tile + (r0 + row) * L::bytes + L::along(lane ^ L::f(row), c0 * 4));
       acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p.f[r], acc, 0, 0, 0);
     }
   } else {
@@ -193,28 +192,27 @@ __device__ __forceinline__ f32x16_t mma_cols(const char *tile, int lane, int r0,
   return acc;
 }
 
-// Copies ROWS rows of a head from global memory into LDS through registers, in `n` pieces a
-// thread: load() issues a piece's read, store() writes it to LDS, so a tile travels while others
-// are worked on. Rows past the last valid one repeat it, and columns past the head's size its
-// last 16 bytes: nothing outside is read, what follows stays finite, and those columns meet zeros
-// (Held) or are not stored.
-template <int DT, int DP, int ROWS> struct Stage {
+// Copies ROWS rows of a head from global memory straight into LDS, in `n` pieces: a wave's piece
+// is 64 chunks that lie side by side in LDS, and each lane fetches the one that belongs there.
+// Rows past the last valid one repeat it, and columns past the head's size its last 16 bytes:
+// nothing outside is read, what follows stays finite, and those columns meet zeros (Held) or are
+// not stored. Arrival is waited for by tile_barrier.
+template <int DT, int DP, int ROWS> struct Carry {
   using L = RowLayout<DT, DP>;
   static constexpr int total = ROWS * L::chunks;
   static constexpr int n = (total + ATTN_THREADS - 1) / ATTN_THREADS;
-  u32x4_t r[n];
-  uint32_t at[n];  // byte offset of this thread's pieces in a whole tile
+  uint32_t at[n];  // byte offset of this lane's chunks in a whole tile
   uint32_t col[n];
-  const char *base;  // first row of the tile that load() reads
+  const char *base;  // first row of the tile
   uint32_t last;     // offset of its last row
 
   __device__ __forceinline__ void init(int stride, int row_bytes) {
 #pragma unroll
     for (int i = 0; i < n; i++) {
-      const int p = threadIdx.x + i * ATTN_THREADS;
-      const int c = p % L::chunks * 16;
+      const int p = threadIdx.x + i * ATTN_THREADS, row = p / L::chunks;
+      const int c = (p % L::chunks * 16) ^ L::f(row);
       col[i] = c < row_bytes ? c : row_bytes - 16;
-      at[i] = (uint32_t)(p / L::chunks * stride) + col[i];
+      at[i] = (uint32_t)(row * stride) + col[i];
     }
   }
   // The tile at `first` (uniform) with `valid` rows from it on; at least one row is read.
@@ -223,24 +221,29 @@ template <int DT, int DP, int ROWS> struct Stage {
     valid = valid < ROWS ? valid : ROWS;
     last = (uint32_t)(valid > 1 ? valid - 1 : 0) * (uint32_t)stride;
   }
-  __device__ __forceinline__ void load(int i) {
+  // Piece i of the tile, to the tile at lds. wave: this wave's number (uniform).
+  __device__ __forceinline__ void go(char *lds, int wave, int i) const {
+    typedef __attribute__((address_space(3))) void lds_void;
+    typedef __attribute__((address_space(1))) const void global_void;
+    const int p = wave * 64 + i * ATTN_THREADS;
+    if (total % ATTN_THREADS != 0 && p >= total) return;
     const uint32_t limit = last + col[i];
-    r[i] = *(const u32x4_t *)(base + (at[i] < limit ? at[i] : limit));
+    __builtin_amdgcn_global_load_lds((global_void *)(base + (at[i] < limit ? at[i] : limit)),
+                                     (lds_void *)(lds + p * 16), 16, 0, 0);
   }
-  __device__ __forceinline__ void store(char *lds, int i) const {
-    const int p = threadIdx.x + i * ATTN_THREADS;
-    if (total % ATTN_THREADS == 0 || p < total)
-      *(u32x4_t *)(lds + p / L::chunks * L::bytes + (p % L::chunks * 16 ^ L::f(p / L::chunks))) = r[i];
-  }
-  __device__ __forceinline__ void load_all() {
+  __device__ __forceinline__ void all(char *lds, int wave) const {
 #pragma unroll
-    for (int i = 0; i < n; i++) load(i);
-  }
-  __device__ __forceinline__ void store_all(char *lds) const {
-#pragma unroll
-    for (int i = 0; i < n; i++) store(lds, i);
+    for (int i = 0; i < n; i++) go(lds, wave, i);
   }
 };
+
+// Every wave's carried pieces and LDS writes have arrived, and its LDS reads are done.
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);  // no loads, no LDS accesses outstanding
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // This lane's share of 32 rows as an mma_rows operand held in registers: row l % 32 (clamped to
 // the last valid one), every step's 16 bytes; columns past the head's size are zero.

@@ -21,6 +21,8 @@ template <int DT, int DP> struct FwdShape {
   static constexpr int waves = DP >= 256 ? 1 : DP >= 96 ? 2 : 3;
 };
 
+template <int N> struct From { static constexpr int value = N; };
+
 template <int DT, int DP, int MODE>
 __global__ void __launch_bounds__(ATTN_THREADS)
 __attribute__((amdgpu_waves_per_eu(FwdShape<DT, DP>::waves, FwdShape<DT, DP>::waves)))
@@ -62,33 +64,23 @@ attn_fwd_kernel(const AttnArgs a) {
   const int wave_most = visible(a, t, wave0 + 31 < t.len ? wave0 + 31 : t.len - 1);
   const int wave_tiles = wave0 < t.len ? (wave_most + BN - 1) / BN : 0;
 
-  // Tiles travel through registers: a piece of K's tile n + 2 and of V's tile n + 1 is written to
-  // LDS in iteration n, into the buffer that no wave reads any more, and the next one's read is
-  // issued in its place. Past the last tile one row is read again, which keeps branches out.
-  Stage<DT, DP, BN> sk, sv;
-  sk.init(a.k_tok, row_bytes);
-  sv.init(a.v_tok, row_bytes);
-  auto aim = [&](auto &stage, const char *p, int tok, int n) {
+  // In iteration n, K's tile n + 2 and V's tile n + 1 are fetched into the buffers that no wave
+  // reads any more. Past the last tile one row is fetched again, which keeps branches out.
+  const int wave = uniform((int)(threadIdx.x >> 6));
+  Carry<DT, DP, BN> ck, cv;
+  ck.init(a.k_tok, row_bytes);
+  cv.init(a.v_tok, row_bytes);
+  auto aim = [&](auto &carry, const char *p, int tok, int n) {
     const int there = n < tiles ? n : tiles - 1;
-    stage.aim(p + (int64_t)there * BN * tok, tok, n < tiles ? t.len - n * BN : 1);
+    carry.aim(p + (int64_t)there * BN * tok, tok, n < tiles ? t.len - n * BN : 1);
   };
-  {
-    Stage<DT, DP, BN> sk1 = sk;
-    aim(sk, kp, a.k_tok, 0);
-    aim(sv, vp, a.v_tok, 0);
-    aim(sk1, kp, a.k_tok, 1);
-    sk.load_all();
-    sv.load_all();
-    sk1.load_all();
-    sk.store_all(lds[0]);
-    sv.store_all(lds[2]);
-    sk1.store_all(lds[1]);
-  }
-  aim(sk, kp, a.k_tok, 2);
-  aim(sv, vp, a.v_tok, 1);
-  sk.load_all();
-  sv.load_all();
-  __syncthreads();
+  aim(ck, kp, a.k_tok, 0);
+  ck.all(lds[0], wave);
+  aim(ck, kp, a.k_tok, 1);
+  ck.all(lds[1], wave);
+  aim(cv, vp, a.v_tok, 0);
+  cv.all(lds[2], wave);
+  tile_barrier();
 
   f32x16_t acc[OT], s[NT];
 #pragma unroll
@@ -98,41 +90,46 @@ attn_fwd_kernel(const AttnArgs a) {
 
   const int row_lane = row_lane_offset<DT, DP>();
   constexpr int N1 = NT * L::steps, N2 = NT * OT * 2, E = NT * 16;  // products; elements of a lane
-  // Matrix work of a step, with share i of other vector work beside instruction i. 16-bit types
-  // run it as a pipeline; fp32 is bound by its matrix instructions alone.
-  auto products = [&](f32x16_t (&x)[NT], int n, auto work) {
-    const char *tile = lds[n & 1];
-    if constexpr (DT == DT_FP32) {
+  // Products of tile n with the keys alone, for the first tile.
+  auto products = [&](f32x16_t (&x)[NT], int n) {
 #pragma unroll
-      for (int b = 0; b < NT; b++) x[b] = mma_tile<DT, DP>(tile + b * 32 * L::bytes, q, zero16());
-#pragma unroll
-      for (int i = 0; i < N1; i++) work(i);
-    } else {
-      pipeline<N1, 4>(
-          [&](int i) { return read_rows<DT, DP>(tile + i / L::steps * 32 * L::bytes, row_lane, i % L::steps); },
-          [&](int i, u32x4_t v) {
-            f32x16_t &c = x[i / L::steps];
-            c = mma_rows<DT>(v, q.f[i % L::steps], i % L::steps ? c : zero16());
-          },
-          work);
-    }
+    for (int b = 0; b < NT; b++) x[b] = mma_tile<DT, DP>(lds[n & 1] + b * 32 * L::bytes, q, zero16());
   };
-  auto values = [&](const Packed<DT> (&p)[NT], int n, auto work) {
-    const char *tile = lds[2 + (n & 1)];
+  // Tile n + 1's products and then, if VALUES, tile n's sum of values, as one run of matrix
+  // instructions: work(i) beside each, i the number of the instruction. fp32 is bound by its
+  // matrix instructions alone.
+  auto run = [&](auto first, f32x16_t (&x)[NT], const Packed<DT> (&p)[NT], int n, auto work) {
+    constexpr int F = decltype(first)::value;  // number of the first instruction: 0, or N1
+    const char *kt = lds[(n + 1) & 1], *vt = lds[2 + (n & 1)];
     if constexpr (DT == DT_FP32) {
+      if constexpr (F == 0) products(x, n + 1);
+#pragma unroll
+      for (int i = F; i < N1; i++) work(i);
 #pragma unroll
       for (int b = 0; b < NT; b++)
 #pragma unroll
         for (int c = 0; c < OT; c++)
-          acc[c] = mma_cols<DT, DP>(tile, tr_lane, b * 32, c * 32, p[b], acc[c]);
+          acc[c] = mma_cols<DT, DP>(vt, tr_lane, b * 32, c * 32, p[b], acc[c]);
 #pragma unroll
-      for (int i = 0; i < N2; i++) work(i);
+      for (int i = N1; i < N1 + N2; i++) work(i);
     } else {
-      // 16 keys after 16, so that neighbours add to different accumulators
-      pipeline<N2, 4>(
-          [&](int i) { return read_cols<DT, DP>(tile, tr_lane, i / OT / 2 * 32, i % OT * 32, i / OT % 2); },
-          [&](int i, u32x4_t v) { acc[i % OT] = mma_rows<DT>(v, p[i / OT / 2].f[i / OT % 2], acc[i % OT]); },
-          work);
+      pipeline<N1 + N2 - F, 4>(
+          [&](int j) {
+            const int i = j + F, y = i - N1;
+            return i < N1 ? read_rows<DT, DP>(kt + i / L::steps * 32 * L::bytes, row_lane, i % L::steps)
+                          // 16 keys after 16, so that neighbours add to different accumulators
+                          : read_cols<DT, DP>(vt, tr_lane, y / OT / 2 * 32, y % OT * 32, y / OT % 2);
+          },
+          [&](int j, u32x4_t v) {
+            const int i = j + F, y = i - N1;
+            if (i < N1) {
+              f32x16_t &c = x[i / L::steps % NT];
+              c = mma_rows<DT>(v, q.f[i % L::steps], i % L::steps ? c : zero16());
+            } else {
+              acc[y % OT] = mma_rows<DT>(v, p[y / OT / 2].f[y / OT % 2], acc[y % OT]);
+            }
+          },
+          [&](int j) { work(j + F); });
     }
   };
   // Products of tile n to scores, and their maximum, elements from .. to - 1. Where no key of the
@@ -180,33 +177,23 @@ attn_fwd_kernel(const AttnArgs a) {
       x[e / 16][e % 16] = w;
     }
   };
-  auto nothing = [](int) {};
-
   if (wave_tiles > 0) {
-    products(s, 0, nothing);
+    products(s, 0);
     scores(s, 0, false, 0, E);
     top = half_max(top) * post;
   }
   for (int n = 0; n < tiles; n++) {
-    __syncthreads();
-    char *const next_k = lds[n & 1], *const next_v = lds[2 + ((n + 1) & 1)];
-    aim(sk, kp, a.k_tok, n + 3);
-    aim(sv, vp, a.v_tok, n + 2);
-    constexpr int P = 2 * Stage<DT, DP, BN>::n;
-    auto travel = [&](int from, int to) {
-#pragma unroll
-      for (int i = from; i < to; i++) {
-        if (i & 1) {
-          sv.store(next_v, i / 2);
-          sv.load(i / 2);
-        } else {
-          sk.store(next_k, i / 2);
-          sk.load(i / 2);
-        }
-      }
+    tile_barrier();
+    aim(ck, kp, a.k_tok, n + 2);
+    aim(cv, vp, a.v_tok, n + 1);
+    constexpr int C = Carry<DT, DP, BN>::n;
+    auto fetch = [&](int i) {
+      if (i < C) ck.go(lds[n & 1], wave, i);
+      else if (i < 2 * C) cv.go(lds[2 + ((n + 1) & 1)], wave, i - C);
     };
-    if (n >= wave_tiles) {
-      travel(0, P);
+    if (n >= wave_tiles) {  // nothing for this wave's rows but to fetch
+#pragma unroll
+      for (int i = 0; i < 2 * C; i++) fetch(i);
       continue;
     }
     // The reference point of the exponentials follows the running maximum only once that is
@@ -222,31 +209,37 @@ attn_fwd_kernel(const AttnArgs a) {
 #pragma unroll
         for (int r = 0; r < 16; r++) acc[c][r] *= f;
     }
+    const float off = base - m;
     Packed<DT> p[NT];
+    f32x16_t next[NT];
     if (n + 1 == wave_tiles) {
-      weights(s, base - m, 0, E);
+      weights(s, off, 0, E);
 #pragma unroll
       for (int b = 0; b < NT; b++) p[b].set(s[b]);
-      values(p, n, [&](int i) { travel(i * P / N2, (i + 1) * P / N2); });
+      run(From<N1>{}, next, p, n, [&](int i) { fetch(i - N1); });
       continue;
     }
-    f32x16_t next[NT];
-    const float off = base - m;
-    products(next, n + 1, [&](int i) { weights(s, off, i * E / N1, (i + 1) * E / N1); });
-#pragma unroll
-    for (int b = 0; b < NT; b++) p[b].set(s[b]);
     top = -INFINITY;
-    if (linear_at(n + 1)) {
-      values(p, n, [&](int i) {
-        scores(next, n + 1, true, i * E / N2, (i + 1) * E / N2);
-        travel(i * P / N2, (i + 1) * P / N2);
+    auto step = [&](bool linear) {
+      run(From<0>{}, next, p, n, [&](int i) {
+        fetch(i);
+        if (i < N1) weights(s, off, i * E / N1, (i + 1) * E / N1);
+        if (i == N1 - 1) {
+#pragma unroll
+          for (int b = 0; b < NT; b++) p[b].set(s[b]);
+        }
+        if (i >= N1) scores(next, n + 1, linear, (i - N1) * E / N2, (i + 1 - N1) * E / N2);
       });
+    };
+    // (the marks keep the compiler from moving the two copies' common start, and with it the
+    // vector work beside the first matrix instructions, before the branch)
+    if (linear_at(n + 1)) {
+      asm volatile("; linear");
+      step(true);
       base = LINEAR ? -form.slope * (float)(i - (n + 1) * BN - 4 * h) : 0.0f;
     } else {
-      values(p, n, [&](int i) {
-        scores(next, n + 1, false, i * E / N2, (i + 1) * E / N2);
-        travel(i * P / N2, (i + 1) * P / N2);
-      });
+      asm volatile("; full");
+      step(false);
       base = 0.0f;
     }
     top = half_max(__builtin_fmaf(top, post, base));  // the halves differ in base
@@ -255,7 +248,7 @@ attn_fwd_kernel(const AttnArgs a) {
   }
   sum = half_sum(sum);
   const bool real = i < t.len && sum > 0.0f;
-  __syncthreads();  // the tiles' memory is free
+  tile_barrier();  // the tiles' memory is free
   if (h == 0 && i < t.rows) *lse = real ? (m + __builtin_amdgcn_logf(sum)) * LN2 : -INFINITY;
   store_rows<DT, DP>(lds[threadIdx.x >> 6], acc, real ? 1.0f / sum : 0.0f,
                      a.o + ((t.row0 + wave0) * a.heads + t.head) * row_bytes,
