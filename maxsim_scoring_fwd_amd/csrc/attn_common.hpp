@@ -144,9 +144,7 @@ template <int DT, int DP> __device__ __forceinline__ int tr_lane_offset() {
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 
-// restrict: without it the compiler takes the read for one of what a Carry may be fetching, and
-// waits for all of that first (tile_barrier has waited for the tile that is read).
-__device__ __forceinline__ s16x4_t read_tr(const char *__restrict__ p) {
+__device__ __forceinline__ s16x4_t read_tr(const char *p) {
   typedef __attribute__((address_space(3))) char lds_char;
   typedef __attribute__((address_space(3))) s16x4_t lds_v4;
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(lds_char *)p);
@@ -217,19 +215,22 @@ template <int DT, int DP, int ROWS> struct Carry {
   }
   // The tile at `first` (uniform) with `valid` rows from it on; at least one row is read.
   __device__ __forceinline__ void aim(const char *first, int stride, int valid) {
-    base = first;
+    base = (const char *)uniform((int64_t)(uintptr_t)first);
     valid = valid < ROWS ? valid : ROWS;
     last = (uint32_t)(valid > 1 ? valid - 1 : 0) * (uint32_t)stride;
   }
   // Piece i of the tile, to the tile at lds. wave: this wave's number (uniform).
   __device__ __forceinline__ void go(char *lds, int wave, int i) const {
-    typedef __attribute__((address_space(3))) void lds_void;
-    typedef __attribute__((address_space(1))) const void global_void;
+    typedef __attribute__((address_space(3))) char lds_char;
     const int p = wave * 64 + i * ATTN_THREADS;
     if (total % ATTN_THREADS != 0 && p >= total) return;
-    const uint32_t limit = last + col[i];
-    __builtin_amdgcn_global_load_lds((global_void *)(base + (at[i] < limit ? at[i] : limit)),
-                                     (lds_void *)(lds + p * 16), 16, 0, 0);
+    const uint32_t limit = last + col[i], from = at[i] < limit ? at[i] : limit;
+    const int to = uniform((int)(uintptr_t)(lds_char *)(lds + p * 16));
+    // The instruction itself: beside the builtin the compiler waits for every LDS read in flight
+    // wherever it needs one. It has no result in registers, and tile_barrier waits for it.
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(to), "v"(from), "s"(base));
   }
   __device__ __forceinline__ void all(char *lds, int wave) const {
 #pragma unroll
