@@ -11,6 +11,7 @@ using namespace maxsim;
 
 namespace {
 
+constexpr int64_t SHORT_DOC = 512;  // mean tokens of a document
 constexpr int64_t MAX_TOKEN_BYTES = (int64_t)1 << 24;  // 64 rows of it stay within 31 bits
 
 // A tensor's strides (in elements, all multiples of 16 bytes) as byte strides.
@@ -24,6 +25,16 @@ int strides(const maxsim_attention_tensor &x, int eb, int64_t &doc, int64_t &hea
   doc = x.doc_stride * eb;
   head = x.head_stride * eb;
   tok = (int)(x.token_stride * eb);
+  return MAXSIM_OK;
+}
+
+// Tiles of `rows` tokens.
+int set_tiles(AttnArgs &a, int rows) {
+  const int64_t per_doc = ((int64_t)a.nd + rows - 1) / rows;
+  const int64_t slots = a.offsets ? a.n_tokens / rows + a.n_docs + 2 : a.n_docs * per_doc;
+  a.tiles_per_doc.set(per_doc ? (uint32_t)per_doc : 1);
+  if (slots > 0x7fffffff || slots * a.heads > 0x7fffffff) return MAXSIM_ERR_SHAPE;
+  a.slots = (uint32_t)slots;
   return MAXSIM_OK;
 }
 
@@ -69,12 +80,7 @@ int fill(const maxsim_attention_desc *s, AttnArgs &a) {
   a.softcap = s->softcap;
   a.scale = s->scale;
   a.slopes = s->slopes;
-  const int64_t per_doc = ((int64_t)a.nd + ATTN_ROWS - 1) / ATTN_ROWS;
-  const int64_t slots = packed ? a.n_tokens / ATTN_ROWS + a.n_docs + 2 : a.n_docs * per_doc;
-  a.tiles_per_doc.set(per_doc ? (uint32_t)per_doc : 1);
-  if (slots > 0x7fffffff || slots * a.heads > 0x7fffffff) return MAXSIM_ERR_SHAPE;
-  a.slots = (uint32_t)slots;
-  return MAXSIM_OK;
+  return set_tiles(a, ATTN_ROWS);
 }
 
 int mode_of(const AttnArgs &a) {
@@ -86,8 +92,7 @@ int run(const void *fn, AttnArgs &a, int n_heads, hipStream_t st) {
   a.per_group.set((uint32_t)(n_heads / a.kv_heads));
   a.per_kv.set(a.slots * a.per_group.d);
   void *kargs[] = {&a};
-  if (hipLaunchKernel(fn, dim3(a.slots * (unsigned)n_heads), dim3(ATTN_THREADS), kargs, 0, st) !=
-      hipSuccess) {
+  if (hipLaunchKernel(fn, dim3(a.slots * (unsigned)n_heads), dim3(ATTN_THREADS), kargs, 0, st) != hipSuccess) {
     (void)hipGetLastError();
     return MAXSIM_ERR_LAUNCH;
   }
@@ -97,6 +102,14 @@ int run(const void *fn, AttnArgs &a, int n_heads, hipStream_t st) {
 const void *pick(int dtype, int dp, int mode, const void *(*bf)(int, int),
                  const void *(*fp)(int, int), const void *(*f32)(int, int)) {
   return dtype == MAXSIM_BF16 ? bf(dp, mode) : dtype == MAXSIM_FP16 ? fp(dp, mode) : f32(dp, mode);
+}
+
+// Blocks of 32 queries of a forward wave.
+int fwd_blocks(const AttnArgs &a, int dtype, int dp, const DeviceInfo &di) {
+  static const int knob = env_knob("MAXSIM_ATTN_BLOCKS", 0);
+  if (dtype == MAXSIM_FP32 || dp > 128) return 1;
+  if (knob) return knob;
+  return a.rows > a.n_docs * SHORT_DOC && a.rows * a.heads >= (int64_t)4 * 256 * di.cus ? 2 : 1;
 }
 
 size_t delta_floats(int64_t n_tokens, int n_heads) {
@@ -119,8 +132,13 @@ int maxsim_attention(const maxsim_attention_desc *desc, void *o, float *lse, voi
   if (rc != MAXSIM_OK) return rc;
   a.o = (char *)o;
   a.lse = lse;
-  return run(pick(desc->dtype, attn_width(a.d), mode_of(a), attn_fwd_bf16, attn_fwd_fp16, attn_fwd_fp32),
-             a, a.heads, (hipStream_t)stream);
+  const int dp = attn_width(a.d), mode = mode_of(a);
+  const int blocks = fwd_blocks(a, desc->dtype, dp, di);
+  if (blocks == 2) set_tiles(a, 2 * ATTN_ROWS);
+  const void *fn = desc->dtype == MAXSIM_BF16   ? attn_fwd_bf16(dp, mode, blocks)
+                   : desc->dtype == MAXSIM_FP16 ? attn_fwd_fp16(dp, mode, blocks)
+                                                : attn_fwd_fp32(dp, mode, blocks);
+  return run(fn, a, a.heads, (hipStream_t)stream);
 }
 
 size_t maxsim_attention_backward_workspace_size(int64_t n_tokens, int n_heads) {

@@ -9,21 +9,13 @@
 namespace maxsim {
 
 template <int DT, int DP, int MODE>
-__global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a) {
+__device__ __forceinline__ void attn_dq_tile(const AttnArgs &a, const AttnTile &t, char *lds) {
   using L = RowLayout<DT, DP>;
   constexpr int BN = 32, OT = DP / 32, TILE = BN * L::bytes;
-  __shared__ __align__(256) char lds[4 * TILE];  // two buffers: one barrier a tile
-  AttnTile t;
-  if (!locate(a, ATTN_ROWS, t)) return;
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave0 = t.first + (int)(threadIdx.x >> 6) * 32;
   const int i = wave0 + (lane & 31);
   const int row_bytes = a.d * L::eb;
-  char *out = a.dq + ((t.row0 + i) * a.heads + t.head) * row_bytes;
-  if (t.first >= t.len) {
-    if (i < t.rows) zero_row<DT>(out, a.d);
-    return;
-  }
   const int iq = i < t.len ? i : t.len - 1;
   Held<DT, DP> q, g;
   q.load(a.q + t.q + t.head * a.q_head, a.q_tok, iq, row_bytes);
@@ -146,31 +138,28 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a)
                      (int64_t)a.heads * row_bytes, t.rows - wave0, row_bytes);
 }
 
+template <int DT, int DP, int MODE>
+__global__ void __launch_bounds__(ATTN_THREADS) attn_dq_kernel(const AttnArgs a) {
+  __shared__ __align__(256) char lds[4 * 32 * RowLayout<DT, DP>::bytes];  // two buffers: one barrier a tile
+  AttnTile t;
+  if (!locate(a, ATTN_ROWS, t)) return;
+  if (t.first < t.len) attn_dq_tile<DT, DP, MODE>(a, t, lds);
+  else zero_tile<DT>(a.dq, a.heads, t, ATTN_ROWS, a.d);
+}
+
 // WHAT: 1 for dK, 2 for dV, 3 for both. Heads wider than 128 take a launch for each: a wave has no
 // registers for both sums, and computing the scores again costs less than spilling.
 template <int DT, int DP, int MODE, int WHAT>
-__global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a) {
+__device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile &t, char *lds, float (*stat)[64]) {
   using L = RowLayout<DT, DP>;
   constexpr int BM = 32, OT = DP / 32, TILE = BM * L::bytes;
   constexpr bool DK = WHAT & 1, DV = WHAT & 2;
   // fp16 P is rounded 2^8 times too large: rows over thousands of keys stay out of the subnormals
   constexpr float SHIFT = DT == DT_FP16 ? 8.0f : 0.0f;
-  __shared__ __align__(256) char lds[4 * TILE];  // two buffers: one barrier a tile
-  __shared__ __align__(16) float stat[2][2 * BM];
-  AttnTile t;
-  if (!locate(a, ATTN_ROWS, t)) return;
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave0 = t.first + (int)(threadIdx.x >> 6) * 32;
   const int j = wave0 + (lane & 31);
   const int row_bytes = a.d * L::eb;
-  const int64_t out = ((t.row0 + j) * a.kv_heads + t.head) * row_bytes;
-  if (t.first >= t.len) {
-    if (j < t.rows) {
-      if (DK) zero_row<DT>(a.dk + out, a.d);
-      if (DV) zero_row<DT>(a.dv + out, a.d);
-    }
-    return;
-  }
   const int jk = j < t.len ? j : t.len - 1;
   Held<DT, DP> k, v;
   k.load(a.k + t.k + t.head * a.k_head, a.k_tok, jk, row_bytes);
@@ -383,6 +372,20 @@ __global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a
   if constexpr (DV)
     store_rows<DT, DP>(mine, dv, real ? (DT == DT_FP16 ? 1.0f / 256.0f : 1.0f) : 0.0f, a.dv + first,
                      stride, t.rows - wave0, row_bytes);
+}
+
+template <int DT, int DP, int MODE, int WHAT>
+__global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a) {
+  __shared__ __align__(256) char lds[4 * 32 * RowLayout<DT, DP>::bytes];  // two buffers: one barrier a tile
+  __shared__ __align__(16) float stat[2][64];
+  AttnTile t;
+  if (!locate(a, ATTN_ROWS, t)) return;
+  if (t.first < t.len) {
+    attn_dkv_tile<DT, DP, MODE, WHAT>(a, t, lds, stat);
+    return;
+  }
+  if (WHAT & 1) zero_tile<DT>(a.dk, a.kv_heads, t, ATTN_ROWS, a.d);
+  if (WHAT & 2) zero_tile<DT>(a.dv, a.kv_heads, t, ATTN_ROWS, a.d);
 }
 
 }  // namespace maxsim

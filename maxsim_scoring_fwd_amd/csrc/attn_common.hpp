@@ -42,7 +42,7 @@ struct AttnArgs {
   int64_t rows;            // rows of o: all tokens
   uint32_t slots;          // tiles along the tokens
   FastDiv tiles_per_doc;   // fixed layout
-  FastDiv per_kv, per_group;  // workgroups of a key/value head, heads of the grid that share one
+  FastDiv per_kv, per_group;  // workgroups of a key/value head; of one tile of it
   // backward
   const char *dO;          // [rows][heads][d]
   const float *delta;      // [heads][rows]: <dO, o>
@@ -447,11 +447,16 @@ __device__ __forceinline__ void store_rows(char *lds, const f32x16_t (&acc)[OT],
   wave_lds_sync();
 }
 
+// Zeros in a tile's rows of out [rows][heads][d].
 template <int DT>
-__device__ __forceinline__ void zero_row(char *row, int d) {
-  const int h = (threadIdx.x & 63) >> 5;
+__device__ __forceinline__ void zero_tile(char *out, int heads, const AttnTile &t, int tile_rows, int d) {
+  const int chunks = d * Elem<DT>::bytes / 16, left = t.rows - t.first;
+  const int rows = left < tile_rows ? left : tile_rows;
   const u32x4_t z = {0, 0, 0, 0};
-  for (int c = h * 16; c < d * Elem<DT>::bytes; c += 32) *(u32x4_t *)(row + c) = z;
+  for (int e = threadIdx.x; e < rows * chunks; e += ATTN_THREADS) {
+    const int r = e / chunks, c = e - r * chunks;
+    *(u32x4_t *)(out + ((t.row0 + t.first + r) * heads + t.head) * (chunks * 16) + c * 16) = z;
+  }
 }
 
 __device__ __forceinline__ float half_max(float v) {

@@ -58,26 +58,41 @@ struct TileSpan {
   int64_t doc;    // document, or -1
 };
 
-// One wave's search, 63 probes a step: one step for up to 61 documents, two for up to 3967. Lane
-// 63 looks one probe further, so that the last step also knows where the span ends. Offsets are
-// clamped to the token range, so that no tile reaches past it whatever they hold.
+// One wave's search, 63 probes a step: one step for up to 61 documents. Lane 63 looks one probe
+// further, so that the last step also knows where the span ends. With more documents the first
+// step looks at the 63 spans around the one that documents of equal length would put there, which
+// is right for most tiles, and the next ones search what that has left. Offsets are clamped to the
+// token range, so that no tile reaches past it whatever they hold.
 __device__ __forceinline__ TileSpan find_tile(const int64_t *offsets, int64_t n_docs,
                                               int64_t n_tokens, int64_t slot, int rows) {
   const int lane = threadIdx.x & 63;
   int64_t lo = 0, hi = n_docs + 2, begin = 0;
+  const float spans = (float)(n_docs + 2), slots = (float)(n_tokens / rows + n_docs + 2);
+  int64_t from = hi <= 63 ? 0 : (int64_t)((float)slot * (spans / slots)) - 31;
+  from = from < 0 ? 0 : (from > hi - 63 ? (hi > 63 ? hi - 63 : 0) : from);
+  int64_t step = 1;
   int last = 0;
-  do {
-    const int64_t step = (uint64_t)(hi - lo + 62) / 63;
-    int64_t p = lo + lane * step;
+  for (;;) {
+    int64_t p = from + lane * step;
     p = p < hi ? p : hi;
     int64_t o = 0;
     if (p > 0) o = p > n_docs + 1 ? n_tokens : offsets[p - 1];
     begin = o < 0 ? 0 : (o > n_tokens ? n_tokens : o);
-    const bool in = lane < 63 && p < hi && (lane == 0 || begin / rows + p <= slot);
-    last = 63 - __builtin_clzll(__ballot(in) | 1);
-    lo += last * step;
-    hi = lo + step < hi ? lo + step : hi;
-  } while (hi - lo > 1);
+    const bool in = lane < 63 && p < hi && (p == lo || begin / rows + p <= slot);
+    const uint64_t found = __ballot(in);
+    if (found == 0) {  // before the window
+      hi = from;
+    } else {
+      last = 63 - __builtin_clzll(found);
+      const int64_t past = from + (last + 1) * step;
+      lo = from + last * step;
+      // the last probe of the window may have spans of its own behind it
+      if (last < 62 || step > 1) hi = past < hi ? past : hi;
+      if (hi - lo <= 1 || (step == 1 && last < 62)) break;
+    }
+    from = lo;
+    step = (uint64_t)(hi - lo + 62) / 63;
+  }
   TileSpan t;
   t.begin = lane_value(begin, last);
   const int64_t end = lane_value(begin, last + 1);

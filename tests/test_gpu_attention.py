@@ -158,6 +158,63 @@ def test_tokens_of_no_document():
     assert not o.any() and t.isneginf(lse).all()
 
 
+@pytest.mark.parametrize("kind", ["ragged", "clustered", "empty tail", "growing", "single tokens"])
+def test_many_documents(kind):
+    """Thousands of documents of uneven lengths: every tile finds its own. With q = 0 a token's
+    result is its document's mean of v, and lse the logarithm of its length."""
+    t = T()
+    rng = np.random.default_rng(3)
+    n = {"ragged": rng.integers(0, 40, 5000), "clustered": np.where(rng.random(4000) < 0.9, 0, 300),
+         "empty tail": np.r_[np.full(3, 3000), np.zeros(3000, int)], "growing": np.arange(0, 600),
+         "single tokens": np.ones(3000, int)}[kind]
+    off = np.r_[0, np.cumsum(n)]
+    rows = int(off[-1])
+    v = t.randn(rows, 1, 64, generator=t.Generator().manual_seed(5))
+    say("case: many documents", kind, rows)
+    o, lse = ms().maxsim_attention(t.zeros(rows, 2, 64, device="cuda"), t.zeros(rows, 1, 64, device="cuda"),
+                                   v.cuda(), t.from_numpy(off).cuda())
+    x = v[:, 0].double().numpy()
+    sums = np.r_[np.zeros((1, 64)), np.cumsum(x, 0)]
+    doc = np.repeat(np.arange(len(n)), n)
+    want = ((sums[off[1:]] - sums[off[:-1]]) / np.maximum(n, 1)[:, None])[doc]
+    # n sums of n terms in 32 bits, and the weights' own division
+    tol = (n[doc][:, None] + 4) * ref.U32 * np.abs(x).max()
+    got = ref.as64(o)
+    assert np.all(np.abs(got - want[:, None]) <= tol[:, None])
+    assert np.all(np.abs(ref.as64(lse) - np.log(n[doc])) <= 1e-5)
+
+
+@pytest.mark.parametrize("dtype, d, heads, kv, causal, cap, bias", [
+    ("bf16", 128, 8, 2, True, 0.0, True), ("fp16", 128, 4, 4, False, 30.0, False),
+    ("bf16", 64, 16, 16, False, 0.0, False), ("fp16", 64, 16, 8, True, 20.0, True),
+    ("bf16", 96, 8, 1, False, 0.0, True), ("fp16", 72, 12, 3, True, 0.0, False),
+    ("bf16", 32, 32, 4, True, 0.0, True)])
+def test_long_batches(dtype, d, heads, kv, causal, cap, bias):
+    """Enough long documents for the widest tiles (64 queries a wave): the results of one of them
+    are what it gets alone, in the narrow tiles, up to the rounding of the weights, whose order of
+    sums differs; and a head of the shortest against 64 bits."""
+    t = T()
+    lens = [1100, 700, 1025, 513, 1400, 900, 640] * 4
+    q, k, v, do, lay, docs = inputs(77, lens, heads, kv, d, dt(dtype), 0)
+    slopes = t.tensor([2.0 ** (-8.0 * (h + 1) / heads) for h in range(heads)]).cuda() if bias else None
+    kw = dict(causal=causal, softcap=cap, slopes=slopes)
+    say("case: long batch", dtype, d, heads)
+    o, lse = ms().maxsim_attention(q, k, v, **lay, **kw)
+    for b in (0, 3, 27):
+        t0, n = docs[b]
+        rows = slice(t0, t0 + n)
+        alone = ms().maxsim_attention(q[rows], k[rows], v[rows], t.tensor([0, n]).cuda(), **kw)
+        s64 = None if slopes is None else ref.as64(slopes)
+        for h in (0, heads - 1):
+            g = h // (heads // kv)
+            want = ref.attention(ref.as64(q[rows, h:h + 1]), ref.as64(k[rows, g:g + 1]),
+                                 ref.as64(v[rows, g:g + 1]), [(0, n)], causal, None, cap,
+                                 None if s64 is None else s64[h:h + 1], dtype=dt(dtype))
+            for got, gl in ((o[rows, h:h + 1], lse[h, rows]), (alone[0][:, h:h + 1], alone[1][h])):
+                check("o", got, want["o"], want["tol_o"])
+                check("lse", gl[None], want["lse"], want["tol_lse"])
+
+
 def test_any_strides():
     """Heads before tokens, gaps between rows, an offset start: the same bits as contiguous."""
     t = T()
