@@ -11,7 +11,6 @@ using namespace maxsim;
 
 namespace {
 
-constexpr int64_t SHORT_DOC = 512;  // mean tokens of a document
 constexpr int64_t MAX_TOKEN_BYTES = (int64_t)1 << 24;  // 64 rows of it stay within 31 bits
 
 // A tensor's strides (in elements, all multiples of 16 bytes) as byte strides.
@@ -104,16 +103,8 @@ const void *pick(int dtype, int dp, int mode, const void *(*bf)(int, int),
   return dtype == MAXSIM_BF16 ? bf(dp, mode) : dtype == MAXSIM_FP16 ? fp(dp, mode) : f32(dp, mode);
 }
 
-// Blocks of 32 queries of a forward wave.
-int fwd_blocks(const AttnArgs &a, int dtype, int dp, const DeviceInfo &di) {
-  static const int knob = env_knob("MAXSIM_ATTN_BLOCKS", 0);
-  if (dtype == MAXSIM_FP32 || dp > 128) return 1;
-  if (knob) return knob;
-  return a.rows > a.n_docs * SHORT_DOC && a.rows * a.heads >= (int64_t)4 * 256 * di.cus ? 2 : 1;
-}
-
-size_t delta_floats(int64_t n_tokens, int n_heads) {
-  return ((size_t)n_tokens * (size_t)n_heads + 3) / 4 * 4;
+size_t stat_floats(int64_t n_tokens, int n_heads) {
+  return ((size_t)n_tokens * (size_t)n_heads + 1) / 2 * 4;
 }
 
 }  // namespace
@@ -132,18 +123,13 @@ int maxsim_attention(const maxsim_attention_desc *desc, void *o, float *lse, voi
   if (rc != MAXSIM_OK) return rc;
   a.o = (char *)o;
   a.lse = lse;
-  const int dp = attn_width(a.d), mode = mode_of(a);
-  const int blocks = fwd_blocks(a, desc->dtype, dp, di);
-  if (blocks == 2) set_tiles(a, 2 * ATTN_ROWS);
-  const void *fn = desc->dtype == MAXSIM_BF16   ? attn_fwd_bf16(dp, mode, blocks)
-                   : desc->dtype == MAXSIM_FP16 ? attn_fwd_fp16(dp, mode, blocks)
-                                                : attn_fwd_fp32(dp, mode, blocks);
-  return run(fn, a, a.heads, (hipStream_t)stream);
+  return run(pick(desc->dtype, attn_width(a.d), mode_of(a), attn_fwd_bf16, attn_fwd_fp16, attn_fwd_fp32),
+             a, a.heads, (hipStream_t)stream);
 }
 
 size_t maxsim_attention_backward_workspace_size(int64_t n_tokens, int n_heads) {
   if (n_tokens < 0 || n_heads < 1) return 0;
-  return (delta_floats(n_tokens, n_heads) + 2 * DELTA_GRID + 4) * sizeof(float);
+  return (stat_floats(n_tokens, n_heads) + 2 * DELTA_GRID + 4) * sizeof(float);
 }
 
 int maxsim_attention_backward(const maxsim_attention_desc *desc, const void *o, const float *lse,
@@ -171,10 +157,10 @@ int maxsim_attention_backward(const maxsim_attention_desc *desc, const void *o, 
   a.dq = (char *)dq;
   a.dk = (char *)dk;
   a.dv = (char *)dv;
-  float *delta = (float *)workspace;
-  float2 *maxima = (float2 *)(delta + delta_floats(a.rows, a.heads));
+  float2 *stats = (float2 *)workspace;
+  float2 *maxima = (float2 *)((float *)workspace + stat_floats(a.rows, a.heads));
   float *gscale = (float *)(maxima + DELTA_GRID);
-  a.delta = delta;
+  a.stats = stats;
   a.grad_scale = gscale;
   // 32 rows of a head a workgroup; fp16 needs one pair of maxima from each, so there are few
   int64_t grid = (a.rows * a.heads + 31) / 32;
@@ -183,7 +169,10 @@ int maxsim_attention_backward(const maxsim_attention_desc *desc, const void *o, 
   const void *fn = desc->dtype == MAXSIM_BF16   ? (const void *)attn_delta_kernel<DT_BF16>
                    : desc->dtype == MAXSIM_FP16 ? (const void *)attn_delta_kernel<DT_FP16>
                                                 : (const void *)attn_delta_kernel<DT_FP32>;
-  void *kargs[] = {&a, &delta, &maxima};
+  const int dp = attn_width(a.d), mode = mode_of(a);
+  float unit = mode == ATTN_CAP ? 1.0f : a.scale * LOG2E;
+  float shift = desc->dtype == MAXSIM_FP16 ? ATTN_WEIGHT_SHIFT : 0.0f;
+  void *kargs[] = {&a, &stats, &maxima, &unit, &shift};
   if (hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), kargs, 0, st) != hipSuccess) {
     (void)hipGetLastError();
     return MAXSIM_ERR_LAUNCH;
@@ -192,7 +181,6 @@ int maxsim_attention_backward(const maxsim_attention_desc *desc, const void *o, 
     hipLaunchKernelGGL(attn_grad_scale_kernel, dim3(1), dim3(64), 0, st, maxima, (int)grid, gscale);
     if (hipGetLastError() != hipSuccess) return MAXSIM_ERR_LAUNCH;
   }
-  const int dp = attn_width(a.d), mode = mode_of(a);
   if (dq) {
     rc = run(pick(desc->dtype, dp, mode, attn_dq_bf16, attn_dq_fp16, attn_dq_fp32), a, a.heads, st);
     if (rc != MAXSIM_OK) return rc;

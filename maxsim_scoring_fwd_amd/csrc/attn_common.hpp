@@ -45,13 +45,16 @@ struct AttnArgs {
   FastDiv per_kv, per_group;  // workgroups of a key/value head; of one tile of it
   // backward
   const char *dO;          // [rows][heads][d]
-  const float *delta;      // [heads][rows]: <dO, o>
+  const float2 *stats;     // [heads][rows]: where S and dP start (attn_delta.hpp)
   const float *grad_scale; // fp16: power of two that dS is scaled by before its rounding
   char *dq, *dk, *dv;      // [rows][heads or kv_heads][d]
 };
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
+// fp16 weights of the backward are rounded 2^8 times too large: over thousands of keys they would
+// be subnormal.
+constexpr float ATTN_WEIGHT_SHIFT = 8.0f;
 constexpr int ATTN_THREADS = 256;
 constexpr int ATTN_ROWS = 128;  // tokens of a workgroup's tile: 32 to a wave
 
@@ -89,6 +92,7 @@ template <int DT> __device__ __forceinline__ f32x16_t mma_rows(u32x4_t a, u32x4_
 // A 32x32 accumulator as the B operand of the next product: rounded to the storage type (to
 // nearest even) for the 16-bit types, as it is for fp32.
 template <int DT> struct Packed {
+  static constexpr int n = 2;  // operands of mma_cols that 32 rows make
   u32x4_t f[2];
   __device__ __forceinline__ void set_half(const f32x16_t &s, int t) {
     using T = typename AttnElem<DT>::type;
@@ -104,6 +108,7 @@ template <int DT> struct Packed {
   }
 };
 template <> struct Packed<DT_FP32> {
+  static constexpr int n = 4;
   f32x16_t f;
   __device__ __forceinline__ void set(const f32x16_t &s) { f = s; }
 };
@@ -131,8 +136,7 @@ template <int DT, int DP> struct RowLayout {
   }
 };
 
-// acc += X^T[columns c0 .. c0 + 31, rows r0 .. r0 + 31] * P, X row-major in LDS; r0 a multiple of
-// 32. lane: this lane's tr_lane_offset in the tile.
+// This lane's place in a tile for read_cols.
 template <int DT, int DP> __device__ __forceinline__ int tr_lane_offset() {
   using L = RowLayout<DT, DP>;
   const int l = threadIdx.x & 63, h = l >> 5;
@@ -160,83 +164,100 @@ template <int DT, int DP>
 __device__ __forceinline__ u32x4_t read_rows(const char *tile, int lane, int s) {
   return load16(tile + RowLayout<DT, DP>::along(lane, 32 * s));
 }
-// Operand t of columns c0 .. c0 + 31, rows r0 + 16 t .., transposed (see mma_cols).
+// Operand t of columns c0 .. c0 + 31 of a tile, transposed: for 16-bit types rows 16 t .. 16 t + 15,
+// for fp32 rows 8 t .. 8 t + 7 (this lane's half of them). lane is tr_lane_offset.
 template <int DT, int DP>
-__device__ __forceinline__ u32x4_t read_cols(const char *tile, int lane, int r0, int c0, int t) {
-  using L = RowLayout<DT, DP>;
-  const char *at = tile + (r0 + 16 * t) * L::bytes;
-  const s16x4_t lo = read_tr(at + L::along(lane, c0 * 2));
-  const s16x4_t hi = read_tr(at + 8 * L::bytes + L::along(lane ^ 32, c0 * 2));
-  return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-
-template <int DT, int DP>
-__device__ __forceinline__ f32x16_t mma_cols(const char *tile, int lane, int r0, int c0,
-                                             const Packed<DT> &p, f32x16_t acc) {
+__device__ __forceinline__ u32x4_t read_cols(const char *tile, int lane, int c0, int t) {
   using L = RowLayout<DT, DP>;
   if constexpr (DT == DT_FP32) {
+    u32x4_t x;
 #pragma unroll
-    for (int r = 0; r < 16; r++) {
-      // rows 8 (r / 4) + r % 4 of this half's, whose f is that row's on top of the lane's
-      const int row = (r & 3) + 8 * (r >> 2);
-      const float a = *(const float *)(tile + (r0 + row) * L::bytes + L::along(lane ^ L::f(row), c0 * 4));
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p.f[r], acc, 0, 0, 0);
-    }
+    for (int e = 0; e < 4; e++)  // row 8 t + e of this half's, whose f is on top of the lane's
+      x[e] = *(const uint32_t *)(tile + (8 * t + e) * L::bytes + L::along(lane ^ L::f(8 * t + e), c0 * 4));
+    return x;
   } else {
-#pragma unroll
-    for (int t = 0; t < 2; t++)
-      acc = mma_rows<DT>(read_cols<DT, DP>(tile, lane, r0, c0, t), p.f[t], acc);
+    const char *at = tile + 16 * t * L::bytes;
+    const s16x4_t lo = read_tr(at + L::along(lane, c0 * 2));
+    const s16x4_t hi = read_tr(at + 8 * L::bytes + L::along(lane ^ 32, c0 * 2));
+    return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   }
-  return acc;
+}
+// acc += X^T[columns, operand t's rows] * P
+template <int DT>
+__device__ __forceinline__ f32x16_t mma_cols(u32x4_t x, const Packed<DT> &p, int t, f32x16_t acc) {
+  if constexpr (DT == DT_FP32) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const uint32_t v = x[e];
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(v), p.f[4 * t + e], acc, 0, 0, 0);
+    }
+    return acc;
+  } else {
+    return mma_rows<DT>(x, p.f[t], acc);
+  }
 }
 
-// Copies ROWS rows of a head from global memory straight into LDS, in `n` pieces: a wave's piece
-// is 64 chunks that lie side by side in LDS, and each lane fetches the one that belongs there.
-// Rows past the last valid one repeat it, and columns past the head's size its last 16 bytes:
-// nothing outside is read, what follows stays finite, and those columns meet zeros (Held) or are
-// not stored. Arrival is waited for by tile_barrier.
-template <int DT, int DP, int ROWS> struct Carry {
+// Copies tiles of 32 rows of a head, one after the other, from global memory straight into LDS, in
+// `n` pieces a tile: a wave's piece is 64 chunks that lie side by side in LDS, and each lane fetches
+// the one that belongs there. Rows past the last one repeat it, and columns past the head's size
+// its last 16 bytes: nothing outside is read, what follows stays finite, and those columns meet
+// zeros (Held) or are not stored. Past the last tile one row is fetched again and again, which
+// keeps branches out of the loops. Arrival is waited for by tile_barrier.
+template <int DT, int DP> struct Carry {
   using L = RowLayout<DT, DP>;
-  static constexpr int total = ROWS * L::chunks;
+  static constexpr int total = 32 * L::chunks;
   static constexpr int n = (total + ATTN_THREADS - 1) / ATTN_THREADS;
   uint32_t at[n];  // byte offset of this lane's chunks in a whole tile
   uint32_t col[n];
-  const char *base;  // first row of the tile
-  uint32_t last;     // offset of its last row
+  uint64_t base;   // first row of the tile (uniform, as what follows)
+  int left;        // rows from there on
+  int stride;
+  uint32_t last;   // offset of the tile's last row
 
-  __device__ __forceinline__ void init(int stride, int row_bytes) {
+  __device__ __forceinline__ void init(int row_stride, int row_bytes) {
+    stride = row_stride;
 #pragma unroll
     for (int i = 0; i < n; i++) {
       const int p = threadIdx.x + i * ATTN_THREADS, row = p / L::chunks;
       const int c = (p % L::chunks * 16) ^ L::f(row);
       col[i] = c < row_bytes ? c : row_bytes - 16;
-      at[i] = (uint32_t)(row * stride) + col[i];
+      at[i] = (uint32_t)(row * row_stride) + col[i];
     }
   }
-  // The tile at `first` (uniform) with `valid` rows from it on; at least one row is read.
-  __device__ __forceinline__ void aim(const char *first, int stride, int valid) {
-    base = (const char *)uniform((int64_t)(uintptr_t)first);
-    valid = valid < ROWS ? valid : ROWS;
-    last = (uint32_t)(valid > 1 ? valid - 1 : 0) * (uint32_t)stride;
+  // The first tile: `rows` rows (at least one) from `first` on.
+  __device__ __forceinline__ void start(const char *first, int rows) {
+    base = (uint64_t)uniform((int64_t)(uintptr_t)first);
+    left = uniform(rows);
+    limit();
   }
-  // Piece i of the tile, to the tile at lds. wave: this wave's number (uniform).
-  __device__ __forceinline__ void go(char *lds, int wave, int i) const {
-    typedef __attribute__((address_space(3))) char lds_char;
+  __device__ __forceinline__ void limit() { last = (uint32_t)((left < 32 ? left : 32) - 1) * (uint32_t)stride; }
+  __device__ __forceinline__ void next() {
+    const bool more = left > 32;
+    base += more ? (uint64_t)(uint32_t)(32 * stride) : 0;
+    left = more ? left - 32 : 1;
+    limit();
+  }
+  // Piece i of the tile, to LDS address `to`. wave: this wave's number (uniform).
+  __device__ __forceinline__ void go(int to, int wave, int i) const {
     const int p = wave * 64 + i * ATTN_THREADS;
     if (total % ATTN_THREADS != 0 && p >= total) return;
-    const uint32_t limit = last + col[i], from = at[i] < limit ? at[i] : limit;
-    const int to = uniform((int)(uintptr_t)(lds_char *)(lds + p * 16));
+    const uint32_t most = last + col[i], from = at[i] < most ? at[i] : most;
     // The instruction itself: beside the builtin the compiler waits for every LDS read in flight
     // wherever it needs one. It has no result in registers, and tile_barrier waits for it.
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
-                 : "s"(to), "v"(from), "s"(base));
+                 : "s"(uniform(to + p * 16)), "v"(from), "s"(uniform((int64_t)base)));
   }
-  __device__ __forceinline__ void all(char *lds, int wave) const {
+  __device__ __forceinline__ void all(int to, int wave) const {
 #pragma unroll
-    for (int i = 0; i < n; i++) go(lds, wave, i);
+    for (int i = 0; i < n; i++) go(to, wave, i);
   }
 };
+
+__device__ __forceinline__ int lds_address(const char *p) {
+  typedef __attribute__((address_space(3))) char lds_char;
+  return uniform((int)(uintptr_t)(lds_char *)p);
+}
 
 // Every wave's carried pieces and LDS writes have arrived, and its LDS reads are done.
 __device__ __forceinline__ void tile_barrier() {

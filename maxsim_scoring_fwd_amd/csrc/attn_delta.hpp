@@ -8,10 +8,12 @@ namespace maxsim {
 
 constexpr int DELTA_GRID = 1024;
 
-// delta = <dO, o> in fp32, 8 lanes to a row of a head. With maxima set (fp16) also the largest
-// squared norm of the rows of dO and of v, one pair per workgroup.
+// For each row of a head where the sums of dK / dV's products start: S from -lse in units of the
+// product (of the score behind a tanh; + shift, see ATTN_WEIGHT_SHIFT), dP from -delta, delta =
+// <dO, o> in fp32. 8 lanes to a row. With maxima set (fp16) also the largest squared norm of the
+// rows of dO and of v, one pair per workgroup.
 template <int DT>
-__global__ void __launch_bounds__(256) attn_delta_kernel(const AttnArgs a, float *delta, float2 *maxima) {
+__global__ void __launch_bounds__(256) attn_delta_kernel(const AttnArgs a, float2 *stats, float2 *maxima, float unit, float shift) {
   using T = typename AttnElem<DT>::type;
   constexpr int V = 16 / Elem<DT>::bytes;
   typedef T vec __attribute__((ext_vector_type(V)));
@@ -42,7 +44,10 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnArgs a, float
     }
     s = sum8(s);
     const int64_t row = at / a.heads, head = at - row * a.heads;
-    if (sub == 0) delta[head * a.rows + row] = s;
+    if (sub == 0) {
+      const int64_t to = head * a.rows + row;
+      stats[to] = make_float2((shift - a.lse[to] * LOG2E) / unit, -s);
+    }
     if (DT == DT_FP16 && exists((uint32_t)row)) top_do = __builtin_fmaxf(top_do, sum8(w));
   }
   if constexpr (DT == DT_FP16) {

@@ -6,10 +6,9 @@
 namespace maxsim {
 
 // The kernel for heads of up to dp columns (a width of attn_width) and a score form.
-// blocks: of 32 queries that a wave takes, 1 or 2 (16-bit heads up to 128).
-const void *attn_fwd_bf16(int dp, int mode, int blocks);
-const void *attn_fwd_fp16(int dp, int mode, int blocks);
-const void *attn_fwd_fp32(int dp, int mode, int blocks);
+const void *attn_fwd_bf16(int dp, int mode);
+const void *attn_fwd_fp16(int dp, int mode);
+const void *attn_fwd_fp32(int dp, int mode);
 const void *attn_dq_bf16(int dp, int mode);
 const void *attn_dq_fp16(int dp, int mode);
 const void *attn_dq_fp32(int dp, int mode);

@@ -4,19 +4,19 @@
 
 namespace maxsim {
 namespace {
-template <int DP, int CB> const void *pick(int mode) {
-  return mode == ATTN_PLAIN  ? (const void *)attn_fwd_kernel<DT_FP32, DP, ATTN_PLAIN, CB>
-         : mode == ATTN_BIAS ? (const void *)attn_fwd_kernel<DT_FP32, DP, ATTN_BIAS, CB>
-                             : (const void *)attn_fwd_kernel<DT_FP32, DP, ATTN_CAP, CB>;
+template <int DP> const void *pick(int mode) {
+  return mode == ATTN_PLAIN  ? (const void *)attn_fwd_kernel<DT_FP32, DP, ATTN_PLAIN>
+         : mode == ATTN_BIAS ? (const void *)attn_fwd_kernel<DT_FP32, DP, ATTN_BIAS>
+                             : (const void *)attn_fwd_kernel<DT_FP32, DP, ATTN_CAP>;
 }
 }  // namespace
 
-const void *attn_fwd_fp32(int dp, int mode, int blocks) {
+const void *attn_fwd_fp32(int dp, int mode) {
   switch (dp) {
-  case 32: return pick<32, 1>(mode);
-  case 64: return pick<64, 1>(mode);
-  case 96: return pick<96, 1>(mode);
-  case 128: return pick<128, 1>(mode);
+  case 32: return pick<32>(mode);
+  case 64: return pick<64>(mode);
+  case 96: return pick<96>(mode);
+  case 128: return pick<128>(mode);
   }
   return nullptr;
 }
