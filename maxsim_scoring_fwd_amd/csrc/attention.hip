@@ -83,7 +83,7 @@ int fill(const maxsim_attention_desc *s, AttnArgs &a) {
 }
 
 int mode_of(const AttnArgs &a) {
-  return a.softcap > 0 ? ATTN_CAP : a.slopes ? ATTN_BIAS : ATTN_PLAIN;
+  return (a.softcap > 0 ? ATTN_CAP : ATTN_PLAIN) + (a.slopes ? ATTN_BIAS : 0);
 }
 
 // One workgroup for every tile of tokens and each of n_heads heads.
@@ -170,7 +170,7 @@ int maxsim_attention_backward(const maxsim_attention_desc *desc, const void *o, 
                    : desc->dtype == MAXSIM_FP16 ? (const void *)attn_delta_kernel<DT_FP16>
                                                 : (const void *)attn_delta_kernel<DT_FP32>;
   const int dp = attn_width(a.d), mode = mode_of(a);
-  float unit = mode == ATTN_CAP ? 1.0f : a.scale * LOG2E;
+  float unit = has_cap(mode) ? 1.0f : a.scale * LOG2E;
   float shift = desc->dtype == MAXSIM_FP16 ? ATTN_WEIGHT_SHIFT : 0.0f;
   void *kargs[] = {&a, &stats, &maxima, &unit, &shift};
   if (hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), kargs, 0, st) != hipSuccess) {

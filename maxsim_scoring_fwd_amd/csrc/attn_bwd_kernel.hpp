@@ -79,7 +79,7 @@ __device__ __forceinline__ void attn_dq_tile(const AttnArgs &a, const AttnTile &
         float y = score<DT, MODE>(form, s[r], dist0 - (float)acc_row(r), &keep);
         if (masked) y = acc_row(r) < left ? y : -INFINITY;
         s[r] = __builtin_amdgcn_exp2f(y - lse);
-        if (MODE == ATTN_CAP) s[r] *= keep;
+        if (has_cap(MODE)) s[r] *= keep;
         if (DT == DT_FP16) s[r] *= gs;
       }
     };
@@ -240,24 +240,24 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
       dp[r] = y[1];
       dp[r + 1] = y[3];
     }
-    s = MODE == ATTN_CAP ? zero16() : lse;
+    s = has_cap(MODE) ? zero16() : lse;
     f32x16_t slope;  // of the cap
     auto weights = [&](int first, int to) {
 #pragma unroll
       for (int r = first; r < to; r++) {
         float keep = 1.0f;
         float y = score<DT, MODE>(form, s[r], dist0 + (float)acc_row(r), &keep);
-        if (MODE == ATTN_CAP) y += lse[r];
+        if (has_cap(MODE)) y += lse[r];
         if (masked) y = acc_row(r) < hide || acc_row(r) >= there ? -INFINITY : y;
         s[r] = __builtin_amdgcn_exp2f(y);
-        if (MODE == ATTN_CAP) slope[r] = keep;
+        if (has_cap(MODE)) slope[r] = keep;
       }
     };
     auto grads = [&](int first, int to) {
 #pragma unroll
       for (int r = first; r < to; r++) {
         dp[r] = s[r] * dp[r];
-        if (MODE == ATTN_CAP) dp[r] *= slope[r];
+        if (has_cap(MODE)) dp[r] *= slope[r];
         if (DT == DT_FP16) dp[r] *= gs8;
       }
     };

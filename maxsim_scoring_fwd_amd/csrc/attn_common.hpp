@@ -21,8 +21,10 @@
 
 namespace maxsim {
 
-// Score forms: plain scale; scale and distance bias; tanh cap and bias (slope 0 without one).
-enum { ATTN_PLAIN = 0, ATTN_BIAS = 1, ATTN_CAP = 2 };
+// Score forms: plain scale; scale and distance bias; scale and tanh cap; all of them.
+enum { ATTN_PLAIN = 0, ATTN_BIAS = 1, ATTN_CAP = 2, ATTN_CAP_BIAS = 3 };
+constexpr bool has_cap(int mode) { return mode == ATTN_CAP || mode == ATTN_CAP_BIAS; }
+constexpr bool has_bias(int mode) { return mode == ATTN_BIAS || mode == ATTN_CAP_BIAS; }
 
 struct AttnArgs {
   const char *q, *k, *v;
@@ -207,46 +209,55 @@ template <int DT, int DP> struct Carry {
   using L = RowLayout<DT, DP>;
   static constexpr int total = 32 * L::chunks;
   static constexpr int n = (total + ATTN_THREADS - 1) / ATTN_THREADS;
-  uint32_t at[n];  // byte offset of this lane's chunks in a whole tile
-  uint32_t col[n];
+  uint32_t at[n];  // byte offset of this lane's chunks in the tile
   uint64_t base;   // first row of the tile (uniform, as what follows)
   int left;        // rows from there on
-  int stride;
-  uint32_t last;   // offset of the tile's last row
+  int stride, row_bytes;
 
-  __device__ __forceinline__ void init(int row_stride, int row_bytes) {
+  __device__ __forceinline__ uint32_t column(int i) const {
+    const int p = threadIdx.x + i * ATTN_THREADS;
+    const int c = (p % L::chunks * 16) ^ L::f(p / L::chunks);
+    return c < row_bytes ? c : row_bytes - 16;
+  }
+  __device__ __forceinline__ void init(int row_stride, int bytes) {
     stride = row_stride;
-#pragma unroll
-    for (int i = 0; i < n; i++) {
-      const int p = threadIdx.x + i * ATTN_THREADS, row = p / L::chunks;
-      const int c = (p % L::chunks * 16) ^ L::f(row);
-      col[i] = c < row_bytes ? c : row_bytes - 16;
-      at[i] = (uint32_t)(row * row_stride) + col[i];
-    }
+    row_bytes = bytes;
   }
   // The first tile: `rows` rows (at least one) from `first` on.
   __device__ __forceinline__ void start(const char *first, int rows) {
     base = (uint64_t)uniform((int64_t)(uintptr_t)first);
     left = uniform(rows);
-    limit();
+#pragma unroll
+    for (int i = 0; i < n; i++)
+      at[i] = (uint32_t)((threadIdx.x + i * ATTN_THREADS) / L::chunks * stride) + column(i);
+    if (left < 32) narrow();
   }
-  __device__ __forceinline__ void limit() { last = (uint32_t)((left < 32 ? left : 32) - 1) * (uint32_t)stride; }
+  __device__ __forceinline__ void narrow() {
+    if (left < 1) {
+      base -= (uint64_t)(uint32_t)(32 * stride);
+      left = 1;
+    }
+    const uint32_t last = (uint32_t)(left - 1) * (uint32_t)stride;
+#pragma unroll
+    for (int i = 0; i < n; i++) {
+      const uint32_t most = last + column(i);
+      at[i] = at[i] < most ? at[i] : most;
+    }
+  }
   __device__ __forceinline__ void next() {
-    const bool more = left > 32;
-    base += more ? (uint64_t)(uint32_t)(32 * stride) : 0;
-    left = more ? left - 32 : 1;
-    limit();
+    base += (uint64_t)(uint32_t)(32 * stride);
+    left -= 32;
+    if (left < 32) narrow();
   }
   // Piece i of the tile, to LDS address `to`. wave: this wave's number (uniform).
   __device__ __forceinline__ void go(int to, int wave, int i) const {
     const int p = wave * 64 + i * ATTN_THREADS;
     if (total % ATTN_THREADS != 0 && p >= total) return;
-    const uint32_t most = last + col[i], from = at[i] < most ? at[i] : most;
     // The instruction itself: beside the builtin the compiler waits for every LDS read in flight
     // wherever it needs one. It has no result in registers, and tile_barrier waits for it.
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
-                 : "s"(uniform(to + p * 16)), "v"(from), "s"(uniform((int64_t)base)));
+                 : "s"(uniform(to + p * 16)), "v"(at[i]), "s"(uniform((int64_t)base)));
   }
   __device__ __forceinline__ void all(int to, int wave) const {
 #pragma unroll
@@ -327,8 +338,8 @@ struct ScoreForm {
 template <int DT, int MODE>
 __device__ __forceinline__ ScoreForm score_form(const AttnArgs &a, int head) {
   ScoreForm f;
-  f.slope = MODE != ATTN_PLAIN && a.slopes ? a.slopes[head] * LOG2E : 0.0f;
-  if (MODE == ATTN_CAP) {
+  f.slope = has_bias(MODE) ? a.slopes[head] * LOG2E : 0.0f;
+  if (has_cap(MODE)) {
     f.a = a.scale / a.softcap * (DT == DT_FP32 ? 1.0f : 2.0f * LOG2E);
     f.b = a.softcap * LOG2E;
   } else {
@@ -344,21 +355,20 @@ __device__ __forceinline__ ScoreForm score_form(const AttnArgs &a, int head) {
 // see; fp32 takes tanhf.
 template <int DT, int MODE>
 __device__ __forceinline__ float score(const ScoreForm &f, float x, float dist, float *keep) {
-  if constexpr (MODE == ATTN_PLAIN) return x * f.a;
-  else if constexpr (MODE == ATTN_BIAS) return __builtin_fmaf(-f.slope, __builtin_fabsf(dist), x * f.a);
-  else {
-    float y;
-    if constexpr (DT == DT_FP32) {
-      const float t = tanhf(x * f.a);
-      y = f.b * t;
-      if (keep) *keep = __builtin_fmaf(-t, t, 1.0f);
-    } else {
-      const float r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * f.a));
-      y = __builtin_fmaf(-2.0f * f.b, r, f.b);
-      if (keep) *keep = 4.0f * r * (1.0f - r);
-    }
-    return __builtin_fmaf(-f.slope, __builtin_fabsf(dist), y);
+  float y;
+  if constexpr (!has_cap(MODE)) {
+    y = x * f.a;
+  } else if constexpr (DT == DT_FP32) {
+    const float t = tanhf(x * f.a);
+    y = f.b * t;
+    if (keep) *keep = __builtin_fmaf(-t, t, 1.0f);
+  } else {
+    const float r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * f.a));
+    y = __builtin_fmaf(-2.0f * f.b, r, f.b);
+    if (keep) *keep = 4.0f * r * (1.0f - r);
   }
+  if constexpr (has_bias(MODE)) y = __builtin_fmaf(-f.slope, __builtin_fabsf(dist), y);
+  return y;
 }
 
 // Where a workgroup works: a tile of a document's rows, and a head.

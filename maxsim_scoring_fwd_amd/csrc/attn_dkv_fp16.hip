@@ -5,9 +5,12 @@
 namespace maxsim {
 namespace {
 template <int DP, int WHAT> const void *pick(int mode) {
-  return mode == ATTN_PLAIN  ? (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_PLAIN, WHAT>
-         : mode == ATTN_BIAS ? (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_BIAS, WHAT>
-                             : (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_CAP, WHAT>;
+  switch (mode) {
+  case ATTN_PLAIN: return (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_PLAIN, WHAT>;
+  case ATTN_BIAS: return (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_BIAS, WHAT>;
+  case ATTN_CAP: return (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_CAP, WHAT>;
+  default: return (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_CAP_BIAS, WHAT>;
+  }
 }
 }  // namespace
 

@@ -5,9 +5,12 @@
 namespace maxsim {
 namespace {
 template <int DP> const void *pick(int mode) {
-  return mode == ATTN_PLAIN  ? (const void *)attn_dq_kernel<DT_BF16, DP, ATTN_PLAIN>
-         : mode == ATTN_BIAS ? (const void *)attn_dq_kernel<DT_BF16, DP, ATTN_BIAS>
-                             : (const void *)attn_dq_kernel<DT_BF16, DP, ATTN_CAP>;
+  switch (mode) {
+  case ATTN_PLAIN: return (const void *)attn_dq_kernel<DT_BF16, DP, ATTN_PLAIN>;
+  case ATTN_BIAS: return (const void *)attn_dq_kernel<DT_BF16, DP, ATTN_BIAS>;
+  case ATTN_CAP: return (const void *)attn_dq_kernel<DT_BF16, DP, ATTN_CAP>;
+  default: return (const void *)attn_dq_kernel<DT_BF16, DP, ATTN_CAP_BIAS>;
+  }
 }
 }  // namespace
 

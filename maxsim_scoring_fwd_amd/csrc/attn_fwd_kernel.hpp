@@ -97,7 +97,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   f32x16_t slope_row;  // slope * key, and the cap's constant term
 #pragma unroll
   for (int r = 0; r < 16; r++) slope_row[r] = __builtin_fmaf(form.slope, (float)acc_row(r), form.b);
-  constexpr bool LINEAR = MODE == ATTN_BIAS || (MODE == ATTN_CAP && DT != DT_FP32);
+  constexpr bool LINEAR = has_bias(MODE) && !(has_cap(MODE) && DT == DT_FP32);
   auto scores = [&](f32x16_t &x, int n, bool linear, int from, int to) {
     const float dist0 = (float)(i - n * BN - 4 * h);
     const int left = vis - n * BN - 4 * h;
@@ -105,7 +105,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
     for (int r = from; r < to; r++) {
       float y = x[r];
       if (LINEAR && linear) {
-        if (MODE == ATTN_CAP)
+        if (has_cap(MODE))
           y = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y * form.a)) * (-2.0f * form.b) + slope_row[r];
         else
           y = __builtin_fmaf(y, form.a, slope_row[r]);
