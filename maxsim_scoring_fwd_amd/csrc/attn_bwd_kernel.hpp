@@ -106,7 +106,8 @@ __device__ __forceinline__ void attn_dq_tile(const AttnArgs &a, const AttnTile &
             grads(0, 16);
             p.set(dp);
           }
-        });
+        },
+        [](int j) { return DT == DT_FP32 ? 0 : j < 2 * A ? 1 : 2; });
   };
   tile_barrier();
   int n = 0;
@@ -298,11 +299,11 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
       if (e < A) fetch(n + 2, e * P / A, (e + 1) * P / A);
     };
     if constexpr (DT == DT_FP32) {  // in two, or it is too long for the compiler to unroll
-      pipeline<A + B, 4>(read, mma, work);
-      pipeline<C + D, 4>([&](int e) { return read(A + B + e); },
-                         [&](int e, u32x4_t x) { mma(A + B + e, x); }, [&](int e) { work(A + B + e); });
+      pipeline<A + B, 4>(read, mma, work, [](int) { return 0; });
+      pipeline<C + D, 4>([&](int e) { return read(A + B + e); }, [&](int e, u32x4_t x) { mma(A + B + e, x); },
+                         [&](int e) { work(A + B + e); }, [](int) { return 0; });
     } else {
-      pipeline<A + B + C + D, 4>(read, mma, work);
+      pipeline<A + B + C + D, 4>(read, mma, work, [](int e) { return e < A + B ? 1 : 2; });
     }
     n++;
   };

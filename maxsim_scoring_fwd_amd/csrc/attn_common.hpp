@@ -299,11 +299,23 @@ template <int DT, int DP> struct Held {
 // would wait out the latency of each.
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
+// Until at most n of this wave's LDS reads are under way.
+__device__ __forceinline__ void wait_reads(int n) {
+  constexpr int NONE = 0xc07f;  // counters that are not waited for
+  switch (n) {
+  case 2: __builtin_amdgcn_s_waitcnt(NONE | 2 << 8); break;
+  case 3: __builtin_amdgcn_s_waitcnt(NONE | 3 << 8); break;
+  case 4: __builtin_amdgcn_s_waitcnt(NONE | 4 << 8); break;
+  }
+}
+
 // N matrix instructions in order, their operands read from LDS AHEAD instructions before, with a
 // share of other work beside each: read(i) gives operand i, mma(i, operand) uses it, work(i) is
-// the i-th share.
-template <int N, int AHEAD, typename Read, typename Mma, typename Work>
-__device__ __forceinline__ void pipeline(Read read, Mma mma, Work work) {
+// the i-th share. The compiler waits for every operand by itself; with the number of LDS reads that
+// make operand i, reads(i), two are waited for at once, which saves a wave an instruction in eight
+// or so where it is alone on its SIMD.
+template <int N, int AHEAD, typename Read, typename Mma, typename Work, typename Reads>
+__device__ __forceinline__ void pipeline(Read read, Mma mma, Work work, Reads reads) {
   constexpr int A = AHEAD < N ? AHEAD : N;
   u32x4_t x[A];
 #pragma unroll
@@ -311,6 +323,13 @@ __device__ __forceinline__ void pipeline(Read read, Mma mma, Work work) {
 #pragma unroll
   for (int i = 0; i < N; i++) {
     keep_order();
+    if (i % 2 == 0 && i + A <= N && reads(0)) {
+      int after = 0;
+#pragma unroll
+      for (int e = 2; e < A; e++) after += reads(i + e);
+      wait_reads(after);
+      keep_order();
+    }
     mma(i, x[i % A]);
     if (i + A < N) x[i % A] = read(i + A);
     work(i);

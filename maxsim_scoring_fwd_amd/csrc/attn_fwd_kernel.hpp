@@ -72,7 +72,8 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   auto values = [&](const Packed<DT> &p, int n, auto work) {
     const char *vt = v_tile(n);
     pipeline<N2, 4>([&](int e) { return read_cols<DT, DP>(vt, tr_lane, e % OT * 32, e / OT); },
-                    [&](int e, u32x4_t v) { acc[e % OT] = mma_cols<DT>(v, p, e / OT, acc[e % OT]); }, work);
+                    [&](int e, u32x4_t v) { acc[e % OT] = mma_cols<DT>(v, p, e / OT, acc[e % OT]); }, work,
+                    [](int) { return DT == DT_FP32 ? 0 : 2; });
   };
   // Tile n + 1's products and then tile n's values in one run, so that reads run ahead across.
   auto both = [&](f32x16_t &x, const Packed<DT> &p, int n, auto work) {
@@ -87,7 +88,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
           if (e < N1) x = mma_rows<DT>(v, q.f[e % N1], e ? x : zero16());
           else acc[y % OT] = mma_cols<DT>(v, p, y / OT, acc[y % OT]);
         },
-        work);
+        work, [](int e) { return DT == DT_FP32 ? 0 : e < N1 ? 1 : 2; });
   };
 
   // Products of tile n to scores, and their maximum, elements from .. to - 1. Where no key of the
@@ -101,20 +102,40 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   auto scores = [&](f32x16_t &x, int n, bool linear, int from, int to) {
     const float dist0 = (float)(i - n * BN - 4 * h);
     const int left = vis - n * BN - 4 * h;
-#pragma unroll
-    for (int r = from; r < to; r++) {
-      float y = x[r];
-      if (LINEAR && linear) {
-        if (has_cap(MODE))
-          y = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y * form.a)) * (-2.0f * form.b) + slope_row[r];
-        else
-          y = __builtin_fmaf(y, form.a, slope_row[r]);
-      } else if (MODE != ATTN_PLAIN) {
-        y = score<DT, MODE>(form, y, dist0 - (float)acc_row(r), nullptr);
-      }
+    auto finish = [&](int r, float y) {
       if (!linear) y = acc_row(r) < left ? y : -INFINITY;
       top = __builtin_fmaxf(top, y);
       x[r] = y;
+    };
+    if constexpr (has_cap(MODE) && DT != DT_FP32) {
+      // b tanh(x) = b - 2 b / (1 + e^2x), one of its three parts at an element, so that none waits
+      // for the one before
+      auto tail = [&](int r) {
+        float y = x[r] * (-2.0f * form.b);
+        if (has_bias(MODE) && linear) y += slope_row[r];
+        else if (has_bias(MODE)) y = __builtin_fmaf(-form.slope, __builtin_fabsf(dist0 - (float)acc_row(r)), y + form.b);
+        else y += form.b;
+        finish(r, y);
+      };
+#pragma unroll
+      for (int r = from; r < to; r++) {
+        if (r >= 2) tail(r - 2);
+        if (r >= 1) x[r - 1] = __builtin_amdgcn_rcpf(1.0f + x[r - 1]);
+        x[r] = __builtin_amdgcn_exp2f(x[r] * form.a);
+      }
+      if (to == 16) {
+        x[15] = __builtin_amdgcn_rcpf(1.0f + x[15]);
+        tail(14);
+        tail(15);
+      }
+    } else {
+#pragma unroll
+      for (int r = from; r < to; r++) {
+        float y = x[r];
+        if (LINEAR && linear) y = __builtin_fmaf(y, form.a, slope_row[r]);
+        else if (MODE != ATTN_PLAIN) y = score<DT, MODE>(form, y, dist0 - (float)acc_row(r), nullptr);
+        finish(r, y);
+      }
     }
   };
   // Tiles below this one are linear (keys after the rows would want the other sign of the slope;
@@ -143,9 +164,10 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
 #pragma unroll
     for (int r = from; r < to; r++) {
       const float w = __builtin_amdgcn_exp2f(MODE == ATTN_PLAIN ? __builtin_fmaf(x[r], post, off) : x[r] + off);
-      sum += w;
+      if (r > 0) sum += x[r - 1];  // one behind: the add does not wait for the exponential
       x[r] = w;
     }
+    if (to == 16) sum += x[15];
   };
   // What iteration n begins with, and its fetches.
   int next_k = 0, next_v = 0;
