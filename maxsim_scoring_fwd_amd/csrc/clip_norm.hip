@@ -14,8 +14,9 @@ using namespace maxsim;
 namespace {
 
 constexpr int CLIP_THREADS = 256;
-constexpr int CLIP_TENSORS = 96;      // per launch: the table travels in the kernel arguments
-constexpr int CLIP_CHUNK = 16384;     // elements of a workgroup's piece of a tensor
+constexpr int CLIP_TENSORS = 128;     // per launch: the table travels in the kernel arguments (4 KiB)
+constexpr int CLIP_CHUNK = 16384;     // most elements of a workgroup's piece of a tensor
+constexpr int CLIP_CHUNK_LEAST = 2048;
 constexpr int CLIP_GRID = 1024;       // most workgroups, and partial sums, of a launch
 
 struct ClipTable {
@@ -26,6 +27,7 @@ struct ClipTable {
   uint8_t dtype[CLIP_TENSORS];
   uint8_t wide[CLIP_TENSORS];  // 16-byte vectors on both sides
   int n;
+  int chunk;  // elements of a piece
   uint32_t chunks;
 };
 
@@ -102,8 +104,8 @@ __global__ void __launch_bounds__(CLIP_THREADS) clip_squares_kernel(const ClipTa
   double s = 0;
   for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const int k = tensor_of(t, c);
-    const int64_t at = (int64_t)(c - t.first[k]) * CLIP_CHUNK;
-    const int64_t n = t.numel[k] - at < CLIP_CHUNK ? t.numel[k] - at : CLIP_CHUNK;
+    const int64_t at = (int64_t)(c - t.first[k]) * t.chunk;
+    const int64_t n = t.numel[k] - at < t.chunk ? t.numel[k] - at : t.chunk;
     const bool w = t.wide[k];
     switch (t.dtype[k]) {
     case MAXSIM_BF16: s += squares((const __bf16 *)t.src[k] + at, n, w); break;
@@ -130,8 +132,8 @@ clip_scale_kernel(const ClipTable t, const double *part, int n_part, double max_
        i >= 0 && t.chunks; i -= gridDim.x) {
     const int k = tensor_of(t, (uint32_t)i);
     if (c == 1.0f && t.src[k] == t.dst[k]) continue;  // nothing to change
-    const int64_t at = (i - t.first[k]) * CLIP_CHUNK;
-    const int64_t n = t.numel[k] - at < CLIP_CHUNK ? t.numel[k] - at : CLIP_CHUNK;
+    const int64_t at = (i - t.first[k]) * t.chunk;
+    const int64_t n = t.numel[k] - at < t.chunk ? t.numel[k] - at : t.chunk;
     const bool w = t.wide[k];
     switch (t.dtype[k]) {
     case MAXSIM_BF16: scaled((const __bf16 *)t.src[k] + at, (__bf16 *)t.dst[k] + at, n, w, c); break;
@@ -146,6 +148,11 @@ clip_scale_kernel(const ClipTable t, const double *part, int n_part, double max_
 // Tensors [from, from + CLIP_TENSORS) of the caller's list that have elements.
 void fill_table(ClipTable &t, const void *const *grads, void *const *outs, const int64_t *numel,
                 const int32_t *dtypes, int from, int to) {
+  // Pieces small enough for every workgroup of a full grid to get one.
+  int64_t total = 0;
+  for (int i = from; i < to; i++) total += numel[i];
+  t.chunk = CLIP_CHUNK_LEAST;
+  while (t.chunk < CLIP_CHUNK && total > (int64_t)t.chunk * CLIP_GRID) t.chunk *= 2;
   t.n = 0;
   t.chunks = 0;
   for (int i = from; i < to; i++) {
@@ -157,7 +164,7 @@ void fill_table(ClipTable &t, const void *const *grads, void *const *outs, const
     t.dtype[k] = (uint8_t)dtypes[i];
     t.wide[k] = aligned(t.src[k], 16) && aligned(t.dst[k], 16);
     t.first[k] = t.chunks;
-    t.chunks += (uint32_t)((numel[i] + CLIP_CHUNK - 1) / CLIP_CHUNK);
+    t.chunks += (uint32_t)((numel[i] + t.chunk - 1) / t.chunk);
   }
 }
 

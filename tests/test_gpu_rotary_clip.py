@@ -139,6 +139,7 @@ def grads(shapes, dtypes, seed=0, std=1e-3):
     ([(0,), (0, 4)], ["fp32", "bf16"]),
     ([(3,)] * 300 + [(100, 100)], ["fp32", "bf16", "fp16"] * 100 + ["bf16"]),
     ([(5_000_001,), (77,)], ["bf16", "fp32"]),
+    ([(3,)] * 130 + [(17_000_003,), (9,)], ["fp16"] * 130 + ["bf16", "fp32"]),
 ])
 def test_clip(shapes, dtypes, max_norm):
     t = T()
