@@ -87,27 +87,33 @@ __device__ __forceinline__ void attn_dq_tile(const AttnArgs &a, const AttnTile &
 #pragma unroll
       for (int r = from; r < to; r++) dp[r] = s[r] * (dp[r] - delta);
     };
-    pipeline<2 * A + C, 4>(
-        [&](int j) {
-          return j < A       ? read_rows<DT, DP>(ldsk, row_lane, j)
-                 : j < 2 * A ? read_rows<DT, DP>(ldsv, row_lane, j - A)
-                             : read_cols<DT, DP>(ldsk, tr_lane, (j - 2 * A) % OT * 32, (j - 2 * A) / OT);
-        },
-        [&](int j, u32x4_t x) {
-          const int y = j - 2 * A;
-          if (j < A) s = mma_rows<DT>(x, q.f[j % A], j ? s : zero16());
-          else if (j < 2 * A) dp = mma_rows<DT>(x, g.f[j % A], j > A ? dp : zero16());
-          else acc[y % OT] = mma_cols<DT>(x, p, y / OT, acc[y % OT]);
-        },
-        [&](int j) {
-          if (j < A) fetch(n + 2, j * P / A, (j + 1) * P / A);
-          else if (j < 2 * A) weights((j - A) * 16 / A, (j + 1 - A) * 16 / A);
-          if (j == 2 * A - 1) {
-            grads(0, 16);
-            p.set(dp);
-          }
-        },
-        [](int j) { return DT == DT_FP32 ? 0 : j < 2 * A ? 1 : 2; });
+    auto read = [&](int j) {
+      return j < A       ? read_rows<DT, DP>(ldsk, row_lane, j)
+             : j < 2 * A ? read_rows<DT, DP>(ldsv, row_lane, j - A)
+                         : read_cols<DT, DP>(ldsk, tr_lane, (j - 2 * A) % OT * 32, (j - 2 * A) / OT);
+    };
+    auto mma = [&](int j, u32x4_t x) {
+      const int y = j - 2 * A;
+      if (j < A) s = mma_rows<DT>(x, q.f[j % A], j ? s : zero16());
+      else if (j < 2 * A) dp = mma_rows<DT>(x, g.f[j % A], j > A ? dp : zero16());
+      else acc[y % OT] = mma_cols<DT>(x, p, y / OT, acc[y % OT]);
+    };
+    auto work = [&](int j) {
+      if (j < A) fetch(n + 2, j * P / A, (j + 1) * P / A);
+      else if (j < 2 * A) weights((j - A) * 16 / A, (j + 1 - A) * 16 / A);
+      if (j == 2 * A - 1) {
+        grads(0, 16);
+        p.set(dp);
+      }
+    };
+    auto reads = [](int j) { return DT == DT_FP32 ? 0 : j < 2 * A ? 1 : 2; };
+    if constexpr (DP > 128) {  // in two, or it is too long for the compiler to unroll
+      pipeline<2 * A, 4>(read, mma, work, reads);
+      pipeline<C, 4>([&](int j) { return read(2 * A + j); }, [&](int j, u32x4_t x) { mma(2 * A + j, x); },
+                     [](int) {}, [&](int j) { return reads(2 * A + j); });
+    } else {
+      pipeline<2 * A + C, 4>(read, mma, work, reads);
+    }
   };
   tile_barrier();
   int n = 0;
@@ -344,8 +350,15 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
                        t.rows - wave0, row_bytes);
 }
 
+// Waves a SIMD: two where 256 registers are enough or nearly so. 16-bit heads of 96 miss that by 2
+// to 20 registers: a backward pass over 256 documents of 20 to 300 tokens and 12 heads takes 397 us
+// with a second wave and 506 without, one over 16 pages of 1060 tokens with cap and bias, which
+// spills six, 666 and 721. Heads of 128 would spill 75 and more.
+template <int DT, int DP> struct DkvWaves { static constexpr int value = DT != DT_FP32 && DP <= 96 ? 2 : 1; };
+
 template <int DT, int DP, int MODE, int WHAT>
-__global__ void __launch_bounds__(ATTN_THREADS) attn_dkv_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(ATTN_THREADS) __attribute__((amdgpu_waves_per_eu(DkvWaves<DT, DP>::value)))
+attn_dkv_kernel(const AttnArgs a) {
   __shared__ __align__(256) char lds[8 * 32 * RowLayout<DT, DP>::bytes];  // two rings of four tiles
   __shared__ __align__(256) float stat[4 * 64];
   AttnTile t;
