@@ -171,7 +171,9 @@ int maxsim_attention_backward(const maxsim_attention_desc *desc, const void *o, 
                                                 : (const void *)attn_delta_kernel<DT_FP32>;
   const int dp = attn_width(a.d), mode = mode_of(a);
   float unit = has_cap(mode) ? 1.0f : a.scale * LOG2E;
+  // what exponents of the weights have beside the product: see ATTN_WEIGHT_SHIFT, ScoreForm::c
   float shift = desc->dtype == MAXSIM_FP16 ? ATTN_WEIGHT_SHIFT : 0.0f;
+  if (has_cap(mode) && desc->dtype != MAXSIM_FP32) shift += a.softcap * LOG2E;
   void *kargs[] = {&a, &stats, &maxima, &unit, &shift};
   if (hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), kargs, 0, st) != hipSuccess) {
     (void)hipGetLastError();

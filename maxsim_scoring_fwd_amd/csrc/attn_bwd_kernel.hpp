@@ -31,7 +31,8 @@ __device__ __forceinline__ void attn_dq_tile(const AttnArgs &a, const AttnTile &
   const int wave_tiles = wave0 < t.len ? (wave_most + BN - 1) / BN : 0;
   const int whole_tiles = wave0 < t.len ? visible(a, t, wave0) / BN : 0;  // nothing hidden in them
   const int64_t at = (int64_t)t.head * a.rows + t.row0 + iq;
-  const float lse = a.lse[at] * LOG2E, delta = -a.stats[at].y;
+  const float start = form.c - a.lse[at] * LOG2E, delta = -a.stats[at].y;
+  constexpr float UNIT = slope_unit<DT, MODE>;
   const float gs = DT == DT_FP16 ? *a.grad_scale : 1.0f;
 
   // Rings of four tiles, as in the forward: tile n + 2 is fetched in iteration n.
@@ -76,11 +77,11 @@ __device__ __forceinline__ void attn_dq_tile(const AttnArgs &a, const AttnTile &
 #pragma unroll
       for (int r = from; r < to; r++) {
         float keep = 1.0f;
-        float y = score<DT, MODE>(form, s[r], dist0 - (float)acc_row(r), &keep);
+        float y = score<DT, MODE>(form, s[r], dist0 - (float)acc_row(r), start, &keep);
         if (masked) y = acc_row(r) < left ? y : -INFINITY;
-        s[r] = __builtin_amdgcn_exp2f(y - lse);
+        s[r] = __builtin_amdgcn_exp2f(y);
         if (has_cap(MODE)) s[r] *= keep;
-        if (DT == DT_FP16) s[r] *= gs;
+        if (DT == DT_FP16) s[r] *= gs * UNIT;
       }
     };
     auto grads = [&](int from, int to) {
@@ -124,7 +125,7 @@ __device__ __forceinline__ void attn_dq_tile(const AttnArgs &a, const AttnTile &
     fetch(n + 2, 0, P);
   }
   tile_barrier();  // the tiles' memory is free
-  store_rows<DT, DP>(lds + wave * TILE, acc, i < t.len ? a.scale / gs : 0.0f,
+  store_rows<DT, DP>(lds + wave * TILE, acc, i < t.len ? (DT == DT_FP16 ? a.scale / gs : a.scale * UNIT) : 0.0f,
                      a.dq + ((t.row0 + wave0) * a.heads + t.head) * row_bytes,
                      (int64_t)a.heads * row_bytes, t.rows - wave0, row_bytes);
 }
@@ -160,7 +161,8 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
   const int from = t.first >= t.prefix ? t.first : 0;
   const int jmask = j < t.prefix ? -1 : j;
   const float gs = DT == DT_FP16 ? *a.grad_scale : 1.0f;
-  const float gs8 = gs * __builtin_amdgcn_exp2f(-SHIFT);
+  constexpr float UNIT = slope_unit<DT, MODE>;
+  const float gs8 = gs * __builtin_amdgcn_exp2f(-SHIFT) * UNIT;
 
   // Rings of four tiles as in the other kernels, the rows of one head after the other's, with the
   // rows' statistics beside them.
@@ -253,8 +255,7 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
 #pragma unroll
       for (int r = first; r < to; r++) {
         float keep = 1.0f;
-        float y = score<DT, MODE>(form, s[r], dist0 + (float)acc_row(r), &keep);
-        if (has_cap(MODE)) y += lse[r];
+        float y = score<DT, MODE>(form, s[r], dist0 + (float)acc_row(r), has_cap(MODE) ? lse[r] : NOTHING, &keep);
         if (masked) y = acc_row(r) < hide || acc_row(r) >= there ? -INFINITY : y;
         s[r] = __builtin_amdgcn_exp2f(y);
         if (has_cap(MODE)) slope[r] = keep;
@@ -344,7 +345,7 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
   char *const mine = lds + wave * TILE;
   const bool real = j < t.len;
   if constexpr (DK)
-    store_rows<DT, DP>(mine, dk, real ? a.scale / gs : 0.0f, a.dk + first, stride, t.rows - wave0, row_bytes);
+    store_rows<DT, DP>(mine, dk, real ? (DT == DT_FP16 ? a.scale / gs : a.scale * UNIT) : 0.0f, a.dk + first, stride, t.rows - wave0, row_bytes);
   if constexpr (DV)
     store_rows<DT, DP>(mine, dv, real ? __builtin_amdgcn_exp2f(-SHIFT) : 0.0f, a.dv + first, stride,
                        t.rows - wave0, row_bytes);

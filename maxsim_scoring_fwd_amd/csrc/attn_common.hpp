@@ -353,42 +353,46 @@ __device__ __forceinline__ int acc_row(int r) { return (r & 3) + 8 * (r >> 2); }
 // Constants of the scores, in units of log 2 (the exponentials are powers of two).
 struct ScoreForm {
   float a, b, slope;
+  float c;  // the score's constant term, which `score` leaves out
 };
 template <int DT, int MODE>
 __device__ __forceinline__ ScoreForm score_form(const AttnArgs &a, int head) {
   ScoreForm f;
   f.slope = has_bias(MODE) ? a.slopes[head] * LOG2E : 0.0f;
+  f.a = a.scale * LOG2E;
+  f.b = f.c = 0.0f;
   if (has_cap(MODE)) {
     f.a = a.scale / a.softcap * (DT == DT_FP32 ? 1.0f : 2.0f * LOG2E);
     f.b = a.softcap * LOG2E;
-  } else {
-    f.a = a.scale * LOG2E;
-    f.b = 0.0f;
+    f.c = DT == DT_FP32 ? 0.0f : f.b;
   }
   return f;
 }
 
-// A product of q and k to its score: scale, cap and bias. dist: i - j. keep: the cap's slope
-// 1 - tanh^2, for the backward. The forward leaves the plain scale to the exponential's FMA.
-// tanh(z) = 1 - 2 / (1 + exp(2 z)): off by about 1e-7 absolutely, which 16-bit inputs do not
-// see; fp32 takes tanhf.
+constexpr float NOTHING = -0.0f;  // x + NOTHING is x for every x, so the compiler drops the sum
+
+// q.k (x) to a score less its constant term, plus off; dist: the tokens' distance. keep: the cap's
+// slope over slope_unit (1 without a cap). tanh x = 1 - 2 / (1 + e^2x) costs a reciprocal and an
+// exponential; near 0 it loses relative accuracy (2^-24 absolute of a score of magnitude softcap),
+// which 16-bit inputs cannot see; fp32 takes tanhf.
 template <int DT, int MODE>
-__device__ __forceinline__ float score(const ScoreForm &f, float x, float dist, float *keep) {
+__device__ __forceinline__ float score(const ScoreForm &f, float x, float dist, float off, float *keep) {
   float y;
   if constexpr (!has_cap(MODE)) {
-    y = x * f.a;
+    y = x * f.a + off;
   } else if constexpr (DT == DT_FP32) {
     const float t = tanhf(x * f.a);
-    y = f.b * t;
+    y = f.b * t + off;
     if (keep) *keep = __builtin_fmaf(-t, t, 1.0f);
   } else {
     const float r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * f.a));
-    y = __builtin_fmaf(-2.0f * f.b, r, f.b);
-    if (keep) *keep = 4.0f * r * (1.0f - r);
+    y = __builtin_fmaf(-2.0f * f.b, r, off);
+    if (keep) *keep = __builtin_fmaf(-r, r, r);
   }
   if constexpr (has_bias(MODE)) y = __builtin_fmaf(-f.slope, __builtin_fabsf(dist), y);
   return y;
 }
+template <int DT, int MODE> constexpr float slope_unit = has_cap(MODE) && DT != DT_FP32 ? 4.0f : 1.0f;
 
 // Where a workgroup works: a tile of a document's rows, and a head.
 struct AttnTile {

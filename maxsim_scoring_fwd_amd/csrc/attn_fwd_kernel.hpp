@@ -30,7 +30,9 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   const int kv = t.head / a.group;
   const char *kp = a.k + t.k + kv * a.k_head, *vp = a.v + t.v + kv * a.v_head;
   const ScoreForm form = score_form<DT, MODE>(a, t.head);
-  const float post = MODE == ATTN_PLAIN ? form.a : 1.0f;  // factor left to the exponentials
+  // Without a bias the last factor of a score and its constant term are left to the exponentials.
+  constexpr bool RAW = MODE == ATTN_PLAIN || (MODE == ATTN_CAP && DT != DT_FP32);
+  const float post = MODE == ATTN_PLAIN ? form.a : RAW ? 2.0f * form.b : 1.0f;
   const int vis = visible(a, t, iq);
   const int last = t.first + ATTN_ROWS < t.len ? t.first + ATTN_ROWS - 1 : t.len - 1;
   const int tiles = (visible(a, t, last) + BN - 1) / BN;
@@ -63,7 +65,8 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
 #pragma unroll
   for (int c = 0; c < OT; c++) acc[c] = zero16();
   float m = -1e30f, sum = 0.0f;  // a finite start: exp2(-inf - m) is 0 for rows that see nothing yet
-  float top = -INFINITY, base = 0.0f;  // of the tile at hand
+  const float base0 = RAW ? form.c : 0.0f;
+  float top = -INFINITY, base = base0;  // of the tile at hand
   const int row_lane = row_lane_offset<DT, DP>(), tr_lane = tr_lane_offset<DT, DP>();
 
   // Operands from LDS: N1 of a tile's products, N2 of its sum of values, a share of the keys after
@@ -97,7 +100,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   // joins an FMA that is there anyway.
   f32x16_t slope_row;  // slope * key, and the cap's constant term
 #pragma unroll
-  for (int r = 0; r < 16; r++) slope_row[r] = __builtin_fmaf(form.slope, (float)acc_row(r), form.b);
+  for (int r = 0; r < 16; r++) slope_row[r] = __builtin_fmaf(form.slope, (float)acc_row(r), form.c);
   constexpr bool LINEAR = has_bias(MODE) && !(has_cap(MODE) && DT == DT_FP32);
   auto scores = [&](f32x16_t &x, int n, bool linear, int from, int to) {
     const float dist0 = (float)(i - n * BN - 4 * h);
@@ -108,23 +111,24 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
       x[r] = y;
     };
     if constexpr (has_cap(MODE) && DT != DT_FP32) {
-      // b tanh(x) = b - 2 b / (1 + e^2x), one of its three parts at an element, so that none waits
+      // b tanh(x) = b + 2 b / (-1 - e^2x), one of its three parts at an element, so that none waits
       // for the one before
       auto tail = [&](int r) {
-        float y = x[r] * (-2.0f * form.b);
-        if (has_bias(MODE) && linear) y += slope_row[r];
-        else if (has_bias(MODE)) y = __builtin_fmaf(-form.slope, __builtin_fabsf(dist0 - (float)acc_row(r)), y + form.b);
-        else y += form.b;
+        float y = x[r];
+        if (has_bias(MODE) && linear) y = __builtin_fmaf(y, 2.0f * form.b, slope_row[r]);
+        else if (has_bias(MODE))
+          y = __builtin_fmaf(-form.slope, __builtin_fabsf(dist0 - (float)acc_row(r)),
+                             __builtin_fmaf(y, 2.0f * form.b, form.c));
         finish(r, y);
       };
 #pragma unroll
       for (int r = from; r < to; r++) {
         if (r >= 2) tail(r - 2);
-        if (r >= 1) x[r - 1] = __builtin_amdgcn_rcpf(1.0f + x[r - 1]);
+        if (r >= 1) x[r - 1] = __builtin_amdgcn_rcpf(-1.0f - x[r - 1]);
         x[r] = __builtin_amdgcn_exp2f(x[r] * form.a);
       }
       if (to == 16) {
-        x[15] = __builtin_amdgcn_rcpf(1.0f + x[15]);
+        x[15] = __builtin_amdgcn_rcpf(-1.0f - x[15]);
         tail(14);
         tail(15);
       }
@@ -133,7 +137,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
       for (int r = from; r < to; r++) {
         float y = x[r];
         if (LINEAR && linear) y = __builtin_fmaf(y, form.a, slope_row[r]);
-        else if (MODE != ATTN_PLAIN) y = score<DT, MODE>(form, y, dist0 - (float)acc_row(r), nullptr);
+        else if (MODE != ATTN_PLAIN) y = score<DT, MODE>(form, y, dist0 - (float)acc_row(r), NOTHING, nullptr);
         finish(r, y);
       }
     }
@@ -163,7 +167,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   auto weights = [&](f32x16_t &x, float off, int from, int to) {
 #pragma unroll
     for (int r = from; r < to; r++) {
-      const float w = __builtin_amdgcn_exp2f(MODE == ATTN_PLAIN ? __builtin_fmaf(x[r], post, off) : x[r] + off);
+      const float w = __builtin_amdgcn_exp2f(RAW ? __builtin_fmaf(x[r], post, off) : x[r] + off);
       if (r > 0) sum += x[r - 1];  // one behind: the add does not wait for the exponential
       x[r] = w;
     }
@@ -195,7 +199,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
       if (e == N1 - 1) p.set(s);
       if (e >= N1) scores(next, n + 1, linear, (e - N1) * 16 / N2, (e + 1 - N1) * 16 / N2);
     });
-    base = LINEAR && linear ? -form.slope * (float)(i - (n + 1) * BN - 4 * h) : 0.0f;
+    base = LINEAR && linear ? -form.slope * (float)(i - (n + 1) * BN - 4 * h) : base0;
     settle();
     s = next;
   };
