@@ -1,7 +1,16 @@
 // Attention backward, after <dO, o> per row (attn_delta.hpp): dQ (keys in tiles, one wave on 32 queries) and
 // dK / dV (queries in tiles, one wave on 32 keys, all heads that share them). The scores are
 // computed again in both: 7 products instead of 5, but every sum has one owner, so there are no
-// atomics and repeated calls give the same bits.
+// atomics and repeated calls give the same bits. With P the weights exp(y - lse), recomputed:
+//   dP = dO V^T,  dS = P (dP - delta) * (the cap's slope),  dQ = scale dS K,  dK = scale dS^T Q,
+//   dV = P^T dO
+// Sums are 32 bits wide; P and dS are rounded to the inputs' type as operands of the last three
+// products (fp16 after a power of two that keeps dS in range).
+//
+// Measured (one MI355X): 512 documents of 20 to 300 tokens, 12 heads of 64, bf16: dQ 187 us, dK / dV
+// 294 us, 0.63 and 0.76 GB, 3.4 and 2.6 TB/s; 16 pages of about 1045 tokens, 16 heads of 128 on 4,
+// with cap: dQ 251 us, dK / dV 368 us, 420 and 380 TFLOP/s. Instructions bound the pages (32 matrix
+// instructions and 300 others a tile of dK / dV, one wave a SIMD), waits the short documents.
 #pragma once
 
 #include "attn_common.hpp"

@@ -1,16 +1,31 @@
-// Attention forward: 4 waves of 32 queries each, keys in tiles of 32 through LDS.
+// Attention forward: 4 waves of 32 queries each, keys in tiles of 32 through LDS. One pass over the
+// keys with a running maximum m and sum of a query's weights:
+//   y_j = score of key j,  w_j = exp2(y_j - m),  sum += w_j,  acc += w_j v_j,
+//   o = acc / sum,  lse = (m + log2 sum) ln 2
+// all in 32 bits; the weights are rounded to the inputs' 16 bits for the second product, which is
+// the rounding that v has anyway (sum holds them unrounded).
 //
 // A wave works on two tiles at once: the next tile's scores (matrix core) beside this tile's
 // exponentials, and this tile's sum of values (matrix core) beside the next tile's scale, mask and
 // maximum. K is therefore used one tile ahead of V. Each has a ring of four tiles in LDS, which
 // makes one barrier every two tiles enough.
+//
+// Measured (one MI355X): 1024 documents of 20 to 300 tokens, 12 heads of 64, bf16: 282 us, 1.0 GB in
+// and out, 3.6 TB/s, 1.4 times a plain copy of it. 48 pages of about 1045 tokens, 8 heads of 256 on
+// one shared, cap: 559 us, 750 TFLOP/s. Two causal documents of 5003 to 8191 tokens, 32 heads of 128
+// on 8, fp16: 890 us, 850 TFLOP/s, where a large library product reaches 1260. No single unit bounds
+// the long ones: of 889 us, 791 are left without LDS reads, 664 without the softmax, 808 without
+// fetches. Matrix cores are busy 43% and vector units 61% of the cycles, at a clock that the load
+// pulls to 1.8 GHz. Short documents spend half a wave's time waiting: to find its document, for
+// the first tiles, and for the waves of its workgroup that have rows.
 #pragma once
 
 #include "attn_common.hpp"
 
 namespace maxsim {
 
-// Waves a SIMD that the registers are divided for.
+// Waves a SIMD that the registers are divided for: as many as spill nothing. The passages above take
+// 282 us with four and 310 with three, the long documents 890 with two and 1095 with one.
 template <int DT, int DP, int MODE> struct FwdWaves {
   static constexpr int value = DP == 256 ? 1 : DP >= 96 ? 2 : DT != DT_FP32 && MODE == ATTN_PLAIN ? 4 : 3;
 };

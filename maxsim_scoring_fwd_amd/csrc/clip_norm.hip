@@ -4,7 +4,9 @@
 // Two passes over the data, since no output is known before the whole norm: the first leaves
 // one partial sum per workgroup, the second sums the partials (every workgroup for itself, in
 // one order, so all hold the same norm) and scales. The second pass walks the chunks backwards:
-// what the first read last is what the caches still hold.
+// what the first read last is what the caches still hold. Measured (one MI355X): 99 bf16 gradients
+// of 180 MB, 30 us for the squares and 60 us for the scaling (6.0 TB/s both); one of 0.4 MB, 3.7
+// and 4.3 us, less than the call's 14 us on the host.
 #include <hip/hip_runtime.h>
 
 #include "host_common.hpp"
@@ -148,7 +150,9 @@ clip_scale_kernel(const ClipTable t, const double *part, int n_part, double max_
 // Tensors [from, from + CLIP_TENSORS) of the caller's list that have elements.
 void fill_table(ClipTable &t, const void *const *grads, void *const *outs, const int64_t *numel,
                 const int32_t *dtypes, int from, int to) {
-  // Pieces small enough for every workgroup of a full grid to get one.
+  // Pieces small enough for every workgroup of a full grid to get one: a gradient of 98304 elements
+  // takes 3.7 + 4.3 us in 49 pieces of 2048 and 4.4 + 7.6 us in 7 of 16384, and large ones lose
+  // nothing to a search every 16384.
   int64_t total = 0;
   for (int i = from; i < to; i++) total += numel[i];
   t.chunk = CLIP_CHUNK_LEAST;

@@ -190,9 +190,8 @@ def test_many_documents(kind):
     ("bf16", 96, 8, 1, False, 0.0, True), ("fp16", 72, 12, 3, True, 0.0, False),
     ("bf16", 32, 32, 4, True, 0.0, True)])
 def test_long_batches(dtype, d, heads, kv, causal, cap, bias):
-    """Enough long documents for the widest tiles (64 queries a wave): the results of one of them
-    are what it gets alone, in the narrow tiles, up to the rounding of the weights, whose order of
-    sums differs; and a head of the shortest against 64 bits."""
+    """Enough long documents for several rounds of workgroups on every CU: single heads of some of
+    them, in the batch and alone, against 64 bits."""
     t = T()
     lens = [1100, 700, 1025, 513, 1400, 900, 640] * 4
     q, k, v, do, lay, docs = inputs(77, lens, heads, kv, d, dt(dtype), 0)
