@@ -61,6 +61,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   const int lds_k = lds_address(lds), lds_v = lds_k + 4 * TILE;
   auto k_tile = [&](int n) { return lds + (n & 3) * TILE; };
   auto v_tile = [&](int n) { return lds + (4 + (n & 3)) * TILE; };
+  // (`at` below: n, or a constant that is n modulo 4 where the rings' places shall be constants.)
   Carry<DT, DP> ck, cv;
   ck.init(a.k_tok, row_bytes);
   cv.init(a.v_tok, row_bytes);
@@ -87,15 +88,15 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   // Operands from LDS: N1 of a tile's products, N2 of its sum of values, a share of the keys after
   // the other, so that neighbours add to different accumulators.
   constexpr int N1 = L::steps, N2 = OT * Packed<DT>::n;
-  auto values = [&](const Packed<DT> &p, int n, auto work) {
-    const char *vt = v_tile(n);
+  auto values = [&](const Packed<DT> &p, int at, auto work) {
+    const char *vt = v_tile(at);
     pipeline<N2, 4>([&](int e) { return read_cols<DT, DP>(vt, tr_lane, e % OT * 32, e / OT); },
                     [&](int e, u32x4_t v) { acc[e % OT] = mma_cols<DT>(v, p, e / OT, acc[e % OT]); }, work,
                     [](int) { return DT == DT_FP32 ? 0 : 2; });
   };
   // Tile n + 1's products and then tile n's values in one run, so that reads run ahead across.
-  auto both = [&](f32x16_t &x, const Packed<DT> &p, int n, auto work) {
-    const char *kt = k_tile(n + 1), *vt = v_tile(n);
+  auto both = [&](f32x16_t &x, const Packed<DT> &p, int at, auto work) {
+    const char *kt = k_tile(at + 1), *vt = v_tile(at);
     pipeline<N1 + N2, 4>(
         [&](int e) {
           return e < N1 ? read_rows<DT, DP>(kt, row_lane, e)
@@ -190,25 +191,25 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   };
   // What iteration n begins with, and its fetches.
   int next_k = 0, next_v = 0;
-  auto begin = [&](int n) {
-    if ((n & 1) == 0) tile_barrier();
+  auto begin = [&](int at) {
+    if ((at & 1) == 0) tile_barrier();
     ck.next();
     cv.next();
-    next_k = lds_k + ((n + 3) & 3) * TILE;
-    next_v = lds_v + ((n + 2) & 3) * TILE;
+    next_k = lds_k + ((at + 3) & 3) * TILE;
+    next_v = lds_v + ((at + 2) & 3) * TILE;
   };
   auto fetch = [&](int e) {
     if (e < C) ck.go(next_k, wave, e);
     else if (e < 2 * C) cv.go(next_v, wave, e - C);
   };
-  auto step = [&](int n, bool linear) {
-    begin(n);
+  auto step = [&](int n, int at, bool linear) {
+    begin(at);
     follow();
     const float off = base - m;
     top = -INFINITY;
     Packed<DT> p;
     f32x16_t next;
-    both(next, p, n, [&](int e) {
+    both(next, p, at, [&](int e) {
       fetch(e);
       if (e < N1) weights(s, off, e * 16 / N1, (e + 1) * 16 / N1);
       if (e == N1 - 1) p.set(s);
@@ -227,8 +228,17 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   }
   // One loop for each kind of tile: merging the kinds in one would copy the accumulators.
   int n = 0;
-  for (; n + 1 < linear_tiles; n++) step(n, true);
-  for (; n + 1 < wave_tiles; n++) step(n, false);
+  // Four at a time the rings' places are constants, and the reads' addresses need no additions: 844
+  // in place of 891 us for the long documents. Heads of 256 gain nothing (their rings pass the 64 KB
+  // that a read's offset reaches: 551 and 545 us for the pages), and with four waves it would spill.
+  if constexpr (FwdWaves<DT, DP, MODE>::value == 2 || FwdWaves<DT, DP, MODE>::value == 3) {
+    for (; n + 4 < linear_tiles; n += 4) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) step(n + e, e, true);
+    }
+  }
+  for (; n + 1 < linear_tiles; n++) step(n, n, true);
+  for (; n + 1 < wave_tiles; n++) step(n, n, false);
   if (wave_tiles > 0) {
     begin(n);
     follow();
