@@ -83,15 +83,31 @@ __device__ __forceinline__ void attn_dq_tile(const AttnArgs &a, const AttnTile &
     f32x16_t s, dp;
     Packed<DT> p;
     // products to weights, times the cap's slope where there is one
+    f32x16_t slope;  // of the cap
+    auto weight = [&](int r, float y) {
+      if (masked) y = acc_row(r) < left ? y : -INFINITY;
+      s[r] = __builtin_amdgcn_exp2f(y);
+    };
+    auto scaled = [&](int r) {
+      if (has_cap(MODE)) s[r] *= slope[r];
+      if (DT == DT_FP16) s[r] *= gs * UNIT;
+    };
     auto weights = [&](int from, int to) {
+      if constexpr (staged<DT, MODE>) {
+        tanh_stages(form, s, from, to, [&](int r) {
+          if (r > 0) scaled(r - 1);
+          slope[r] = slope_of_tanh(s[r]);
+          weight(r, score_of_tanh<MODE>(form, s[r], dist0 - (float)acc_row(r), start));
+          if (r == 15) scaled(15);
+        });
+      } else {
 #pragma unroll
-      for (int r = from; r < to; r++) {
-        float keep = 1.0f;
-        float y = score<DT, MODE>(form, s[r], dist0 - (float)acc_row(r), start, &keep);
-        if (masked) y = acc_row(r) < left ? y : -INFINITY;
-        s[r] = __builtin_amdgcn_exp2f(y);
-        if (has_cap(MODE)) s[r] *= keep;
-        if (DT == DT_FP16) s[r] *= gs * UNIT;
+        for (int r = from; r < to; r++) {
+          float keep = 1.0f;
+          weight(r, score<DT, MODE>(form, s[r], dist0 - (float)acc_row(r), start, &keep));
+          slope[r] = keep;
+          scaled(r);
+        }
       }
     };
     auto grads = [&](int from, int to) {
@@ -213,10 +229,10 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
       else cq.go(lds_q + (n & 3) * TILE, wave, e / 2);
     }
   };
-  auto fetch_stats = [&](int n) {  // 32 pairs, 4 bytes a lane of the first wave
+  auto fetch_stats = [&](int n) {  // 32 pairs to 32 first and 32 second halves, a lane of wave 0 each
     if (wave == 0) {
-      const uint32_t most = (uint32_t)(cq.left < BM ? cq.left : BM) * 8 - 4;
-      const uint32_t at = lane * 4 < most ? lane * 4 : most;
+      const int last = cq.left < BM ? cq.left - 1 : BM - 1, row = lane & 31;
+      const uint32_t at = (uint32_t)(row < last ? row : last) * 8 + h * 4;
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                    :
                    : "s"(uniform(lds_s + (n & 3) * 256)), "v"(at), "s"(uniform((int64_t)next_stats)));
@@ -248,7 +264,7 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
   auto tile = [&](const ScoreForm &form, int i0, int at, bool masked) {
     begin(at);
     const char *const ldsq = lds + (at & 3) * TILE, *const ldsg = ldsq + 4 * TILE;
-    const f32x4_t *const stats = (const f32x4_t *)(stat + (at & 3) * 64 + 8 * h);
+    const f32x4_t *const stats = (const f32x4_t *)(stat + (at & 3) * 64 + 4 * h);
     const float dist0 = (float)(i0 + 4 * h - j);
     const int hide = jmask - i0 - 4 * h;   // rows below it do not see key j
     const int there = t.len - i0 - 4 * h;  // rows from it on do not exist
@@ -258,24 +274,33 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
     // neither is subtracted (nor held) afterwards. The tanh wants S itself.
     f32x16_t lse;
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-      const f32x4_t y = stats[e / 2 * 4 + e % 2];  // two rows' pairs
-      const int r = e / 2 * 4 + e % 2 * 2;
-      lse[r] = y[0];
-      lse[r + 1] = y[2];
-      dp[r] = y[1];
-      dp[r + 1] = y[3];
+    for (int e = 0; e < 4; e++) {
+      const f32x4_t y = stats[2 * e], z = stats[2 * e + 8];  // rows 8 e + 4 h + 0 .. 3
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        lse[4 * e + g] = y[g];
+        dp[4 * e + g] = z[g];
+      }
     }
     s = has_cap(MODE) ? zero16() : lse;
     f32x16_t slope;  // of the cap
+    auto weight = [&](int r, float y) {
+      if (masked) y = acc_row(r) < hide || acc_row(r) >= there ? -INFINITY : y;
+      s[r] = __builtin_amdgcn_exp2f(y);
+    };
     auto weights = [&](int first, int to) {
+      if constexpr (staged<DT, MODE>) {
+        tanh_stages(form, s, first, to, [&](int r) {
+          slope[r] = slope_of_tanh(s[r]);
+          weight(r, score_of_tanh<MODE>(form, s[r], dist0 + (float)acc_row(r), lse[r]));
+        });
+      } else {
 #pragma unroll
-      for (int r = first; r < to; r++) {
-        float keep = 1.0f;
-        float y = score<DT, MODE>(form, s[r], dist0 + (float)acc_row(r), has_cap(MODE) ? lse[r] : NOTHING, &keep);
-        if (masked) y = acc_row(r) < hide || acc_row(r) >= there ? -INFINITY : y;
-        s[r] = __builtin_amdgcn_exp2f(y);
-        if (has_cap(MODE)) slope[r] = keep;
+        for (int r = first; r < to; r++) {
+          float keep = 1.0f;
+          weight(r, score<DT, MODE>(form, s[r], dist0 + (float)acc_row(r), has_cap(MODE) ? lse[r] : NOTHING, &keep));
+          slope[r] = keep;
+        }
       }
     };
     auto grads = [&](int first, int to) {
@@ -322,12 +347,13 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
       }
       if (e < A) fetch(at + 2, e * P / A, (e + 1) * P / A);
     };
-    if constexpr (DT == DT_FP32) {  // in two, or it is too long for the compiler to unroll
-      pipeline<A + B, 4>(read, mma, work, [](int) { return 0; });
+    auto reads = [](int e) { return DT == DT_FP32 ? 0 : e < A + B ? 1 : 2; };
+    if constexpr (DT == DT_FP32 || DP > 128) {  // in two, or it is too long for the compiler to unroll
+      pipeline<A + B, 4>(read, mma, work, reads);
       pipeline<C + D, 4>([&](int e) { return read(A + B + e); }, [&](int e, u32x4_t x) { mma(A + B + e, x); },
-                         [&](int e) { work(A + B + e); }, [](int) { return 0; });
+                         [&](int e) { work(A + B + e); }, [&](int e) { return reads(A + B + e); });
     } else {
-      pipeline<A + B + C + D, 4>(read, mma, work, [](int e) { return e < A + B ? 1 : 2; });
+      pipeline<A + B + C + D, 4>(read, mma, work, reads);
     }
     n++;
   };

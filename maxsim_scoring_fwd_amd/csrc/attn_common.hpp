@@ -353,7 +353,7 @@ __device__ __forceinline__ int acc_row(int r) { return (r & 3) + 8 * (r >> 2); }
 // Constants of the scores, in units of log 2 (the exponentials are powers of two).
 struct ScoreForm {
   float a, b, slope;
-  float c;  // the score's constant term, which `score` leaves out
+  float c;  // the constant term that score_of_tanh leaves out
 };
 template <int DT, int MODE>
 __device__ __forceinline__ ScoreForm score_form(const AttnArgs &a, int head) {
@@ -371,28 +371,50 @@ __device__ __forceinline__ ScoreForm score_form(const AttnArgs &a, int head) {
 
 constexpr float NOTHING = -0.0f;  // x + NOTHING is x for every x, so the compiler drops the sum
 
-// q.k (x) to a score less its constant term, plus off; dist: the tokens' distance. keep: the cap's
-// slope over slope_unit (1 without a cap). tanh x = 1 - 2 / (1 + e^2x) costs a reciprocal and an
-// exponential; near 0 it loses relative accuracy (2^-24 absolute of a score of magnitude softcap),
-// which 16-bit inputs cannot see; fp32 takes tanhf.
+// q.k (x) to a score, plus off; dist: the tokens' distance. keep: the cap's slope (fp32). 16-bit
+// types take their tanh in stages, below.
 template <int DT, int MODE>
 __device__ __forceinline__ float score(const ScoreForm &f, float x, float dist, float off, float *keep) {
   float y;
-  if constexpr (!has_cap(MODE)) {
-    y = x * f.a + off;
-  } else if constexpr (DT == DT_FP32) {
+  if constexpr (has_cap(MODE)) {
     const float t = tanhf(x * f.a);
     y = f.b * t + off;
     if (keep) *keep = __builtin_fmaf(-t, t, 1.0f);
   } else {
-    const float r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * f.a));
-    y = __builtin_fmaf(-2.0f * f.b, r, off);
-    if (keep) *keep = __builtin_fmaf(-r, r, r);
+    y = x * f.a + off;
   }
   if constexpr (has_bias(MODE)) y = __builtin_fmaf(-f.slope, __builtin_fabsf(dist), y);
   return y;
 }
-template <int DT, int MODE> constexpr float slope_unit = has_cap(MODE) && DT != DT_FP32 ? 4.0f : 1.0f;
+
+// tanh x = 1 + 2 u, u = -1 / (1 + e^2x): a reciprocal and an exponential. Near 0 it loses relative
+// accuracy (2^-24 absolute of a score of magnitude softcap), which 16-bit inputs cannot see.
+template <int DT, int MODE> constexpr bool staged = has_cap(MODE) && DT != DT_FP32;
+// Elements from .. to - 1 of x: each goes from q.k to u, one step of it beside another element's
+// next, so that none waits for the one before; then done(r) takes it on.
+template <typename Done>
+__device__ __forceinline__ void tanh_stages(const ScoreForm &f, f32x16_t &x, int from, int to, Done done) {
+#pragma unroll
+  for (int r = from; r < to; r++) {
+    if (r >= 2) done(r - 2);
+    if (r >= 1) x[r - 1] = __builtin_amdgcn_rcpf(-1.0f - x[r - 1]);
+    x[r] = __builtin_amdgcn_exp2f(x[r] * f.a);
+  }
+  if (to == 16) {
+    x[15] = __builtin_amdgcn_rcpf(-1.0f - x[15]);
+    done(14);
+    done(15);
+  }
+}
+// u to a score less its constant term, plus off, and the cap's slope over slope_unit.
+template <int MODE>
+__device__ __forceinline__ float score_of_tanh(const ScoreForm &f, float u, float dist, float off) {
+  float y = __builtin_fmaf(2.0f * f.b, u, off);
+  if constexpr (has_bias(MODE)) y = __builtin_fmaf(-f.slope, __builtin_fabsf(dist), y);
+  return y;
+}
+__device__ __forceinline__ float slope_of_tanh(float u) { return __builtin_fmaf(-u, u, -u); }
+template <int DT, int MODE> constexpr float slope_unit = staged<DT, MODE> ? 4.0f : 1.0f;
 
 // Where a workgroup works: a tile of a document's rows, and a head.
 struct AttnTile {

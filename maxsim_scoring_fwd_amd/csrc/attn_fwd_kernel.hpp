@@ -46,7 +46,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   const char *kp = a.k + t.k + kv * a.k_head, *vp = a.v + t.v + kv * a.v_head;
   const ScoreForm form = score_form<DT, MODE>(a, t.head);
   // Without a bias the last factor of a score and its constant term are left to the exponentials.
-  constexpr bool RAW = MODE == ATTN_PLAIN || (MODE == ATTN_CAP && DT != DT_FP32);
+  constexpr bool RAW = MODE == ATTN_PLAIN || (MODE == ATTN_CAP && staged<DT, MODE>);
   const float post = MODE == ATTN_PLAIN ? form.a : RAW ? 2.0f * form.b : 1.0f;
   const int vis = visible(a, t, iq);
   const int last = t.first + ATTN_ROWS < t.len ? t.first + ATTN_ROWS - 1 : t.len - 1;
@@ -126,28 +126,13 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
       top = __builtin_fmaxf(top, y);
       x[r] = y;
     };
-    if constexpr (has_cap(MODE) && DT != DT_FP32) {
-      // b tanh(x) = b + 2 b / (-1 - e^2x), one of its three parts at an element, so that none waits
-      // for the one before
-      auto tail = [&](int r) {
+    if constexpr (staged<DT, MODE>) {
+      tanh_stages(form, x, from, to, [&](int r) {
         float y = x[r];
         if (has_bias(MODE) && linear) y = __builtin_fmaf(y, 2.0f * form.b, slope_row[r]);
-        else if (has_bias(MODE))
-          y = __builtin_fmaf(-form.slope, __builtin_fabsf(dist0 - (float)acc_row(r)),
-                             __builtin_fmaf(y, 2.0f * form.b, form.c));
+        else if (has_bias(MODE)) y = score_of_tanh<MODE>(form, y, dist0 - (float)acc_row(r), form.c);
         finish(r, y);
-      };
-#pragma unroll
-      for (int r = from; r < to; r++) {
-        if (r >= 2) tail(r - 2);
-        if (r >= 1) x[r - 1] = __builtin_amdgcn_rcpf(-1.0f - x[r - 1]);
-        x[r] = __builtin_amdgcn_exp2f(x[r] * form.a);
-      }
-      if (to == 16) {
-        x[15] = __builtin_amdgcn_rcpf(-1.0f - x[15]);
-        tail(14);
-        tail(15);
-      }
+      });
     } else {
 #pragma unroll
       for (int r = from; r < to; r++) {
