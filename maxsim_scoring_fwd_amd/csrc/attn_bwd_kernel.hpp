@@ -379,9 +379,10 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
       continue;
     }
     for (; i0 < t.len && i0 < some_rows; i0 += BM) tile(form, i0, n, true);
-    // As in the forward: constant places, 145 vector instructions to 128; with dQ's, training on the
-    // pages takes 775 in place of 802 us. Narrower heads have no registers to spare beside a second wave.
-    if constexpr (DP == 128) {
+    // As in the forward: constant places, 145 vector instructions to 128 for heads of 128; with dQ's,
+    // training on the pages takes 775 in place of 802 us, and the backward pass of 16 pages with heads
+    // of 64 347 in place of 359. Heads of 96, and fp32's of 64, have no registers to spare.
+    if constexpr (DP == 128 || (DP == 64 && DT != DT_FP32)) {
       for (; i0 + BM <= t.len && (n & 3); i0 += BM) tile(form, i0, n, false);
       for (; i0 + 4 * BM <= t.len; i0 += 4 * BM) {
 #pragma unroll
@@ -403,14 +404,16 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
                        t.rows - wave0, row_bytes);
 }
 
-// Waves a SIMD: two where 256 registers are enough or nearly so. 16-bit heads of 96 miss that by 2
-// to 20 registers: a backward pass over 256 documents of 20 to 300 tokens and 12 heads takes 397 us
-// with a second wave and 506 without, one over 16 pages of 1060 tokens with cap and bias, which
-// spills six, 666 and 721. Heads of 128 would spill 75 and more.
-template <int DT, int DP> struct DkvWaves { static constexpr int value = DT != DT_FP32 && DP <= 96 ? 2 : 1; };
+// Waves a SIMD: left to itself the compiler takes a few registers more than the 256 of two waves for
+// 16-bit heads of 96 with a cap: 666 us for the backward pass of 16 pages of 1060 tokens with cap and
+// bias, 593 when held to them. The other forms fit or miss by far (heads of 128 would spill 75 and
+// more), and holding them costs 1 to 3%.
+template <int DT, int DP, int MODE> struct DkvWaves {
+  static constexpr int value = DT != DT_FP32 && DP == 96 && has_cap(MODE) ? 2 : 1;
+};
 
 template <int DT, int DP, int MODE, int WHAT>
-__global__ void __launch_bounds__(ATTN_THREADS) __attribute__((amdgpu_waves_per_eu(DkvWaves<DT, DP>::value)))
+__global__ void __launch_bounds__(ATTN_THREADS) __attribute__((amdgpu_waves_per_eu(DkvWaves<DT, DP, MODE>::value)))
 attn_dkv_kernel(const AttnArgs a) {
   __shared__ __align__(256) char lds[8 * 32 * RowLayout<DT, DP>::bytes];  // two rings of four tiles
   __shared__ __align__(256) float stat[4 * 64];
