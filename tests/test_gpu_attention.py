@@ -81,6 +81,7 @@ LENGTHS = {
     "tiny": [1, 2, 3, 0, 1],
     "one": [1],
     "long": [700, 33],
+    "turns": [423, 290, 517],  # whole tiles that begin and end anywhere in a ring of four
     "edges": [31, 32, 33, 63, 64, 65, 127, 128, 129],
 }
 
@@ -107,6 +108,15 @@ CASES = [
     ("edges", 2, 1, 96, "fp32", 130, True, True, 10.0, True),
     ("tiny", 2, 2, 40, "bf16", 3, False, False, 0.0, True),
     ("long", 2, 1, 256, "bf16", 701, True, False, 0.0, False),
+    ("turns", 6, 2, 64, "bf16", 0, False, False, 0.0, False),
+    ("turns", 3, 1, 64, "fp16", 0, True, False, 20.0, False),
+    ("turns", 3, 1, 128, "fp16", 0, True, True, 30.0, True),
+    ("turns", 6, 2, 128, "bf16", 0, False, False, 30.0, False),
+    ("turns", 3, 1, 128, "bf16", 0, False, False, 0.0, False),
+    ("turns", 2, 1, 128, "fp32", 0, False, False, 0.0, True),
+    ("turns", 3, 1, 128, "fp32", 0, True, False, 15.0, False),
+    ("turns", 4, 2, 96, "bf16", 0, False, False, 30.0, True),
+    ("turns", 2, 1, 256, "fp16", 0, False, False, 30.0, True),
 ]
 
 
