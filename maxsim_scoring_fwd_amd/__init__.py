@@ -455,18 +455,25 @@ def _on(t: torch.Tensor, name: str, device) -> int:
     return t.data_ptr()
 
 
-def _ours(t: torch.Tensor, stream) -> torch.Tensor:
-    """A buffer allocated here for work on `stream`: the allocator may not hand it out again
-    before that stream is past it."""
-    if stream is not None and t.is_cuda:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        t.record_stream(s)
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor for work on `stream`. It comes from that stream's own memory: a block that the
+    current stream has given back may still have work queued on it there, which `stream` would not
+    wait for. The caller goes on with it on the current stream: it is not handed out again before
+    that one is past it either."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
     return t
 
 
 def _like(t: torch.Tensor, stream) -> torch.Tensor:
     """A new contiguous tensor like t, for work on `stream`."""
-    return _ours(torch.empty_like(t, memory_format=torch.contiguous_format), stream)
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _new(t.shape, t.dtype, t.device, stream)
 
 
 _ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
@@ -638,7 +645,7 @@ def maxsim_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     else:
         _need(out, "out", q.dtype, shape=q.shape)
     if lse is None:
-        lse = _ours(q.new_empty((heads, rows), dtype=torch.float32), stream)
+        lse = _new((heads, rows), torch.float32, q.device, stream)
     else:
         _need(lse, "lse", torch.float32, shape=(heads, rows))
     _check(lib().maxsim_attention(desc, _dev(out, "out"), _dev(lse, "lse"), _stream(stream)),
@@ -675,8 +682,8 @@ def maxsim_attention_backward(grad_o: torch.Tensor, q: torch.Tensor, k: torch.Te
         return _like(like, stream) if g is None else g
     dq, dk, dv = grad(dq, q, "dq", want_dq), grad(dk, k, "dk", want_dkv), grad(dv, v, "dv", want_dkv)
     if workspace is None:
-        workspace = _ours(q.new_empty(attention_backward_workspace_size(rows, heads),
-                                      dtype=torch.uint8), stream)
+        workspace = _new(attention_backward_workspace_size(rows, heads), torch.uint8, q.device,
+                         stream)
     _check(lib().maxsim_attention_backward(
         desc, _dev(o, "o"), _dev(lse, "lse"), _dev(grad_o, "grad_o"), _dev(dq, "dq"),
         _dev(dk, "dk"), _dev(dv, "dv"), _dev(workspace, "workspace"), workspace.numel(),
@@ -754,12 +761,11 @@ def maxsim_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor |
         raise ValueError("out must hold tensors of the gradients' dtypes and sizes")
     ptrs = array("Q", map(torch.Tensor.data_ptr, each))
     if norm is None:
-        norm = _ours(torch.empty((), dtype=torch.float32, device=grads[0].device), stream)
+        norm = _new((), torch.float32, grads[0].device, stream)
     else:
         _need(norm, "norm", torch.float32, numel=1)
     if workspace is None:
-        workspace = _ours(torch.empty(clip_grad_norm_workspace_size(n), dtype=torch.uint8,
-                                      device=grads[0].device), stream)
+        workspace = _new(clip_grad_norm_workspace_size(n), torch.uint8, grads[0].device, stream)
     else:
         _need(workspace, "workspace", torch.uint8)
     src = ptrs.buffer_info()[0]
