@@ -126,9 +126,23 @@ def _dtype_code(t: torch.Tensor) -> int:
     return _TORCH_DTYPE[t.dtype]
 
 
-def _out(out, n, device, dtype=torch.float32):
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor for work on `stream`. It comes from that stream's own memory: a block that the
+    current stream has given back may still have work queued on it there, which `stream` would not
+    wait for. The caller goes on with it on the current stream: it is not handed out again before
+    that one is past it either."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _out(out, n, device, stream, dtype=torch.float32):
     if out is None:
-        return torch.empty(n, dtype=dtype, device=device)
+        return _new(n, dtype, device, stream)
     _need(out, "out", dtype, numel=n)
     return out
 
@@ -182,7 +196,7 @@ def maxsim_score(Q: torch.Tensor, D: torch.Tensor, doc_offsets: torch.Tensor,
         raise ValueError("maxsim_score needs doc_offsets (use maxsim_score_fixed without)")
     _docs_like(Q, D, doc_offsets)
     n_docs = doc_offsets.numel() - 1
-    out = _out(out, n_docs, Q.device)
+    out = _out(out, n_docs, Q.device, stream)
     _check(lib().maxsim_score(_dev(Q, "Q"), Q.shape[0], _dev(D, "D"),
                               _dev(doc_offsets, "doc_offsets"), n_docs, Q.shape[1],
                               _dtype_code(Q), _dev(out, "out"), _stream(stream)), "maxsim_score")
@@ -197,7 +211,7 @@ def maxsim_score_fixed(Q: torch.Tensor, D: torch.Tensor, doc_lens: torch.Tensor 
     _docs_like(Q, D, None)
     n_docs, nd = D.shape[0], D.shape[1]
     _need(doc_lens, "doc_lens", torch.int32, numel=n_docs)
-    out = _out(out, n_docs, Q.device)
+    out = _out(out, n_docs, Q.device, stream)
     _check(lib().maxsim_score_fixed(_dev(Q, "Q"), Q.shape[0], _dev(D, "D"), n_docs, nd,
                                     _dev(doc_lens, "doc_lens"), Q.shape[1], _dtype_code(Q),
                                     _dev(out, "out"), _stream(stream)), "maxsim_score_fixed")
@@ -222,11 +236,11 @@ def maxsim_score_i8(Q: torch.Tensor, q_scale: torch.Tensor, D: torch.Tensor,
         _need(doc_offsets, "doc_offsets", torch.int64, dim=1)
         n_docs, nd = doc_offsets.numel() - 1, 0
     _need(d_scale, "d_scale", torch.float32, numel=D.numel() // max(d, 1))
-    out = _out(out, n_docs, Q.device)
+    out = _out(out, n_docs, Q.device, stream)
     tm = ta = None
     if with_token_max:
-        tm = torch.empty((n_docs, q_len), dtype=torch.float32, device=Q.device)
-        ta = torch.empty((n_docs, q_len), dtype=torch.int32, device=Q.device)
+        tm = _new((n_docs, q_len), torch.float32, Q.device, stream)
+        ta = _new((n_docs, q_len), torch.int32, Q.device, stream)
     _check(lib().maxsim_score_i8(_dev(Q, "Q"), _dev(q_scale, "q_scale"), q_len, _dev(D, "D"),
                                  _dev(d_scale, "d_scale"), _dev(doc_offsets, "doc_offsets"),
                                  n_docs, nd, d, _dev(out, "out"), _dev(tm, "tok_max"),
@@ -250,13 +264,13 @@ def maxsim_score_argmax(Q: torch.Tensor, D: torch.Tensor, doc_offsets: torch.Ten
     _docs_like(Q, D, doc_offsets)
     q_len, d = Q.shape
     n_docs, nd = _docs(D, doc_offsets)
-    out = _out(out, n_docs, Q.device)
+    out = _out(out, n_docs, Q.device, stream)
     _need(tok_max, "tok_max", torch.float32, shape=(n_docs, q_len))
     _need(tok_arg, "tok_arg", torch.int32, shape=(n_docs, q_len))
     if tok_max is None:
-        tok_max = torch.empty((n_docs, q_len), dtype=torch.float32, device=Q.device)
+        tok_max = _new((n_docs, q_len), torch.float32, Q.device, stream)
     if tok_arg is None:
-        tok_arg = torch.empty((n_docs, q_len), dtype=torch.int32, device=Q.device)
+        tok_arg = _new((n_docs, q_len), torch.int32, Q.device, stream)
     _check(lib().maxsim_score_argmax(_dev(Q, "Q"), q_len, _dev(D, "D"),
                                      _dev(doc_offsets, "doc_offsets"), n_docs, nd, d,
                                      _dtype_code(Q), _dev(out, "out"), _dev(tok_max, "tok_max"),
@@ -275,7 +289,7 @@ def maxsim_score_batch(Q: torch.Tensor, D: torch.Tensor, doc_offsets: torch.Tens
     n_q, q_len, d = Q.shape
     n_docs, nd = _docs(D, doc_offsets)
     if out is None:
-        out = torch.empty((n_q, n_docs), dtype=torch.float32, device=Q.device)
+        out = _new((n_q, n_docs), torch.float32, Q.device, stream)
     _need(out, "out", torch.float32, numel=n_q * n_docs)
     _check(lib().maxsim_score_batch(_dev(Q, "Q"), n_q, q_len, _dev(D, "D"),
                                     _dev(doc_offsets, "doc_offsets"), n_docs, nd, d,
@@ -302,12 +316,12 @@ def maxsim_topk(scores: torch.Tensor, k: int, out_scores=None, out_index=None, w
     _need(out_index, "out_index", torch.int32, numel=rows * k)
     _need(workspace, "workspace", torch.uint8)
     if out_scores is None:
-        out_scores = torch.empty(shape, dtype=torch.float32, device=scores.device)
+        out_scores = _new(shape, torch.float32, scores.device, stream)
     if out_index is None:
-        out_index = torch.empty(shape, dtype=torch.int32, device=scores.device)
+        out_index = _new(shape, torch.int32, scores.device, stream)
     need = topk_workspace_size(n, rows, k)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=scores.device)
+        workspace = _new(need, torch.uint8, scores.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().maxsim_topk(_dev(scores, "scores"), n, rows, k, _dev(out_scores, "out_scores"),
                              _dev(out_index, "out_index"), _dev(workspace, "workspace"), ws_bytes,
@@ -360,9 +374,9 @@ def maxsim_backward(Q: torch.Tensor, D: torch.Tensor, tok_arg: torch.Tensor,
     _need(dD, "dD", grad_dtype, shape=tuple(D.shape))
     _need(workspace, "workspace", torch.uint8)
     if want_dQ and dQ is None:
-        dQ = torch.empty((q_len, d), dtype=grad_dtype, device=Q.device)
+        dQ = _new((q_len, d), grad_dtype, Q.device, stream)
     if want_dD and dD is None:
-        dD = torch.empty(D.shape, dtype=grad_dtype, device=Q.device)
+        dD = _new(D.shape, grad_dtype, Q.device, stream)
     if not want_dQ:
         dQ = None
     if not want_dD:
@@ -371,7 +385,7 @@ def maxsim_backward(Q: torch.Tensor, D: torch.Tensor, tok_arg: torch.Tensor,
     if dQ is not None:
         ws_bytes = backward_workspace_size(q_len, d, n_docs)
         if workspace is None:
-            workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=Q.device)
+            workspace = _new(max(ws_bytes, 16), torch.uint8, Q.device, stream)
         ws_bytes = workspace.numel() * workspace.element_size()
     else:
         workspace = None
@@ -416,7 +430,7 @@ def maxsim_pq_tables(Q: torch.Tensor, C: torch.Tensor, T: torch.Tensor | None = 
     if Q.shape[1] != M * dsub:
         raise ValueError(f"Q has d = {Q.shape[1]}, the codebook M * dsub = {M * dsub}")
     if T is None:
-        T = torch.empty((Q.shape[0], M, K), dtype=torch.float32, device=Q.device)
+        T = _new((Q.shape[0], M, K), torch.float32, Q.device, stream)
     _need(T, "T", torch.float32, shape=(Q.shape[0], M, K))
     _check(lib().maxsim_pq_tables(_dev(Q, "Q"), Q.shape[0], _dtype_code(Q), _dev(C, "C"), M, K,
                                   dsub, _dev(T, "T"), _stream(stream)), "maxsim_pq_tables")
@@ -437,7 +451,7 @@ def maxsim_score_pq(T: torch.Tensor, codes: torch.Tensor, doc_offsets: torch.Ten
     elif nd < 1:
         raise ValueError("fixed documents need nd >= 1")
     n_docs = doc_offsets.numel() - 1 if doc_offsets is not None else codes.shape[0] // max(nd, 1)
-    out = _out(out, n_docs, T.device)
+    out = _out(out, n_docs, T.device, stream)
     _check(lib().maxsim_score_pq(_dev(T, "T"), q_len, M, K, _dev(codes, "codes"),
                                  _dev(doc_offsets, "doc_offsets"), n_docs, nd, _dev(out, "out"),
                                  _stream(stream)), "maxsim_score_pq")
@@ -453,20 +467,6 @@ def _on(t: torch.Tensor, name: str, device) -> int:
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     return t.data_ptr()
-
-
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """A new tensor for work on `stream`. It comes from that stream's own memory: a block that the
-    current stream has given back may still have work queued on it there, which `stream` would not
-    wait for. The caller goes on with it on the current stream: it is not handed out again before
-    that one is past it either."""
-    if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(s):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream())
-    return t
 
 
 def _like(t: torch.Tensor, stream) -> torch.Tensor:

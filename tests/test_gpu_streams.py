@@ -27,9 +27,13 @@ def data():
     freq = (10000.0 ** (-t.arange(D // 2, dtype=t.float64) / (D // 2))).float().cuda()
     long = t.randn(8192, 8192, device="cuda")
     out = t.empty_like(q)
+    Q, docs = do[:32, 0].contiguous(), q[:, 0].contiguous()
+    arg = ms().maxsim_score_argmax(Q, docs, off)[2]
+    scoring = dict(Q=Q, docs=docs, arg=arg, do_scores=t.randn(3, device="cuda"),
+                   book=t.randn(8, 256, D // 8, generator=g).cuda())
     t.mm(long, long)  # whatever its first call prepares
     t.cuda.synchronize()
-    return dict(q=q, k=k, v=v, do=do, off=off, o=o, lse=lse, freq=freq, long=long, out=out)
+    return dict(q=q, k=k, v=v, do=do, off=off, o=o, lse=lse, freq=freq, long=long, out=out, **scoring)
 
 
 def attention(x, stream):
@@ -49,7 +53,34 @@ def clip(x, stream):
     return [ms().maxsim_clip_grad_norm([x["q"]], 0.5, out=[x["out"]], stream=stream)]
 
 
-CALLS = [attention, backward, rotary, clip]
+def score(x, stream):
+    return [ms().maxsim_score(x["Q"], x["docs"], x["off"], stream=stream),
+            ms().maxsim_score_fixed(x["Q"], x["docs"].view(64, 64, D), stream=stream)]
+
+
+def argmax(x, stream):
+    return list(ms().maxsim_score_argmax(x["Q"], x["docs"], x["off"], stream=stream))
+
+
+def batch(x, stream):
+    return [ms().maxsim_score_batch(x["Q"].view(2, 16, D), x["docs"].view(64, 64, D),
+                                    stream=stream)]
+
+
+def score_backward(x, stream):
+    return list(ms().maxsim_backward(x["Q"], x["docs"], x["arg"], x["do_scores"], x["off"],
+                                     stream=stream))
+
+
+def topk(x, stream):
+    return list(ms().maxsim_topk(x["long"][0], 5, stream=stream))
+
+
+def pq(x, stream):
+    return [ms().maxsim_pq_tables(x["Q"], x["book"], stream=stream)]
+
+
+CALLS = [attention, backward, rotary, clip, score, argmax, batch, score_backward, topk, pq]
 
 
 def handle(t, stream, as_int):
