@@ -279,8 +279,8 @@ int maxsim_rotary(const void *x, int64_t n_tokens, int n_heads, int d, int64_t x
  *
  * Layouts: packed, with doc_offsets (int64 [n_docs + 1], not decreasing; entries are clamped
  * to [0, n_tokens]); or fixed, n_docs documents of nd tokens (n_tokens = n_docs * nd) with a
- * nullable doc_lens (int32 [n_docs], clamped to [0, nd]). The contents of rows past doc_lens
- * are never used.
+ * nullable doc_lens (int32 [n_docs], clamped to [0, nd]). The contents of rows past doc_lens, and
+ * of tokens of no document, are never used.
  *   q       [token][n_heads][d]; k, v [token][n_kv_heads][d], all in `dtype`, at any token,
  *           head and (fixed layout) document strides, given in elements; every stride and
  *           address a multiple of 16 bytes; a token's stride at most 16 MiB

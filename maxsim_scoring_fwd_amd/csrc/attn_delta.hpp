@@ -20,8 +20,12 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnArgs a, float
   typedef T vec __attribute__((ext_vector_type(V)));
   const int sub = threadIdx.x & 7;
   const int chunks = a.d / V;
-  auto exists = [&](uint32_t row) {  // rows past a fixed document's length hold anything
-    if (!a.lens) return true;
+  // Rows of no document hold anything: those past a fixed document's length, and those before the
+  // first offset or after the last.
+  const int64_t begin = DT == DT_FP16 && a.offsets ? a.offsets[0] : 0;
+  const int64_t end = DT == DT_FP16 && a.offsets ? a.offsets[a.n_docs] : a.rows;
+  auto exists = [&](uint32_t row) {
+    if (!a.lens) return row >= begin && row < end;
     const uint32_t doc = row / (uint32_t)a.nd;
     return (int)(row - doc * (uint32_t)a.nd) < a.lens[doc];
   };

@@ -347,3 +347,27 @@ def test_unsupported_head_is_an_error():
     with pytest.raises(ms().MaxSimError) as e:  # rows that are not a multiple of 16 bytes apart
         ms().maxsim_attention(q, q, q, t.tensor([0, 4]).cuda())
     assert e.value.status == -4
+
+
+def test_tokens_of_no_document_hold_anything():
+    """A packed buffer whose ends hold no document: whatever lies there, the results are those of
+    clean ends, fp16's small gradients included, whose scale is taken from grad_o and v."""
+    t = T()
+    for dtype in ("bf16", "fp16", "fp32"):
+        q, k, v, do, lay, docs = inputs(13, [140, 3, 150], 4, 2, 64, dt(dtype), 0)
+        off = t.tensor([130, 143, 143, 260], dtype=t.int64)
+        docs = ref.spans(293, offsets=off.tolist())
+        do = (do.float() * 2.0 ** -9).to(dt(dtype))
+        say("case: anything outside the offsets", dtype)
+        clean = run_case(q, k, v, do, dict(doc_offsets=off.cuda()), docs, dt(dtype))
+        for value in (6e4, math.inf, math.nan):
+            dirty = [x.clone() for x in (q, k, v, do)]
+            for x in dirty:
+                x[:130] = value
+                x[260:] = -value
+            kw = dict(doc_offsets=off.cuda())
+            o, lse = ms().maxsim_attention(*dirty[:3], **kw)
+            g = ms().maxsim_attention_backward(dirty[3], *dirty[:3], o, lse, **kw)
+            t.cuda.synchronize()
+            for a, b in zip((o, lse, *g), (clean[0], clean[1], *clean[2])):
+                assert t.equal(a, b), value
