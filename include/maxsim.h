@@ -286,7 +286,9 @@ int maxsim_rotary(const void *x, int64_t n_tokens, int n_heads, int d, int64_t x
  *           address a multiple of 16 bytes; a token's stride at most 16 MiB
  *   d       a multiple of 8, 8 <= d <= MAXSIM_MAX_HEAD (fp32: <= MAXSIM_MAX_HEAD_FP32, else
  *           MAXSIM_ERR_UNSUPPORTED)
- *   scale   > 0
+ *   scale   > 0 and finite
+ *   softcap 0 for none, or > 0 and finite. Above 512 the 16-bit types take a slower tanh, whose
+ *           error is relative to the score; above 2^100 the score is its own capped form
  *   o       [n_tokens][n_heads][d] in `dtype`;  lse fp32 [n_heads][n_tokens]
  * n_tokens == 0 enqueues nothing.
  */

@@ -82,8 +82,10 @@ int fill(const maxsim_attention_desc *s, AttnArgs &a) {
   return set_tiles(a, ATTN_ROWS);
 }
 
-int mode_of(const AttnArgs &a) {
-  return (a.softcap > 0 ? ATTN_CAP : ATTN_PLAIN) + (a.slopes ? ATTN_BIAS : 0);
+int mode_of(const AttnArgs &a, int dtype) {
+  const bool cap = a.softcap > 0 && a.softcap <= ATTN_NO_CAP;
+  if (cap && dtype != MAXSIM_FP32 && a.softcap > ATTN_NEAR_CAP) return ATTN_FAR_CAP;
+  return (cap ? ATTN_CAP : ATTN_PLAIN) + (a.slopes ? ATTN_BIAS : 0);
 }
 
 // One workgroup for every tile of tokens and each of n_heads heads.
@@ -123,7 +125,7 @@ int maxsim_attention(const maxsim_attention_desc *desc, void *o, float *lse, voi
   if (rc != MAXSIM_OK) return rc;
   a.o = (char *)o;
   a.lse = lse;
-  return run(pick(desc->dtype, attn_width(a.d), mode_of(a), attn_fwd_bf16, attn_fwd_fp16, attn_fwd_fp32),
+  return run(pick(desc->dtype, attn_width(a.d), mode_of(a, desc->dtype), attn_fwd_bf16, attn_fwd_fp16, attn_fwd_fp32),
              a, a.heads, (hipStream_t)stream);
 }
 
@@ -169,11 +171,11 @@ int maxsim_attention_backward(const maxsim_attention_desc *desc, const void *o, 
   const void *fn = desc->dtype == MAXSIM_BF16   ? (const void *)attn_delta_kernel<DT_BF16>
                    : desc->dtype == MAXSIM_FP16 ? (const void *)attn_delta_kernel<DT_FP16>
                                                 : (const void *)attn_delta_kernel<DT_FP32>;
-  const int dp = attn_width(a.d), mode = mode_of(a);
+  const int dp = attn_width(a.d), mode = mode_of(a, desc->dtype);
   float unit = has_cap(mode) ? 1.0f : a.scale * LOG2E;
   // what exponents of the weights have beside the product: see ATTN_WEIGHT_SHIFT, ScoreForm::c
   float shift = desc->dtype == MAXSIM_FP16 ? ATTN_WEIGHT_SHIFT : 0.0f;
-  if (has_cap(mode) && desc->dtype != MAXSIM_FP32) shift += a.softcap * LOG2E;
+  if ((mode == ATTN_CAP || mode == ATTN_CAP_BIAS) && desc->dtype != MAXSIM_FP32) shift += a.softcap * LOG2E;
   void *kargs[] = {&a, &stats, &maxima, &unit, &shift};
   if (hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), kargs, 0, st) != hipSuccess) {
     (void)hipGetLastError();

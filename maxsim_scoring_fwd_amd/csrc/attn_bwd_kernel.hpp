@@ -409,7 +409,7 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
 // bias, 593 when held to them. The other forms fit or miss by far (heads of 128 would spill 75 and
 // more), and holding them costs 1 to 3%.
 template <int DT, int DP, int MODE> struct DkvWaves {
-  static constexpr int value = DT != DT_FP32 && DP == 96 && has_cap(MODE) ? 2 : 1;
+  static constexpr int value = DT != DT_FP32 && DP == 96 && staged<DT, MODE> ? 2 : 1;
 };
 
 template <int DT, int DP, int MODE, int WHAT>

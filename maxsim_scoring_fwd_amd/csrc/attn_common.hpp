@@ -21,10 +21,20 @@
 
 namespace maxsim {
 
-// Score forms: plain scale; scale and distance bias; scale and tanh cap; all of them.
-enum { ATTN_PLAIN = 0, ATTN_BIAS = 1, ATTN_CAP = 2, ATTN_CAP_BIAS = 3 };
-constexpr bool has_cap(int mode) { return mode == ATTN_CAP || mode == ATTN_CAP_BIAS; }
-constexpr bool has_bias(int mode) { return mode == ATTN_BIAS || mode == ATTN_CAP_BIAS; }
+// Score forms: plain scale; scale and distance bias; scale and tanh cap; all of them; and 16-bit
+// types' caps above ATTN_NEAR_CAP, with or without a bias (whose slope is 0 then).
+enum { ATTN_PLAIN = 0, ATTN_BIAS = 1, ATTN_CAP = 2, ATTN_CAP_BIAS = 3, ATTN_FAR_CAP = 4 };
+constexpr bool has_cap(int mode) { return mode >= ATTN_CAP; }
+constexpr bool has_bias(int mode) { return mode == ATTN_BIAS || mode >= ATTN_CAP_BIAS; }
+
+// Largest cap of the 16-bit types' tanh in stages (tanh_stages). Its error, up to 2^-22 of the cap
+// whatever the score, is then at most 2^-13 of a weight, a quarter of half a step of fp16. Larger
+// caps take tanhf, whose error is relative to the score, and which takes longer: 16 pages of 1045
+// tokens, 16 heads of 128 on 4, bf16, forward 190 and 257 us, backward 697 and 941.
+constexpr float ATTN_NEAR_CAP = 512.0f;
+// Above this one the capped score is the score itself in 32 bits for all scores below 2^88, and
+// cap * log2 e and scale / cap would leave the range of fp32: no cap is applied.
+constexpr float ATTN_NO_CAP = 1.2676506e30f;  // 2^100
 
 struct AttnArgs {
   const char *q, *k, *v;
@@ -350,6 +360,9 @@ __device__ __forceinline__ f32x16_t mma_tile(const char *tile, const Held<DT, DP
 
 __device__ __forceinline__ int acc_row(int r) { return (r & 3) + 8 * (r >> 2); }
 
+// Whether a tanh goes in stages (tanh_stages).
+template <int DT, int MODE> constexpr bool staged = has_cap(MODE) && MODE != ATTN_FAR_CAP && DT != DT_FP32;
+
 // Constants of the scores, in units of log 2 (the exponentials are powers of two).
 struct ScoreForm {
   float a, b, slope;
@@ -358,21 +371,22 @@ struct ScoreForm {
 template <int DT, int MODE>
 __device__ __forceinline__ ScoreForm score_form(const AttnArgs &a, int head) {
   ScoreForm f;
-  f.slope = has_bias(MODE) ? a.slopes[head] * LOG2E : 0.0f;
+  f.slope = has_bias(MODE) && (MODE != ATTN_FAR_CAP || a.slopes) ? a.slopes[head] * LOG2E : 0.0f;
   f.a = a.scale * LOG2E;
   f.b = f.c = 0.0f;
   if (has_cap(MODE)) {
-    f.a = a.scale / a.softcap * (DT == DT_FP32 ? 1.0f : 2.0f * LOG2E);
+    f.a = a.scale / a.softcap * (staged<DT, MODE> ? 2.0f * LOG2E : 1.0f);
+    f.a = __builtin_fminf(f.a, __FLT_MAX__);  // a tiny cap: 0 stays 0, the rest saturates
     f.b = a.softcap * LOG2E;
-    f.c = DT == DT_FP32 ? 0.0f : f.b;
+    f.c = staged<DT, MODE> ? f.b : 0.0f;
   }
   return f;
 }
 
 constexpr float NOTHING = -0.0f;  // x + NOTHING is x for every x, so the compiler drops the sum
 
-// q.k (x) to a score, plus off; dist: the tokens' distance. keep: the cap's slope (fp32). 16-bit
-// types take their tanh in stages, below.
+// q.k (x) to a score, plus off; dist: the tokens' distance. keep: the cap's slope. 16-bit types
+// take their tanh in stages, below, up to ATTN_NEAR_CAP.
 template <int DT, int MODE>
 __device__ __forceinline__ float score(const ScoreForm &f, float x, float dist, float off, float *keep) {
   float y;
@@ -388,8 +402,7 @@ __device__ __forceinline__ float score(const ScoreForm &f, float x, float dist, 
 }
 
 // tanh x = 1 + 2 u, u = -1 / (1 + e^2x): a reciprocal and an exponential. Near 0 it loses relative
-// accuracy (2^-24 absolute of a score of magnitude softcap), which 16-bit inputs cannot see.
-template <int DT, int MODE> constexpr bool staged = has_cap(MODE) && DT != DT_FP32;
+// accuracy: a score is off by up to 2^-22 of the cap, see ATTN_NEAR_CAP.
 // Elements from .. to - 1 of x: each goes from q.k to u, one step of it beside another element's
 // next, so that none waits for the one before; then done(r) takes it on.
 template <typename Done>

@@ -9,6 +9,7 @@ template <int DP, int WHAT> const void *pick(int mode) {
   case ATTN_PLAIN: return (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_PLAIN, WHAT>;
   case ATTN_BIAS: return (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_BIAS, WHAT>;
   case ATTN_CAP: return (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_CAP, WHAT>;
+  case ATTN_FAR_CAP: return (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_FAR_CAP, WHAT>;
   default: return (const void *)attn_dkv_kernel<DT_FP16, DP, ATTN_CAP_BIAS, WHAT>;
   }
 }

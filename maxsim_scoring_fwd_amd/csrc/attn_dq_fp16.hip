@@ -9,6 +9,7 @@ template <int DP> const void *pick(int mode) {
   case ATTN_PLAIN: return (const void *)attn_dq_kernel<DT_FP16, DP, ATTN_PLAIN>;
   case ATTN_BIAS: return (const void *)attn_dq_kernel<DT_FP16, DP, ATTN_BIAS>;
   case ATTN_CAP: return (const void *)attn_dq_kernel<DT_FP16, DP, ATTN_CAP>;
+  case ATTN_FAR_CAP: return (const void *)attn_dq_kernel<DT_FP16, DP, ATTN_FAR_CAP>;
   default: return (const void *)attn_dq_kernel<DT_FP16, DP, ATTN_CAP_BIAS>;
   }
 }

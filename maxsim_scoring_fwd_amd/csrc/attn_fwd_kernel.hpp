@@ -118,7 +118,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   f32x16_t slope_row;  // slope * key, and the cap's constant term
 #pragma unroll
   for (int r = 0; r < 16; r++) slope_row[r] = __builtin_fmaf(form.slope, (float)acc_row(r), form.c);
-  constexpr bool LINEAR = has_bias(MODE) && !(has_cap(MODE) && DT == DT_FP32);
+  constexpr bool LINEAR = has_bias(MODE) && (!has_cap(MODE) || staged<DT, MODE>);
   auto scores = [&](f32x16_t &x, int n, bool linear, int from, int to) {
     const float dist0 = (float)(i - n * BN - 4 * h);
     const int left = vis - n * BN - 4 * h;

@@ -371,3 +371,39 @@ def test_tokens_of_no_document_hold_anything():
             t.cuda.synchronize()
             for a, b in zip((o, lse, *g), (clean[0], clean[1], *clean[2])):
                 assert t.equal(a, b), value
+
+
+@pytest.mark.parametrize("dtype, d, heads, kv, causal, bias", [
+    ("bf16", 64, 4, 2, False, False), ("bf16", 256, 2, 1, True, True), ("fp16", 96, 3, 1, True, True),
+    ("fp16", 128, 2, 2, False, False), ("fp16", 32, 2, 1, False, True), ("fp32", 128, 2, 1, True, False),
+    ("bf16", 96, 4, 4, False, False), ("fp32", 32, 2, 1, False, True)])
+def test_caps_far_above_the_scores(dtype, d, heads, kv, causal, bias):
+    """A cap far above every score changes the scores by less than they are rounded by, so the
+    results are within the bounds of a call without a cap, however large it is."""
+    t = T()
+    x = inputs(51 + d, [1, 70, 0, 200, 33], heads, kv, d, dt(dtype), 0)
+    q, k, v, do, lay, docs = x
+    slopes = np.float32([2.0 ** (-8.0 * (h + 1) / heads) for h in range(heads)]) if bias else None
+    args = (*(ref.as64(y) for y in (q, k, v)), docs, causal, None)
+    s64 = None if slopes is None else slopes.astype(np.float64)
+    bound = ref.attention(*args, 0.0, s64, None, ref.as64(do), dt(dtype))
+    for cap in (1e3, 1e4, 1e5, 1e6, 1e8, 1e20, 1e35, 3.4e38):
+        say("case: far cap", cap, dtype, d)
+        want = ref.attention(*args, cap, s64, None, ref.as64(do), dt(dtype))
+        kw = dict(lay, causal=causal, softcap=cap, slopes=None if slopes is None else t.tensor(slopes).cuda())
+        o, lse = ms().maxsim_attention(q, k, v, **kw)
+        grads = ms().maxsim_attention_backward(do, q, k, v, o, lse, **kw)
+        t.cuda.synchronize()
+        for name, got in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+            check(name, got, want[name], bound["tol_" + name])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("cap", [1e-42, 511.0, 513.0])
+def test_caps_that_scores_reach(cap, dtype):
+    """Scores of up to twice the cap on either side of the two forms of the tanh, and caps so small
+    that every score saturates."""
+    say("case: reached cap", cap, dtype)
+    q, k, v, do, lay, docs = inputs(61, [90, 40], 2, 1, 64, dt(dtype), 0)
+    q[3] = 0  # scores of exactly 0
+    run_case(q, k, v, do, lay, docs, dt(dtype), cap=cap, scale=40.0 if cap > 1 else None)
