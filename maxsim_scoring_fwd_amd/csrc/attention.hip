@@ -42,7 +42,7 @@ int fill(const maxsim_attention_desc *s, AttnArgs &a) {
   const int eb = elem_bytes(s->dtype);
   if (eb == 0) return MAXSIM_ERR_DTYPE;
   const bool packed = s->doc_offsets != nullptr;
-  if (s->n_docs < 0 || s->n_tokens < 0 || s->n_heads < 1 || s->n_kv_heads < 1 ||
+  if (s->n_docs < 0 || s->n_docs > 0x7fffffff || s->n_tokens < 0 || s->n_heads < 1 || s->n_kv_heads < 1 ||
       s->n_heads % s->n_kv_heads || s->d < 8 || s->d > MAXSIM_MAX_HEAD || s->d % 8)
     return MAXSIM_ERR_SHAPE;
   if (!packed && (s->nd < 0 || s->n_tokens != s->n_docs * s->nd)) return MAXSIM_ERR_SHAPE;
@@ -92,10 +92,14 @@ int mode_of(const AttnArgs &a, int dtype) {
 int run(const void *fn, AttnArgs &a, int n_heads, hipStream_t st) {
   a.per_group.set((uint32_t)(n_heads / a.kv_heads));
   a.per_kv.set(a.slots * a.per_group.d);
+  a.total = a.slots * (uint32_t)n_heads;
   void *kargs[] = {&a};
-  if (hipLaunchKernel(fn, dim3(a.slots * (unsigned)n_heads), dim3(ATTN_THREADS), kargs, 0, st) != hipSuccess) {
-    (void)hipGetLastError();
-    return MAXSIM_ERR_LAUNCH;
+  for (a.base = 0; a.base < a.total; a.base += LAUNCH_MOST) {
+    const uint32_t left = a.total - a.base, grid = left < LAUNCH_MOST ? left : LAUNCH_MOST;
+    if (hipLaunchKernel(fn, dim3(grid), dim3(ATTN_THREADS), kargs, 0, st) != hipSuccess) {
+      (void)hipGetLastError();
+      return MAXSIM_ERR_LAUNCH;
+    }
   }
   return MAXSIM_OK;
 }

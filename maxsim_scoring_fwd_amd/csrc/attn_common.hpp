@@ -55,6 +55,7 @@ struct AttnArgs {
   uint32_t slots;          // tiles along the tokens
   FastDiv tiles_per_doc;   // fixed layout
   FastDiv per_kv, per_group;  // workgroups of a key/value head; of one tile of it
+  uint32_t base, total;    // first workgroup of this launch, workgroups of all launches
   // backward
   const char *dO;          // [rows][heads][d]
   const float2 *stats;     // [heads][rows]: where S and dP start (attn_delta.hpp)
@@ -449,7 +450,7 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t n) {
 
 // False where the tile does not exist.
 __device__ __forceinline__ bool locate(const AttnArgs &a, int rows, AttnTile &t) {
-  const uint32_t id = xcd_order(blockIdx.x, gridDim.x);
+  const uint32_t id = xcd_order(a.base + blockIdx.x, a.total);
   const uint32_t kv = a.per_kv(id), in = id - kv * a.per_kv.d;
   uint32_t slot = a.per_group(in);
   t.head = kv * a.per_group.d + (in - slot * a.per_group.d);

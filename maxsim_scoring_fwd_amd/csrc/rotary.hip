@@ -19,7 +19,7 @@ struct RotaryArgs {
   const char *x;
   char *y;
   int64_t x_token, x_head, y_token, y_head;  // strides in bytes
-  int64_t n_tokens;
+  int64_t first, n_tokens;  // first token of this launch; all tokens
   const float *freq;
   const int64_t *offsets;
   int64_t n_docs;
@@ -48,7 +48,7 @@ template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(ROT_THREADS) rotary_kernel(RotaryArgs a) {
   __shared__ float2 turn[ROT_ANGLES];
   __shared__ int64_t place[64];
-  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+  const int64_t t0 = a.first + (int64_t)blockIdx.x * a.tokens;
   const int n = (int)(a.n_tokens - t0 < a.tokens ? a.n_tokens - t0 : a.tokens);
   const int tid = threadIdx.x;
   if (tid < n) {
@@ -196,17 +196,19 @@ extern "C" int maxsim_rotary(const void *x, int64_t n_tokens, int n_heads, int d
   if (tokens > 64) tokens = 64;
   while (tokens > 1 && tokens * a.per_token > 65535) tokens--;
   a.tokens = (int)(tokens < 1 ? 1 : tokens);
-  const int64_t grid = (n_tokens + a.tokens - 1) / a.tokens;
-  if (grid > 0x7fffffff) return MAXSIM_ERR_SHAPE;
   const bool inter = layout == MAXSIM_ROTARY_INTERLEAVED;
   const void *fn = dtype == MAXSIM_FP32   ? rotary_pick<float>(v, inter)
                    : dtype == MAXSIM_FP16 ? rotary_pick<_Float16>(v, inter)
                                           : rotary_pick<__bf16>(v, inter);
   void *kargs[] = {&a};
-  if (hipLaunchKernel(fn, dim3((unsigned)grid), dim3(ROT_THREADS), kargs, 0,
-                      (hipStream_t)stream) != hipSuccess) {
-    (void)hipGetLastError();
-    return MAXSIM_ERR_LAUNCH;
+  const int64_t most = (int64_t)LAUNCH_MOST * a.tokens;
+  for (a.first = 0; a.first < n_tokens; a.first += most) {
+    const int64_t left = n_tokens - a.first < most ? n_tokens - a.first : most;
+    const unsigned grid = (unsigned)((left + a.tokens - 1) / a.tokens);
+    if (hipLaunchKernel(fn, dim3(grid), dim3(ROT_THREADS), kargs, 0, (hipStream_t)stream) != hipSuccess) {
+      (void)hipGetLastError();
+      return MAXSIM_ERR_LAUNCH;
+    }
   }
   return MAXSIM_OK;
 }

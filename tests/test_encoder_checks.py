@@ -200,3 +200,9 @@ def test_reference_gradients_against_differences(causal, prefix, cap, bias):
             side.append(float((ref.attention(*y, **kw)["o"] * do).sum()))
         got, want = (side[0] - side[1]) / 2e-5, float((g[name] * step).sum())
         assert abs(got - want) <= 1e-7 * max(1.0, float(np.abs(g[name] * step).sum()))
+
+
+def test_attention_c_entry_refuses_more_documents_than_it_counts(L):
+    for n in (1 << 31, (1 << 63) - 1):
+        assert L.maxsim_attention(desc(n_docs=n), P, P, None) == SHAPE
+    assert L.maxsim_attention(desc(n_docs=(1 << 31) - 8), P, P, None) == SHAPE  # times 4 heads
