@@ -528,28 +528,30 @@ def maxsim_rotary(x: torch.Tensor, freq: torch.Tensor, doc_offsets: torch.Tensor
 
 
 class RotaryFunction(torch.autograd.Function):
-    """Differentiable rotary positions; freq and the positions are constants."""
+    """Differentiable rotary positions, to any order; freq and the positions are constants."""
 
     @staticmethod
-    def forward(ctx, x, freq, doc_offsets, positions, layout, mscale):
+    def forward(ctx, x, freq, doc_offsets, positions, layout, mscale, inverse):
         ctx.save_for_backward(freq, doc_offsets, positions)
-        ctx.layout, ctx.mscale = layout, mscale
-        return maxsim_rotary(x, freq, doc_offsets, positions, layout, mscale)
+        ctx.layout, ctx.mscale, ctx.inverse = layout, mscale, inverse
+        return maxsim_rotary(x, freq, doc_offsets, positions, layout, mscale, inverse)
 
     @staticmethod
     def backward(ctx, grad):
         freq, doc_offsets, positions = ctx.saved_tensors
         if grad.stride(2) != 1:
             grad = grad.contiguous()
-        dx = maxsim_rotary(grad, freq, doc_offsets, positions, ctx.layout, ctx.mscale, inverse=True)
-        return dx, None, None, None, None, None
+        # with create_graph the gradient is to be differentiated itself: it is linear in grad
+        turn = RotaryFunction.apply if torch.is_grad_enabled() else maxsim_rotary
+        dx = turn(grad, freq, doc_offsets, positions, ctx.layout, ctx.mscale, not ctx.inverse)
+        return dx, None, None, None, None, None, None
 
 
 def rotary(x: torch.Tensor, freq: torch.Tensor, doc_offsets: torch.Tensor | None = None,
            positions: torch.Tensor | None = None, layout: str = "half",
            mscale: float = 1.0) -> torch.Tensor:
-    """maxsim_rotary that autograd can differentiate with respect to x."""
-    return RotaryFunction.apply(x, freq, doc_offsets, positions, layout, mscale)
+    """maxsim_rotary that autograd can differentiate with respect to x, to any order."""
+    return RotaryFunction.apply(x, freq, doc_offsets, positions, layout, mscale, False)
 
 
 def _attention_refuse(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, slopes):

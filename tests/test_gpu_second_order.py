@@ -1,0 +1,34 @@
+"""Gradients of gradients: right, or an error; a term is never left out without one."""
+import pytest
+
+from gpu_util import ms, say
+
+pytestmark = pytest.mark.gpu
+
+
+def T():
+    import torch
+    return torch
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_gradients_of_gradients(layout):
+    """With y the turned x and R the turning, the gradient of sum(y^2 w) is R^T (2 w R x), and that
+    of its squared length |h|^2 is 2 R^T (2 w R h): three turnings there and three back."""
+    t = T()
+    say("case: rotary twice", layout)
+    g = t.Generator().manual_seed(4)
+    x = t.randn(50, 3, 64, generator=g).cuda().requires_grad_(True)
+    w = t.randn(50, 3, 64, generator=g).cuda()
+    freq = (10000.0 ** (-t.arange(16, dtype=t.float64) / 16)).float().cuda()
+    off = t.tensor([0, 20, 50]).cuda()
+    kw = dict(doc_offsets=off, layout=layout, mscale=1.2)
+    h, = t.autograd.grad((ms().rotary(x, freq, **kw).square() * w).sum(), x, create_graph=True)
+    got, = t.autograd.grad(h.square().sum(), x)
+    turn = lambda z, back: ms().maxsim_rotary(z, freq, inverse=back, **kw)  # noqa: E731
+    lin = lambda z: turn(2 * w * turn(z, False), True)  # noqa: E731
+    x = x.detach()
+    # the same turnings in the same order: some 20 roundings of 32 bits apart, of values that a
+    # turning mixes in pairs
+    want = 2 * lin(lin(x))
+    assert bool(((got - want).abs() <= 1e-5 * want.abs().max()).all())
