@@ -693,8 +693,22 @@ def maxsim_attention_backward(grad_o: torch.Tensor, q: torch.Tensor, k: torch.Te
     return dq, dk, dv
 
 
+class FirstOrderFunction(torch.autograd.Function):
+    """Gradients (what `gradients` returns) that depend on `inputs` and have no derivative here:
+    with create_graph they are part of the graph, and differentiating them is an error."""
+
+    @staticmethod
+    def forward(ctx, name, gradients, *inputs):
+        ctx.name = name
+        return gradients()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"the gradients of {ctx.name} cannot be differentiated again")
+
+
 class AttentionFunction(torch.autograd.Function):
-    """Differentiable attention: gradients of q, k and v; the slopes are constants."""
+    """Differentiable attention: first gradients of q, k and v; the slopes are constants."""
 
     @staticmethod
     def forward(ctx, q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap, slopes, scale):
@@ -707,10 +721,17 @@ class AttentionFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         q, k, v, o, lse, doc_offsets, doc_lens, prefix_lens, slopes = ctx.saved_tensors
-        dq, dk, dv = maxsim_attention_backward(
-            grad.contiguous(), q, k, v, o, lse, doc_offsets, doc_lens, ctx.causal, prefix_lens,
-            ctx.softcap, slopes, ctx.scale, want_dq=ctx.needs_input_grad[0],
-            want_dkv=ctx.needs_input_grad[1] or ctx.needs_input_grad[2])
+        want_dq = ctx.needs_input_grad[0]
+        want_dkv = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
+
+        def gradients():
+            return maxsim_attention_backward(
+                grad.contiguous(), q, k, v, o, lse, doc_offsets, doc_lens, ctx.causal, prefix_lens,
+                ctx.softcap, slopes, ctx.scale, want_dq=want_dq, want_dkv=want_dkv)
+        if torch.is_grad_enabled():
+            dq, dk, dv = FirstOrderFunction.apply("attention", gradients, grad, q, k, v)
+        else:
+            dq, dk, dv = gradients()
         return dq, dk, dv, None, None, None, None, None, None, None
 
 
@@ -719,7 +740,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
               causal: bool = False, prefix_lens: torch.Tensor | None = None,
               softcap: float = 0.0, slopes: torch.Tensor | None = None,
               scale: float | None = None) -> torch.Tensor:
-    """maxsim_attention's o, which autograd can differentiate with respect to q, k and v."""
+    """maxsim_attention's o, which autograd can differentiate with respect to q, k and v, once: a
+    gradient of its gradients is an error."""
     return AttentionFunction.apply(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap,
                                    slopes, scale)
 

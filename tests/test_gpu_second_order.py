@@ -32,3 +32,34 @@ def test_rotary_gradients_of_gradients(layout):
     # turning mixes in pairs
     want = 2 * lin(lin(x))
     assert bool(((got - want).abs() <= 1e-5 * want.abs().max()).all())
+
+
+def first_order(f, *inputs):
+    """f(*inputs), a sum, has right first gradients under create_graph, other terms may be
+    differentiated again beside them, and what depends on the gradients themselves is an error."""
+    t = T()
+    want = t.autograd.grad(f(*inputs), inputs)
+    got = t.autograd.grad(f(*inputs), inputs, create_graph=True)
+    assert all(t.equal(a, b) and b.requires_grad for a, b in zip(want, got))
+    x = inputs[0]
+    both = f(*inputs) + x.float().pow(3).sum()
+    g, = t.autograd.grad(both, x, create_graph=True)
+    with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+        t.autograd.grad(g.float().square().sum(), x)
+    x2 = x.detach().clone().requires_grad_(True)
+    h, = t.autograd.grad(x2.float().pow(3).sum() + f(*inputs), x2, create_graph=True)
+    assert t.equal(t.autograd.grad(h.float().sum(), x2)[0], (6 * x2.float()).to(x2.dtype))
+
+
+def test_attention_gradients_of_gradients_are_an_error():
+    t = T()
+    say("case: attention twice")
+    g = t.Generator().manual_seed(6)
+    q, k, v = (t.randn(60, h, 64, generator=g).cuda().requires_grad_(True) for h in (4, 2, 2))
+    off = t.tensor([0, 25, 60]).cuda()
+    first_order(lambda *x: ms().attention(*x, off).sum(), q, k, v)
+    first_order(lambda *x: (ms().attention(*x, off, causal=True).square()).sum(), q, k, v)
+    # one input alone
+    g, = t.autograd.grad(ms().attention(q, k.detach(), v.detach(), off).sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+        g.sum().backward()
