@@ -397,6 +397,20 @@ def maxsim_backward(Q: torch.Tensor, D: torch.Tensor, tok_arg: torch.Tensor,
     return dQ, dD
 
 
+class FirstOrderFunction(torch.autograd.Function):
+    """Gradients (what `gradients` returns) that depend on `inputs` and have no derivative here:
+    with create_graph they are part of the graph, and differentiating them is an error."""
+
+    @staticmethod
+    def forward(ctx, name, gradients, *inputs):
+        ctx.name = name
+        return gradients()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"the gradients of {ctx.name} cannot be differentiated again")
+
+
 class MaxSimFunction(torch.autograd.Function):
     """Differentiable MaxSim scores: the forward keeps the argmax, the backward turns it
     into dQ and dD with the library's kernels (gradients in the input dtype)."""
@@ -410,14 +424,21 @@ class MaxSimFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad_scores):
         Q, D, doc_offsets, tok_arg = ctx.saved_tensors
-        dQ, dD = maxsim_backward(Q, D, tok_arg, grad_scores.float().contiguous(), doc_offsets,
-                                 want_dQ=ctx.needs_input_grad[0], want_dD=ctx.needs_input_grad[1],
-                                 grad_dtype=Q.dtype)
+        want_dQ, want_dD = ctx.needs_input_grad[:2]
+
+        def gradients():
+            return maxsim_backward(Q, D, tok_arg, grad_scores.float().contiguous(), doc_offsets,
+                                   want_dQ=want_dQ, want_dD=want_dD, grad_dtype=Q.dtype)
+        if torch.is_grad_enabled():
+            dQ, dD = FirstOrderFunction.apply("maxsim", gradients, grad_scores, Q, D)
+        else:
+            dQ, dD = gradients()
         return dQ, dD, None
 
 
 def maxsim(Q: torch.Tensor, D: torch.Tensor, doc_offsets: torch.Tensor | None = None):
-    """Scores [n_docs] that autograd can differentiate with respect to Q and D."""
+    """Scores [n_docs] that autograd can differentiate with respect to Q and D, once: a gradient of
+    the gradients is an error."""
     return MaxSimFunction.apply(Q, D, doc_offsets)
 
 
@@ -691,20 +712,6 @@ def maxsim_attention_backward(grad_o: torch.Tensor, q: torch.Tensor, k: torch.Te
         _dev(dk, "dk"), _dev(dv, "dv"), _dev(workspace, "workspace"), workspace.numel(),
         _stream(stream)), "maxsim_attention_backward")
     return dq, dk, dv
-
-
-class FirstOrderFunction(torch.autograd.Function):
-    """Gradients (what `gradients` returns) that depend on `inputs` and have no derivative here:
-    with create_graph they are part of the graph, and differentiating them is an error."""
-
-    @staticmethod
-    def forward(ctx, name, gradients, *inputs):
-        ctx.name = name
-        return gradients()
-
-    @staticmethod
-    def backward(ctx, *grads):
-        raise RuntimeError(f"the gradients of {ctx.name} cannot be differentiated again")
 
 
 class AttentionFunction(torch.autograd.Function):

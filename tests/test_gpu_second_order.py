@@ -63,3 +63,14 @@ def test_attention_gradients_of_gradients_are_an_error():
     g, = t.autograd.grad(ms().attention(q, k.detach(), v.detach(), off).sum(), q, create_graph=True)
     with pytest.raises(RuntimeError, match="cannot be differentiated again"):
         g.sum().backward()
+
+
+def test_maxsim_gradients_of_gradients_are_an_error():
+    t = T()
+    say("case: maxsim twice")
+    g = t.Generator().manual_seed(8)
+    Q = t.randn(16, 64, generator=g).cuda().requires_grad_(True)
+    D = t.randn(90, 64, generator=g).cuda().requires_grad_(True)
+    off = t.tensor([0, 25, 90]).cuda()
+    first_order(lambda *x: ms().maxsim(*x, off).sum(), Q, D)
+    first_order(lambda *x: ms().maxsim(*x, off).square().sum(), Q, D)
