@@ -481,13 +481,30 @@ def maxsim_score_pq(T: torch.Tensor, codes: torch.Tensor, doc_offsets: torch.Ten
 
 # ---- what an encoder in front of the scoring needs ----
 
-def _on(t: torch.Tensor, name: str, device) -> int:
-    """Address of a device tensor of any strides on `device`."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _on(t: torch.Tensor, name: str, at: int) -> int:
+    """Address of a tensor of any strides on device number `at`."""
+    if at < 0 or t.get_device() != at:
+        if at < 0 or not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{at}")
     return t.data_ptr()
+
+
+def _at(t: torch.Tensor | None, name: str, at: int):
+    """Address of a contiguous tensor on device number `at`, or None."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _on(t, name, at)
+
+
+def _stream_at(stream, at: int) -> int | None:
+    """The stream's handle; launches go to the current device, which has to be number `at`."""
+    now = torch._C._cuda_getDevice()
+    if now != at:
+        raise ValueError(f"the tensors are on cuda:{at}, the current device is cuda:{now}")
+    return _stream(stream)
 
 
 def _like(t: torch.Tensor, stream) -> torch.Tensor:
@@ -539,12 +556,12 @@ def maxsim_rotary(x: torch.Tensor, freq: torch.Tensor, doc_offsets: torch.Tensor
         out_token, out_head, out_entry = out.stride()
         if out_entry != 1:
             raise ValueError("out needs the entries of a head side by side")
-    dev = x.device
+    at = x.get_device()
     _check(lib().maxsim_rotary(
-        _on(x, "x", dev), n, heads, d, x_token, x_head, _TORCH_DTYPE[x.dtype], _dev(freq, "freq"),
+        _on(x, "x", at), n, heads, d, x_token, x_head, _TORCH_DTYPE[x.dtype], _at(freq, "freq", at),
         2 * half, _ROTARY_LAYOUT[layout], mscale, 1 if inverse else 0,
-        _dev(doc_offsets, "doc_offsets"), docs, _dev(positions, "positions"), _on(out, "out", dev),
-        out_token, out_head, _stream(stream)), "maxsim_rotary")
+        _at(doc_offsets, "doc_offsets", at), docs, _at(positions, "positions", at),
+        _on(out, "out", at), out_token, out_head, _stream_at(stream, at)), "maxsim_rotary")
     return out
 
 
@@ -605,7 +622,7 @@ def _attention_refuse(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, slope
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if t.stride(-1) != 1:
             raise ValueError(f"{name} needs the entries of a head side by side")
-        _on(t, name, q.device)
+        _on(t, name, q.get_device())
     raise ValueError("the arguments of the attention do not fit together")
 
 
@@ -614,9 +631,9 @@ def _fits(t, dtype, shape) -> bool:
 
 
 def _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap, slopes, scale):
-    """(the library's description of an attention call, heads, rows), with the checks that the
-    library cannot make: all in one condition, told apart only where it fails."""
-    sq, sk, dt, dev = q.shape, k.shape, q.dtype, q.device
+    """(the library's description of an attention call, heads, rows, device number), with the checks
+    that the library cannot make: all in one condition, told apart only where it fails."""
+    sq, sk, dt, at = q.shape, k.shape, q.dtype, q.get_device()
     tq, tk, tv = q.stride(), k.stride(), v.stride()
     heads, d, kv = sq[-2], sq[-1], sk[-2]
     scale = d ** -0.5 if scale is None else float(scale)
@@ -635,16 +652,16 @@ def _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, softcap
         known = _fits(doc_lens, torch.int32, (docs,))
     if not (known and dt in _TORCH_DTYPE and k.dtype == dt and v.dtype == dt and len(sq) == dim
             and sk == v.shape and sk[:-2] == sq[:-2] and sk[-1] == d and kv and heads % kv == 0
-            and tq[-1] == 1 and tk[-1] == 1 and tv[-1] == 1 and q.is_cuda and k.device == dev
-            and v.device == dev and (prefix_lens is None or causal)
+            and tq[-1] == 1 and tk[-1] == 1 and tv[-1] == 1 and at >= 0 and k.get_device() == at
+            and v.get_device() == at and (prefix_lens is None or causal)
             and _fits(prefix_lens, torch.int32, (docs,)) and _fits(slopes, torch.float32, (heads,))):
         _attention_refuse(q, k, v, doc_offsets, doc_lens, causal, prefix_lens, slopes)
     return _ATTENTION_DESC.pack(
         q.data_ptr(), tq[-3], tq[-2], tq[0], k.data_ptr(), tk[-3], tk[-2], tk[0],
-        v.data_ptr(), tv[-3], tv[-2], tv[0], _dev(doc_offsets, "doc_offsets") or 0,
-        _dev(doc_lens, "doc_lens") or 0, rows, docs, _dev(prefix_lens, "prefix_lens") or 0,
-        _dev(slopes, "slopes") or 0, nd, heads, kv, d, _TORCH_DTYPE[dt], 1 if causal else 0,
-        softcap, scale), heads, rows
+        v.data_ptr(), tv[-3], tv[-2], tv[0], _at(doc_offsets, "doc_offsets", at) or 0,
+        _at(doc_lens, "doc_lens", at) or 0, rows, docs, _at(prefix_lens, "prefix_lens", at) or 0,
+        _at(slopes, "slopes", at) or 0, nd, heads, kv, d, _TORCH_DTYPE[dt], 1 if causal else 0,
+        softcap, scale), heads, rows, at
 
 
 def maxsim_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -661,8 +678,8 @@ def maxsim_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     scores become softcap * tanh(score / softcap); slopes (fp32 [n_heads]): slope * |i - j| is
     taken off; scale: d ** -0.5 unless given. Returns (o shaped like q, lse fp32 [n_heads,
     tokens])."""
-    desc, heads, rows = _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens,
-                                        softcap, slopes, scale)
+    desc, heads, rows, at = _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens,
+                                            softcap, slopes, scale)
     if out is None:
         out = _like(q, stream)
     else:
@@ -671,8 +688,8 @@ def maxsim_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         lse = _new((heads, rows), torch.float32, q.device, stream)
     else:
         _need(lse, "lse", torch.float32, shape=(heads, rows))
-    _check(lib().maxsim_attention(desc, _dev(out, "out"), _dev(lse, "lse"), _stream(stream)),
-           "maxsim_attention")
+    _check(lib().maxsim_attention(desc, _at(out, "out", at), _at(lse, "lse", at),
+                                  _stream_at(stream, at)), "maxsim_attention")
     return out, lse
 
 
@@ -691,8 +708,8 @@ def maxsim_attention_backward(grad_o: torch.Tensor, q: torch.Tensor, k: torch.Te
                               dv=None, workspace=None, stream=None):
     """Gradients (dq, dk, dv) of maxsim_attention from its result's gradient grad_o and its
     outputs o and lse; None for what is not wanted. The other arguments are the forward's."""
-    desc, heads, rows = _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens,
-                                        softcap, slopes, scale)
+    desc, heads, rows, at = _attention_desc(q, k, v, doc_offsets, doc_lens, causal, prefix_lens,
+                                            softcap, slopes, scale)
     _need(grad_o, "grad_o", q.dtype, shape=q.shape)
     _need(o, "o", q.dtype, shape=q.shape)
     _need(lse, "lse", torch.float32, shape=(heads, rows))
@@ -708,9 +725,9 @@ def maxsim_attention_backward(grad_o: torch.Tensor, q: torch.Tensor, k: torch.Te
         workspace = _new(attention_backward_workspace_size(rows, heads), torch.uint8, q.device,
                          stream)
     _check(lib().maxsim_attention_backward(
-        desc, _dev(o, "o"), _dev(lse, "lse"), _dev(grad_o, "grad_o"), _dev(dq, "dq"),
-        _dev(dk, "dk"), _dev(dv, "dv"), _dev(workspace, "workspace"), workspace.numel(),
-        _stream(stream)), "maxsim_attention_backward")
+        desc, _at(o, "o", at), _at(lse, "lse", at), _at(grad_o, "grad_o", at), _at(dq, "dq", at),
+        _at(dk, "dk", at), _at(dv, "dv", at), _at(workspace, "workspace", at), workspace.numel(),
+        _stream_at(stream, at)), "maxsim_attention_backward")
     return dq, dk, dv
 
 
@@ -784,7 +801,7 @@ def maxsim_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor |
     devices = set(map(torch.Tensor.get_device, each))
     if len(devices) != 1 or -1 in devices:
         raise ValueError("every tensor must be a device tensor, all on one device")
-    n = len(grads)
+    n, at = len(grads), devices.pop()
     code = array("i", [_TORCH_DTYPE[t] for t in map(_DTYPE_OF, grads)])
     numel = array("q", map(torch.Tensor.numel, grads))
     if out is not None and (list(map(_DTYPE_OF, outs)) != list(map(_DTYPE_OF, grads)) or
@@ -802,8 +819,8 @@ def maxsim_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor |
     src = ptrs.buffer_info()[0]
     _check(lib().maxsim_clip_grad_norm(
         src, None if out is None else src + 8 * n, numel.buffer_info()[0], code.buffer_info()[0], n,
-        max_norm, _dev(norm, "norm"), _dev(workspace, "workspace"), workspace.numel(),
-        _stream(stream)), "maxsim_clip_grad_norm")
+        max_norm, _at(norm, "norm", at), _at(workspace, "workspace", at), workspace.numel(),
+        _stream_at(stream, at)), "maxsim_clip_grad_norm")
     return norm
 
 

@@ -206,3 +206,59 @@ def test_attention_c_entry_refuses_more_documents_than_it_counts(L):
     for n in (1 << 31, (1 << 63) - 1):
         assert L.maxsim_attention(desc(n_docs=n), P, P, None) == SHAPE
     assert L.maxsim_attention(desc(n_docs=(1 << 31) - 8), P, P, None) == SHAPE  # times 4 heads
+
+
+class On0(torch.Tensor):
+    """A tensor that says it is on device 0; calls that have to be refused never read it."""
+    index = 0
+    is_cuda = True
+
+    def get_device(self):
+        return self.index
+
+
+class On1(On0):
+    index = 1
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0)
+    here, there = (lambda t: t.as_subclass(On0)), (lambda t: t.as_subclass(On1))
+    q = here(Z(10, 4, 64))
+    off = here(OFF)
+    args = dict(doc_offsets=OFF, prefix_lens=torch.zeros(2, dtype=i32), slopes=Z(4, dtype=f32),
+                out=Z(10, 4, 64), lse=Z(4, 10, dtype=f32))
+    for name in args:
+        kw = {n: (there if n == name else here)(t) for n, t in args.items()}
+        refuses(f"{name} is on cuda:1, expected cuda:0", ms.maxsim_attention, q, q, q, causal=True, **kw)
+    refuses("v is on cuda:1", ms.maxsim_attention, q, q, there(q), off)
+    Q = here(Z(2, 5, 4, 64))
+    refuses("doc_lens is on cuda:1", ms.maxsim_attention, Q, Q, Q, doc_lens=there(torch.zeros(2, dtype=i32)))
+    args = dict(grad_o=Z(10, 4, 64), o=Z(10, 4, 64), lse=Z(4, 10, dtype=f32), dq=Z(10, 4, 64),
+                dk=Z(10, 4, 64), dv=Z(10, 4, 64), workspace=torch.zeros(1 << 16, dtype=torch.uint8))
+    for name in args:
+        kw = {n: (there if n == name else here)(t) for n, t in args.items()}
+        refuses(f"{name} is on cuda:1", ms.maxsim_attention_backward, q=q, k=q, v=q, doc_offsets=off, **kw)
+    args = dict(freq=Z(32, dtype=f32), doc_offsets=OFF, out=Z(10, 4, 64))
+    for name in args:
+        kw = {n: (there if n == name else here)(t) for n, t in args.items()}
+        refuses(f"{name} is on cuda:1", ms.maxsim_rotary, q, **kw)
+    refuses("positions is on cuda:1", ms.maxsim_rotary, q, here(Z(32, dtype=f32)),
+            positions=there(torch.zeros(10, dtype=i32)), out=q)
+    # all of them on one device that is not the current one
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    refuses("the current device is cuda:1", ms.maxsim_rotary, q, here(Z(32, dtype=f32)), out=q)
+    refuses("the current device is cuda:1", ms.maxsim_attention, q, q, q, off, out=here(Z(10, 4, 64)),
+            lse=here(Z(4, 10, dtype=f32)))
+
+
+@pytest.mark.gpu
+def test_clipping_on_another_device_is_refused(monkeypatch):
+    g = [torch.ones(5, device="cuda")]
+    norm, ws = torch.zeros((), device="cuda"), torch.zeros(1 << 14, dtype=torch.uint8, device="cuda")
+    for name, t in (("norm", norm), ("workspace", ws)):
+        kw = dict(dict(norm=norm, workspace=ws), **{name: t.as_subclass(On1)})
+        refuses(f"{name} is on cuda:1", ms.maxsim_clip_grad_norm, g, 1.0, **kw)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    refuses("the current device is cuda:1", ms.maxsim_clip_grad_norm, g, 1.0, norm=norm, workspace=ws)
