@@ -782,7 +782,8 @@ def maxsim_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor |
                           workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Scales a list of gradients (contiguous bf16, fp16 or fp32 tensors, mixed as they come) by
     min(1, max_norm / (norm + 1e-6)), norm their global 2-norm. In place, or into the list `out`
-    of tensors like them. Returns the norm before clipping, an fp32 scalar on the device."""
+    of tensors like them. Entries of None (parameters without a gradient) are left out. Returns the
+    norm before clipping, an fp32 scalar on the device."""
     grads = list(grads)
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
@@ -794,8 +795,17 @@ def maxsim_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor |
         raise ValueError(f"max_norm must not be negative, got {max_norm}")
     each = grads if out is None else grads + outs
     # whole lists at a time: an encoder has hundreds of gradients
-    if not set(map(_DTYPE_OF, each)) <= _TORCH_DTYPE.keys():
-        raise ValueError(f"unsupported dtype among {set(map(_DTYPE_OF, each))}")
+    try:
+        dtypes = set(map(_DTYPE_OF, each))
+    except AttributeError:  # some entry is no tensor: those without a gradient are left out
+        given = [(g, o) for g, o in zip(grads, outs) if g is not None]
+        if len(given) == len(grads):
+            raise ValueError("every entry must be a tensor, or None among the gradients") from None
+        return maxsim_clip_grad_norm([g for g, _ in given], max_norm,
+                                     None if out is None else [o for _, o in given], norm, workspace,
+                                     stream)
+    if not dtypes <= _TORCH_DTYPE.keys():
+        raise ValueError(f"unsupported dtype among {dtypes}")
     if not all(map(torch.Tensor.is_contiguous, each)):
         raise ValueError("every tensor must be contiguous")
     devices = set(map(torch.Tensor.get_device, each))

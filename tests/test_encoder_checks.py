@@ -208,6 +208,15 @@ def test_attention_c_entry_refuses_more_documents_than_it_counts(L):
     assert L.maxsim_attention(desc(n_docs=(1 << 31) - 8), P, P, None) == SHAPE  # times 4 heads
 
 
+def test_clip_binding_refuses_what_is_no_tensor():
+    clip = ms.maxsim_clip_grad_norm
+    refuses("at least one", clip, [None, None], 1.0)
+    refuses("must be a tensor", clip, [Z(3), 2.0], 1.0)
+    refuses("must be a tensor", clip, [Z(3), Z(4)], 1.0, out=[Z(3), None])
+    refuses("must be a tensor", clip, [Z(3), None, 2.0], 1.0)
+    refuses("device tensor", clip, [Z(3), None], 1.0)
+
+
 class On0(torch.Tensor):
     """A tensor that says it is on device 0; calls that have to be refused never read it."""
     index = 0

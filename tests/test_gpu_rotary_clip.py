@@ -213,3 +213,20 @@ def test_clip_same_bits_graph_and_stream():
         graph.replay()
         t.cuda.synchronize()
         assert t.equal(norm, want_norm) and all(t.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_clip_leaves_out_parameters_without_a_gradient():
+    t = T()
+    gs = grads([(70, 33), (5,), (300,)], ["bf16", "fp32", "fp16"])
+    outs = [t.empty_like(x) for x in gs]
+    want_norm = ms().maxsim_clip_grad_norm(gs, 1e-3, out=outs)
+    kept = t.full((4,), 7.0, device="cuda")
+    got = [t.empty_like(x) for x in gs]
+    say("case: clip with None")
+    norm = ms().maxsim_clip_grad_norm([gs[0], None, *gs[1:], None], 1e-3,
+                                      out=[got[0], kept, *got[1:], None])
+    assert t.equal(norm, want_norm) and all(t.equal(a, b) for a, b in zip(got, outs))
+    assert bool((kept == 7.0).all())
+    inplace = [x.clone() for x in gs]
+    assert t.equal(ms().maxsim_clip_grad_norm([None, *inplace], 1e-3), want_norm)
+    assert all(t.equal(a, b) for a, b in zip(inplace, outs))
