@@ -133,3 +133,20 @@ def test_results_read_on_the_current_stream_are_kept(data, call):
     t.cuda.synchronize()
     assert all(t.equal(a, b) for a, b in zip(kept, want))
     assert all(t.equal(a, b) for a, b in zip(again, want))
+
+
+def test_current_stream_without_torchs_private_functions(data, monkeypatch):
+    t = T()
+    say("case: public stream functions")
+    side = t.cuda.Stream()
+    for stream in (t.cuda.current_stream(), side):
+        with t.cuda.stream(stream):
+            handles = []
+            for raw in (True, False):
+                monkeypatch.setattr(ms(), "_RAW_STREAMS", raw)
+                handles.append((ms()._current_device(), ms()._stream(None)))
+            assert handles[0] == handles[1] == (t.cuda.current_device(), stream.cuda_stream)
+    want = rotary(data, None)
+    t.cuda.synchronize()
+    monkeypatch.setattr(ms(), "_RAW_STREAMS", False)
+    assert t.equal(rotary(data, None)[0], want[0]) and t.equal(attention(data, None)[0], data["o"])
