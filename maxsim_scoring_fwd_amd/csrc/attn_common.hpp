@@ -268,7 +268,8 @@ template <int DT, int DP> struct Carry {
     // wherever it needs one. It has no result in registers, and tile_barrier waits for it.
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
-                 : "s"(uniform(to + p * 16)), "v"(at[i]), "s"(uniform((int64_t)base)));
+                 : "s"(uniform(to + p * 16)), "v"(at[i]), "s"(uniform((int64_t)base))
+                 : "m0");
   }
   __device__ __forceinline__ void all(int to, int wave) const {
 #pragma unroll
