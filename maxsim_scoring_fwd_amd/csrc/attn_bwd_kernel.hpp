@@ -233,10 +233,9 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
     if (wave == 0) {
       const int last = cq.left < BM ? cq.left - 1 : BM - 1, row = lane & 31;
       const uint32_t at = (uint32_t)(row < last ? row : last) * 8 + h * 4;
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+      asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2"
                    :
-                   : "s"(uniform(lds_s + (n & 3) * 256)), "v"(at), "s"(uniform((int64_t)next_stats))
-                   : "m0");
+                   : "{m0}"(uniform(lds_s + (n & 3) * 256)), "v"(at), "s"(uniform((int64_t)next_stats)));
     }
   };
   start_head();

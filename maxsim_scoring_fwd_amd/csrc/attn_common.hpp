@@ -266,10 +266,9 @@ template <int DT, int DP> struct Carry {
     if (total % ATTN_THREADS != 0 && p >= total) return;
     // The instruction itself: beside the builtin the compiler waits for every LDS read in flight
     // wherever it needs one. It has no result in registers, and tile_barrier waits for it.
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
-                 : "s"(uniform(to + p * 16)), "v"(at[i]), "s"(uniform((int64_t)base))
-                 : "m0");
+                 : "{m0}"(uniform(to + p * 16)), "v"(at[i]), "s"(uniform((int64_t)base)));
   }
   __device__ __forceinline__ void all(int to, int wave) const {
 #pragma unroll
