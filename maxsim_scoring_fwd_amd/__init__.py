@@ -493,11 +493,11 @@ def maxsim_score_pq(T: torch.Tensor, codes: torch.Tensor, doc_offsets: torch.Ten
 
 def _on(t: torch.Tensor, name: str, at: int) -> int:
     """Address of a tensor of any strides on device number `at`."""
-    if at < 0 or t.get_device() != at:
-        if at < 0 or not t.is_cuda:
-            raise ValueError(f"{name} must be a device tensor")
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{at}")
-    return t.data_ptr()
+    if t.get_device() == at >= 0:
+        return t.data_ptr()
+    if at < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{at}")
 
 
 def _at(t: torch.Tensor | None, name: str, at: int):
@@ -506,7 +506,7 @@ def _at(t: torch.Tensor | None, name: str, at: int):
         return None
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return _on(t, name, at)
+    return t.data_ptr() if t.get_device() == at >= 0 else _on(t, name, at)
 
 
 def _stream_at(stream, at: int) -> int | None:
@@ -514,6 +514,8 @@ def _stream_at(stream, at: int) -> int | None:
     now = _current_device()
     if now != at:
         raise ValueError(f"the tensors are on cuda:{at}, the current device is cuda:{now}")
+    if stream is None and _RAW_STREAMS:
+        return torch._C._cuda_getCurrentRawStream(at)
     return _stream(stream)
 
 
@@ -695,7 +697,8 @@ def maxsim_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     else:
         _need(out, "out", q.dtype, shape=q.shape)
     if lse is None:
-        lse = _new((heads, rows), torch.float32, q.device, stream)
+        lse = q.new_empty((heads, rows), dtype=torch.float32) if stream is None else \
+            _new((heads, rows), torch.float32, q.device, stream)
     else:
         _need(lse, "lse", torch.float32, shape=(heads, rows))
     _check(lib().maxsim_attention(desc, _at(out, "out", at), _at(lse, "lse", at),
@@ -732,8 +735,9 @@ def maxsim_attention_backward(grad_o: torch.Tensor, q: torch.Tensor, k: torch.Te
         return _like(like, stream) if g is None else g
     dq, dk, dv = grad(dq, q, "dq", want_dq), grad(dk, k, "dk", want_dkv), grad(dv, v, "dv", want_dkv)
     if workspace is None:
-        workspace = _new(attention_backward_workspace_size(rows, heads), torch.uint8, q.device,
-                         stream)
+        size = attention_backward_workspace_size(rows, heads)
+        workspace = q.new_empty(size, dtype=torch.uint8) if stream is None else \
+            _new(size, torch.uint8, q.device, stream)
     _check(lib().maxsim_attention_backward(
         desc, _at(o, "o", at), _at(lse, "lse", at), _at(grad_o, "grad_o", at), _at(dq, "dq", at),
         _at(dk, "dk", at), _at(dv, "dv", at), _at(workspace, "workspace", at), workspace.numel(),
