@@ -405,9 +405,10 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnArgs &a, const AttnTile 
 }
 
 // Waves a SIMD: left to itself the compiler takes a few registers more than the 256 of two waves for
-// 16-bit heads of 96 with a cap: 666 us for the backward pass of 16 pages of 1060 tokens with cap and
-// bias, 593 when held to them. The other forms fit or miss by far (heads of 128 would spill 75 and
-// more), and holding them costs 1 to 3%.
+// 16-bit heads of 96 with a cap. Held to them, fp16 with cap and bias spills one; dK / dV of 16 pages
+// of 1060 tokens with 8 heads take 210 us so and 247 with one wave, of 256 documents of 300 with 12
+// heads 575 and 818, of two of 4000 with 16 on 4 580 and 568. The other forms fit or miss by far
+// (heads of 128 would spill 75 and more), and holding them costs 1 to 3%.
 template <int DT, int DP, int MODE> struct DkvWaves {
   static constexpr int value = DT != DT_FP32 && DP == 96 && staged<DT, MODE> ? 2 : 1;
 };

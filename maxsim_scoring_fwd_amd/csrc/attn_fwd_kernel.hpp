@@ -25,10 +25,17 @@
 
 namespace maxsim {
 
-// Waves a SIMD that the registers are divided for: as many as spill nothing. The passages above take
-// 282 us with four and 310 with three, the long documents 890 with two and 1095 with one.
+// Waves a SIMD that the registers are divided for: as many as spill nothing, and no more than have
+// room for their tiles in LDS (a workgroup's four waves are on four SIMDs), where fewer registers
+// would buy nothing. The passages above take 282 us with four and 310 with three, the long documents
+// 890 with two and 1095 with one. fp32 heads of 64, two by their LDS, take 514 to 524 us for 16 pages
+// of 1045 tokens and 12 heads, held to the registers of three or not.
 template <int DT, int DP, int MODE> struct FwdWaves {
-  static constexpr int value = DP == 256 ? 1 : DP >= 96 ? 2 : DT != DT_FP32 && MODE == ATTN_PLAIN ? 4 : 3;
+  static constexpr int lds = 8 * 32 * RowLayout<DT, DP>::bytes;  // four tiles of K, four of V
+  static constexpr int room = 160 * 1024 / lds;
+  static constexpr int most = DP == 256 ? 1 : DP >= 96 ? 2 : DT != DT_FP32 && MODE == ATTN_PLAIN ? 4 : 3;
+  static constexpr int value = room < most ? room : most;
+  static_assert(value >= 1 && value * lds <= 160 * 1024, "waves without room for their tiles");
 };
 
 template <int DT, int DP, int MODE>
@@ -217,7 +224,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnArgs &a, const AttnTile 
   // Four at a time the rings' places are constants, and the reads' addresses need no additions: 844
   // in place of 891 us for the long documents. Heads of 256 gain nothing (their rings pass the 64 KB
   // that a read's offset reaches: 551 and 545 us for the pages), and with four waves it would spill.
-  if constexpr (FwdWaves<DT, DP, MODE>::value == 2 || FwdWaves<DT, DP, MODE>::value == 3) {
+  if constexpr (DP != 256 && FwdWaves<DT, DP, MODE>::value != 4) {
     for (; n + 4 < linear_tiles; n += 4) {
 #pragma unroll
       for (int e = 0; e < 4; e++) step(n + e, e, true);
@@ -253,7 +260,7 @@ template <int DT, int DP, int MODE>
 __global__ void __launch_bounds__(ATTN_THREADS)
 __attribute__((amdgpu_waves_per_eu(FwdWaves<DT, DP, MODE>::value, FwdWaves<DT, DP, MODE>::value)))
 attn_fwd_kernel(const AttnArgs a) {
-  __shared__ __align__(256) char lds[8 * 32 * RowLayout<DT, DP>::bytes];  // four tiles of K, four of V
+  __shared__ __align__(256) char lds[FwdWaves<DT, DP, MODE>::lds];
   AttnTile t;
   if (!locate(a, ATTN_ROWS, t)) return;
   if (t.first < t.len) {
