@@ -1,4 +1,5 @@
-"""Calls with more work than one launch may have threads (2^32): 2^24 workgroups and more."""
+"""Calls with more work than one launch may have threads (2^32), and tensors of more than 2^31
+elements."""
 import numpy as np
 import pytest
 
@@ -59,3 +60,22 @@ def test_rotary_over_a_billion_tokens():
     # every token is there: turning keeps a pair's length (0.9014) up to two roundings of it
     for part in y.split(2 ** 27):
         assert bool(((part.float().square().sum(-1).sqrt() - 0.9014).abs() < 0.01).all())
+
+
+def test_clipping_of_two_billion_elements():
+    """All of one value but the last, whose square is as large as the others' together."""
+    import torch as t
+    n = 2 ** 31 + 777
+    x = t.ones(n, dtype=t.bfloat16, device="cuda")
+    x[-1] = 2.0 ** 15.5  # rounded to 46336
+    last = float(x[-1])
+    norm = (n - 1 + last ** 2) ** 0.5
+    say("case: clipping of", n, "elements")
+    got = ms().maxsim_clip_grad_norm([x], 1.0)
+    assert abs(float(got) - norm) <= 2 * ref.U32 * norm
+    want = t.tensor([1 / (norm + 1e-6), last / (norm + 1e-6)], dtype=t.float64)
+    # the factor and the product round to 32 bits, the result to its type
+    tol = (ref.HALF_STEP[t.bfloat16] + 3 * ref.U32) * want
+    assert bool(((x[:-1].amin().double().cpu() - want[0]).abs() <= tol[0]))
+    assert bool(((x[:-1].amax().double().cpu() - want[0]).abs() <= tol[0]))
+    assert bool(((x[-1].double().cpu() - want[1]).abs() <= tol[1]))
