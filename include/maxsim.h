@@ -290,6 +290,9 @@ int maxsim_rotary(const void *x, int64_t n_tokens, int n_heads, int d, int64_t x
  *   softcap 0 for none, or > 0 and finite. Above 512 the 16-bit types take a slower tanh, whose
  *           error is relative to the score; above 2^100 the score is its own capped form
  *   o       [n_tokens][n_heads][d] in `dtype`;  lse fp32 [n_heads][n_tokens]
+ * Documents' tokens hold finite values (a weight of 0 does not hide an infinity or a NaN), and
+ * scores (scale * <q_i, k_j>) stay within 2^20: they are 32 bits wide, so a weight is off by some
+ * 2^-22 of its score, in the backward, which takes it from lse, too.
  * n_tokens and n_docs stay below 2^31, and so do (n_tokens / 128 + n_docs + 2) * n_heads (fixed
  * layout: n_docs * ceil(nd / 128) * n_heads). n_tokens == 0 enqueues nothing.
  */

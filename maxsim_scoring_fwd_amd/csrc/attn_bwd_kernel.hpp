@@ -7,10 +7,11 @@
 // Sums are 32 bits wide; P and dS are rounded to the inputs' type as operands of the last three
 // products (fp16 after a power of two that keeps dS in range).
 //
-// Measured (one MI355X): 512 documents of 20 to 300 tokens, 12 heads of 64, bf16: dQ 189 us, dK / dV
-// 285 us, 0.63 and 0.76 GB, 3.3 and 2.7 TB/s; 16 pages of about 1045 tokens, 16 heads of 128 on 4,
-// with cap: dQ 248 us, dK / dV 346 us, 425 and 405 TFLOP/s. Instructions bound the pages (32 matrix
-// instructions and 255 others a tile of dK / dV, one wave a SIMD), waits the short documents.
+// Measured (one MI355X): 512 documents of 20 to 300 tokens, 12 heads of 64, bf16: dQ 179 us, dK / dV
+// 265 us, 0.63 and 0.76 GB, 3.5 and 2.9 TB/s; 16 pages of about 1045 tokens, 16 heads of 128 on 4,
+// with cap: dQ 234 us, dK / dV 304 us, 900 and 920 TFLOP/s, 41 and 38% of what the matrix cores do
+// at the clock of these passes. Instructions bound the pages (32 matrix instructions and 255 others a
+// tile of dK / dV, one wave a SIMD), waits the short documents.
 #pragma once
 
 #include "attn_common.hpp"

@@ -10,10 +10,10 @@
 // maximum. K is therefore used one tile ahead of V. Each has a ring of four tiles in LDS, which
 // makes one barrier every two tiles enough.
 //
-// Measured (one MI355X): 1024 documents of 20 to 300 tokens, 12 heads of 64, bf16: 283 us, 1.0 GB in
-// and out, 3.5 TB/s, 1.4 times a plain copy of it. 48 pages of about 1045 tokens, 8 heads of 256 on
-// one shared, cap: 555 us, 760 TFLOP/s. Two causal documents of 5003 to 8191 tokens, 32 heads of 128
-// on 8, fp16: 850 us, 890 TFLOP/s, where a large library product reaches 1260. No single unit bounds
+// Measured (one MI355X): 1024 documents of 20 to 300 tokens, 12 heads of 64, bf16: 284 us, 1.0 GB in
+// and out, 3.6 TB/s, 1.4 times a plain copy of it. 48 pages of about 1045 tokens, 8 heads of 256 on
+// one shared, cap: 554 us, 760 TFLOP/s. Two causal documents of 5003 to 8191 tokens, 32 heads of 128
+// on 8, fp16: 841 to 863 us by the GPU, 875 to 897 TFLOP/s, where a large library product reaches 1260. No single unit bounds
 // the long ones: before the reads' addresses became constants, of 889 us 791 were left without LDS
 // reads, 664 without the softmax, 808 without fetches. Matrix cores are busy 48% and vector units 62%
 // of the cycles, at a clock that the load pulls to 1.7 GHz. Short documents spend half a wave's time

@@ -1,8 +1,8 @@
 // Rotary positions (include/maxsim.h, maxsim_rotary): each pair (a, b) of a head is turned by
 // the angle position * freq. One read and one write of the tensor bound it: the angles of a
 // token (rot / 2 of them) are computed once and shared by all its heads. Measured (one MI355X):
-// 204 us for 1.08 GB of 40 fp16 heads of 128 (5.3 TB/s; a 2 GiB copy runs at 4.9), 83 us for 396 MB
-// of 16 fp32 heads of 96 with positions given (4.8 TB/s); 3.4 us for one query's 24 heads.
+// 207 us for 1.08 GB of 40 fp16 heads of 128 (5.2 TB/s; a 2 GiB copy runs at 4.9), 84 us for 396 MB
+// of 16 fp32 heads of 96 with positions given (4.7 TB/s); 3.5 us for one query's 24 heads.
 #include <hip/hip_runtime.h>
 
 #include "doc_lookup.hpp"
