@@ -6,6 +6,7 @@
 #include "attn_delta.hpp"
 #include "attn_dispatch.hpp"
 #include "host_common.hpp"
+#include "launch_parts.hpp"
 
 using namespace maxsim;
 

@@ -16,10 +16,6 @@ namespace maxsim {
 
 inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// Most workgroups of 256 threads in one launch: a grid has fewer than 2^32 threads along x. Larger
-// grids go in several launches. A multiple of 8, so that each begins on the first XCD.
-constexpr uint32_t LAUNCH_MOST = 1u << 23;
-
 inline int elem_bytes(int dtype) {
   switch (dtype) {
   case MAXSIM_BF16:

@@ -7,6 +7,7 @@
 
 #include "doc_lookup.hpp"
 #include "host_common.hpp"
+#include "launch_parts.hpp"
 
 using namespace maxsim;
 
