@@ -177,6 +177,38 @@ int maxsim_score_i8(const int8_t *Q, const float *q_scale, int q_len, const int8
                     int d, float *out, float *tok_max, int32_t *tok_arg, void *stream);
 
 /*
+ * Microscaled 4-bit vectors: 32 entries of a row share a power of two, 2^k, kept as the byte
+ * k + 127, and each is a 4-bit code: a sign (the highest bit) and one of 0, 1/2, 1, 3/2, 2, 3, 4, 6,
+ * times 2^k. k = floor(log2 of the block's largest absolute entry) - 2, from -127 up; an entry goes
+ * to the nearest, ties to the even code, and to 6 where it is larger. A block of zeros has byte 0; one
+ * with a NaN or an infinity has byte 255 (not a number) and codes 0.
+ *   x       [n_rows][d] in `dtype`, d a multiple of 32 in [MAXSIM_MIN_D, MAXSIM_MAX_D]
+ *   codes   uint8 [n_rows][d / 2], two entries a byte, the first in the low half; 16-byte aligned
+ *   scales  uint8 [n_rows][d / 32]
+ * maxsim_dequantize_mx4 gives the values that they stand for, in `dtype`.
+ */
+int maxsim_quantize_mx4(const void *x, int64_t n_rows, int d, int dtype, uint8_t *codes,
+                        uint8_t *scales, void *stream);
+
+int maxsim_dequantize_mx4(const uint8_t *codes, const uint8_t *scales, int64_t n_rows, int d,
+                          int dtype, void *x, void *stream);
+
+/*
+ * Scores of microscaled 4-bit queries and documents, out[b] = sum_i max_j <q_i, d_j>, on the scaled
+ * matrix instructions: the products are exact and summed in fp32.
+ *   Q        codes [q_len][d / 2], q_scale [q_len][d / 32]
+ *   D        codes [tokens][d / 2], d_scale [tokens][d / 32]
+ *   doc_offsets  nullable: CSR as in maxsim_score; NULL means fixed documents of nd tokens each, of
+ *            which doc_lens (nullable int32 [n_docs], clamped to [0, nd]) count
+ *   d        a multiple of 32 in [MAXSIM_MIN_D, MAXSIM_MAX_D]; queries of more than 64 tokens:
+ *            q_len in whole 16s times the row's bytes (d / 2, up to 64, 128, 256 or 512) at most
+ *            64 KiB, else MAXSIM_ERR_UNSUPPORTED
+ */
+int maxsim_score_mx4(const uint8_t *Q, const uint8_t *q_scale, int q_len, const uint8_t *D,
+                     const uint8_t *d_scale, const int64_t *doc_offsets, int64_t n_docs, int nd,
+                     const int32_t *doc_lens, int d, float *out, void *stream);
+
+/*
  * Per-query product-quantisation distance tables (TileMaxSim deep reading,
  * section 2 item (3)):  T[i][m][k] = sum_{t < dsub} Q[i][m*dsub + t] * C[m][k][t]
  *   Q  [q_len][M*dsub] in `dtype`
@@ -349,6 +381,112 @@ int maxsim_clip_grad_norm(const void *const *grads, void *const *outs, const int
                           void *workspace, size_t workspace_bytes, void *stream);
 
 size_t maxsim_clip_grad_norm_workspace_size(int n_tensors);
+
+/*
+ * Dropout: out = x / (1 - p) where an entry is kept, else 0. The mask comes from a counter-based
+ * generator and is made again wherever it is needed; it is never stored, and the gradient of x is
+ * the same call on the gradient of out.
+ *   Generator: Philox4x32 with 7 rounds; the key is rng[0] (64 bits), the counter (block, block
+ *   >> 32, rng[1], call), 32 bits each. Entry i of x has bits 16 (i % 8) .. 16 (i % 8) + 15 of the
+ *   128 bits of block i / 8, as a number u, and is kept where u >= t, t = p * 65536 rounded to the
+ *   nearest whole number (ties to even). What is kept is multiplied by 65536 / (65536 - t), in fp32,
+ *   and rounded once. A dropped entry is 0 whatever it held.
+ *   x, out  [n] in `dtype`, densely packed; out may be x itself
+ *   p       0 <= p <= 1
+ *   rng     int64 [2] on the DEVICE: key and step (its low 32 bits); a program that replays a
+ *           captured step raises the step between replays
+ *   call    >= 0: tells the calls of one step apart
+ */
+int maxsim_dropout(const void *x, int64_t n, int dtype, double p, const int64_t *rng, int call,
+                   void *out, void *stream);
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *     h = residual + dropout(x), rounded to `dtype`     (either may be left out)
+ *     y = h * rstd * weight,  rstd = 1 / sqrt(mean of h^2 + eps)
+ * The norm is of h as it is handed on, so that the backward, which reads h, differentiates just
+ * this function. The mean is held in 32 bits: rows whose squares sum past its range get y = 0.
+ *   x, residual  [n_rows][d] in `dtype`, rows at strides given in entries, entries of a row side by
+ *            side; any d up to MAXSIM_MAX_NORM (else MAXSIM_ERR_UNSUPPORTED), any alignment of the
+ *            type; residual nullable; n_rows <= 2^31
+ *   weight   [d], in weight_dtype: `dtype` or MAXSIM_FP32
+ *   dropout, rng, call  as for maxsim_dropout, with the 8 entries of a block side by side in a row:
+ *            entry e of row r is number e % 8 of block r * ceil(d / 8) + e / 8. rng may be NULL
+ *            where dropout is 0
+ *   y        [n_rows][d] in `dtype`, densely packed; may be x itself where that is
+ *   h        as y; needed with a residual or dropout, else nullable; may be the residual
+ *   rstd     nullable fp32 [n_rows], for the backward
+ */
+#define MAXSIM_MAX_NORM 8192
+
+int maxsim_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                    int64_t n_rows, int d, int dtype, const void *weight, int weight_dtype, float eps,
+                    double dropout, const int64_t *rng, int call, void *y, void *h, float *rstd,
+                    void *stream);
+
+/*
+ * maxsim_rms_norm with y in 8 bits, as maxsim_score_i8 takes it: scale[row] = max |y| / 127 and
+ * codes = y / scale to the nearest (ties to even). A row of zeros has scale 0 and codes 0; one with a
+ * NaN or an infinity has such a scale, and codes 0.
+ */
+int maxsim_rms_norm_i8(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                       int64_t n_rows, int d, int dtype, const void *weight, int weight_dtype,
+                       float eps, int8_t *codes, float *scale, void *h, void *stream);
+
+/*
+ * Gradients of maxsim_rms_norm, from those of y and (nullable: none) of h. With n = h * rstd and
+ * g = grad_y * weight:
+ *     dresidual = rstd * (g - n * mean of g * n) + grad_h
+ *     dx        = dropout's share of it (the same where there is no dropout)
+ *     dweight   = sum of grad_y * n over the rows, in weight_dtype
+ * each nullable; sums are fp32. h is the forward's (x where it had neither residual nor dropout) at
+ * a row stride in entries; the other tensors are densely packed.
+ *   workspace  4-byte aligned, maxsim_rms_norm_backward_workspace_size bytes, with dweight
+ * With n_rows == 0 dweight is set to zero.
+ */
+int maxsim_rms_norm_backward(const void *grad_y, const void *grad_h, const void *h, int64_t h_stride,
+                             int64_t n_rows, int d, int dtype, const void *weight, int weight_dtype,
+                             const float *rstd, double dropout, const int64_t *rng, int call, void *dx,
+                             void *dresidual, void *dweight, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+size_t maxsim_rms_norm_backward_workspace_size(int64_t n_rows, int d);
+
+/*
+ * Softmax cross entropy of a linear layer over a vocabulary, without keeping its logits:
+ *     z_v = scale * <w_v, h_i>,   lse[i] = log sum_v exp(z_v),   loss[i] = lse[i] - z_label[i]
+ * A row whose label lies outside [0, vocab) is left out: loss 0, lse -inf, no gradient; what it holds
+ * is never used, and it costs nothing beside its label (masked-token training labels few rows).
+ * Products run on the matrix cores with fp32 sums; statistics are fp32.
+ *   h       [n_rows][d], w [vocab][d] in `dtype`, densely packed, 16-byte aligned, finite;
+ *           d * element bytes a multiple of 16, d <= 16384; n_rows and vocab below 2^31
+ *   labels  int64 [n_rows]
+ *   scale   > 0 and finite
+ *   loss, lse  fp32 [n_rows]
+ *   workspace  16-byte aligned, maxsim_linear_cross_entropy_workspace_size bytes
+ */
+int maxsim_linear_cross_entropy(const void *h, const void *w, const int64_t *labels, int64_t n_rows,
+                                int64_t vocab, int d, int dtype, float scale, float *loss, float *lse,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+size_t maxsim_linear_cross_entropy_workspace_size(int64_t n_rows, int64_t vocab, int d, int dtype);
+
+/*
+ * Gradients of maxsim_linear_cross_entropy from those of its losses (fp32 [n_rows]) and the forward's
+ * lse: dh [n_rows][d] and dw [vocab][d] in `dtype`, each nullable. Piece by piece of the vocabulary,
+ *     P = (exp(z - lse) - [v is the label]) * grad_loss * scale,   dh = P w,   dw = P^T h
+ * with P, one piece of it, in the workspace, rounded to `dtype` (fp16: scaled by a power of two
+ * taken from the largest gradient first). Sums are fp32, each result is rounded once. A piece of P
+ * takes 256 MiB at most, or 256 columns. With n_rows == 0 dw is set to zero.
+ */
+int maxsim_linear_cross_entropy_backward(const float *grad_loss, const void *h, const void *w,
+                                         const int64_t *labels, const float *lse, int64_t n_rows,
+                                         int64_t vocab, int d, int dtype, float scale, void *dh,
+                                         void *dw, void *workspace, size_t workspace_bytes,
+                                         void *stream);
+
+size_t maxsim_linear_cross_entropy_backward_workspace_size(int64_t n_rows, int64_t vocab, int d,
+                                                           int dtype);
 
 /* Static description of a status code. */
 const char *maxsim_status_string(int status);

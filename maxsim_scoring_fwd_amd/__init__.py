@@ -9,8 +9,9 @@ gfx950 device is present, the calls raise.
     score(q_i, d_j) summed:  out[b] = sum_i max_j <q_i, d_j>
 
 Beside the scoring it has what the encoder in front of it needs, on the same document
-layouts: attention within documents, rotary positions, and the clipping of gradients by their
-global norm.
+layouts: attention within documents, rotary positions, the norm with the residual's addition,
+dropout, the cross entropy over a vocabulary, and the clipping of gradients by their global norm;
+and for the index 8-bit and 4-bit vectors.
 """
 from __future__ import annotations
 
@@ -84,13 +85,36 @@ def lib() -> ctypes.CDLL:
         L.maxsim_clip_grad_norm.argtypes = [vp, vp, vp, vp, i32, f64, vp, vp, sz, vp]
         L.maxsim_clip_grad_norm_workspace_size.argtypes = [i32]
         L.maxsim_clip_grad_norm_workspace_size.restype = sz
+        L.maxsim_dropout.argtypes = [vp, i64, i32, f64, vp, i32, vp, vp]
+        L.maxsim_rms_norm.argtypes = [vp, i64, vp, i64, i64, i32, i32, vp, i32, f32, f64, vp, i32,
+                                      vp, vp, vp, vp]
+        L.maxsim_rms_norm_i8.argtypes = [vp, i64, vp, i64, i64, i32, i32, vp, i32, f32, vp, vp, vp,
+                                         vp]
+        L.maxsim_rms_norm_backward.argtypes = [vp, vp, vp, i64, i64, i32, i32, vp, i32, vp, f64, vp,
+                                               i32, vp, vp, vp, vp, sz, vp]
+        L.maxsim_linear_cross_entropy.argtypes = [vp, vp, vp, i64, i64, i32, i32, f32, vp, vp, vp,
+                                                  sz, vp]
+        L.maxsim_linear_cross_entropy_backward.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, i32,
+                                                           f32, vp, vp, vp, sz, vp]
+        L.maxsim_rms_norm_backward_workspace_size.argtypes = [i64, i32]
+        L.maxsim_linear_cross_entropy_workspace_size.argtypes = [i64, i64, i32, i32]
+        L.maxsim_linear_cross_entropy_backward_workspace_size.argtypes = [i64, i64, i32, i32]
+        for f in ("rms_norm_backward", "linear_cross_entropy", "linear_cross_entropy_backward"):
+            getattr(L, f"maxsim_{f}_workspace_size").restype = sz
+        L.maxsim_quantize_mx4.argtypes = [vp, i64, i32, i32, vp, vp, vp]
+        L.maxsim_dequantize_mx4.argtypes = [vp, vp, i64, i32, i32, vp, vp]
+        L.maxsim_score_mx4.argtypes = [vp, vp, i32, vp, vp, vp, i64, i32, vp, i32, vp, vp]
         L.maxsim_status_string.argtypes = [i32]
         L.maxsim_status_string.restype = ctypes.c_char_p
         L.maxsim_version.argtypes = []
         for f in ("maxsim_score", "maxsim_score_fixed", "maxsim_score_i8", "maxsim_pq_tables",
                   "maxsim_score_pq", "maxsim_version", "maxsim_score_argmax", "maxsim_backward",
                   "maxsim_score_batch", "maxsim_topk", "maxsim_topk_no_alloc", "maxsim_rotary",
-                  "maxsim_attention", "maxsim_attention_backward", "maxsim_clip_grad_norm"):
+                  "maxsim_attention", "maxsim_attention_backward", "maxsim_clip_grad_norm",
+                  "maxsim_dropout", "maxsim_rms_norm", "maxsim_rms_norm_i8",
+                  "maxsim_rms_norm_backward", "maxsim_linear_cross_entropy",
+                  "maxsim_linear_cross_entropy_backward", "maxsim_quantize_mx4",
+                  "maxsim_dequantize_mx4", "maxsim_score_mx4"):
             getattr(L, f).restype = ctypes.c_int
         _lib_handle = L
     return _lib_handle
@@ -784,6 +808,357 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                                    slopes, scale)
 
 
+def _rows(t: torch.Tensor, name: str):
+    """(rows, entries between them) of t [..., d] whose rows lie at one distance from each other."""
+    d = t.shape[-1]
+    if t.is_contiguous():
+        return t.numel() // d, d
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, d)
+        except RuntimeError:
+            raise ValueError(f"{name} needs rows at one distance from each other") from None
+    if t.stride(1) != 1 and d > 1:
+        raise ValueError(f"{name} needs the entries of a row side by side")
+    return t.shape[0], t.stride(0)
+
+
+def _chance(dropout: float, rng, call: int) -> float:
+    """dropout as a number, with the checks of what belongs to it."""
+    dropout = float(dropout)
+    if not 0 <= dropout <= 1:
+        raise ValueError(f"dropout must lie in [0, 1], got {dropout}")
+    if dropout and rng is None:
+        raise ValueError("dropout needs rng")
+    _need(rng, "rng", torch.int64, shape=(2,))
+    if not 0 <= call < 1 << 31:
+        raise ValueError(f"call must lie in [0, 2^31), got {call}")
+    return dropout
+
+
+def maxsim_dropout(x: torch.Tensor, dropout: float, rng: torch.Tensor, call: int = 0,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """x / (1 - dropout) where an entry is kept, else 0; x contiguous, of any shape. The mask is made
+    from rng (int64 [2] on the device: key and step) and call, and never stored: the same call on a
+    gradient of the result is the gradient of x. dropout counts in steps of 2^-16. Raise the step
+    from one training step to the next (in place, in a captured one: between replays), and give each
+    place that drops a call of its own. out may be x itself."""
+    _need(x, "x", _FLOAT_STORAGE)
+    if rng is None:
+        raise ValueError("dropout needs rng")
+    dropout = _chance(dropout, rng, call)
+    if out is None:
+        out = _like(x, stream)
+    else:
+        _need(out, "out", x.dtype, shape=x.shape)
+    at = x.get_device()
+    _check(lib().maxsim_dropout(_at(x, "x", at), x.numel(), _TORCH_DTYPE[x.dtype], dropout,
+                                _at(rng, "rng", at), call, _at(out, "out", at),
+                                _stream_at(stream, at)), "maxsim_dropout")
+    return out
+
+
+class DropoutFunction(torch.autograd.Function):
+    """Differentiable dropout, to any order: it is linear in x."""
+
+    @staticmethod
+    def forward(ctx, x, dropout, rng, call):
+        ctx.save_for_backward(rng)
+        ctx.dropout, ctx.call = dropout, call
+        return maxsim_dropout(x, dropout, rng, call)
+
+    @staticmethod
+    def backward(ctx, grad):
+        drop = DropoutFunction.apply if torch.is_grad_enabled() else maxsim_dropout
+        return drop(grad.contiguous(), ctx.dropout, ctx.saved_tensors[0], ctx.call), None, None, None
+
+
+def dropout(x: torch.Tensor, dropout: float, rng: torch.Tensor, call: int = 0) -> torch.Tensor:
+    """maxsim_dropout that autograd can differentiate with respect to x, to any order. Raise the step
+    in rng after the backward, which makes the same mask again."""
+    return DropoutFunction.apply(x, dropout, rng, call)
+
+
+def _norm_args(x, weight, residual, eps):
+    """(rows, row stride of x, of the residual) of a norm, checked."""
+    _need(x, "x", _FLOAT_STORAGE)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x needs rows of at least one entry")
+    _need(weight, "weight", (x.dtype, torch.float32), shape=x.shape[-1:])
+    if not eps >= 0:
+        raise ValueError(f"eps must not be negative, got {eps}")
+    n, stride = _rows(x, "x")
+    if residual is None:
+        return n, stride, 0
+    _need(residual, "residual", x.dtype, shape=x.shape)
+    return n, stride, _rows(residual, "residual")[1]
+
+
+def maxsim_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                    eps: float = 1e-6, dropout: float = 0.0, rng: torch.Tensor | None = None,
+                    call: int = 0, out=None, out_h=None, rstd=None, stream=None):
+    """h = residual + dropout(x), rounded to x's type (both optional: else h is x), and its root-mean-
+    square norm y = h * rstd * weight. x [..., d] and residual alike, rows at one distance from each
+    other; weight [d] in x's type or fp32; dropout, rng and call as in maxsim_dropout. Returns (y, h,
+    rstd fp32 [...]). out may be x, and out_h the residual, where those are contiguous."""
+    n, stride, r_stride = _norm_args(x, weight, residual, eps)
+    dropout = _chance(dropout, rng, call)
+    dt, at = x.dtype, x.get_device()
+    if out is None:
+        out = _like(x, stream)
+    else:
+        _need(out, "out", dt, shape=x.shape)
+    h = None
+    if residual is not None or dropout:
+        h = _like(x, stream) if out_h is None else out_h
+        _need(h, "out_h", dt, shape=x.shape)
+    elif out_h is not None:
+        raise ValueError("out_h needs a residual or dropout: h is x itself")
+    if rstd is None:
+        rstd = _new(x.shape[:-1], torch.float32, x.device, stream)
+    else:
+        _need(rstd, "rstd", torch.float32, shape=x.shape[:-1])
+    _check(lib().maxsim_rms_norm(
+        _on(x, "x", at), stride, None if residual is None else _on(residual, "residual", at),
+        r_stride, n, x.shape[-1], _TORCH_DTYPE[dt], _at(weight, "weight", at),
+        _TORCH_DTYPE[weight.dtype], eps, dropout, _at(rng, "rng", at), call, _at(out, "out", at),
+        _at(h, "out_h", at), _at(rstd, "rstd", at), _stream_at(stream, at)), "maxsim_rms_norm")
+    return out, x if h is None else h, rstd
+
+
+def maxsim_rms_norm_i8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                       eps: float = 1e-6, out=None, scale=None, out_h=None, stream=None):
+    """maxsim_rms_norm with y in 8 bits, for maxsim_score_i8: returns (codes int8 shaped like x,
+    scale fp32 [...], h) with y = codes * scale, scale a row's largest |y| / 127."""
+    n, stride, r_stride = _norm_args(x, weight, residual, eps)
+    dt, at = x.dtype, x.get_device()
+    _need(out, "out", torch.int8, shape=x.shape)
+    _need(scale, "scale", torch.float32, shape=x.shape[:-1])
+    if out is None:
+        out = _new(x.shape, torch.int8, x.device, stream)
+    if scale is None:
+        scale = _new(x.shape[:-1], torch.float32, x.device, stream)
+    h = None
+    if residual is not None:
+        h = _like(x, stream) if out_h is None else out_h
+        _need(h, "out_h", dt, shape=x.shape)
+    elif out_h is not None:
+        raise ValueError("out_h needs a residual: h is x itself")
+    _check(lib().maxsim_rms_norm_i8(
+        _on(x, "x", at), stride, None if residual is None else _on(residual, "residual", at),
+        r_stride, n, x.shape[-1], _TORCH_DTYPE[dt], _at(weight, "weight", at),
+        _TORCH_DTYPE[weight.dtype], eps, _at(out, "out", at), _at(scale, "scale", at),
+        _at(h, "out_h", at), _stream_at(stream, at)), "maxsim_rms_norm_i8")
+    return out, scale, x if h is None else h
+
+
+def rms_norm_backward_workspace_size(n_rows: int, d: int) -> int:
+    """Bytes of workspace maxsim_rms_norm_backward needs for the weight's gradient."""
+    return int(lib().maxsim_rms_norm_backward_workspace_size(n_rows, d))
+
+
+def maxsim_rms_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                             rstd: torch.Tensor, grad_h: torch.Tensor | None = None,
+                             dropout: float = 0.0, rng: torch.Tensor | None = None, call: int = 0,
+                             want_dx: bool = True, want_dresidual: bool = True,
+                             want_dweight: bool = True, dx=None, dresidual=None, dweight=None,
+                             workspace=None, stream=None):
+    """Gradients (dx, dresidual, dweight) of maxsim_rms_norm, from those of its y and (optionally) h
+    and its outputs h and rstd; None for what is not wanted. Without dropout dx and dresidual are
+    one tensor, unless two are given."""
+    n, stride, _ = _norm_args(h, weight, None, 0.0)
+    dropout = _chance(dropout, rng, call)
+    dt, at, d = h.dtype, h.get_device(), h.shape[-1]
+    _need(grad_y, "grad_y", dt, shape=h.shape)
+    _need(grad_h, "grad_h", dt, shape=h.shape)
+    _need(rstd, "rstd", torch.float32, shape=h.shape[:-1])
+    _need(dx, "dx", dt, shape=h.shape)
+    _need(dresidual, "dresidual", dt, shape=h.shape)
+    _need(dweight, "dweight", weight.dtype, shape=weight.shape)
+    _need(workspace, "workspace", torch.uint8)
+    one = want_dx and want_dresidual and not dropout and (dx is None or dresidual is None)
+    if one:
+        dx = dresidual = dx if dx is not None else dresidual
+    if want_dresidual and dresidual is None:
+        dresidual = _like(h, stream)
+    if one:
+        dx = dresidual
+    elif want_dx and dx is None:
+        dx = _like(h, stream)
+    if want_dweight and dweight is None:
+        dweight = _new(weight.shape, weight.dtype, h.device, stream)
+    if want_dweight and workspace is None:
+        workspace = _new(rms_norm_backward_workspace_size(n, d), torch.uint8, h.device, stream)
+    dx = dx if want_dx else None
+    dresidual = dresidual if want_dresidual else None
+    dweight = dweight if want_dweight else None
+    _check(lib().maxsim_rms_norm_backward(
+        _at(grad_y, "grad_y", at), _at(grad_h, "grad_h", at), _on(h, "h", at), stride, n, d,
+        _TORCH_DTYPE[dt], _at(weight, "weight", at), _TORCH_DTYPE[weight.dtype],
+        _at(rstd, "rstd", at), dropout, _at(rng, "rng", at), call,
+        None if one else _at(dx, "dx", at), _at(dresidual, "dresidual", at),
+        _at(dweight, "dweight", at), _at(workspace, "workspace", at),
+        0 if workspace is None else workspace.numel(), _stream_at(stream, at)),
+        "maxsim_rms_norm_backward")
+    return dx, dresidual, dweight
+
+
+class RmsNormFunction(torch.autograd.Function):
+    """Differentiable norm: first gradients of x, the residual and the weight."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps, dropout, rng, call):
+        y, h, rstd = maxsim_rms_norm(x, weight, residual, eps, dropout, rng, call)
+        ctx.save_for_backward(h, weight, rstd, rng)
+        ctx.dropout, ctx.call = dropout, call
+        ctx.set_materialize_grads(False)
+        return y if h is x else (y, h)
+
+    @staticmethod
+    def backward(ctx, grad_y, grad_h=None):
+        h, weight, rstd, rng = ctx.saved_tensors
+        if grad_y is None and grad_h is None:
+            return None, None, None, None, None, None, None
+        want_dx, want_dw, want_dr = ctx.needs_input_grad[:3]
+
+        def gradients():
+            dy = torch.zeros_like(h) if grad_y is None else grad_y
+            return maxsim_rms_norm_backward(
+                dy.contiguous(), h, weight, rstd, None if grad_h is None else grad_h.contiguous(),
+                ctx.dropout, rng, ctx.call, want_dx, want_dr, want_dw)
+
+        def apart():
+            dx, dr, dw = gradients()
+            return dx, dr.clone() if dr is dx and dr is not None else dr, dw
+        if torch.is_grad_enabled():
+            dx, dr, dw = FirstOrderFunction.apply("rms_norm", apart, grad_y, grad_h, h, weight)
+        else:
+            dx, dr, dw = gradients()
+        return dx, dw, dr, None, None, None, None
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+             eps: float = 1e-6, dropout: float = 0.0, rng: torch.Tensor | None = None, call: int = 0):
+    """maxsim_rms_norm's (y, h), which autograd can differentiate with respect to x, weight and
+    residual, once: a gradient of its gradients is an error. Raise the step in rng after the
+    backward, which makes the same mask again."""
+    if residual is None and not dropout:
+        return RmsNormFunction.apply(x, weight, None, eps, 0.0, None, 0), x
+    return RmsNormFunction.apply(x, weight, residual, eps, dropout, rng, call)
+
+
+def linear_cross_entropy_workspace_size(n_rows: int, vocab: int, d: int, dtype: torch.dtype) -> int:
+    """Bytes of workspace maxsim_linear_cross_entropy needs."""
+    return int(lib().maxsim_linear_cross_entropy_workspace_size(n_rows, vocab, d, _TORCH_DTYPE[dtype]))
+
+
+def linear_cross_entropy_backward_workspace_size(n_rows: int, vocab: int, d: int,
+                                                 dtype: torch.dtype) -> int:
+    """Bytes of workspace maxsim_linear_cross_entropy_backward needs."""
+    return int(lib().maxsim_linear_cross_entropy_backward_workspace_size(n_rows, vocab, d,
+                                                                         _TORCH_DTYPE[dtype]))
+
+
+def _loss_args(h, w, labels, scale):
+    _need(h, "h", _FLOAT_STORAGE, dim=2)
+    _need(w, "w", h.dtype, dim=2)
+    if w.shape[1] != h.shape[1]:
+        raise ValueError(f"w has d = {w.shape[1]}, h has d = {h.shape[1]}")
+    if w.shape[0] < 1:
+        raise ValueError("w needs at least one row")
+    _need(labels, "labels", torch.int64, shape=h.shape[:1])
+    scale = float(scale)
+    if not 0 < scale < math.inf:
+        raise ValueError(f"scale must be positive and finite, got {scale}")
+    return h.shape[0], w.shape[0], h.shape[1], scale, h.get_device()
+
+
+def maxsim_linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, labels: torch.Tensor,
+                                scale: float = 1.0, loss=None, lse=None, workspace=None, stream=None):
+    """Softmax cross entropy of the logits scale * h w^T over a vocabulary, which are not kept. h
+    [n_rows, d], w [vocab, d] (same type; rows of whole 16 bytes), labels int64 [n_rows]; a row whose
+    label lies outside the vocabulary is left out: loss 0, lse -inf, and no work. Returns (loss, lse)
+    fp32 [n_rows]."""
+    n, vocab, d, scale, at = _loss_args(h, w, labels, scale)
+    _need(loss, "loss", torch.float32, shape=(n,))
+    _need(lse, "lse", torch.float32, shape=(n,))
+    _need(workspace, "workspace", torch.uint8)
+    if loss is None:
+        loss = _new((n,), torch.float32, h.device, stream)
+    if lse is None:
+        lse = _new((n,), torch.float32, h.device, stream)
+    if workspace is None:
+        workspace = _new(linear_cross_entropy_workspace_size(n, vocab, d, h.dtype), torch.uint8,
+                         h.device, stream)
+    _check(lib().maxsim_linear_cross_entropy(
+        _at(h, "h", at), _at(w, "w", at), _at(labels, "labels", at), n, vocab, d,
+        _TORCH_DTYPE[h.dtype], scale, _at(loss, "loss", at), _at(lse, "lse", at),
+        _at(workspace, "workspace", at), workspace.numel(), _stream_at(stream, at)),
+        "maxsim_linear_cross_entropy")
+    return loss, lse
+
+
+def maxsim_linear_cross_entropy_backward(grad_loss: torch.Tensor, h: torch.Tensor, w: torch.Tensor,
+                                         labels: torch.Tensor, lse: torch.Tensor, scale: float = 1.0,
+                                         want_dh: bool = True, want_dw: bool = True, dh=None, dw=None,
+                                         workspace=None, stream=None):
+    """Gradients (dh, dw) of maxsim_linear_cross_entropy's losses from theirs (fp32 [n_rows]) and its
+    lse; None for what is not wanted. The vocabulary goes in pieces, of which the workspace holds
+    one."""
+    n, vocab, d, scale, at = _loss_args(h, w, labels, scale)
+    _need(grad_loss, "grad_loss", torch.float32, shape=(n,))
+    _need(lse, "lse", torch.float32, shape=(n,))
+    _need(dh, "dh", h.dtype, shape=h.shape)
+    _need(dw, "dw", w.dtype, shape=w.shape)
+    _need(workspace, "workspace", torch.uint8)
+    if want_dh and dh is None:
+        dh = _like(h, stream)
+    if want_dw and dw is None:
+        dw = _like(w, stream)
+    if workspace is None:
+        workspace = _new(linear_cross_entropy_backward_workspace_size(n, vocab, d, h.dtype),
+                         torch.uint8, h.device, stream)
+    dh, dw = dh if want_dh else None, dw if want_dw else None
+    _check(lib().maxsim_linear_cross_entropy_backward(
+        _at(grad_loss, "grad_loss", at), _at(h, "h", at), _at(w, "w", at), _at(labels, "labels", at),
+        _at(lse, "lse", at), n, vocab, d, _TORCH_DTYPE[h.dtype], scale, _at(dh, "dh", at),
+        _at(dw, "dw", at), _at(workspace, "workspace", at), workspace.numel(),
+        _stream_at(stream, at)), "maxsim_linear_cross_entropy_backward")
+    return dh, dw
+
+
+class LinearCrossEntropyFunction(torch.autograd.Function):
+    """Differentiable cross entropy: first gradients of h and w."""
+
+    @staticmethod
+    def forward(ctx, h, w, labels, scale):
+        loss, lse = maxsim_linear_cross_entropy(h, w, labels, scale)
+        ctx.save_for_backward(h, w, labels, lse)
+        ctx.scale = scale
+        return loss
+
+    @staticmethod
+    def backward(ctx, grad):
+        h, w, labels, lse = ctx.saved_tensors
+        want_dh, want_dw = ctx.needs_input_grad[:2]
+
+        def gradients():
+            return maxsim_linear_cross_entropy_backward(grad.contiguous(), h, w, labels, lse,
+                                                        ctx.scale, want_dh, want_dw)
+        if torch.is_grad_enabled():
+            dh, dw = FirstOrderFunction.apply("linear_cross_entropy", gradients, grad, h, w)
+        else:
+            dh, dw = gradients()
+        return dh, dw, None, None
+
+
+def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, labels: torch.Tensor,
+                         scale: float = 1.0) -> torch.Tensor:
+    """maxsim_linear_cross_entropy's losses [n_rows], which autograd can differentiate with respect to
+    h and w, once: a gradient of its gradients is an error."""
+    return LinearCrossEntropyFunction.apply(h, w, labels, scale)
+
+
 def clip_grad_norm_workspace_size(n_tensors: int) -> int:
     """Bytes of workspace maxsim_clip_grad_norm needs."""
     return int(lib().maxsim_clip_grad_norm_workspace_size(n_tensors))
@@ -846,6 +1221,81 @@ def maxsim_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor |
         max_norm, _at(norm, "norm", at), _at(workspace, "workspace", at), workspace.numel(),
         _stream_at(stream, at)), "maxsim_clip_grad_norm")
     return norm
+
+
+def maxsim_quantize_mx4(x: torch.Tensor, codes=None, scales=None, stream=None):
+    """Token vectors x [..., d] in microscaled 4-bit floating point: 32 entries share a power of two,
+    each is a sign and one of 0, 1/2, 1, 3/2, 2, 3, 4, 6. Returns (codes uint8 [..., d / 2], two
+    entries a byte, the first in the low half; scales uint8 [..., d / 32], exponents plus 127)."""
+    _need(x, "x", _FLOAT_STORAGE)
+    d = x.shape[-1] if x.dim() else 0
+    if d < 32 or d % 32:
+        raise ValueError(f"x needs rows of whole 32 entries, got shape {tuple(x.shape)}")
+    _need(codes, "codes", torch.uint8, shape=(*x.shape[:-1], d // 2))
+    _need(scales, "scales", torch.uint8, shape=(*x.shape[:-1], d // 32))
+    if codes is None:
+        codes = _new((*x.shape[:-1], d // 2), torch.uint8, x.device, stream)
+    if scales is None:
+        scales = _new((*x.shape[:-1], d // 32), torch.uint8, x.device, stream)
+    at = x.get_device()
+    _check(lib().maxsim_quantize_mx4(
+        _at(x, "x", at), x.numel() // d, d, _TORCH_DTYPE[x.dtype], _at(codes, "codes", at),
+        _at(scales, "scales", at), _stream_at(stream, at)), "maxsim_quantize_mx4")
+    return codes, scales
+
+
+def _mx4(codes, scales, names, dim=None):
+    """d of stored vectors, checked."""
+    _need(codes, names[0], torch.uint8, dim=dim)
+    if not codes.dim() or codes.shape[-1] < 16 or codes.shape[-1] % 16:
+        raise ValueError(f"{names[0]} needs rows of whole 16 bytes, got shape {tuple(codes.shape)}")
+    _need(scales, names[1], torch.uint8, shape=(*codes.shape[:-1], codes.shape[-1] // 16))
+    return codes.shape[-1] * 2
+
+
+def maxsim_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.float32, out=None,
+                          stream=None) -> torch.Tensor:
+    """The values [..., d] that codes and scales from maxsim_quantize_mx4 stand for, in dtype."""
+    d = _mx4(codes, scales, ("codes", "scales"))
+    if dtype not in _TORCH_DTYPE:
+        raise ValueError(f"unsupported dtype {dtype}")
+    shape = (*codes.shape[:-1], d)
+    _need(out, "out", dtype, shape=shape)
+    if out is None:
+        out = _new(shape, dtype, codes.device, stream)
+    at = codes.get_device()
+    _check(lib().maxsim_dequantize_mx4(
+        _at(codes, "codes", at), _at(scales, "scales", at), out.numel() // d, d, _TORCH_DTYPE[dtype],
+        _at(out, "out", at), _stream_at(stream, at)), "maxsim_dequantize_mx4")
+    return out
+
+
+def maxsim_score_mx4(Q: torch.Tensor, q_scale: torch.Tensor, D: torch.Tensor, d_scale: torch.Tensor,
+                     doc_offsets: torch.Tensor | None = None, doc_lens: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Scores of microscaled 4-bit queries and documents (maxsim_quantize_mx4). Q [q_len, d / 2] with
+    q_scale [q_len, d / 32]; fixed documents D [n_docs, nd, d / 2] with d_scale alike, of which
+    doc_lens (int32 [n_docs]) tokens count, or with doc_offsets CSR D [n_tokens, d / 2]. Returns fp32
+    scores [n_docs]."""
+    d = _mx4(Q, q_scale, ("Q", "q_scale"), dim=2)
+    if _mx4(D, d_scale, ("D", "d_scale"), dim=3 if doc_offsets is None else 2) != d:
+        raise ValueError(f"D has d = {2 * D.shape[-1]}, Q has d = {d}")
+    if doc_offsets is not None:
+        _need(doc_offsets, "doc_offsets", torch.int64, dim=1)
+        if doc_offsets.numel() < 1:
+            raise ValueError("doc_offsets needs n_docs + 1 >= 1 entries")
+        if doc_lens is not None:
+            raise ValueError("give doc_offsets or doc_lens, not both")
+    n_docs, nd = _docs(D, doc_offsets)
+    _need(doc_lens, "doc_lens", torch.int32, shape=(n_docs,))
+    out = _out(out, n_docs, Q.device, stream)
+    at = Q.get_device()
+    _check(lib().maxsim_score_mx4(
+        _at(Q, "Q", at), _at(q_scale, "q_scale", at), Q.shape[0], _at(D, "D", at),
+        _at(d_scale, "d_scale", at), _at(doc_offsets, "doc_offsets", at), n_docs, nd,
+        _at(doc_lens, "doc_lens", at), d, _at(out, "out", at), _stream_at(stream, at)),
+        "maxsim_score_mx4")
+    return out
 
 
 def version() -> int:

@@ -31,9 +31,9 @@ HIP_FLAGS = [
 ]
 
 
-# Clipping passes NaN and infinities on, and rotary positions the values that they are given:
-# these files keep NaN semantics.
-KEEP_NANS = ("rotary", "clip_norm")
+# Clipping, the norm, dropout, the cross entropy and the 4-bit conversion pass NaN and infinities on,
+# and rotary positions the values that they are given: these files keep NaN semantics.
+KEEP_NANS = ("rotary", "clip_norm", "rms_norm", "dropout", "ce_", "cross_entropy", "mx4_quant")
 
 
 def flags_of(source: str) -> list[str]:

@@ -1,0 +1,69 @@
+// Launches of maxsim_linear_cross_entropy's kernels, for one storage type.
+#pragma once
+
+#include "ce_kernels.hpp"
+#include "host_common.hpp"
+
+namespace maxsim {
+
+constexpr int CE_STAGES = 3, CE_SMALL_STAGES = 6;
+constexpr int64_t CE_FEW = 64;  // rows
+
+template <typename Kernel> int ce_launch(Kernel kernel, int64_t tiles, int lds, int cus, const CeArgs &a, hipStream_t st) {
+  // the tiles are dealt out on the device, where their number is known: no more workgroups than
+  // there can be tiles, nor than the chip holds at once
+  const int64_t most = (int64_t)cus * blocks_per_cu((const void *)kernel, GEMM_THREADS, lds);
+  const unsigned grid = (unsigned)(tiles < most ? tiles : most);
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(GEMM_THREADS), lds, st, a);
+  return hipGetLastError() == hipSuccess ? MAXSIM_OK : MAXSIM_ERR_LAUNCH;
+}
+
+template <int DT> int ce_gathered(const CeArgs &a, bool count, hipStream_t st) {
+  if (count)
+    hipLaunchKernelGGL(ce_count_kernel<DT>, dim3((unsigned)blocks_of(a.n, CE_COUNT)), dim3(GEMM_THREADS), 0, st, a);
+  if (count && hipGetLastError() != hipSuccess) return MAXSIM_ERR_LAUNCH;
+  hipLaunchKernelGGL(ce_gather_kernel<DT>, dim3((unsigned)blocks_of(a.n, CE_GATHER)), dim3(GEMM_THREADS), 0, st, a);
+  return hipGetLastError() == hipSuccess ? MAXSIM_OK : MAXSIM_ERR_LAUNCH;
+}
+
+template <int DT> int ce_forward(const CeArgs &a, int cus, hipStream_t st) {
+  int rc = ce_gathered<DT>(a, a.n > CE_COUNT, st);
+  if (rc != MAXSIM_OK) return rc;
+  const bool few = a.n <= CE_FEW;
+  const int64_t across = blocks_of(a.vocab, few ? CE_SMALL_BM : CE_BM);
+  if (few) {
+    using G = TileGemm<DT, CE_SMALL_BM, CE_SMALL_BN, 4, false, false, CE_SMALL_STAGES>;
+    rc = ce_launch(ce_forward_kernel<DT, CE_SMALL_BM, CE_SMALL_BN, 4, CE_SMALL_STAGES>,
+                   across * blocks_of(a.n, CE_SMALL_BN), G::lds, cus, a, st);
+  } else {
+    using G = TileGemm<DT, CE_BM, CE_BN, 2, false, false, CE_STAGES>;
+    rc = ce_launch(ce_forward_kernel<DT, CE_BM, CE_BN, 2, CE_STAGES>, across * blocks_of(a.n, CE_BN), G::lds, cus, a, st);
+  }
+  if (rc != MAXSIM_OK) return rc;
+  hipLaunchKernelGGL(ce_join_kernel<DT>, dim3((unsigned)blocks_of(a.n, 8)), dim3(GEMM_THREADS), 0, st, a, (int)across);
+  return hipGetLastError() == hipSuccess ? MAXSIM_OK : MAXSIM_ERR_LAUNCH;
+}
+
+template <int DT> int ce_backward(CeArgs &a, int64_t pieces, int cus, hipStream_t st) {
+  int rc = ce_gathered<DT>(a, true, st);
+  if (rc != MAXSIM_OK) return rc;
+  const int64_t any = (int64_t)1 << 30;
+  for (a.piece = 0; a.piece < pieces; a.piece++) {
+    using GP = TileGemm<DT, CE_BM, CE_BN, 2, false, false, CE_STAGES>;
+    rc = ce_launch(ce_p_kernel<DT, CE_STAGES>, any, GP::lds, cus, a, st);
+    if (rc != MAXSIM_OK) return rc;
+    if (a.dw) {
+      using GW = TileGemm<DT, CE_BM, CE_BN, 2, true, true, CE_STAGES>;
+      rc = ce_launch(ce_dw_kernel<DT, CE_STAGES>, any, GW::lds, cus, a, st);
+      if (rc != MAXSIM_OK) return rc;
+    }
+    if (a.dh) {
+      using GH = TileGemm<DT, CE_BM, CE_BN, 2, true, false, CE_STAGES>;
+      rc = ce_launch(ce_dh_kernel<DT, CE_STAGES>, any, GH::lds, cus, a, st);
+      if (rc != MAXSIM_OK) return rc;
+    }
+  }
+  return a.dh ? ce_launch(ce_dh_join_kernel<DT>, any, 0, cus, a, st) : MAXSIM_OK;
+}
+
+}  // namespace maxsim

@@ -1,0 +1,11 @@
+// The fp32 kernels of maxsim_linear_cross_entropy.
+#include "ce_dispatch.hpp"
+
+namespace maxsim {
+
+int ce_forward_fp32(const CeArgs &a, int cus, hipStream_t st) { return ce_forward<DT_FP32>(a, cus, st); }
+int ce_backward_fp32(CeArgs &a, int64_t pieces, int cus, hipStream_t st) {
+  return ce_backward<DT_FP32>(a, pieces, cus, st);
+}
+
+}  // namespace maxsim

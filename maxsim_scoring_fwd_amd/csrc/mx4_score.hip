@@ -1,0 +1,81 @@
+// maxsim_score_mx4: checks and the choice of the kernel (mx4_score_kernel.hpp).
+#include "host_common.hpp"
+#include "mx4_score_kernel.hpp"
+
+using namespace maxsim;
+
+namespace {
+
+constexpr int MX4_LDS_QUERY = 64 * 1024;  // most bytes of a query's codes held in LDS
+
+template <int KS, int QB, bool QLDS> int mx4_launch(Mx4Args &a, const DeviceInfo &di, hipStream_t st) {
+  // about 8 KiB of codes in flight a wave; at wide rows two tiles
+  constexpr int P = KS >= 4 ? 2 : 8 / KS;
+  const size_t lds = QLDS ? (size_t)QB * KS * WAVE * 17 : 0;
+  auto kernel = mx4_score_kernel<KS, QB, P, QLDS>;
+  const int bpc = blocks_per_cu((const void *)kernel, DENSE_THREADS, lds);
+  int64_t grid = (int64_t)di.cus * bpc;
+  const int64_t most = (a.doc.n_docs + DENSE_WAVES - 1) / DENSE_WAVES;
+  if (grid > most) grid = most;
+  a.doc.contiguous = a.doc.n_docs >= 4 * grid * DENSE_WAVES;
+  log_launch("mx4", (const void *)kernel, grid, DENSE_THREADS, lds, bpc);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(DENSE_THREADS), lds, st, a);
+  return hipGetLastError() == hipSuccess ? MAXSIM_OK : MAXSIM_ERR_LAUNCH;
+}
+
+// Up to 64 query tokens stay in registers; more come from LDS, all blocks for every tile, so that
+// the documents are still read once.
+template <int KS> int mx4_pick(Mx4Args &a, const DeviceInfo &di, hipStream_t st) {
+  const int qb = (a.q_len + 15) / 16;
+  if (qb <= 1) return mx4_launch<KS, 1, false>(a, di, st);
+  if (qb <= 2) return mx4_launch<KS, 2, false>(a, di, st);
+  if (qb <= 4) return mx4_launch<KS, 4, false>(a, di, st);
+  if (qb <= 8) return mx4_launch<KS, 8, true>(a, di, st);
+  if constexpr (KS <= 4)
+    if (qb <= 16) return mx4_launch<KS, 16, true>(a, di, st);
+  if constexpr (KS <= 2)
+    if (qb <= 32) return mx4_launch<KS, 32, true>(a, di, st);
+  if constexpr (KS <= 1)
+    if (qb <= 64) return mx4_launch<KS, 64, true>(a, di, st);
+  return MAXSIM_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" int maxsim_score_mx4(const uint8_t *Q, const uint8_t *q_scale, int q_len, const uint8_t *D,
+                                const uint8_t *d_scale, const int64_t *doc_offsets, int64_t n_docs, int nd,
+                                const int32_t *doc_lens, int d, float *out, void *stream) {
+  if (n_docs < 0 || q_len < 1 || q_len > MAXSIM_MAX_Q_LEN || d < MAXSIM_MIN_D || d > MAXSIM_MAX_D || d % 32 ||
+      (!doc_offsets && nd < 1))
+    return MAXSIM_ERR_SHAPE;
+  if (!Q || !q_scale || !D || !d_scale || !out) return MAXSIM_ERR_NULL;
+  if (doc_offsets && doc_lens) return MAXSIM_ERR_UNSUPPORTED;
+  if (!aligned(Q, 16) || !aligned(D, 16) || !aligned(out, 4) || (doc_offsets && !aligned(doc_offsets, 8)) ||
+      (doc_lens && !aligned(doc_lens, 4)))
+    return MAXSIM_ERR_ALIGN;
+  const int steps = (d + 127) / 128, ks = steps <= 1 ? 1 : steps <= 2 ? 2 : steps <= 4 ? 4 : 8;
+  if (q_len > 64 && (int64_t)((q_len + 15) / 16) * 16 * ks * 64 > MX4_LDS_QUERY) return MAXSIM_ERR_UNSUPPORTED;
+  if (n_docs == 0) return MAXSIM_OK;
+  DeviceInfo di;
+  const int rc = current_device(di);
+  if (rc != MAXSIM_OK) return rc;
+  Mx4Args a{};
+  a.doc.D = (const char *)D;
+  a.doc.offsets = doc_offsets;
+  a.doc.n_docs = n_docs;
+  a.doc.nd = doc_offsets ? 0 : nd;
+  a.doc.doc_lens = doc_lens;
+  a.doc.out = out;
+  a.d_scale = d_scale;
+  a.q_scale = q_scale;
+  a.Q = (const char *)Q;
+  a.q_len = q_len;
+  a.blocks = d / 32;
+  hipStream_t st = (hipStream_t)stream;
+  switch (ks) {
+  case 1: return mx4_pick<1>(a, di, st);
+  case 2: return mx4_pick<2>(a, di, st);
+  case 4: return mx4_pick<4>(a, di, st);
+  default: return mx4_pick<8>(a, di, st);
+  }
+}
