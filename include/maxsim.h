@@ -459,7 +459,7 @@ size_t maxsim_rms_norm_backward_workspace_size(int64_t n_rows, int d);
  * is never used, and it costs nothing beside its label (masked-token training labels few rows).
  * Products run on the matrix cores with fp32 sums; statistics are fp32.
  *   h       [n_rows][d], w [vocab][d] in `dtype`, densely packed, 16-byte aligned, finite;
- *           d * element bytes a multiple of 16, d <= 16384; n_rows and vocab below 2^31
+ *           d * element bytes a multiple of 16, d <= 16384; n_rows <= 2^22, vocab below 2^31
  *   labels  int64 [n_rows]
  *   scale   > 0 and finite
  *   loss, lse  fp32 [n_rows]

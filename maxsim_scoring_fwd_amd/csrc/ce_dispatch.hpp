@@ -32,11 +32,11 @@ template <int DT> int ce_forward(const CeArgs &a, int cus, hipStream_t st) {
   const bool few = a.n <= CE_FEW;
   const int64_t across = blocks_of(a.vocab, few ? CE_SMALL_BM : CE_BM);
   if (few) {
-    using G = TileGemm<DT, CE_SMALL_BM, CE_SMALL_BN, 4, false, false, CE_SMALL_STAGES>;
+    using G = CeLogits<DT, CE_SMALL_BM, CE_SMALL_BN, 4, CE_SMALL_STAGES>;
     rc = ce_launch(ce_forward_kernel<DT, CE_SMALL_BM, CE_SMALL_BN, 4, CE_SMALL_STAGES>,
                    across * blocks_of(a.n, CE_SMALL_BN), G::lds, cus, a, st);
   } else {
-    using G = TileGemm<DT, CE_BM, CE_BN, 2, false, false, CE_STAGES>;
+    using G = CeLogits<DT, CE_BM, CE_BN, 2, CE_STAGES>;
     rc = ce_launch(ce_forward_kernel<DT, CE_BM, CE_BN, 2, CE_STAGES>, across * blocks_of(a.n, CE_BN), G::lds, cus, a, st);
   }
   if (rc != MAXSIM_OK) return rc;
@@ -48,20 +48,13 @@ template <int DT> int ce_backward(CeArgs &a, int64_t pieces, int cus, hipStream_
   int rc = ce_gathered<DT>(a, true, st);
   if (rc != MAXSIM_OK) return rc;
   const int64_t any = (int64_t)1 << 30;
+  using Z = CeLogits<DT, CE_BM, CE_BN, 2, CE_STAGES>;
+  using G = TileGemm<DT, CE_PM, CE_PN, 2, SIDE_COLS_P, SIDE_COLS_P, CE_STAGES>;
+  a.lanes = cus * blocks_per_cu((const void *)ce_products_kernel<DT, CE_STAGES>, GEMM_THREADS, G::lds);
   for (a.piece = 0; a.piece < pieces; a.piece++) {
-    using GP = TileGemm<DT, CE_BM, CE_BN, 2, false, false, CE_STAGES>;
-    rc = ce_launch(ce_p_kernel<DT, CE_STAGES>, any, GP::lds, cus, a, st);
+    rc = ce_launch(ce_p_kernel<DT, CE_STAGES>, any, Z::lds, cus, a, st);
+    if (rc == MAXSIM_OK) rc = ce_launch(ce_products_kernel<DT, CE_STAGES>, any, G::lds, cus, a, st);
     if (rc != MAXSIM_OK) return rc;
-    if (a.dw) {
-      using GW = TileGemm<DT, CE_BM, CE_BN, 2, true, true, CE_STAGES>;
-      rc = ce_launch(ce_dw_kernel<DT, CE_STAGES>, any, GW::lds, cus, a, st);
-      if (rc != MAXSIM_OK) return rc;
-    }
-    if (a.dh) {
-      using GH = TileGemm<DT, CE_BM, CE_BN, 2, true, false, CE_STAGES>;
-      rc = ce_launch(ce_dh_kernel<DT, CE_STAGES>, any, GH::lds, cus, a, st);
-      if (rc != MAXSIM_OK) return rc;
-    }
   }
   return a.dh ? ce_launch(ce_dh_join_kernel<DT>, any, 0, cus, a, st) : MAXSIM_OK;
 }

@@ -16,7 +16,8 @@
 
 namespace maxsim {
 
-constexpr int CE_BM = 256, CE_BN = 128;              // vocabulary (or columns) x rows of a tile
+constexpr int CE_BM = 128, CE_BN = 256;              // vocabulary x rows of a tile of logits
+constexpr int CE_PM = 256, CE_PN = 128;              // columns x vocabulary (dw) or rows (dh) of a product's
 constexpr int CE_SMALL_BM = 128, CE_SMALL_BN = 32;   // for few rows
 constexpr int CE_GATHER = 32;                        // rows of a workgroup of the gathering
 constexpr int CE_COUNT = 1024;                       // rows of a workgroup of the counting
@@ -34,22 +35,31 @@ struct CeArgs {
   int32_t *counted;       // [1]: rows that have a label
   int32_t *counts;        // [blocks of CE_COUNT rows]
   float *most;            // [the same]: the largest absolute gradient
-  int32_t *row, *label;   // [n]: of gathered row i
-  char *hc;               // [n][d]: gathered rows
+  int4 *info;             // [n]: of gathered row i (CeRow)
+  char *hc;               // gathered rows in panels of 64 bytes, n rows each, zeros past d
   float2 *part;           // [tiles of the vocabulary][n]: largest logit (in units of log 2), sum
   float *picked;          // [n]: the label's logit, in units of log 2
-  char *p;                // [rows][piece]: P
+  char *p;                // P in panels of 64 bytes, whole tiles of rows each
   float *dhp;             // tiles of dh in the kernels' register layout
+  int32_t *queue;         // [8]: units of the products that are taken
   int64_t p_elements;     // that p has room for
   int64_t slots;          // tiles that dhp has room for
   int64_t piece;          // backward: number of this piece
+  int lanes;              // backward: workgroups of the products
+};
+
+// A gathered row: its label, its place among all rows, and for the backward its lse in units of log
+// 2 and its gradient times scale.
+struct CeRow {
+  int label, row;
+  float lse, grad;
 };
 
 // The pieces of the vocabulary for m rows: as many whole tiles as P's room takes, of equal size.
 struct CePieces {
-  int64_t cols, n;
+  int64_t cols, n, rows;
   __device__ __host__ __forceinline__ CePieces(int64_t m, int64_t vocab, int64_t p_elements) {
-    const int64_t rows = blocks_of(m < 1 ? 1 : m, CE_BN) * CE_BN;
+    rows = blocks_of(m < 1 ? 1 : m, CE_BN) * CE_BN;
     const int64_t tiles = blocks_of(vocab, CE_BM);
     int64_t most = p_elements / (rows * CE_BM);
     most = most < 1 ? 1 : most;
@@ -59,13 +69,24 @@ struct CePieces {
   }
 };
 
-// How many parts dh's sums over a piece go in: as many as there is room for and steps enough.
-__device__ __host__ __forceinline__ int64_t ce_splits(int64_t tiles, int64_t slots, int64_t cols, int bk) {
-  const int64_t most = cols / (8 * bk);
-  int64_t s = slots / (tiles < 1 ? 1 : tiles);
-  s = s < most ? s : most;
-  return s < 1 ? 1 : s;
-}
+// The products of one piece: dw's tiles, and dh's, whose sums over the piece go in several parts, so
+// that all workgroups end about together: a part is about a third of a workgroup's share.
+template <int DT> struct CeUnits {
+  uint32_t w_across, w_down, h_across, h_down, splits;
+  __device__ __host__ __forceinline__ CeUnits(const CeArgs &a, int64_t m, const CePieces &p) {
+    constexpr int BK = 64 / Elem<DT>::bytes;
+    w_across = h_across = (uint32_t)blocks_of(a.d, CE_PM);
+    w_down = (uint32_t)blocks_of(p.cols, CE_PN);
+    h_down = (uint32_t)blocks_of(m, CE_PN);
+    const int64_t tiles = (int64_t)h_across * h_down, steps = p.cols / BK;
+    const int64_t all = (a.dw ? (int64_t)w_across * w_down * blocks_of(m, BK) : 0) + tiles * steps;
+    int64_t s = blocks_of(3 * steps * a.lanes, all < 1 ? 1 : all);
+    const int64_t room = a.slots / (tiles < 1 ? 1 : tiles), most = steps / 8;
+    s = s < room ? s : room;
+    s = s < most ? s : most;
+    splits = (uint32_t)(s < 1 ? 1 : s);
+  }
+};
 
 // fp16: the power of two that P is scaled by.
 template <int DT> __device__ __forceinline__ float ce_up(const CeArgs &a) {
@@ -133,8 +154,12 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_gather_kern
     const int at = before + __popcll(all & ((1ull << threadIdx.x) - 1));
     if (threadIdx.x < CE_GATHER) place[threadIdx.x] = counts ? at : -1;
     if (counts) {
-      a.row[at] = (int32_t)r;
-      a.label[at] = (int32_t)label;
+      CeRow row{(int)label, (int)r, 0.0f, 0.0f};
+      if (a.grad) {
+        row.lse = a.lse[r] * LOG2E;
+        row.grad = a.grad[r] * a.scale;
+      }
+      a.info[at] = __builtin_bit_cast(int4, row);
     } else if (in && a.loss) {
       a.loss[r] = 0.0f;
       a.lse[r] = -__builtin_inff();
@@ -142,92 +167,181 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_gather_kern
     if (threadIdx.x == 0 && r0 + CE_GATHER >= a.n) *a.counted = before + __popcll(all);
   }
   __syncthreads();
-  const int chunks = a.row_bytes / 16;
-  for (int i = threadIdx.x >> 6; i < CE_GATHER && r0 + i < a.n; i += 4) {
-    const int at = uniform(place[i]);
-    const char *from = a.h + (r0 + i) * a.row_bytes;
-    if (at >= 0) {
-      char *to = a.hc + (int64_t)at * a.row_bytes;
-      for (int c = threadIdx.x & 63; c < chunks; c += 64) *(u32x4_t *)(to + c * 16) = load16(from + c * 16);
-    } else if (a.dh) {
-      char *to = a.dh + (r0 + i) * a.row_bytes;
-      for (int c = threadIdx.x & 63; c < chunks; c += 64) *(u32x4_t *)(to + c * 16) = u32x4_t{0, 0, 0, 0};
+  // two panels at a time: 32 rows x 128 bytes, so that both sides move whole lines
+  const int i = threadIdx.x / 8, c0 = threadIdx.x % 8 * 16;
+  if (r0 + i >= a.n) return;
+  const int at = place[i];
+  const char *from = a.h + (r0 + i) * a.row_bytes;
+  const int padded = (a.row_bytes + PANEL - 1) / PANEL * PANEL;
+  if (at >= 0) {
+    char *to = a.hc + (int64_t)at * PANEL;
+#pragma unroll 4
+    for (int c = c0; c < padded; c += 128) {
+      u32x4_t x = {0, 0, 0, 0};
+      if (c < a.row_bytes) x = load16(from + c);
+      *(u32x4_t *)(to + (int64_t)(c / PANEL) * a.n * PANEL + c % PANEL) = x;
     }
+  } else if (a.dh) {
+    char *to = a.dh + (r0 + i) * a.row_bytes;
+    for (int c = c0; c < a.row_bytes; c += 128) *(u32x4_t *)(to + c) = u32x4_t{0, 0, 0, 0};
   }
 }
 
-// Tile number i of `across` tiles of the vocabulary times `down` tiles of rows, so that tiles
-// beside each other in the order share both operands in an XCD's L2: 8 tiles of rows at a time.
+// A block of 32 x 32 of P, each lane's row times f, rounded, to a panel's 32 rows (fp32: two panels').
+template <int DT> __device__ __forceinline__ void store_block(char *lds, const f32x16_t &x, float f, char *out, int64_t panel) {
+  using L = RowLayout<DT, 32>;
+  using T = typename AttnElem<DT>::type;
+  typedef T v4 __attribute__((ext_vector_type(4)));
+  const int l = threadIdx.x & 63, row = l & 31, h = l >> 5;
+#pragma unroll
+  for (int g = 0; g < 4; g++) {
+    v4 y;
+#pragma unroll
+    for (int e = 0; e < 4; e++) y[e] = (T)(x[4 * g + e] * f);
+    const int at = (8 * g + 4 * h) * L::eb;
+    *(v4 *)(lds + row * L::bytes + ((at & ~15) ^ L::f(row)) + (at & 15)) = y;
+  }
+  wave_lds_sync();
+#pragma unroll
+  for (int i = 0; i < (32 * L::chunks) / 64; i++) {
+    const int p = i * 64 + l, r = p / L::chunks, c = p % L::chunks * 16;
+    *(u32x4_t *)(out + c / PANEL * panel + r * PANEL + c % PANEL) = *(const u32x4_t *)(lds + r * L::bytes + (c ^ L::f(r)));
+  }
+  wave_lds_sync();
+}
+
+// Tile number i of `across` tiles along one side times `down` along the other, so that tiles beside
+// each other in the order share both operands in an XCD's L2: 8 tiles down at a time.
 __device__ __forceinline__ void ce_tile(uint32_t i, uint32_t across, uint32_t down, uint32_t &v, uint32_t &r) {
   const uint32_t group = i / (8 * across), in = i - group * 8 * across;
   const uint32_t wide = down - group * 8 < 8 ? down - group * 8 : 8;
   v = in / wide;
   r = group * 8 + in - v * wide;
 }
+// The same with an eighth of the vocabulary for each XCD: the vocabulary's rows are then read by one
+// XCD alone, and 8 tiles of rows stay in its L2 while it goes through its eighth.
+__device__ __forceinline__ void ce_tile_of_xcd(uint32_t i, uint32_t across, uint32_t down, uint32_t &v, uint32_t &r) {
+  const uint32_t eighth = (across + 7) / 8, x = i / (eighth * down), v0 = x * eighth;
+  ce_tile(i - x * eighth * down, across - v0 < eighth ? across - v0 : eighth, down, v, r);
+  v += v0;
+}
 
-// Logits of a tile, z in units of log 2 less nothing: acc[n][m] of lane l is row 32 n + l % 32 and
-// vocabulary entry 32 m + acc_row(reg) + 4 (l / 32) of the wave's part.
+// Logits of a tile: acc[n][m] of lane l is row 32 n + l % 32 and vocabulary entry 32 m +
+// acc_row(reg) + 4 (l / 32) of the wave's part, without scale. The rows' CeRow come to LDS with the
+// first loads. A workgroup takes tiles one after the other; the first loads of the next one are
+// under way while it goes on with the logits.
 template <int DT, int BM, int BN, int WM, int STAGES> struct CeLogits {
-  using G = TileGemm<DT, BM, BN, WM, false, false, STAGES>;
-  static __device__ __forceinline__ void run(G &g, const CeArgs &a, char *ring, int64_t v0, int64_t r0, int m) {
-    const int64_t vs = a.vocab - v0;
-    g.a.start(a.w + v0 * a.row_bytes, a.row_bytes, vs < BM ? (int)vs : BM);
-    g.b.start(a.hc + r0 * a.row_bytes, a.row_bytes, m - (int)r0 < BN ? m - (int)r0 : BN);
+  using G = TileGemm<DT, BM, BN, WM, SIDE_ROWS, SIDE_ROWS_P, STAGES>;
+  static constexpr int ring = G::lds, info = (BN < 64 ? 64 : BN) * 16, lds = ring + 2 * info;
+  static constexpr int scratch = (STAGES - 1) * G::stage;  // of the ring: free between tiles
+  G g;
+  uint32_t across, down, total, next;  // tiles; number of the next one
+  int64_t v0, r0;                      // of the tile at hand
+  int64_t v1, r1;                      // of the next
+  int m, which;                        // place of the tile's CeRows
+
+  __device__ __forceinline__ void start(const CeArgs &a, char *lds, int rows, int64_t vocab0, int64_t cols) {
+    m = rows;
+    across = (uint32_t)blocks_of(cols, BM);
+    down = (uint32_t)blocks_of(m, BN);
+    total = across * down;
+    next = blockIdx.x;
+    which = 1;
+    begin(a, lds, vocab0);
+  }
+  __device__ __forceinline__ void begin(const CeArgs &a, char *lds, int64_t vocab0) {
+    which ^= 1;
+    if (next >= total) return;
+    uint32_t tv, tr;
+    ce_tile_of_xcd(xcd_order(next, total), across, down, tv, tr);
+    v1 = vocab0 + (int64_t)tv * BM;
+    r1 = (int64_t)tr * BN;
+    const int exist = m - (int)r1 < BN ? m - (int)r1 : BN;
+    const int wave = uniform((int)threadIdx.x >> 6);
+    if (wave * 64 < BN) {
+      const int r = (int)threadIdx.x < exist ? (int)threadIdx.x : exist - 1;
+      const int to = lds_address(lds + ring + which * info) + wave * 1024;  // 64 rows a wave
+      asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                   :
+                   : "{m0}"(uniform(to)), "v"((uint32_t)r * 16u),
+                     "s"(uniform((int64_t)(uintptr_t)(a.info + r1))));
+    }
+    const int64_t vs = a.vocab - v1;
+    g.a.start(a.w + v1 * a.row_bytes, a.row_bytes, vs < BM ? (int)vs : BM);
+    g.b.start(a.hc + r1 * PANEL, a.n * PANEL, exist);
+    const int steps = (a.row_bytes + 63) / 64;
+    g.begin(lds, steps, a.row_bytes - (steps - 1) * 64, 64);  // the panels hold zeros past d
+  }
+  // The next tile's logits; false after the last. row(i): CeRow i of the tile.
+  __device__ __forceinline__ bool tile(const CeArgs &a, char *lds, int64_t vocab0) {
+    if (next >= total) return false;
+    v0 = v1;
+    r0 = r1;
     g.clear();
-    const int steps = (a.row_bytes + 63) / 64, left = a.row_bytes - (steps - 1) * 64;
-    g.run(ring, steps, left, 0, 0, a.row_bytes, a.row_bytes);
+    g.finish(lds);
+    next += gridDim.x;
+    begin(a, lds, vocab0);
+    return true;
+  }
+  __device__ __forceinline__ CeRow row(const char *lds, int i) const {
+    return *(const CeRow *)(lds + ring + (which ^ 1) * info + i * 16);
   }
 };
 
 template <int DT, int BM, int BN, int WM, int STAGES>
 __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_forward_kernel(CeArgs a) {
-  using G = TileGemm<DT, BM, BN, WM, false, false, STAGES>;
-  extern __shared__ __attribute__((aligned(1024))) char ring[];
-  const int m = uniform(*a.counted);
-  const uint32_t across = (uint32_t)blocks_of(a.vocab, BM), down = (uint32_t)blocks_of(m, BN);
-  const uint32_t total = across * down;
+  using Z = CeLogits<DT, BM, BN, WM, STAGES>;
+  using G = typename Z::G;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
-  for (uint32_t i = blockIdx.x; i < total; i += gridDim.x) {
-    uint32_t tv, tr;
-    ce_tile(xcd_order(i, total), across, down, tv, tr);
-    const int64_t v0 = (int64_t)tv * BM, r0 = (int64_t)tr * BN;
-    G g;
-    CeLogits<DT, BM, BN, WM, STAGES>::run(g, a, ring, v0, r0, m);
+  const int h4 = 4 * (lane >> 5);
+  const float f = a.scale * LOG2E;
+  float2 *red = (float2 *)(lds + Z::scratch);
+  Z z;
+  z.start(a, lds, uniform(*a.counted), 0, a.vocab);
+  while (z.tile(a, lds, 0)) {
     // largest logit and sum of exponentials of each row over this wave's part of the vocabulary
-    const float f = a.scale * LOG2E;
-    const int64_t first = v0 + wm * (BM / WM);
+    const int64_t first = z.v0 + wm * (BM / WM);
     const int exist = a.vocab - first < BM / WM ? (int)(a.vocab - first) : BM / WM;
-    float2 *red = (float2 *)ring;
 #pragma unroll
     for (int n = 0; n < G::TN; n++) {
-      const int64_t r = r0 + (wn * G::TN + n) * 32 + (lane & 31);
-      const int at = (r < m ? a.label[r] - (int)first : -1) - 4 * (lane >> 5);
-      float most = -__builtin_inff(), z = 0.0f;
-      bool mine = false;
+      f32x16_t(&x)[G::TM] = z.g.acc[n];
+      const int i = (wn * G::TN + n) * 32 + (lane & 31);
+      const int64_t r = z.r0 + i;
+      const int at = r < z.m ? z.row(lds, i).label - (int)first : -1;
+      if (__any(at >= 0 && at < BM / WM)) {
+        float picked = 0.0f;
+#pragma unroll
+        for (int k = 0; k < G::TM; k++)
+#pragma unroll
+          for (int e = 0; e < 16; e++)
+            if (k * 32 + acc_row(e) == at - h4) picked = x[k][e];
+        if (at >= 0 && at < BM / WM && (at & 4) == h4) a.picked[r] = picked * f;
+      }
+      if (exist < BM / WM) {
+#pragma unroll
+        for (int k = 0; k < G::TM; k++)
+#pragma unroll
+          for (int e = 0; e < 16; e++)
+            if (k * 32 + acc_row(e) + h4 >= exist) x[k][e] = -__builtin_inff();
+      }
+      float most = -__builtin_inff();
 #pragma unroll
       for (int k = 0; k < G::TM; k++)
 #pragma unroll
-        for (int e = 0; e < 16; e++) {
-          const int v = k * 32 + acc_row(e);
-          float x = g.acc[n][k][e] * f;
-          if (v == at) z = x, mine = true;
-          if (v + 4 * (lane >> 5) >= exist) x = -__builtin_inff();
-          most = __builtin_fmaxf(most, x);
-          g.acc[n][k][e] = x;
-        }
-      most = half_max(most);
+        for (int e = 0; e < 16; e++) most = __builtin_fmaxf(most, x[k][e]);
+      most = half_max(most) * f;  // scale is positive
       const float from = most == -__builtin_inff() ? 0.0f : most;
       float sum = 0.0f;
 #pragma unroll
       for (int k = 0; k < G::TM; k++)
 #pragma unroll
-        for (int e = 0; e < 16; e++) sum += __builtin_amdgcn_exp2f(g.acc[n][k][e] - from);
+        for (int e = 0; e < 16; e++) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(x[k][e], f, -from));
       sum = half_sum(sum);
-      if (lane < 32) red[wm * BN + (wn * G::TN + n) * 32 + lane] = make_float2(most, sum);
-      if (mine && r < m) a.picked[r] = z;
+      if (lane < 32) red[wm * BN + i] = make_float2(most, sum);
     }
     __syncthreads();
-    if (threadIdx.x < BN && r0 + threadIdx.x < m) {
+    if (threadIdx.x < BN && z.r0 + threadIdx.x < z.m) {
       float2 s = red[threadIdx.x];
 #pragma unroll
       for (int k = 1; k < WM; k++) {
@@ -236,9 +350,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_forward_kernel(CeArgs a) {
         s.y = s.y * __builtin_amdgcn_exp2f(s.x - from) + o.y * __builtin_amdgcn_exp2f(o.x - from);
         s.x = most;
       }
-      a.part[(int64_t)tv * a.n + r0 + threadIdx.x] = s;
+      a.part[z.v0 / BM * a.n + z.r0 + threadIdx.x] = s;
     }
-    __syncthreads();
   }
 }
 
@@ -267,7 +380,7 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_join_kernel
   if (slice == 0 && r < m) {
     s = part[0][row];
     const float l = s.x + __builtin_log2f(s.y);
-    const int64_t to = a.row[r];
+    const int64_t to = __builtin_bit_cast(CeRow, a.info[r]).row;
     a.lse[to] = l * LN2;
     a.loss[to] = (l - a.picked[r]) * LN2;
   }
@@ -278,154 +391,162 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_join_kernel
 template <int DT, int STAGES>
 __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_p_kernel(CeArgs a) {
   constexpr int BM = CE_BM, BN = CE_BN, WM = 2;
-  using G = TileGemm<DT, BM, BN, WM, false, false, STAGES>;
-  extern __shared__ __attribute__((aligned(1024))) char ring[];
+  using Z = CeLogits<DT, BM, BN, WM, STAGES>;
+  using G = typename Z::G;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  if (blockIdx.x == 0 && threadIdx.x < 8) a.queue[threadIdx.x] = 0;
   const int m = uniform(*a.counted);
   const CePieces pieces(m, a.vocab, a.p_elements);
   if (a.piece >= pieces.n) return;
   const int64_t piece0 = a.piece * pieces.cols;
   const int64_t cols = a.vocab - piece0 < pieces.cols ? a.vocab - piece0 : pieces.cols;
-  const uint32_t across = (uint32_t)blocks_of(cols, BM), down = (uint32_t)blocks_of(m, BN), total = across * down;
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
-  const float up = ce_up<DT>(a);
+  const int h4 = 4 * (lane >> 5);
+  const float up = ce_up<DT>(a), f = a.scale * LOG2E;
+  // a block of 32 x 32 leaves through LDS: a panel of 32 rows, which is one piece of memory
   constexpr int eb = Elem<DT>::bytes, part = BM / WM;
-  for (uint32_t i = blockIdx.x; i < total; i += gridDim.x) {
-    uint32_t tv, tr;
-    ce_tile(xcd_order(i, total), across, down, tv, tr);
-    const int64_t v0 = piece0 + (int64_t)tv * BM, r0 = (int64_t)tr * BN;
-    const int64_t first = v0 + wm * part;
+  char *mine = lds + Z::scratch + wave * (32 * 32 * eb);
+  const int64_t panel = pieces.rows * PANEL;
+  Z z;
+  z.start(a, lds, m, piece0, cols);
+  while (z.tile(a, lds, piece0)) {
+    const int64_t first = z.v0 + wm * part;
     const int exist = a.vocab - first < part ? (int)(a.vocab - first) : part;  // or negative
-    G g;
-    CeLogits<DT, BM, BN, WM, STAGES>::run(g, a, ring, v0, r0, m);
-    const float f = a.scale * LOG2E;
-    char *mine = ring + wave * (32 * part * eb);
 #pragma unroll
     for (int n = 0; n < G::TN; n++) {
-      const int64_t r = r0 + (wn * G::TN + n) * 32 + (lane & 31);
-      const bool real = r < m;
-      const int64_t source = real ? a.row[r] : 0;
-      const float by = real ? a.grad[source] * a.scale * up : 0.0f;
-      const float from = real ? a.lse[source] * LOG2E : 0.0f;
-      const int at = (real ? a.label[r] - (int)first : -1) - 4 * (lane >> 5);
+      f32x16_t(&x)[G::TM] = z.g.acc[n];
+      const int i = (wn * G::TN + n) * 32 + (lane & 31);
+      const CeRow row = z.row(lds, i);  // past the last row: the last one's, with a gradient of 0
+      const bool real = z.r0 + i < z.m;
+      const float by = real ? row.grad * up : 0.0f;
 #pragma unroll
       for (int k = 0; k < G::TM; k++)
 #pragma unroll
-        for (int e = 0; e < 16; e++) {
-          const int v = k * 32 + acc_row(e);
-          float x = __builtin_amdgcn_exp2f(g.acc[n][k][e] * f - from);
-          if (v == at) x -= 1.0f;
-          x *= by;
-          g.acc[n][k][e] = real && v + 4 * (lane >> 5) < exist ? x : 0.0f;
-        }
-      const int64_t out = (r0 + (wn * G::TN + n) * 32) * pieces.cols + (first - piece0);
-      store_rows<DT, part, G::TM>(mine, g.acc[n], 1.0f, a.p + out * eb, pieces.cols * eb, 32, part * eb);
+        for (int e = 0; e < 16; e++) x[k][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[k][e], f, -row.lse));
+      const int at = real ? row.label - (int)first : -1;
+      if (__any(at >= 0 && at < part)) {
+#pragma unroll
+        for (int k = 0; k < G::TM; k++)
+#pragma unroll
+          for (int e = 0; e < 16; e++)
+            if (k * 32 + acc_row(e) == at - h4) x[k][e] -= 1.0f;
+      }
+      if (exist < part) {
+#pragma unroll
+        for (int k = 0; k < G::TM; k++)
+#pragma unroll
+          for (int e = 0; e < 16; e++)
+            if (k * 32 + acc_row(e) + h4 >= exist) x[k][e] = 0.0f;
+      }
+      char *out = a.p + (first - piece0) * eb / PANEL * panel + (z.r0 + (wn * G::TN + n) * 32) * PANEL;
+#pragma unroll
+      for (int k = 0; k < G::TM; k++) store_block<DT>(mine, x[k], by, out + k * 32 * eb / PANEL * panel, panel);
     }
-    __syncthreads();
   }
 }
 
-// dw of one piece: P^T h over the gathered rows.
+// The products of one piece: dw = P^T h over the gathered rows, tile by tile; and dh's sums over the
+// piece, added to those of the pieces before, in parts, in the register layout. The units of each
+// XCD's workgroups lie side by side, so that its L2 serves what they share; a workgroup takes the
+// next one when it has ended one, the long ones first. Who makes a unit does not change it.
 template <int DT, int STAGES>
-__global__ void __launch_bounds__(GEMM_THREADS, 2) ce_dw_kernel(CeArgs a) {
-  constexpr int BM = CE_BM, BN = CE_BN, WM = 2;
-  using G = TileGemm<DT, BM, BN, WM, true, true, STAGES>;
-  extern __shared__ __attribute__((aligned(1024))) char ring[];
+__global__ void __launch_bounds__(GEMM_THREADS, 2) ce_products_kernel(CeArgs a) {
+  constexpr int BM = CE_PM, BN = CE_PN, WM = 2;
+  using GW = TileGemm<DT, BM, BN, WM, SIDE_COLS_P, SIDE_COLS_P, STAGES>;
+  using GH = TileGemm<DT, BM, BN, WM, SIDE_COLS, SIDE_ROWS_P, STAGES>;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  __shared__ int taken;
   const int m = uniform(*a.counted);
   const CePieces pieces(m, a.vocab, a.p_elements);
   if (a.piece >= pieces.n) return;
   const int64_t piece0 = a.piece * pieces.cols;
   const int64_t cols = a.vocab - piece0 < pieces.cols ? a.vocab - piece0 : pieces.cols;
-  const uint32_t across = (uint32_t)blocks_of(a.d, BM), down = (uint32_t)blocks_of(cols, BN), total = across * down;
+  const CeUnits<DT> units(a, m, pieces);
+  const uint32_t w_down = (uint32_t)blocks_of(cols, BN), h_tiles = units.h_across * units.h_down;
+  const uint32_t w_units = a.dw ? units.w_across * w_down : 0, h_units = a.dh ? h_tiles * units.splits : 0;
+  const uint32_t x = blockIdx.x & 7;
+  const uint32_t w_from = (uint64_t)w_units * x / 8, w_n = (uint64_t)w_units * (x + 1) / 8 - w_from;
+  const uint32_t h_from = (uint64_t)h_units * x / 8, h_n = (uint64_t)h_units * (x + 1) / 8 - h_from;
   const int wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
   const float back = 1.0f / ce_up<DT>(a);
   constexpr int eb = Elem<DT>::bytes, part = BM / WM;
-  const int steps = (int)blocks_of(m, G::BK);
-  for (uint32_t i = blockIdx.x; i < total; i += gridDim.x) {
-    uint32_t tc, tv;
-    ce_tile(xcd_order(i, total), across, down, tc, tv);
-    const int c0 = (int)tc * BM;
-    const int64_t v0 = (int64_t)tv * BN;
-    G g;
-    g.clear();
-    if (steps > 0) {
-      g.a.start(a.hc + (int64_t)c0 * eb, a.row_bytes, a.row_bytes - c0 * eb);
-      g.b.start(a.p + v0 * eb, pieces.cols * eb, BN * eb);
-      // rows of P past the last are zeros, and whole tiles of rows are there
-      g.run(ring, steps, 64, m - (steps - 1) * G::BK, G::BK, a.row_bytes, pieces.cols * eb);
-    }
-    char *mine = ring + wave * (32 * part * eb);
-    const int at = c0 + wm * part;
-    const int row_bytes = (a.d - at < part ? a.d - at : part) * eb;
-#pragma unroll
-    for (int n = 0; n < G::TN; n++) {
-      const int64_t v = v0 + (wn * G::TN + n) * 32;
-      const int64_t left = cols - v;
-      if (row_bytes > 0 && left > 0)
-        store_rows<DT, part, G::TM>(mine, g.acc[n], back, a.dw + (piece0 + v) * a.row_bytes + (int64_t)at * eb,
-                                    a.row_bytes, left < 32 ? (int)left : 32, row_bytes);
-    }
+  const int64_t panel = pieces.rows * PANEL;
+  for (;;) {
     __syncthreads();
-  }
-}
-
-// dh's sums over one piece, added to those of the pieces before: tiles in register layout, the
-// piece's steps in several parts where there are few tiles.
-template <int DT, int STAGES>
-__global__ void __launch_bounds__(GEMM_THREADS, 2) ce_dh_kernel(CeArgs a) {
-  constexpr int BM = CE_BM, BN = CE_BN, WM = 2;
-  using G = TileGemm<DT, BM, BN, WM, true, false, STAGES>;
-  extern __shared__ __attribute__((aligned(1024))) char ring[];
-  const int m = uniform(*a.counted);
-  const CePieces pieces(m, a.vocab, a.p_elements);
-  if (a.piece >= pieces.n) return;
-  const int64_t piece0 = a.piece * pieces.cols;
-  const int64_t cols = a.vocab - piece0 < pieces.cols ? a.vocab - piece0 : pieces.cols;
-  const uint32_t across = (uint32_t)blocks_of(a.d, BM), down = (uint32_t)blocks_of(m, BN), tiles = across * down;
-  const uint32_t splits = (uint32_t)ce_splits(tiles, a.slots, pieces.cols, G::BK), total = tiles * splits;
-  const int steps = (int)blocks_of(cols, G::BK);
-  constexpr int eb = Elem<DT>::bytes;
-  for (uint32_t i = blockIdx.x; i < total; i += gridDim.x) {
-    const uint32_t id = xcd_order(i, total), split = id / tiles;
+    if (threadIdx.x == 0) taken = atomicAdd(a.queue + x, 1);
+    __syncthreads();
+    const uint32_t unit = uniform(taken);
+    if (unit >= w_n + h_n) break;
     uint32_t tc, tr;
-    ce_tile(id - split * tiles, across, down, tc, tr);
-    const int c0 = (int)tc * BM;
-    const int64_t r0 = (int64_t)tr * BN;
-    const int from = (int)((int64_t)steps * split / splits), to = (int)((int64_t)steps * (split + 1) / splits);
-    G g;
-    g.clear();
-    if (to > from) {
-      const int64_t k0 = (int64_t)from * G::BK;
-      g.a.start(a.w + (piece0 + k0) * a.row_bytes + (int64_t)c0 * eb, a.row_bytes, a.row_bytes - c0 * eb);
-      g.b.start(a.p + (r0 * pieces.cols + k0) * eb, pieces.cols * eb, BN);
-      // columns of P past the vocabulary are zeros
-      const int64_t left = cols - (int64_t)(to - 1) * G::BK;
-      g.run(ring, to - from, 64, left < G::BK ? (int)left : G::BK, 0, a.row_bytes, pieces.cols * eb);
+    if (unit < w_n) {
+      ce_tile(w_from + unit, units.w_across, w_down, tc, tr);
+      const int c0 = (int)tc * BM;
+      const int64_t v0 = (int64_t)tr * BN;
+      GW g;
+      g.clear();
+      const int steps = (int)blocks_of(m, GW::BK);
+      if (steps > 0) {
+        g.a.start(a.hc + (int64_t)(c0 * eb / PANEL) * a.n * PANEL, a.n * PANEL, a.row_bytes - c0 * eb);
+        g.b.start(a.p + v0 * eb / PANEL * panel, panel, BN * eb);
+        // rows of P past the last are zeros, and whole tiles of rows are there
+        g.begin(lds, steps, m - (steps - 1) * GW::BK, GW::BK);
+        g.finish(lds);
+      }
+      char *mine = lds + wave * (32 * part * eb);
+      const int at = c0 + wm * part;
+      const int row_bytes = (a.d - at < part ? a.d - at : part) * eb;
+#pragma unroll
+      for (int n = 0; n < GW::TN; n++) {
+        const int64_t v = v0 + (wn * GW::TN + n) * 32, left = cols - v;
+        if (row_bytes > 0 && left > 0)
+          store_rows<DT, part, GW::TM>(mine, g.acc[n], back, a.dw + (piece0 + v) * a.row_bytes + (int64_t)at * eb,
+                                       a.row_bytes, left < 32 ? (int)left : 32, row_bytes);
+      }
+    } else {
+      const uint32_t id = h_from + unit - w_n, split = id / h_tiles;
+      ce_tile(id - split * h_tiles, units.h_across, units.h_down, tc, tr);
+      const int c0 = (int)tc * BM;
+      const int64_t r0 = (int64_t)tr * BN;
+      const int steps = (int)blocks_of(cols, GH::BK);
+      const int from = (int)((int64_t)steps * split / units.splits);
+      const int to = (int)((int64_t)steps * (split + 1) / units.splits);
+      GH g;
+      g.clear();
+      if (to > from) {
+        const int64_t k0 = (int64_t)from * GH::BK;
+        g.a.start(a.w + (piece0 + k0) * a.row_bytes + (int64_t)c0 * eb, a.row_bytes, a.row_bytes - c0 * eb);
+        g.b.start(a.p + k0 * eb / PANEL * panel + r0 * PANEL, panel, BN);
+        // columns of P past the vocabulary are zeros
+        const int64_t left = cols - (int64_t)(to - 1) * GH::BK;
+        g.begin(lds, to - from, left < GH::BK ? (int)left : GH::BK, 64);
+        g.finish(lds);
+      }
+      f32x4_t *out = (f32x4_t *)a.dhp + (int64_t)id * (BM * BN / 4) + threadIdx.x;
+#pragma unroll
+      for (int n = 0; n < GH::TN; n++)
+#pragma unroll
+        for (int k = 0; k < GH::TM; k++)
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            f32x4_t y = {g.acc[n][k][4 * q], g.acc[n][k][4 * q + 1], g.acc[n][k][4 * q + 2], g.acc[n][k][4 * q + 3]};
+            f32x4_t *at = out + ((n * GH::TM + k) * 4 + q) * GEMM_THREADS;
+            if (a.piece > 0) y += *at;
+            *at = y;
+          }
     }
-    f32x4_t *out = (f32x4_t *)a.dhp + (int64_t)id * (BM * BN / 4) + threadIdx.x;
-#pragma unroll
-    for (int n = 0; n < G::TN; n++)
-#pragma unroll
-      for (int k = 0; k < G::TM; k++)
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          f32x4_t x = {g.acc[n][k][4 * q], g.acc[n][k][4 * q + 1], g.acc[n][k][4 * q + 2], g.acc[n][k][4 * q + 3]};
-          f32x4_t *at = out + ((n * G::TM + k) * 4 + q) * GEMM_THREADS;
-          if (a.piece > 0) x += *at;
-          *at = x;
-        }
   }
 }
 
 // dh from its parts, rounded once, to the rows' own places.
 template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_dh_join_kernel(CeArgs a) {
-  constexpr int BM = CE_BM, BN = CE_BN, WM = 2;
-  using G = TileGemm<DT, BM, BN, WM, true, false, 3>;
+  constexpr int BM = CE_PM, BN = CE_PN, WM = 2;
+  using G = TileGemm<DT, BM, BN, WM, SIDE_COLS, SIDE_ROWS_P, 3>;
   using T = typename AttnElem<DT>::type;
   typedef T v4 __attribute__((ext_vector_type(4)));
   const int m = uniform(*a.counted);
   const CePieces pieces(m, a.vocab, a.p_elements);
-  const uint32_t across = (uint32_t)blocks_of(a.d, BM), down = (uint32_t)blocks_of(m, BN), tiles = across * down;
-  const uint32_t splits = (uint32_t)ce_splits(tiles, a.slots, pieces.cols, G::BK);
+  const CeUnits<DT> units(a, m, pieces);
+  const uint32_t across = units.h_across, down = units.h_down, tiles = across * down, splits = units.splits;
   const float back = 1.0f / ce_up<DT>(a);
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
   // a block of 32 x 32 of a tile for each round
@@ -443,7 +564,7 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_dh_join_ker
 #pragma unroll
       for (int q = 0; q < 4; q++) x[q] += p[(int64_t)s * tiles * (BM * BN / 4) + q * GEMM_THREADS];
     if (r >= m) continue;
-    T *to = (T *)(a.dh + (int64_t)a.row[r] * a.row_bytes);
+    T *to = (T *)(a.dh + (int64_t)__builtin_bit_cast(CeRow, a.info[r]).row * a.row_bytes);
 #pragma unroll
     for (int q = 0; q < 4; q++) {
       if (c + 8 * q >= a.d) break;  // d is a multiple of 4 entries

@@ -10,8 +10,11 @@ namespace {
 // Room for P, one piece of the vocabulary: what stays in the chip's 256 MiB cache between the kernel
 // that makes it and those that read it, and at least one tile of the vocabulary for all rows.
 constexpr int64_t CE_P_BYTES = (int64_t)256 << 20;
-// dh's tiles in parts: two workgroups a CU
-constexpr int64_t CE_SLOTS = 512;
+// dh's tiles in parts: two for every workgroup that the chip holds (CeUnits)
+constexpr int64_t CE_SLOTS = 1024;
+
+// A step's panels are reached by 32-bit offsets.
+constexpr int64_t CE_MOST_ROWS = (int64_t)1 << 22;
 
 struct Carver {
   char *base;
@@ -24,7 +27,7 @@ struct Carver {
 };
 
 bool ce_sizes(int64_t n, int64_t vocab, int d, int dtype) {
-  return n >= 0 && n < ((int64_t)1 << 31) && vocab >= 1 && vocab < ((int64_t)1 << 31) && d >= 1 &&
+  return n >= 0 && n <= CE_MOST_ROWS && vocab >= 1 && vocab < ((int64_t)1 << 31) && d >= 1 &&
          d <= 16384 && d * elem_bytes(dtype) % 16 == 0;
 }
 
@@ -34,9 +37,8 @@ size_t ce_carve(CeArgs &a, int eb, bool backward, char *base) {
   a.counted = c.take<int32_t>(1);
   a.counts = c.take<int32_t>(blocks_of(a.n, CE_COUNT));
   a.most = c.take<float>(blocks_of(a.n, CE_COUNT));
-  a.row = c.take<int32_t>(a.n);
-  a.label = c.take<int32_t>(a.n);
-  a.hc = c.take<char>(a.n * a.d * eb);
+  a.info = c.take<int4>(a.n);
+  a.hc = c.take<char>(a.n * (blocks_of((int64_t)a.d * eb, PANEL) * PANEL));
   if (!backward) {
     const int64_t tiles = blocks_of(a.vocab, a.n <= 64 ? CE_SMALL_BM : CE_BM);
     a.part = c.take<float2>(tiles * a.n);
@@ -49,9 +51,10 @@ size_t ce_carve(CeArgs &a, int eb, bool backward, char *base) {
   if (p < rows * CE_BM) p = rows * CE_BM;
   a.p_elements = p;
   a.p = c.take<char>(p * eb);
-  a.slots = blocks_of(a.d, CE_BM) * blocks_of(a.n, CE_BN);
+  a.queue = c.take<int32_t>(8);
+  a.slots = blocks_of(a.d, CE_PM) * blocks_of(a.n, CE_PN);
   if (a.slots < CE_SLOTS) a.slots = CE_SLOTS;
-  a.dhp = c.take<float>(a.slots * CE_BM * CE_BN);
+  a.dhp = c.take<float>(a.slots * CE_PM * CE_PN);
   return c.at;
 }
 

@@ -1,10 +1,13 @@
 // Products of two matrices tile by tile, for kernels that go on with a tile in registers:
 //   acc[n][m] += sum over k of A[m][k] * B[k][n]
-// A workgroup of four waves makes a tile of BM x BN, a wave TM x TN blocks of 32x32 of it. Either
-// operand is given in rows along k (ROWS) or in rows of one k each (COLS): the second is what
-// LDS delivers transposed. Tiles of 64 bytes along k go from memory straight into a ring of STAGES
-// places in LDS, swizzled so that neither kind of read meets a bank twice; a place is filled again
-// one step after it was read, so that STAGES - 1 tiles are under way and one barrier a step does.
+// A workgroup of four waves makes a tile of BM x BN, a wave TM x TN blocks of 32x32 of it. An operand
+// is given in rows along k (ROWS) or in rows of one k each (COLS; LDS delivers it transposed), and
+// either as a matrix of rows or in panels: 64 bytes of every row, one row after the other, panel
+// after panel (_P). A step takes 64 bytes along k: of a matrix that is half a cache line of each
+// row, of panels it is one piece, which halves the requests to L2. Steps go from memory straight into
+// a ring of STAGES places in LDS, swizzled so that the reads meet no bank twice; a place is filled
+// again one step after it was read, so that STAGES - 1 steps are under way and one barrier a step
+// does.
 #pragma once
 
 #include "attn_common.hpp"
@@ -12,43 +15,61 @@
 namespace maxsim {
 
 constexpr int GEMM_THREADS = 256;
+constexpr int PANEL = 64;  // bytes of a row in a panel
 
-// One operand's tiles. R: its rows (of the result's side), COLS: rows of one k each.
-template <int DT, int R, bool COLS> struct GemmSide {
+enum { SIDE_ROWS, SIDE_COLS, SIDE_ROWS_P, SIDE_COLS_P };
+
+// One operand's steps. R: its rows, or columns (of the result's side).
+template <int DT, int R, int KIND> struct GemmSide {
   static constexpr int eb = Elem<DT>::bytes;
   static constexpr int BK = 64 / eb;  // of a step
-  using L = RowLayout<DT, COLS ? R : BK>;
+  static constexpr bool along_k = KIND == SIDE_ROWS || KIND == SIDE_ROWS_P;
+  using L = RowLayout<DT, KIND == SIDE_COLS ? R : BK>;  // a row in LDS
   static constexpr int bytes = R * 64;
   static constexpr int pieces = R / 64 < 1 ? 1 : R / 64;  // 16 bytes a thread each
   static constexpr bool partial = R < 64;                  // fewer pieces than threads
   uint32_t at[pieces];
-  uint64_t base;
-  uint32_t step;  // bytes from one step to the next
+  uint64_t base, step;  // and the bytes from one step to the next
+  uint32_t stride;      // of rows, or of k rows
 
-  // ROWS: `first` is row 0 of the tile at k = 0, of which `rows` exist (the last is repeated), with
-  // rows `stride` bytes apart. COLS: `first` is column 0 of the tile at k = 0, of which `rows`
-  // bytes exist (the last 16 are repeated); k rows `stride` bytes apart.
-  __device__ __forceinline__ void start(const char *first, int64_t stride, int rows) {
+  // Piece i of this thread: its row in LDS and the byte within that row; and for panels of columns
+  // the panel.
+  struct Place {
+    int row, byte, panel;
+  };
+  __device__ __forceinline__ static Place place(int i) {
+    const int p = threadIdx.x + i * GEMM_THREADS, q = p / L::chunks;
+    const int r = KIND == SIDE_COLS_P ? q % BK : q;
+    return {r, (p % L::chunks * 16) ^ L::f(r), q / BK};
+  }
+  // first: row or column 0 of the tile at k = 0, of which `exist` rows, or bytes of columns, exist (the
+  // last row, or 16 bytes, is repeated). `by`: a matrix's bytes from row to row, or panels' from one
+  // to the next.
+  __device__ __forceinline__ void start(const char *first, int64_t by, int exist) {
     base = (uint64_t)uniform((int64_t)(uintptr_t)first);
-    step = COLS ? (uint32_t)(BK * stride) : 64u;
+    stride = KIND == SIDE_ROWS || KIND == SIDE_COLS ? (uint32_t)by : PANEL;
+    step = KIND == SIDE_ROWS ? 64 : KIND == SIDE_ROWS_P ? (uint64_t)by : (uint64_t)BK * stride;
 #pragma unroll
     for (int i = 0; i < pieces; i++) {
-      const int p = threadIdx.x + i * GEMM_THREADS;
-      const int r = p / L::chunks, c = (p % L::chunks * 16) ^ L::f(r);
-      if (COLS) at[i] = (uint32_t)(r * stride) + (c < rows ? c : rows - 16);
-      else at[i] = (uint32_t)((r < rows ? r : rows - 1) * stride) + c;
+      const Place p = place(i);
+      if constexpr (along_k) {
+        at[i] = (uint32_t)(p.row < exist ? p.row : exist - 1) * stride + p.byte;
+      } else {
+        int c = KIND == SIDE_COLS ? p.byte : p.panel * PANEL + p.byte;
+        c = c < exist ? c : exist - 16;
+        at[i] = (uint32_t)p.row * stride + (KIND == SIDE_COLS ? (uint32_t)c : (uint32_t)(c / PANEL * by) + c % PANEL);
+      }
     }
   }
   // The last step: `left` bytes (ROWS) or k rows (COLS) of it exist, the last ones are repeated.
-  __device__ __forceinline__ void narrow(int left, int64_t stride) {
+  __device__ __forceinline__ void narrow(int left) {
 #pragma unroll
     for (int i = 0; i < pieces; i++) {
-      const int p = threadIdx.x + i * GEMM_THREADS;
-      const int r = p / L::chunks, c = (p % L::chunks * 16) ^ L::f(r);
-      if (COLS) {
-        if (r >= left) at[i] -= (uint32_t)((r - left + 1) * stride);
-      } else if (c >= left) {
-        at[i] -= (uint32_t)(c - left + 16);
+      const Place p = place(i);
+      if constexpr (along_k) {
+        if (p.byte >= left) at[i] -= (uint32_t)(p.byte - left + 16);
+      } else {
+        if (p.row >= left) at[i] -= (uint32_t)(p.row - left + 1) * stride;
       }
     }
   }
@@ -63,55 +84,55 @@ template <int DT, int R, bool COLS> struct GemmSide {
     }
     base += step;
   }
-  // ROWS: zeros past `left` bytes along k.
-  __device__ __forceinline__ static void clear_from(char *tile, int left) {
-#pragma unroll
-    for (int i = 0; i < pieces; i++) {
-      const int p = threadIdx.x + i * GEMM_THREADS;
-      const int r = p / L::chunks, c = (p % L::chunks * 16) ^ L::f(r);
-      if (p < R * 4 && c >= left) *(u32x4_t *)(tile + p * 16) = u32x4_t{0, 0, 0, 0};
-    }
-  }
   // Loads of one wave (uniform): a partial tile's last waves have none.
   __device__ __forceinline__ static int loads(int wave) {
     return partial ? (wave * 64 < R * 4 ? 1 : 0) : pieces;
   }
 
-  // This lane's place in a block of 32 rows, and the operand of step t (of two) of block `b`.
+  // This lane's place in a block of 32 rows or columns, and the operand of step t (of two) of block
+  // `b`: k = 16 t + 8 h + 0 .. 7 (fp32: 8 t + 4 h + 0 .. 3) in lanes of half h.
   __device__ __forceinline__ static int lane_offset() {
     const int l = threadIdx.x & 63, h = l >> 5;
-    if constexpr (!COLS) return (l & 31) * L::bytes + ((h * 16) ^ L::f(l & 31));
-    else if constexpr (DT == DT_FP32) return 4 * h * L::bytes + (((l & 31) * 4) ^ L::f(4 * h));
-    else {
+    if constexpr (along_k) {
+      return (l & 31) * L::bytes + ((h * 16) ^ L::f(l & 31));
+    } else if constexpr (DT == DT_FP32) {
+      // columns of panels: 16 to a panel
+      const int c = KIND == SIDE_COLS ? l & 31 : l & 15;
+      return 4 * h * L::bytes + ((c * 4) ^ L::f(4 * h)) + (KIND == SIDE_COLS ? 0 : ((l >> 4) & 1) * BK * PANEL);
+    } else {
       const int row = 8 * h + ((l & 15) >> 2);
       return row * L::bytes + ((((l >> 4) & 1) * 32 + (l & 2) * 8) ^ L::f(row)) + (l & 1) * 8;
     }
   }
   __device__ __forceinline__ static u32x4_t operand(const char *tile, int lane, int b, int t) {
-    if constexpr (!COLS) {
+    if constexpr (along_k) {
       return load16(tile + b * 32 * L::bytes + L::along(lane, 32 * t));
     } else if constexpr (DT == DT_FP32) {
       u32x4_t x;
 #pragma unroll
-      for (int e = 0; e < 4; e++)
-        x[e] = *(const uint32_t *)(tile + (8 * t + e) * L::bytes + L::along(lane ^ L::f(8 * t + e), b * 128));
+      for (int e = 0; e < 4; e++) {
+        const int row = 8 * t + e, in = lane ^ L::f(row);
+        x[e] = *(const uint32_t *)(tile + row * L::bytes +
+                                   (KIND == SIDE_COLS ? L::along(in, b * 128) : in + b * 2 * BK * PANEL));
+      }
       return x;
     } else {
       // rows 8 h .. 8 h + 3 and the four after them, whose f differs in its lowest bit
-      const char *at = tile + 16 * t * L::bytes;
-      const s16x4_t lo = read_tr(at + L::along(lane, b * 64));
-      const s16x4_t hi = read_tr(at + 4 * L::bytes + L::along(lane ^ 16, b * 64));
+      const char *at = tile + 16 * t * L::bytes + (KIND == SIDE_COLS ? 0 : b * BK * PANEL);
+      const int by = KIND == SIDE_COLS ? b * 64 : 0;
+      const s16x4_t lo = read_tr(at + L::along(lane, by));
+      const s16x4_t hi = read_tr(at + 4 * L::bytes + L::along(lane ^ 16, by));
       return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
 };
 
-template <int DT, int BM, int BN, int WM, bool ACOLS, bool BCOLS, int STAGES> struct TileGemm {
+template <int DT, int BM, int BN, int WM, int AKIND, int BKIND, int STAGES> struct TileGemm {
   static constexpr int WN = 4 / WM;
   static constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
   static_assert(TM * WM * 32 == BM && TN * WN * 32 == BN, "whole blocks");
-  using A = GemmSide<DT, BM, ACOLS>;
-  using B = GemmSide<DT, BN, BCOLS>;
+  using A = GemmSide<DT, BM, AKIND>;
+  using B = GemmSide<DT, BN, BKIND>;
   static constexpr int stage = A::bytes + B::bytes;
   static constexpr int lds = STAGES * stage;
   static constexpr int BK = A::BK;
@@ -143,55 +164,67 @@ template <int DT, int BM, int BN, int WM, bool ACOLS, bool BCOLS, int STAGES> st
       for (int m = 0; m < TM; m++) acc[n][m] = zero16();
   }
 
-  // The two steps of a place in the ring.
+  // The two steps of a place in the ring. All operands are read before the first product: a wave
+  // waits once a place, and the other one of its SIMD fills that in.
   __device__ __forceinline__ void multiply(const char *tile, int la, int lb, int wm, int wn) {
+    u32x4_t x[2][TM], y[2][TN];
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-      u32x4_t x[TM], y[TN];
 #pragma unroll
-      for (int m = 0; m < TM; m++) x[m] = A::operand(tile, la, wm * TM + m, t);
+      for (int m = 0; m < TM; m++) {
+        if (m < TN) y[t][m] = B::operand(tile + A::bytes, lb, wn * TN + m, t);
+        x[t][m] = A::operand(tile, la, wm * TM + m, t);
+      }
 #pragma unroll
-      for (int n = 0; n < TN; n++) y[n] = B::operand(tile + A::bytes, lb, wn * TN + n, t);
+      for (int n = TM; n < TN; n++) y[t][n] = B::operand(tile + A::bytes, lb, wn * TN + n, t);
+    }
+    keep_order();
+#pragma unroll
+    for (int t = 0; t < 2; t++)
 #pragma unroll
       for (int n = 0; n < TN; n++)
 #pragma unroll
-        for (int m = 0; m < TM; m++) acc[n][m] = mma_rows<DT>(x[m], y[n], acc[n][m]);
-    }
+        for (int m = 0; m < TM; m++) acc[n][m] = mma_rows<DT>(x[t][m], y[t][n], acc[n][m]);
+    keep_order();
   }
 
-  // All steps (at least one). Bytes along k that exist in the last step of ROWS operands: `left` (64
-  // for all); k rows that exist in that of COLS operands: a_last and b_last, the last is repeated.
+  // ---- all steps of a tile (at least one): begin, then finish ----
+  // What exists of the last step along k: a_last and b_last bytes (ROWS; 64 for all) or k rows (COLS;
+  // BK for all). The last bytes or rows are repeated, so one side has to hold zeros there.
+  int steps, fetched, a_last, b_last, to;
+
+  __device__ __forceinline__ void fetch(int ring_at, int wave) {
+    if (fetched == steps - 1) {
+      if (a_last < (A::along_k ? 64 : BK)) a.narrow(a_last);
+      if (b_last < (B::along_k ? 64 : BK)) b.narrow(b_last);
+    }
+    a.go(ring_at + to, wave);
+    b.go(ring_at + to + A::bytes, wave);
+    fetched++;
+    to = to == (STAGES - 1) * stage ? 0 : to + stage;
+  }
+  // The first STAGES - 1 steps' loads, to the first places of a ring that nobody reads; the last
+  // place stays free until finish.
+  __device__ __forceinline__ void begin(char *ring, int n_steps, int last_a, int last_b) {
+    steps = n_steps;
+    a_last = last_a;
+    b_last = last_b;
+    fetched = to = 0;
+    const int wave = uniform((int)threadIdx.x >> 6), ring_at = lds_address(ring);
+    for (int i = 0; i < STAGES - 1; i++)
+      if (fetched < steps) fetch(ring_at, wave);
+  }
   // The ring is free again afterwards.
-  __device__ __forceinline__ void run(char *ring, int steps, int left, int a_last, int b_last, int64_t a_stride,
-                                      int64_t b_stride) {
+  __device__ __forceinline__ void finish(char *ring) {
     const int wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
     const int la = A::lane_offset(), lb = B::lane_offset();
     const int ring_at = lds_address(ring);
     const int loads = A::loads(wave) + B::loads(wave);
-    int fetched = 0, to = 0;
-    auto fetch = [&]() {
-      if (fetched == steps - 1) {
-        if (ACOLS ? a_last < BK : left < 64) a.narrow(ACOLS ? a_last : left, a_stride);
-        if (BCOLS ? b_last < BK : left < 64) b.narrow(BCOLS ? b_last : left, b_stride);
-      }
-      a.go(ring_at + to, wave);
-      b.go(ring_at + to + A::bytes, wave);
-      fetched++;
-      to = to == (STAGES - 1) * stage ? 0 : to + stage;
-    };
-    for (int i = 0; i < STAGES - 1; i++)
-      if (fetched < steps) fetch();
     int from = 0;
     for (int i = 0; i < steps; i++) {
       const int ahead = fetched - i - 1;
       wait(ahead >= STAGES - 2 ? (STAGES - 2) * loads : 0);
-      if (fetched < steps) fetch();
-      if (!ACOLS && i == steps - 1 && left < 64) {
-        // what the last step lacks along k counts as 0: the same loop serves it
-        A::clear_from(ring + from, left);
-        if (!BCOLS) B::clear_from(ring + from + A::bytes, left);
-        wait(0);
-      }
+      if (fetched < steps) fetch(ring_at, wave);
       multiply(ring + from, la, lb, wm, wn);
       from = from == (STAGES - 1) * stage ? 0 : from + stage;
     }
