@@ -6,9 +6,7 @@
 
 namespace maxsim {
 
-constexpr int CE_STAGES = 3, CE_SMALL_STAGES = 6;
-constexpr int64_t CE_FEW = 64;  // rows
-
+constexpr int CE_STAGES = 3, CE_FEW_STAGES = 12;
 template <typename Kernel> int ce_launch(Kernel kernel, int64_t tiles, int lds, int cus, const CeArgs &a, hipStream_t st) {
   // the tiles are dealt out on the device, where their number is known: no more workgroups than
   // there can be tiles, nor than the chip holds at once
@@ -27,25 +25,27 @@ template <int DT> int ce_gathered(const CeArgs &a, bool count, hipStream_t st) {
 }
 
 template <int DT> int ce_forward(const CeArgs &a, int cus, hipStream_t st) {
-  int rc = ce_gathered<DT>(a, a.n > CE_COUNT, st);
-  if (rc != MAXSIM_OK) return rc;
-  const bool few = a.n <= CE_FEW;
-  const int64_t across = blocks_of(a.vocab, few ? CE_SMALL_BM : CE_BM);
-  if (few) {
-    using G = CeLogits<DT, CE_SMALL_BM, CE_SMALL_BN, 4, CE_SMALL_STAGES>;
-    rc = ce_launch(ce_forward_kernel<DT, CE_SMALL_BM, CE_SMALL_BN, 4, CE_SMALL_STAGES>,
-                   across * blocks_of(a.n, CE_SMALL_BN), G::lds, cus, a, st);
+  int across = (int)blocks_of(a.vocab, CE_BM);
+  if (ce_few(a)) {
+    using G = TileGemm<DT, CE_SMALL_BM, CE_SMALL_BN, 4, SIDE_ROWS, SIDE_ROWS, CE_FEW_STAGES>;
+    constexpr int lds = G::lds + CE_FEW * sizeof(CeRow);
+    across = (int)blocks_of(a.vocab, CE_SMALL_BM);
+    const unsigned grid = (unsigned)(across * blocks_of(a.n, CE_SMALL_BN));
+    hipLaunchKernelGGL((ce_few_kernel<DT, CE_FEW_STAGES>), dim3(grid), dim3(GEMM_THREADS), lds, st, a);
+    if (hipGetLastError() != hipSuccess) return MAXSIM_ERR_LAUNCH;
   } else {
-    using G = CeLogits<DT, CE_BM, CE_BN, 2, CE_STAGES>;
-    rc = ce_launch(ce_forward_kernel<DT, CE_BM, CE_BN, 2, CE_STAGES>, across * blocks_of(a.n, CE_BN), G::lds, cus, a, st);
+    using Z = CeLogits<DT, CE_BM, CE_BN, 2, CE_STAGES>;
+    int rc = ce_gathered<DT>(a, a.n > CE_DIRECT, st);
+    if (rc == MAXSIM_OK)
+      rc = ce_launch(ce_forward_kernel<DT, CE_BM, CE_BN, 2, CE_STAGES>, across * blocks_of(a.n, CE_BN), Z::lds, cus, a, st);
+    if (rc != MAXSIM_OK) return rc;
   }
-  if (rc != MAXSIM_OK) return rc;
-  hipLaunchKernelGGL(ce_join_kernel<DT>, dim3((unsigned)blocks_of(a.n, 8)), dim3(GEMM_THREADS), 0, st, a, (int)across);
+  hipLaunchKernelGGL(ce_join_kernel<DT>, dim3((unsigned)blocks_of(a.n, 8)), dim3(GEMM_THREADS), 0, st, a, across);
   return hipGetLastError() == hipSuccess ? MAXSIM_OK : MAXSIM_ERR_LAUNCH;
 }
 
 template <int DT> int ce_backward(CeArgs &a, int64_t pieces, int cus, hipStream_t st) {
-  int rc = ce_gathered<DT>(a, true, st);
+  int rc = ce_gathered<DT>(a, DT == DT_FP16 || a.n > CE_DIRECT, st);
   if (rc != MAXSIM_OK) return rc;
   const int64_t any = (int64_t)1 << 30;
   using Z = CeLogits<DT, CE_BM, CE_BN, 2, CE_STAGES>;

@@ -19,8 +19,10 @@ namespace maxsim {
 constexpr int CE_BM = 128, CE_BN = 256;              // vocabulary x rows of a tile of logits
 constexpr int CE_PM = 256, CE_PN = 128;              // columns x vocabulary (dw) or rows (dh) of a product's
 constexpr int CE_SMALL_BM = 128, CE_SMALL_BN = 32;   // for few rows
-constexpr int CE_GATHER = 32;                        // rows of a workgroup of the gathering
+constexpr int CE_FEW = 64;                           // most rows of the kernel for few rows
+constexpr int CE_GATHER = 16;                        // rows of a workgroup of the gathering
 constexpr int CE_COUNT = 1024;                       // rows of a workgroup of the counting
+constexpr int CE_DIRECT = 8192;                      // up to so many rows the gathering counts for itself
 
 struct CeArgs {
   const char *h, *w;
@@ -47,6 +49,9 @@ struct CeArgs {
   int64_t piece;          // backward: number of this piece
   int lanes;              // backward: workgroups of the products
 };
+
+// Whether the forward takes the kernel for few rows.
+inline bool ce_few(const CeArgs &a) { return a.n <= CE_FEW && a.row_bytes % 64 == 0; }
 
 // A gathered row: its label, its place among all rows, and for the backward its lse in units of log
 // 2 and its gradient times scale.
@@ -84,7 +89,10 @@ template <int DT> struct CeUnits {
     const int64_t room = a.slots / (tiles < 1 ? 1 : tiles), most = steps / 8;
     s = s < room ? s : room;
     s = s < most ? s : most;
-    splits = (uint32_t)(s < 1 ? 1 : s);
+    // a power of two: the parts are dealt to 8 XCDs in order, and one that has parts of two kinds
+    // reads the columns of both (8192 x 30522 x 768: 729 us in 3 parts, 663 in 4, 710 in 6)
+    splits = 1;
+    while (2 * splits <= s) splits *= 2;
   }
 };
 
@@ -139,9 +147,10 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_count_kerne
 // Copies the rows that have a label to their places, in order; the others get their results here.
 template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_gather_kernel(CeArgs a) {
   __shared__ int place[CE_GATHER];
-  const int64_t r0 = (int64_t)blockIdx.x * CE_GATHER, block = r0 / CE_COUNT;
+  const int64_t r0 = (int64_t)blockIdx.x * CE_GATHER, block = a.n > CE_DIRECT ? r0 / CE_COUNT : 0;
   int before = 0;
   for (int64_t i = threadIdx.x; i < block; i += GEMM_THREADS) before += a.counts[i];
+#pragma unroll 4
   for (int64_t r = block * CE_COUNT + threadIdx.x; r < r0; r += GEMM_THREADS)
     before += ce_counts(a, a.labels[r]) ? 1 : 0;
   before = ce_block_sum(before);
@@ -167,8 +176,9 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_gather_kern
     if (threadIdx.x == 0 && r0 + CE_GATHER >= a.n) *a.counted = before + __popcll(all);
   }
   __syncthreads();
-  // two panels at a time: 32 rows x 128 bytes, so that both sides move whole lines
-  const int i = threadIdx.x / 8, c0 = threadIdx.x % 8 * 16;
+  // four panels at a time: 16 rows x 256 bytes, so that both sides move whole lines
+  constexpr int BYTES = GEMM_THREADS / CE_GATHER * 16;
+  const int i = threadIdx.x / (BYTES / 16), c0 = threadIdx.x % (BYTES / 16) * 16;
   if (r0 + i >= a.n) return;
   const int at = place[i];
   const char *from = a.h + (r0 + i) * a.row_bytes;
@@ -176,14 +186,14 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_gather_kern
   if (at >= 0) {
     char *to = a.hc + (int64_t)at * PANEL;
 #pragma unroll 4
-    for (int c = c0; c < padded; c += 128) {
+    for (int c = c0; c < padded; c += BYTES) {
       u32x4_t x = {0, 0, 0, 0};
       if (c < a.row_bytes) x = load16(from + c);
       *(u32x4_t *)(to + (int64_t)(c / PANEL) * a.n * PANEL + c % PANEL) = x;
     }
   } else if (a.dh) {
     char *to = a.dh + (r0 + i) * a.row_bytes;
-    for (int c = c0; c < a.row_bytes; c += 128) *(u32x4_t *)(to + c) = u32x4_t{0, 0, 0, 0};
+    for (int c = c0; c < a.row_bytes; c += BYTES) *(u32x4_t *)(to + c) = u32x4_t{0, 0, 0, 0};
   }
 }
 
@@ -288,71 +298,123 @@ template <int DT, int BM, int BN, int WM, int STAGES> struct CeLogits {
   }
 };
 
-template <int DT, int BM, int BN, int WM, int STAGES>
-__global__ void __launch_bounds__(GEMM_THREADS, 2) ce_forward_kernel(CeArgs a) {
-  using Z = CeLogits<DT, BM, BN, WM, STAGES>;
-  using G = typename Z::G;
-  extern __shared__ __attribute__((aligned(1024))) char lds[];
+// What a tile of logits leaves: for every row the largest logit and the sum of exponentials over the
+// tile, and the label's logit where the tile holds it. label(i): the label of row i of the tile;
+// red: scratch of WM * BN pairs. The workgroup is together again afterwards.
+template <typename G, int BM, int BN, int WM, typename Label>
+__device__ __forceinline__ void ce_tile_sums(const CeArgs &a, G &g, int64_t v0, int64_t r0, int m, float2 *red, Label label) {
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
   const int h4 = 4 * (lane >> 5);
   const float f = a.scale * LOG2E;
-  float2 *red = (float2 *)(lds + Z::scratch);
+  // this wave's part of the vocabulary
+  const int64_t first = v0 + wm * (BM / WM);
+  const int exist = a.vocab - first < BM / WM ? (int)(a.vocab - first) : BM / WM;
+#pragma unroll
+  for (int n = 0; n < G::TN; n++) {
+    f32x16_t(&x)[G::TM] = g.acc[n];
+    const int i = (wn * G::TN + n) * 32 + (lane & 31);
+    const int64_t r = r0 + i;
+    const int at = r < m ? label(i) - (int)first : -1;
+    if (__any(at >= 0 && at < BM / WM)) {
+      float picked = 0.0f;
+#pragma unroll
+      for (int k = 0; k < G::TM; k++)
+#pragma unroll
+        for (int e = 0; e < 16; e++)
+          if (k * 32 + acc_row(e) == at - h4) picked = x[k][e];
+      if (at >= 0 && at < BM / WM && (at & 4) == h4) a.picked[r] = picked * f;
+    }
+    if (exist < BM / WM) {
+#pragma unroll
+      for (int k = 0; k < G::TM; k++)
+#pragma unroll
+        for (int e = 0; e < 16; e++)
+          if (k * 32 + acc_row(e) + h4 >= exist) x[k][e] = -__builtin_inff();
+    }
+    float most = -__builtin_inff();
+#pragma unroll
+    for (int k = 0; k < G::TM; k++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) most = __builtin_fmaxf(most, x[k][e]);
+    most = half_max(most) * f;  // scale is positive
+    const float from = most == -__builtin_inff() ? 0.0f : most;
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < G::TM; k++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(x[k][e], f, -from));
+    sum = half_sum(sum);
+    if (lane < 32) red[wm * BN + i] = make_float2(most, sum);
+  }
+  __syncthreads();
+  if (threadIdx.x < BN && r0 + threadIdx.x < m) {
+    float2 s = red[threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < WM; k++) {
+      const float2 o = red[k * BN + threadIdx.x];
+      const float most = __builtin_fmaxf(s.x, o.x), from = most == -__builtin_inff() ? 0.0f : most;
+      s.y = s.y * __builtin_amdgcn_exp2f(s.x - from) + o.y * __builtin_amdgcn_exp2f(o.x - from);
+      s.x = most;
+    }
+    a.part[v0 / BM * a.n + r0 + threadIdx.x] = s;
+  }
+}
+
+template <int DT, int BM, int BN, int WM, int STAGES>
+__global__ void __launch_bounds__(GEMM_THREADS, 2) ce_forward_kernel(CeArgs a) {
+  using Z = CeLogits<DT, BM, BN, WM, STAGES>;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
   Z z;
   z.start(a, lds, uniform(*a.counted), 0, a.vocab);
-  while (z.tile(a, lds, 0)) {
-    // largest logit and sum of exponentials of each row over this wave's part of the vocabulary
-    const int64_t first = z.v0 + wm * (BM / WM);
-    const int exist = a.vocab - first < BM / WM ? (int)(a.vocab - first) : BM / WM;
-#pragma unroll
-    for (int n = 0; n < G::TN; n++) {
-      f32x16_t(&x)[G::TM] = z.g.acc[n];
-      const int i = (wn * G::TN + n) * 32 + (lane & 31);
-      const int64_t r = z.r0 + i;
-      const int at = r < z.m ? z.row(lds, i).label - (int)first : -1;
-      if (__any(at >= 0 && at < BM / WM)) {
-        float picked = 0.0f;
-#pragma unroll
-        for (int k = 0; k < G::TM; k++)
-#pragma unroll
-          for (int e = 0; e < 16; e++)
-            if (k * 32 + acc_row(e) == at - h4) picked = x[k][e];
-        if (at >= 0 && at < BM / WM && (at & 4) == h4) a.picked[r] = picked * f;
+  while (z.tile(a, lds, 0))
+    ce_tile_sums<typename Z::G, BM, BN, WM>(a, z.g, z.v0, z.r0, z.m, (float2 *)(lds + Z::scratch),
+                                            [&](int i) { return z.row(lds, i).label; });
+}
+
+// Few rows (up to 64, of whole steps): every workgroup finds the ones with a label by itself and
+// reads them where they are, which saves the launch that gathers them; one workgroup a tile. The
+// vocabulary's bytes bound it: as many steps under way as LDS holds.
+template <int DT, int STAGES>
+__global__ void __launch_bounds__(GEMM_THREADS) ce_few_kernel(CeArgs a) {
+  constexpr int BM = CE_SMALL_BM, BN = CE_SMALL_BN, WM = 4;
+  using G = TileGemm<DT, BM, BN, WM, SIDE_ROWS, SIDE_ROWS, STAGES>;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  CeRow *row = (CeRow *)(lds + G::lds);  // of the rows that count
+  const int across = (int)blocks_of(a.vocab, BM), tv = blockIdx.x % across, tr = blockIdx.x / across;
+  int m;
+  {
+    const int r = threadIdx.x & 63;  // in every wave, for m
+    const int64_t label = r < a.n ? a.labels[r] : -1;
+    const bool counts = r < a.n && ce_counts(a, label);
+    const uint64_t all = __ballot(counts);
+    m = __popcll(all);
+    const CeRow mine{(int)label, r, 0.0f, 0.0f};
+    const int at = __popcll(all & ((1ull << r) - 1));
+    if (threadIdx.x < 64) {
+      if (counts) row[at] = mine;
+      if (blockIdx.x == 0) {  // for the joining
+        if (counts) {
+          a.info[at] = __builtin_bit_cast(int4, mine);
+        } else if (r < a.n) {
+          a.loss[r] = 0.0f;
+          a.lse[r] = -__builtin_inff();
+        }
+        if (r == 0) *a.counted = m;
       }
-      if (exist < BM / WM) {
-#pragma unroll
-        for (int k = 0; k < G::TM; k++)
-#pragma unroll
-          for (int e = 0; e < 16; e++)
-            if (k * 32 + acc_row(e) + h4 >= exist) x[k][e] = -__builtin_inff();
-      }
-      float most = -__builtin_inff();
-#pragma unroll
-      for (int k = 0; k < G::TM; k++)
-#pragma unroll
-        for (int e = 0; e < 16; e++) most = __builtin_fmaxf(most, x[k][e]);
-      most = half_max(most) * f;  // scale is positive
-      const float from = most == -__builtin_inff() ? 0.0f : most;
-      float sum = 0.0f;
-#pragma unroll
-      for (int k = 0; k < G::TM; k++)
-#pragma unroll
-        for (int e = 0; e < 16; e++) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(x[k][e], f, -from));
-      sum = half_sum(sum);
-      if (lane < 32) red[wm * BN + i] = make_float2(most, sum);
-    }
-    __syncthreads();
-    if (threadIdx.x < BN && z.r0 + threadIdx.x < z.m) {
-      float2 s = red[threadIdx.x];
-#pragma unroll
-      for (int k = 1; k < WM; k++) {
-        const float2 o = red[k * BN + threadIdx.x];
-        const float most = __builtin_fmaxf(s.x, o.x), from = most == -__builtin_inff() ? 0.0f : most;
-        s.y = s.y * __builtin_amdgcn_exp2f(s.x - from) + o.y * __builtin_amdgcn_exp2f(o.x - from);
-        s.x = most;
-      }
-      a.part[z.v0 / BM * a.n + z.r0 + threadIdx.x] = s;
     }
   }
+  const int64_t v0 = (int64_t)tv * BM, r0 = (int64_t)tr * BN;
+  if (r0 >= m) return;
+  __syncthreads();
+  G g;
+  const int64_t vs = a.vocab - v0;
+  g.a.start(a.w + v0 * a.row_bytes, a.row_bytes, vs < BM ? (int)vs : BM);
+  const int exist = m - (int)r0 < BN ? m - (int)r0 : BN;
+  g.b.start(a.h, a.row_bytes, exist, [&](int i) { return row[r0 + i].row; });
+  g.clear();
+  g.begin(lds, a.row_bytes / 64, 64, 64);
+  g.finish(lds);
+  ce_tile_sums<G, BM, BN, WM>(a, g, v0, r0, m, (float2 *)lds, [&](int i) { return row[r0 + i].label; });
 }
 
 // lse and loss of a row from its tiles' parts: 8 rows a workgroup, 32 threads to each.

@@ -9,7 +9,7 @@ namespace {
 
 // Room for P, one piece of the vocabulary: what stays in the chip's 256 MiB cache between the kernel
 // that makes it and those that read it, and at least one tile of the vocabulary for all rows.
-constexpr int64_t CE_P_BYTES = (int64_t)256 << 20;
+constexpr int64_t CE_P_BYTES = (int64_t)512 << 20;
 // dh's tiles in parts: two for every workgroup that the chip holds (CeUnits)
 constexpr int64_t CE_SLOTS = 1024;
 
@@ -40,7 +40,7 @@ size_t ce_carve(CeArgs &a, int eb, bool backward, char *base) {
   a.info = c.take<int4>(a.n);
   a.hc = c.take<char>(a.n * (blocks_of((int64_t)a.d * eb, PANEL) * PANEL));
   if (!backward) {
-    const int64_t tiles = blocks_of(a.vocab, a.n <= 64 ? CE_SMALL_BM : CE_BM);
+    const int64_t tiles = blocks_of(a.vocab, CE_SMALL_BM < CE_BM ? CE_SMALL_BM : CE_BM);
     a.part = c.take<float2>(tiles * a.n);
     a.picked = c.take<float>(a.n);
     return c.at;

@@ -46,6 +46,10 @@ template <int DT, int R, int KIND> struct GemmSide {
   // last row, or 16 bytes, is repeated). `by`: a matrix's bytes from row to row, or panels' from one
   // to the next.
   __device__ __forceinline__ void start(const char *first, int64_t by, int exist) {
+    start(first, by, exist, [](int row) { return row; });
+  }
+  // row(i): which of the matrix's rows is row i (ROWS).
+  template <typename Row> __device__ __forceinline__ void start(const char *first, int64_t by, int exist, Row row) {
     base = (uint64_t)uniform((int64_t)(uintptr_t)first);
     stride = KIND == SIDE_ROWS || KIND == SIDE_COLS ? (uint32_t)by : PANEL;
     step = KIND == SIDE_ROWS ? 64 : KIND == SIDE_ROWS_P ? (uint64_t)by : (uint64_t)BK * stride;
@@ -53,7 +57,7 @@ template <int DT, int R, int KIND> struct GemmSide {
     for (int i = 0; i < pieces; i++) {
       const Place p = place(i);
       if constexpr (along_k) {
-        at[i] = (uint32_t)(p.row < exist ? p.row : exist - 1) * stride + p.byte;
+        at[i] = (uint32_t)row(p.row < exist ? p.row : exist - 1) * stride + p.byte;
       } else {
         int c = KIND == SIDE_COLS ? p.byte : p.panel * PANEL + p.byte;
         c = c < exist ? c : exist - 16;
@@ -143,13 +147,14 @@ template <int DT, int BM, int BN, int WM, int AKIND, int BKIND, int STAGES> stru
 
   // Until at most n of this wave's loads are under way, its LDS reads are done, and so is every
   // other wave: s_waitcnt takes a constant.
+  // (counts that have no case wait for all)
   __device__ __forceinline__ static void wait(int n) {
     asm volatile("" ::: "memory");
     switch (n) {
     case 0: __builtin_amdgcn_s_waitcnt(0x0070); break;
 #define MAXSIM_WAIT(N) case N: __builtin_amdgcn_s_waitcnt(0x0070 | ((N) & 15) | ((N) >> 4) << 14); break;
     MAXSIM_WAIT(1) MAXSIM_WAIT(2) MAXSIM_WAIT(3) MAXSIM_WAIT(4) MAXSIM_WAIT(5) MAXSIM_WAIT(6)
-    MAXSIM_WAIT(8) MAXSIM_WAIT(10) MAXSIM_WAIT(12) MAXSIM_WAIT(15) MAXSIM_WAIT(16)
+    MAXSIM_WAIT(8) MAXSIM_WAIT(12) MAXSIM_WAIT(20) MAXSIM_WAIT(30)
 #undef MAXSIM_WAIT
     default: __builtin_amdgcn_s_waitcnt(0x0070); break;
     }
