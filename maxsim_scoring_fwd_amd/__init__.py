@@ -550,6 +550,14 @@ def _like(t: torch.Tensor, stream) -> torch.Tensor:
     return _new(t.shape, t.dtype, t.device, stream)
 
 
+def _beside(t: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """A new tensor on t's device, for work on `stream`."""
+    if stream is None:
+        # numbers are read faster than a shape
+        return t.new_empty(*shape, dtype=dtype) if shape else t.new_empty((), dtype=dtype)
+    return _new(shape, dtype, t.device, stream)
+
+
 _ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
 
 
@@ -825,6 +833,8 @@ def _rows(t: torch.Tensor, name: str):
 
 def _chance(dropout: float, rng, call: int) -> float:
     """dropout as a number, with the checks of what belongs to it."""
+    if not dropout and rng is None and not call:
+        return 0.0
     dropout = float(dropout)
     if not 0 <= dropout <= 1:
         raise ValueError(f"dropout must lie in [0, 1], got {dropout}")
@@ -880,7 +890,16 @@ def dropout(x: torch.Tensor, dropout: float, rng: torch.Tensor, call: int = 0) -
 
 
 def _norm_args(x, weight, residual, eps):
-    """(rows, row stride of x, of the residual) of a norm, checked."""
+    """(rows, row stride of x, of the residual) of a norm, checked: what most calls are in one
+    condition, the others one by one."""
+    tensor = torch.Tensor
+    if isinstance(x, tensor) and isinstance(weight, tensor):
+        shape, dt = x.shape, x.dtype
+        if dt in _TORCH_DTYPE and x.is_contiguous() and eps >= 0 and weight.shape == shape[-1:] and \
+                (weight.dtype == dt or weight.dtype == torch.float32) and x.numel() and \
+                (residual is None or (isinstance(residual, tensor) and residual.dtype == dt and
+                                      residual.shape == shape and residual.is_contiguous())):
+            return x.numel() // shape[-1], shape[-1], shape[-1]
     _need(x, "x", _FLOAT_STORAGE)
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x needs rows of at least one entry")
@@ -910,12 +929,15 @@ def maxsim_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tenso
         _need(out, "out", dt, shape=x.shape)
     h = None
     if residual is not None or dropout:
-        h = _like(x, stream) if out_h is None else out_h
-        _need(h, "out_h", dt, shape=x.shape)
+        if out_h is None:
+            h = _like(x, stream)
+        else:
+            h = out_h
+            _need(h, "out_h", dt, shape=x.shape)
     elif out_h is not None:
         raise ValueError("out_h needs a residual or dropout: h is x itself")
     if rstd is None:
-        rstd = _new(x.shape[:-1], torch.float32, x.device, stream)
+        rstd = _beside(x, x.shape[:-1], torch.float32, stream)
     else:
         _need(rstd, "rstd", torch.float32, shape=x.shape[:-1])
     _check(lib().maxsim_rms_norm(
@@ -932,16 +954,21 @@ def maxsim_rms_norm_i8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Te
     scale fp32 [...], h) with y = codes * scale, scale a row's largest |y| / 127."""
     n, stride, r_stride = _norm_args(x, weight, residual, eps)
     dt, at = x.dtype, x.get_device()
-    _need(out, "out", torch.int8, shape=x.shape)
-    _need(scale, "scale", torch.float32, shape=x.shape[:-1])
     if out is None:
-        out = _new(x.shape, torch.int8, x.device, stream)
+        out = _beside(x, x.shape, torch.int8, stream)
+    else:
+        _need(out, "out", torch.int8, shape=x.shape)
     if scale is None:
-        scale = _new(x.shape[:-1], torch.float32, x.device, stream)
+        scale = _beside(x, x.shape[:-1], torch.float32, stream)
+    else:
+        _need(scale, "scale", torch.float32, shape=x.shape[:-1])
     h = None
     if residual is not None:
-        h = _like(x, stream) if out_h is None else out_h
-        _need(h, "out_h", dt, shape=x.shape)
+        if out_h is None:
+            h = _like(x, stream)
+        else:
+            h = out_h
+            _need(h, "out_h", dt, shape=x.shape)
     elif out_h is not None:
         raise ValueError("out_h needs a residual: h is x itself")
     _check(lib().maxsim_rms_norm_i8(
@@ -986,9 +1013,9 @@ def maxsim_rms_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torc
     elif want_dx and dx is None:
         dx = _like(h, stream)
     if want_dweight and dweight is None:
-        dweight = _new(weight.shape, weight.dtype, h.device, stream)
+        dweight = _beside(h, weight.shape, weight.dtype, stream)
     if want_dweight and workspace is None:
-        workspace = _new(rms_norm_backward_workspace_size(n, d), torch.uint8, h.device, stream)
+        workspace = _beside(h, (rms_norm_backward_workspace_size(n, d),), torch.uint8, stream)
     dx = dx if want_dx else None
     dresidual = dresidual if want_dresidual else None
     dweight = dweight if want_dweight else None
@@ -1080,16 +1107,19 @@ def maxsim_linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, labels: torch.
     label lies outside the vocabulary is left out: loss 0, lse -inf, and no work. Returns (loss, lse)
     fp32 [n_rows]."""
     n, vocab, d, scale, at = _loss_args(h, w, labels, scale)
-    _need(loss, "loss", torch.float32, shape=(n,))
-    _need(lse, "lse", torch.float32, shape=(n,))
-    _need(workspace, "workspace", torch.uint8)
     if loss is None:
-        loss = _new((n,), torch.float32, h.device, stream)
+        loss = _beside(h, (n,), torch.float32, stream)
+    else:
+        _need(loss, "loss", torch.float32, shape=(n,))
     if lse is None:
-        lse = _new((n,), torch.float32, h.device, stream)
+        lse = _beside(h, (n,), torch.float32, stream)
+    else:
+        _need(lse, "lse", torch.float32, shape=(n,))
     if workspace is None:
-        workspace = _new(linear_cross_entropy_workspace_size(n, vocab, d, h.dtype), torch.uint8,
-                         h.device, stream)
+        size = linear_cross_entropy_workspace_size(n, vocab, d, h.dtype)
+        workspace = _beside(h, (size,), torch.uint8, stream)
+    else:
+        _need(workspace, "workspace", torch.uint8)
     _check(lib().maxsim_linear_cross_entropy(
         _at(h, "h", at), _at(w, "w", at), _at(labels, "labels", at), n, vocab, d,
         _TORCH_DTYPE[h.dtype], scale, _at(loss, "loss", at), _at(lse, "lse", at),
@@ -1116,8 +1146,8 @@ def maxsim_linear_cross_entropy_backward(grad_loss: torch.Tensor, h: torch.Tenso
     if want_dw and dw is None:
         dw = _like(w, stream)
     if workspace is None:
-        workspace = _new(linear_cross_entropy_backward_workspace_size(n, vocab, d, h.dtype),
-                         torch.uint8, h.device, stream)
+        size = linear_cross_entropy_backward_workspace_size(n, vocab, d, h.dtype)
+        workspace = _beside(h, (size,), torch.uint8, stream)
     dh, dw = dh if want_dh else None, dw if want_dw else None
     _check(lib().maxsim_linear_cross_entropy_backward(
         _at(grad_loss, "grad_loss", at), _at(h, "h", at), _at(w, "w", at), _at(labels, "labels", at),
@@ -1231,12 +1261,15 @@ def maxsim_quantize_mx4(x: torch.Tensor, codes=None, scales=None, stream=None):
     d = x.shape[-1] if x.dim() else 0
     if d < 32 or d % 32:
         raise ValueError(f"x needs rows of whole 32 entries, got shape {tuple(x.shape)}")
-    _need(codes, "codes", torch.uint8, shape=(*x.shape[:-1], d // 2))
-    _need(scales, "scales", torch.uint8, shape=(*x.shape[:-1], d // 32))
+    rows = x.shape[:-1]
     if codes is None:
-        codes = _new((*x.shape[:-1], d // 2), torch.uint8, x.device, stream)
+        codes = _beside(x, (*rows, d // 2), torch.uint8, stream)
+    else:
+        _need(codes, "codes", torch.uint8, shape=(*rows, d // 2))
     if scales is None:
-        scales = _new((*x.shape[:-1], d // 32), torch.uint8, x.device, stream)
+        scales = _beside(x, (*rows, d // 32), torch.uint8, stream)
+    else:
+        _need(scales, "scales", torch.uint8, shape=(*rows, d // 32))
     at = x.get_device()
     _check(lib().maxsim_quantize_mx4(
         _at(x, "x", at), x.numel() // d, d, _TORCH_DTYPE[x.dtype], _at(codes, "codes", at),
@@ -1260,9 +1293,10 @@ def maxsim_dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch
     if dtype not in _TORCH_DTYPE:
         raise ValueError(f"unsupported dtype {dtype}")
     shape = (*codes.shape[:-1], d)
-    _need(out, "out", dtype, shape=shape)
     if out is None:
-        out = _new(shape, dtype, codes.device, stream)
+        out = _beside(codes, shape, dtype, stream)
+    else:
+        _need(out, "out", dtype, shape=shape)
     at = codes.get_device()
     _check(lib().maxsim_dequantize_mx4(
         _at(codes, "codes", at), _at(scales, "scales", at), out.numel() // d, d, _TORCH_DTYPE[dtype],

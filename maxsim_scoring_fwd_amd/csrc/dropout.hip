@@ -15,42 +15,42 @@ namespace {
 constexpr int DROP_THREADS = 256;
 constexpr int DROP_PER = 4;  // chunks of a thread
 
-template <typename T>
+// DROP: else a copy (p = 0, and p that rounds to it).
+template <typename T, bool DROP>
 __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const T *x, T *y, int64_t n, int64_t first,
                                                                DropArgs drop) {
-  DropKey key;
-  key.load(drop.rng);
-  const int64_t base = first + (int64_t)blockIdx.x * (DROP_THREADS * DROP_PER * 8);
-  const int left = (int)(n - base < DROP_THREADS * DROP_PER * 8 ? n - base : DROP_THREADS * DROP_PER * 8);
-  float v[DROP_PER][8];
+  constexpr int PER = DROP_THREADS * DROP_PER * 8;
+  DropKey key{};
+  if (DROP) key.load(drop.rng);
+  const int64_t base = first + (int64_t)blockIdx.x * PER;
+  auto run = [&](int at, float (&v)[8]) {
+    if (!DROP) return;
+    DropBits bits;
+    bits.make(key, drop, (uint64_t)(base + at) >> 3);
 #pragma unroll
-  for (int i = 0; i < DROP_PER; i++) {
-    const int at = (i * DROP_THREADS + threadIdx.x) * 8;
-    if (at < left) load_chunk(x + base, at, left, v[i]);
-  }
+    for (int e = 0; e < 8; e++) v[e] = bits.apply(drop, e, v[e]);
+  };
+  if (n - base >= PER) {  // all of a thread's loads are under way at once
+    Chunk8<T> c[DROP_PER];
 #pragma unroll
-  for (int i = 0; i < DROP_PER; i++) {
-    const int at = (i * DROP_THREADS + threadIdx.x) * 8;
-    if (at >= left) break;
-    const uint32_t keep = drop_keep(key, drop, (uint64_t)(base + at) >> 3);
+    for (int i = 0; i < DROP_PER; i++) c[i] = whole_chunk(x + base + (i * DROP_THREADS + threadIdx.x) * 8);
 #pragma unroll
-    for (int e = 0; e < 8; e++) v[i][e] = keep >> e & 1 ? v[i][e] * drop.up : 0.0f;
-    store_chunk(y + base, at, left, v[i]);
-  }
-}
-
-// p = 0, and p that rounds to it: a copy.
-template <typename T>
-__global__ void __launch_bounds__(DROP_THREADS) keep_kernel(const T *x, T *y, int64_t n, int64_t first) {
-  const int64_t base = first + (int64_t)blockIdx.x * (DROP_THREADS * DROP_PER * 8);
-  const int left = (int)(n - base < DROP_THREADS * DROP_PER * 8 ? n - base : DROP_THREADS * DROP_PER * 8);
+    for (int i = 0; i < DROP_PER; i++) {
+      const int at = (i * DROP_THREADS + threadIdx.x) * 8;
+      float v[8];
 #pragma unroll
-  for (int i = 0; i < DROP_PER; i++) {
-    const int at = (i * DROP_THREADS + threadIdx.x) * 8;
-    if (at >= left) break;
-    float v[8];
-    load_chunk(x + base, at, left, v);
-    store_chunk(y + base, at, left, v);
+      for (int e = 0; e < 8; e++) v[e] = (float)c[i].e[e];
+      run(at, v);
+      *(Chunk8<T> *)(y + base + at) = rounded<T>(v);
+    }
+  } else {
+    const int left = (int)(n - base);
+    for (int at = threadIdx.x * 8; at < left; at += DROP_THREADS * 8) {
+      float v[8];
+      load_chunk(x + base, at, left, v);
+      run(at, v);
+      store_chunk(y + base, at, left, v);
+    }
   }
 }
 
@@ -61,10 +61,11 @@ int dropout_run(const void *x, int64_t n, const DropArgs &drop, void *out, hipSt
     const int64_t left = (n - first + per - 1) / per;
     const unsigned grid = (unsigned)(left < (int64_t)LAUNCH_MOST ? left : LAUNCH_MOST);
     if (drop.rng)
-      hipLaunchKernelGGL(dropout_kernel<T>, dim3(grid), dim3(DROP_THREADS), 0, st, (const T *)x, (T *)out, n,
+      hipLaunchKernelGGL((dropout_kernel<T, true>), dim3(grid), dim3(DROP_THREADS), 0, st, (const T *)x, (T *)out, n,
                          first, drop);
     else
-      hipLaunchKernelGGL(keep_kernel<T>, dim3(grid), dim3(DROP_THREADS), 0, st, (const T *)x, (T *)out, n, first);
+      hipLaunchKernelGGL((dropout_kernel<T, false>), dim3(grid), dim3(DROP_THREADS), 0, st, (const T *)x, (T *)out, n,
+                         first, drop);
     if (hipGetLastError() != hipSuccess) return MAXSIM_ERR_LAUNCH;
   }
   return MAXSIM_OK;

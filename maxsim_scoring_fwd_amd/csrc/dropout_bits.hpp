@@ -41,28 +41,33 @@ struct DropKey {
   }
 };
 
-// The 8 entries of block `at`: bit e of the result is set where entry e is kept.
-__device__ __forceinline__ uint32_t drop_keep(const DropKey &key, const DropArgs &a, uint64_t at) {
-  uint32_t c0 = (uint32_t)at, c1 = (uint32_t)(at >> 32), c2 = key.step, c3 = a.call;
-  uint32_t k0 = key.k0, k1 = key.k1;
+// The bits of a block: 16 for each of its 8 entries.
+struct DropBits {
+  uint32_t w[4];
+  __device__ __forceinline__ void make(const DropKey &key, const DropArgs &a, uint64_t block) {
+    uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = key.step, c3 = a.call;
+    uint32_t k0 = key.k0, k1 = key.k1;
+    constexpr int XOR3 = 0x96;  // truth table of a ^ b ^ c
 #pragma unroll
-  for (int r = 0; r < DROP_ROUNDS; r++) {
-    const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
-    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
-    c1 = (uint32_t)p1;
-    c3 = (uint32_t)p0;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
+    for (int r = 0; r < DROP_ROUNDS; r++) {
+      const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
+      c0 = __builtin_amdgcn_bitop3_b32((uint32_t)(p1 >> 32), c1, k0, XOR3);
+      c2 = __builtin_amdgcn_bitop3_b32((uint32_t)(p0 >> 32), c3, k1, XOR3);
+      c1 = (uint32_t)p1;
+      c3 = (uint32_t)p0;
+      k0 += 0x9E3779B9u;
+      k1 += 0xBB67AE85u;
+    }
+    w[0] = c0;
+    w[1] = c1;
+    w[2] = c2;
+    w[3] = c3;
   }
-  const uint32_t w[4] = {c0, c1, c2, c3};
-  uint32_t keep = 0;
-#pragma unroll
-  for (int e = 0; e < 4; e++) {
-    keep |= (w[e] & 0xffffu) >= a.least ? 1u << 2 * e : 0u;
-    keep |= w[e] >> 16 >= a.least ? 2u << 2 * e : 0u;
+  // x * up where entry e (a constant) is kept, else 0.
+  __device__ __forceinline__ float apply(const DropArgs &a, int e, float x) const {
+    const uint32_t u = e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
+    return u >= a.least ? __fmul_rn(x, a.up) : 0.0f;
   }
-  return keep;
-}
+};
 
 }  // namespace maxsim

@@ -22,26 +22,29 @@ __device__ __forceinline__ float power_of(uint32_t byte) {
 }
 
 // Chunks of 8 entries; four neighbouring lanes hold a block of 32. n: chunks, a multiple of 4, so
-// that the lanes of a block are in or out together.
+// that the lanes of a block are in or out together. A thread past the end takes the last chunks
+// again and stores nothing: no branch before the loads, which are all under way at once.
 template <typename T>
 __global__ void __launch_bounds__(MX4_THREADS) mx4_quantize_kernel(const T *x, uint32_t *codes, uint8_t *scales,
                                                                    int64_t n, int64_t first) {
   const int64_t base = first + (int64_t)blockIdx.x * (MX4_THREADS * MX4_PER) + threadIdx.x;
-  float v[MX4_PER][8];
+  const int64_t last = n - 4 + (threadIdx.x & 3);
+  Chunk8<T> c[MX4_PER];
 #pragma unroll
   for (int i = 0; i < MX4_PER; i++) {
     const int64_t at = base + i * MX4_THREADS;
-    if (at < n) load_chunk(x + at * 8, 0, 8, v[i]);
+    c[i] = whole_chunk(x + (at < n ? at : last) * 8);
   }
 #pragma unroll
   for (int i = 0; i < MX4_PER; i++) {
     const int64_t at = base + i * MX4_THREADS;
-    if (at >= n) break;
+    float v[8];
     // bit patterns of absolute values: a NaN is above infinity, infinity above all numbers
     uint32_t most = 0;
 #pragma unroll
     for (int e = 0; e < 8; e++) {
-      const uint32_t b = __float_as_uint(v[i][e]) & 0x7fffffffu;
+      v[e] = (float)c[i].e[e];
+      const uint32_t b = __float_as_uint(v[e]) & 0x7fffffffu;
       most = b > most ? b : most;
     }
     uint32_t o = __builtin_amdgcn_update_dpp(0u, most, DPP_XOR1, 0xF, 0xF, true);
@@ -53,18 +56,14 @@ __global__ void __launch_bounds__(MX4_THREADS) mx4_quantize_kernel(const T *x, u
     const uint32_t byte = finite ? (ex > 2 ? ex - 2 : 0) : 255;
     const float to = finite ? power_of(254 - byte) : 0.0f;
     uint32_t q = 0;
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-      const float lo = v[i][2 * e] * to, hi = v[i][2 * e + 1] * to;
-      switch (e) {
-      case 0: q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, lo, hi, 1.0f, 0); break;
-      case 1: q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, lo, hi, 1.0f, 1); break;
-      case 2: q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, lo, hi, 1.0f, 2); break;
-      default: q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, lo, hi, 1.0f, 3); break;
-      }
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0] * to, v[1] * to, 1.0f, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2] * to, v[3] * to, 1.0f, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4] * to, v[5] * to, 1.0f, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6] * to, v[7] * to, 1.0f, 3);
+    if (at < n) {
+      codes[at] = finite ? q : 0;
+      if ((threadIdx.x & 3) == 0) scales[at >> 2] = (uint8_t)byte;
     }
-    codes[at] = finite ? q : 0;
-    if ((threadIdx.x & 3) == 0) scales[at >> 2] = (uint8_t)byte;
   }
 }
 
@@ -76,15 +75,13 @@ __global__ void __launch_bounds__(MX4_THREADS) mx4_values_kernel(const uint32_t 
   uint32_t q[MX4_PER], byte[MX4_PER];
 #pragma unroll
   for (int i = 0; i < MX4_PER; i++) {
-    const int64_t at = base + i * MX4_THREADS;
-    if (at >= n) break;
-    q[i] = codes[at];
-    byte[i] = scales[at >> 2];
+    const int64_t at = base + i * MX4_THREADS, in = at < n ? at : n - 1;
+    q[i] = codes[in];
+    byte[i] = scales[in >> 2];
   }
 #pragma unroll
   for (int i = 0; i < MX4_PER; i++) {
     const int64_t at = base + i * MX4_THREADS;
-    if (at >= n) break;
     const float by = byte[i] < 255 ? power_of(byte[i]) : __builtin_nanf("");
     const f32x2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 0),
                         __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 1),
@@ -93,7 +90,7 @@ __global__ void __launch_bounds__(MX4_THREADS) mx4_values_kernel(const uint32_t 
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; e++) v[e] = p[e / 2][e & 1] * by;
-    store_chunk(x + at * 8, 0, 8, v);
+    if (at < n) *(Chunk8<T> *)(x + at * 8) = rounded<T>(v);
   }
 }
 

@@ -13,6 +13,7 @@
 #pragma once
 
 #include "dense_kernel.hpp"
+#include "doc_lookup.hpp"
 
 namespace maxsim {
 
@@ -31,6 +32,35 @@ __device__ __forceinline__ f32x4_t mfma_mx4(u32x4_t a, uint32_t sa, u32x4_t b, u
   const i32x8_t y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
   constexpr int FP4 = 4;
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, FP4, FP4, 0, (int)sa, 0, (int)sb);
+}
+
+// The document boundaries nearest to the token targets lo and hi, as nearest_boundary finds one: the
+// halves of the wave search for one each, which takes half as many loads that wait for each other.
+__device__ __forceinline__ void nearest_boundaries(const int64_t *off, int64_t n_docs, int64_t lo, int64_t hi,
+                                                   int lane, int64_t &first, int64_t &end) {
+  const int64_t target = lane < 32 ? lo : hi;
+  int64_t a = 0, b = n_docs + 1;  // the first offset that is not below the target lies in [a, b]
+  while (__any(a < b)) {
+    const int64_t step = (b - a + 31) / 32, at = a + (lane & 31) * step;
+    const bool less = at < b && off[at] < target;  // these are a prefix of the probes
+    const uint64_t all = __ballot(less);
+    const int n = __popc((uint32_t)(all >> (lane & 32)));
+    if (a < b) {
+      const int64_t next = a + n * step;
+      if (n == 0) {
+        b = a;
+      } else {
+        a = next - step + 1;
+        b = next < b ? next : b;
+      }
+    }
+  }
+  if (a > 0) {
+    const int64_t below = off[a - 1], above = a <= n_docs ? off[a] : below;
+    if (a > n_docs || target - below < above - target) a--;
+  }
+  first = lane_value(a, 0);
+  end = lane_value(a, 32);
 }
 
 // KS: steps of 128 entries in a row; QB: blocks of 16 query tokens; P: tiles in flight; QLDS: the
@@ -94,8 +124,8 @@ __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
     const int64_t t0 = uniform(a.doc.offsets[0]);
     const int64_t ntok = uniform(a.doc.offsets[a.doc.n_docs]) - t0;
     const int64_t lo = t0 + ntok * wave / nwaves, hi = t0 + ntok * (wave + 1) / nwaves;
-    pb = nearest_boundary(a.doc.offsets, a.doc.n_docs, lo, lane);
-    pend = wave == nwaves - 1 ? a.doc.n_docs : nearest_boundary(a.doc.offsets, a.doc.n_docs, hi, lane);
+    nearest_boundaries(a.doc.offsets, a.doc.n_docs, lo, hi, lane, pb, pend);
+    if (wave == nwaves - 1) pend = a.doc.n_docs;
     if (wave == 0) pb = 0;
     pstep = 1;
   } else if (a.doc.contiguous) {

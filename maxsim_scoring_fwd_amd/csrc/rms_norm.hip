@@ -4,6 +4,8 @@
 // registers, so that each tensor is read and written once.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "dropout_bits.hpp"
 #include "host_common.hpp"
@@ -16,14 +18,13 @@ namespace {
 
 constexpr int NORM_THREADS = 256;
 constexpr int NORM_MOST_D = MAXSIM_MAX_NORM;
-constexpr int NORM_CHUNKS = 4;  // most chunks of 8 entries that a lane holds
 
 struct NormArgs {
   const void *x, *residual, *weight;
   int64_t x_stride, residual_stride;  // entries
   int64_t first, rows;                // first row of this launch, all rows
-  int d, weight_fp32;
-  float eps;
+  int d;
+  float eps, one_over_d;
   DropArgs drop;
   void *y, *h;
   int8_t *codes;
@@ -86,110 +87,126 @@ template <int G> __device__ __forceinline__ uint32_t group_max(uint32_t v, float
   return v;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_weight(const NormArgs &a, int at, float (&w)[8]) {
-  if (a.weight_fp32) load_chunk((const float *)a.weight, at, a.d, w);
-  else load_chunk((const T *)a.weight, at, a.d, w);
-}
-
-// A row's 8 kept entries of dropout are in block row * ceil(d / 8) + column / 8.
+// A row's entry e has bits e % 8 of block row * ceil(d / 8) + e / 8.
 __device__ __forceinline__ uint64_t drop_block(int64_t row, int d, int chunk) {
   return (uint64_t)row * (uint32_t)((d + 7) / 8) + chunk;
 }
 
-// T: storage type, G: lanes of a row, C: chunks of a lane (lane l of the group holds chunks l,
-// l + G, ...). I8: 8-bit output.
-template <typename T, int G, int C, bool I8>
-__global__ void __launch_bounds__(NORM_THREADS) norm_kernel(NormArgs a) {
-  __shared__ float lds[4];
-  const int lane = threadIdx.x % G;
-  const int64_t row = a.first + (int64_t)blockIdx.x * (NORM_THREADS / G) + threadIdx.x / G;
-  const bool real = row < a.rows;  // every lane takes part in the reductions
-  const T *x = (const T *)a.x + row * a.x_stride;
-  const T *r = a.residual ? (const T *)a.residual + row * a.residual_stride : nullptr;
-  DropKey key{};
-  if (a.drop.rng) key.load(a.drop.rng);
-  float h[C][8], res[C][8];
-#pragma unroll
-  for (int c = 0; c < C; c++) {
-    const int at = (c * G + lane) * 8;
-#pragma unroll
-    for (int e = 0; e < 8; e++) h[c][e] = 0.0f;
-    if (real && at < a.d) {
-      load_chunk(x, at, a.d, h[c]);
-      if (r) load_chunk(r, at, a.d, res[c]);
-    }
-  }
-  float squares = 0.0f;
-#pragma unroll
-  for (int c = 0; c < C; c++) {
-    const int at = (c * G + lane) * 8;
-    if (!real || at >= a.d) continue;
-    if (a.drop.rng) {
-      const uint32_t keep = drop_keep(key, a.drop, drop_block(row, a.d, at / 8));
-      // the product and the sum are rounded apart: what is handed on does not depend on the compiler
-#pragma unroll
-      for (int e = 0; e < 8; e++) h[c][e] = keep >> e & 1 ? __fmul_rn(h[c][e], a.drop.up) : 0.0f;
-    }
-    if (r) {
-#pragma unroll
-      for (int e = 0; e < 8; e++) h[c][e] = __fadd_rn(h[c][e], res[c][e]);
-    }
-    // The norm is of h as it is handed on, rounded: the backward, which reads that h, is the
-    // derivative of just this function.
-#pragma unroll
-    for (int e = 0; e < 8; e++) h[c][e] = (float)(T)h[c][e];
-    if (a.h) store_chunk((T *)a.h + row * a.d, at, a.d, h[c]);
-    if (a.d - at < 8) {
-#pragma unroll
-      for (int e = 0; e < 8; e++)
-        if (at + e >= a.d) h[c][e] = 0.0f;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; e++) squares = __builtin_fmaf(h[c][e], h[c][e], squares);
-  }
-  squares = group_sum<G>(squares, lds);
-  const float rstd = 1.0f / __builtin_sqrtf(squares / (float)a.d + a.eps);
-  if (!I8 && a.rstd && real && lane == 0) a.rstd[row] = rstd;
-  uint32_t most = 0;
-#pragma unroll
-  for (int c = 0; c < C; c++) {
-    const int at = (c * G + lane) * 8;
-    if (!real || at >= a.d) continue;
-    float w[8];
-    load_weight<T>(a, at, w);
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      h[c][e] = h[c][e] * rstd * w[e];
-      if (I8 && at + e < a.d) most = max_u32(most, __float_as_uint(h[c][e]) & 0x7fffffffu);
-    }
-    if (!I8) store_chunk((T *)a.y + row * a.d, at, a.d, h[c]);
-  }
-  if constexpr (I8) {
-    most = group_max<G>(most, lds);
-    // A row that holds an infinity or a NaN has that as its scale, and codes of 0.
-    const float scale = __uint_as_float(most) / 127.0f;
-    // 127 / most stays finite: rows of tiny entries are lifted by 2^100 first
-    const float lift = most < 0x0d800000u ? 0x1p100f : 1.0f;
-    const float to = most > 0 && most < 0x7f800000u ? 127.0f / (__uint_as_float(most) * lift) : 0.0f;
-    if (real && lane == 0) a.scale[row] = scale;
+// What a lane holds of a row: C chunks, lane l of the row's G lanes chunks l, l + G, ... WHOLE: d is a
+// multiple of 8, and loads need no branch: those past the row's end fetch its last chunk again, so
+// that all of a lane's loads are under way at once; has(c) tells which count. Otherwise the last
+// chunk goes entry by entry.
+template <typename T, int G, int C, bool WHOLE> struct NormRow {
+  int lane, d;
+  __device__ __forceinline__ int at(int c) const { return (c * G + lane) * 8; }
+  __device__ __forceinline__ bool has(int c) const { return at(c) < d; }
+  template <typename V> __device__ __forceinline__ void load(const V *row, Chunk8<V> (&v)[C]) const {
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      const int at = (c * G + lane) * 8;
-      if (!real || at >= a.d) continue;
-      Chunk8<int8_t> q;
+      if constexpr (WHOLE) {
+        v[c] = whole_chunk(row + (has(c) ? at(c) : d - 8));
+      } else {
+        float f[8] = {};
+        if (has(c)) load_chunk(row, at(c), d, f);
+        v[c] = rounded<V>(f);  // exact: they were of this type
+      }
+    }
+  }
+  template <typename V> __device__ __forceinline__ void store(V *row, int c, const float (&f)[8]) const {
+    if constexpr (WHOLE) *(Chunk8<V> *)(row + at(c)) = rounded<V>(f);
+    else store_chunk(row, at(c), d, f);
+  }
+};
+
+// Rows of a group of lanes: where a lane holds one chunk of a row it takes two rows at once (500000
+// rows of 128 in bf16 to 8 bits: 50.2 us one at a time, 47.3 two, 49.9 four).
+template <int C> constexpr int norm_rows = C == 1 ? 2 : 1;
+
+// T: storage type, G: lanes of a row, C: chunks of a lane, W32: weights in fp32, else in T. I8: 8-bit
+// output.
+template <typename T, int G, int C, bool WHOLE, bool W32, bool I8>
+__global__ void __launch_bounds__(NORM_THREADS) norm_kernel(NormArgs a) {
+  using W = std::conditional_t<W32, float, T>;
+  constexpr int GROUPS = NORM_THREADS / G, R = norm_rows<C>;
+  __shared__ float lds[4];
+  const NormRow<T, G, C, WHOLE> part{(int)threadIdx.x % G, a.d};
+  const int64_t row0 = a.first + (int64_t)blockIdx.x * (GROUPS * R) + threadIdx.x / G;
+  Chunk8<T> x[R][C], r[R][C];
+  Chunk8<W> w[C];
+  // every lane takes part in the reductions: past the last row it holds that one again
+#pragma unroll
+  for (int i = 0; i < R; i++) {
+    const int64_t row = row0 + i * GROUPS < a.rows ? row0 + i * GROUPS : a.rows - 1;
+    part.load((const T *)a.x + row * a.x_stride, x[i]);
+    if (a.residual) part.load((const T *)a.residual + row * a.residual_stride, r[i]);
+  }
+  part.load((const W *)a.weight, w);
+  DropKey key{};
+  if (a.drop.rng) key.load(a.drop.rng);
+#pragma unroll
+  for (int i = 0; i < R; i++) {
+    const int64_t row = row0 + i * GROUPS;
+    const bool real = row < a.rows;
+    float h[C][8], squares = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+      DropBits bits;
+      if (a.drop.rng) bits.make(key, a.drop, drop_block(row, a.d, part.at(c) / 8));
 #pragma unroll
       for (int e = 0; e < 8; e++) {
-        const float v = __builtin_rintf(h[c][e] * lift * to);  // an infinity times 0 is a NaN
-        q.e[e] = (int8_t)(v == v ? (int)v : 0);
+        // the product and the sum are rounded apart: what is handed on does not depend on the compiler
+        float v = (float)x[i][c].e[e];
+        if (a.drop.rng) v = bits.apply(a.drop, e, v);
+        if (a.residual) v = __fadd_rn(v, (float)r[i][c].e[e]);
+        // The norm is of h as it is handed on, rounded: the backward, which reads that h, is the
+        // derivative of just this function.
+        h[c][e] = (float)(T)v;
       }
-      int8_t *o = a.codes + row * a.d;
-      if (at + 8 <= a.d) {
-        *(Chunk8<int8_t> *)(o + at) = q;
-      } else {
+      if (a.h && real && part.has(c)) part.store((T *)a.h + row * a.d, c, h[c]);
 #pragma unroll
-        for (int e = 0; e < 8; e++)
-          if (at + e < a.d) o[at + e] = q.e[e];
+      for (int e = 0; e < 8; e++) {
+        if (!part.has(c) || (!WHOLE && part.at(c) + e >= a.d)) h[c][e] = 0.0f;
+        squares = __builtin_fmaf(h[c][e], h[c][e], squares);
+      }
+    }
+    squares = group_sum<G>(squares, lds);
+    const float rstd = rsqrtf(__builtin_fmaf(squares, a.one_over_d, a.eps));
+    if (!I8 && a.rstd && real && part.lane == 0) a.rstd[row] = rstd;
+    uint32_t most = 0;
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        h[c][e] = h[c][e] * rstd * (float)w[c].e[e];
+        if (I8 && part.has(c) && (WHOLE || part.at(c) + e < a.d)) most = max_u32(most, __float_as_uint(h[c][e]) & 0x7fffffffu);
+      }
+      if (!I8 && real && part.has(c)) part.store((T *)a.y + row * a.d, c, h[c]);
+    }
+    if constexpr (I8) {
+      most = group_max<G>(most, lds);
+      // A row that holds an infinity or a NaN has that as its scale, and codes of 0.
+      const float scale = __uint_as_float(most) * (1.0f / 127.0f);
+      // 127 / most stays finite: rows of tiny entries are lifted by 2^100 first
+      const float lift = most < 0x0d800000u ? 0x1p100f : 1.0f;
+      const float to = most > 0 && most < 0x7f800000u ? 127.0f * __builtin_amdgcn_rcpf(__uint_as_float(most) * lift) : 0.0f;
+      if (real && part.lane == 0) a.scale[row] = scale;
+#pragma unroll
+      for (int c = 0; c < C; c++) {
+        if (!part.has(c) || !real) continue;
+        Chunk8<int8_t> q;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const float v = __builtin_rintf(h[c][e] * lift * to);  // an infinity times 0 is a NaN
+          q.e[e] = (int8_t)(v == v ? (int)v : 0);
+        }
+        int8_t *o = a.codes + row * a.d;
+        if (WHOLE || part.at(c) + 8 <= a.d) {
+          *(Chunk8<int8_t> *)(o + part.at(c)) = q;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; e++)
+            if (part.at(c) + e < a.d) o[part.at(c) + e] = q.e[e];
+        }
       }
     }
   }
@@ -198,74 +215,84 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_kernel(NormArgs a) {
 // Gradients. With n = h * rstd and g = grad_y * w: dh = rstd * (g - n * mean(g * n)) + grad_h, the
 // residual's gradient as it is and x's through dropout; the weight's is the sum of grad_y * n over
 // the rows: a group of lanes keeps the sums of the rows that it takes in registers, a workgroup
-// leaves one row of sums, and norm_weight_kernel adds those up, all in a fixed order.
-template <typename T, int G, int C>
+// leaves one row of sums, and norm_weight_kernel adds those up, all in a fixed order. The next row's
+// loads are under way while a row is worked on.
+template <typename T, int G, int C, bool WHOLE, bool W32>
 __global__ void __launch_bounds__(NORM_THREADS) norm_backward_kernel(NormArgs a) {
+  using W = std::conditional_t<W32, float, T>;
   constexpr int GROUPS = NORM_THREADS / G;
   __shared__ float lds[4];
   __shared__ float sums[NORM_THREADS * 8];
-  const int lane = threadIdx.x % G, group = threadIdx.x / G;
+  const NormRow<T, G, C, WHOLE> part{(int)threadIdx.x % G, a.d};
+  const int group = threadIdx.x / G;
   DropKey key{};
   if (a.drop.rng) key.load(a.drop.rng);
-  float w[C][8], dw[C][8];
+  Chunk8<W> w[C];
+  part.load((const W *)a.weight, w);
+  float dw[C][8];
 #pragma unroll
-  for (int c = 0; c < C; c++) {
-    const int at = (c * G + lane) * 8;
+  for (int c = 0; c < C; c++)
 #pragma unroll
-    for (int e = 0; e < 8; e++) w[c][e] = dw[c][e] = 0.0f;
-    if (at < a.d) load_weight<T>(a, at, w[c]);
-  }
+    for (int e = 0; e < 8; e++) dw[c][e] = 0.0f;
+  Chunk8<T> hn[C], gn[C], kn[C];
+  float rn = 0.0f;
+  auto load = [&](int64_t asked) {
+    const int64_t row = asked < a.rows ? asked : a.rows - 1;
+    part.load((const T *)a.x + row * a.x_stride, hn);
+    part.load((const T *)a.grad_y + row * a.d, gn);
+    if (a.grad_h) part.load((const T *)a.grad_h + row * a.d, kn);
+    rn = a.rstd[row];
+  };
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  int64_t base = (int64_t)blockIdx.x * GROUPS;
+  load(base + group);
   // every group of a workgroup makes the same number of rounds: the reductions hold barriers
-  for (int64_t base = (int64_t)blockIdx.x * GROUPS; base < a.rows; base += (int64_t)gridDim.x * GROUPS) {
+  for (; base < a.rows; base += step) {
     const int64_t row = base + group;
     const bool real = row < a.rows;
-    const T *gy = (const T *)a.grad_y + row * a.d, *hp = (const T *)a.x + row * a.x_stride;
-    const T *gh = a.grad_h ? (const T *)a.grad_h + row * a.d : nullptr;
-    float g[C][8], n[C][8];
-    const float rstd = real ? a.rstd[row] : 0.0f;
+    Chunk8<T> k[C];
+    float g[C][8], n[C][8], dot = 0.0f;
+    const float rstd = real ? rn : 0.0f;
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      const int at = (c * G + lane) * 8;
+      k[c] = kn[c];
 #pragma unroll
-      for (int e = 0; e < 8; e++) g[c][e] = n[c][e] = 0.0f;
-      if (real && at < a.d) {
-        load_chunk(hp, at, a.d, n[c]);
-        load_chunk(gy, at, a.d, g[c]);
+      for (int e = 0; e < 8; e++) {
+        const bool in = part.has(c) && real && (WHOLE || part.at(c) + e < a.d);
+        n[c][e] = in ? (float)hn[c].e[e] * rstd : 0.0f;
+        g[c][e] = in ? (float)gn[c].e[e] : 0.0f;
       }
     }
-    float dot = 0.0f;
+    if (base + step < a.rows) load(row + step);
 #pragma unroll
     for (int c = 0; c < C; c++)
 #pragma unroll
       for (int e = 0; e < 8; e++) {
-        n[c][e] *= rstd;
         dw[c][e] = __builtin_fmaf(g[c][e], n[c][e], dw[c][e]);
-        g[c][e] *= w[c][e];
+        g[c][e] *= (float)w[c].e[e];
         dot = __builtin_fmaf(g[c][e], n[c][e], dot);
       }
     if (!a.dx && !a.dresidual) continue;
-    dot = group_sum<G>(dot, lds) / (float)a.d;
+    dot = group_sum<G>(dot, lds) * a.one_over_d;
+    if (!real) continue;
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      const int at = (c * G + lane) * 8;
-      if (!real || at >= a.d) continue;
+      if (!part.has(c)) continue;
       float o[8];
 #pragma unroll
-      for (int e = 0; e < 8; e++) o[e] = rstd * (g[c][e] - n[c][e] * dot);
-      if (gh) {
-        float k[8];
-        load_chunk(gh, at, a.d, k);
-#pragma unroll
-        for (int e = 0; e < 8; e++) o[e] += k[e];
+      for (int e = 0; e < 8; e++) {
+        o[e] = rstd * (g[c][e] - n[c][e] * dot);
+        if (a.grad_h) o[e] += (float)k[c].e[e];
       }
-      if (a.dresidual) store_chunk((T *)a.dresidual + row * a.d, at, a.d, o);
+      if (a.dresidual) part.store((T *)a.dresidual + row * a.d, c, o);
       if (!a.dx) continue;
       if (a.drop.rng) {
-        const uint32_t keep = drop_keep(key, a.drop, drop_block(row, a.d, at / 8));
+        DropBits bits;
+        bits.make(key, a.drop, drop_block(row, a.d, part.at(c) / 8));
 #pragma unroll
-        for (int e = 0; e < 8; e++) o[e] = keep >> e & 1 ? o[e] * a.drop.up : 0.0f;
+        for (int e = 0; e < 8; e++) o[e] = bits.apply(a.drop, e, o[e]);
       }
-      store_chunk((T *)a.dx + row * a.d, at, a.d, o);
+      part.store((T *)a.dx + row * a.d, c, o);
     }
   }
   if (!a.part) return;
@@ -285,59 +312,76 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_backward_kernel(NormArgs a)
   }
 }
 
-// The weight's gradient from the workgroups' sums: 32 entries a workgroup, 8 threads to each.
+// The weight's gradient from the workgroups' sums: 16 entries a workgroup, 64 threads to each.
+constexpr int NORM_JOIN = 1024;
 template <typename W>
-__global__ void __launch_bounds__(NORM_THREADS) norm_weight_kernel(const float *part, int n, int d, W *dw) {
-  __shared__ float sums[8][32];
-  const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int at = blockIdx.x * 32 + col;
+__global__ void __launch_bounds__(NORM_JOIN) norm_weight_kernel(const float *part, int n, int d, W *dw) {
+  __shared__ float sums[64][17];
+  const int col = threadIdx.x & 15, slice = threadIdx.x >> 4;
+  const int at = blockIdx.x * 16 + col;
   float s = 0.0f;
-  if (at < d)
-    for (int i = slice; i < n; i += 8) s += part[(int64_t)i * d + at];
+  if (at < d) {
+#pragma unroll 8
+    for (int i = slice; i < n; i += 64) s += part[(int64_t)i * d + at];
+  }
   sums[slice][col] = s;
   __syncthreads();
-  if (slice == 0 && at < d) {
-#pragma unroll
-    for (int k = 1; k < 8; k++) s += sums[k][col];
-    dw[at] = (W)s;
+  for (int o = 32; o > 0; o >>= 1) {
+    if (slice < o) sums[slice][col] += sums[slice + o][col];
+    __syncthreads();
   }
+  if (slice == 0 && at < d) dw[at] = (W)sums[0][col];
+}
+
+enum { NORM_Y, NORM_I8, NORM_BACK };
+
+template <typename T, int G, int C, bool WHOLE, int WHICH> const void *norm_kernel_of(bool w32) {
+  if constexpr (WHICH == NORM_BACK)
+    return w32 ? (const void *)norm_backward_kernel<T, G, C, WHOLE, true>
+               : (const void *)norm_backward_kernel<T, G, C, WHOLE, false>;
+  else
+    return w32 ? (const void *)norm_kernel<T, G, C, WHOLE, true, WHICH == NORM_I8>
+               : (const void *)norm_kernel<T, G, C, WHOLE, false, WHICH == NORM_I8>;
 }
 
 // Lanes of a row and chunks of a lane: the fewest lanes whose registers hold the row, so that the
-// fewest of them stand idle at its end (768 entries: 32 lanes of 3 chunks).
-template <typename T, template <typename, int, int> class F> const void *norm_pick(int d, int &g) {
+// fewest of them stand idle at its end (768 entries: 32 lanes of 3 chunks). Rows that are no multiple
+// of 8 entries, which go slower anyway, have fewer forms.
+int norm_lanes(int d) {
   const int n = (d + 7) / 8;
-  g = n <= 16 * NORM_CHUNKS ? 16 : n <= 32 * NORM_CHUNKS ? 32 : n <= 64 * NORM_CHUNKS ? 64 : 256;
-  const int c = (n + g - 1) / g;
-  auto of = [&](auto lanes) -> const void * {
-    constexpr int G = decltype(lanes)::value;
-    switch (c) {
-    case 1: return F<T, G, 1>::kernel();
-    case 2: return F<T, G, 2>::kernel();
-    case 3: return F<T, G, 3>::kernel();
-    default: return F<T, G, 4>::kernel();
-    }
-  };
-  switch (g) {
-  case 16: return of(std::integral_constant<int, 16>());
-  case 32: return of(std::integral_constant<int, 32>());
-  case 64: return of(std::integral_constant<int, 64>());
-  default: return of(std::integral_constant<int, 256>());
+  if (d % 8) return n <= 16 ? 16 : n <= 256 ? 64 : 256;
+  return n <= 64 ? 16 : n <= 128 ? 32 : n <= 256 ? 64 : 256;
+}
+int norm_chunks(int d) {
+  const int g = norm_lanes(d), n = (d + 7) / 8;
+  return d % 8 ? (g == 16 ? 1 : 4) : (n + g - 1) / g;
+}
+template <typename T, int WHICH> const void *norm_pick(int d, bool w32) {
+  const int g = norm_lanes(d), c = norm_chunks(d);
+  if (d % 8) {
+    if (g == 16) return norm_kernel_of<T, 16, 1, false, WHICH>(w32);
+    if (g == 64) return norm_kernel_of<T, 64, 4, false, WHICH>(w32);
+    return norm_kernel_of<T, 256, 4, false, WHICH>(w32);
+  }
+  switch (g * 8 + c) {
+  case 16 * 8 + 1: return norm_kernel_of<T, 16, 1, true, WHICH>(w32);
+  case 16 * 8 + 2: return norm_kernel_of<T, 16, 2, true, WHICH>(w32);
+  case 16 * 8 + 3: return norm_kernel_of<T, 16, 3, true, WHICH>(w32);
+  case 16 * 8 + 4: return norm_kernel_of<T, 16, 4, true, WHICH>(w32);
+  case 32 * 8 + 3: return norm_kernel_of<T, 32, 3, true, WHICH>(w32);
+  case 32 * 8 + 4: return norm_kernel_of<T, 32, 4, true, WHICH>(w32);
+  case 64 * 8 + 3: return norm_kernel_of<T, 64, 3, true, WHICH>(w32);
+  case 64 * 8 + 4: return norm_kernel_of<T, 64, 4, true, WHICH>(w32);
+  case 256 * 8 + 2: return norm_kernel_of<T, 256, 2, true, WHICH>(w32);
+  case 256 * 8 + 3: return norm_kernel_of<T, 256, 3, true, WHICH>(w32);
+  default: return norm_kernel_of<T, 256, 4, true, WHICH>(w32);
   }
 }
-template <typename T, int G, int C> struct Forward {
-  static const void *kernel() { return (const void *)norm_kernel<T, G, C, false>; }
-};
-template <typename T, int G, int C> struct Forward8 {
-  static const void *kernel() { return (const void *)norm_kernel<T, G, C, true>; }
-};
-template <typename T, int G, int C> struct Backward {
-  static const void *kernel() { return (const void *)norm_backward_kernel<T, G, C>; }
-};
-template <template <typename, int, int> class F> const void *norm_pick(int dtype, int d, int &g) {
-  return dtype == MAXSIM_FP32   ? norm_pick<float, F>(d, g)
-         : dtype == MAXSIM_FP16 ? norm_pick<_Float16, F>(d, g)
-                                : norm_pick<__bf16, F>(d, g);
+template <int WHICH> const void *norm_pick(int dtype, int d, int weight_dtype) {
+  const bool w32 = weight_dtype == MAXSIM_FP32;
+  return dtype == MAXSIM_FP32   ? norm_pick<float, WHICH>(d, true)
+         : dtype == MAXSIM_FP16 ? norm_pick<_Float16, WHICH>(d, w32)
+                                : norm_pick<__bf16, WHICH>(d, w32);
 }
 
 int norm_sizes(int64_t rows, int d, int dtype, int weight_dtype) {
@@ -347,8 +391,9 @@ int norm_sizes(int64_t rows, int d, int dtype, int weight_dtype) {
   return d > NORM_MOST_D ? MAXSIM_ERR_UNSUPPORTED : MAXSIM_OK;
 }
 
-int norm_launch(const void *kernel, NormArgs &a, int g, hipStream_t st) {
-  const int64_t per = NORM_THREADS / g;
+int norm_launch(const void *kernel, NormArgs &a, hipStream_t st) {
+  const int g = norm_lanes(a.d), c = norm_chunks(a.d);
+  const int64_t per = NORM_THREADS / g * (c == 1 ? norm_rows<1> : norm_rows<2>);
   void *kargs[] = {&a};
   for (a.first = 0; a.first < a.rows; a.first += (int64_t)LAUNCH_MOST * per) {
     const int64_t left = (a.rows - a.first + per - 1) / per;
@@ -396,17 +441,15 @@ int maxsim_rms_norm(const void *x, int64_t x_stride, const void *residual, int64
   a.residual = residual;
   a.residual_stride = residual_stride;
   a.weight = weight;
-  a.weight_fp32 = weight_dtype == MAXSIM_FP32;
   a.rows = n_rows;
   a.d = d;
+  a.one_over_d = 1.0f / (float)d;
   a.eps = eps;
   a.drop = drop;
   a.y = y;
   a.h = h;
   a.rstd = rstd;
-  int g;
-  const void *kernel = norm_pick<Forward>(dtype, d, g);
-  return norm_launch(kernel, a, g, (hipStream_t)stream);
+  return norm_launch(norm_pick<NORM_Y>(dtype, d, weight_dtype), a, (hipStream_t)stream);
 }
 
 int maxsim_rms_norm_i8(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
@@ -430,23 +473,19 @@ int maxsim_rms_norm_i8(const void *x, int64_t x_stride, const void *residual, in
   a.residual = residual;
   a.residual_stride = residual_stride;
   a.weight = weight;
-  a.weight_fp32 = weight_dtype == MAXSIM_FP32;
   a.rows = n_rows;
   a.d = d;
+  a.one_over_d = 1.0f / (float)d;
   a.eps = eps;
   a.codes = codes;
   a.scale = scale;
   a.h = h;
-  int g;
-  const void *kernel = norm_pick<Forward8>(dtype, d, g);
-  return norm_launch(kernel, a, g, (hipStream_t)stream);
+  return norm_launch(norm_pick<NORM_I8>(dtype, d, weight_dtype), a, (hipStream_t)stream);
 }
 
 size_t maxsim_rms_norm_backward_workspace_size(int64_t n_rows, int d) {
   if (n_rows < 1 || d < 1 || d > NORM_MOST_D) return 0;
-  int g;
-  (void)norm_pick<Backward>(MAXSIM_FP32, d, g);
-  return (size_t)norm_back_grid(n_rows, g) * d * sizeof(float);
+  return (size_t)norm_back_grid(n_rows, norm_lanes(d)) * d * sizeof(float);
 }
 
 int maxsim_rms_norm_backward(const void *grad_y, const void *grad_h, const void *h, int64_t h_stride,
@@ -480,16 +519,15 @@ int maxsim_rms_norm_backward(const void *grad_y, const void *grad_h, const void 
     a.x_stride = h_stride;
     a.rows = n_rows;
     a.d = d;
+    a.one_over_d = 1.0f / (float)d;
     a.weight = weight;
-    a.weight_fp32 = weight_dtype == MAXSIM_FP32;
     a.rstd = const_cast<float *>(rstd);
     a.drop = drop_args(dropout, rng, call);
     a.dx = dx;
     a.dresidual = dresidual;
     a.part = dweight ? (float *)workspace : nullptr;
-    int g;
-    const void *kernel = norm_pick<Backward>(dtype, d, g);
-    grid = norm_back_grid(n_rows, g);
+    const void *kernel = norm_pick<NORM_BACK>(dtype, d, weight_dtype);
+    grid = norm_back_grid(n_rows, norm_lanes(d));
     void *kargs[] = {&a};
     if (hipLaunchKernel(kernel, dim3(grid), dim3(NORM_THREADS), kargs, 0, st) != hipSuccess) {
       (void)hipGetLastError();
@@ -497,14 +535,14 @@ int maxsim_rms_norm_backward(const void *grad_y, const void *grad_h, const void 
     }
   }
   if (!dweight) return MAXSIM_OK;
-  const dim3 cols((d + 31) / 32);
+  const dim3 cols((d + 15) / 16);
   const float *part = (const float *)workspace;
   if (weight_dtype == MAXSIM_FP32)
-    hipLaunchKernelGGL(norm_weight_kernel<float>, cols, dim3(NORM_THREADS), 0, st, part, (int)grid, d, (float *)dweight);
+    hipLaunchKernelGGL(norm_weight_kernel<float>, cols, dim3(NORM_JOIN), 0, st, part, (int)grid, d, (float *)dweight);
   else if (weight_dtype == MAXSIM_FP16)
-    hipLaunchKernelGGL(norm_weight_kernel<_Float16>, cols, dim3(NORM_THREADS), 0, st, part, (int)grid, d, (_Float16 *)dweight);
+    hipLaunchKernelGGL(norm_weight_kernel<_Float16>, cols, dim3(NORM_JOIN), 0, st, part, (int)grid, d, (_Float16 *)dweight);
   else
-    hipLaunchKernelGGL(norm_weight_kernel<__bf16>, cols, dim3(NORM_THREADS), 0, st, part, (int)grid, d, (__bf16 *)dweight);
+    hipLaunchKernelGGL(norm_weight_kernel<__bf16>, cols, dim3(NORM_JOIN), 0, st, part, (int)grid, d, (__bf16 *)dweight);
   return hipGetLastError() == hipSuccess ? MAXSIM_OK : MAXSIM_ERR_LAUNCH;
 }
 

@@ -12,6 +12,14 @@ template <typename T> struct Chunk8 {
   T e[8];
 } __attribute__((packed, aligned(sizeof(T))));
 
+template <typename T> __device__ __forceinline__ Chunk8<T> whole_chunk(const T *p) { return *(const Chunk8<T> *)p; }
+template <typename T> __device__ __forceinline__ Chunk8<T> rounded(const float (&v)[8]) {
+  Chunk8<T> c;
+#pragma unroll
+  for (int e = 0; e < 8; e++) c.e[e] = (T)v[e];
+  return c;
+}
+
 // Entries at .. at + 7 of a row of n; those past its end are 0.
 template <typename T> __device__ __forceinline__ void load_chunk(const T *row, int at, int n, float (&v)[8]) {
   if (at + 8 <= n) {
