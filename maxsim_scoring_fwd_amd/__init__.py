@@ -995,7 +995,7 @@ def maxsim_rms_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torc
     one tensor, unless two are given."""
     n, stride, _ = _norm_args(h, weight, None, 0.0)
     dropout = _chance(dropout, rng, call)
-    dt, at, d = h.dtype, h.get_device(), h.shape[-1]
+    dt, at = h.dtype, h.get_device()
     _need(grad_y, "grad_y", dt, shape=h.shape)
     _need(grad_h, "grad_h", dt, shape=h.shape)
     _need(rstd, "rstd", torch.float32, shape=h.shape[:-1])
@@ -1003,30 +1003,44 @@ def maxsim_rms_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torc
     _need(dresidual, "dresidual", dt, shape=h.shape)
     _need(dweight, "dweight", weight.dtype, shape=weight.shape)
     _need(workspace, "workspace", torch.uint8)
+    for t, name in ((grad_y, "grad_y"), (grad_h, "grad_h"), (weight, "weight"), (rstd, "rstd"), (rng, "rng"),
+                    (dx, "dx"), (dresidual, "dresidual"), (dweight, "dweight"), (workspace, "workspace")):
+        _at(t, name, at)
+    _on(h, "h", at)
+    return _norm_gradients(grad_y, grad_h, h, n, stride, weight, rstd, dropout, rng, call, want_dx,
+                           want_dresidual, want_dweight, dx, dresidual, dweight, workspace, stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_gradients(grad_y, grad_h, h, n, stride, weight, rstd, dropout, rng, call, want_dx, want_dresidual,
+                    want_dweight, dx=None, dresidual=None, dweight=None, workspace=None, stream=None):
+    """maxsim_rms_norm_backward without its checks."""
+    d, size = h.shape[-1], 0
     one = want_dx and want_dresidual and not dropout and (dx is None or dresidual is None)
     if one:
         dx = dresidual = dx if dx is not None else dresidual
+    dx, dresidual, dweight = (dx if want_dx else None, dresidual if want_dresidual else None,
+                              dweight if want_dweight else None)
     if want_dresidual and dresidual is None:
         dresidual = _like(h, stream)
     if one:
         dx = dresidual
     elif want_dx and dx is None:
         dx = _like(h, stream)
-    if want_dweight and dweight is None:
-        dweight = _beside(h, weight.shape, weight.dtype, stream)
-    if want_dweight and workspace is None:
-        workspace = _beside(h, (rms_norm_backward_workspace_size(n, d),), torch.uint8, stream)
-    dx = dx if want_dx else None
-    dresidual = dresidual if want_dresidual else None
-    dweight = dweight if want_dweight else None
+    if want_dweight:
+        if dweight is None:
+            dweight = _like(weight, stream)
+        if workspace is None:
+            workspace = _beside(h, (rms_norm_backward_workspace_size(n, d),), torch.uint8, stream)
+        size = workspace.numel()
     _check(lib().maxsim_rms_norm_backward(
-        _at(grad_y, "grad_y", at), _at(grad_h, "grad_h", at), _on(h, "h", at), stride, n, d,
-        _TORCH_DTYPE[dt], _at(weight, "weight", at), _TORCH_DTYPE[weight.dtype],
-        _at(rstd, "rstd", at), dropout, _at(rng, "rng", at), call,
-        None if one else _at(dx, "dx", at), _at(dresidual, "dresidual", at),
-        _at(dweight, "dweight", at), _at(workspace, "workspace", at),
-        0 if workspace is None else workspace.numel(), _stream_at(stream, at)),
-        "maxsim_rms_norm_backward")
+        grad_y.data_ptr(), _ptr(grad_h), h.data_ptr(), stride, n, d, _TORCH_DTYPE[h.dtype],
+        weight.data_ptr(), _TORCH_DTYPE[weight.dtype], rstd.data_ptr(), dropout, _ptr(rng), call,
+        None if one else _ptr(dx), _ptr(dresidual), _ptr(dweight), _ptr(workspace), size,
+        _stream_at(stream, h.get_device())), "maxsim_rms_norm_backward")
     return dx, dresidual, dweight
 
 
@@ -1047,12 +1061,13 @@ class RmsNormFunction(torch.autograd.Function):
         if grad_y is None and grad_h is None:
             return None, None, None, None, None, None, None
         want_dx, want_dw, want_dr = ctx.needs_input_grad[:3]
+        n, stride = _rows(h, "h")
 
         def gradients():
-            dy = torch.zeros_like(h) if grad_y is None else grad_y
-            return maxsim_rms_norm_backward(
-                dy.contiguous(), h, weight, rstd, None if grad_h is None else grad_h.contiguous(),
-                ctx.dropout, rng, ctx.call, want_dx, want_dr, want_dw)
+            dy = torch.zeros_like(h, memory_format=torch.contiguous_format) if grad_y is None else grad_y
+            return _norm_gradients(dy.contiguous(), None if grad_h is None else grad_h.contiguous(), h, n,
+                                   stride, weight, rstd, ctx.dropout, rng, ctx.call, want_dx, want_dr,
+                                   want_dw)
 
         def apart():
             dx, dr, dw = gradients()
@@ -1138,13 +1153,15 @@ def maxsim_linear_cross_entropy_backward(grad_loss: torch.Tensor, h: torch.Tenso
     n, vocab, d, scale, at = _loss_args(h, w, labels, scale)
     _need(grad_loss, "grad_loss", torch.float32, shape=(n,))
     _need(lse, "lse", torch.float32, shape=(n,))
-    _need(dh, "dh", h.dtype, shape=h.shape)
-    _need(dw, "dw", w.dtype, shape=w.shape)
-    _need(workspace, "workspace", torch.uint8)
-    if want_dh and dh is None:
+    if dh is not None:
+        _need(dh, "dh", h.dtype, shape=h.shape)
+    elif want_dh:
         dh = _like(h, stream)
-    if want_dw and dw is None:
+    if dw is not None:
+        _need(dw, "dw", w.dtype, shape=w.shape)
+    elif want_dw:
         dw = _like(w, stream)
+    _need(workspace, "workspace", torch.uint8)
     if workspace is None:
         size = linear_cross_entropy_backward_workspace_size(n, vocab, d, h.dtype)
         workspace = _beside(h, (size,), torch.uint8, stream)
