@@ -185,11 +185,20 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_gather_kern
   const int padded = (a.row_bytes + PANEL - 1) / PANEL * PANEL;
   if (at >= 0) {
     char *to = a.hc + (int64_t)at * PANEL;
-#pragma unroll 4
-    for (int c = c0; c < padded; c += BYTES) {
-      u32x4_t x = {0, 0, 0, 0};
-      if (c < a.row_bytes) x = load16(from + c);
-      *(u32x4_t *)(to + (int64_t)(c / PANEL) * a.n * PANEL + c % PANEL) = x;
+    constexpr int AHEAD = 4;
+    for (int c = c0; c < padded; c += AHEAD * BYTES) {
+      u32x4_t x[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; j++) {
+        const int k = c + j * BYTES;
+        x[j] = load16(from + (k < a.row_bytes ? k : a.row_bytes - 16));
+      }
+#pragma unroll
+      for (int j = 0; j < AHEAD; j++) {
+        const int k = c + j * BYTES;
+        if (k >= a.row_bytes) x[j] = u32x4_t{0, 0, 0, 0};
+        if (k < padded) *(u32x4_t *)(to + (int64_t)(k / PANEL) * a.n * PANEL + k % PANEL) = x[j];
+      }
     }
   } else if (a.dh) {
     char *to = a.dh + (r0 + i) * a.row_bytes;
