@@ -427,7 +427,8 @@ int maxsim_rms_norm(const void *x, int64_t x_stride, const void *residual, int64
 /*
  * maxsim_rms_norm with y in 8 bits, as maxsim_score_i8 takes it: scale[row] = max |y| / 127 and
  * codes = y / scale to the nearest (ties to even). A row of zeros has scale 0 and codes 0; one with a
- * NaN or an infinity has such a scale, and codes 0.
+ * NaN or an infinity has such a scale, and codes 0. (A row of zeros needs eps > 0, here as above: its y is
+ * NaN without.)
  */
 int maxsim_rms_norm_i8(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
                        int64_t n_rows, int d, int dtype, const void *weight, int weight_dtype,
@@ -459,7 +460,8 @@ size_t maxsim_rms_norm_backward_workspace_size(int64_t n_rows, int d);
  * is never used, and it costs nothing beside its label (masked-token training labels few rows).
  * Products run on the matrix cores with fp32 sums; statistics are fp32.
  *   h       [n_rows][d], w [vocab][d] in `dtype`, densely packed, 16-byte aligned, finite;
- *           d * element bytes a multiple of 16, d <= 16384; n_rows <= 2^22, vocab below 2^31
+ *           d * element bytes a multiple of 16, d <= 16384; n_rows <= 2^22, vocab <= 2^26, and
+ *           ceil(n_rows / 256) * ceil(vocab / 128) below 2^31
  *   labels  int64 [n_rows]
  *   scale   > 0 and finite
  *   loss, lse  fp32 [n_rows]
@@ -477,7 +479,7 @@ size_t maxsim_linear_cross_entropy_workspace_size(int64_t n_rows, int64_t vocab,
  *     P = (exp(z - lse) - [v is the label]) * grad_loss * scale,   dh = P w,   dw = P^T h
  * with P, one piece of it, in the workspace, rounded to `dtype` (fp16: scaled by a power of two
  * taken from the largest gradient first). Sums are fp32, each result is rounded once. A piece of P
- * takes 256 MiB at most, or 256 columns. With n_rows == 0 dw is set to zero.
+ * takes 512 MiB at most, or 128 columns. With n_rows == 0 dw is set to zero.
  */
 int maxsim_linear_cross_entropy_backward(const float *grad_loss, const void *h, const void *w,
                                          const int64_t *labels, const float *lse, int64_t n_rows,

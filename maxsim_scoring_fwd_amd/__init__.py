@@ -816,6 +816,13 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                                    slopes, scale)
 
 
+def _must(t, name: str, *a, **k):
+    """_need for a tensor that cannot be left out."""
+    if t is None:
+        raise ValueError(f"{name} must be a torch.Tensor")
+    _need(t, name, *a, **k)
+
+
 def _rows(t: torch.Tensor, name: str):
     """(rows, entries between them) of t [..., d] whose rows lie at one distance from each other."""
     d = t.shape[-1]
@@ -853,7 +860,7 @@ def maxsim_dropout(x: torch.Tensor, dropout: float, rng: torch.Tensor, call: int
     gradient of the result is the gradient of x. dropout counts in steps of 2^-16. Raise the step
     from one training step to the next (in place, in a captured one: between replays), and give each
     place that drops a call of its own. out may be x itself."""
-    _need(x, "x", _FLOAT_STORAGE)
+    _must(x, "x", _FLOAT_STORAGE)
     if rng is None:
         raise ValueError("dropout needs rng")
     dropout = _chance(dropout, rng, call)
@@ -900,10 +907,10 @@ def _norm_args(x, weight, residual, eps):
                 (residual is None or (isinstance(residual, tensor) and residual.dtype == dt and
                                       residual.shape == shape and residual.is_contiguous())):
             return x.numel() // shape[-1], shape[-1], shape[-1]
-    _need(x, "x", _FLOAT_STORAGE)
+    _must(x, "x", _FLOAT_STORAGE)
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x needs rows of at least one entry")
-    _need(weight, "weight", (x.dtype, torch.float32), shape=x.shape[-1:])
+    _must(weight, "weight", (x.dtype, torch.float32), shape=x.shape[-1:])
     if not eps >= 0:
         raise ValueError(f"eps must not be negative, got {eps}")
     n, stride = _rows(x, "x")
@@ -996,9 +1003,9 @@ def maxsim_rms_norm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torc
     n, stride, _ = _norm_args(h, weight, None, 0.0)
     dropout = _chance(dropout, rng, call)
     dt, at = h.dtype, h.get_device()
-    _need(grad_y, "grad_y", dt, shape=h.shape)
+    _must(grad_y, "grad_y", dt, shape=h.shape)
     _need(grad_h, "grad_h", dt, shape=h.shape)
-    _need(rstd, "rstd", torch.float32, shape=h.shape[:-1])
+    _must(rstd, "rstd", torch.float32, shape=h.shape[:-1])
     _need(dx, "dx", dt, shape=h.shape)
     _need(dresidual, "dresidual", dt, shape=h.shape)
     _need(dweight, "dweight", weight.dtype, shape=weight.shape)
@@ -1102,13 +1109,13 @@ def linear_cross_entropy_backward_workspace_size(n_rows: int, vocab: int, d: int
 
 
 def _loss_args(h, w, labels, scale):
-    _need(h, "h", _FLOAT_STORAGE, dim=2)
-    _need(w, "w", h.dtype, dim=2)
+    _must(h, "h", _FLOAT_STORAGE, dim=2)
+    _must(w, "w", h.dtype, dim=2)
     if w.shape[1] != h.shape[1]:
         raise ValueError(f"w has d = {w.shape[1]}, h has d = {h.shape[1]}")
     if w.shape[0] < 1:
         raise ValueError("w needs at least one row")
-    _need(labels, "labels", torch.int64, shape=h.shape[:1])
+    _must(labels, "labels", torch.int64, shape=h.shape[:1])
     scale = float(scale)
     if not 0 < scale < math.inf:
         raise ValueError(f"scale must be positive and finite, got {scale}")
@@ -1151,8 +1158,8 @@ def maxsim_linear_cross_entropy_backward(grad_loss: torch.Tensor, h: torch.Tenso
     lse; None for what is not wanted. The vocabulary goes in pieces, of which the workspace holds
     one."""
     n, vocab, d, scale, at = _loss_args(h, w, labels, scale)
-    _need(grad_loss, "grad_loss", torch.float32, shape=(n,))
-    _need(lse, "lse", torch.float32, shape=(n,))
+    _must(grad_loss, "grad_loss", torch.float32, shape=(n,))
+    _must(lse, "lse", torch.float32, shape=(n,))
     if dh is not None:
         _need(dh, "dh", h.dtype, shape=h.shape)
     elif want_dh:
@@ -1274,7 +1281,7 @@ def maxsim_quantize_mx4(x: torch.Tensor, codes=None, scales=None, stream=None):
     """Token vectors x [..., d] in microscaled 4-bit floating point: 32 entries share a power of two,
     each is a sign and one of 0, 1/2, 1, 3/2, 2, 3, 4, 6. Returns (codes uint8 [..., d / 2], two
     entries a byte, the first in the low half; scales uint8 [..., d / 32], exponents plus 127)."""
-    _need(x, "x", _FLOAT_STORAGE)
+    _must(x, "x", _FLOAT_STORAGE)
     d = x.shape[-1] if x.dim() else 0
     if d < 32 or d % 32:
         raise ValueError(f"x needs rows of whole 32 entries, got shape {tuple(x.shape)}")
@@ -1296,10 +1303,10 @@ def maxsim_quantize_mx4(x: torch.Tensor, codes=None, scales=None, stream=None):
 
 def _mx4(codes, scales, names, dim=None):
     """d of stored vectors, checked."""
-    _need(codes, names[0], torch.uint8, dim=dim)
+    _must(codes, names[0], torch.uint8, dim=dim)
     if not codes.dim() or codes.shape[-1] < 16 or codes.shape[-1] % 16:
         raise ValueError(f"{names[0]} needs rows of whole 16 bytes, got shape {tuple(codes.shape)}")
-    _need(scales, names[1], torch.uint8, shape=(*codes.shape[:-1], codes.shape[-1] // 16))
+    _must(scales, names[1], torch.uint8, shape=(*codes.shape[:-1], codes.shape[-1] // 16))
     return codes.shape[-1] * 2
 
 

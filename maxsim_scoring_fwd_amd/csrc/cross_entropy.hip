@@ -14,7 +14,7 @@ constexpr int64_t CE_P_BYTES = (int64_t)512 << 20;
 constexpr int64_t CE_SLOTS = 1024;
 
 // A step's panels are reached by 32-bit offsets.
-constexpr int64_t CE_MOST_ROWS = (int64_t)1 << 22;
+constexpr int64_t CE_MOST_ROWS = (int64_t)1 << 22, CE_MOST_VOCAB = (int64_t)1 << 26;
 
 struct Carver {
   char *base;
@@ -27,8 +27,9 @@ struct Carver {
 };
 
 bool ce_sizes(int64_t n, int64_t vocab, int d, int dtype) {
-  return n >= 0 && n <= CE_MOST_ROWS && vocab >= 1 && vocab < ((int64_t)1 << 31) && d >= 1 &&
-         d <= 16384 && d * elem_bytes(dtype) % 16 == 0;
+  return n >= 0 && n <= CE_MOST_ROWS && vocab >= 1 && vocab <= CE_MOST_VOCAB && d >= 1 && d <= 16384 &&
+         d * elem_bytes(dtype) % 16 == 0 &&
+         blocks_of(n, CE_BN) * blocks_of(vocab, CE_BM) < ((int64_t)1 << 31);  // tiles are counted in 32 bits
 }
 
 // The workspace, carved up; with base NULL only its size is worked out.

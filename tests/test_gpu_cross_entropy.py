@@ -52,3 +52,189 @@ def check(h, w, y, scale=1.0, dl=None, backward=True):
 def test_against_reference(n, vocab, d, dtype, share):
     print("case: cross entropy", n, vocab, d, dtype, share, flush=True)
     check(*make(n, vocab, d, dtype, share, seed=n), scale=0.7 if n % 2 else 1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+@pytest.mark.parametrize("n", [40, 300])
+def test_rows_left_out_hide_what_they_hold(n, dtype):
+    """NaN and infinities in rows without a label change nothing; labels of all sizes that are none."""
+    h, w, y = make(n, 400, 96, dtype, 0.6, seed=3)
+    out = y < 0
+    bad = torch.tensor([-1, -100, 400, 1 << 40, -(1 << 63), (1 << 63) - 1], device="cuda")
+    y[out] = bad[torch.arange(int(out.sum()), device="cuda") % 6]
+    dl = torch.rand(n, device="cuda") + 0.5
+    want = [*ms.maxsim_linear_cross_entropy(h, w, y)]
+    want += ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, want[1])
+    check(h, w, y, dl=dl)
+    x = h.clone()
+    x[out] = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda", dtype=dtype).repeat(32)
+    dl = torch.where(out, torch.full_like(dl, float("nan")), dl)
+    got = [*ms.maxsim_linear_cross_entropy(x, w, y)]
+    got += ms.maxsim_linear_cross_entropy_backward(dl, x, w, y, got[1])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert not got[0][out].any() and (got[1][out] == -float("inf")).all() and not got[2][out].any()
+
+
+@pytest.mark.parametrize("n", [1, 64, 65, 2000, 9000])
+def test_no_row_counts(n):
+    h, w, _ = make(n, 300, 64, BF16)
+    y = torch.full((n,), -100, device="cuda")
+    loss, lse = ms.maxsim_linear_cross_entropy(h, w, y)
+    assert not loss.any() and (lse == -float("inf")).all()
+    dh, dw = ms.maxsim_linear_cross_entropy_backward(torch.ones(n, device="cuda"), h, w, y, lse,
+                                                     dh=torch.ones_like(h), dw=torch.ones_like(w))
+    assert not dh.any() and not dw.any()
+
+
+def test_no_rows():
+    h, w = torch.zeros(0, 64, device="cuda"), torch.ones(300, 64, device="cuda")
+    y = torch.zeros(0, dtype=torch.int64, device="cuda")
+    loss, lse = ms.maxsim_linear_cross_entropy(h, w, y)
+    dh, dw = ms.maxsim_linear_cross_entropy_backward(loss, h, w, y, lse, dw=w.clone())
+    assert loss.shape == lse.shape == (0,) and dh.shape == (0, 64) and not dw.any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+@pytest.mark.parametrize("size", [1e-7, 1e3])
+def test_sizes_of_gradients(size, dtype):
+    """Gradients of the losses far from 1, some 0, of both signs; fp16's results may pass its range."""
+    h, w, y = make(150, 700, 64, dtype, 0.8, seed=9)
+    dl = torch.linspace(-1, 1, 150, device="cuda") * size
+    dl[::7] = 0
+    if dtype == FP16 and size > 1:
+        w *= 0.05  # so that dh stays in range
+        h *= 0.05
+    check(h, w, y, 2.0, dl)
+
+
+def test_large_logits():
+    """Scores of some thousands: the exponentials of all but a few are 0."""
+    h, w, y = make(200, 1000, 128, FP32, seed=4, std=8.0)
+    check(h, w, y, 20.0)
+
+
+def test_one_direction_only_and_given_buffers():
+    h, w, y = make(100, 333, 64, BF16, 0.7)
+    dl = torch.rand(100, device="cuda")
+    loss, lse = ms.maxsim_linear_cross_entropy(h, w, y)
+    dh, dw = ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, lse)
+    a = ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, lse, want_dw=False)
+    b = ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, lse, want_dh=False)
+    assert a[1] is None and b[0] is None and torch.equal(a[0], dh) and torch.equal(b[1], dw)
+    size = ms.linear_cross_entropy_backward_workspace_size(100, 333, 64, BF16)
+    ws = torch.full((size + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+    big = torch.full((337, 64), 3.0, dtype=BF16, device="cuda")
+    top = torch.full((104, 64), 3.0, dtype=BF16, device="cuda")
+    ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, lse, dh=top[2:102], dw=big[2:335], workspace=ws[:size])
+    assert torch.equal(top[2:102], dh) and torch.equal(big[2:335], dw)
+    assert (top[[0, 1, 102, 103]] == 3).all() and (big[[0, 1, 335, 336]] == 3).all() and (ws[size:] == 0x5A).all()
+    size = ms.linear_cross_entropy_workspace_size(100, 333, 64, BF16)
+    ws = torch.full((size + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+    outs = torch.full((2, 104), 3.0, device="cuda")
+    ms.maxsim_linear_cross_entropy(h, w, y, loss=outs[0, :100], lse=outs[1, :100], workspace=ws[:size])
+    assert torch.equal(outs[0, :100], loss) and torch.equal(outs[1, :100], lse)
+    assert (outs[:, 100:] == 3).all() and (ws[size:] == 0x5A).all()
+
+
+def test_repeated_calls_give_the_same_bits():
+    h, w, y = make(3000, 4001, 264, BF16, 0.9)
+    dl = torch.rand(3000, device="cuda")
+    first = [*ms.maxsim_linear_cross_entropy(h, w, y)]
+    first += ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, first[1])
+    for _ in range(4):
+        loss, lse = ms.maxsim_linear_cross_entropy(h, w, y)
+        again = [loss, lse, *ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, lse)]
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def part_of_gradients(h, w, y, lse, dl, scale, dh, dw, rows, vocab):
+    """dh of some rows and dw of some entries against 64 bits, with the lse given (it is checked
+    elsewhere): each needs one row or column of P."""
+    n, V = len(y), w.shape[0]
+    H, W, labels, L, g = as64(h), as64(w), y.cpu().numpy(), as64(lse), as64(dl)
+    ok = (labels >= 0) & (labels < V)
+    u = ref.HALF_STEP[h.dtype]
+    f = np.where(ok, g * scale, 0)
+    least = 2.0 ** -38 * np.abs(f).max() if h.dtype == FP16 else 2.0 ** -133
+
+    def weights(z, L, hot, size):
+        """P before its gradient, and how far it may be off: the logit's error, the lse's rounding and
+        the exponential's."""
+        p = np.exp(z - L)
+        off = p * ((h.shape[1] + 12) * ref.U32 * size + 12 * ref.U32 * (np.abs(z) + np.abs(L) + 1))
+        return p - hot, off
+    for i in rows:
+        if not ok[i]:
+            assert not dh[i].any()
+            continue
+        p, off = weights(scale * (W @ H[i]), L[i], np.arange(V) == labels[i], scale * (np.abs(W) @ np.abs(H[i])))
+        P, tP = p * f[i], np.abs(f[i]) * (off + np.abs(p) * (u + V * ref.U32)) + least
+        want = P @ W
+        ref.close(dh[i], want, tP @ np.abs(W) + u * np.abs(want) + ref.TINY[h.dtype], f"dh of row {i}")
+    for v in vocab:
+        p, off = weights(scale * (H[ok] @ W[v]), L[ok], labels[ok] == v, scale * (np.abs(H[ok]) @ np.abs(W[v])))
+        P, tP = p * f[ok], np.abs(f[ok]) * (off + np.abs(p) * (u + n * ref.U32)) + least
+        want = P @ H[ok]
+        ref.close(dw[v], want, tP @ np.abs(H[ok]) + u * np.abs(want) + ref.TINY[h.dtype], f"dw of entry {v}")
+
+
+@pytest.mark.parametrize("n, vocab, d, dtype, share", [
+    (20011, 14001, 64, BF16, 1.0),    # more than one piece of the vocabulary
+    (9000, 33001, 40, FP16, 0.95),    # the same with a part of the rows left out
+    (9001, 16001, 20, FP32, 1.0),
+    (40000, 20001, 32, BF16, 0.1),    # pieces for all rows, one for those that count
+])
+def test_pieces_of_the_vocabulary(n, vocab, d, dtype, share):
+    print("case: pieces", n, vocab, d, dtype, share, flush=True)
+    h, w, y = make(n, vocab, d, dtype, share, seed=n)
+    dl = torch.rand(n, device="cuda") / n
+    loss, lse = ms.maxsim_linear_cross_entropy(h, w, y)
+    dh, dw = ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, lse)
+    rows = [0, 1, n // 2, n - 1]
+    want = ref.loss(as64(h[rows]), as64(w), y[rows].cpu().numpy(), 1.0)
+    ref.close(loss[rows], want["loss"], want["tol_loss"], "loss")
+    ref.close(lse[rows], want["lse"], want["tol_lse"], "lse")
+    edge = [c + i for c in range(0, vocab, 128) for i in (0, 127) if c % 1024 == 0 or abs(c - vocab / 2) < 400]
+    edge = [v for v in edge if v < vocab] + [vocab - 1]
+    part_of_gradients(h, w, y, lse, dl, 1.0, dh, dw, rows, edge)
+    assert torch.isfinite(dh).all() and torch.isfinite(dw).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=str)
+def test_autograd(dtype):
+    h, w, y = make(77, 200, 64, dtype, 0.7)
+    h.requires_grad_(), w.requires_grad_()
+    count = (y >= 0).sum()
+    loss = ms.linear_cross_entropy(h, w, y, 1.5)
+    got = torch.autograd.grad(loss.sum() / count, (h, w))  # an expanded gradient
+    l, lse = ms.maxsim_linear_cross_entropy(h.detach(), w.detach(), y, 1.5)
+    want = ms.maxsim_linear_cross_entropy_backward(torch.ones_like(l) / count, h.detach(), w.detach(), y, lse, 1.5)
+    assert torch.equal(loss.detach(), l) and all(torch.equal(a, b) for a, b in zip(got, want))
+    (dh,) = torch.autograd.grad(ms.linear_cross_entropy(h, w.detach(), y, 1.5).sum() / count, h)
+    assert torch.equal(dh, want[0])
+    (g,) = torch.autograd.grad(ms.linear_cross_entropy(h, w, y).sum(), h, create_graph=True)
+    with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+        g.sum().backward()
+
+
+def test_gradients_against_differences():
+    """fp32 values along a direction: central differences of step 2^-5 are off by its square (the
+    loss's third derivatives along a unit-size direction are below 1) and by some 2^-22 of the loss
+    over 2^-5."""
+    h, w, y = make(50, 300, 64, FP32, 0.8, seed=2)
+    dl = torch.rand(50, device="cuda") - 0.3
+    loss, lse = ms.maxsim_linear_cross_entropy(h, w, y)
+    g = ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, lse)
+    e = 2.0 ** -5
+    for i in (0, 1):
+        t = torch.randn(g[i].shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(i))
+        t /= 8  # rows of about unit length
+        side = []
+        for s in (e, -e):
+            a = [h, w]
+            a[i] = a[i] + s * t
+            side.append(float((ms.maxsim_linear_cross_entropy(*a, y)[0].double() * dl).sum()))
+        got, want = (side[0] - side[1]) / (2 * e), float((g[i].double() * t).sum())
+        size = float((g[i].double() * t).abs().sum()) + float(dl.abs().sum())
+        assert abs(got - want) <= size * (e * e + 2.0 ** -22 / e * 8)

@@ -172,6 +172,6 @@ def close(got, want, tol, what=""):
     assert got.shape == want.shape, (what, got.shape, want.shape)
     fine = np.isfinite(want)
     assert np.array_equal(got[~fine], want[~fine], equal_nan=True), f"{what}: other values than finite ones"
-    off = np.abs(got - want)[fine] - np.broadcast_to(tol, want.shape)[fine]
+    off = np.abs(got[fine] - want[fine]) - np.broadcast_to(tol, want.shape)[fine]
     assert not np.isnan(got[fine]).any(), f"{what}: NaN"
     assert off.size == 0 or off.max() <= 0, f"{what}: {off.max()} past the bound"
