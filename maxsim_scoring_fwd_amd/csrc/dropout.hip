@@ -16,7 +16,8 @@ constexpr int DROP_THREADS = 256;
 constexpr int DROP_PER = 4;  // chunks of a thread
 
 // DROP: else a copy (p = 0, and p that rounds to it).
-template <typename T, bool DROP>
+// ONCE: past the caches.
+template <typename T, bool DROP, bool ONCE>
 __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const T *x, T *y, int64_t n, int64_t first,
                                                                DropArgs drop) {
   constexpr int PER = DROP_THREADS * DROP_PER * 8;
@@ -33,7 +34,7 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const T *x, T *y,
   if (n - base >= PER) {  // all of a thread's loads are under way at once
     Chunk8<T> c[DROP_PER];
 #pragma unroll
-    for (int i = 0; i < DROP_PER; i++) c[i] = whole_chunk(x + base + (i * DROP_THREADS + threadIdx.x) * 8);
+    for (int i = 0; i < DROP_PER; i++) c[i] = whole_chunk<ONCE>(x + base + (i * DROP_THREADS + threadIdx.x) * 8);
 #pragma unroll
     for (int i = 0; i < DROP_PER; i++) {
       const int at = (i * DROP_THREADS + threadIdx.x) * 8;
@@ -41,7 +42,7 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const T *x, T *y,
 #pragma unroll
       for (int e = 0; e < 8; e++) v[e] = (float)c[i].e[e];
       run(at, v);
-      *(Chunk8<T> *)(y + base + at) = rounded<T>(v);
+      store_whole<ONCE>(y + base + at, rounded<T>(v));
     }
   } else {
     const int left = (int)(n - base);
@@ -57,15 +58,13 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const T *x, T *y,
 template <typename T>
 int dropout_run(const void *x, int64_t n, const DropArgs &drop, void *out, hipStream_t st) {
   constexpr int64_t per = DROP_THREADS * DROP_PER * 8;
+  const bool once = 2 * n * (int64_t)sizeof(T) > CACHE_BYTES;
+  auto kernel = drop.rng ? (once ? dropout_kernel<T, true, true> : dropout_kernel<T, true, false>)
+                         : (once ? dropout_kernel<T, false, true> : dropout_kernel<T, false, false>);
   for (int64_t first = 0; first < n; first += (int64_t)LAUNCH_MOST * per) {
     const int64_t left = (n - first + per - 1) / per;
     const unsigned grid = (unsigned)(left < (int64_t)LAUNCH_MOST ? left : LAUNCH_MOST);
-    if (drop.rng)
-      hipLaunchKernelGGL((dropout_kernel<T, true>), dim3(grid), dim3(DROP_THREADS), 0, st, (const T *)x, (T *)out, n,
-                         first, drop);
-    else
-      hipLaunchKernelGGL((dropout_kernel<T, false>), dim3(grid), dim3(DROP_THREADS), 0, st, (const T *)x, (T *)out, n,
-                         first, drop);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(DROP_THREADS), 0, st, (const T *)x, (T *)out, n, first, drop);
     if (hipGetLastError() != hipSuccess) return MAXSIM_ERR_LAUNCH;
   }
   return MAXSIM_OK;

@@ -24,7 +24,7 @@ __device__ __forceinline__ float power_of(uint32_t byte) {
 // Chunks of 8 entries; four neighbouring lanes hold a block of 32. n: chunks, a multiple of 4, so
 // that the lanes of a block are in or out together. A thread past the end takes the last chunks
 // again and stores nothing: no branch before the loads, which are all under way at once.
-template <typename T>
+template <typename T, bool ONCE>
 __global__ void __launch_bounds__(MX4_THREADS) mx4_quantize_kernel(const T *x, uint32_t *codes, uint8_t *scales,
                                                                    int64_t n, int64_t first) {
   const int64_t base = first + (int64_t)blockIdx.x * (MX4_THREADS * MX4_PER) + threadIdx.x;
@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(MX4_THREADS) mx4_quantize_kernel(const T *x, u
 #pragma unroll
   for (int i = 0; i < MX4_PER; i++) {
     const int64_t at = base + i * MX4_THREADS;
-    c[i] = whole_chunk(x + (at < n ? at : last) * 8);
+    c[i] = whole_chunk<ONCE>(x + (at < n ? at : last) * 8);
   }
 #pragma unroll
   for (int i = 0; i < MX4_PER; i++) {
@@ -61,13 +61,15 @@ __global__ void __launch_bounds__(MX4_THREADS) mx4_quantize_kernel(const T *x, u
     q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4] * to, v[5] * to, 1.0f, 2);
     q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6] * to, v[7] * to, 1.0f, 3);
     if (at < n) {
-      codes[at] = finite ? q : 0;
+      q = finite ? q : 0;
+      if (ONCE) __builtin_nontemporal_store(q, codes + at);
+      else codes[at] = q;
       if ((threadIdx.x & 3) == 0) scales[at >> 2] = (uint8_t)byte;
     }
   }
 }
 
-template <typename T>
+template <typename T, bool ONCE>
 __global__ void __launch_bounds__(MX4_THREADS) mx4_values_kernel(const uint32_t *codes, const uint8_t *scales, T *x,
                                                                  int64_t n, int64_t first) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(MX4_THREADS) mx4_values_kernel(const uint32_t 
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; e++) v[e] = p[e / 2][e & 1] * by;
-    if (at < n) *(Chunk8<T> *)(x + at * 8) = rounded<T>(v);
+    if (at < n) store_whole<ONCE>(x + at * 8, rounded<T>(v));
   }
 }
 
@@ -110,6 +112,25 @@ template <typename Launch> int mx4_parts(int64_t n, Launch launch) {
   return MAXSIM_OK;
 }
 
+// Bytes that n chunks take in both forms.
+template <typename T> bool mx4_once(int64_t n) { return n * (int64_t)(8 * sizeof(T) + 4) > CACHE_BYTES; }
+
+template <typename T>
+int mx4_quantize_run(const T *x, uint8_t *codes, uint8_t *scales, int64_t n, hipStream_t st) {
+  auto kernel = mx4_once<T>(n) ? mx4_quantize_kernel<T, true> : mx4_quantize_kernel<T, false>;
+  return mx4_parts(n, [&](unsigned grid, int64_t first) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(MX4_THREADS), 0, st, x, (uint32_t *)codes, scales, n, first);
+  });
+}
+
+template <typename T>
+int mx4_values_run(const uint8_t *codes, const uint8_t *scales, T *x, int64_t n, hipStream_t st) {
+  auto kernel = mx4_once<T>(n) ? mx4_values_kernel<T, true> : mx4_values_kernel<T, false>;
+  return mx4_parts(n, [&](unsigned grid, int64_t first) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(MX4_THREADS), 0, st, (const uint32_t *)codes, scales, x, n, first);
+  });
+}
+
 }  // namespace
 
 extern "C" {
@@ -126,18 +147,11 @@ int maxsim_quantize_mx4(const void *x, int64_t n_rows, int d, int dtype, uint8_t
   rc = current_device(di);
   if (rc != MAXSIM_OK) return rc;
   hipStream_t st = (hipStream_t)stream;
-  const int64_t n = n_rows * (d / 8);
-  return mx4_parts(n, [&](unsigned grid, int64_t first) {
-    if (dtype == MAXSIM_FP32)
-      hipLaunchKernelGGL(mx4_quantize_kernel<float>, dim3(grid), dim3(MX4_THREADS), 0, st, (const float *)x,
-                         (uint32_t *)codes, scales, n, first);
-    else if (dtype == MAXSIM_FP16)
-      hipLaunchKernelGGL(mx4_quantize_kernel<_Float16>, dim3(grid), dim3(MX4_THREADS), 0, st, (const _Float16 *)x,
-                         (uint32_t *)codes, scales, n, first);
-    else
-      hipLaunchKernelGGL(mx4_quantize_kernel<__bf16>, dim3(grid), dim3(MX4_THREADS), 0, st, (const __bf16 *)x,
-                         (uint32_t *)codes, scales, n, first);
-  });
+  switch (dtype) {
+  case MAXSIM_BF16: return mx4_quantize_run((const __bf16 *)x, codes, scales, n_rows * (d / 8), st);
+  case MAXSIM_FP16: return mx4_quantize_run((const _Float16 *)x, codes, scales, n_rows * (d / 8), st);
+  default: return mx4_quantize_run((const float *)x, codes, scales, n_rows * (d / 8), st);
+  }
 }
 
 int maxsim_dequantize_mx4(const uint8_t *codes, const uint8_t *scales, int64_t n_rows, int d, int dtype, void *x,
@@ -152,18 +166,11 @@ int maxsim_dequantize_mx4(const uint8_t *codes, const uint8_t *scales, int64_t n
   rc = current_device(di);
   if (rc != MAXSIM_OK) return rc;
   hipStream_t st = (hipStream_t)stream;
-  const int64_t n = n_rows * (d / 8);
-  return mx4_parts(n, [&](unsigned grid, int64_t first) {
-    if (dtype == MAXSIM_FP32)
-      hipLaunchKernelGGL(mx4_values_kernel<float>, dim3(grid), dim3(MX4_THREADS), 0, st, (const uint32_t *)codes,
-                         scales, (float *)x, n, first);
-    else if (dtype == MAXSIM_FP16)
-      hipLaunchKernelGGL(mx4_values_kernel<_Float16>, dim3(grid), dim3(MX4_THREADS), 0, st, (const uint32_t *)codes,
-                         scales, (_Float16 *)x, n, first);
-    else
-      hipLaunchKernelGGL(mx4_values_kernel<__bf16>, dim3(grid), dim3(MX4_THREADS), 0, st, (const uint32_t *)codes,
-                         scales, (__bf16 *)x, n, first);
-  });
+  switch (dtype) {
+  case MAXSIM_BF16: return mx4_values_run(codes, scales, (__bf16 *)x, n_rows * (d / 8), st);
+  case MAXSIM_FP16: return mx4_values_run(codes, scales, (_Float16 *)x, n_rows * (d / 8), st);
+  default: return mx4_values_run(codes, scales, (float *)x, n_rows * (d / 8), st);
+  }
 }
 
 }  // extern "C"

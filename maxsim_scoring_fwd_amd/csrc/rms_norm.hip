@@ -5,6 +5,7 @@
 #include "host_common.hpp"
 #include "launch_parts.hpp"
 #include "rms_norm_args.hpp"
+#include "row_chunks.hpp"
 
 using namespace maxsim;
 
@@ -31,11 +32,12 @@ __global__ void __launch_bounds__(NORM_JOIN) norm_weight_kernel(const float *par
   if (slice == 0 && at < d) dw[at] = (W)sums[0][col];
 }
 
-const void *norm_kernel(int which, int dtype, int d, int weight_dtype) {
-  const bool w32 = weight_dtype == MAXSIM_FP32;
-  return dtype == MAXSIM_FP32   ? norm_kernel_fp32(which, d, true)
-         : dtype == MAXSIM_FP16 ? norm_kernel_fp16(which, d, w32)
-                                : norm_kernel_bf16(which, d, w32);
+// tensors: how many of n_rows x d the call moves.
+const void *norm_kernel(int which, int dtype, int64_t n_rows, int d, int weight_dtype, int tensors) {
+  const bool w32 = weight_dtype == MAXSIM_FP32, once = n_rows * d * elem_bytes(dtype) * tensors > CACHE_BYTES;
+  return dtype == MAXSIM_FP32   ? norm_kernel_fp32(which, d, true, once)
+         : dtype == MAXSIM_FP16 ? norm_kernel_fp16(which, d, w32, once)
+                                : norm_kernel_bf16(which, d, w32, once);
 }
 
 int norm_sizes(int64_t rows, int d, int dtype, int weight_dtype) {
@@ -103,7 +105,7 @@ int maxsim_rms_norm(const void *x, int64_t x_stride, const void *residual, int64
   a.y = y;
   a.h = h;
   a.rstd = rstd;
-  return norm_launch(norm_kernel(NORM_Y, dtype, d, weight_dtype), a, (hipStream_t)stream);
+  return norm_launch(norm_kernel(NORM_Y, dtype, n_rows, d, weight_dtype, 2 + (residual != nullptr) + (h != nullptr)), a, (hipStream_t)stream);
 }
 
 int maxsim_rms_norm_i8(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
@@ -134,7 +136,7 @@ int maxsim_rms_norm_i8(const void *x, int64_t x_stride, const void *residual, in
   a.codes = codes;
   a.scale = scale;
   a.h = h;
-  return norm_launch(norm_kernel(NORM_I8, dtype, d, weight_dtype), a, (hipStream_t)stream);
+  return norm_launch(norm_kernel(NORM_I8, dtype, n_rows, d, weight_dtype, 0), a, (hipStream_t)stream);
 }
 
 size_t maxsim_rms_norm_backward_workspace_size(int64_t n_rows, int d) {
@@ -180,7 +182,8 @@ int maxsim_rms_norm_backward(const void *grad_y, const void *grad_h, const void 
     a.dx = dx;
     a.dresidual = dresidual;
     a.part = dweight ? (float *)workspace : nullptr;
-    const void *kernel = norm_kernel(NORM_BACK, dtype, d, weight_dtype);
+    const void *kernel = norm_kernel(NORM_BACK, dtype, n_rows, d, weight_dtype,
+                                     2 + (grad_h != nullptr) + (dx != nullptr) + (dresidual != nullptr));
     grid = norm_back_grid(n_rows, norm_lanes(d));
     void *kargs[] = {&a};
     if (hipLaunchKernel(kernel, dim3(grid), dim3(NORM_THREADS), kargs, 0, st) != hipSuccess) {

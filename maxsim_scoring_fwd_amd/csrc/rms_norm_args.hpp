@@ -43,9 +43,10 @@ inline int norm_chunks(int d) {
   return d % 8 == 0 || c <= 2 && g == 16 ? c : 4;
 }
 
-// The kernel (of the three above) for rows of d entries; weights in fp32 or in the rows' type.
-const void *norm_kernel_bf16(int which, int d, bool w32);
-const void *norm_kernel_fp16(int which, int d, bool w32);
-const void *norm_kernel_fp32(int which, int d, bool w32);
+// The kernel (of the three above) for rows of d entries; weights in fp32 or in the rows' type; past the
+// caches or not.
+const void *norm_kernel_bf16(int which, int d, bool w32, bool once);
+const void *norm_kernel_fp16(int which, int d, bool w32, bool once);
+const void *norm_kernel_fp32(int which, int d, bool w32, bool once);
 
 }  // namespace maxsim

@@ -81,16 +81,17 @@ enum { ROW_WHOLE, ROW_TAIL, ROW_TINY };
 // no branch, so that all of a lane's are under way at once: those past the row's end fetch its last 8
 // entries again, and a shorter last chunk is moved into place afterwards (settle); has(c) tells
 // which chunks count, in(c, e) which entries. TINY rows, of less than 8 entries, go one by one.
-template <typename T, int G, int C, int KIND> struct NormRow {
+template <typename T, int G, int C, int KIND, bool ONCE> struct NormRow {
   int lane, d;
   __device__ __forceinline__ int at(int c) const { return (c * G + lane) * 8; }
   __device__ __forceinline__ bool has(int c) const { return at(c) < d; }
   __device__ __forceinline__ bool in(int c, int e) const { return KIND == ROW_WHOLE ? has(c) : at(c) + e < d; }
-  template <typename V> __device__ __forceinline__ void load(const V *row, Chunk8<V> (&v)[C]) const {
+  template <typename V> __device__ __forceinline__ void load(const V *row, Chunk8<V> (&v)[C]) const { load<ONCE>(row, v); }
+  template <bool PAST, typename V> __device__ __forceinline__ void load(const V *row, Chunk8<V> (&v)[C]) const {
 #pragma unroll
     for (int c = 0; c < C; c++) {
       if constexpr (KIND != ROW_TINY) {
-        v[c] = whole_chunk(row + (at(c) + 8 <= d ? at(c) : d - 8));
+        v[c] = whole_chunk<PAST>(row + (at(c) + 8 <= d ? at(c) : d - 8));
       } else {
         float f[8] = {};
         if (has(c)) load_chunk(row, at(c), d, f);
@@ -114,19 +115,19 @@ template <typename T, int G, int C, int KIND> struct NormRow {
     }
   }
   template <typename V> __device__ __forceinline__ void store(V *row, int c, const float (&f)[8]) const {
-    if constexpr (KIND == ROW_WHOLE) *(Chunk8<V> *)(row + at(c)) = rounded<V>(f);
+    if constexpr (KIND == ROW_WHOLE) store_whole<ONCE>(row + at(c), rounded<V>(f));
     else store_chunk(row, at(c), d, f);
   }
 };
 
 // T: storage type, G: lanes of a row, C: chunks of a lane, W32: weights in fp32, else in T. I8: 8-bit
-// output.
-template <typename T, int G, int C, int KIND, bool W32, bool I8>
+// output. ONCE: past the caches.
+template <typename T, int G, int C, int KIND, bool W32, bool I8, bool ONCE>
 __global__ void __launch_bounds__(NORM_THREADS) norm_kernel(NormArgs a) {
   using W = std::conditional_t<W32, float, T>;
   constexpr int GROUPS = NORM_THREADS / G, R = norm_rows<C>;
   __shared__ float lds[4];
-  const NormRow<T, G, C, KIND> part{(int)threadIdx.x % G, a.d};
+  const NormRow<T, G, C, KIND, ONCE> part{(int)threadIdx.x % G, a.d};
   const int64_t row0 = a.first + (int64_t)blockIdx.x * (GROUPS * R) + threadIdx.x / G;
   Chunk8<T> x[R][C], r[R][C];
   Chunk8<W> w[C];
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_kernel(NormArgs a) {
     part.load((const T *)a.x + row * a.x_stride, x[i]);
     if (a.residual) part.load((const T *)a.residual + row * a.residual_stride, r[i]);
   }
-  part.load((const W *)a.weight, w);
+  part.template load<false>((const W *)a.weight, w);
   DropKey key{};
   if (a.drop.rng) key.load(a.drop.rng);
   part.settle(w);
@@ -217,18 +218,18 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_kernel(NormArgs a) {
 // the rows: a group of lanes keeps the sums of the rows that it takes in registers, a workgroup
 // leaves one row of sums, and norm_weight_kernel adds those up, all in a fixed order. The next row's
 // loads are under way while a row is worked on.
-template <typename T, int G, int C, int KIND, bool W32>
+template <typename T, int G, int C, int KIND, bool W32, bool ONCE>
 __global__ void __launch_bounds__(NORM_THREADS) norm_backward_kernel(NormArgs a) {
   using W = std::conditional_t<W32, float, T>;
   constexpr int GROUPS = NORM_THREADS / G;
   __shared__ float lds[4];
   __shared__ float sums[NORM_THREADS * 8];
-  const NormRow<T, G, C, KIND> part{(int)threadIdx.x % G, a.d};
+  const NormRow<T, G, C, KIND, ONCE> part{(int)threadIdx.x % G, a.d};
   const int group = threadIdx.x / G;
   DropKey key{};
   if (a.drop.rng) key.load(a.drop.rng);
   Chunk8<W> w[C];
-  part.load((const W *)a.weight, w);
+  part.template load<false>((const W *)a.weight, w);
   part.settle(w);
   float dw[C][8];
 #pragma unroll
@@ -316,46 +317,51 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_backward_kernel(NormArgs a)
   }
 }
 
-template <typename T, int G, int C, int KIND, int WHICH> const void *norm_kernel_of(bool w32) {
+template <typename T, int G, int C, int KIND, int WHICH, bool ONCE> const void *norm_kernel_of(bool w32) {
   if constexpr (WHICH == NORM_BACK)
-    return w32 ? (const void *)norm_backward_kernel<T, G, C, KIND, true>
-               : (const void *)norm_backward_kernel<T, G, C, KIND, false>;
+    return w32 ? (const void *)norm_backward_kernel<T, G, C, KIND, true, ONCE>
+               : (const void *)norm_backward_kernel<T, G, C, KIND, false, ONCE>;
   else
-    return w32 ? (const void *)norm_kernel<T, G, C, KIND, true, WHICH == NORM_I8>
-               : (const void *)norm_kernel<T, G, C, KIND, false, WHICH == NORM_I8>;
+    return w32 ? (const void *)norm_kernel<T, G, C, KIND, true, WHICH == NORM_I8, ONCE>
+               : (const void *)norm_kernel<T, G, C, KIND, false, WHICH == NORM_I8, ONCE>;
+}
+template <typename T, int G, int C, int KIND, int WHICH> const void *norm_kernel_of(bool w32, bool once) {
+  if constexpr (KIND == ROW_WHOLE && WHICH != NORM_I8)
+    if (once) return norm_kernel_of<T, G, C, KIND, WHICH, true>(w32);
+  return norm_kernel_of<T, G, C, KIND, WHICH, false>(w32);
 }
 
-template <typename T, int WHICH> const void *norm_pick(int d, bool w32) {
+template <typename T, int WHICH> const void *norm_pick(int d, bool w32, bool once) {
   const int of = norm_lanes(d) * 8 + norm_chunks(d);
-  if (d < 8) return norm_kernel_of<T, 16, 1, ROW_TINY, WHICH>(w32);
+  if (d < 8) return norm_kernel_of<T, 16, 1, ROW_TINY, WHICH>(w32, once);
   if (d % 8) {
     switch (of) {
-    case 16 * 8 + 1: return norm_kernel_of<T, 16, 1, ROW_TAIL, WHICH>(w32);
-    case 16 * 8 + 2: return norm_kernel_of<T, 16, 2, ROW_TAIL, WHICH>(w32);
-    case 16 * 8 + 4: return norm_kernel_of<T, 16, 4, ROW_TAIL, WHICH>(w32);
-    case 32 * 8 + 4: return norm_kernel_of<T, 32, 4, ROW_TAIL, WHICH>(w32);
-    case 64 * 8 + 4: return norm_kernel_of<T, 64, 4, ROW_TAIL, WHICH>(w32);
-    default: return norm_kernel_of<T, 256, 4, ROW_TAIL, WHICH>(w32);
+    case 16 * 8 + 1: return norm_kernel_of<T, 16, 1, ROW_TAIL, WHICH>(w32, once);
+    case 16 * 8 + 2: return norm_kernel_of<T, 16, 2, ROW_TAIL, WHICH>(w32, once);
+    case 16 * 8 + 4: return norm_kernel_of<T, 16, 4, ROW_TAIL, WHICH>(w32, once);
+    case 32 * 8 + 4: return norm_kernel_of<T, 32, 4, ROW_TAIL, WHICH>(w32, once);
+    case 64 * 8 + 4: return norm_kernel_of<T, 64, 4, ROW_TAIL, WHICH>(w32, once);
+    default: return norm_kernel_of<T, 256, 4, ROW_TAIL, WHICH>(w32, once);
     }
   }
   switch (of) {
-  case 16 * 8 + 1: return norm_kernel_of<T, 16, 1, ROW_WHOLE, WHICH>(w32);
-  case 16 * 8 + 2: return norm_kernel_of<T, 16, 2, ROW_WHOLE, WHICH>(w32);
-  case 16 * 8 + 3: return norm_kernel_of<T, 16, 3, ROW_WHOLE, WHICH>(w32);
-  case 16 * 8 + 4: return norm_kernel_of<T, 16, 4, ROW_WHOLE, WHICH>(w32);
-  case 32 * 8 + 3: return norm_kernel_of<T, 32, 3, ROW_WHOLE, WHICH>(w32);
-  case 32 * 8 + 4: return norm_kernel_of<T, 32, 4, ROW_WHOLE, WHICH>(w32);
-  case 64 * 8 + 3: return norm_kernel_of<T, 64, 3, ROW_WHOLE, WHICH>(w32);
-  case 64 * 8 + 4: return norm_kernel_of<T, 64, 4, ROW_WHOLE, WHICH>(w32);
-  case 256 * 8 + 2: return norm_kernel_of<T, 256, 2, ROW_WHOLE, WHICH>(w32);
-  case 256 * 8 + 3: return norm_kernel_of<T, 256, 3, ROW_WHOLE, WHICH>(w32);
-  default: return norm_kernel_of<T, 256, 4, ROW_WHOLE, WHICH>(w32);
+  case 16 * 8 + 1: return norm_kernel_of<T, 16, 1, ROW_WHOLE, WHICH>(w32, once);
+  case 16 * 8 + 2: return norm_kernel_of<T, 16, 2, ROW_WHOLE, WHICH>(w32, once);
+  case 16 * 8 + 3: return norm_kernel_of<T, 16, 3, ROW_WHOLE, WHICH>(w32, once);
+  case 16 * 8 + 4: return norm_kernel_of<T, 16, 4, ROW_WHOLE, WHICH>(w32, once);
+  case 32 * 8 + 3: return norm_kernel_of<T, 32, 3, ROW_WHOLE, WHICH>(w32, once);
+  case 32 * 8 + 4: return norm_kernel_of<T, 32, 4, ROW_WHOLE, WHICH>(w32, once);
+  case 64 * 8 + 3: return norm_kernel_of<T, 64, 3, ROW_WHOLE, WHICH>(w32, once);
+  case 64 * 8 + 4: return norm_kernel_of<T, 64, 4, ROW_WHOLE, WHICH>(w32, once);
+  case 256 * 8 + 2: return norm_kernel_of<T, 256, 2, ROW_WHOLE, WHICH>(w32, once);
+  case 256 * 8 + 3: return norm_kernel_of<T, 256, 3, ROW_WHOLE, WHICH>(w32, once);
+  default: return norm_kernel_of<T, 256, 4, ROW_WHOLE, WHICH>(w32, once);
   }
 }
-template <typename T> const void *norm_kernel_for(int which, int d, bool w32) {
-  return which == NORM_Y    ? norm_pick<T, NORM_Y>(d, w32)
-         : which == NORM_I8 ? norm_pick<T, NORM_I8>(d, w32)
-                            : norm_pick<T, NORM_BACK>(d, w32);
+template <typename T> const void *norm_kernel_for(int which, int d, bool w32, bool once) {
+  return which == NORM_Y    ? norm_pick<T, NORM_Y>(d, w32, once)
+         : which == NORM_I8 ? norm_pick<T, NORM_I8>(d, w32, once)
+                            : norm_pick<T, NORM_BACK>(d, w32, once);
 }
 
 }  // namespace maxsim

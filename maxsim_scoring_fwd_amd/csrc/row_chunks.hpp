@@ -8,11 +8,38 @@
 
 namespace maxsim {
 
+// A call that moves more than the chip's last cache holds passes it by (non-temporal loads and
+// stores): its lines would be gone before anyone could use them, and writing them back costs the
+// call itself or the next one. Dropout of a tensor, and of its result, and so on: 128 MiB (256 moved)
+// 39.4 us through the caches and 43.7 past them, 192 MiB 69.5 and 65.2; a norm's forward and backward
+// in turn, 64 MiB a tensor (256 moved by the forward) 85.0 and 90.1, 96 MiB 138.2 and 133.5.
+constexpr int64_t CACHE_BYTES = (int64_t)256 << 20;
+
 template <typename T> struct Chunk8 {
   T e[8];
 } __attribute__((packed, aligned(sizeof(T))));
 
-template <typename T> __device__ __forceinline__ Chunk8<T> whole_chunk(const T *p) { return *(const Chunk8<T> *)p; }
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes anywhere
+template <typename T> struct Chunk8Words {
+  u32x4_any v[sizeof(T) / 2];
+};
+template <bool ONCE = false, typename T> __device__ __forceinline__ Chunk8<T> whole_chunk(const T *p) {
+  if constexpr (!ONCE) return *(const Chunk8<T> *)p;
+  Chunk8Words<T> x;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; i++) x.v[i] = __builtin_nontemporal_load((const u32x4_any *)p + i);
+  return __builtin_bit_cast(Chunk8<T>, x);
+}
+template <bool ONCE = false, typename T> __device__ __forceinline__ void store_whole(T *p, const Chunk8<T> &c) {
+  if constexpr (!ONCE) {
+    *(Chunk8<T> *)p = c;
+  } else {
+    const Chunk8Words<T> x = __builtin_bit_cast(Chunk8Words<T>, c);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; i++) __builtin_nontemporal_store(x.v[i], (u32x4_any *)p + i);
+  }
+}
+
 template <typename T> __device__ __forceinline__ Chunk8<T> rounded(const float (&v)[8]) {
   Chunk8<T> c;
 #pragma unroll
