@@ -902,7 +902,7 @@ def _norm_args(x, weight, residual, eps):
     tensor = torch.Tensor
     if isinstance(x, tensor) and isinstance(weight, tensor):
         shape, dt = x.shape, x.dtype
-        if dt in _TORCH_DTYPE and x.is_contiguous() and eps >= 0 and weight.shape == shape[-1:] and \
+        if dt in _TORCH_DTYPE and shape and x.is_contiguous() and eps >= 0 and weight.shape == shape[-1:] and \
                 (weight.dtype == dt or weight.dtype == torch.float32) and x.numel() and \
                 (residual is None or (isinstance(residual, tensor) and residual.dtype == dt and
                                       residual.shape == shape and residual.is_contiguous())):

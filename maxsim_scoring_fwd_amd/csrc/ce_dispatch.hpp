@@ -6,7 +6,9 @@
 
 namespace maxsim {
 
+// Places of the rings: three leave room for two workgroups a CU; twelve of 10 KB fill one's LDS.
 constexpr int CE_STAGES = 3, CE_FEW_STAGES = 12;
+
 template <typename Kernel> int ce_launch(Kernel kernel, int64_t tiles, int lds, int cus, const CeArgs &a, hipStream_t st) {
   // the tiles are dealt out on the device, where their number is known: no more workgroups than
   // there can be tiles, nor than the chip holds at once
@@ -25,11 +27,10 @@ template <int DT> int ce_gathered(const CeArgs &a, bool count, hipStream_t st) {
 }
 
 template <int DT> int ce_forward(const CeArgs &a, int cus, hipStream_t st) {
-  int across = (int)blocks_of(a.vocab, CE_BM);
+  const int across = (int)blocks_of(a.vocab, CE_BM);
   if (ce_few(a)) {
-    using G = TileGemm<DT, CE_SMALL_BM, CE_SMALL_BN, 4, SIDE_ROWS, SIDE_ROWS, CE_FEW_STAGES>;
+    using G = TileGemm<DT, CE_BM, CE_SMALL_BN, 4, SIDE_ROWS, SIDE_ROWS, CE_FEW_STAGES>;
     constexpr int lds = G::lds + CE_FEW * sizeof(CeRow);
-    across = (int)blocks_of(a.vocab, CE_SMALL_BM);
     const unsigned grid = (unsigned)(across * blocks_of(a.n, CE_SMALL_BN));
     hipLaunchKernelGGL((ce_few_kernel<DT, CE_FEW_STAGES>), dim3(grid), dim3(GEMM_THREADS), lds, st, a);
     if (hipGetLastError() != hipSuccess) return MAXSIM_ERR_LAUNCH;

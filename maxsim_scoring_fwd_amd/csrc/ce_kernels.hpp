@@ -10,19 +10,30 @@
 // Sums are 32 bits wide, every one has one owner and a fixed order. P is rounded because the matrix
 // cores take 16-bit operands; in fp16, whose range is short, it is scaled by a power of two first,
 // taken from the largest gradient of a row.
+// The matrix cores bound the training step and the bytes of w the few rows of a query. Measured (one
+// MI355X): 8192 rows, 30522 entries, d = 768 in bf16: gathering 11 us (twice), logits and their
+// sums 374 to 390 (1.03 to 0.99 PFLOP/s; a library product of the shape takes 410 and writes the
+// logits), join 8.5, P 397 to 412, both products 656 to 663 (1.17; the library 419 + 573), dh's join
+// 23; the clock falls to 1.6 to 1.8 GHz meanwhile, and the matrix cores are busy half of the cycles
+// (54, 51 and 64 in 100). 32 rows: 11.8 us and 4.2 for the join, of which 9.3 are w's 47 MB.
 #pragma once
 
 #include "tile_gemm.hpp"
 
 namespace maxsim {
 
-constexpr int CE_BM = 128, CE_BN = 256;              // vocabulary x rows of a tile of logits
-constexpr int CE_PM = 256, CE_PN = 128;              // columns x vocabulary (dw) or rows (dh) of a product's
-constexpr int CE_SMALL_BM = 128, CE_SMALL_BN = 32;   // for few rows
-constexpr int CE_FEW = 64;                           // most rows of the kernel for few rows
-constexpr int CE_GATHER = 16;                        // rows of a workgroup of the gathering
-constexpr int CE_COUNT = 1024;                       // rows of a workgroup of the counting
-constexpr int CE_DIRECT = 8192;                      // up to so many rows the gathering counts for itself
+// Tiles: 128 registers of sums a lane, and a ring of three steps in 72 KB, so that two workgroups fit a
+// CU and one multiplies while the other one waits or goes on with its logits. Tiles of 128 x 128
+// read a third more (logits of 8192 x 30522 x 768: 424 us for 395, the panels' share included).
+constexpr int CE_BM = 128, CE_BN = 256;   // vocabulary x rows of a tile of logits
+constexpr int CE_PM = 256, CE_PN = 128;   // columns x vocabulary (dw) or rows (dh) of a product's
+constexpr int CE_SMALL_BN = 32;           // rows of a tile for few rows
+constexpr int CE_FEW = 64;                // most rows of the kernel for few rows: lanes of a wave
+constexpr int CE_GATHER = 16;             // rows of a workgroup of the gathering
+constexpr int CE_COUNT = 1024;            // rows of a workgroup of the counting
+// Up to so many rows the gathering counts the labels before its own by itself: at most 64 KB of them
+// from L2, which hides behind the rows' copies, and a launch of some 5 us less.
+constexpr int CE_DIRECT = 8192;
 
 struct CeArgs {
   const char *h, *w;
@@ -50,7 +61,8 @@ struct CeArgs {
   int lanes;              // backward: workgroups of the products
 };
 
-// Whether the forward takes the kernel for few rows.
+// Whether the forward takes the kernel for few rows: two launches for three, and all steps that LDS
+// holds under way for three (32 rows, 30522 x 768 in bf16: 15.6 us for 22.4).
 inline bool ce_few(const CeArgs &a) { return a.n <= CE_FEW && a.row_bytes % 64 == 0; }
 
 // A gathered row: its label, its place among all rows, and for the backward its lse in units of log
@@ -238,7 +250,8 @@ __device__ __forceinline__ void ce_tile(uint32_t i, uint32_t across, uint32_t do
   r = group * 8 + in - v * wide;
 }
 // The same with an eighth of the vocabulary for each XCD: the vocabulary's rows are then read by one
-// XCD alone, and 8 tiles of rows stay in its L2 while it goes through its eighth.
+// XCD alone, and 8 tiles of rows stay in its L2 while it goes through its eighth (8192 x 30522 x 768:
+// logits 390 us for 395 with one order over all XCDs, P 404 for 418).
 __device__ __forceinline__ void ce_tile_of_xcd(uint32_t i, uint32_t across, uint32_t down, uint32_t &v, uint32_t &r) {
   const uint32_t eighth = (across + 7) / 8, x = i / (eighth * down), v0 = x * eighth;
   ce_tile(i - x * eighth * down, across - v0 < eighth ? across - v0 : eighth, down, v, r);
@@ -385,7 +398,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_forward_kernel(CeArgs a) {
 // vocabulary's bytes bound it: as many steps under way as LDS holds.
 template <int DT, int STAGES>
 __global__ void __launch_bounds__(GEMM_THREADS) ce_few_kernel(CeArgs a) {
-  constexpr int BM = CE_SMALL_BM, BN = CE_SMALL_BN, WM = 4;
+  constexpr int BM = CE_BM, BN = CE_SMALL_BN, WM = 4;
   using G = TileGemm<DT, BM, BN, WM, SIDE_ROWS, SIDE_ROWS, STAGES>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   CeRow *row = (CeRow *)(lds + G::lds);  // of the rows that count

@@ -7,10 +7,13 @@ using namespace maxsim;
 
 namespace {
 
-// Room for P, one piece of the vocabulary: what stays in the chip's 256 MiB cache between the kernel
-// that makes it and those that read it, and at least one tile of the vocabulary for all rows.
+// Room for P, one piece of the vocabulary, and at least one tile of it for all rows. Fewer and longer
+// pieces are worth more than a P that stays in the chip's 256 MiB cache: each piece adds to dh's
+// sums and ends with workgroups that wait for the last (8192 x 30522 x 768 in bf16, both products
+// of all pieces: room of 128 MiB 818 us, 256 MiB 718, 512 MiB 677, where P is one piece).
 constexpr int64_t CE_P_BYTES = (int64_t)512 << 20;
-// dh's tiles in parts: two for every workgroup that the chip holds (CeUnits)
+// Room for dh's tiles in parts: two for every workgroup that the chip holds at once, so that CeUnits
+// can make parts short enough where there are few tiles.
 constexpr int64_t CE_SLOTS = 1024;
 
 // A step's panels are reached by 32-bit offsets.
@@ -41,7 +44,7 @@ size_t ce_carve(CeArgs &a, int eb, bool backward, char *base) {
   a.info = c.take<int4>(a.n);
   a.hc = c.take<char>(a.n * (blocks_of((int64_t)a.d * eb, PANEL) * PANEL));
   if (!backward) {
-    const int64_t tiles = blocks_of(a.vocab, CE_SMALL_BM < CE_BM ? CE_SMALL_BM : CE_BM);
+    const int64_t tiles = blocks_of(a.vocab, CE_BM);
     a.part = c.take<float2>(tiles * a.n);
     a.picked = c.take<float>(a.n);
     return c.at;

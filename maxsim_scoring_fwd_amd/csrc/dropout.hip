@@ -1,6 +1,8 @@
 // Dropout (include/maxsim.h, maxsim_dropout): y = x / (1 - p) where an entry is kept, else 0. One
-// read and one write of the tensor, or the generator's arithmetic, bounds it: a thread makes the
-// bits of the 8 entries that it holds.
+// read and one write of the tensor bound it, with the generator's arithmetic hidden behind them: a
+// thread makes the bits of the 8 entries that it holds, for 4 chunks whose loads are under way
+// together (81907 x 2048 in bf16 on one MI355X: 107 to 111 us, 671 MB at 6.2 TB/s, and 188 with loads
+// that wait for each other; 101 x 513 3.1 us).
 #include <hip/hip_runtime.h>
 
 #include "dropout_bits.hpp"

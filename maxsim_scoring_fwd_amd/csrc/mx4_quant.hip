@@ -1,7 +1,8 @@
 // Microscaled 4-bit vectors (include/maxsim.h, maxsim_quantize_mx4): 32 entries share a power of
 // two, 2^(floor(log2 of the largest) - 2), and each is the nearest of 0, 1/2, 1, 3/2, 2, 3, 4 and 6
 // times that, ties to the even code, 6 where it is larger. The conversions are the hardware's, on
-// entries that were multiplied by an exact power of two first. Bytes bound both directions.
+// entries that were multiplied by an exact power of two first. Bytes bound both directions (1638401
+// rows of 128 in bf16 on one MI355X: 84 us to codes, 531 MB at 6.3 TB/s, and 87 us back).
 #include <hip/hip_runtime.h>
 
 #include "device_common.hpp"

@@ -9,7 +9,10 @@
 // to the operand as they lie: 16 bytes and one byte a lane, the whole 64-byte rows of 128 entries
 // side by side in one instruction. Each product of two entries and their powers of two is exact in
 // 32 bits. Rows shorter than whole 128 entries: the lanes past the end fetch the row's first block
-// (finite, in range) and meet zeros in the query's operand.
+// (finite, in range) and meet zeros in the query's operand. The read of the documents bounds it: on
+// one MI355X 100000 documents of 128 tokens, d = 128, take 129 to 132 us (870 MB at 6.7 TB/s), and
+// 20000 of 20 to 300 tokens, d = 96, 34 us (163 MB at 4.8 TB/s, of which the search for a wave's
+// documents and the last tiles are some 10 us).
 #pragma once
 
 #include "dense_kernel.hpp"

