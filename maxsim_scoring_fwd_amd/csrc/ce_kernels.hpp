@@ -87,7 +87,10 @@ struct CePieces {
 };
 
 // The products of one piece: dw's tiles, and dh's, whose sums over the piece go in several parts, so
-// that all workgroups end about together: a part is about a third of a workgroup's share.
+// that all workgroups end about together: parts of at most a workgroup's share, of 8 steps and more.
+// Shorter ones, of a third, cost more to join than they even out, since the longer units go first and a
+// workgroup that is left alone on its CU runs faster (backward of 3001 rows, 50021 x 512 in fp16: 559
+// us in thirds, 548; 2048 rows, 30522 x 768 in bf16: 321 and 306).
 template <int DT> struct CeUnits {
   uint32_t w_across, w_down, h_across, h_down, splits;
   __device__ __host__ __forceinline__ CeUnits(const CeArgs &a, int64_t m, const CePieces &p) {
@@ -97,14 +100,13 @@ template <int DT> struct CeUnits {
     h_down = (uint32_t)blocks_of(m, CE_PN);
     const int64_t tiles = (int64_t)h_across * h_down, steps = p.cols / BK;
     const int64_t all = (a.dw ? (int64_t)w_across * w_down * blocks_of(m, BK) : 0) + tiles * steps;
-    int64_t s = blocks_of(3 * steps * a.lanes, all < 1 ? 1 : all);
-    const int64_t room = a.slots / (tiles < 1 ? 1 : tiles), most = steps / 8;
-    s = s < room ? s : room;
-    s = s < most ? s : most;
+    const int64_t least = blocks_of(steps * a.lanes, all < 1 ? 1 : all);
+    int64_t most = a.slots / (tiles < 1 ? 1 : tiles);
+    most = most < steps / 8 ? most : steps / 8;
     // a power of two: the parts are dealt to 8 XCDs in order, and one that has parts of two kinds
-    // reads the columns of both (8192 x 30522 x 768: 729 us in 3 parts, 663 in 4, 710 in 6)
+    // reads the columns of both (8192 rows, 30522 x 768: 729 us in 3 parts, 663 in 4, 710 in 6)
     splits = 1;
-    while (2 * splits <= s) splits *= 2;
+    while (splits < least && 2 * splits <= most) splits *= 2;
   }
 };
 
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_p_kernel(CeArgs a) {
 // The products of one piece: dw = P^T h over the gathered rows, tile by tile; and dh's sums over the
 // piece, added to those of the pieces before, in parts, in the register layout. The units of each
 // XCD's workgroups lie side by side, so that its L2 serves what they share; a workgroup takes the
-// next one when it has ended one, the long ones first. Who makes a unit does not change it.
+// next one when it has ended one, the longer kind first. Who makes a unit does not change it.
 template <int DT, int STAGES>
 __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_products_kernel(CeArgs a) {
   constexpr int BM = CE_PM, BN = CE_PN, WM = 2;
@@ -551,6 +553,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_products_kernel(CeArgs a) 
   const uint32_t x = blockIdx.x & 7;
   const uint32_t w_from = (uint64_t)w_units * x / 8, w_n = (uint64_t)w_units * (x + 1) / 8 - w_from;
   const uint32_t h_from = (uint64_t)h_units * x / 8, h_n = (uint64_t)h_units * (x + 1) / 8 - h_from;
+  const bool h_first = cols > (int64_t)m * units.splits;
+  const uint32_t first_n = h_first ? h_n : w_n;
   const int wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
   const float back = 1.0f / ce_up<DT>(a);
   constexpr int eb = Elem<DT>::bytes, part = BM / WM;
@@ -559,10 +563,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_products_kernel(CeArgs a) 
     __syncthreads();
     if (threadIdx.x == 0) taken = atomicAdd(a.queue + x, 1);
     __syncthreads();
-    const uint32_t unit = uniform(taken);
+    uint32_t unit = uniform(taken);
     if (unit >= w_n + h_n) break;
+    const bool second = unit >= first_n;
+    if (second) unit -= first_n;
     uint32_t tc, tr;
-    if (unit < w_n) {
+    if (second == h_first) {
       ce_tile(w_from + unit, units.w_across, w_down, tc, tr);
       const int c0 = (int)tc * BM;
       const int64_t v0 = (int64_t)tr * BN;
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_products_kernel(CeArgs a) 
                                        a.row_bytes, left < 32 ? (int)left : 32, row_bytes);
       }
     } else {
-      const uint32_t id = h_from + unit - w_n, split = id / h_tiles;
+      const uint32_t id = h_from + unit, split = id / h_tiles;
       ce_tile(id - split * h_tiles, units.h_across, units.h_down, tc, tr);
       const int c0 = (int)tc * BM;
       const int64_t r0 = (int64_t)tr * BN;
@@ -621,7 +627,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_products_kernel(CeArgs a) 
   }
 }
 
-// dh from its parts, rounded once, to the rows' own places.
+// dh from its parts, rounded once, to the rows' own places. The parts' bytes bound it; where there are few
+// tiles of many parts, their loads' waits do: 8 under way (130 rows, 100000 x 128, 256 parts: the
+// backward 158 us with one block a workgroup and a part at a time, 88 so).
 template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_dh_join_kernel(CeArgs a) {
   constexpr int BM = CE_PM, BN = CE_PN, WM = 2;
   using G = TileGemm<DT, BM, BN, WM, SIDE_COLS, SIDE_ROWS_P, 3>;
@@ -633,30 +641,37 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_dh_join_ker
   const uint32_t across = units.h_across, down = units.h_down, tiles = across * down, splits = units.splits;
   const float back = 1.0f / ce_up<DT>(a);
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
-  // a block of 32 x 32 of a tile for each round
-  const uint32_t total = tiles * G::TN * G::TM;
+  // A quarter of a block of 32 x 32 of a tile for each wave and round, so that few tiles of many parts
+  // spread over the chip; the quarters of a block on one XCD, whose L2 joins what they write.
+  const uint32_t total = tiles * G::TN * G::TM * 4;
+  static_assert(G::TN * G::TM % 8 == 0, "whole rounds of the XCDs");
+  const int64_t part = (int64_t)tiles * (BM * BN / 4);
   for (uint32_t i = blockIdx.x; i < total; i += gridDim.x) {
-    const uint32_t tile = i / (G::TN * G::TM), nk = i - tile * (G::TN * G::TM);
+    const uint32_t block = i / 32 * 8 + i % 8, q = i / 8 % 4;
+    const uint32_t tile = block / (G::TN * G::TM), nk = block - tile * (G::TN * G::TM);
     const int n = nk / G::TM, k = nk - n * G::TM;
     uint32_t tc, tr;
     ce_tile(tile, across, down, tc, tr);
     const int64_t r = (int64_t)tr * BN + (wn * G::TN + n) * 32 + (lane & 31);
-    const int c = (int)tc * BM + (wm * G::TM + k) * 32 + 4 * (lane >> 5);
-    const f32x4_t *p = (const f32x4_t *)a.dhp + (int64_t)tile * (BM * BN / 4) + nk * 4 * GEMM_THREADS + threadIdx.x;
-    f32x4_t x[4] = {};
-    for (uint32_t s = 0; s < splits; s++)
+    const int c = (int)tc * BM + (wm * G::TM + k) * 32 + 4 * (lane >> 5) + 8 * q;
+    const f32x4_t *p = (const f32x4_t *)a.dhp + (int64_t)tile * (BM * BN / 4) + (nk * 4 + q) * GEMM_THREADS + threadIdx.x;
+    constexpr int AHEAD = 8;
+    f32x4_t x = {};
+    uint32_t s = 0;
+    for (; s + AHEAD <= splits; s += AHEAD) {
+      f32x4_t y[AHEAD];
 #pragma unroll
-      for (int q = 0; q < 4; q++) x[q] += p[(int64_t)s * tiles * (BM * BN / 4) + q * GEMM_THREADS];
-    if (r >= m) continue;
-    T *to = (T *)(a.dh + (int64_t)__builtin_bit_cast(CeRow, a.info[r]).row * a.row_bytes);
+      for (int j = 0; j < AHEAD; j++) y[j] = p[(s + j) * part];
 #pragma unroll
-    for (int q = 0; q < 4; q++) {
-      if (c + 8 * q >= a.d) break;  // d is a multiple of 4 entries
-      v4 o;
-#pragma unroll
-      for (int e = 0; e < 4; e++) o[e] = (T)(x[q][e] * back);
-      *(v4 *)(to + c + 8 * q) = o;
+      for (int j = 0; j < AHEAD; j++) x += y[j];
     }
+    for (; s < splits; s++) x += p[s * part];
+    if (r >= m || c >= a.d) continue;  // d is a multiple of 4 entries
+    T *to = (T *)(a.dh + (int64_t)__builtin_bit_cast(CeRow, a.info[r]).row * a.row_bytes);
+    v4 o;
+#pragma unroll
+    for (int e = 0; e < 4; e++) o[e] = (T)(x[e] * back);
+    *(v4 *)(to + c) = o;
   }
 }
 
