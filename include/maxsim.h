@@ -479,7 +479,8 @@ size_t maxsim_linear_cross_entropy_workspace_size(int64_t n_rows, int64_t vocab,
  *     P = (exp(z - lse) - [v is the label]) * grad_loss * scale,   dh = P w,   dw = P^T h
  * with P, one piece of it, in the workspace, rounded to `dtype` (fp16: scaled by a power of two
  * taken from the largest gradient first). Sums are fp32, each result is rounded once. A piece of P
- * takes 512 MiB at most, or 128 columns. With n_rows == 0 dw is set to zero.
+ * takes 512 MiB at most, or 128 columns; dh's sums take 4 bytes an entry and at least 128 MiB, a
+ * small vocabulary's dw 128 MiB. With n_rows == 0 dw is set to zero.
  */
 int maxsim_linear_cross_entropy_backward(const float *grad_loss, const void *h, const void *w,
                                          const int64_t *labels, const float *lse, int64_t n_rows,

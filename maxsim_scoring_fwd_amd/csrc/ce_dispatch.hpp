@@ -51,13 +51,15 @@ template <int DT> int ce_backward(CeArgs &a, int64_t pieces, int cus, hipStream_
   const int64_t any = (int64_t)1 << 30;
   using Z = CeLogits<DT, CE_BM, CE_BN, 2, CE_STAGES>;
   using G = TileGemm<DT, CE_PM, CE_PN, 2, SIDE_COLS_P, SIDE_COLS_P, CE_STAGES>;
-  a.lanes = cus * blocks_per_cu((const void *)ce_products_kernel<DT, CE_STAGES>, GEMM_THREADS, G::lds);
+  // with fewer rows there are fewer pieces and more tiles of dw in one
+  if (CeUnits(a, a.n, CePieces(a.n, a.vocab, a.p_elements), Elem<DT>::bytes).w_splits == 1) a.w_slots = 0;
   for (a.piece = 0; a.piece < pieces; a.piece++) {
     rc = ce_launch(ce_p_kernel<DT, CE_STAGES>, any, Z::lds, cus, a, st);
     if (rc == MAXSIM_OK) rc = ce_launch(ce_products_kernel<DT, CE_STAGES>, any, G::lds, cus, a, st);
+    if (rc == MAXSIM_OK && a.dw && a.w_slots) rc = ce_launch(ce_parts_kernel<DT, true>, any, 0, cus, a, st);
     if (rc != MAXSIM_OK) return rc;
   }
-  return a.dh ? ce_launch(ce_dh_join_kernel<DT>, any, 0, cus, a, st) : MAXSIM_OK;
+  return a.dh ? ce_launch(ce_parts_kernel<DT, false>, any, 0, cus, a, st) : MAXSIM_OK;
 }
 
 }  // namespace maxsim

@@ -53,12 +53,11 @@ struct CeArgs {
   float2 *part;           // [tiles of the vocabulary][n]: largest logit (in units of log 2), sum
   float *picked;          // [n]: the label's logit, in units of log 2
   char *p;                // P in panels of 64 bytes, whole tiles of rows each
-  float *dhp;             // tiles of dh in the kernels' register layout
+  float *dhp, *dwp;       // tiles of dh and, where they go in parts, of dw, in the kernels' register layout
   int32_t *queue;         // [8]: units of the products that are taken
   int64_t p_elements;     // that p has room for
-  int64_t slots;          // tiles that dhp has room for
+  int64_t slots, w_slots; // tiles that dhp and dwp have room for
   int64_t piece;          // backward: number of this piece
-  int lanes;              // backward: workgroups of the products
 };
 
 // Whether the forward takes the kernel for few rows: two launches for three, and all steps that LDS
@@ -86,27 +85,37 @@ struct CePieces {
   }
 };
 
-// The products of one piece: dw's tiles, and dh's, whose sums over the piece go in several parts, so
-// that all workgroups end about together: parts of at most a workgroup's share, of 8 steps and more.
-// Shorter ones, of a third, cost more to join than they even out, since the longer units go first and a
-// workgroup that is left alone on its CU runs faster (backward of 3001 rows, 50021 x 512 in fp16: 559
-// us in thirds, 548; 2048 rows, 30522 x 768 in bf16: 321 and 306).
-template <int DT> struct CeUnits {
-  uint32_t w_across, w_down, h_across, h_down, splits;
-  __device__ __host__ __forceinline__ CeUnits(const CeArgs &a, int64_t m, const CePieces &p) {
-    constexpr int BK = 64 / Elem<DT>::bytes;
+// The products of one piece: tiles of dw, and of dh, whose sums over the piece go in several parts
+// where a tile is more than a workgroup's share of it all, so that all workgroups end about together.
+// dh's parts are a share at most, of 8 steps and more. Shorter ones, of a third, cost more to join
+// than they even out, since the longer units go first and a workgroup that is left alone on its CU
+// runs faster (backward of 3001 rows, 50021 x 512 in fp16: 559 us in thirds, 548; 2048 rows, 30522 x
+// 768 in bf16: 321 and 306); fp32's products leave no such slack: half a share (2000 rows, 20000 x
+// 512: 1114 us in shares, 986 in halves). dw's tiles are few where the rows are many and short, and
+// need a launch more to be joined: parts of half a share, of 16 steps and more (whole and in parts:
+// 32768 rows, 30522 x 256 in bf16 3135 and 2130 us; 16384 rows, 10000 x 384 in fp16 555 and 547, in
+// shares 588; 8192 rows, 500 x 512 164 and 66).
+constexpr int CE_LANES = 512;  // workgroups at once: two on each of 256 CUs
+struct CeUnits {
+  uint32_t w_across, w_down, h_across, h_down;
+  uint32_t w_splits, h_splits;  // parts along the rows, along the piece
+  __device__ __host__ __forceinline__ CeUnits(const CeArgs &a, int64_t m, const CePieces &p, int eb) {
     w_across = h_across = (uint32_t)blocks_of(a.d, CE_PM);
     w_down = (uint32_t)blocks_of(p.cols, CE_PN);
     h_down = (uint32_t)blocks_of(m, CE_PN);
-    const int64_t tiles = (int64_t)h_across * h_down, steps = p.cols / BK;
-    const int64_t all = (a.dw ? (int64_t)w_across * w_down * blocks_of(m, BK) : 0) + tiles * steps;
-    const int64_t least = blocks_of(steps * a.lanes, all < 1 ? 1 : all);
-    int64_t most = a.slots / (tiles < 1 ? 1 : tiles);
-    most = most < steps / 8 ? most : steps / 8;
-    // a power of two: the parts are dealt to 8 XCDs in order, and one that has parts of two kinds
+    const int64_t w = (int64_t)w_across * w_down, h = (int64_t)h_across * h_down;
+    const int64_t w_steps = blocks_of(m * eb, 64), h_steps = p.cols * eb / 64;
+    const int64_t all = (a.dw ? w * w_steps : 0) + (a.dh ? h * h_steps : 0);
+    // powers of two: the parts are dealt to 8 XCDs in order, and one that has parts of two kinds
     // reads the columns of both (8192 rows, 30522 x 768: 729 us in 3 parts, 663 in 4, 710 in 6)
-    splits = 1;
-    while (splits < least && 2 * splits <= most) splits *= 2;
+    auto parts = [&](int64_t tiles, int64_t steps, int64_t slots, int least, int fine) {
+      uint32_t n = 1;
+      if (all >= steps * CE_LANES) return n;  // a tile is within a share
+      while (n * all < steps * CE_LANES * fine && 2 * n * tiles <= slots && 2 * least * n <= steps) n *= 2;
+      return n;
+    };
+    w_splits = parts(w, w_steps, a.w_slots, 16, 2);
+    h_splits = parts(h, h_steps, a.slots, 8, eb == 4 ? 2 : 1);
   }
 };
 
@@ -531,8 +540,23 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_p_kernel(CeArgs a) {
   }
 }
 
-// The products of one piece: dw = P^T h over the gathered rows, tile by tile; and dh's sums over the
-// piece, added to those of the pieces before, in parts, in the register layout. The units of each
+// A tile in the register layout, added to what is there or not.
+template <typename G> __device__ __forceinline__ void ce_store_tile(const G &g, f32x4_t *out, bool add) {
+#pragma unroll
+  for (int n = 0; n < G::TN; n++)
+#pragma unroll
+    for (int k = 0; k < G::TM; k++)
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        f32x4_t y = {g.acc[n][k][4 * q], g.acc[n][k][4 * q + 1], g.acc[n][k][4 * q + 2], g.acc[n][k][4 * q + 3]};
+        f32x4_t *at = out + ((n * G::TM + k) * 4 + q) * GEMM_THREADS + threadIdx.x;
+        if (add) y += *at;
+        *at = y;
+      }
+}
+
+// The products of one piece: dw = P^T h over the gathered rows, tile by tile, in parts in the register
+// layout or at once; and dh's sums over the piece, added to those of the pieces before, likewise. The units of each
 // XCD's workgroups lie side by side, so that its L2 serves what they share; a workgroup takes the
 // next one when it has ended one, the longer kind first. Who makes a unit does not change it.
 template <int DT, int STAGES>
@@ -547,13 +571,14 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_products_kernel(CeArgs a) 
   if (a.piece >= pieces.n) return;
   const int64_t piece0 = a.piece * pieces.cols;
   const int64_t cols = a.vocab - piece0 < pieces.cols ? a.vocab - piece0 : pieces.cols;
-  const CeUnits<DT> units(a, m, pieces);
-  const uint32_t w_down = (uint32_t)blocks_of(cols, BN), h_tiles = units.h_across * units.h_down;
-  const uint32_t w_units = a.dw ? units.w_across * w_down : 0, h_units = a.dh ? h_tiles * units.splits : 0;
+  const CeUnits units(a, m, pieces, Elem<DT>::bytes);
+  const uint32_t w_down = (uint32_t)blocks_of(cols, BN);
+  const uint32_t w_tiles = units.w_across * w_down, h_tiles = units.h_across * units.h_down;
+  const uint32_t w_units = a.dw ? w_tiles * units.w_splits : 0, h_units = a.dh ? h_tiles * units.h_splits : 0;
   const uint32_t x = blockIdx.x & 7;
   const uint32_t w_from = (uint64_t)w_units * x / 8, w_n = (uint64_t)w_units * (x + 1) / 8 - w_from;
   const uint32_t h_from = (uint64_t)h_units * x / 8, h_n = (uint64_t)h_units * (x + 1) / 8 - h_from;
-  const bool h_first = cols > (int64_t)m * units.splits;
+  const bool h_first = cols * units.w_splits > (int64_t)m * units.h_splits;
   const uint32_t first_n = h_first ? h_n : w_n;
   const int wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
   const float back = 1.0f / ce_up<DT>(a);
@@ -569,18 +594,27 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_products_kernel(CeArgs a) 
     if (second) unit -= first_n;
     uint32_t tc, tr;
     if (second == h_first) {
-      ce_tile(w_from + unit, units.w_across, w_down, tc, tr);
+      const uint32_t id = w_from + unit, split = id / w_tiles;
+      ce_tile(id - split * w_tiles, units.w_across, w_down, tc, tr);
       const int c0 = (int)tc * BM;
       const int64_t v0 = (int64_t)tr * BN;
+      const int steps = (int)blocks_of(m, GW::BK);
+      const int from = (int)((int64_t)steps * split / units.w_splits);
+      const int to = (int)((int64_t)steps * (split + 1) / units.w_splits);
       GW g;
       g.clear();
-      const int steps = (int)blocks_of(m, GW::BK);
-      if (steps > 0) {
-        g.a.start(a.hc + (int64_t)(c0 * eb / PANEL) * a.n * PANEL, a.n * PANEL, a.row_bytes - c0 * eb);
-        g.b.start(a.p + v0 * eb / PANEL * panel, panel, BN * eb);
+      if (to > from) {
+        const int64_t k0 = (int64_t)from * GW::BK;
+        g.a.start(a.hc + ((int64_t)(c0 * eb / PANEL) * a.n + k0) * PANEL, a.n * PANEL, a.row_bytes - c0 * eb);
+        g.b.start(a.p + v0 * eb / PANEL * panel + k0 * PANEL, panel, BN * eb);
         // rows of P past the last are zeros, and whole tiles of rows are there
-        g.begin(lds, steps, m - (steps - 1) * GW::BK, GW::BK);
+        const int left = m - (to - 1) * GW::BK;
+        g.begin(lds, to - from, left < GW::BK ? left : GW::BK, GW::BK);
         g.finish(lds);
+      }
+      if (units.w_splits > 1) {
+        ce_store_tile(g, (f32x4_t *)a.dwp + (int64_t)id * (BM * BN / 4), false);
+        continue;
       }
       char *mine = lds + wave * (32 * part * eb);
       const int at = c0 + wm * part;
@@ -598,8 +632,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_products_kernel(CeArgs a) 
       const int c0 = (int)tc * BM;
       const int64_t r0 = (int64_t)tr * BN;
       const int steps = (int)blocks_of(cols, GH::BK);
-      const int from = (int)((int64_t)steps * split / units.splits);
-      const int to = (int)((int64_t)steps * (split + 1) / units.splits);
+      const int from = (int)((int64_t)steps * split / units.h_splits);
+      const int to = (int)((int64_t)steps * (split + 1) / units.h_splits);
       GH g;
       g.clear();
       if (to > from) {
@@ -611,34 +645,27 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_products_kernel(CeArgs a) 
         g.begin(lds, to - from, left < GH::BK ? (int)left : GH::BK, 64);
         g.finish(lds);
       }
-      f32x4_t *out = (f32x4_t *)a.dhp + (int64_t)id * (BM * BN / 4) + threadIdx.x;
-#pragma unroll
-      for (int n = 0; n < GH::TN; n++)
-#pragma unroll
-        for (int k = 0; k < GH::TM; k++)
-#pragma unroll
-          for (int q = 0; q < 4; q++) {
-            f32x4_t y = {g.acc[n][k][4 * q], g.acc[n][k][4 * q + 1], g.acc[n][k][4 * q + 2], g.acc[n][k][4 * q + 3]};
-            f32x4_t *at = out + ((n * GH::TM + k) * 4 + q) * GEMM_THREADS;
-            if (a.piece > 0) y += *at;
-            *at = y;
-          }
+      ce_store_tile(g, (f32x4_t *)a.dhp + (int64_t)id * (BM * BN / 4), a.piece > 0);
     }
   }
 }
 
-// dh from its parts, rounded once, to the rows' own places. The parts' bytes bound it; where there are few
+// dh (or, of one piece, dw) from its parts, rounded once, to the rows' own places. The parts' bytes bound it; where there are few
 // tiles of many parts, their loads' waits do: 8 under way (130 rows, 100000 x 128, 256 parts: the
 // backward 158 us with one block a workgroup and a part at a time, 88 so).
-template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_dh_join_kernel(CeArgs a) {
+template <int DT, bool DW> __global__ void __launch_bounds__(GEMM_THREADS) ce_parts_kernel(CeArgs a) {
   constexpr int BM = CE_PM, BN = CE_PN, WM = 2;
   using G = TileGemm<DT, BM, BN, WM, SIDE_COLS, SIDE_ROWS_P, 3>;
   using T = typename AttnElem<DT>::type;
   typedef T v4 __attribute__((ext_vector_type(4)));
   const int m = uniform(*a.counted);
   const CePieces pieces(m, a.vocab, a.p_elements);
-  const CeUnits<DT> units(a, m, pieces);
-  const uint32_t across = units.h_across, down = units.h_down, tiles = across * down, splits = units.splits;
+  const CeUnits units(a, m, pieces, Elem<DT>::bytes);
+  const int64_t piece0 = a.piece * pieces.cols;
+  if (DW && (a.piece >= pieces.n || units.w_splits == 1)) return;
+  const int64_t rows = DW ? (a.vocab - piece0 < pieces.cols ? a.vocab - piece0 : pieces.cols) : m;
+  const uint32_t across = DW ? units.w_across : units.h_across, splits = DW ? units.w_splits : units.h_splits;
+  const uint32_t down = (uint32_t)blocks_of(rows, BN), tiles = across * down;
   const float back = 1.0f / ce_up<DT>(a);
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
   // A quarter of a block of 32 x 32 of a tile for each wave and round, so that few tiles of many parts
@@ -654,7 +681,8 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_dh_join_ker
     ce_tile(tile, across, down, tc, tr);
     const int64_t r = (int64_t)tr * BN + (wn * G::TN + n) * 32 + (lane & 31);
     const int c = (int)tc * BM + (wm * G::TM + k) * 32 + 4 * (lane >> 5) + 8 * q;
-    const f32x4_t *p = (const f32x4_t *)a.dhp + (int64_t)tile * (BM * BN / 4) + (nk * 4 + q) * GEMM_THREADS + threadIdx.x;
+    const f32x4_t *p = (const f32x4_t *)(DW ? a.dwp : a.dhp) + (int64_t)tile * (BM * BN / 4) +
+                       (nk * 4 + q) * GEMM_THREADS + threadIdx.x;
     constexpr int AHEAD = 8;
     f32x4_t x = {};
     uint32_t s = 0;
@@ -666,8 +694,9 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_dh_join_ker
       for (int j = 0; j < AHEAD; j++) x += y[j];
     }
     for (; s < splits; s++) x += p[s * part];
-    if (r >= m || c >= a.d) continue;  // d is a multiple of 4 entries
-    T *to = (T *)(a.dh + (int64_t)__builtin_bit_cast(CeRow, a.info[r]).row * a.row_bytes);
+    if (r >= rows || c >= a.d) continue;  // d is a multiple of 4 entries
+    T *to = (T *)(DW ? a.dw + (piece0 + r) * a.row_bytes
+                     : a.dh + (int64_t)__builtin_bit_cast(CeRow, a.info[r]).row * a.row_bytes);
     v4 o;
 #pragma unroll
     for (int e = 0; e < 4; e++) o[e] = (T)(x[e] * back);

@@ -13,8 +13,9 @@ namespace {
 // of all pieces: room of 128 MiB 818 us, 256 MiB 718, 512 MiB 677, where P is one piece).
 constexpr int64_t CE_P_BYTES = (int64_t)512 << 20;
 // Room for dh's tiles in parts: two for every workgroup that the chip holds at once, so that CeUnits
-// can make parts short enough where there are few tiles.
-constexpr int64_t CE_SLOTS = 1024;
+// can make parts short enough where there are few tiles; and for dw's of a piece, where there are less
+// than one for each.
+constexpr int64_t CE_SLOTS = 2 * CE_LANES;
 
 // A step's panels are reached by 32-bit offsets.
 constexpr int64_t CE_MOST_ROWS = (int64_t)1 << 22, CE_MOST_VOCAB = (int64_t)1 << 26;
@@ -59,6 +60,9 @@ size_t ce_carve(CeArgs &a, int eb, bool backward, char *base) {
   a.slots = blocks_of(a.d, CE_PM) * blocks_of(a.n, CE_PN);
   if (a.slots < CE_SLOTS) a.slots = CE_SLOTS;
   a.dhp = c.take<float>(a.slots * CE_PM * CE_PN);
+  const int64_t w = blocks_of(a.d, CE_PM) * blocks_of(CePieces(a.n, a.vocab, p).cols, CE_PN);
+  a.w_slots = w < CE_LANES ? CE_SLOTS : 0;
+  a.dwp = c.take<float>(a.w_slots * CE_PM * CE_PN);
   return c.at;
 }
 

@@ -201,6 +201,41 @@ def test_pieces_of_the_vocabulary(n, vocab, d, dtype, share):
     assert torch.isfinite(dh).all() and torch.isfinite(dw).all()
 
 
+@pytest.mark.parametrize("n, vocab, d, dtype, share", [
+    (4100, 300, 128, BF16, 1.0),
+    (8192, 129, 264, FP16, 0.97),
+    (2500, 513, 36, FP32, 0.9),
+    (9000, 100, 512, BF16, 0.03),     # as many rows, few that count
+])
+def test_many_rows_of_a_small_vocabulary(n, vocab, d, dtype, share):
+    """So few tiles of dw that their sums over the rows go in parts; each direction alone too, within
+    the workspace."""
+    print("case: many rows", n, vocab, d, dtype, share, flush=True)
+    h, w, y = make(n, vocab, d, dtype, share, seed=n)
+    dl = torch.linspace(-1, 2, n, device="cuda") / n
+    loss, lse = check(h, w, y, 0.8, dl)
+    want = ref.loss(as64(h), as64(w), y.cpu().numpy(), 0.8, as64(dl), h.dtype)
+    size = ms.linear_cross_entropy_backward_workspace_size(n, vocab, d, dtype)
+    for dh, dw in ((True, False), (False, True), (True, True)):
+        ws = torch.full((size + 64,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN in every type
+        got = ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, lse, 0.8, dh, dw, workspace=ws[:size])
+        for g, name in zip(got, ("dh", "dw")):
+            if g is not None:
+                ref.close(g, want[name], want["tol_" + name], name)
+        assert (ws[size:] == 0xFF).all()
+
+
+def test_few_tiles_in_several_pieces():
+    n, vocab, d = 70001, 4200, 64
+    h, w, y = make(n, vocab, d, BF16, seed=8)
+    dl = torch.rand(n, device="cuda") / n
+    loss, lse = ms.maxsim_linear_cross_entropy(h, w, y)
+    dh, dw = ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, lse)
+    part_of_gradients(h, w, y, lse, dl, 1.0, dh, dw, [0, 35000, n - 1], [*range(0, vocab, 127), vocab - 1])
+    again = ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, lse)
+    assert torch.equal(again[0], dh) and torch.equal(again[1], dw)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=str)
 def test_autograd(dtype):
     h, w, y = make(77, 200, 64, dtype, 0.7)
