@@ -6,8 +6,9 @@
 
 namespace maxsim {
 
-// Places of the rings: three leave room for two workgroups a CU; twelve of 10 KB fill one's LDS.
-constexpr int CE_STAGES = 3, CE_FEW_STAGES = 12;
+// Places of the rings: three of 24 KB, or four of 16, leave room for two workgroups a CU; twelve of 10 KB
+// fill one's LDS.
+constexpr int CE_STAGES = 3, CE_HALF_STAGES = 4, CE_FEW_STAGES = 12;
 
 template <typename Kernel> int ce_launch(Kernel kernel, int64_t tiles, int lds, int cus, const CeArgs &a, hipStream_t st) {
   // the tiles are dealt out on the device, where their number is known: no more workgroups than
@@ -29,16 +30,19 @@ template <int DT> int ce_gathered(const CeArgs &a, bool count, hipStream_t st) {
 template <int DT> int ce_forward(const CeArgs &a, int cus, hipStream_t st) {
   const int across = (int)blocks_of(a.vocab, CE_BM);
   if (ce_few(a)) {
-    using G = TileGemm<DT, CE_BM, CE_SMALL_BN, 4, SIDE_ROWS, SIDE_ROWS, CE_FEW_STAGES>;
+    using G = TileGemm<DT, CE_BM, CE_FEW, 4, SIDE_ROWS, SIDE_ROWS, CE_FEW_STAGES>;
     constexpr int lds = G::lds + CE_FEW * sizeof(CeRow);
-    const unsigned grid = (unsigned)(across * blocks_of(a.n, CE_SMALL_BN));
-    hipLaunchKernelGGL((ce_few_kernel<DT, CE_FEW_STAGES>), dim3(grid), dim3(GEMM_THREADS), lds, st, a);
+    hipLaunchKernelGGL((ce_few_kernel<DT, CE_FEW_STAGES>), dim3(across), dim3(GEMM_THREADS), lds, st, a);
     if (hipGetLastError() != hipSuccess) return MAXSIM_ERR_LAUNCH;
   } else {
     using Z = CeLogits<DT, CE_BM, CE_BN, 2, CE_STAGES>;
+    using H = CeLogits<DT, CE_BM, CE_HALF_BN, 2, CE_HALF_STAGES>;
     int rc = ce_gathered<DT>(a, a.n > CE_DIRECT, st);
     if (rc == MAXSIM_OK)
-      rc = ce_launch(ce_forward_kernel<DT, CE_BM, CE_BN, 2, CE_STAGES>, across * blocks_of(a.n, CE_BN), Z::lds, cus, a, st);
+      rc = a.n <= CE_HALF_BN
+               ? ce_launch(ce_forward_kernel<DT, CE_BM, CE_HALF_BN, 2, CE_HALF_STAGES>, across, H::lds, cus, a, st)
+               : ce_launch(ce_forward_kernel<DT, CE_BM, CE_BN, 2, CE_STAGES>, across * blocks_of(a.n, CE_BN), Z::lds,
+                           cus, a, st);
     if (rc != MAXSIM_OK) return rc;
   }
   hipLaunchKernelGGL(ce_join_kernel<DT>, dim3((unsigned)blocks_of(a.n, 8)), dim3(GEMM_THREADS), 0, st, a, across);
@@ -50,11 +54,14 @@ template <int DT> int ce_backward(CeArgs &a, int64_t pieces, int cus, hipStream_
   if (rc != MAXSIM_OK) return rc;
   const int64_t any = (int64_t)1 << 30;
   using Z = CeLogits<DT, CE_BM, CE_BN, 2, CE_STAGES>;
+  using H = CeLogits<DT, CE_BM, CE_HALF_BN, 2, CE_HALF_STAGES>;
   using G = TileGemm<DT, CE_PM, CE_PN, 2, SIDE_COLS_P, SIDE_COLS_P, CE_STAGES>;
   // with fewer rows there are fewer pieces and more tiles of dw in one
   if (CeUnits(a, a.n, CePieces(a.n, a.vocab, a.p_elements), Elem<DT>::bytes).w_splits == 1) a.w_slots = 0;
   for (a.piece = 0; a.piece < pieces; a.piece++) {
-    rc = ce_launch(ce_p_kernel<DT, CE_STAGES>, any, Z::lds, cus, a, st);
+    rc = a.n <= CE_HALF_BN
+             ? ce_launch(ce_p_kernel<DT, CE_BM, CE_HALF_BN, 2, CE_HALF_STAGES>, any, H::lds, cus, a, st)
+             : ce_launch(ce_p_kernel<DT, CE_BM, CE_BN, 2, CE_STAGES>, any, Z::lds, cus, a, st);
     if (rc == MAXSIM_OK) rc = ce_launch(ce_products_kernel<DT, CE_STAGES>, any, G::lds, cus, a, st);
     if (rc == MAXSIM_OK && a.dw && a.w_slots) rc = ce_launch(ce_parts_kernel<DT, true>, any, 0, cus, a, st);
     if (rc != MAXSIM_OK) return rc;

@@ -27,8 +27,10 @@ namespace maxsim {
 // read a third more (logits of 8192 x 30522 x 768: 424 us for 395, the panels' share included).
 constexpr int CE_BM = 128, CE_BN = 256;   // vocabulary x rows of a tile of logits
 constexpr int CE_PM = 256, CE_PN = 128;   // columns x vocabulary (dw) or rows (dh) of a product's
-constexpr int CE_SMALL_BN = 32;           // rows of a tile for few rows
-constexpr int CE_FEW = 64;                // most rows of the kernel for few rows: lanes of a wave
+// Where there are no more rows than that (100 rows, 100000 x 896 in fp16: forward 48 us and backward
+// 169, in tiles of 256 rows 62 and 187; 78 rows, 25314 x 712 in fp32 64 and 159 for 107 and 203).
+constexpr int CE_HALF_BN = 128;
+constexpr int CE_FEW = 32;                // most rows of the kernel for few rows: one tile's
 constexpr int CE_GATHER = 16;             // rows of a workgroup of the gathering
 constexpr int CE_COUNT = 1024;            // rows of a workgroup of the counting
 // Up to so many rows the gathering counts the labels before its own by itself: at most 64 KB of them
@@ -60,9 +62,10 @@ struct CeArgs {
   int64_t piece;          // backward: number of this piece
 };
 
-// Whether the forward takes the kernel for few rows: two launches for three, and all steps that LDS
-// holds under way for three (32 rows, 30522 x 768 in bf16: 15.6 us for 22.4).
-inline bool ce_few(const CeArgs &a) { return a.n <= CE_FEW && a.row_bytes % 64 == 0; }
+// Whether the forward takes the kernel for few rows: two launches for three, and as many steps under
+// way as LDS holds (32 rows, 30522 x 768 in bf16: 15.6 us for 22.4; 64 rows would take two rounds
+// of its tiles, 27 us, and take 22 in tiles of 128).
+inline bool ce_few(const CeArgs &a) { return a.n <= CE_FEW; }
 
 // A gathered row: its label, its place among all rows, and for the backward its lse in units of log
 // 2 and its gradient times scale.
@@ -404,16 +407,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_forward_kernel(CeArgs a) {
                                             [&](int i) { return z.row(lds, i).label; });
 }
 
-// Few rows (up to 64, of whole steps): every workgroup finds the ones with a label by itself and
+// Few rows (up to 32): every workgroup finds the ones with a label by itself and
 // reads them where they are, which saves the launch that gathers them; one workgroup a tile. The
 // vocabulary's bytes bound it: as many steps under way as LDS holds.
 template <int DT, int STAGES>
 __global__ void __launch_bounds__(GEMM_THREADS) ce_few_kernel(CeArgs a) {
-  constexpr int BM = CE_BM, BN = CE_SMALL_BN, WM = 4;
+  constexpr int BM = CE_BM, BN = CE_FEW, WM = 4;
   using G = TileGemm<DT, BM, BN, WM, SIDE_ROWS, SIDE_ROWS, STAGES>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   CeRow *row = (CeRow *)(lds + G::lds);  // of the rows that count
-  const int across = (int)blocks_of(a.vocab, BM), tv = blockIdx.x % across, tr = blockIdx.x / across;
   int m;
   {
     const int r = threadIdx.x & 63;  // in every wave, for m
@@ -436,18 +438,18 @@ __global__ void __launch_bounds__(GEMM_THREADS) ce_few_kernel(CeArgs a) {
       }
     }
   }
-  const int64_t v0 = (int64_t)tv * BM, r0 = (int64_t)tr * BN;
-  if (r0 >= m) return;
+  if (m == 0) return;
+  const int64_t v0 = (int64_t)blockIdx.x * BM;
   __syncthreads();
   G g;
   const int64_t vs = a.vocab - v0;
   g.a.start(a.w + v0 * a.row_bytes, a.row_bytes, vs < BM ? (int)vs : BM);
-  const int exist = m - (int)r0 < BN ? m - (int)r0 : BN;
-  g.b.start(a.h, a.row_bytes, exist, [&](int i) { return row[r0 + i].row; });
+  g.b.start(a.h, a.row_bytes, m, [&](int i) { return row[i].row; });
   g.clear();
-  g.begin(lds, a.row_bytes / 64, 64, 64);
-  g.finish(lds);
-  ce_tile_sums<G, BM, BN, WM>(a, g, v0, r0, m, (float2 *)lds, [&](int i) { return row[r0 + i].label; });
+  const int steps = (a.row_bytes + 63) / 64, last = a.row_bytes - (steps - 1) * 64;
+  g.begin(lds, steps, last, last);
+  g.template finish<true>(lds);
+  ce_tile_sums<G, BM, BN, WM>(a, g, v0, 0, m, (float2 *)lds, [&](int i) { return row[i].label; });
 }
 
 // lse and loss of a row from its tiles' parts: 8 rows a workgroup, 32 threads to each.
@@ -483,9 +485,8 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_join_kernel
 
 // P of one piece: [rows, whole tiles of them][cols], zeros past the rows and, in whole tiles, past
 // the vocabulary.
-template <int DT, int STAGES>
+template <int DT, int BM, int BN, int WM, int STAGES>
 __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_p_kernel(CeArgs a) {
-  constexpr int BM = CE_BM, BN = CE_BN, WM = 2;
   using Z = CeLogits<DT, BM, BN, WM, STAGES>;
   using G = typename Z::G;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
@@ -500,6 +501,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_p_kernel(CeArgs a) {
   const float up = ce_up<DT>(a), f = a.scale * LOG2E;
   // a block of 32 x 32 leaves through LDS: a panel of 32 rows, which is one piece of memory
   constexpr int eb = Elem<DT>::bytes, part = BM / WM;
+  static_assert(4 * 32 * 32 * eb <= G::stage, "within the place that is free");
   char *mine = lds + Z::scratch + wave * (32 * 32 * eb);
   const int64_t panel = pieces.rows * PANEL;
   Z z;

@@ -94,6 +94,15 @@ template <int DT, int R, int KIND> struct GemmSide {
     return partial ? (wave * 64 < R * 4 ? 1 : 0) : pieces;
   }
 
+  // Zeros for what lies past `left` bytes of every row of a step that is in LDS (ROWS).
+  __device__ __forceinline__ static void clear_past(char *tile, int left) {
+#pragma unroll
+    for (int i = 0; i < pieces; i++) {
+      const int p = threadIdx.x + i * GEMM_THREADS;
+      if (p < R * 4 && (int)place(i).byte >= left) *(u32x4_t *)(tile + p * 16) = u32x4_t{0, 0, 0, 0};
+    }
+  }
+
   // This lane's place in a block of 32 rows or columns, and the operand of step t (of two) of block
   // `b`: k = 16 t + 8 h + 0 .. 7 (fp32: 8 t + 4 h + 0 .. 3) in lanes of half h.
   __device__ __forceinline__ static int lane_offset() {
@@ -152,7 +161,7 @@ template <int DT, int BM, int BN, int WM, int AKIND, int BKIND, int STAGES> stru
     asm volatile("" ::: "memory");
     switch (n) {
 #define MAXSIM_WAIT(N) case N: __builtin_amdgcn_s_waitcnt(0x0070 | ((N) & 15) | ((N) >> 4) << 14); break;
-    MAXSIM_WAIT(6) MAXSIM_WAIT(20) MAXSIM_WAIT(30)
+    MAXSIM_WAIT(6) MAXSIM_WAIT(8) MAXSIM_WAIT(20) MAXSIM_WAIT(30)
 #undef MAXSIM_WAIT
     default: __builtin_amdgcn_s_waitcnt(0x0070); break;
     }
@@ -193,7 +202,8 @@ template <int DT, int BM, int BN, int WM, int AKIND, int BKIND, int STAGES> stru
 
   // ---- all steps of a tile (at least one): begin, then finish ----
   // What exists of the last step along k: a_last and b_last bytes (ROWS; 64 for all) or k rows (COLS;
-  // BK for all). The last bytes or rows are repeated, so one side has to hold zeros there.
+  // BK for all). The last bytes or rows are repeated, so one side has to hold zeros there, or B is
+  // cleared there (finish).
   int steps, fetched, a_last, b_last, to;
 
   __device__ __forceinline__ void fetch(int ring_at, int wave) {
@@ -217,8 +227,8 @@ template <int DT, int BM, int BN, int WM, int AKIND, int BKIND, int STAGES> stru
     for (int i = 0; i < STAGES - 1; i++)
       if (fetched < steps) fetch(ring_at, wave);
   }
-  // The ring is free again afterwards.
-  __device__ __forceinline__ void finish(char *ring) {
+  // The ring is free again afterwards. CLEAR: with zeros for what B has not got of the last step.
+  template <bool CLEAR = false> __device__ __forceinline__ void finish(char *ring) {
     const int wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
     const int la = A::lane_offset(), lb = B::lane_offset();
     const int ring_at = lds_address(ring);
@@ -228,6 +238,10 @@ template <int DT, int BM, int BN, int WM, int AKIND, int BKIND, int STAGES> stru
       const int ahead = fetched - i - 1;
       wait(ahead >= STAGES - 2 ? (STAGES - 2) * loads : 0);
       if (fetched < steps) fetch(ring_at, wave);
+      if (CLEAR && i == steps - 1 && b_last < 64) {
+        B::clear_past(ring + from + A::bytes, b_last);
+        __syncthreads();
+      }
       multiply(ring + from, la, lb, wm, wn);
       from = from == (STAGES - 1) * stage ? 0 : from + stage;
     }

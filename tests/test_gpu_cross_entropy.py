@@ -40,6 +40,10 @@ def check(h, w, y, scale=1.0, dl=None, backward=True):
     (1, 300, 64, BF16, 1.0),
     (7, 1000, 40, FP16, 1.0),      # a last step along d that is not whole
     (33, 257, 72, BF16, 1.0),      # one entry past a tile, one row past a small tile
+    (32, 700, 104, FP16, 0.8),     # as many rows as the smallest tile has
+    (31, 129, 52, FP32, 1.0),
+    (128, 300, 200, FP32, 0.9),    # as many as the next one
+    (128, 1000, 96, FP16, 1.0),
     (64, 777, 256, FP32, 1.0),
     (65, 500, 320, BF16, 1.0),     # the first size of the large tiles
     (129, 255, 24, FP16, 0.5),
@@ -55,7 +59,7 @@ def test_against_reference(n, vocab, d, dtype, share):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
-@pytest.mark.parametrize("n", [40, 300])
+@pytest.mark.parametrize("n", [20, 40, 300])
 def test_rows_left_out_hide_what_they_hold(n, dtype):
     """NaN and infinities in rows without a label change nothing; labels of all sizes that are none."""
     h, w, y = make(n, 400, 96, dtype, 0.6, seed=3)
