@@ -8,11 +8,11 @@ namespace {
 
 constexpr int MX4_LDS_QUERY = 64 * 1024;  // most bytes of a query's codes held in LDS
 
-template <int KS, int QB, bool QLDS> int mx4_launch(Mx4Args &a, const DeviceInfo &di, hipStream_t st) {
+template <int KS, int QB, bool QLDS, int SUB = 1> int mx4_launch(Mx4Args &a, const DeviceInfo &di, hipStream_t st) {
   // about 8 KiB of codes in flight a wave; at wide rows two tiles
   constexpr int P = KS >= 4 ? 2 : 8 / KS;
   const size_t lds = QLDS ? (size_t)QB * KS * WAVE * 17 : 0;
-  auto kernel = mx4_score_kernel<KS, QB, P, QLDS>;
+  auto kernel = mx4_score_kernel<KS, QB, P, QLDS, SUB>;
   int bpc = blocks_per_cu((const void *)kernel, DENSE_THREADS, lds);
   // Packed documents go to waves in whole ones: with fewer waves the longest share is nearer the mean,
   // and 12 waves a CU have bytes enough under way (20000 documents of 20 to 300 tokens, d = 96: 43.2
@@ -29,8 +29,14 @@ template <int KS, int QB, bool QLDS> int mx4_launch(Mx4Args &a, const DeviceInfo
 
 // Up to 64 query tokens stay in registers; more come from LDS, all blocks for every tile, so that
 // the documents are still read once.
+template <int SUB> int mx4_narrow(int qb, Mx4Args &a, const DeviceInfo &di, hipStream_t st) {
+  if (qb <= 1) return mx4_launch<1, 1, false, SUB>(a, di, st);
+  if (qb <= 2) return mx4_launch<1, 2, false, SUB>(a, di, st);
+  return mx4_launch<1, 4, false, SUB>(a, di, st);
+}
 template <int KS> int mx4_pick(Mx4Args &a, const DeviceInfo &di, hipStream_t st) {
   const int qb = (a.q_len + 15) / 16;
+  if (KS == 1 && qb <= 4 && a.blocks <= 2) return a.blocks == 1 ? mx4_narrow<4>(qb, a, di, st) : mx4_narrow<2>(qb, a, di, st);
   if (qb <= 1) return mx4_launch<KS, 1, false>(a, di, st);
   if (qb <= 2) return mx4_launch<KS, 2, false>(a, di, st);
   if (qb <= 4) return mx4_launch<KS, 4, false>(a, di, st);

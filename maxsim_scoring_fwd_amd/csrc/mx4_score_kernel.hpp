@@ -1,6 +1,6 @@
 // MaxSim scores of 4-bit microscaled vectors (include/maxsim.h, maxsim_score_mx4).
 //
-// One wave takes a document at a time, 16 tokens a tile, as in the dense kernel: persistent waves
+// One wave takes a document at a time, 16 tokens a tile (32 or 64 of rows of 64 or 32 entries), as in the dense kernel: persistent waves
 // with contiguous, token-balanced document ranges, a ring of P tiles in flight, rows past a
 // document's end clamped to its last token (a duplicate does not change a maximum), the running
 // maxima in one register per 16 query tokens. The products run on the scaled matrix instruction
@@ -67,8 +67,10 @@ __device__ __forceinline__ void nearest_boundaries(const int64_t *off, int64_t n
 }
 
 // KS: steps of 128 entries in a row; QB: blocks of 16 query tokens; P: tiles in flight; QLDS: the
-// query's operands come from LDS, else they stay in registers.
-template <int KS, int QB, int P, bool QLDS>
+// query's operands come from LDS, else they stay in registers. SUB: rows of 128 / SUB entries, of which
+// an operand holds SUB sixteens side by side, and the query stands in its own part of SUB operands
+// beside zeros: as many products, but whole loads.
+template <int KS, int QB, int P, bool QLDS, int SUB>
 __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & (WAVE - 1);
@@ -77,27 +79,32 @@ __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
   const int64_t nwaves = (int64_t)gridDim.x * DENSE_WAVES;
   const int64_t RB = (int64_t)a.blocks * 16;  // bytes of a row's codes
   const int q_len = a.q_len;
+  static_assert(SUB == 1 || (KS == 1 && !QLDS), "narrow rows, short queries");
 
-  // this lane's block of every step, or block 0 where the row has none there
+  // this lane's block of every step, or block 0 where the row has none there; and which of the
+  // tile's rows it holds
+  constexpr int ROWS = 16 * SUB;
+  const int part = SUB == 1 ? 0 : g * SUB / 4, tile_row = part * 16 + r16;
   uint32_t blk[KS];
   bool has[KS];
 #pragma unroll
   for (int c = 0; c < KS; c++) {
-    has[c] = c * 4 + g < a.blocks;
-    blk[c] = has[c] ? c * 4 + g : 0;
+    const int at = c * 4 + (SUB == 1 ? g : g % (4 / SUB));
+    has[c] = at < a.blocks;
+    blk[c] = has[c] ? at : 0;
   }
-  auto query = [&](int qb, int c, uint32_t &s) {
+  auto query = [&](int qb, int c, int sub, uint32_t &s) {
     const int qi = qb * 16 + r16;
     u32x4_t v = {0u, 0u, 0u, 0u};
     s = 0;
-    if (qi < q_len && has[c]) {
+    if (qi < q_len && has[c] && sub == part) {
       v = load16(a.Q + (int64_t)qi * RB + blk[c] * 16);
       s = a.q_scale[(int64_t)qi * a.blocks + blk[c]];
     }
     return v;
   };
-  u32x4_t qreg[QLDS ? 1 : QB][QLDS ? 1 : KS];
-  uint32_t qs[QLDS ? 1 : QB][QLDS ? 1 : KS];
+  u32x4_t qreg[QLDS ? 1 : QB][QLDS ? 1 : KS * SUB];
+  uint32_t qs[QLDS ? 1 : QB][QLDS ? 1 : KS * SUB];
   // operands of block qb, step c in LDS: 64 lanes x 16 bytes, then, after all of those, exponents
   constexpr int OPERAND = WAVE * 16;
   if constexpr (QLDS) {
@@ -118,7 +125,9 @@ __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
 #pragma unroll
     for (int qb = 0; qb < QB; qb++)
 #pragma unroll
-      for (int c = 0; c < KS; c++) qreg[qb][c] = query(qb, c, qs[qb][c]);
+      for (int c = 0; c < KS; c++)
+#pragma unroll
+        for (int sub = 0; sub < SUB; sub++) qreg[qb][c * SUB + sub] = query(qb, c, sub, qs[qb][c * SUB + sub]);
   }
 
   // ---- producer: the (document, tile) sequence of this wave ----
@@ -158,12 +167,12 @@ __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
       if (plen <= 0) {
         sl.doc_end = sl.empty = true;
       } else {
-        const int64_t t0 = ptile * 16, rem = plen - 1 - t0;
-        last = rem < 15 ? (int)rem : 15;
+        const int64_t t0 = ptile * ROWS, rem = plen - 1 - t0;
+        last = rem < ROWS - 1 ? (int)rem : ROWS - 1;
         base = a.doc.D + (pfirst + t0) * RB;
         sbase = a.d_scale + (pfirst + t0) * a.blocks;
         sl.empty = false;
-        sl.doc_end = rem < 16;
+        sl.doc_end = rem < ROWS;
         advance = sl.doc_end;
         ptile++;
       }
@@ -173,7 +182,7 @@ __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
         if (pb < pend) doc_extent(a.doc, pb, pfirst, plen);
       }
     }
-    const uint32_t row = r16 < last ? r16 : last;
+    const uint32_t row = tile_row < last ? tile_row : last;
 #pragma unroll
     for (int c = 0; c < KS; c++) {
       const uint32_t at = row * a.blocks + blk[c];
@@ -193,7 +202,8 @@ __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
     for (int p = 0; p < P; p++) {
       if (!slot[p].valid) goto done;
 #pragma unroll
-      for (int qb = 0; qb < QB; qb++) {
+      for (int qs_at = 0; qs_at < QB * SUB; qs_at++) {
+        const int qb = qs_at / SUB, sub = qs_at % SUB;
         f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < KS; c++) {
@@ -203,7 +213,7 @@ __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
             const uint32_t s = (uint8_t)lds[QB * KS * OPERAND + i * WAVE + lane];
             acc = mfma_mx4(buf[p][c], sc[p][c], v, s, acc);
           } else {
-            acc = mfma_mx4(buf[p][c], sc[p][c], qreg[qb][c], qs[qb][c], acc);
+            acc = mfma_mx4(buf[p][c], sc[p][c], qreg[qb][c * SUB + sub], qs[qb][c * SUB + sub], acc);
           }
         }
         m[qb] = __builtin_fmaxf(__builtin_fmaxf(m[qb], acc[0]), acc[1]);
