@@ -69,7 +69,8 @@ __device__ __forceinline__ void nearest_boundaries(const int64_t *off, int64_t n
 // KS: steps of 128 entries in a row; QB: blocks of 16 query tokens; P: tiles in flight; QLDS: the
 // query's operands come from LDS, else they stay in registers. SUB: rows of 128 / SUB entries, of which
 // an operand holds SUB sixteens side by side, and the query stands in its own part of SUB operands
-// beside zeros: as many products, but whole loads.
+// beside zeros: as many products, but whole loads (documents of 128 tokens, 60000 with d = 64: 72 us
+// with SUB = 1, 56 with 2; 100000 with d = 32: 80 with 1, 45 with 4).
 template <int KS, int QB, int P, bool QLDS, int SUB>
 __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -202,8 +203,8 @@ __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
     for (int p = 0; p < P; p++) {
       if (!slot[p].valid) goto done;
 #pragma unroll
-      for (int qs_at = 0; qs_at < QB * SUB; qs_at++) {
-        const int qb = qs_at / SUB, sub = qs_at % SUB;
+      for (int block = 0; block < QB * SUB; block++) {
+        const int qb = block / SUB, sub = block % SUB;
         f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < KS; c++) {
