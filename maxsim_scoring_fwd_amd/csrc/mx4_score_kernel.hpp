@@ -202,6 +202,12 @@ __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
 #pragma unroll
     for (int p = 0; p < P; p++) {
       if (!slot[p].valid) goto done;
+      // The operands are read anew for every tile: kept in registers, as the compiler would, they leave
+      // room for one wave a SIMD (5000 documents of 180 tokens, d = 128: 300 query tokens 117 us so,
+      // 46 read anew; 500 tokens, d = 256: 121 and 72). 64 blocks do not fit there anyway, and the
+      // compiler's own choice is better (1024 tokens: 83 us, 133 read anew).
+      int at = lane;
+      if constexpr (QLDS && QB < 64) asm volatile("" : "+v"(at));
 #pragma unroll
       for (int block = 0; block < QB * SUB; block++) {
         const int qb = block / SUB, sub = block % SUB;
@@ -210,8 +216,8 @@ __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
         for (int c = 0; c < KS; c++) {
           if constexpr (QLDS) {
             const int i = qb * KS + c;
-            const u32x4_t v = *(const u32x4_t *)(lds + i * OPERAND + lane * 16);
-            const uint32_t s = (uint8_t)lds[QB * KS * OPERAND + i * WAVE + lane];
+            const u32x4_t v = *(const u32x4_t *)(lds + i * OPERAND + at * 16);
+            const uint32_t s = (uint8_t)lds[QB * KS * OPERAND + i * WAVE + at];
             acc = mfma_mx4(buf[p][c], sc[p][c], v, s, acc);
           } else {
             acc = mfma_mx4(buf[p][c], sc[p][c], qreg[qb][c * SUB + sub], qs[qb][c * SUB + sub], acc);
