@@ -63,10 +63,9 @@ template <int DT> int ce_backward(CeArgs &a, int64_t pieces, int cus, hipStream_
              ? ce_launch(ce_p_kernel<DT, CE_BM, CE_HALF_BN, 2, CE_HALF_STAGES>, any, H::lds, cus, a, st)
              : ce_launch(ce_p_kernel<DT, CE_BM, CE_BN, 2, CE_STAGES>, any, Z::lds, cus, a, st);
     if (rc == MAXSIM_OK) rc = ce_launch(ce_products_kernel<DT, CE_STAGES>, any, G::lds, cus, a, st);
-    if (rc == MAXSIM_OK && a.dw && a.w_slots) rc = ce_launch(ce_parts_kernel<DT, true>, any, 0, cus, a, st);
     if (rc != MAXSIM_OK) return rc;
   }
-  return a.dh ? ce_launch(ce_parts_kernel<DT, false>, any, 0, cus, a, st) : MAXSIM_OK;
+  return a.dh || a.w_slots ? ce_launch(ce_parts_kernel<DT>, any, 0, cus, a, st) : MAXSIM_OK;
 }
 
 }  // namespace maxsim

@@ -8,8 +8,8 @@
 //             grad * scale, rounded to the storage type, into a workspace that holds one piece, then
 //             dw = P^T h of the piece and dh += P w over it.
 // Sums are 32 bits wide, every one has one owner and a fixed order. P is rounded because the matrix
-// cores take 16-bit operands; in fp16, whose range is short, it is scaled by a power of two first,
-// taken from the largest gradient of a row.
+// cores take 16-bit operands, after a scaling (ce_up) that fits fp16's short range and leaves a mean's
+// gradients exact.
 // The matrix cores bound the training step and the bytes of w the few rows of a query. Measured (one
 // MI355X): 8192 rows, 30522 entries, d = 768 in bf16: gathering 11 us (twice), logits and their
 // sums 374 to 390 (1.03 to 0.99 PFLOP/s; a library product of the shape takes 410 and writes the
@@ -122,18 +122,28 @@ struct CeUnits {
   }
 };
 
-// fp16: the power of two that P is scaled by.
+// What P is multiplied by before it is rounded. Its entries at the labels are the gradients (times p -
+// 1, which is -1 but for well known labels), and those of a mean are all alike: divided by the
+// mantissa of one of them they are powers of two, and rounding does not move them all by the same
+// amount. fp16: that of the largest, which becomes 2^14; bf16: that of the first row.
 template <int DT> __device__ __forceinline__ float ce_up(const CeArgs &a) {
-  if constexpr (DT != DT_FP16) return 1.0f;
+  if constexpr (DT == DT_FP32) return 1.0f;
   float most = 0.0f;
-  const int64_t blocks = blocks_of(a.n, CE_COUNT);
-  for (int64_t i = threadIdx.x & 63; i < blocks; i += 64) most = __builtin_fmaxf(most, a.most[i]);
-  for (int o = 32; o > 0; o >>= 1) most = __builtin_fmaxf(most, __shfl_xor(most, o, 64));
-  most *= a.scale;
-  if (!(most > 0.0f && most < __builtin_inff())) return 1.0f;
-  int e = 14 - (int)((__float_as_uint(most) >> 23) & 255) + 127;
+  if constexpr (DT == DT_BF16) {
+    most = __builtin_bit_cast(CeRow, a.info[0]).grad;
+  } else {
+    const int64_t blocks = blocks_of(a.n, CE_COUNT);
+    for (int64_t i = threadIdx.x & 63; i < blocks; i += 64) most = __builtin_fmaxf(most, a.most[i]);
+    for (int o = 32; o > 0; o >>= 1) most = __builtin_fmaxf(most, __shfl_xor(most, o, 64));
+    most *= a.scale;
+  }
+  const uint32_t bits = __float_as_uint(most), exponent = (bits >> 23) & 255;
+  if (exponent == 0 || exponent == 255) return 1.0f;  // zero, or not a number
+  const float up = __builtin_amdgcn_rcpf(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
+  if constexpr (DT == DT_BF16) return up;
+  int e = 14 - (int)exponent + 127;
   e = e > 120 ? 120 : (e < -120 ? -120 : e);
-  return __uint_as_float((uint32_t)(e + 127) << 23);
+  return up * __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
 __device__ __forceinline__ bool ce_counts(const CeArgs &a, int64_t label) { return label >= 0 && label < a.vocab; }
@@ -483,8 +493,64 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_join_kernel
   }
 }
 
+// dh, or a piece's dw, from its parts, rounded once, to the rows' own places, by the whole launch. The
+// parts' bytes bound it; where there are few tiles of many parts, their loads' waits do: 8 under way
+// (130 rows, 100000 x 128, 256 parts: the backward 158 us with one block a workgroup and a part at
+// a time, 88 so).
+template <int DT, bool DW>
+__device__ __forceinline__ void ce_join_parts(const CeArgs &a, int m, const CePieces &pieces, int64_t piece) {
+  constexpr int BM = CE_PM, BN = CE_PN, WM = 2;
+  using G = TileGemm<DT, BM, BN, WM, SIDE_COLS, SIDE_ROWS_P, 3>;
+  using T = typename AttnElem<DT>::type;
+  typedef T v4 __attribute__((ext_vector_type(4)));
+  const CeUnits units(a, m, pieces, Elem<DT>::bytes);
+  const int64_t piece0 = piece * pieces.cols;
+  if (DW && units.w_splits == 1) return;
+  const int64_t rows = DW ? (a.vocab - piece0 < pieces.cols ? a.vocab - piece0 : pieces.cols) : m;
+  const uint32_t across = DW ? units.w_across : units.h_across, splits = DW ? units.w_splits : units.h_splits;
+  const uint32_t down = (uint32_t)blocks_of(rows, BN), tiles = across * down;
+  const float back = 1.0f / ce_up<DT>(a);
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
+  // A quarter of a block of 32 x 32 of a tile for each wave and round, so that few tiles of many parts
+  // spread over the chip; the quarters of a block on one XCD, whose L2 joins what they write.
+  const uint32_t total = tiles * G::TN * G::TM * 4;
+  static_assert(G::TN * G::TM % 8 == 0, "whole rounds of the XCDs");
+  const int64_t part = (int64_t)tiles * (BM * BN / 4);
+  for (uint32_t i = blockIdx.x; i < total; i += gridDim.x) {
+    const uint32_t block = i / 32 * 8 + i % 8, q = i / 8 % 4;
+    const uint32_t tile = block / (G::TN * G::TM), nk = block - tile * (G::TN * G::TM);
+    const int n = nk / G::TM, k = nk - n * G::TM;
+    uint32_t tc, tr;
+    ce_tile(tile, across, down, tc, tr);
+    const int64_t r = (int64_t)tr * BN + (wn * G::TN + n) * 32 + (lane & 31);
+    const int c = (int)tc * BM + (wm * G::TM + k) * 32 + 4 * (lane >> 5) + 8 * q;
+    const f32x4_t *p = (const f32x4_t *)(DW ? a.dwp : a.dhp) + (int64_t)tile * (BM * BN / 4) +
+                       (nk * 4 + q) * GEMM_THREADS + threadIdx.x;
+    constexpr int AHEAD = 8;
+    f32x4_t x = {};
+    uint32_t s = 0;
+    for (; s + AHEAD <= splits; s += AHEAD) {
+      f32x4_t y[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; j++) y[j] = p[(s + j) * part];
+#pragma unroll
+      for (int j = 0; j < AHEAD; j++) x += y[j];
+    }
+    for (; s < splits; s++) x += p[s * part];
+    if (r >= rows || c >= a.d) continue;  // d is a multiple of 4 entries
+    T *to = (T *)(DW ? a.dw + (piece0 + r) * a.row_bytes
+                     : a.dh + (int64_t)__builtin_bit_cast(CeRow, a.info[r]).row * a.row_bytes);
+    v4 o;
+#pragma unroll
+    for (int e = 0; e < 4; e++) o[e] = (T)(x[e] * back);
+    *(v4 *)(to + c) = o;
+  }
+}
+
 // P of one piece: [rows, whole tiles of them][cols], zeros past the rows and, in whole tiles, past
 // the vocabulary.
+// Where dw goes in parts, those of the piece before are joined first: a launch for it would also cost
+// the pieces that are not there (3001 of 20011 rows count: 18 us of 746).
 template <int DT, int BM, int BN, int WM, int STAGES>
 __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_p_kernel(CeArgs a) {
   using Z = CeLogits<DT, BM, BN, WM, STAGES>;
@@ -494,6 +560,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_p_kernel(CeArgs a) {
   const int m = uniform(*a.counted);
   const CePieces pieces(m, a.vocab, a.p_elements);
   if (a.piece >= pieces.n) return;
+  if (a.piece > 0 && a.dw && a.w_slots) ce_join_parts<DT, true>(a, m, pieces, a.piece - 1);
   const int64_t piece0 = a.piece * pieces.cols;
   const int64_t cols = a.vocab - piece0 < pieces.cols ? a.vocab - piece0 : pieces.cols;
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
@@ -652,58 +719,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_products_kernel(CeArgs a) 
   }
 }
 
-// dh (or, of one piece, dw) from its parts, rounded once, to the rows' own places. The parts' bytes bound it; where there are few
-// tiles of many parts, their loads' waits do: 8 under way (130 rows, 100000 x 128, 256 parts: the
-// backward 158 us with one block a workgroup and a part at a time, 88 so).
-template <int DT, bool DW> __global__ void __launch_bounds__(GEMM_THREADS) ce_parts_kernel(CeArgs a) {
-  constexpr int BM = CE_PM, BN = CE_PN, WM = 2;
-  using G = TileGemm<DT, BM, BN, WM, SIDE_COLS, SIDE_ROWS_P, 3>;
-  using T = typename AttnElem<DT>::type;
-  typedef T v4 __attribute__((ext_vector_type(4)));
+// dh, and the last piece's dw, from their parts.
+template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_parts_kernel(CeArgs a) {
   const int m = uniform(*a.counted);
   const CePieces pieces(m, a.vocab, a.p_elements);
-  const CeUnits units(a, m, pieces, Elem<DT>::bytes);
-  const int64_t piece0 = a.piece * pieces.cols;
-  if (DW && (a.piece >= pieces.n || units.w_splits == 1)) return;
-  const int64_t rows = DW ? (a.vocab - piece0 < pieces.cols ? a.vocab - piece0 : pieces.cols) : m;
-  const uint32_t across = DW ? units.w_across : units.h_across, splits = DW ? units.w_splits : units.h_splits;
-  const uint32_t down = (uint32_t)blocks_of(rows, BN), tiles = across * down;
-  const float back = 1.0f / ce_up<DT>(a);
-  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
-  // A quarter of a block of 32 x 32 of a tile for each wave and round, so that few tiles of many parts
-  // spread over the chip; the quarters of a block on one XCD, whose L2 joins what they write.
-  const uint32_t total = tiles * G::TN * G::TM * 4;
-  static_assert(G::TN * G::TM % 8 == 0, "whole rounds of the XCDs");
-  const int64_t part = (int64_t)tiles * (BM * BN / 4);
-  for (uint32_t i = blockIdx.x; i < total; i += gridDim.x) {
-    const uint32_t block = i / 32 * 8 + i % 8, q = i / 8 % 4;
-    const uint32_t tile = block / (G::TN * G::TM), nk = block - tile * (G::TN * G::TM);
-    const int n = nk / G::TM, k = nk - n * G::TM;
-    uint32_t tc, tr;
-    ce_tile(tile, across, down, tc, tr);
-    const int64_t r = (int64_t)tr * BN + (wn * G::TN + n) * 32 + (lane & 31);
-    const int c = (int)tc * BM + (wm * G::TM + k) * 32 + 4 * (lane >> 5) + 8 * q;
-    const f32x4_t *p = (const f32x4_t *)(DW ? a.dwp : a.dhp) + (int64_t)tile * (BM * BN / 4) +
-                       (nk * 4 + q) * GEMM_THREADS + threadIdx.x;
-    constexpr int AHEAD = 8;
-    f32x4_t x = {};
-    uint32_t s = 0;
-    for (; s + AHEAD <= splits; s += AHEAD) {
-      f32x4_t y[AHEAD];
-#pragma unroll
-      for (int j = 0; j < AHEAD; j++) y[j] = p[(s + j) * part];
-#pragma unroll
-      for (int j = 0; j < AHEAD; j++) x += y[j];
-    }
-    for (; s < splits; s++) x += p[s * part];
-    if (r >= rows || c >= a.d) continue;  // d is a multiple of 4 entries
-    T *to = (T *)(DW ? a.dw + (piece0 + r) * a.row_bytes
-                     : a.dh + (int64_t)__builtin_bit_cast(CeRow, a.info[r]).row * a.row_bytes);
-    v4 o;
-#pragma unroll
-    for (int e = 0; e < 4; e++) o[e] = (T)(x[e] * back);
-    *(v4 *)(to + c) = o;
-  }
+  if (a.dw && a.w_slots) ce_join_parts<DT, true>(a, m, pieces, pieces.n - 1);
+  if (a.dh) ce_join_parts<DT, false>(a, m, pieces, 0);
 }
 
 int ce_forward_bf16(const CeArgs &a, int cus, hipStream_t st);

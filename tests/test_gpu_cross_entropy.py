@@ -229,6 +229,20 @@ def test_many_rows_of_a_small_vocabulary(n, vocab, d, dtype, share):
         assert (ws[size:] == 0xFF).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=str)
+@pytest.mark.parametrize("n", [300, 1009])
+def test_a_means_gradients_keep_their_size(n, dtype):
+    """1 / n is no number of 16 bits, and its rounding would move all gradients by up to half a step:
+    what they are along the exact ones is within 2^-13. (P at a label is p - 1, rounded to -1: p is some
+    2^-14. All other roundings point anywhere, and average over 19200 entries and more.)"""
+    h, w, y = make(n, 20000, 64, dtype, seed=n, std=0.25)
+    dl = torch.full((n,), 1.0 / n, device="cuda")
+    loss, lse = ms.maxsim_linear_cross_entropy(h, w, y)
+    dh = ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, lse)[0]
+    want = ref.loss(as64(h), as64(w), y.cpu().numpy(), 1.0, as64(dl), dtype)["dh"]
+    assert abs((as64(dh) * want).sum() / (want * want).sum() - 1) <= 2.0 ** -13
+
+
 def test_few_tiles_in_several_pieces():
     n, vocab, d = 70001, 4200, 64
     h, w, y = make(n, vocab, d, BF16, seed=8)
