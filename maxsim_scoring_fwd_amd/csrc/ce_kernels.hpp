@@ -13,9 +13,9 @@
 // The matrix cores bound the training step and the bytes of w the few rows of a query. Measured (one
 // MI355X): 8192 rows, 30522 entries, d = 768 in bf16: gathering 11 us (twice), logits and their
 // sums 374 to 390 (1.03 to 0.99 PFLOP/s; a library product of the shape takes 410 and writes the
-// logits), join 8.5, P 397 to 412, both products 656 to 663 (1.17; the library 419 + 573), dh's join
-// 23; the clock falls to 1.6 to 1.8 GHz meanwhile, and the matrix cores are busy half of the cycles
-// (54, 51 and 64 in 100). 32 rows: 11.8 us and 4.2 for the join, of which 9.3 are w's 47 MB.
+// logits), join 8.5, P 389 to 412, both products 656 to 675 (1.15; the library 419 + 573), dh's join
+// 19; the clock falls to 1.6 to 1.8 GHz meanwhile, and the matrix cores are busy half of the cycles
+// (54, 51 and 65 in 100). 32 rows: 12 us and 4.4 for the join, of which 9.3 are w's 47 MB.
 #pragma once
 
 #include "tile_gemm.hpp"
