@@ -479,8 +479,8 @@ size_t maxsim_linear_cross_entropy_workspace_size(int64_t n_rows, int64_t vocab,
  *     P = (exp(z - lse) - [v is the label]) * grad_loss * scale,   dh = P w,   dw = P^T h
  * with P, one piece of it, in the workspace, rounded to `dtype` (16-bit types: after a scaling that
  * makes a mean's gradients powers of two, in fp16 from the largest of them). Sums are fp32, each result is rounded once. A piece of P
- * takes 512 MiB at most, or 128 columns; dh's sums take 4 bytes an entry and at least 128 MiB, a
- * small vocabulary's dw 128 MiB. With n_rows == 0 dw is set to zero.
+ * takes 512 MiB at most, or 128 columns; dh's sums take 4 bytes an entry or up to 128 MiB, and those
+ * of dw with many rows and a small vocabulary 128 MiB. With n_rows == 0 dw is set to zero.
  */
 int maxsim_linear_cross_entropy_backward(const float *grad_loss, const void *h, const void *w,
                                          const int64_t *labels, const float *lse, int64_t n_rows,

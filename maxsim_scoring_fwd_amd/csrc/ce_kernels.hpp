@@ -99,6 +99,7 @@ struct CePieces {
 // 32768 rows, 30522 x 256 in bf16 3135 and 2130 us; 16384 rows, 10000 x 384 in fp16 555 and 547, in
 // shares 588; 8192 rows, 500 x 512 164 and 66).
 constexpr int CE_LANES = 512;  // workgroups at once: two on each of 256 CUs
+constexpr int CE_H_LEAST = 8, CE_W_LEAST = 16;  // steps of a part
 struct CeUnits {
   uint32_t w_across, w_down, h_across, h_down;
   uint32_t w_splits, h_splits;  // parts along the rows, along the piece
@@ -117,8 +118,8 @@ struct CeUnits {
       while (n * all < steps * CE_LANES * fine && 2 * n * tiles <= slots && 2 * least * n <= steps) n *= 2;
       return n;
     };
-    w_splits = parts(w, w_steps, a.w_slots, 16, 2);
-    h_splits = parts(h, h_steps, a.slots, 8, eb == 4 ? 2 : 1);
+    w_splits = parts(w, w_steps, a.w_slots, CE_W_LEAST, 2);
+    h_splits = parts(h, h_steps, a.slots, CE_H_LEAST, eb == 4 ? 2 : 1);
   }
 };
 

@@ -57,11 +57,13 @@ size_t ce_carve(CeArgs &a, int eb, bool backward, char *base) {
   a.p_elements = p;
   a.p = c.take<char>(p * eb);
   a.queue = c.take<int32_t>(8);
-  a.slots = blocks_of(a.d, CE_PM) * blocks_of(a.n, CE_PN);
-  if (a.slots < CE_SLOTS) a.slots = CE_SLOTS;
+  const int64_t cols = CePieces(a.n, a.vocab, p).cols;
+  const int64_t h = blocks_of(a.d, CE_PM) * blocks_of(a.n, CE_PN), w = blocks_of(a.d, CE_PM) * blocks_of(cols, CE_PN);
+  // no more than tiles and parts can be: fewer rows have fewer tiles of as many parts
+  const int64_t h_most = h * (cols * eb / 64 / CE_H_LEAST + 1), room = h_most < CE_SLOTS ? h_most : CE_SLOTS;
+  a.slots = h > room ? h : room;
   a.dhp = c.take<float>(a.slots * CE_PM * CE_PN);
-  const int64_t w = blocks_of(a.d, CE_PM) * blocks_of(CePieces(a.n, a.vocab, p).cols, CE_PN);
-  a.w_slots = w < CE_LANES ? CE_SLOTS : 0;
+  a.w_slots = w < CE_LANES && blocks_of(a.n * eb, 64) >= 2 * CE_W_LEAST ? CE_SLOTS : 0;
   a.dwp = c.take<float>(a.w_slots * CE_PM * CE_PN);
   return c.at;
 }
