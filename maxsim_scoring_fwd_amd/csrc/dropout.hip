@@ -60,9 +60,10 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const T *x, T *y,
 template <typename T>
 int dropout_run(const void *x, int64_t n, const DropArgs &drop, void *out, hipStream_t st) {
   constexpr int64_t per = DROP_THREADS * DROP_PER * 8;
-  const bool once = 2 * n * (int64_t)sizeof(T) > CACHE_BYTES;
-  auto kernel = drop.rng ? (once ? dropout_kernel<T, true, true> : dropout_kernel<T, true, false>)
-                         : (once ? dropout_kernel<T, false, true> : dropout_kernel<T, false, false>);
+  auto kernel = drop.rng ? dropout_kernel<T, true, false> : dropout_kernel<T, false, false>;
+  if constexpr (sizeof(T) == 2)
+    if (past_caches(2 * n * (int64_t)sizeof(T), sizeof(T)))
+      kernel = drop.rng ? dropout_kernel<T, true, true> : dropout_kernel<T, false, true>;
   for (int64_t first = 0; first < n; first += (int64_t)LAUNCH_MOST * per) {
     const int64_t left = (n - first + per - 1) / per;
     const unsigned grid = (unsigned)(left < (int64_t)LAUNCH_MOST ? left : LAUNCH_MOST);

@@ -113,12 +113,14 @@ template <typename Launch> int mx4_parts(int64_t n, Launch launch) {
   return MAXSIM_OK;
 }
 
-// Bytes that n chunks take in both forms.
-template <typename T> bool mx4_once(int64_t n) { return n * (int64_t)(8 * sizeof(T) + 4) > CACHE_BYTES; }
+// Whether n chunks in both forms pass the caches by.
+template <typename T> bool mx4_once(int64_t n) { return past_caches(n * (int64_t)(8 * sizeof(T) + 4), sizeof(T)); }
 
 template <typename T>
 int mx4_quantize_run(const T *x, uint8_t *codes, uint8_t *scales, int64_t n, hipStream_t st) {
-  auto kernel = mx4_once<T>(n) ? mx4_quantize_kernel<T, true> : mx4_quantize_kernel<T, false>;
+  auto kernel = mx4_quantize_kernel<T, false>;
+  if constexpr (sizeof(T) == 2)
+    if (mx4_once<T>(n)) kernel = mx4_quantize_kernel<T, true>;
   return mx4_parts(n, [&](unsigned grid, int64_t first) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(MX4_THREADS), 0, st, x, (uint32_t *)codes, scales, n, first);
   });
@@ -126,7 +128,9 @@ int mx4_quantize_run(const T *x, uint8_t *codes, uint8_t *scales, int64_t n, hip
 
 template <typename T>
 int mx4_values_run(const uint8_t *codes, const uint8_t *scales, T *x, int64_t n, hipStream_t st) {
-  auto kernel = mx4_once<T>(n) ? mx4_values_kernel<T, true> : mx4_values_kernel<T, false>;
+  auto kernel = mx4_values_kernel<T, false>;
+  if constexpr (sizeof(T) == 2)
+    if (mx4_once<T>(n)) kernel = mx4_values_kernel<T, true>;
   return mx4_parts(n, [&](unsigned grid, int64_t first) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(MX4_THREADS), 0, st, (const uint32_t *)codes, scales, x, n, first);
   });

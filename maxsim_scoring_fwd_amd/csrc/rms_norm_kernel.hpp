@@ -326,7 +326,7 @@ template <typename T, int G, int C, int KIND, int WHICH, bool ONCE> const void *
                : (const void *)norm_kernel<T, G, C, KIND, false, WHICH == NORM_I8, ONCE>;
 }
 template <typename T, int G, int C, int KIND, int WHICH> const void *norm_kernel_of(bool w32, bool once) {
-  if constexpr (KIND == ROW_WHOLE && WHICH != NORM_I8)
+  if constexpr (KIND == ROW_WHOLE && WHICH != NORM_I8 && sizeof(T) == 2)
     if (once) return norm_kernel_of<T, G, C, KIND, WHICH, true>(w32);
   return norm_kernel_of<T, G, C, KIND, WHICH, false>(w32);
 }

@@ -12,31 +12,27 @@ namespace maxsim {
 // stores): its lines would be gone before anyone could use them, and writing them back costs the
 // call itself or the next one. Dropout of a tensor, and of its result, and so on: 128 MiB (256 moved)
 // 39.4 us through the caches and 43.7 past them, 192 MiB 69.5 and 65.2; a norm's forward and backward
-// in turn, 64 MiB a tensor (256 moved by the forward) 85.0 and 90.1, 96 MiB 138.2 and 133.5.
+// in turn, 64 MiB a tensor (256 moved by the forward) 85.0 and 90.1, 96 MiB 138.2 and 133.5. Only
+// 16-bit types: a chunk of fp32 is two accesses, each of half of what its lanes' lines hold, which the
+// caches have to put together (260416 x 768 in fp32 from 4 bits: 221 us through them, 346 past them;
+// dropout 285 and 307; the norm of 80000 x 768 177 and 193).
 constexpr int64_t CACHE_BYTES = (int64_t)256 << 20;
+inline bool past_caches(int64_t bytes, int entry_bytes) { return entry_bytes == 2 && bytes > CACHE_BYTES; }
 
 template <typename T> struct Chunk8 {
   T e[8];
 } __attribute__((packed, aligned(sizeof(T))));
 
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes anywhere
-template <typename T> struct Chunk8Words {
-  u32x4_any v[sizeof(T) / 2];
-};
 template <bool ONCE = false, typename T> __device__ __forceinline__ Chunk8<T> whole_chunk(const T *p) {
   if constexpr (!ONCE) return *(const Chunk8<T> *)p;
-  Chunk8Words<T> x;
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; i++) x.v[i] = __builtin_nontemporal_load((const u32x4_any *)p + i);
-  return __builtin_bit_cast(Chunk8<T>, x);
+  else return __builtin_bit_cast(Chunk8<T>, __builtin_nontemporal_load((const u32x4_any *)p));
 }
 template <bool ONCE = false, typename T> __device__ __forceinline__ void store_whole(T *p, const Chunk8<T> &c) {
   if constexpr (!ONCE) {
     *(Chunk8<T> *)p = c;
   } else {
-    const Chunk8Words<T> x = __builtin_bit_cast(Chunk8Words<T>, c);
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; i++) __builtin_nontemporal_store(x.v[i], (u32x4_any *)p + i);
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4_any, c), (u32x4_any *)p);
   }
 }
 

@@ -52,6 +52,10 @@ def check(h, w, y, scale=1.0, dl=None, backward=True):
     (1023, 511, 128, FP16, 0.9),
     (1025, 513, 36, FP32, 0.5),    # more rows than one count
     (3000, 700, 88, BF16, 0.02),
+    (300, 50001, 24, BF16, 1.0),   # tiles of 256 rows: more than 384 of them
+    (257, 27000, 72, FP16, 0.8),
+    (513, 17001, 36, FP32, 1.0),
+    (3000, 5001, 40, BF16, 0.3),
 ])
 def test_against_reference(n, vocab, d, dtype, share):
     print("case: cross entropy", n, vocab, d, dtype, share, flush=True)
@@ -59,7 +63,7 @@ def test_against_reference(n, vocab, d, dtype, share):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
-@pytest.mark.parametrize("n", [20, 40, 300])
+@pytest.mark.parametrize("n", [20, 40, 300, 25000])
 def test_rows_left_out_hide_what_they_hold(n, dtype):
     """NaN and infinities in rows without a label change nothing; labels of all sizes that are none."""
     h, w, y = make(n, 400, 96, dtype, 0.6, seed=3)
@@ -141,8 +145,9 @@ def test_one_direction_only_and_given_buffers():
     assert (outs[:, 100:] == 3).all() and (ws[size:] == 0x5A).all()
 
 
-def test_repeated_calls_give_the_same_bits():
-    h, w, y = make(3000, 4001, 264, BF16, 0.9)
+@pytest.mark.parametrize("vocab", [4001, 9001])  # tiles of 128 and of 256 rows
+def test_repeated_calls_give_the_same_bits(vocab):
+    h, w, y = make(3000, vocab, 264, BF16, 0.9)
     dl = torch.rand(3000, device="cuda")
     first = [*ms.maxsim_linear_cross_entropy(h, w, y)]
     first += ms.maxsim_linear_cross_entropy_backward(dl, h, w, y, first[1])
