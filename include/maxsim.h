@@ -425,8 +425,9 @@ int maxsim_rms_norm(const void *x, int64_t x_stride, const void *residual, int64
                     void *stream);
 
 /*
- * maxsim_rms_norm with y in 8 bits, as maxsim_score_i8 takes it: scale[row] = max |y| / 127 and
- * codes = y / scale to the nearest (ties to even). A row of zeros has scale 0 and codes 0; one with a
+ * maxsim_rms_norm with y, held in fp32, in 8 bits, as maxsim_score_i8 takes it: scale[row] = max |y| / 127
+ * (to within 2^-23 of it) and codes = y / scale to the nearest (ties to even); a scale below fp32's normal
+ * range is rounded after that division. A row of zeros has scale 0 and codes 0; one with a
  * NaN or an infinity has such a scale, and codes 0. (A row of zeros needs eps > 0, here as above: its y is
  * NaN without.)
  */

@@ -1,5 +1,7 @@
 """The norm with the residual's addition, its 8-bit form and its gradients, and dropout, against
 64-bit references."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -113,6 +115,55 @@ def test_8_bit_rows_of_other_sizes():
     assert torch.isnan(scale[1]) and torch.isnan(scale[2]) and not code[1:3].any()
     y, _, _ = ms.maxsim_rms_norm(x, w, eps=0.0)
     assert torch.isnan(y[1]).all() and torch.isnan(y[2, 3]) and torch.isfinite(y[0]).all()
+
+
+def codes_of(y, scale):
+    """y / scale to the nearest, ties to even. The quotient in 64 bits: a product of a scale of 24 bits and a
+    code and a half of 8 is exact there, and a fp32 y that is not that product is off by 2^-25 of it."""
+    return np.rint(as64(y) / as64(scale)[:, None])
+
+
+def test_8_bit_codes_are_the_nearest_ones():
+    """Entries on the halves between two codes and fp32's neighbours of those, for scales of many
+    mantissas (127: ties are exact), beside entries of any size. Rows of ones keep their weights: the
+    mean of 1024 squares is 1."""
+    x = torch.ones(1, 1024, device="cuda")
+    for i in range(40):
+        most = torch.tensor(127.0 if i % 8 == 0 else 1 + i / 40, device="cuda") * 2.0 ** (i - 20)
+        unit = float(ms.maxsim_rms_norm_i8(x[:, :1], most[None], eps=0.0)[1])
+        assert abs(unit - float(most) / 127) <= 2 ** -23 * unit
+        half = (torch.arange(-127, 127, device="cuda") + 0.5) * unit
+        ends = [torch.nextafter(half, torch.full_like(half, s * math.inf)) for s in (1, -1)]
+        w = torch.cat([most[None], half, *ends, rand(1024 - 1 - 3 * 254, seed=i).clamp(-1, 1) * most])
+        code, scale, _ = ms.maxsim_rms_norm_i8(x, w, eps=0.0)
+        y = ms.maxsim_rms_norm(x, w, eps=0.0)[0]
+        assert torch.equal(y[0], w) and float(scale) == unit
+        assert np.array_equal(as64(code), codes_of(y, scale)), f"scale {float(scale)}"
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("d", [7, 64, 200, 768, 2056])
+def test_8_bit_codes_of_every_form(d, dtype):
+    """The same for rows as they come; fp32 rows of the same values have the same y."""
+    x, w = rand(500, d, dtype=dtype, seed=d), rand(d, seed=d + 1)
+    code, scale, _ = ms.maxsim_rms_norm_i8(x, w)
+    y = ms.maxsim_rms_norm(x.float(), w)[0]
+    most = np.abs(as64(y)).max(1)
+    assert (np.abs(as64(scale) - most / 127) <= 2 ** -23 * most / 127).all()
+    assert np.array_equal(as64(code), codes_of(y, scale))
+
+
+def test_8_bit_rows_at_both_ends_of_the_range():
+    """Rows whose largest entry's reciprocal is no normal number, or whose scale is none, keep their
+    codes."""
+    x = torch.ones(1, 64, device="cuda")
+    for e in (-140, -127, -110, -101, -100, -99, 99, 100, 101, 125, 126, 127):
+        w = (torch.arange(64, device="cuda") * 2 + 1).double() * 2.0 ** e / 127
+        w = w.float()  # the largest is 2^e, up to a rounding
+        code, scale, _ = ms.maxsim_rms_norm_i8(x, w, eps=0.0)
+        most = as64(w).max()
+        assert np.array_equal(as64(code)[0], np.rint(as64(w) / most * 127)), f"2^{e}"
+        assert abs(float(scale) - most / 127) <= 2 * U32 * most / 127 + TINY[torch.float32]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
