@@ -200,6 +200,8 @@ int maxsim_dequantize_mx4(const uint8_t *codes, const uint8_t *scales, int64_t n
  *   D        codes [tokens][d / 2], d_scale [tokens][d / 32]
  *   doc_offsets  nullable: CSR as in maxsim_score; NULL means fixed documents of nd tokens each, of
  *            which doc_lens (nullable int32 [n_docs], clamped to [0, nd]) count
+ *   With n_docs == 0 any array may be NULL. Documents without a token (doc_offsets all equal) score
+ *   -inf, and nothing is read at D and d_scale, which still have to be addresses.
  *   d        a multiple of 32 in [MAXSIM_MIN_D, MAXSIM_MAX_D]; queries of more than 64 tokens:
  *            q_len in whole 16s times the row's bytes (d / 2, up to 64, 128, 256 or 512) at most
  *            64 KiB, else MAXSIM_ERR_UNSUPPORTED

@@ -1348,9 +1348,13 @@ def maxsim_score_mx4(Q: torch.Tensor, q_scale: torch.Tensor, D: torch.Tensor, d_
     _need(doc_lens, "doc_lens", torch.int32, shape=(n_docs,))
     out = _out(out, n_docs, Q.device, stream)
     at = Q.get_device()
+    at_D, at_scale = _at(D, "D", at), _at(d_scale, "d_scale", at)
+    if doc_offsets is not None and not D.numel():
+        # documents without a token: an empty tensor has no address, and none is read
+        at_D, at_scale = Q.data_ptr(), q_scale.data_ptr()
     _check(lib().maxsim_score_mx4(
-        _at(Q, "Q", at), _at(q_scale, "q_scale", at), Q.shape[0], _at(D, "D", at),
-        _at(d_scale, "d_scale", at), _at(doc_offsets, "doc_offsets", at), n_docs, nd,
+        _at(Q, "Q", at), _at(q_scale, "q_scale", at), Q.shape[0], at_D,
+        at_scale, _at(doc_offsets, "doc_offsets", at), n_docs, nd,
         _at(doc_lens, "doc_lens", at), d, _at(out, "out", at), _stream_at(stream, at)),
         "maxsim_score_mx4")
     return out

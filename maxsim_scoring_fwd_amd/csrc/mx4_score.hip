@@ -58,14 +58,14 @@ extern "C" int maxsim_score_mx4(const uint8_t *Q, const uint8_t *q_scale, int q_
   if (n_docs < 0 || q_len < 1 || q_len > MAXSIM_MAX_Q_LEN || d < MAXSIM_MIN_D || d > MAXSIM_MAX_D || d % 32 ||
       (!doc_offsets && nd < 1))
     return MAXSIM_ERR_SHAPE;
-  if (!Q || !q_scale || !D || !d_scale || !out) return MAXSIM_ERR_NULL;
   if (doc_offsets && doc_lens) return MAXSIM_ERR_UNSUPPORTED;
+  const int steps = (d + 127) / 128, ks = steps <= 1 ? 1 : steps <= 2 ? 2 : steps <= 4 ? 4 : 8;
+  if (q_len > 64 && (int64_t)((q_len + 15) / 16) * 16 * ks * 64 > MX4_LDS_QUERY) return MAXSIM_ERR_UNSUPPORTED;
+  if (n_docs == 0) return MAXSIM_OK;  // arrays of no documents have no address
+  if (!Q || !q_scale || !D || !d_scale || !out) return MAXSIM_ERR_NULL;
   if (!aligned(Q, 16) || !aligned(D, 16) || !aligned(out, 4) || (doc_offsets && !aligned(doc_offsets, 8)) ||
       (doc_lens && !aligned(doc_lens, 4)))
     return MAXSIM_ERR_ALIGN;
-  const int steps = (d + 127) / 128, ks = steps <= 1 ? 1 : steps <= 2 ? 2 : steps <= 4 ? 4 : 8;
-  if (q_len > 64 && (int64_t)((q_len + 15) / 16) * 16 * ks * 64 > MX4_LDS_QUERY) return MAXSIM_ERR_UNSUPPORTED;
-  if (n_docs == 0) return MAXSIM_OK;
   DeviceInfo di;
   const int rc = current_device(di);
   if (rc != MAXSIM_OK) return rc;

@@ -112,3 +112,26 @@ def test_many_documents():
     rng = np.random.default_rng(3)
     scores(32, rng.integers(0, 90, 9001).tolist(), 64, "packed")
     scores(20, [48] * 30011, 32, "fixed")
+
+
+def test_empty_collections():
+    """No documents, and documents without a token, in tensors that have no address."""
+    Q, qs = ms.maxsim_quantize_mx4(rand(32, 128))
+
+    def empty(*shape):
+        return torch.empty(shape, dtype=torch.uint8, device="cuda")
+    zeros = torch.zeros(5, dtype=torch.int64, device="cuda")
+    assert empty(0, 64).data_ptr() == 0
+    assert ms.maxsim_score_mx4(Q, qs, empty(0, 7, 64), empty(0, 7, 4)).shape == (0,)
+    lens = torch.zeros(0, dtype=torch.int32, device="cuda")
+    assert ms.maxsim_score_mx4(Q, qs, empty(0, 7, 64), empty(0, 7, 4), doc_lens=lens).shape == (0,)
+    assert ms.maxsim_score_mx4(Q, qs, empty(0, 64), empty(0, 4), zeros[:1]).shape == (0,)
+    D, ds = ms.maxsim_quantize_mx4(rand(0, 128))
+    got = ms.maxsim_score_mx4(Q, qs, D, ds, zeros)
+    assert got.tolist() == [-float("inf")] * 4
+    Q, qs = ms.maxsim_quantize_mx4(rand(100, 128))  # its operands from LDS
+    assert ms.maxsim_score_mx4(Q, qs, D, ds, zeros).tolist() == [-float("inf")] * 4
+    for d in (32, 64, 512):
+        Q, qs = ms.maxsim_quantize_mx4(rand(20, d))
+        D, ds = ms.maxsim_quantize_mx4(rand(0, d))
+        assert ms.maxsim_score_mx4(Q, qs, D, ds, zeros).tolist() == [-float("inf")] * 4

@@ -273,6 +273,14 @@ def test_mx4_c_entries_refuse(L):
     assert f(n=0) == OK
 
 
+def test_4_bit_scores_of_no_documents_need_no_address(L):
+    def f(Q=None, qs=None, q=32, D=None, ds=None, off=None, nd=4, lens=None, d=128, out=None):
+        return L.maxsim_score_mx4(Q, qs, q, D, ds, off, 0, nd, lens, d, out, None)
+    assert f() == OK and f(off=P) == OK and f(Q=P, qs=P, lens=P) == OK
+    assert f(q=0) == SHAPE and f(nd=0) == SHAPE and f(d=48) == SHAPE and f(off=P, lens=P) == UNSUP
+    assert f(q=129, d=1024) == UNSUP
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU error path")
 def test_valid_calls_without_gpu_report_a_device_error(L):
     assert L.maxsim_rms_norm(P, 64, P, 64, 10, 64, 0, P, 2, 1e-6, 0.1, P, 0, P, P, P, None) == DEVICE
