@@ -182,7 +182,7 @@ int maxsim_score_i8(const int8_t *Q, const float *q_scale, int q_len, const int8
  * times 2^k. k = floor(log2 of the block's largest absolute entry) - 2, from -127 up; an entry goes
  * to the nearest, ties to the even code, and to 6 where it is larger. A block of zeros has byte 0; one
  * with a NaN or an infinity has byte 255 (not a number) and codes 0.
- *   x       [n_rows][d] in `dtype`, d a multiple of 32 in [MAXSIM_MIN_D, MAXSIM_MAX_D]
+ *   x       [n_rows][d] in `dtype`, 16-byte aligned, d a multiple of 32 in [MAXSIM_MIN_D, MAXSIM_MAX_D]
  *   codes   uint8 [n_rows][d / 2], two entries a byte, the first in the low half; 16-byte aligned
  *   scales  uint8 [n_rows][d / 32]
  * maxsim_dequantize_mx4 gives the values that they stand for, in `dtype`.
@@ -200,6 +200,9 @@ int maxsim_dequantize_mx4(const uint8_t *codes, const uint8_t *scales, int64_t n
  *   D        codes [tokens][d / 2], d_scale [tokens][d / 32]
  *   doc_offsets  nullable: CSR as in maxsim_score; NULL means fixed documents of nd tokens each, of
  *            which doc_lens (nullable int32 [n_docs], clamped to [0, nd]) count
+ *   A byte of 255 (a block that held a NaN or an infinity) leaves a document's score undefined, and one
+ *   in the query every score; the other documents' are what they are without it. (In rows of 32 and 64
+ *   entries such a block also hides other tokens of its document.)
  *   With n_docs == 0 any array may be NULL. Documents without a token (doc_offsets all equal) score
  *   -inf, and nothing is read at D and d_scale, which still have to be addresses.
  *   d        a multiple of 32 in [MAXSIM_MIN_D, MAXSIM_MAX_D]; queries of more than 64 tokens:

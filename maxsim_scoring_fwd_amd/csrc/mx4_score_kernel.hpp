@@ -70,7 +70,8 @@ __device__ __forceinline__ void nearest_boundaries(const int64_t *off, int64_t n
 // query's operands come from LDS, else they stay in registers. SUB: rows of 128 / SUB entries, of which
 // an operand holds SUB sixteens side by side, and the query stands in its own part of SUB operands
 // beside zeros: as many products, but whole loads (documents of 128 tokens, 60000 with d = 64: 72 us
-// with SUB = 1, 56 with 2; 100000 with d = 32: 80 with 1, 45 with 4).
+// with SUB = 1, 56 with 2; 100000 with d = 32: 80 with 1, 45 with 4). A block that is not a number
+// meets the zeros too, and takes out the tokens of its document that lie 16, 32 and 48 places away.
 template <int KS, int QB, int P, bool QLDS, int SUB>
 __global__ void __launch_bounds__(DENSE_THREADS) mx4_score_kernel(Mx4Args a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];

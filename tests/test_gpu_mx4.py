@@ -135,3 +135,27 @@ def test_empty_collections():
         Q, qs = ms.maxsim_quantize_mx4(rand(20, d))
         D, ds = ms.maxsim_quantize_mx4(rand(0, d))
         assert ms.maxsim_score_mx4(Q, qs, D, ds, zeros).tolist() == [-float("inf")] * 4
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 512])
+def test_blocks_that_are_no_number_stay_in_their_document(d):
+    """A NaN in one token leaves its own document's score undefined, and every other as it is."""
+    lens = [20, 70, 64, 5, 0, 33]
+    x = rand(sum(lens), d, seed=d)
+    off = torch.tensor([0, *np.cumsum(lens)], dtype=torch.int64, device="cuda")
+    for q_len in (20, 70):
+        Q, qs = ms.maxsim_quantize_mx4(rand(q_len, d))
+        want = ms.maxsim_score_mx4(Q, qs, *ms.maxsim_quantize_mx4(x), off)
+        for b, at in ((1, 20), (1, 89), (2, 100), (5, 191)):
+            bad = x.clone()
+            bad[at, 3] = float("nan")
+            got = ms.maxsim_score_mx4(Q, qs, *ms.maxsim_quantize_mx4(bad), off)
+            others = [i for i in range(len(lens)) if i != b]
+            assert torch.equal(got[others], want[others])
+    fixed = x[:180].view(6, 30, d)
+    Q, qs = ms.maxsim_quantize_mx4(rand(20, d))
+    want = ms.maxsim_score_mx4(Q, qs, *ms.maxsim_quantize_mx4(fixed))
+    bad = fixed.clone()
+    bad[2, 29, d - 1] = float("inf")
+    got = ms.maxsim_score_mx4(Q, qs, *ms.maxsim_quantize_mx4(bad))
+    assert torch.equal(got[[0, 1, 3, 4, 5]], want[[0, 1, 3, 4, 5]])
