@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(NORM_JOIN) norm_weight_kernel(const float *par
 const void *norm_kernel(int which, int dtype, int64_t n_rows, int d, int weight_dtype, int tensors) {
   const bool w32 = weight_dtype == MAXSIM_FP32;
   const bool once = past_caches(n_rows * d * elem_bytes(dtype) * tensors, elem_bytes(dtype));
-  return dtype == MAXSIM_FP32   ? norm_kernel_fp32(which, d, true, once)
+  return dtype == MAXSIM_FP32   ? norm_kernel_fp32(which, d)
          : dtype == MAXSIM_FP16 ? norm_kernel_fp16(which, d, w32, once)
                                 : norm_kernel_bf16(which, d, w32, once);
 }

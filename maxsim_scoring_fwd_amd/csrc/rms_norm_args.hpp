@@ -44,9 +44,9 @@ inline int norm_chunks(int d) {
 }
 
 // The kernel (of the three above) for rows of d entries; weights in fp32 or in the rows' type; past the
-// caches or not.
+// caches or not. fp32 rows have neither choice.
 const void *norm_kernel_bf16(int which, int d, bool w32, bool once);
 const void *norm_kernel_fp16(int which, int d, bool w32, bool once);
-const void *norm_kernel_fp32(int which, int d, bool w32, bool once);
+const void *norm_kernel_fp32(int which, int d);
 
 }  // namespace maxsim

@@ -339,13 +339,15 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_backward_kernel(NormArgs a)
   }
 }
 
+template <typename T, int G, int C, int KIND, int WHICH, bool W32, bool ONCE> const void *norm_kernel_of() {
+  static_assert(W32 || sizeof(T) == 2, "fp32 rows have fp32 weights");
+  if constexpr (WHICH == NORM_BACK) return (const void *)norm_backward_kernel<T, G, C, KIND, W32, ONCE>;
+  else return (const void *)norm_kernel<T, G, C, KIND, W32, WHICH == NORM_I8, ONCE>;
+}
 template <typename T, int G, int C, int KIND, int WHICH, bool ONCE> const void *norm_kernel_of(bool w32) {
-  if constexpr (WHICH == NORM_BACK)
-    return w32 ? (const void *)norm_backward_kernel<T, G, C, KIND, true, ONCE>
-               : (const void *)norm_backward_kernel<T, G, C, KIND, false, ONCE>;
-  else
-    return w32 ? (const void *)norm_kernel<T, G, C, KIND, true, WHICH == NORM_I8, ONCE>
-               : (const void *)norm_kernel<T, G, C, KIND, false, WHICH == NORM_I8, ONCE>;
+  if constexpr (sizeof(T) == 2)
+    if (!w32) return norm_kernel_of<T, G, C, KIND, WHICH, false, ONCE>();
+  return norm_kernel_of<T, G, C, KIND, WHICH, true, ONCE>();
 }
 template <typename T, int G, int C, int KIND, int WHICH> const void *norm_kernel_of(bool w32, bool once) {
   if constexpr (KIND == ROW_WHOLE && WHICH != NORM_I8 && sizeof(T) == 2)
