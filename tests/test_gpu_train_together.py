@@ -94,6 +94,38 @@ def test_index_scores_are_those_of_the_vectors_it_stands_for(example):
         assert float((index.scores(Q).double() - want).abs().max()) <= tol
 
 
+@pytest.mark.parametrize("kind", ["bf16", "int8", "mx4"])
+def test_search_finds_what_plain_scores_find(example, monkeypatch, kind):
+    """Each query of a search: its scores are those of the vectors that the index stands for in 64 bits, and the
+    documents found and the best five are the plain scores' own, but where two of them are as near to
+    each other as the sums' rounding."""
+    print("case: search", kind, flush=True)
+    _, encoder = example.train(5, masked=5, report=lambda line: None)
+    values = {"bf16": lambda x: x.double(), "int8": lambda c, s: c.double() * s.double()[:, None],
+              "mx4": lambda c, s: ms.maxsim_dequantize_mx4(c, s).double()}[kind]
+    scores, plain, tol = example.Index.scores, [], 0.0
+
+    def checked(index, Q):
+        nonlocal tol
+        got = scores(index, Q)
+        s = values(*index.store(Q)) @ values(*index.stored).t()
+        off = index.offsets.tolist()
+        plain.append(torch.stack([s[:, a:b].max(1).values.sum() for a, b in zip(off[:-1], off[1:])]))
+        # unit vectors (in 8 bits sqrt(128) long): 32 sums of 128 products in 32 bits
+        tol = max(tol, 2.0 ** -24 * 140 * 32 * (128.0 if kind == "int8" else 1.0) * 1.25)
+        assert float((got.double() - plain[-1]).abs().max()) <= tol
+        return got
+    monkeypatch.setattr(example.Index, "scores", checked)
+    found, best = example.search(encoder, index=kind)
+    assert len(plain) == 20
+    first = [(float(p[i]), float(torch.cat([p[:i], p[i + 1:]]).max())) for i, p in enumerate(plain)]
+    assert sum(a > b + 2 * tol for a, b in first) <= found <= sum(a >= b - 2 * tol for a, b in first)
+    p = plain[-1]
+    assert len(set(best)) == 5
+    order = torch.sort(p, descending=True).values[:5]
+    assert float((p[best] - order).abs().max()) <= 2 * tol
+
+
 def test_a_whole_step_captured():
     """Norm, rotary positions, attention, norm, loss, and all their gradients in one graph: replays
     are the eager step's bits, with the masks of each replay's own step."""
