@@ -15,9 +15,13 @@ template <int KS, int QB, bool QLDS, int SUB = 1> int mx4_launch(Mx4Args &a, con
   auto kernel = mx4_score_kernel<KS, QB, P, QLDS, SUB>;
   int bpc = blocks_per_cu((const void *)kernel, DENSE_THREADS, lds);
   // Packed documents go to waves in whole ones: with fewer waves the longest share is nearer the mean,
-  // and 12 waves a CU have bytes enough under way (20000 documents of 20 to 300 tokens, d = 96: 43.2
-  // us with 7 workgroups a CU, 38.5 with 3; 100000 documents of equal length: 136.3 and 136.5).
-  if (a.doc.offsets && bpc > 3) bpc = 3;
+  // and 12 waves a CU have bytes enough under way (20000 documents of 20 to 300 tokens, 32 query tokens,
+  // as many workgroups as fit and 3 of them a CU: d = 32 21.3 and 21.9 us, 64 28.6 and 28.4, 96 42.5 and
+  // 39.8, 128 50.0 and 49.4; 10000 with d = 256 53.5 and 52.4, 5000 with 512 60.8 and 60.9, 3000 with 1024
+  // 83.5 both; 64 query tokens, d = 128, 48.9 and 48.6; fixed documents of equal length 136.3 and 136.5).
+  // A query in LDS makes the matrix cores and LDS the bound, and those want every wave (5000 documents of
+  // 20 to 340, d = 128: 128 query tokens 26.5 and 28.6 us, 300 61.5 and 64.0).
+  if (!QLDS && a.doc.offsets && bpc > 3) bpc = 3;
   int64_t grid = (int64_t)di.cus * bpc;
   const int64_t most = (a.doc.n_docs + DENSE_WAVES - 1) / DENSE_WAVES;
   if (grid > most) grid = most;
