@@ -410,7 +410,8 @@ int maxsim_dropout(const void *x, int64_t n, int dtype, double p, const int64_t 
  *     h = residual + dropout(x), rounded to `dtype`     (either may be left out)
  *     y = h * rstd * weight,  rstd = 1 / sqrt(mean of h^2 + eps)
  * The norm is of h as it is handed on, so that the backward, which reads h, differentiates just
- * this function. The mean is held in 32 bits: rows whose squares sum past its range get y = 0.
+ * this function. The mean is held in 32 bits: rows whose squares sum past its range get y = 0,
+ * and squares below it (of entries under 2^-75) count as nothing, which eps hides unless it is 0.
  *   x, residual  [n_rows][d] in `dtype`, rows at strides given in entries, entries of a row side by
  *            side; any d up to MAXSIM_MAX_NORM (else MAXSIM_ERR_UNSUPPORTED), any alignment of the
  *            type; residual nullable; n_rows <= 2^31
@@ -483,10 +484,19 @@ size_t maxsim_linear_cross_entropy_workspace_size(int64_t n_rows, int64_t vocab,
  * Gradients of maxsim_linear_cross_entropy from those of its losses (fp32 [n_rows]) and the forward's
  * lse: dh [n_rows][d] and dw [vocab][d] in `dtype`, each nullable. Piece by piece of the vocabulary,
  *     P = (exp(z - lse) - [v is the label]) * grad_loss * scale,   dh = P w,   dw = P^T h
- * with P, one piece of it, in the workspace, rounded to `dtype` (16-bit types: after a scaling that
- * makes a mean's gradients powers of two, in fp16 from the largest of them). Sums are fp32, each result is rounded once. A piece of P
- * takes 512 MiB at most, or 128 columns; dh's sums take 4 bytes an entry or up to 128 MiB, and those
- * of dw with many rows and a small vocabulary 128 MiB. With n_rows == 0 dw is set to zero.
+ * with P, one piece of it, in the workspace, rounded to `dtype`. Sums are fp32, each result is rounded once.
+ *   P's rounding  in 16-bit types P is scaled first, so that the gradients of a mean are powers of two, which
+ *            rounding leaves alone. Gradients that differ from row to row are rounded like all of P, by
+ *            up to half a step each: with gradients uniform in [0, 1 / n] dh and dw are off by some 1.45
+ *            times (bf16) or up to 1.35 times (fp16) what their own rounding alone leaves, with a mean's by
+ *            up to 1.15 times (root mean squares). In fp16 entries of P below 2^-28 of the largest gradient
+ *            have steps of 2^-38 of it.
+ *   workspace  16-byte aligned, maxsim_linear_cross_entropy_backward_workspace_size bytes: a copy of the rows
+ *            (each in whole 64 bytes); a piece of P, rows in 256s times columns in 128s, of at most
+ *            512 MiB, or 128 columns; dh's sums in fp32, rows in 128s times d in 256s, or parts of them
+ *            up to 128 MiB; and 128 MiB for parts of dw where it has fewer than 512 tiles of 256 x 128 in
+ *            a piece and there are some 1000 rows or more (500 in fp32)
+ * With n_rows == 0 dw is set to zero.
  */
 int maxsim_linear_cross_entropy_backward(const float *grad_loss, const void *h, const void *w,
                                          const int64_t *labels, const float *lse, int64_t n_rows,

@@ -9,7 +9,9 @@
 //             dw = P^T h of the piece and dh += P w over it.
 // Sums are 32 bits wide, every one has one owner and a fixed order. P is rounded because the matrix
 // cores take 16-bit operands, after a scaling (ce_up) that fits fp16's short range and leaves a mean's
-// gradients exact.
+// gradients exact. Where they differ from row to row they are rounded as well, half a step of 16 bits
+// each at most: relative errors of dh and dw against 64 bits (2048 rows, 8000 x 256 in bf16) 0.00168 with
+// a mean's, 0.00235 with gradients uniform in [0, 1 / n], and 0.00166 from rounding dh and dw alone.
 // The matrix cores bound the training step and the bytes of w the few rows of a query. Measured (one
 // MI355X): 8192 rows, 30522 entries, d = 768 in bf16: gathering 11 us (twice), logits and their
 // sums 374 to 390 (1.03 to 0.99 PFLOP/s; a library product of the shape takes 410 and writes the
@@ -126,7 +128,8 @@ struct CeUnits {
 // What P is multiplied by before it is rounded. Its entries at the labels are the gradients (times p -
 // 1, which is -1 but for well known labels), and those of a mean are all alike: divided by the
 // mantissa of one of them they are powers of two, and rounding does not move them all by the same
-// amount. fp16: that of the largest, which becomes 2^14; bf16: that of the first row.
+// amount. fp16: that of the largest, which becomes 2^14; bf16: that of the first row. Where the
+// gradients are not alike it fits that row only, and the others are rounded as they come.
 template <int DT> __device__ __forceinline__ float ce_up(const CeArgs &a) {
   if constexpr (DT == DT_FP32) return 1.0f;
   float most = 0.0f;

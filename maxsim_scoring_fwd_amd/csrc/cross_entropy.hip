@@ -10,7 +10,9 @@ namespace {
 // Room for P, one piece of the vocabulary, and at least one tile of it for all rows. Fewer and longer
 // pieces are worth more than a P that stays in the chip's 256 MiB cache: each piece adds to dh's
 // sums and ends with workgroups that wait for the last (8192 x 30522 x 768 in bf16, both products
-// of all pieces: room of 128 MiB 818 us, 256 MiB 718, 512 MiB 677, where P is one piece).
+// of all pieces: room of 128 MiB 818 us, 256 MiB 718, 512 MiB 677, where P is one piece). Rows are wide
+// there and P's own way to memory and back hides behind the products; at narrow widths it does not, and
+// no other room was tried there.
 constexpr int64_t CE_P_BYTES = (int64_t)512 << 20;
 // Room for dh's tiles in parts: two for every workgroup that the chip holds at once, so that CeUnits
 // can make parts short enough where there are few tiles; and for dw's of a piece, where there are less

@@ -12,7 +12,10 @@
 // (finite, in range) and meet zeros in the query's operand. The read of the documents bounds it: on
 // one MI355X 100000 documents of 128 tokens, d = 128, take 129 to 132 us (870 MB at 6.7 TB/s), and
 // 20000 of 20 to 300 tokens, d = 96, 34 us (163 MB at 4.8 TB/s, of which the search for a wave's
-// documents and the last tiles are some 10 us).
+// documents and the last tiles are some 10 us). Wide rows have few documents a wave, and the longest share
+// sets the time (10000 documents of 128 tokens: d = 256 42 us, 4.1 TB/s, 512 83 us, 4.2; 5000, d = 1024
+// 91 us, 3.8). With a long query LDS and the matrix cores share it (5000 documents of 180 tokens, d = 128,
+// 300 query tokens: 44 us for 12 of bytes; LDS busy 41 in 100 cycles, the matrix cores 26).
 #pragma once
 
 #include "dense_kernel.hpp"

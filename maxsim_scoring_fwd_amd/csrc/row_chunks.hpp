@@ -15,7 +15,7 @@ namespace maxsim {
 // in turn, 64 MiB a tensor (256 moved by the forward) 85.0 and 90.1, 96 MiB 138.2 and 133.5. Only
 // 16-bit types: a chunk of fp32 is two accesses, each of half of what its lanes' lines hold, which the
 // caches have to put together (260416 x 768 in fp32 from 4 bits: 221 us through them, 346 past them;
-// dropout 285 and 307; the norm of 80000 x 768 177 and 193).
+// dropout of that tensor 285 and 307; the norm of 80000 x 768 with a residual 177 and 193).
 constexpr int64_t CACHE_BYTES = (int64_t)256 << 20;
 inline bool past_caches(int64_t bytes, int entry_bytes) { return entry_bytes == 2 && bytes > CACHE_BYTES; }
 

@@ -251,6 +251,24 @@ def test_loss_c_entries_refuse(L):
     assert size(32768, 130000, 768, 0) < 32768 * 130000 * 4 // 50
 
 
+@pytest.mark.parametrize("n, vocab, d, dt", [(1, 1, 8, 0), (40, 4500001, 512, 0), (130, 100000, 128, 0),
+                                             (8192, 30522, 768, 0), (200000, 1000, 64, 0), (1 << 22, 1000, 8, 1),
+                                             (32768, 30522, 256, 2), (9000, 100, 512, 2)])
+def test_backward_workspace_of_the_loss_is_what_the_header_says(L, n, vocab, d, dt):
+    """A copy of the rows, a piece of P, dh's sums and dw's parts, each as stated, and 20 bytes a row and some
+    lines beside them."""
+    def up(x, by):
+        return -(-x // by) * by
+    eb = 4 if dt == 2 else 2
+    rows, tile = up(n, 256), 256 * 128 * 4
+    piece = max(min(512 << 20, rows * up(vocab, 128) * eb), rows * 128 * eb)
+    sums = max(up(n, 128) * up(d, 256) * 4, 128 << 20)
+    size = L.maxsim_linear_cross_entropy_backward_workspace_size(n, vocab, d, dt)
+    assert size <= n * up(d * eb, 64) + piece + sums + (128 << 20) + 20 * n + 4096
+    # and no less than a whole tile of everything
+    assert size >= n * d * eb + min(piece, rows * 128 * eb) + up(n, 128) * up(d, 256) * 4 >= tile
+
+
 def test_mx4_c_entries_refuse(L):
     def q(x=P, n=4, d=64, dt=0, c=P, s=P):
         return L.maxsim_quantize_mx4(x, n, d, dt, c, s, None)
