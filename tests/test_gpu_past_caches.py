@@ -129,3 +129,31 @@ def test_4_bit_vectors(n, d, dtype):
     want, k = ref.mx4(as64(x[n - 100:]))
     assert np.array_equal(ref.unpack(codes[n - 100:]), want)
     assert torch.equal(values[n - 100:].cpu(), torch.from_numpy(ref.mx4_values(want, k)).to(dtype))
+
+
+def test_more_rows_than_one_launch_takes():
+    """2^28 rows of 3 entries fill a launch's grid; the ones behind them go in another."""
+    print("case: rows of two launches", flush=True)
+    n, d = (1 << 28) + 1000, 3
+    x = rand(1000, d, dtype=BF16).repeat(n // 1000 + 1, 1)[:n]
+    w, rng = rand(d, seed=1), torch.tensor([4, 9], device="cuda")
+    y, h, rstd = ms.maxsim_rms_norm(x, w, None, 1e-6, 0.5, rng, 2)
+    code, scale, _ = ms.maxsim_rms_norm_i8(x, w)
+    small = ms.maxsim_rms_norm_i8(x[:1000], w)
+    for first in (0, (1 << 28) - 500, (1 << 28), n - 1000):
+        at = slice(first, first + 1000)
+        keep, up = ref.kept(rng.tolist(), 2, 0.5, 1000, d, first)
+        want = torch.where(torch.from_numpy(keep), x[at].cpu().float() * torch.tensor(up), torch.zeros(()))
+        assert torch.equal(h[at].cpu(), want.to(BF16))
+        want, tol, wr = ref.norm(as64(h[at]), as64(w), 1e-6, BF16)
+        ref.close(y[at], want, tol, "y")
+        ref.close(rstd[at], wr[:, 0], wr[:, 0] * 32 * U32, "rstd")
+        turn = first % 1000
+        assert torch.equal(code[at], small[0].roll(-turn, 0)) and torch.equal(scale[at], small[1].roll(-turn, 0))
+    gy = x[:1000].flip(0).repeat(n // 1000 + 1, 1)[:n]
+    dx, _, _ = ms.maxsim_rms_norm_backward(gy, h, w, rstd, None, 0.5, rng, 2, want_dresidual=False, want_dweight=False)
+    for first in (0, (1 << 28) - 500, n - 1000):
+        at = slice(first, first + 1000)
+        keep, up = ref.kept(rng.tolist(), 2, 0.5, 1000, d, first)
+        g = ref.norm_backward(as64(h[at]), as64(w), 1e-6, as64(gy[at]), 0.0, keep * np.float64(up), BF16, FP32)
+        ref.close(dx[at], g["dx"], g["tol_dx"], "dx")
