@@ -465,7 +465,8 @@ size_t maxsim_rms_norm_backward_workspace_size(int64_t n_rows, int d);
  *     z_v = scale * <w_v, h_i>,   lse[i] = log sum_v exp(z_v),   loss[i] = lse[i] - z_label[i]
  * A row whose label lies outside [0, vocab) is left out: loss 0, lse -inf, no gradient; what it holds
  * is never used, and it costs nothing beside its label (masked-token training labels few rows).
- * Products run on the matrix cores with fp32 sums; statistics are fp32.
+ * Products run on the matrix cores with fp32 sums; statistics are fp32, and loss and lse, differences of
+ * logits in 64 bits, are rounded once.
  *   h       [n_rows][d], w [vocab][d] in `dtype`, densely packed, 16-byte aligned, finite;
  *           d * element bytes a multiple of 16, d <= 16384; n_rows <= 2^22, vocab <= 2^26, and
  *           ceil(n_rows / 256) * ceil(vocab / 128) below 2^31

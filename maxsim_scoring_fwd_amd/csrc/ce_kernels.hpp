@@ -54,8 +54,8 @@ struct CeArgs {
   float *most;            // [the same]: the largest absolute gradient
   int4 *info;             // [n]: of gathered row i (CeRow)
   char *hc;               // gathered rows in panels of 64 bytes, n rows each, zeros past d
-  float2 *part;           // [tiles of the vocabulary][n]: largest logit (in units of log 2), sum
-  float *picked;          // [n]: the label's logit, in units of log 2
+  float2 *part;           // [tiles of the vocabulary][n]: largest product, and sum (CeSum)
+  float *picked;          // [n]: the label's product
   char *p;                // P in panels of 64 bytes, whole tiles of rows each
   float *dhp, *dwp;       // tiles of dh and, where they go in parts, of dw, in the kernels' register layout
   int32_t *queue;         // [8]: units of the products that are taken
@@ -69,8 +69,8 @@ struct CeArgs {
 // of its tiles, 27 us, and take 22 in tiles of 128).
 inline bool ce_few(const CeArgs &a) { return a.n <= CE_FEW; }
 
-// A gathered row: its label, its place among all rows, and for the backward its lse in units of log
-// 2 and its gradient times scale.
+// A gathered row: its label, its place among all rows, and for the backward its lse (16-bit types: in
+// units of log 2) and its gradient times scale.
 struct CeRow {
   int label, row;
   float lse, grad;
@@ -205,7 +205,7 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_gather_kern
     if (counts) {
       CeRow row{(int)label, (int)r, 0.0f, 0.0f};
       if (a.grad) {
-        row.lse = a.lse[r] * LOG2E;
+        row.lse = DT == DT_FP32 ? a.lse[r] : a.lse[r] * LOG2E;
         row.grad = a.grad[r] * a.scale;
       }
       a.info[at] = __builtin_bit_cast(int4, row);
@@ -348,8 +348,38 @@ template <int DT, int BM, int BN, int WM, int STAGES> struct CeLogits {
   }
 };
 
-// What a tile of logits leaves: for every row the largest logit and the sum of exponentials over the
-// tile, and the label's logit where the tile holds it. label(i): the label of row i of the tile;
+// The exponentials of a row over a part of the vocabulary: the largest product x.most, unscaled, and the
+// sum of 2^(x f - round(most f)), f = scale / log 2 rounded. What the rounding of most f takes away the
+// exponentials hold, so that nothing of the size of the logits is rounded before the end (finish).
+struct CeSum {
+  float most, sum;
+  __device__ __forceinline__ void add(const CeSum &o, float f) {
+#pragma clang fp contract(off)  // most f is to be rounded before anything is taken from it
+    const float m = __builtin_fmaxf(most, o.most), from = m == -__builtin_inff() ? 0.0f : m * f;
+    sum = sum * __builtin_amdgcn_exp2f(most * f - from) + o.sum * __builtin_amdgcn_exp2f(o.most * f - from);
+    most = m;
+  }
+  // lse and loss, each rounded once from 64 bits: the logarithm is of what is left beside the largest
+  // logit, and the logit of a product is exact. (In 32 bits and units of log 2, rounded at each step,
+  // losses of 1.3 to 29 from logits of 193 to 413 were off by up to 2.9e-5, here 5e-7.)
+  __device__ __forceinline__ void finish(float scale, float f, float picked, float &lse, float &loss) const {
+#pragma clang fp contract(off)
+    // sum = m 2^e with m in [3/4, 3/2): the logarithm of a sum near 1 keeps its digits
+    float m = __builtin_amdgcn_frexp_mantf(sum);
+    int e = __builtin_amdgcn_frexp_expf(sum);
+    if (m < 0.75f) {
+      m *= 2.0f;
+      e--;
+    }
+    const double product = (double)most, beside = (double)(most * f) - product * (double)f + e + (double)__builtin_log2f(m);
+    constexpr double LN2_64 = 0.693147180559945309417;
+    lse = (float)(scale * product + beside * LN2_64);
+    loss = (float)(scale * (product - (double)picked) + beside * LN2_64);
+  }
+};
+
+// What a tile of logits leaves: for every row its CeSum over the tile, and the label's product where the
+// tile holds it. label(i): the label of row i of the tile;
 // red: scratch of WM * BN pairs. The workgroup is together again afterwards.
 template <typename G, int BM, int BN, int WM, typename Label>
 __device__ __forceinline__ void ce_tile_sums(const CeArgs &a, G &g, int64_t v0, int64_t r0, int m, float2 *red, Label label) {
@@ -372,7 +402,7 @@ __device__ __forceinline__ void ce_tile_sums(const CeArgs &a, G &g, int64_t v0, 
 #pragma unroll
         for (int e = 0; e < 16; e++)
           if (k * 32 + acc_row(e) == at - h4) picked = x[k][e];
-      if (at >= 0 && at < BM / WM && (at & 4) == h4) a.picked[r] = picked * f;
+      if (at >= 0 && at < BM / WM && (at & 4) == h4) a.picked[r] = picked;
     }
     if (exist < BM / WM) {
 #pragma unroll
@@ -386,8 +416,8 @@ __device__ __forceinline__ void ce_tile_sums(const CeArgs &a, G &g, int64_t v0, 
     for (int k = 0; k < G::TM; k++)
 #pragma unroll
       for (int e = 0; e < 16; e++) most = __builtin_fmaxf(most, x[k][e]);
-    most = half_max(most) * f;  // scale is positive
-    const float from = most == -__builtin_inff() ? 0.0f : most;
+    most = half_max(most);  // scale is positive
+    const float from = most == -__builtin_inff() ? 0.0f : most * f;
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < G::TM; k++)
@@ -398,15 +428,10 @@ __device__ __forceinline__ void ce_tile_sums(const CeArgs &a, G &g, int64_t v0, 
   }
   __syncthreads();
   if (threadIdx.x < BN && r0 + threadIdx.x < m) {
-    float2 s = red[threadIdx.x];
+    CeSum s = __builtin_bit_cast(CeSum, red[threadIdx.x]);
 #pragma unroll
-    for (int k = 1; k < WM; k++) {
-      const float2 o = red[k * BN + threadIdx.x];
-      const float most = __builtin_fmaxf(s.x, o.x), from = most == -__builtin_inff() ? 0.0f : most;
-      s.y = s.y * __builtin_amdgcn_exp2f(s.x - from) + o.y * __builtin_amdgcn_exp2f(o.x - from);
-      s.x = most;
-    }
-    a.part[v0 / BM * a.n + r0 + threadIdx.x] = s;
+    for (int k = 1; k < WM; k++) s.add(__builtin_bit_cast(CeSum, red[k * BN + threadIdx.x]), f);
+    a.part[v0 / BM * a.n + r0 + threadIdx.x] = __builtin_bit_cast(float2, s);
   }
 }
 
@@ -472,28 +497,22 @@ template <int DT> __global__ void __launch_bounds__(GEMM_THREADS) ce_join_kernel
   const int row = threadIdx.x & 7, slice = threadIdx.x >> 3;
   const int64_t r = (int64_t)blockIdx.x * 8 + row;
   if ((int64_t)blockIdx.x * 8 >= m) return;
-  __shared__ float2 part[32][8];
-  float2 s = make_float2(-__builtin_inff(), 0.0f);
-  auto add = [](float2 s, float2 o) {
-    const float most = __builtin_fmaxf(s.x, o.x), from = most == -__builtin_inff() ? 0.0f : most;
-    return make_float2(most, s.y * __builtin_amdgcn_exp2f(s.x - from) + o.y * __builtin_amdgcn_exp2f(o.x - from));
-  };
+  __shared__ CeSum part[32][8];
+  CeSum s{-__builtin_inff(), 0.0f};
+  const float f = a.scale * LOG2E;
   if (r < m) {
 #pragma unroll 4
-    for (int t = slice; t < tiles; t += 32) s = add(s, a.part[(int64_t)t * a.n + r]);
+    for (int t = slice; t < tiles; t += 32) s.add(__builtin_bit_cast(CeSum, a.part[(int64_t)t * a.n + r]), f);
   }
   part[slice][row] = s;
   __syncthreads();
   for (int o = 16; o > 0; o >>= 1) {
-    if (slice < o) part[slice][row] = add(part[slice][row], part[slice + o][row]);
+    if (slice < o) part[slice][row].add(part[slice + o][row], f);
     __syncthreads();
   }
   if (slice == 0 && r < m) {
-    s = part[0][row];
-    const float l = s.x + __builtin_log2f(s.y);
     const int64_t to = __builtin_bit_cast(CeRow, a.info[r]).row;
-    a.lse[to] = l * LN2;
-    a.loss[to] = (l - a.picked[r]) * LN2;
+    part[0][row].finish(a.scale, f, a.picked[r], a.lse[to], a.loss[to]);
   }
 }
 
@@ -590,7 +609,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 2) ce_p_kernel(CeArgs a) {
 #pragma unroll
       for (int k = 0; k < G::TM; k++)
 #pragma unroll
-        for (int e = 0; e < 16; e++) x[k][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[k][e], f, -row.lse));
+        for (int e = 0; e < 16; e++)
+          // fp32: the difference before the change of units, so that nothing is rounded at the size of the
+          // logits (of 645 to 1745: dw off by 1.6e-5 of its size otherwise, 4e-8 so); 16 bits are rounded by
+          // far more
+          x[k][e] = DT == DT_FP32 ? __builtin_amdgcn_exp2f(__builtin_fmaf(x[k][e], a.scale, -row.lse) * LOG2E)
+                                  : __builtin_amdgcn_exp2f(__builtin_fmaf(x[k][e], f, -row.lse));
       const int at = real ? row.label - (int)first : -1;
       if (__any(at >= 0 && at < part)) {
 #pragma unroll

@@ -296,3 +296,66 @@ def test_gradients_against_differences():
         got, want = (side[0] - side[1]) / (2 * e), float((g[i].double() * t).sum())
         size = float((g[i].double() * t).abs().sum()) + float(dl.abs().sum())
         assert abs(got - want) <= size * (e * e + 2.0 ** -22 / e * 8)
+
+
+def rows_with_a_leader(scale, n=300, vocab=700, seed=0):
+    """h and w of whole numbers, so that products are exact: each row's logits are 0 but those of entry a, some
+    hundreds, and b, `gap` units below; all others' exponentials are nothing beside theirs."""
+    g = np.random.default_rng(seed)
+    d = 16
+    w, h = np.zeros((vocab, d)), np.zeros((n, d))
+    # 8 pairs of entries: pair k answers to column 2 k with `up` and column 2 k + 1 with 1 for a, 0 for b
+    a, b = 10 + 80 * np.arange(8), 50 + 80 * np.arange(8)
+    w[a, 2 * np.arange(8)] = w[b, 2 * np.arange(8)] = 64
+    w[a, 2 * np.arange(8) + 1] = 1
+    k = np.arange(n) % 8
+    gap = g.integers(1, 30, n)
+    h[np.arange(n), 2 * k] = g.integers(1, 5, n) * 1.0 + np.ceil(100 / scale / 64)
+    h[np.arange(n), 2 * k + 1] = gap
+    return h, w, a[k], b[k], gap
+
+
+@pytest.mark.parametrize("scale", [0.7, 1.0, 3.3, 5.0, 11.1])
+@pytest.mark.parametrize("n", [20, 100, 300])
+def test_losses_of_large_logits_are_rounded_once(n, scale):
+    """Statistics of logits of some hundreds, where a loss is a small difference of them: a result's own
+    rounding, and for the two exponentials, their sum and its logarithm some steps of 2^-23."""
+    scale = float(np.float32(scale))
+    h, w, a, b, gap = rows_with_a_leader(scale, n)
+    top, below = (h * w[a]).sum(1) * scale, (h * w[b]).sum(1) * scale
+    more = np.log1p(np.exp(below - top))
+    for dtype in (FP32, BF16):
+        H, W = (torch.from_numpy(t).to(dtype).cuda() for t in (h, w))
+        assert np.array_equal(as64(H), h) and np.array_equal(as64(W), w)
+        for label, z in ((a, top), (b, below)):
+            loss, lse = ms.maxsim_linear_cross_entropy(H, W, torch.from_numpy(label).cuda(), scale)
+            ref.close(lse, top + more, ref.U32 * (top + more) + 6 * 2.0 ** -23, "lse")
+            want = top - z + more
+            ref.close(loss, want, ref.U32 * want + 6 * 2.0 ** -23, "loss")
+
+
+@pytest.mark.parametrize("scale", [0.7, 1.0, 3.3, 5.0, 11.1])
+def test_gradients_of_large_logits(scale):
+    """fp32: with the lse given, each weight is exp(z - lse) to within some steps of 2^-23 of itself, however
+    large z and lse are."""
+    scale = float(np.float32(scale))
+    h, w, a, b, gap = rows_with_a_leader(scale, 64, seed=1)
+    top, below = (h * w[a]).sum(1) * scale, (h * w[b]).sum(1) * scale
+    lse = torch.from_numpy(top + np.log1p(np.exp(below - top))).float()
+    L, dl = as64(lse), np.random.default_rng(2).random(64)
+    dl = as64(torch.from_numpy(dl).float())
+    one = np.arange(64)
+    P = np.zeros((64, 700))
+    P[one, a], P[one, b] = np.exp(top - L), np.exp(below - L)
+    size = P.copy()
+    P[one, b] -= 1
+    size[one, b] += 1
+    P, size = P * (dl * scale)[:, None], size * (dl * scale)[:, None]
+    to = dict(dtype=FP32, device="cuda")
+    dh, dw = ms.maxsim_linear_cross_entropy_backward(torch.tensor(dl, **to), torch.tensor(h, **to), torch.tensor(w, **to),
+                                                     torch.from_numpy(b).cuda(), lse.cuda(), scale)
+    # the difference's rounding, its factor's, the exponential's, the subtraction's and the gradient's
+    off = 8 * 2.0 ** -23
+    gone = 700 * np.exp(-90)  # all other weights
+    ref.close(dh, P @ w, (off + 4 * ref.U32) * (size @ np.abs(w)) + 64 * gone, "dh")
+    ref.close(dw, P.T @ h, (off + 64 * ref.U32) * (size.T @ np.abs(h)) + 64 * 64 * gone, "dw")
