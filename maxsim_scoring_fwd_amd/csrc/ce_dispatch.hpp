@@ -22,7 +22,7 @@ template <typename Kernel> int ce_launch(Kernel kernel, int64_t tiles, int lds, 
 // Whether logits go in tiles of 128 rows: where there are no more rows, or fewer tiles of 256 than
 // three quarters of the workgroups (forward, tiles of 256 and of 128: 2000 rows, 2000 x 768 in bf16, 128
 // tiles, 30.1 and 24.7 us; 300 rows, 20000 x 768, 314 tiles, 31.6 and 26.5; 512 rows, 30522 x 768, 478
-// tiles, 38.2 and 43.0; 346 rows, 1547 x 640 in fp32 93 and 55).
+// tiles, 38.2 and 43.0; 346 rows, 1547 x 640 in fp32 93 and 61).
 inline bool ce_half(const CeArgs &a) {
   return a.n <= CE_HALF_BN || 4 * blocks_of(a.vocab, CE_BM) * blocks_of(a.n, CE_BN) <= 3 * CE_LANES;
 }

@@ -30,7 +30,7 @@ namespace maxsim {
 constexpr int CE_BM = 128, CE_BN = 256;   // vocabulary x rows of a tile of logits
 constexpr int CE_PM = 256, CE_PN = 128;   // columns x vocabulary (dw) or rows (dh) of a product's
 // Where there are no more rows than that, or few tiles (100 rows, 100000 x 896 in fp16: forward 48 us and backward
-// 169, in tiles of 256 rows 62 and 187; 78 rows, 25314 x 712 in fp32 64 and 159 for 107 and 203).
+// 169, in tiles of 256 rows 62 and 187; 78 rows, 25314 x 712 in fp32 70 and 168 for 107 and 203).
 constexpr int CE_HALF_BN = 128;
 constexpr int CE_FEW = 32;                // most rows of the kernel for few rows: one tile's
 constexpr int CE_GATHER = 16;             // rows of a workgroup of the gathering

@@ -1,4 +1,6 @@
 """The cross entropy over a vocabulary and its gradients against a 64-bit reference."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -359,3 +361,20 @@ def test_gradients_of_large_logits(scale):
     gone = 700 * np.exp(-90)  # all other weights
     ref.close(dh, P @ w, (off + 4 * ref.U32) * (size @ np.abs(w)) + 64 * gone, "dh")
     ref.close(dw, P.T @ h, (off + 64 * ref.U32) * (size.T @ np.abs(h)) + 64 * 64 * gone, "dw")
+
+
+@pytest.mark.parametrize("n", [1, 32, 100])
+def test_small_products_behind_a_large_one_are_kept(n):
+    """fp32, up to 128 rows: 2^24 and then halves. Two halves at a time are below half a step of 2^24 and
+    would all be lost; groups of 16 are 8, four steps, and only the first group's are."""
+    d, vocab, scale = 1024, 300, 2.0 ** -20
+    w = torch.zeros(vocab, d, device="cuda")
+    w[7] = 0.5
+    w[7, 0] = 2.0 ** 24
+    h = torch.ones(n, d, device="cuda")
+    y = torch.full((n,), 3, device="cuda")
+    loss, lse = ms.maxsim_linear_cross_entropy(h, w, y, scale)
+    z = scale * (2.0 ** 24 + (d - 1) / 2)
+    want = z + math.log1p((vocab - 1) * math.exp(-z))
+    tol = 8 * scale + ref.U32 * want + 6 * 2.0 ** -23
+    assert float((loss.double() - want).abs().max()) <= tol and float((lse.double() - want).abs().max()) <= tol
