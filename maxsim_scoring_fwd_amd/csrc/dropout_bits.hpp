@@ -65,8 +65,9 @@ struct DropBits {
   }
   // x * up where entry e (a constant) is kept, else 0.
   __device__ __forceinline__ float apply(const DropArgs &a, int e, float x) const {
+#pragma clang fp contract(off)  // the product is rounded, whatever it is added to
     const uint32_t u = e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
-    return u >= a.least ? __fmul_rn(x, a.up) : 0.0f;
+    return u >= a.least ? x * a.up : 0.0f;
   }
 };
 
