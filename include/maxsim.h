@@ -490,9 +490,9 @@ size_t maxsim_linear_cross_entropy_workspace_size(int64_t n_rows, int64_t vocab,
  *            rounding leaves alone. Gradients that differ from row to row are rounded like all of P, by
  *            up to half a step each: with gradients uniform in [0, 1 / n] dh and dw are off by some 1.45
  *            times (bf16) or up to 1.35 times (fp16) what their own rounding alone leaves, with a mean's by
- *            up to 1.15 times (root mean squares over hundreds of rows and more; with one or a few rows that count
- *            a single entry of P weighs, and either may be up to twice as far off). In fp16 entries of P below 2^-28 of the largest gradient
- *            have steps of 2^-38 of it.
+ *            up to 1.15 times (root mean squares over hundreds of rows and more; with one or a few rows
+ *            that count a single entry of P weighs, and either may be up to twice as far off). In fp16
+ *            entries of P below 2^-28 of the largest gradient have steps of 2^-38 of it.
  *   workspace  16-byte aligned, maxsim_linear_cross_entropy_backward_workspace_size bytes: a copy of the rows
  *            (each in whole 64 bytes); a piece of P, rows in 256s times columns in 128s, of at most
  *            512 MiB, or 128 columns; dh's sums in fp32, rows in 128s times d in 256s, or parts of them
